@@ -333,6 +333,204 @@ ln_status ln_bwd_noalloc(const void* dy, const void* x_sum, const void* gamma,
 ln_status ln_softmax_fwd(const void* x, void* y, cudaStream_t stream, int64_t rows,
                          int64_t hidden, ln_dtype dtype);
 
+/*
+ * Group norm with an activation, channels last.
+ *
+ * The pages behind the entry points above stop at LayerNorm and RMSNorm; in
+ * the diffusion networks they name (NVIDIA/cutlass discussion 874), the
+ * residual blocks have a group norm and an activation where the transformer
+ * blocks have a LayerNorm. Group norm: Wu and He, 2018.
+ *
+ * Activations are [samples, rows, channels], channels contiguous: rows are
+ * the pixels (or points) of a sample. Their strides are given in elements:
+ * *_sample from one sample to the next, *_row from one row to the next, so
+ * that a tensor may be a slice of the channels of a wider one. Group g has
+ * the channels [g, g + 1) * channels / groups, M = rows * channels / groups
+ * values in a sample. gamma and beta are [channels] (param_sample = 0), or
+ * one row of [channels] for each sample, param_sample elements apart.
+ *
+ * Everything else is as above: device pointers owned by the caller, one
+ * dtype for x, gamma, beta, y, dy and dx, fp32 arithmetic, work enqueued on
+ * `stream`, a status for an answer, nothing touched on a refusal. Rows that
+ * are not 16-byte aligned (base, strides, channels * sizeof(dtype)) take
+ * kernels of one element an access, with the same results up to the order of
+ * the sums. The results depend on the arguments and the number of SMs only.
+ */
+#define GN_MAX_CHANNELS 65536
+
+typedef enum { GN_ACT_NONE = 0, GN_ACT_SILU = 1, GN_ACT_GELU = 2 } gn_act;
+
+/*
+ * gn_fwd: y = act((x - mean) * rstd * w + beta), with mean and the biased
+ * variance of each sample's groups, rstd = 1/sqrt(var + eps), w = gamma or
+ * 1 + gamma; act: none, z / (1 + e^-z), or z * Phi(z) (the exact GELU).
+ *
+ * x          [samples, rows, channels], required. rows up to 2^40, samples
+ *            below 2^31.
+ * gamma      NULL = 1; beta NULL = 0.
+ * eps        >= 0 and finite.
+ * y          as x, required; overlaps no input and not itself.
+ * mean, rstd [samples, groups] fp32, NULL = not stored; the backward reads
+ *            them. rows = 0 stores zeros.
+ * groups     divides channels, else LN_ERR_SHAPE.
+ * workspace  gn_workspace_bytes(..., backward = 0), 16-byte aligned, owned by
+ *            the caller, not initialised; calls that may run at the same time
+ *            need one each.
+ */
+ln_status gn_fwd(const void* x, int64_t x_sample, int64_t x_row, const void* gamma,
+                 const void* beta, int64_t param_sample, float eps, gn_act act,
+                 int zero_centered_gamma, void* y, int64_t y_sample, int64_t y_row,
+                 float* mean, float* rstd, cudaStream_t stream, int64_t samples,
+                 int64_t rows, int64_t channels, int64_t groups, ln_dtype dtype,
+                 void* workspace, size_t workspace_bytes);
+
+/*
+ * gn_bwd: the gradients of gn_fwd from dy, its x and its statistics. With
+ * z as in gn_fwd, recomputed, dz = dy * act'(z) and sums in fp32:
+ *   A[n, c] = sum over rows of dz, B[n, c] = sum over rows of dz * xhat;
+ *   c1 = sum over the group of w A / M, c2 = sum over the group of w B / M;
+ *   dx = rstd * (w dz - c1 - xhat * c2), rounded to dtype;
+ *   dgamma = sum over samples of B, dbeta = sum over samples of A, or B and A
+ *   themselves where gamma and beta are per sample.
+ * dgamma and dbeta are added up in a fixed order (compensated sums over the
+ * slices of the rows and the samples), rounded once to grad_dtype.
+ *
+ * dy, x      as in gn_fwd, each with its strides.
+ * mean, rstd what gn_fwd stored.
+ * dx         required; overlaps no input and not itself.
+ * dgamma, dbeta  [channels], or [samples, channels] (contiguous) when
+ *            param_sample is not 0 (65535 samples at most then); grad_dtype;
+ *            NULL = not computed.
+ * workspace  gn_workspace_bytes(..., backward = 1), as above.
+ */
+ln_status gn_bwd(const void* dy, int64_t dy_sample, int64_t dy_row, const void* x,
+                 int64_t x_sample, int64_t x_row, const void* gamma, const void* beta,
+                 int64_t param_sample, gn_act act, int zero_centered_gamma,
+                 const float* mean, const float* rstd, void* dx, int64_t dx_sample,
+                 int64_t dx_row, void* dgamma, void* dbeta, cudaStream_t stream,
+                 int64_t samples, int64_t rows, int64_t channels, int64_t groups,
+                 ln_dtype dtype, ln_dtype grad_dtype, void* workspace,
+                 size_t workspace_bytes);
+
+/* Bytes of workspace gn_fwd (backward = 0) or gn_bwd (backward != 0) need
+ * for this shape on the current device, whatever the alignment. */
+ln_status gn_workspace_bytes(int64_t samples, int64_t rows, int64_t channels, int64_t groups,
+                             ln_dtype dtype, int backward, size_t* bytes);
+
+/*
+ * Rotary positions (Su et al., 2021) of a transformer's queries and keys,
+ * with the RMSNorm of each head in front where a gamma is given.
+ *
+ * A tensor is [batch, tokens, heads, head_dim], head_dim contiguous, with
+ * strides in elements for batch, token and head: slices of a packed
+ * projection, [batch, heads, tokens, head_dim] in memory and expanded inputs
+ * are all given that way. The first `rot` elements of a head form rot / 2
+ * pairs: (j, j + rot / 2) for ROPE_HALF, (2j, 2j + 1) for ROPE_INTERLEAVED;
+ * the elements after them pass through. Per head, in fp32:
+ *   u = x * rstd * w, rstd = 1/sqrt(sum x^2 / head_dim + eps), w = gamma or
+ *   1 + gamma (without a gamma u = x);
+ *   t = sum over the axes of position * frequency, of the pair;
+ *   y0 = scale * (u0 cos t - u1 sin t), y1 = scale * (u1 cos t + u0 sin t);
+ * y is rounded once, to dtype. Angles are exact modulo one turn (the
+ * frequency as a 64-bit fraction of a turn times the integer position), so
+ * positions of any size, negative ones too, lose nothing to fp32.
+ *
+ * An output may be its own input (same pointer and strides); apart from that
+ * outputs overlap neither inputs nor each other nor themselves. Interleaved
+ * slices (queries and keys of one buffer) do not count as overlapping.
+ */
+#define ROPE_MAX_HEADS 65536
+
+typedef enum { ROPE_HALF = 0, ROPE_INTERLEAVED = 1 } rope_layout;
+
+typedef struct {
+  const void* pos;      /* int32 or int64 positions, device */
+  int bits;             /* 32 or 64 */
+  int64_t axes;         /* 1..4 position axes (an image's tokens have 2) */
+  int64_t stride[3];    /* of axis, batch and token, in elements; 0 = shared */
+  const double* freqs;  /* [axes, rot / 2] radians a position, device */
+  int64_t rot;          /* even, 2..head_dim */
+  rope_layout layout;
+  float scale;          /* of cos and sin; 1, or a long-context factor */
+} rope_positions;
+
+typedef struct {
+  const void* x;        /* input */
+  void* y;              /* output */
+  const void* gamma;    /* [head_dim], NULL = no norm */
+  int64_t heads;
+  int64_t x_stride[3];  /* of batch, token and head */
+  int64_t y_stride[3];
+} rope_heads;
+
+typedef struct {
+  const void* dy;       /* gradient of y */
+  const void* x;        /* the forward's input; needed with gamma only */
+  void* dx;
+  const void* gamma;    /* [head_dim], NULL = no norm */
+  void* dgamma;         /* [head_dim] grad_dtype, NULL = not computed */
+  int64_t heads;
+  int64_t dy_stride[3];
+  int64_t x_stride[3];
+  int64_t dx_stride[3];
+} rope_heads_grad;
+
+/*
+ * rope_fwd: both tensors in one launch; k may be NULL, and either may have 0
+ * heads. head_dim even, 2..512; any batch and number of tokens.
+ */
+ln_status rope_fwd(const rope_heads* q, const rope_heads* k, const rope_positions* positions,
+                   float eps, int zero_centered_gamma, cudaStream_t stream, int64_t batch,
+                   int64_t tokens, int64_t head_dim, ln_dtype dtype);
+
+/*
+ * rope_bwd: with g' the transposed rotation of dy, xhat = x * rstd and
+ * g = g' * w: dgamma = sum over tokens and heads of g' * xhat,
+ * dx = rstd * (g - xhat * sum(g * xhat) / head_dim); without a gamma dx = g'.
+ * The statistics are taken anew from x. dgamma is added up in a fixed order
+ * and rounded once to grad_dtype.
+ *
+ * workspace  rope_bwd_workspace_bytes() bytes, 16-byte aligned, when a dgamma
+ *            is given (else NULL is fine); not initialised; calls that may
+ *            run at the same time need one each.
+ */
+ln_status rope_bwd(const rope_heads_grad* q, const rope_heads_grad* k,
+                   const rope_positions* positions, float eps, int zero_centered_gamma,
+                   cudaStream_t stream, int64_t batch, int64_t tokens, int64_t head_dim,
+                   ln_dtype dtype, ln_dtype grad_dtype, void* workspace,
+                   size_t workspace_bytes);
+
+ln_status rope_bwd_workspace_bytes(int64_t head_dim, size_t* bytes);
+
+/*
+ * rope_frequencies: the rot / 2 frequencies base^(-2j / rot), in radians a
+ * position, into a HOST array, scaled for contexts `factor` times as long as
+ * the `original` one a model was trained with, and the scale of cos and sin
+ * that goes with them. No device is needed.
+ *   ROPE_SCALING_NONE    as they are, scale 1 (factor and original ignored).
+ *   ROPE_SCALING_LINEAR  divided by factor (positions interpolated), scale 1.
+ *   ROPE_SCALING_NTK     base * factor^(rot / (rot - 2)) for base: the slowest
+ *                        pair is divided by factor, the fastest stays. Scale 1.
+ *                        rot = 2 has one pair, which stays.
+ *   ROPE_SCALING_YARN    (Peng et al., 2023) pairs that make more than
+ *                        turns_fast turns in the original context stay, those
+ *                        that make fewer than turns_slow are divided by
+ *                        factor, a linear ramp over the pairs between;
+ *                        scale 0.1 ln(factor) + 1.
+ * base > 1, factor >= 1, original >= 1, turns_fast >= turns_slow > 0 where the
+ * scaling uses them, else LN_ERR_INVALID; rot even and >= 2, else LN_ERR_SHAPE.
+ */
+typedef enum {
+  ROPE_SCALING_NONE = 0,
+  ROPE_SCALING_LINEAR = 1,
+  ROPE_SCALING_NTK = 2,
+  ROPE_SCALING_YARN = 3
+} rope_scaling;
+
+ln_status rope_frequencies(int64_t rot, double base, rope_scaling scaling, double factor,
+                           int64_t original, double turns_fast, double turns_slow,
+                           double* freqs, float* scale);
+
 /* Static, human-readable name of a status code. */
 const char* ln_status_string(ln_status status);
 

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -31,6 +32,10 @@ __all__ = [
     "ln_testing_select_kernels", "ln_testing_plan", "exported_symbols", "ln_fwd_from_partials",
     "LN_PARTIALS_SUM_SQ", "LN_PARTIALS_SUM_M2", "fused_norm_fwd_from_partials",
     "fused_norm_fwd", "fused_norm_bwd", "Workspace",
+    "GN_ACT_NONE", "GN_ACT_SILU", "GN_ACT_GELU", "gn_fwd", "gn_bwd", "gn_workspace_bytes",
+    "fused_group_norm_fwd", "fused_group_norm_bwd",
+    "ROPE_HALF", "ROPE_INTERLEAVED", "rope_fwd", "rope_bwd", "rope_bwd_workspace_bytes",
+    "rope_frequencies", "rope_axes", "fused_rope_fwd", "fused_rope_bwd",
 ]
 
 # Mirrors of include/normfuse.h (a CPU test checks them against the header).
@@ -45,6 +50,16 @@ _PARTIAL_CODES = {"sum_sq": LN_PARTIALS_SUM_SQ, "sum_m2": LN_PARTIALS_SUM_M2,
 _DTYPE_CODES = {torch.float32: LN_F32, torch.bfloat16: LN_BF16, torch.float16: LN_F16}
 _MODE_CODES = {"layernorm": LN_LAYERNORM, "rmsnorm": LN_RMSNORM,
                LN_LAYERNORM: LN_LAYERNORM, LN_RMSNORM: LN_RMSNORM}
+
+GN_ACT_NONE, GN_ACT_SILU, GN_ACT_GELU = 0, 1, 2
+_ACT_CODES = {"none": GN_ACT_NONE, None: GN_ACT_NONE, "silu": GN_ACT_SILU, "gelu": GN_ACT_GELU,
+              GN_ACT_NONE: GN_ACT_NONE, GN_ACT_SILU: GN_ACT_SILU, GN_ACT_GELU: GN_ACT_GELU}
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+_SCALING_CODES = {"none": 0, None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+# The C structs rope_heads, rope_heads_grad and rope_positions.
+_ROPE_HEADS = struct.Struct("@PPPq3q3q")
+_ROPE_HEADS_GRAD = struct.Struct("@PPPPPq3q3q3q")
+_ROPE_POSITIONS = struct.Struct("@Piq3qPqif")
 
 _lib = None
 _lock = threading.Lock()
@@ -106,16 +121,37 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.ln_testing_select_kernels.restype = ci
         lib.ln_testing_plan.argtypes = [ci, i64, i64, ci, ci, ci, ctypes.POINTER(ci)]
         lib.ln_testing_plan.restype = ci
+        lib.gn_fwd.argtypes = [vp, i64, i64, vp, vp, i64, f32, ci, ci, vp, i64, i64, vp, vp, vp,
+                               i64, i64, i64, i64, ci, vp, sz]
+        lib.gn_fwd.restype = ci
+        lib.gn_bwd.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, i64, ci, ci, vp, vp, vp, i64,
+                               i64, vp, vp, vp, i64, i64, i64, i64, ci, ci, vp, sz]
+        lib.gn_bwd.restype = ci
+        lib.gn_workspace_bytes.argtypes = [i64, i64, i64, i64, ci, ci, ctypes.POINTER(sz)]
+        lib.gn_workspace_bytes.restype = ci
+        lib.rope_fwd.argtypes = [vp, vp, vp, f32, ci, vp, i64, i64, i64, ci]
+        lib.rope_fwd.restype = ci
+        lib.rope_bwd.argtypes = [vp, vp, vp, f32, ci, vp, i64, i64, i64, ci, ci, vp, sz]
+        lib.rope_bwd.restype = ci
+        lib.rope_bwd_workspace_bytes.argtypes = [i64, ctypes.POINTER(sz)]
+        lib.rope_bwd_workspace_bytes.restype = ci
+        lib.rope_frequencies.argtypes = [i64, ctypes.c_double, ci, ctypes.c_double, i64,
+                                         ctypes.c_double, ctypes.c_double, vp,
+                                         ctypes.POINTER(f32)]
+        lib.rope_frequencies.restype = ci
         _lib = lib
         return lib
 
 
-def exported_symbols() -> list[str]:
-    """Names of the C entry points this binding wraps."""
-    return ["ln_fwd", "ln_fwd_ex", "ln_bwd", "ln_bwd_ex", "ln_bwd_workspace_bytes",
-            "ln_status_string", "ln_last_cuda_error", "ln_device_error", "ln_bwd_noalloc",
-            "ln_softmax_fwd", "ln_testing_select_kernels", "ln_fwd_from_partials",
-            "ln_testing_plan"]
+def exported_symbols(prefix: str = "ln_") -> list[str]:
+    """Names of the C entry points this binding wraps that start with
+    ``prefix``: "ln_", "gn_" (group norm) or "rope_" (rotary positions)."""
+    names = ["ln_fwd", "ln_fwd_ex", "ln_bwd", "ln_bwd_ex", "ln_bwd_workspace_bytes",
+             "ln_status_string", "ln_last_cuda_error", "ln_device_error", "ln_bwd_noalloc",
+             "ln_softmax_fwd", "ln_testing_select_kernels", "ln_fwd_from_partials",
+             "ln_testing_plan", "gn_fwd", "gn_bwd", "gn_workspace_bytes", "rope_fwd", "rope_bwd",
+             "rope_bwd_workspace_bytes", "rope_frequencies"]
+    return [n for n in names if n.startswith(prefix)]
 
 
 _FAMILY_CODES = {"default": 0, "ring": 1}
@@ -369,7 +405,10 @@ class Workspace:
         self.buf = torch.empty(0, dtype=torch.uint8, device=self.device)
 
     def get(self, rows: int, hidden: int, dtype, mode) -> torch.Tensor:
-        need = ln_bwd_workspace_bytes(rows, hidden, dtype, mode)
+        return self.take(ln_bwd_workspace_bytes(rows, hidden, dtype, mode))
+
+    def take(self, need: int) -> torch.Tensor:
+        """A buffer of at least ``need`` bytes."""
         if self.buf.numel() < need:
             self.buf = torch.empty(need, dtype=torch.uint8, device=self.device)
         return self.buf
@@ -434,3 +473,476 @@ def fused_norm_bwd(dy, x_sum, gamma, mean, rstd, *, mode="layernorm", zero_cente
         ln_bwd(dy, x_sum, gamma, mean, rstd, dx, dgamma, dbeta, stream, mode=mode,
                zero_centered_gamma=zero_centered_gamma, workspace=ws)
     return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta, "dbias": dbias}
+
+
+# ---- group norm and rotary positions ------------------------------------------
+# These take tensors of any strides (the last dimension contiguous), run on the
+# device of their first tensor whatever the current one is, and allocate on the
+# stream that they launch on, so that a buffer of theirs is not handed out again
+# while the launch is using it.
+
+def _on_device(where: str, first, *others) -> torch.device:
+    """The CUDA device that all given tensors live on."""
+    for t in (first, *others):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: expected a torch.Tensor or None, got {type(t).__name__}")
+        if not t.is_cuda:
+            raise ValueError(f"{where}: tensors passed to the CUDA library must live on a CUDA "
+                             "device")
+        if t.device != first.device:
+            raise ValueError(f"{where}: tensors on {first.device} and {t.device}")
+    return first.device
+
+
+class _Launch:
+    """Makes ``device`` and ``stream`` (None: torch's current stream of that
+    device) current, where they are not, and gives the raw stream."""
+
+    __slots__ = ("raw", "_guards")
+
+    def __init__(self, device, stream):
+        self._guards = ()
+        if device.index != torch.cuda.current_device():
+            self._guards = (torch.cuda.device(device),)
+        if stream is None:
+            self.raw = torch.cuda.current_stream(device).cuda_stream
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            # 0 is the legacy default stream, torch's own default
+            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                      else torch.cuda.default_stream(device))
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        self.raw = stream.cuda_stream
+        self._guards += (torch.cuda.stream(stream),)
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _dense_last(t, name):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _rows_of(t, name):
+    """(samples, rows, channels, sample stride, row stride) of [N, ..., C]."""
+    if t.dim() < 2:
+        raise ValueError(f"{name}: expected [samples, ..., channels]")
+    _dense_last(t, name)
+    shape, stride = t.shape, t.stride()
+    rows, row = 1, 0
+    for n, s in zip(shape[-2:0:-1], stride[-2:0:-1]):
+        if n == 1:
+            continue
+        if rows > 1 and s != row * rows and rows * n > 0:
+            raise ValueError(f"{name}: the dimensions between samples and channels must have one "
+                             "stride from row to row")
+        row = s if rows == 1 else row
+        rows *= n
+    return shape[0], rows, shape[-1], stride[0], row
+
+
+def _affine(p, name, N, C, dtype):
+    """Stride between samples of gamma or beta: 0 for [C], else that of [N, C]."""
+    if p.dtype != dtype:
+        raise TypeError(f"{name}: {p.dtype} with activations of {dtype}")
+    _dense_last(p, name)
+    if p.shape == (C,):
+        return 0
+    if p.shape == (N, C):
+        return p.stride(0) if N > 1 else C
+    raise ValueError(f"{name}: expected [{C}] or [{N}, {C}], got {list(p.shape)}")
+
+
+def _affines(where, gamma, beta, N, C, dtype):
+    steps = [_affine(p, f"{where}: {n}", N, C, dtype) for p, n in ((gamma, "gamma"), (beta, "beta"))
+             if p is not None]
+    if len(set(steps)) > 1:
+        raise ValueError(f"{where}: gamma and beta must both be shared or both per sample, with "
+                         "the same stride")
+    return steps[0] if steps else 0
+
+
+def _activation(act) -> int:
+    try:
+        return _ACT_CODES[act]
+    except KeyError:
+        raise ValueError(f"unknown activation {act!r}") from None
+
+
+def _same(where, name, t, ref):
+    if t.shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{where}: {name} must have the shape and dtype of x")
+
+
+def _check_stats(where, mean, rstd, N, G, optional):
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is None and optional:
+            continue
+        if t is None or t.shape != (N, G) or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be a contiguous float32 [{N}, {G}]")
+
+
+def gn_workspace_bytes(samples, rows, channels, groups, dtype, backward=False) -> int:
+    """Bytes of workspace ``gn_fwd`` or ``gn_bwd`` needs for this shape."""
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    code = _DTYPE_CODES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    st = lib.gn_workspace_bytes(int(samples), int(rows), int(channels), int(groups), code,
+                                int(bool(backward)), ctypes.byref(out))
+    if st:
+        raise NormError(st, "gn_workspace_bytes")
+    return int(out.value)
+
+
+def _workspace(workspace, need, device):
+    if isinstance(workspace, Workspace):
+        workspace = workspace.take(need)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is None or not workspace.numel():
+        return None, None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
+           stream=None, *, workspace=None) -> None:
+    """Enqueue the group norm of ``x`` [samples, ..., channels] into ``y``.
+
+    gamma and beta are [channels], [samples, channels] or None; mean and rstd
+    fp32 [samples, groups] or None; ``activation`` "none", "silu" or "gelu";
+    ``workspace`` a CUDA tensor of ``gn_workspace_bytes`` bytes or a
+    ``Workspace`` (one is allocated for the call when None). See ``gn_fwd`` in
+    include/normfuse.h.
+    """
+    lib = _lib or load_library()
+    device = _on_device("gn_fwd", x, gamma, beta, y, mean, rstd)
+    dt = _dtype(x)
+    N, R, C, xs, xr = _rows_of(x, "gn_fwd: x")
+    _same("gn_fwd", "y", y, x)
+    _, _, _, ys, yr = _rows_of(y, "gn_fwd: y")
+    ps = _affines("gn_fwd", gamma, beta, N, C, x.dtype)
+    _check_stats("gn_fwd", mean, rstd, N, groups, True)
+    act = _activation(activation)
+    with _Launch(device, stream) as raw:
+        if workspace is None or isinstance(workspace, Workspace):
+            need = gn_workspace_bytes(N, R, C, groups, dt)
+        else:
+            need = 0
+        _held, ws, ws_bytes = _workspace(workspace, need, device)
+        st = lib.gn_fwd(x.data_ptr() or None, xs, xr, None if gamma is None else gamma.data_ptr(),
+                        None if beta is None else beta.data_ptr(), ps, eps, act,
+                        1 if zero_centered_gamma else 0, y.data_ptr() or None, ys, yr,
+                        None if mean is None else mean.data_ptr(),
+                        None if rstd is None else rstd.data_ptr(), raw or None, N, R, C, groups,
+                        dt, ws, ws_bytes)
+    if st:
+        raise NormError(st, "gn_fwd")
+
+
+def gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx, dgamma,
+           dbeta, stream=None, *, workspace=None) -> None:
+    """Enqueue the backward of ``gn_fwd``: dx, and dgamma and dbeta (contiguous,
+    the shape of gamma, one dtype of float32, bfloat16 or float16; may be
+    None). See ``gn_bwd`` in include/normfuse.h."""
+    lib = _lib or load_library()
+    device = _on_device("gn_bwd", x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta)
+    dt = _dtype(x)
+    N, R, C, xs, xr = _rows_of(x, "gn_bwd: x")
+    _same("gn_bwd", "dy", dy, x)
+    _same("gn_bwd", "dx", dx, x)
+    _, _, _, ds, dr = _rows_of(dy, "gn_bwd: dy")
+    _, _, _, os_, or_ = _rows_of(dx, "gn_bwd: dx")
+    ps = _affines("gn_bwd", gamma, beta, N, C, x.dtype)
+    _check_stats("gn_bwd", mean, rstd, N, groups, False)
+    grads = [g for g in (dgamma, dbeta) if g is not None]
+    for g in grads:
+        if (g.shape != ((N, C) if ps else (C,)) or not g.is_contiguous()
+                or g.dtype != grads[0].dtype):
+            raise ValueError("gn_bwd: dgamma and dbeta must be contiguous, of the shape of gamma "
+                             "and of one dtype")
+    gdt = _dtype(grads[0]) if grads else LN_F32
+    act = _activation(activation)
+    with _Launch(device, stream) as raw:
+        if workspace is None or isinstance(workspace, Workspace):
+            need = gn_workspace_bytes(N, R, C, groups, dt, True)
+        else:
+            need = 0
+        _held, ws, ws_bytes = _workspace(workspace, need, device)
+        st = lib.gn_bwd(dy.data_ptr() or None, ds, dr, x.data_ptr() or None, xs, xr,
+                        None if gamma is None else gamma.data_ptr(),
+                        None if beta is None else beta.data_ptr(), ps, act,
+                        1 if zero_centered_gamma else 0, mean.data_ptr() or None,
+                        rstd.data_ptr() or None, dx.data_ptr() or None, os_, or_,
+                        None if dgamma is None else dgamma.data_ptr(),
+                        None if dbeta is None else dbeta.data_ptr(), raw or None, N, R, C, groups,
+                        dt, gdt, ws, ws_bytes)
+    if st:
+        raise NormError(st, "gn_bwd")
+
+
+def fused_group_norm_fwd(x, groups, gamma=None, beta=None, *, eps=1e-5, activation="none",
+                         zero_centered_gamma=False, out=None, workspace=None, stream=None):
+    """Group norm of a channels-last tensor [samples, ..., channels] with an
+    activation ("none", "silu", "gelu") behind it; returns a dict with ``y``,
+    ``mean`` and ``rstd`` ([samples, groups], for the backward). An NCHW tensor
+    in torch's channels_last format goes in as ``x.permute(0, 2, 3, 1)``.
+
+    gamma and beta are [channels], or [samples, channels] for a scale and
+    shift of each sample. ``x`` and ``out`` may be slices of the channels of
+    wider tensors.
+    """
+    device = _on_device("fused_group_norm_fwd", x)
+    with _Launch(device, stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
+        mean, rstd = torch.empty((2, x.shape[0], groups), dtype=torch.float32, device=device)
+        gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
+               None, workspace=workspace)
+    return {"y": y, "mean": mean, "rstd": rstd}
+
+
+def fused_group_norm_bwd(dy, x, groups, gamma, beta, mean, rstd, *, activation="none",
+                         zero_centered_gamma=False, grad_dtype=torch.float32, workspace=None,
+                         stream=None):
+    """The backward of ``fused_group_norm_fwd`` from its x and statistics;
+    returns a dict with ``dx``, ``dgamma`` and ``dbeta`` (None where gamma or
+    beta is None)."""
+    device = _on_device("fused_group_norm_bwd", x)
+    with _Launch(device, stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dgamma = dbeta = None
+        if gamma is not None:
+            dgamma = torch.empty(gamma.shape, dtype=grad_dtype, device=device)
+        if beta is not None:
+            dbeta = torch.empty(beta.shape, dtype=grad_dtype, device=device)
+        gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx, dgamma,
+               dbeta, None, workspace=workspace)
+    return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
+
+
+def rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original=4096,
+                     turns_fast=32.0, turns_slow=1.0, device="cuda"):
+    """(frequencies, scale) of rotary positions: a float64 [rot / 2] tensor of
+    radians a position on ``device``, and the scale of cos and sin.
+
+    ``scaling`` stretches the context ``original`` by ``factor``: "linear",
+    "ntk" or "yarn" (see ``rope_frequencies`` in include/normfuse.h).
+    """
+    lib = load_library()
+    try:
+        code = _SCALING_CODES[scaling]
+    except KeyError:
+        raise ValueError(f"unknown scaling {scaling!r}") from None
+    host = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    scale = ctypes.c_float(0)
+    st = lib.rope_frequencies(int(rot), base, code, factor, int(original), turns_fast, turns_slow,
+                              host.data_ptr() or None, ctypes.byref(scale))
+    if st:
+        raise NormError(st, "rope_frequencies")
+    return host.to(device), float(scale.value)
+
+
+def rope_axes(*frequencies):
+    """Frequencies for positions of several axes: the pairs of the first one
+    turn with the first axis, those of the next with the next, and so on.
+    Returns [axes, sum of the pairs]."""
+    pairs = sum(f.numel() for f in frequencies)
+    out = torch.zeros(len(frequencies), pairs, dtype=torch.float64, device=frequencies[0].device)
+    at = 0
+    for a, f in enumerate(frequencies):
+        out[a, at:at + f.numel()] = f
+        at += f.numel()
+    return out
+
+
+def _heads(t, name, like=None):
+    """(batch, tokens, heads, dim) and the strides of the first three, of
+    [tokens, heads, dim] or [batch, tokens, heads, dim]."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name}: expected [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    _dense_last(t, name)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name}: expected {list(like.shape)} of {like.dtype}")
+    if t.dim() == 3:
+        return (1, *t.shape), (0, *t.stride()[:2])
+    return tuple(t.shape), t.stride()[:3]
+
+
+def _positions(where, positions, freqs, interleaved, scale, shape, dims):
+    """The packed rope_positions struct."""
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{where}: positions must be int32 or int64, got {positions.dtype}")
+    if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.dim() not in (1, 2):
+        raise ValueError(f"{where}: frequencies must be a contiguous float64 [pairs] or "
+                         "[axes, pairs]")
+    axes = freqs.shape[0] if freqs.dim() == 2 else 1
+    p, batch, tokens = positions, shape[0], shape[1]
+    want, step = list(p.shape), list(p.stride())
+    axis = 0
+    if freqs.dim() == 2:
+        if not want or want[0] != axes:
+            raise ValueError(f"{where}: positions must start with the {axes} axes of the "
+                             "frequencies")
+        axis = step[0]
+        want, step = want[1:], step[1:]
+    if len(want) == 1 and want[0] == tokens:
+        strides = (axis, 0, step[0])
+    elif len(want) == 2 and want[0] == batch and want[1] == tokens and dims == 4:
+        strides = (axis, step[0], step[1])
+    else:
+        raise ValueError(f"{where}: positions must be [tokens] or [batch, tokens] (behind the "
+                         f"axes), got {list(p.shape)} for {batch} x {tokens}")
+    return _ROPE_POSITIONS.pack(p.data_ptr(), 32 if p.dtype == torch.int32 else 64, axes, *strides,
+                                freqs.data_ptr(), 2 * freqs.shape[-1], 1 if interleaved else 0,
+                                scale)
+
+
+def _gamma_ptr(g, name, D, dtype):
+    if g is None:
+        return 0
+    if g.shape != (D,) or g.dtype != dtype or not g.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous [{D}] of {dtype}")
+    return g.data_ptr()
+
+
+def rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma, interleaved,
+             scale, out_q, out_k, stream=None) -> None:
+    """Enqueue the rotary positions of ``q`` and ``k`` (k may be None), with the
+    RMSNorm of each head where its gamma is given. Tensors are
+    [batch, tokens, heads, dim] or [tokens, heads, dim] of any strides; an
+    output may be its input. See ``rope_fwd`` in include/normfuse.h."""
+    lib = _lib or load_library()
+    device = _on_device("rope_fwd", q, k, positions, freqs, q_gamma, k_gamma, out_q, out_k)
+    shape, xs = _heads(q, "rope_fwd: q")
+    _, ys = _heads(out_q, "rope_fwd: out_q", q)
+    D = shape[3]
+    qs = _ROPE_HEADS.pack(q.data_ptr(), out_q.data_ptr(),
+                          _gamma_ptr(q_gamma, "rope_fwd: q_gamma", D, q.dtype), shape[2], *xs, *ys)
+    ks = None
+    if k is not None:
+        kshape, xs = _heads(k, "rope_fwd: k")
+        _, ys = _heads(out_k, "rope_fwd: out_k", k)
+        if kshape[:2] != shape[:2] or kshape[3] != D or k.dtype != q.dtype or k.dim() != q.dim():
+            raise ValueError("rope_fwd: q and k must share batch, tokens, dim and dtype")
+        ks = _ROPE_HEADS.pack(k.data_ptr(), out_k.data_ptr(),
+                              _gamma_ptr(k_gamma, "rope_fwd: k_gamma", D, q.dtype), kshape[2], *xs,
+                              *ys)
+    pos = _positions("rope_fwd", positions, freqs, interleaved, scale, shape, q.dim())
+    with _Launch(device, stream) as raw:
+        st = lib.rope_fwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, raw or None, shape[0],
+                          shape[1], D, _dtype(q))
+    if st:
+        raise NormError(st, "rope_fwd")
+
+
+def rope_bwd_workspace_bytes(head_dim) -> int:
+    """Bytes of workspace ``rope_bwd`` needs for the gradients of gammas."""
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    st = lib.rope_bwd_workspace_bytes(int(head_dim), ctypes.byref(out))
+    if st:
+        raise NormError(st, "rope_bwd_workspace_bytes")
+    return int(out.value)
+
+
+def rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+             interleaved, scale, out_dq, out_dk, dq_gamma, dk_gamma, stream=None, *,
+             workspace=None) -> None:
+    """Enqueue the backward of ``rope_fwd``: ``dq`` and ``dk`` are the gradients
+    of its outputs, ``out_dq`` and ``out_dk`` those of its inputs (an output
+    may be its gradient). q and k are needed with a gamma only; dq_gamma and
+    dk_gamma ([dim], one dtype) may be None."""
+    lib = _lib or load_library()
+    device = _on_device("rope_bwd", dq, dk, q, k, positions, freqs, q_gamma, k_gamma, out_dq,
+                        out_dk, dq_gamma, dk_gamma)
+    shape, _ = _heads(dq, "rope_bwd: dq")
+    D = shape[3]
+    grads = [g for g in (dq_gamma, dk_gamma) if g is not None]
+    for g in grads:
+        if g.shape != (D,) or not g.is_contiguous() or g.dtype != grads[0].dtype:
+            raise ValueError(f"rope_bwd: dq_gamma and dk_gamma must be contiguous [{D}] of one "
+                             "dtype")
+
+    def side(d, x, gamma, out, dgamma, name):
+        if d is None:
+            return None
+        dshape, ds = _heads(d, f"rope_bwd: d{name}")
+        if (dshape[:2] != shape[:2] or dshape[3] != D or d.dtype != dq.dtype
+                or d.dim() != dq.dim()):
+            raise ValueError("rope_bwd: dq and dk must share batch, tokens, dim and dtype")
+        _, os_ = _heads(out, f"rope_bwd: out_d{name}", d)
+        xs = (0, 0, 0)
+        if gamma is not None:
+            if x is None:
+                raise ValueError(f"rope_bwd: {name} is needed with its gamma")
+            _, xs = _heads(x, f"rope_bwd: {name}", d)
+        return _ROPE_HEADS_GRAD.pack(
+            d.data_ptr(), 0 if gamma is None else x.data_ptr(), out.data_ptr(),
+            _gamma_ptr(gamma, f"rope_bwd: {name}_gamma", D, d.dtype),
+            0 if dgamma is None else dgamma.data_ptr(), dshape[2], *ds, *xs, *os_)
+
+    qs = side(dq, q, q_gamma, out_dq, dq_gamma, "q")
+    ks = side(dk, k, k_gamma, out_dk, dk_gamma, "k")
+    pos = _positions("rope_bwd", positions, freqs, interleaved, scale, shape, dq.dim())
+    with _Launch(device, stream) as raw:
+        need = rope_bwd_workspace_bytes(D) if grads and (
+            workspace is None or isinstance(workspace, Workspace)) else 0
+        _held, ws, ws_bytes = _workspace(workspace, need, device)
+        st = lib.rope_bwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, raw or None, shape[0],
+                          shape[1], D, _dtype(dq), _dtype(grads[0]) if grads else LN_F32, ws,
+                          ws_bytes)
+    if st:
+        raise NormError(st, "rope_bwd")
+
+
+def fused_rope_fwd(q, k, positions, freqs, *, q_gamma=None, k_gamma=None, eps=1e-6,
+                   zero_centered_gamma=False, interleaved=False, scale=1.0, out_q=None, out_k=None,
+                   stream=None):
+    """Rotary positions of queries and keys [batch, tokens, heads, dim] (or
+    [tokens, heads, dim]), with the RMSNorm of each head before the rotation
+    where a gamma is given; returns a dict with ``q`` and ``k``.
+
+    ``positions`` are int32 or int64 [tokens] or [batch, tokens]; ``freqs`` is
+    what ``rope_frequencies`` gives ([pairs]: 2 * pairs elements of a head are
+    rotated, the others pass through), or [axes, pairs] from ``rope_axes``
+    with positions of [axes, ...]. ``out_q=q`` and ``out_k=k`` work in place.
+    """
+    device = _on_device("fused_rope_fwd", q)
+    with _Launch(device, stream):
+        if out_q is None:
+            out_q = torch.empty_like(q)
+        if out_k is None and k is not None:
+            out_k = torch.empty_like(k)
+        rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma, interleaved,
+                 scale, out_q, out_k, None)
+    return {"q": out_q, "k": out_k}
+
+
+def fused_rope_bwd(dq, dk, positions, freqs, *, q=None, k=None, q_gamma=None, k_gamma=None,
+                   eps=1e-6, zero_centered_gamma=False, interleaved=False, scale=1.0,
+                   grad_dtype=torch.float32, workspace=None, stream=None):
+    """The backward of ``fused_rope_fwd``; ``q`` and ``k`` are its inputs,
+    needed with a gamma. Returns a dict with ``dq``, ``dk``, ``dq_gamma`` and
+    ``dk_gamma`` (None where there is none)."""
+    device = _on_device("fused_rope_bwd", dq)
+    with _Launch(device, stream):
+        out_dq = torch.empty_like(dq)
+        out_dk = torch.empty_like(dk) if dk is not None else None
+        D = dq.shape[-1]
+        gq = torch.empty(D, dtype=grad_dtype, device=device) if q_gamma is not None else None
+        gk = (torch.empty(D, dtype=grad_dtype, device=device)
+              if k_gamma is not None and dk is not None else None)
+        rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+                 interleaved, scale, out_dq, out_dk, gq, gk, None, workspace=workspace)
+    return {"dq": out_dq, "dk": out_dk, "dq_gamma": gq, "dk_gamma": gk}

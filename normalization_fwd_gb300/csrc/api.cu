@@ -9,6 +9,7 @@
 #include "../../include/normfuse.h"
 #include "../../include/normfuse_testing.h"
 #include "launch.h"
+#include "validate.h"
 
 namespace nf {
 namespace {
@@ -36,42 +37,8 @@ std::vector<OccEntry>& occ_cache() {
   return v;
 }
 
-size_t elem_size(ln_dtype dt) { return dt == LN_F32 ? 4 : 2; }
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// Byte ranges for the overlap check.
-struct Range {
-  const void* p;
-  size_t bytes;
-};
-bool overlap(const Range& a, const Range& b) {
-  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, a1 = a0 + a.bytes;
-  const uintptr_t b0 = (uintptr_t)b.p, b1 = b0 + b.bytes;
-  return a0 < b1 && b0 < a1;
-}
-bool any_overlap(const Range* outs, int n_out, const Range* ins, int n_in) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-  }
-  return false;
-}
-
 int max_hidden(ln_dtype dt, bool vec) {
   return vec ? kMaxVecSlots * (int)(16 / elem_size(dt)) : kMaxHiddenScalar;
-}
-
-template <typename F>
-cudaError_t by_dtype(ln_dtype dt, F&& f) {
-  switch (dt) {
-    case LN_F32: return f(float{});
-    case LN_BF16: return f(bf16{});
-    default: return f(f16{});
-  }
 }
 
 }  // namespace

@@ -34,7 +34,8 @@ __device__ __forceinline__ void comp_add(float& s, float& c, float x) {
 //
 // Block (32, 32): thread (x, y) owns column blockIdx.x * 32 + x and slice y,
 // so a warp reads 128 contiguous bytes of one partial row and every thread
-// waits for only ceil(P / 32) independent loads.
+// waits for only ceil(P / 32) independent loads. blockIdx.y takes one of
+// several such sums: P partial rows of ws and one row of each output apiece.
 __global__ void __launch_bounds__(kFinCols* kFinSlices)
     bwd_finalize_kernel(const float* __restrict__ ws, int P, int C, int H, int beta_cols,
                         void* dgamma, void* dbeta, void* dbias, int out_dtype) {
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(kFinCols* kFinSlices)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int x = threadIdx.x, y = threadIdx.y;
   const int c = blockIdx.x * kFinCols + x;
+  ws += (int64_t)blockIdx.y * P * C;
   float s = 0.f, e = 0.f;
   if (c < C) {
 #pragma unroll 8
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kFinCols* kFinSlices)
   if (y == 0 && c < C) {
     const double t = (double)ps[0][x] + (double)pc[0][x];   // exact
     void* out = nullptr;
-    int j = 0;
+    int64_t j = 0;
     if (c < H) {
       out = dgamma;
       j = c;
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(kFinCols* kFinSlices)
       out = dbias;
       j = c - (C - H);
     }
+    j += (int64_t)blockIdx.y * H;
     if (out != nullptr) {
       if (out_dtype == 1) {
         static_cast<bf16*>(out)[j] = __double2bfloat16(t);
@@ -91,11 +94,11 @@ __global__ void __launch_bounds__(kFinCols* kFinSlices)
 
 cudaError_t launch_bwd_finalize(const float* ws, int P, int C, int H, bool beta_cols,
                                 void* dgamma, void* dbeta, void* dbias, int out_dtype,
-                                cudaStream_t st) {
+                                cudaStream_t st, int outer) {
   // Programmatic stream serialization: the finalize may be scheduled while
   // the backward kernel drains; griddepcontrol.wait above orders its reads.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((C + kFinCols - 1) / kFinCols);
+  cfg.gridDim = dim3((C + kFinCols - 1) / kFinCols, outer);
   cfg.blockDim = dim3(kFinCols, kFinSlices);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = st;

@@ -1,0 +1,343 @@
+// Group norm with an activation: C entry points, argument checks and launch
+// plan.
+#include <math.h>
+
+#include "../../include/normfuse.h"
+#include "gn_kernels.cuh"
+#include "launch.h"
+#include "validate.h"
+
+namespace nf {
+
+const void* gn_table_f32(bool bwd, bool vec, int act);
+const void* gn_table_bf16(bool bwd, bool vec, int act);
+const void* gn_table_f16(bool bwd, bool vec, int act);
+
+namespace {
+
+ln_status cuda_fail(cudaError_t e) {
+  nf_set_last_cuda_error((int)e);
+  return LN_ERR_CUDA;
+}
+
+int gcd(int a, int b) {
+  while (b) {
+    const int t = a % b;
+    a = b;
+    b = t;
+  }
+  return a;
+}
+
+// How a call is cut up: column tiles, slices of the rows and batches of
+// panels (a panel is one sample's column tile).
+struct GnPlan {
+  int tiles, tw, max_groups, slices;
+  int64_t slice_rows;
+  int64_t panels, batch;   // all panels, and those of one launch
+  size_t part_bytes, cols_bytes;
+  size_t bytes() const { return part_bytes + cols_bytes; }
+};
+
+constexpr int64_t kBatchBytes = 48ll << 20;
+
+bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es, bool bwd, bool vec,
+             int sms, GnPlan* p) {
+  const int V = vec ? (int)(16 / es) : 1;
+  const int nv = channels / V, cpg = channels / groups;
+  const int most = vec ? 64 : 256, target = vec ? 32 : 256;
+  const int lv = cpg / gcd(cpg, V);   // vectors that whole groups and whole vectors fill
+  bool whole = true;                  // every group lies in one tile
+  int tw = nv;
+  if (nv > target) {
+    if (lv <= most) {
+      const int units = nv / lv;
+      int per = target / lv > 0 ? target / lv : 1;
+      const int t = (units + per - 1) / per;
+      per = (units + t - 1) / t;
+      tw = per * lv;
+    } else {
+      const int t = (nv + target - 1) / target;
+      tw = (nv + t - 1) / t;
+      whole = false;
+    }
+  }
+  p->tw = tw;
+  p->tiles = (nv + tw - 1) / tw;
+  const int tc = tw * V;
+  p->max_groups = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
+  if (p->max_groups > groups) p->max_groups = groups;
+  p->panels = samples * p->tiles;
+  const double per_panel = (double)rows * tc * es * (bwd ? 2 : 1);
+  p->batch = p->panels;
+  if (per_panel * p->panels > (double)kBatchBytes) {
+    const int64_t step = whole ? 1 : p->tiles;
+    int64_t b = (int64_t)(kBatchBytes / per_panel) / step * step;
+    p->batch = b < step ? step : b;
+    if (p->batch > p->panels) p->batch = p->panels;
+  }
+  const int TY = kGnThreads / tw;
+  const int64_t want = (int64_t)sms * 6;
+  int64_t slices = (want + p->batch - 1) / p->batch;
+  const int64_t least = 4 * TY;       // rows of a slice: four a thread
+  if (slices > (rows + least - 1) / least) slices = (rows + least - 1) / least;
+  if (slices < 1) slices = 1;
+  p->slice_rows = (rows + slices - 1) / slices;
+  p->slices = (int)((rows + p->slice_rows - 1) / p->slice_rows);
+  p->part_bytes = (size_t)p->panels * p->slices * p->max_groups * sizeof(float2);
+  p->part_bytes = (p->part_bytes + 15) / 16 * 16;
+  p->cols_bytes = bwd ? (size_t)samples * p->slices * 2 * channels * sizeof(float) : 0;
+  return p->panels * p->slices <= INT32_MAX;
+}
+
+struct GnCall {
+  int64_t samples, rows, channels, groups;
+  ln_dtype dtype;
+};
+
+ln_status check_shape(const GnCall& c) {
+  if (!known_dtype(c.dtype)) return LN_ERR_UNSUPPORTED;
+  if (c.samples < 0 || c.samples > INT32_MAX || c.rows < 0 || c.rows > (1ll << 40) ||
+      c.channels < 1 || c.channels > GN_MAX_CHANNELS ||
+      c.groups < 1 || c.channels % c.groups != 0)
+    return LN_ERR_SHAPE;
+  return LN_OK;
+}
+
+Strided tensor(const void* p, int64_t sample, int64_t row, const GnCall& c) {
+  const int64_t es = (int64_t)elem_size(c.dtype);
+  Strided s;
+  s.p = p;
+  s.n[0] = c.samples;
+  s.n[1] = c.rows;
+  s.stride[0] = sample * es;
+  s.stride[1] = row * es;
+  s.width = c.channels * es;
+  return s;
+}
+
+bool vec_ok(const void* p, int64_t sample, int64_t row, size_t es) {
+  return aligned(p, 16) && (sample * (int64_t)es) % 16 == 0 && (row * (int64_t)es) % 16 == 0;
+}
+
+// The plan of a call whose pointers allow vectors or not; the vector plan
+// and the scalar plan differ in their need of workspace.
+ln_status plan_call(const GnCall& c, bool bwd, bool vec, GnPlan* p) {
+  int sms = 0;
+  const cudaError_t e = (cudaError_t)device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return gn_plan(c.samples, c.rows, (int)c.channels, (int)c.groups, elem_size(c.dtype), bwd, vec,
+                 sms, p)
+             ? LN_OK
+             : LN_ERR_SHAPE;
+}
+
+ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec, int act,
+                 cudaStream_t st) {
+  a.slice_rows = p.slice_rows;
+  a.slices = p.slices;
+  a.channels = (int)c.channels;
+  a.groups = (int)c.groups;
+  a.cpg = (int)(c.channels / c.groups);
+  a.tiles = p.tiles;
+  a.tw = p.tw;
+  a.max_groups = p.max_groups;
+  a.rows = c.rows;
+  a.inv_m = (float)(1.0 / ((double)c.rows * a.cpg));
+  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, vec, act)
+                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, vec, act)
+                                        : gn_table_f16(bwd, vec, act);
+  // Launch j takes the statistics of batch j and applies batch j - 1, whose
+  // rows are then still in the L2 cache.
+  const int64_t batches = (p.panels + p.batch - 1) / p.batch;
+  const auto first = [&](int64_t j) { return (int)(j * p.batch < p.panels ? j * p.batch : p.panels); };
+  for (int64_t j = 0; j <= batches; ++j) {
+    int s0 = first(j), s1 = first(j + 1);
+    int a0 = j > 0 ? first(j - 1) : 0, a1 = j > 0 ? s0 : 0;
+    const int n = s1 - s0 > a1 - a0 ? s1 - s0 : a1 - a0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n * p.slices));
+    cfg.blockDim = dim3(kGnThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = j > 0 ? 1 : 0;   // the first launch waits for the stream as any other
+    void* args[] = {&a, &s0, &s1, &a0, &a1};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return LN_OK;
+}
+
+}  // namespace
+}  // namespace nf
+
+using namespace nf;
+
+extern "C" {
+
+ln_status gn_workspace_bytes(int64_t samples, int64_t rows, int64_t channels, int64_t groups,
+                             ln_dtype dtype, int backward, size_t* bytes) {
+  if (bytes == nullptr) return LN_ERR_NULL;
+  const GnCall c = {samples, rows, channels, groups, dtype};
+  ln_status s = check_shape(c);
+  if (s != LN_OK) return s;
+  *bytes = 0;
+  if (samples == 0 || rows == 0) return LN_OK;
+  size_t need = 0;
+  for (int v = 0; v < 2; ++v) {
+    if (v && (channels * (int64_t)elem_size(dtype)) % 16 != 0) continue;
+    GnPlan p;
+    s = plan_call(c, backward != 0, v != 0, &p);
+    if (s != LN_OK) return s;
+    if (p.bytes() > need) need = p.bytes();
+  }
+  *bytes = need;
+  return LN_OK;
+}
+
+ln_status gn_fwd(const void* x, int64_t x_sample, int64_t x_row, const void* gamma,
+                 const void* beta, int64_t param_sample, float eps, gn_act act,
+                 int zero_centered_gamma, void* y, int64_t y_sample, int64_t y_row, float* mean,
+                 float* rstd, cudaStream_t stream, int64_t samples, int64_t rows,
+                 int64_t channels, int64_t groups, ln_dtype dtype, void* workspace,
+                 size_t workspace_bytes) {
+  const GnCall c = {samples, rows, channels, groups, dtype};
+  ln_status s = check_shape(c);
+  if (s != LN_OK) return s;
+  if (act != GN_ACT_NONE && act != GN_ACT_SILU && act != GN_ACT_GELU) return LN_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return LN_ERR_INVALID;
+  if (x_sample < 0 || x_row < 0 || y_sample < 0 || y_row < 0) return LN_ERR_INVALID;
+  if (param_sample != 0 && param_sample < channels) return LN_ERR_INVALID;
+  const bool some = samples > 0 && rows > 0;
+  if (some && (x == nullptr || y == nullptr)) return LN_ERR_NULL;
+  const size_t es = elem_size(dtype);
+  const void* tensors[] = {x, gamma, beta, y};
+  for (const void* t : tensors)
+    if (!aligned(t, es)) return LN_ERR_ALIGN;
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return LN_ERR_ALIGN;
+  const Strided sx = tensor(x, x_sample, x_row, c), sy = tensor(y, y_sample, y_row, c);
+  if (self_overlaps(sy) || may_overlap(sy, sx)) return LN_ERR_INVALID;
+  const size_t stats = (size_t)samples * groups * 4;
+  const size_t params = samples > 0 ? ((size_t)(samples - 1) * param_sample + channels) * es : 0;
+  const Range outs[] = {{mean, stats}, {rstd, stats}, {workspace, workspace_bytes}};
+  const Range ins[] = {sx.range(), {gamma, params}, {beta, params}, sy.range()};
+  if (any_overlap(outs, 3, ins, 4)) return LN_ERR_INVALID;
+  const Range yr = sy.range();
+  if (any_overlap(&yr, 1, ins + 1, 2)) return LN_ERR_INVALID;
+  if (samples == 0) return LN_OK;
+  if (rows == 0) {
+    cudaError_t e = cudaSuccess;
+    if (mean) e = cudaMemsetAsync(mean, 0, stats, stream);
+    if (e == cudaSuccess && rstd) e = cudaMemsetAsync(rstd, 0, stats, stream);
+    return e == cudaSuccess ? LN_OK : cuda_fail(e);
+  }
+  const bool vec = (channels * (int64_t)es) % 16 == 0 && vec_ok(x, x_sample, x_row, es) &&
+                   vec_ok(y, y_sample, y_row, es) && vec_ok(gamma, param_sample, 0, es) &&
+                   vec_ok(beta, param_sample, 0, es);
+  GnPlan p;
+  s = plan_call(c, false, vec, &p);
+  if (s != LN_OK) return s;
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < p.bytes())
+    return LN_ERR_WORKSPACE;
+  GnArgs a = {};
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.out = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.part = static_cast<float2*>(workspace);
+  a.x_sample = x_sample;
+  a.x_row = x_row;
+  a.out_sample = y_sample;
+  a.out_row = y_row;
+  a.param_sample = param_sample;
+  a.eps = eps;
+  a.zero_centered = zero_centered_gamma ? 1 : 0;
+  return launch(c, p, a, false, vec, (int)act, stream);
+}
+
+ln_status gn_bwd(const void* dy, int64_t dy_sample, int64_t dy_row, const void* x,
+                 int64_t x_sample, int64_t x_row, const void* gamma, const void* beta,
+                 int64_t param_sample, gn_act act, int zero_centered_gamma, const float* mean,
+                 const float* rstd, void* dx, int64_t dx_sample, int64_t dx_row, void* dgamma,
+                 void* dbeta, cudaStream_t stream, int64_t samples, int64_t rows,
+                 int64_t channels, int64_t groups, ln_dtype dtype, ln_dtype grad_dtype,
+                 void* workspace, size_t workspace_bytes) {
+  const GnCall c = {samples, rows, channels, groups, dtype};
+  ln_status s = check_shape(c);
+  if (s != LN_OK) return s;
+  if (!known_dtype(grad_dtype)) return LN_ERR_UNSUPPORTED;
+  if (act != GN_ACT_NONE && act != GN_ACT_SILU && act != GN_ACT_GELU) return LN_ERR_UNSUPPORTED;
+  if (dy_sample < 0 || dy_row < 0 || x_sample < 0 || x_row < 0 || dx_sample < 0 || dx_row < 0)
+    return LN_ERR_INVALID;
+  if (param_sample != 0 && param_sample < channels) return LN_ERR_INVALID;
+  const bool some = samples > 0 && rows > 0;
+  if (some && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr ||
+               dx == nullptr))
+    return LN_ERR_NULL;
+  const size_t es = elem_size(dtype), gs = elem_size(grad_dtype);
+  const void* tensors[] = {dy, x, gamma, beta, dx};
+  for (const void* t : tensors)
+    if (!aligned(t, es)) return LN_ERR_ALIGN;
+  if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, gs) || !aligned(dbeta, gs))
+    return LN_ERR_ALIGN;
+  const Strided sx = tensor(x, x_sample, x_row, c), sd = tensor(dy, dy_sample, dy_row, c),
+                so = tensor(dx, dx_sample, dx_row, c);
+  if (self_overlaps(so) || may_overlap(so, sx) || may_overlap(so, sd)) return LN_ERR_INVALID;
+  const size_t stats = (size_t)samples * groups * 4;
+  const size_t params = samples > 0 ? ((size_t)(samples - 1) * param_sample + channels) * es : 0;
+  const int64_t grad_rows = param_sample != 0 ? samples : 1;
+  const size_t grads = (size_t)grad_rows * channels * gs;
+  const Range outs[] = {{dgamma, grads}, {dbeta, grads}, {workspace, workspace_bytes}};
+  const Range ins[] = {sd.range(), sx.range(), {gamma, params}, {beta, params}, {mean, stats},
+                       {rstd, stats}, so.range()};
+  if (any_overlap(outs, 3, ins, 7)) return LN_ERR_INVALID;
+  const Range dr = so.range();
+  if (any_overlap(&dr, 1, ins + 2, 4)) return LN_ERR_INVALID;
+  if (!some) {
+    cudaError_t e = cudaSuccess;
+    if (dgamma && grads) e = cudaMemsetAsync(dgamma, 0, grads, stream);
+    if (e == cudaSuccess && dbeta && grads) e = cudaMemsetAsync(dbeta, 0, grads, stream);
+    return e == cudaSuccess ? LN_OK : cuda_fail(e);
+  }
+  if (grad_rows > 65535) return LN_ERR_SHAPE;   // rows of the finalize's grid
+  const bool vec = (channels * (int64_t)es) % 16 == 0 && vec_ok(x, x_sample, x_row, es) &&
+                   vec_ok(dy, dy_sample, dy_row, es) && vec_ok(dx, dx_sample, dx_row, es) &&
+                   vec_ok(gamma, param_sample, 0, es) && vec_ok(beta, param_sample, 0, es);
+  GnPlan p;
+  s = plan_call(c, true, vec, &p);
+  if (s != LN_OK) return s;
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < p.bytes())
+    return LN_ERR_WORKSPACE;
+  GnArgs a = {};
+  a.x = x;
+  a.dy = dy;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.out = dx;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.part = static_cast<float2*>(workspace);
+  a.cols = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_bytes);
+  a.x_sample = x_sample;
+  a.x_row = x_row;
+  a.dy_sample = dy_sample;
+  a.dy_row = dy_row;
+  a.out_sample = dx_sample;
+  a.out_row = dx_row;
+  a.param_sample = param_sample;
+  a.zero_centered = zero_centered_gamma ? 1 : 0;
+  s = launch(c, p, a, true, vec, (int)act, stream);
+  if (s != LN_OK || (dgamma == nullptr && dbeta == nullptr)) return s;
+  const int H = (int)channels;
+  const int64_t P = (param_sample != 0 ? 1 : samples) * p.slices;
+  const cudaError_t e = launch_bwd_finalize(a.cols, (int)P, 2 * H, H, true, dgamma, dbeta, nullptr,
+                                            (int)grad_dtype, stream, (int)grad_rows);
+  return e == cudaSuccess ? LN_OK : cuda_fail(e);
+}
+
+}  // extern "C"

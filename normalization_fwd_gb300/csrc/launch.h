@@ -99,10 +99,11 @@ cudaError_t softmax_launch(const SmxArgs& a, const Plan& p, cudaStream_t st);
 // Fixed-order sum of the backward's per-CTA partials (finalize.cu).
 // Columns of a partial row: [0, H) dgamma, then [H, 2H) dbeta when `beta_cols`,
 // then H columns of dbias when dbias is non-null. out_dtype: 0 fp32,
-// 1 bf16, 2 fp16 (the ln_dtype codes) for all three outputs.
+// 1 bf16, 2 fp16 (the ln_dtype codes) for all three outputs. `outer` sums of
+// P partial rows each, one after the other in ws and in the outputs.
 cudaError_t launch_bwd_finalize(const float* ws, int P, int C, int H, bool beta_cols,
                                 void* dgamma, void* dbeta, void* dbias, int out_dtype,
-                                cudaStream_t st);
+                                cudaStream_t st, int outer = 1);
 
 }  // namespace nf
 

@@ -1,0 +1,376 @@
+// Rotary positions (Su et al., 2021) of attention heads, with the RMSNorm of
+// each head before the rotation where a gamma is given:
+//   u = x * rstd * w, rstd = 1/sqrt(sum x^2 / D + eps)      (or u = x)
+//   y0 = s (u0 cos t - u1 sin t), y1 = s (u1 cos t + u0 sin t)
+// for the pairs (j, j + rot/2) or (2j, 2j + 1) of the first `rot` elements;
+// the others pass through. The backward applies the transposed rotation to
+// dy, then the RMSNorm's: with g' the rotated-back gradient, dgamma sums
+// g' * xhat over tokens and heads, g = g' * w,
+//   dx = rstd (g - xhat * sum(g * xhat) / D).
+// The statistics are taken anew from x, whose head is in registers anyway.
+//
+// Angles: a position times a frequency passes fp32's precision at a few
+// thousand radians. A frequency is turned into a 64-bit fraction of a turn,
+// the product with the integer position is taken modulo 2^64, which is
+// modulo one turn exactly, and its top 32 bits go to sincospi. The error is
+// that of the frequency itself times the position, plus 2^-32 turns.
+#pragma once
+
+#include "common.cuh"
+
+namespace nf {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxDim = 512;
+constexpr int kRopeMaxAxes = 4;
+
+// One of the tensors a call takes (queries or keys).
+struct RopeSide {
+  const void* in;        // x, or dy in the backward
+  const void* x;         // backward: the forward's x, when gamma is given
+  void* out;             // y, or dx
+  const void* gamma;     // nullable: no norm
+  int heads;             // 0: absent
+  int chunks;            // ceil(heads / heads_per_unit)
+  int64_t in_s[3], x_s[3], out_s[3];   // strides of batch, token, head (elements)
+};
+
+struct RopeArgs {
+  RopeSide side[2];
+  const void* pos;
+  const double* freqs;   // [axes][rot / 2] radians a position
+  int64_t pos_s[3];      // strides of axis, batch, token (elements)
+  int64_t tokens;        // of a sequence
+  int64_t units_tokens;  // batch * tokens
+  float* ws;             // backward: [max of blocks][2 * dim] partials, or null
+  int blocks[2];         // CTAs of each side, the queries' first
+  int pos64, axes;
+  int dim, rot;
+  int lanes;             // threads of one head, a power of two <= 32
+  int heads_per_unit;
+  float scale, eps, inv_dim;
+  int zero_centered;
+};
+
+// VEC elements from memory; ALIGNED: one access of VEC * sizeof(T) bytes.
+template <typename T, int VEC, bool ALIGNED>
+__device__ __forceinline__ void rope_load(const T* p, float* f) {
+  constexpr int B = VEC * (int)sizeof(T);
+  union {
+    uint4 q;
+    uint2 d;
+    unsigned w;
+    T t[VEC];
+  } u;
+  if (ALIGNED && B == 16) u.q = *reinterpret_cast<const uint4*>(p);
+  else if (ALIGNED && B == 8) u.d = *reinterpret_cast<const uint2*>(p);
+  else if (ALIGNED && B == 4) u.w = *reinterpret_cast<const unsigned*>(p);
+  else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) u.t[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = to_f(u.t[i]);
+}
+template <typename T, int VEC, bool ALIGNED>
+__device__ __forceinline__ void rope_store(T* p, const float* f) {
+  constexpr int B = VEC * (int)sizeof(T);
+  union {
+    uint4 q;
+    uint2 d;
+    unsigned w;
+    T t[VEC];
+  } u;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) u.t[i] = from_f<T>(f[i]);
+  if (ALIGNED && B == 16) *reinterpret_cast<uint4*>(p) = u.q;
+  else if (ALIGNED && B == 8) *reinterpret_cast<uint2*>(p) = u.d;
+  else if (ALIGNED && B == 4) *reinterpret_cast<unsigned*>(p) = u.w;
+  else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = u.t[i];
+  }
+}
+
+// A frequency in radians as a 64-bit fraction of a turn: f * 2^64 / (2 pi)
+// modulo 2^64, by integers (double arithmetic is slow on this part). With
+// f = m * 2^e, m of 53 bits, and K = 2^130 / (2 pi), rounded to 128 bits, it
+// is (m * K) >> (66 - e), bits 64 and up of which fall away. Off by less than
+// 2^-64 turns for frequencies up to 2^60.
+__device__ __forceinline__ unsigned long long turns_of(double f) {
+  const unsigned long long k1 = 0xa2f9836e4e441529ull, k0 = 0xfc2757d1f534ddc1ull;
+  const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
+  const int ex = (int)(bits >> 52) & 0x7ff;
+  if (ex == 0 || ex == 0x7ff) return 0;   // zero, below 2^-1022, or not finite
+  const unsigned long long m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  // m * K = (w2, w1, w0)
+  const unsigned long long w0 = m * k0, w1 = m * k1 + __umul64hi(m, k0);
+  const unsigned long long w2 = __umul64hi(m, k1) + (w1 < m * k1 ? 1 : 0);
+  const int sh = 1077 - ex;               // t = (w2, w1, w0) >> (64 + sh)
+  unsigned long long t;
+  if (sh >= 128) t = 0;
+  else if (sh >= 64) t = w2 >> (sh - 64);
+  else if (sh > 0) t = (w1 >> sh) | (w2 << (64 - sh));
+  else if (sh == 0) t = w1;
+  else t = sh > -64 ? (w1 << -sh) | (w0 >> (64 + sh)) : 0;
+  return (long long)bits < 0 ? 0ull - t : t;
+}
+
+// Which vectors a head's lane slot s holds. The first `rot` elements make
+// rot / 2 pairs; HALF: vectors (s, s + rv) of the rotated part, then pairs
+// of vectors of what passes through; INTER: vectors s and s + ceil(nv / 2),
+// each holding VEC / 2 neighbouring pairs.
+struct RopeSlot {
+  int a, b;              // first elements of the two vectors
+  bool on, on_b;
+  unsigned turned;       // bit i: pair i of the slot is rotated
+};
+// Pair number of a slot's pair i (HALF: that of the vectors' elements i;
+// INTER: VEC / 2 pairs of the first vector, then those of the second).
+template <int VEC, bool INTER> __device__ __forceinline__ int rope_pair(const RopeSlot& r, int i) {
+  if (!INTER) return r.a + i;
+  return i < VEC / 2 ? r.a / 2 + i : r.b / 2 + i - VEC / 2;
+}
+template <int VEC, bool INTER>
+__device__ __forceinline__ RopeSlot rope_slot(int s, int dim, int rot) {
+  RopeSlot r;
+  const int nv = dim / VEC;
+  if (INTER) {
+    const int n2 = (nv + 1) / 2;
+    r.on = s < n2;
+    r.on_b = r.on && s + n2 < nv;
+    r.a = s * VEC;
+    r.b = (s + n2) * VEC;
+    r.turned = 0;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (r.on && rope_pair<VEC, true>(r, i) < rot / 2) r.turned |= 1u << i;
+  } else {
+    const int rv = rot / 2 / VEC;
+    if (s < rv) {
+      r.on = r.on_b = true;
+      r.turned = (1u << VEC) - 1;
+      r.a = s * VEC;
+      r.b = (s + rv) * VEC;
+    } else {
+      const int np = nv - 2 * rv, n2 = (np + 1) / 2, p = s - rv;
+      r.on = p < n2;
+      r.on_b = r.on && p + n2 < np;
+      r.turned = 0;
+      r.a = (2 * rv + p) * VEC;
+      r.b = (2 * rv + p + n2) * VEC;
+    }
+  }
+  return r;
+}
+
+// Rotate a slot's pairs in place by (cos, sin); INV: the transposed
+// rotation. Pairs that pass through are not touched (an infinity times a
+// sine of 0 would be a NaN in its neighbour).
+template <int VEC, bool INTER, bool INV>
+__device__ __forceinline__ void rope_rotate(float (*v)[VEC], const float* cs, const float* sn,
+                                            unsigned turned) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    constexpr int H = VEC > 1 ? VEC / 2 : 1;   // pairs of a vector (INTER)
+    float& p = INTER ? v[i / H][2 * (i % H) % VEC] : v[0][i];
+    float& q = INTER ? v[i / H][(2 * (i % H) + 1) % VEC] : v[1][i];
+    const float c = cs[i], s = INV ? -sn[i] : sn[i];
+    const float p0 = p, q0 = q;
+    if (turned >> i & 1) {
+      p = p0 * c - q0 * s;
+      q = q0 * c + p0 * s;
+    }
+  }
+}
+
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A group of `lanes` threads takes a unit: one token and up to
+// heads_per_unit of its heads, whose cos and sin it works out once. A CTA
+// works on the queries or on the keys.
+template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool BWD>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs A) {
+  const int L = A.lanes, per_cta = kRopeThreads / L;
+  const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
+  RopeSlot slot[NS];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER>(l + n * L, A.dim, A.rot);
+  extern __shared__ float red[];
+  const int side = (int)blockIdx.x >= A.blocks[0] ? 1 : 0;
+  const int blk = blockIdx.x - (side ? A.blocks[0] : 0), blks = A.blocks[side];
+  {
+    const RopeSide& S = A.side[side];
+    const bool norm = S.gamma != nullptr;
+    float w[NS][2][VEC], acc[NS][2][VEC];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        w[n][0][i] = w[n][1][i] = 1.f;
+        acc[n][0][i] = acc[n][1][i] = 0.f;
+      }
+    if (norm) {
+      const T* gm = static_cast<const T*>(S.gamma);
+      const float add = A.zero_centered ? 1.f : 0.f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (slot[n].on) w[n][0][i] = to_f(gm[slot[n].a + i]) + add;
+          if (slot[n].on_b) w[n][1][i] = to_f(gm[slot[n].b + i]) + add;
+        }
+      }
+    }
+    const int64_t units = A.units_tokens * S.chunks;
+    // Whole warps run the loop, so that every lane reaches the shuffles.
+    const int64_t steps = (units + (int64_t)blks * per_cta - 1) / ((int64_t)blks * per_cta);
+    for (int64_t st = 0; st < steps; ++st) {
+      const int64_t u = (st * blks + blk) * per_cta + grp;
+      const bool live = u < units;
+      const int64_t tok = live ? u / S.chunks : 0;
+      const int h0 = live ? (int)(u - tok * S.chunks) * A.heads_per_unit : 0;
+      const int nh = live ? min(A.heads_per_unit, S.heads - h0) : 0;
+      const int64_t bi = tok / A.tokens, ti = tok - bi * A.tokens;
+      float cs[NS][VEC], sn[NS][VEC];
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const int j = rope_pair<VEC, INTER>(slot[n], i);
+          cs[n][i] = 1.f;
+          sn[n][i] = 0.f;
+          if (live && (slot[n].turned >> i & 1)) {
+            unsigned long long t = 0;
+            for (int ax = 0; ax < A.axes; ++ax) {
+              const int64_t at = ax * A.pos_s[0] + bi * A.pos_s[1] + ti * A.pos_s[2];
+              const int64_t p = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
+                                        : (int64_t)static_cast<const int*>(A.pos)[at];
+              t += (unsigned long long)p * turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
+            }
+            const int top = (int)((t + 0x80000000ull) >> 32);   // signed 2^-32 turns
+            float s, c;
+            sincospif((float)top * 0x1p-31f, &s, &c);
+            cs[n][i] = c * A.scale;
+            sn[n][i] = s * A.scale;
+          }
+        }
+      const int most = __reduce_max_sync(0xffffffffu, nh);
+      for (int h = 0; h < most; ++h) {
+        const bool act = h < nh;
+        const int64_t in_at = bi * S.in_s[0] + ti * S.in_s[1] + (int64_t)(h0 + h) * S.in_s[2];
+        const int64_t out_at = bi * S.out_s[0] + ti * S.out_s[1] + (int64_t)(h0 + h) * S.out_s[2];
+        const T* in = static_cast<const T*>(S.in) + in_at;
+        T* out = static_cast<T*>(S.out) + out_at;
+        float v[NS][2][VEC], xv[BWD ? NS : 1][2][VEC];
+        float ss = 0.f, gs = 0.f;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[n][0][i] = v[n][1][i] = 0.f;
+          if (act && slot[n].on) {
+            rope_load<T, VEC, ALIGNED>(in + slot[n].a, v[n][0]);
+            if (slot[n].on_b) rope_load<T, VEC, ALIGNED>(in + slot[n].b, v[n][1]);
+          }
+        }
+        if (!BWD) {
+          float rstd = 1.f;
+          if (norm) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                ss = fmaf(v[n][0][i], v[n][0][i], ss);
+                ss = fmaf(v[n][1][i], v[n][1][i], ss);
+              }
+            ss = lanes_sum(ss, L);
+            rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
+          }
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+            if (norm) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                v[n][0][i] = v[n][0][i] * rstd * w[n][0][i];
+                v[n][1][i] = v[n][1][i] * rstd * w[n][1][i];
+              }
+            }
+            rope_rotate<VEC, INTER, false>(v[n], cs[n], sn[n], slot[n].turned);
+          }
+        } else {
+          const T* xp = static_cast<const T*>(S.x) + bi * S.x_s[0] + ti * S.x_s[1] +
+                        (int64_t)(h0 + h) * S.x_s[2];
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) xv[n][0][i] = xv[n][1][i] = 0.f;
+            if (norm && act && slot[n].on) {
+              rope_load<T, VEC, ALIGNED>(xp + slot[n].a, xv[n][0]);
+              if (slot[n].on_b) rope_load<T, VEC, ALIGNED>(xp + slot[n].b, xv[n][1]);
+            }
+            rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
+          }
+          if (norm) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) ss = fmaf(xv[n][k][i], xv[n][k][i], ss);
+            ss = lanes_sum(ss, L);
+            const float rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                  xv[n][k][i] *= rstd;
+                  if (act) acc[n][k][i] = fmaf(v[n][k][i], xv[n][k][i], acc[n][k][i]);
+                  v[n][k][i] *= w[n][k][i];
+                  gs = fmaf(v[n][k][i], xv[n][k][i], gs);
+                }
+            gs = lanes_sum(gs, L) * A.inv_dim;
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[n][k][i] = rstd * fmaf(-xv[n][k][i], gs, v[n][k][i]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          if (act && slot[n].on) {
+            rope_store<T, VEC, ALIGNED>(out + slot[n].a, v[n][0]);
+            if (slot[n].on_b) rope_store<T, VEC, ALIGNED>(out + slot[n].b, v[n][1]);
+          }
+        }
+      }
+    }
+    if (BWD && A.ws != nullptr) {
+      // The groups' sums, added in their order, into this CTA's partial row.
+      // The side with fewer CTAs has its other rows zeroed by the other side.
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (slot[n].on) red[grp * A.dim + slot[n].a + i] = acc[n][0][i];
+          if (slot[n].on_b) red[grp * A.dim + slot[n].b + i] = acc[n][1][i];
+        }
+      __syncthreads();
+      float* row = A.ws + (int64_t)blk * 2 * A.dim;
+      for (int d = threadIdx.x; d < A.dim; d += kRopeThreads) {
+        float t = 0.f;
+        for (int g = 0; g < per_cta; ++g) t += red[g * A.dim + d];
+        row[side * A.dim + d] = t;
+        if (blk >= A.blocks[1 - side]) row[(1 - side) * A.dim + d] = 0.f;
+      }
+    }
+  }
+}
+
+}  // namespace nf
