@@ -9,9 +9,9 @@
 
 namespace nf {
 
-const void* gn_table_f32(bool bwd, bool vec, int act);
-const void* gn_table_bf16(bool bwd, bool vec, int act);
-const void* gn_table_f16(bool bwd, bool vec, int act);
+const void* gn_table_f32(bool bwd, bool cluster, bool vec, int act);
+const void* gn_table_bf16(bool bwd, bool cluster, bool vec, int act);
+const void* gn_table_f16(bool bwd, bool cluster, bool vec, int act);
 
 namespace {
 
@@ -29,9 +29,11 @@ int gcd(int a, int b) {
   return a;
 }
 
-// How a call is cut up: column tiles, slices of the rows and batches of
-// panels (a panel is one sample's column tile).
+// How a call is cut up: column tiles, slices of the rows and, where it takes
+// more than one launch, batches of panels (a panel is one sample's column
+// tile).
 struct GnPlan {
+  bool cluster;            // one launch, a cluster a panel
   int tiles, tw, max_groups, slices;
   int64_t slice_rows;
   int64_t panels, batch;   // all panels, and those of one launch
@@ -40,22 +42,24 @@ struct GnPlan {
 };
 
 constexpr int64_t kBatchBytes = 48ll << 20;
+constexpr int kTileBytes = 128;
+constexpr int kClusterCtas = 4;              // CTAs an SM that clusters aim for
+constexpr int64_t kSlabBytes = 4ll << 20;
 
-bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es, bool bwd, bool vec,
-             int sms, GnPlan* p) {
-  const int V = vec ? (int)(16 / es) : 1;
-  const int nv = channels / V, cpg = channels / groups;
-  const int most = vec ? 64 : 256, target = vec ? 32 : 256;
-  const int lv = cpg / gcd(cpg, V);   // vectors that whole groups and whole vectors fill
-  bool whole = true;                  // every group lies in one tile
+// Column tiles of about `target` vectors. Whole groups and whole vectors
+// where `lv`, the vectors that both fill, is no more than `most`; false when
+// a tile may end inside a group.
+bool gn_tiles(int nv, int lv, int target, int most, GnPlan* p) {
   int tw = nv;
+  bool whole = true;
   if (nv > target) {
     if (lv <= most) {
       const int units = nv / lv;
-      int per = target / lv > 0 ? target / lv : 1;
+      int per = (target + lv - 1) / lv;
+      if (per * lv > most) per = most / lv;
+      if (per > units) per = units;
       const int t = (units + per - 1) / per;
-      per = (units + t - 1) / t;
-      tw = per * lv;
+      tw = (units + t - 1) / t * lv;
     } else {
       const int t = (nv + target - 1) / target;
       tw = (nv + t - 1) / t;
@@ -64,28 +68,48 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
   }
   p->tw = tw;
   p->tiles = (nv + tw - 1) / tw;
-  const int tc = tw * V;
+  return whole;
+}
+
+bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es, bool bwd, bool vec,
+             int sms, GnPlan* p) {
+  const int V = vec ? (int)(16 / es) : 1;
+  const int nv = channels / V, cpg = channels / groups;
+  const int most = vec ? 64 : 256;
+  const int vb = V * (int)es;                       // bytes of a vector
+  const int lv = cpg / gcd(cpg, V);
+  const int target = kTileBytes / vb < most ? kTileBytes / vb : most;
+  const bool whole = gn_tiles(nv, lv, target, most, p);
+  const int tc = p->tw * V, TY = kGnThreads / p->tw;
+  p->panels = samples * p->tiles;
   p->max_groups = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
   if (p->max_groups > groups) p->max_groups = groups;
-  p->panels = samples * p->tiles;
-  const double per_panel = (double)rows * tc * es * (bwd ? 2 : 1);
-  p->batch = p->panels;
-  if (per_panel * p->panels > (double)kBatchBytes) {
-    const int64_t step = whole ? 1 : p->tiles;
-    int64_t b = (int64_t)(kBatchBytes / per_panel) / step * step;
-    p->batch = b < step ? step : b;
-    if (p->batch > p->panels) p->batch = p->panels;
+  const double slab = (double)rows * tc * es * (bwd ? 2 : 1);   // what a panel reads
+  p->cluster = whole && slab <= (double)kSlabBytes;
+  if (p->cluster) {
+    int s = 1;
+    while (s < 16 && p->panels * s < (int64_t)sms * kClusterCtas && rows > (int64_t)s * TY * 2) s *= 2;
+    p->slices = s;
+    p->slice_rows = (rows + s - 1) / s;
+    p->batch = p->panels;
+    p->part_bytes = 0;
+  } else {
+    p->batch = p->panels;
+    if (slab * p->panels > (double)kBatchBytes) {
+      const int64_t step = whole ? 1 : p->tiles;
+      int64_t b = (int64_t)(kBatchBytes / slab) / step * step;
+      p->batch = b < step ? step : b;
+      if (p->batch > p->panels) p->batch = p->panels;
+    }
+    int64_t slices = ((int64_t)sms * 4 + p->batch - 1) / p->batch;
+    const int64_t least = 4 * TY;       // rows of a slice: four a thread
+    if (slices > (rows + least - 1) / least) slices = (rows + least - 1) / least;
+    if (slices < 1) slices = 1;
+    p->slice_rows = (rows + slices - 1) / slices;
+    p->slices = (int)((rows + p->slice_rows - 1) / p->slice_rows);
+    p->part_bytes = (size_t)p->panels * p->slices * p->max_groups * sizeof(float2);
+    p->part_bytes = (p->part_bytes + 15) / 16 * 16;
   }
-  const int TY = kGnThreads / tw;
-  const int64_t want = (int64_t)sms * 6;
-  int64_t slices = (want + p->batch - 1) / p->batch;
-  const int64_t least = 4 * TY;       // rows of a slice: four a thread
-  if (slices > (rows + least - 1) / least) slices = (rows + least - 1) / least;
-  if (slices < 1) slices = 1;
-  p->slice_rows = (rows + slices - 1) / slices;
-  p->slices = (int)((rows + p->slice_rows - 1) / p->slice_rows);
-  p->part_bytes = (size_t)p->panels * p->slices * p->max_groups * sizeof(float2);
-  p->part_bytes = (p->part_bytes + 15) / 16 * 16;
   p->cols_bytes = bwd ? (size_t)samples * p->slices * 2 * channels * sizeof(float) : 0;
   return p->panels * p->slices <= INT32_MAX;
 }
@@ -144,9 +168,29 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
   a.max_groups = p.max_groups;
   a.rows = c.rows;
   a.inv_m = (float)(1.0 / ((double)c.rows * a.cpg));
-  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, vec, act)
-                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, vec, act)
-                                        : gn_table_f16(bwd, vec, act);
+  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, act)
+                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, act)
+                                        : gn_table_f16(bwd, p.cluster, vec, act);
+  if (p.cluster) {
+    if (p.slices > 8) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return cuda_fail(e);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.panels * p.slices));
+    cfg.blockDim = dim3(kGnThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.slices;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&a};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    return e == cudaSuccess ? LN_OK : cuda_fail(e);
+  }
   // Launch j takes the statistics of batch j and applies batch j - 1, whose
   // rows are then still in the L2 cache.
   const int64_t batches = (p.panels + p.batch - 1) / p.batch;
@@ -240,7 +284,8 @@ ln_status gn_fwd(const void* x, int64_t x_sample, int64_t x_row, const void* gam
   GnPlan p;
   s = plan_call(c, false, vec, &p);
   if (s != LN_OK) return s;
-  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < p.bytes())
+  if (p.bytes() > 0 &&
+      (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < p.bytes()))
     return LN_ERR_WORKSPACE;
   GnArgs a = {};
   a.x = x;

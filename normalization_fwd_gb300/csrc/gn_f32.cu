@@ -2,7 +2,7 @@
 #include "gn_table.cuh"
 
 namespace nf {
-const void* gn_table_f32(bool bwd, bool vec, int act) {
-  return vec ? gn_table<float, Vec<float>::N>(bwd, act) : gn_table<float, 1>(bwd, act);
+const void* gn_table_f32(bool bwd, bool cluster, bool vec, int act) {
+  return vec ? gn_table<float, Vec<float>::N>(bwd, cluster, act) : gn_table<float, 1>(bwd, cluster, act);
 }
 }  // namespace nf

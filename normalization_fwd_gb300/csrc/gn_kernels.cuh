@@ -109,7 +109,7 @@ __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice)
   u.c1 = min(a.channels, u.c0 + a.tw * VEC);
   u.g0 = u.c0 / a.cpg;
   u.ng = (u.c1 - 1) / a.cpg - u.g0 + 1;
-  u.r0 = (int64_t)slice * a.slice_rows;
+  u.r0 = min(a.rows, (int64_t)slice * a.slice_rows);   // a cluster's last CTAs may have none
   u.r1 = min(a.rows, u.r0 + a.slice_rows);
   return u;
 }
@@ -143,8 +143,8 @@ __device__ __forceinline__ void gn_params(const GnArgs& a, int n, int c, float* 
 struct GnSmem {
   float a[kGnThreads * 8];
   float b[kGnThreads * 8];
-  float g0[kGnMaxTileCh];
-  float g1[kGnMaxTileCh];
+  float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
+  float g1[kGnMaxTileCh];       // rstd, or c2
 };
 
 // ---- forward: partial statistics of one unit -------------------------------------
@@ -155,7 +155,8 @@ struct GnSmem {
 // The threads' (mean, M2) are merged by the parallel-variance identity
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
 template <typename T, int VEC>
-__device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
+__device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                              float2* out) {
   const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
   const int c = u.c0 + tx * VEC;
   const bool on = ty < TY && c < u.c1;
@@ -224,7 +225,8 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
       const int k = gn_lane_rows(n_rows, y, TY);
       if (k > 0) s = fmaf((float)k, sm.a[at] - base, s);
     }
-    const float m = base + group_sum<32>(s) / ((float)n_rows * (float)nc);
+    s = group_sum<32>(s);
+    const float m = n_rows > 0 ? base + s / ((float)n_rows * (float)nc) : 0.f;
     s = 0.f;
     for (int e = lane; e < total; e += 32) {
       const int y = e / nc, at = y * (a.tw * VEC) + cs + (e - y * nc);
@@ -233,11 +235,27 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
       if (k > 0) s += fmaf((float)k * d, d, sm.b[at]);
     }
     s = group_sum<32>(s);
-    if (lane == 0)
-      a.part[(((int64_t)u.n * a.tiles + u.tile) * a.slices + u.slice) * a.max_groups + lg] =
-          make_float2(m, s);
+    if (lane == 0) out[lg] = make_float2(m, s);
   }
   __syncthreads();
+}
+
+// What the merged sums become: mean and rstd (forward, stored by one CTA of
+// the group's), or c1 and c2.
+template <bool BWD>
+__device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSmem& sm, int lg,
+                                          float s0, float s1, bool store) {
+  if (!BWD) {
+    if (s1 < 0.f) s1 = 0.f;   // rounding alone; a NaN stays one
+    s1 = 1.f / sqrtf(s1 + a.eps);
+    if (store) {
+      const int64_t g = (int64_t)u.n * a.groups + u.g0 + lg;
+      if (a.mean != nullptr) a.mean[g] = s0;
+      if (a.rstd != nullptr) a.rstd[g] = s1;
+    }
+  }
+  sm.g0[lg] = s0;
+  sm.g1[lg] = s1;
 }
 
 // Merge the partials of the unit's groups into sm.g0 = mean, sm.g1 = rstd
@@ -284,17 +302,51 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
         }
       }
       s1 = group_sum<32>(s1) * a.inv_m;
-      if (s1 < 0.f) s1 = 0.f;   // rounding alone; a NaN stays one
-      s1 = 1.f / sqrtf(s1 + a.eps);
     }
-    if (lane == 0) {
-      sm.g0[lg] = s0;
-      sm.g1[lg] = s1;
-      if (!BWD && u.slice == 0 && u.tile == t0) {
-        if (a.mean != nullptr) a.mean[(int64_t)u.n * a.groups + g] = s0;
-        if (a.rstd != nullptr) a.rstd[(int64_t)u.n * a.groups + g] = s1;
-      }
+    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0 && u.tile == t0);
+  }
+  __syncthreads();
+}
+
+// ---- clusters -----------------------------------------------------------------------
+// A thread-block cluster shares a panel: its CTAs are the slices, and the
+// partials stay in their shared memory, read from one another.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 cluster_read(const float2* p, int rank) {
+  const unsigned at = (unsigned)__cvta_generic_to_shared(p);
+  unsigned far;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(far) : "memory");
+  return v;
+}
+
+// The merge of gn_combine over the cluster's CTAs: a lane a CTA.
+template <bool BWD>
+__device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                                   const float2* part) {
+  const int lane = threadIdx.x & 31;
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
+    float2 v = make_float2(0.f, 0.f);
+    if (lane < a.slices) v = cluster_read(part + lg, lane);
+    float s0, s1;
+    if (BWD) {
+      s0 = group_sum<32>(v.x) * a.inv_m;
+      s1 = group_sum<32>(v.y) * a.inv_m;
+    } else {
+      const float base = __shfl_sync(0xffffffffu, v.x, 0);
+      const int64_t nr = min(a.slice_rows, a.rows - lane * a.slice_rows);
+      const float cnt = lane < a.slices && nr > 0 ? (float)nr * (float)a.cpg : 0.f;
+      s0 = base + group_sum<32>(cnt * (lane < a.slices ? v.x - base : 0.f)) * a.inv_m;
+      const float d = v.x - s0;
+      s1 = group_sum<32>(lane < a.slices ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
     }
+    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0);
   }
   __syncthreads();
 }
@@ -302,7 +354,6 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
 // ---- forward: normalize one unit -------------------------------------------------
 template <typename T, int VEC, int ACT>
 __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
-  gn_combine<VEC, false>(a, u, sm);
   const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
   const int c = u.c0 + tx * VEC;
   if (ty < TY && c < u.c1) {
@@ -349,7 +400,8 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
 
 // ---- backward: sums of one unit ----------------------------------------------------
 template <typename T, int VEC, int ACT>
-__device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
+__device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                                  float2* out) {
   const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
   const int tc = a.tw * VEC;
   const int c = u.c0 + tx * VEC;
@@ -436,8 +488,7 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
       s.y += sm.b[k];
     }
     s = group_sum2<32>(s);
-    if (lane == 0)
-      a.part[(((int64_t)u.n * a.tiles + u.tile) * a.slices + u.slice) * a.max_groups + lg] = s;
+    if (lane == 0) out[lg] = s;
   }
   __syncthreads();
 }
@@ -445,7 +496,6 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
 // ---- backward: dx of one unit --------------------------------------------------------
 template <typename T, int VEC, int ACT>
 __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
-  gn_combine<VEC, true>(a, u, sm);
   const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
   const int c = u.c0 + tx * VEC;
   if (ty < TY && c < u.c1) {
@@ -506,6 +556,10 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
 }
 
 // ---- kernels ----------------------------------------------------------------------
+__device__ __forceinline__ float2* gn_part(const GnArgs& a, const GnUnit& u) {
+  return a.part + (((int64_t)u.n * a.tiles + u.tile) * a.slices + u.slice) * a.max_groups;
+}
+
 // One launch takes the statistics of the panels [stat0, stat1) and applies
 // those of [app0, app1), which an earlier launch gathered.
 template <typename T, int VEC, int ACT>
@@ -513,10 +567,15 @@ __global__ void __launch_bounds__(kGnThreads)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
-  if (stat0 + p < stat1) gn_stats_unit<T, VEC>(a, gn_unit<VEC>(a, stat0 + p, s), sm);
+  if (stat0 + p < stat1) {
+    const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
+    gn_stats_unit<T, VEC>(a, u, sm, gn_part(a, u));
+  }
   if (app0 + p < app1) {
+    const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_apply_unit<T, VEC, ACT>(a, gn_unit<VEC>(a, app0 + p, s), sm);
+    gn_combine<VEC, false>(a, u, sm);
+    gn_apply_unit<T, VEC, ACT>(a, u, sm);
   }
 }
 
@@ -525,11 +584,48 @@ __global__ void __launch_bounds__(kGnThreads)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
-  if (stat0 + p < stat1) gn_bwd_stats_unit<T, VEC, ACT>(a, gn_unit<VEC>(a, stat0 + p, s), sm);
-  if (app0 + p < app1) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_bwd_apply_unit<T, VEC, ACT>(a, gn_unit<VEC>(a, app0 + p, s), sm);
+  if (stat0 + p < stat1) {
+    const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
+    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, gn_part(a, u));
   }
+  if (app0 + p < app1) {
+    const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    gn_combine<VEC, true>(a, u, sm);
+    gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm);
+  }
+}
+
+// A panel a cluster, in one launch: the statistics, a barrier of the
+// cluster, and the rows again, out of the L2 cache.
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnThreads) gn_fwd_cluster_kernel(GnArgs a) {
+  __shared__ GnSmem sm;
+  __shared__ float2 part[kGnMaxTileCh];
+  const int p = blockIdx.x / a.slices;
+  const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
+  gn_stats_unit<T, VEC>(a, u, sm, part);
+  cluster_arrive();
+  cluster_wait();
+  gn_combine_cluster<false>(a, u, sm, part);
+  cluster_arrive();
+  gn_apply_unit<T, VEC, ACT>(a, u, sm);
+  cluster_wait();   // no CTA leaves while another reads its partials
+}
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnThreads) gn_bwd_cluster_kernel(GnArgs a) {
+  __shared__ GnSmem sm;
+  __shared__ float2 part[kGnMaxTileCh];
+  const int p = blockIdx.x / a.slices;
+  const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
+  gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, part);
+  cluster_arrive();
+  cluster_wait();
+  gn_combine_cluster<true>(a, u, sm, part);
+  cluster_arrive();
+  gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm);
+  cluster_wait();
 }
 
 }  // namespace nf
