@@ -9,7 +9,9 @@
 //
 // A thread owns one 16-byte vector of channels (one element where rows are
 // not 16-byte aligned) for the whole launch, so every sum over rows stays in
-// its registers and the channel parameters are loaded once. Sums are fp32.
+// its registers; the CTA then adds up its columns in shared memory, and one
+// warp a group merges the columns. Sums are fp32. Values go in pairs, which
+// this part adds, multiplies and fmas in one instruction.
 #pragma once
 
 #include "common.cuh"
@@ -19,6 +21,8 @@ namespace nf {
 constexpr int kGnThreads = 256;
 constexpr int kGnWarps = kGnThreads / 32;
 constexpr int kGnMaxTileCh = 512;   // most channels of a column tile
+constexpr int kGnFwdHold = 8;       // rows a thread keeps in registers in one launch
+constexpr int kGnBwdHold = 4;
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
@@ -49,55 +53,118 @@ struct GnArgs {
   int zero_centered;
 };
 
-// ---- activations ------------------------------------------------------------
-// sigmoid by the hardware exponential and division (a few 2^-23 relative);
-// e^-z may overflow to infinity, which gives 0.
-__device__ __forceinline__ float sigmoid_f(float z) {
-  return __fdividef(1.f, 1.f + __expf(-z));
+// ---- activations, of pairs ----------------------------------------------------
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-template <int ACT> __device__ __forceinline__ float act_f(float z) {
-  if (ACT == kActSilu) return __fdividef(z, 1.f + __expf(-z));
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + e^-z) by the hardware's exponential and reciprocal (each good to
+// about 2^-23, relative); an e^-z that overflows gives 0.
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+  const float2 t = mul2(z, splat2(-1.4426950408889634f));
+  const float2 d = add2(make_float2(ex2f(t.x), ex2f(t.y)), splat2(1.f));
+  return make_float2(rcpf(d.x), rcpf(d.y));
+}
+template <int ACT> __device__ __forceinline__ float2 act2(float2 z) {
+  if (ACT == kActSilu) return mul2(z, sigmoid2(z));
   // normcdff keeps relative accuracy in the lower tail, where (1 + erf) / 2
   // cancels.
-  if (ACT == kActGelu) return z * normcdff(z);
+  if (ACT == kActGelu) return mul2(z, make_float2(normcdff(z.x), normcdff(z.y)));
   return z;
 }
-template <int ACT> __device__ __forceinline__ float act_grad_f(float z) {
+__device__ __forceinline__ float gelu_grad(float z) {
+  return normcdff(z) + z * 0.3989422804f * __expf(-0.5f * z * z);
+}
+template <int ACT> __device__ __forceinline__ float2 act_grad2(float2 z) {
   if (ACT == kActSilu) {
-    const float s = sigmoid_f(z);
-    return s * (1.f + z * (1.f - s));
+    const float2 s = sigmoid2(z);
+    const float2 o = fma2(s, splat2(-1.f), splat2(1.f));   // 1 - s
+    return mul2(s, fma2(z, o, splat2(1.f)));
   }
-  if (ACT == kActGelu) return normcdff(z) + z * 0.3989422804f * __expf(-0.5f * z * z);
-  return 1.f;
+  if (ACT == kActGelu) return make_float2(gelu_grad(z.x), gelu_grad(z.y));
+  return splat2(1.f);
 }
 
-// ---- loads and stores of VEC elements ---------------------------------------
-template <typename T, int VEC> struct Pack;
-template <typename T> struct Pack<T, 1> {
-  T v;
-  __device__ __forceinline__ void load(const T* p) { v = *p; }
-  __device__ __forceinline__ void store(T* p) const { *p = v; }
-  __device__ __forceinline__ void get(float* f) const { f[0] = to_f(v); }
-  __device__ __forceinline__ void set(const float* f) { v = from_f<T>(f[0]); }
-};
-template <typename T> struct PackVec {
+// ---- a thread's VEC elements, as NP pairs ---------------------------------------
+// A vector of 16 bytes, or one element (whose pair has an idle second half).
+template <typename T, int VEC> struct Pack {
+  static constexpr int NP = VEC / 2;
   uint4 v;
   __device__ __forceinline__ void load(const T* p) { v = ld_vec(p); }
   __device__ __forceinline__ void store(T* p) const { st_vec(p, v); }
-  __device__ __forceinline__ void get(float* f) const { unpack<T>(v, f); }
-  __device__ __forceinline__ void set(const float* f) { v = pack<T>(f); }
+  __device__ __forceinline__ void get(float2* f) const { unpack2<T>(v, f); }
+  __device__ __forceinline__ void set(const float2* f) { v = pack2<T>(f); }
+  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
 };
-template <> struct Pack<float, 4> : PackVec<float> {};
-template <> struct Pack<bf16, 8> : PackVec<bf16> {};
-template <> struct Pack<f16, 8> : PackVec<f16> {};
+template <typename T> struct Pack<T, 1> {
+  static constexpr int NP = 1;
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = v; }
+  __device__ __forceinline__ void get(float2* f) const { f[0] = make_float2(to_f(v), 0.f); }
+  __device__ __forceinline__ void set(const float2* f) { v = from_f<T>(f[0].x); }
+  __device__ __forceinline__ void clear() { v = from_f<T>(0.f); }
+};
+
+// Shared memory: the row lanes' sums before they are added up, and in their
+// place, afterwards, the parameters of the tile's columns.
+struct GnSmem {
+  union {
+    struct {
+      float a[kGnThreads * 8];
+      float b[kGnThreads * 8];
+    } lane;
+    float par[6][kGnMaxTileCh];
+  };
+  float ca[2 * kGnMaxTileCh];   // column sums, in parts, then whole
+  float cb[2 * kGnMaxTileCh];
+  float k[kGnMaxTileCh];        // forward: what the columns are shifted by
+  float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
+  float g1[kGnMaxTileCh];       // rstd, or c2
+};
+
+template <int VEC> __device__ __forceinline__ void put_pairs(float* s, const float2* f) {
+  if (VEC == 1) {
+    s[0] = f[0].x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i)
+      reinterpret_cast<float4*>(s)[i] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x,
+                                                    f[2 * i + 1].y);
+  }
+}
+template <int VEC> __device__ __forceinline__ void get_pairs(const float* s, float2* f) {
+  if (VEC == 1) {
+    f[0] = make_float2(s[0], 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(s)[i];
+      f[2 * i] = make_float2(v.x, v.y);
+      f[2 * i + 1] = make_float2(v.z, v.w);
+    }
+  }
+}
 
 // ---- geometry -----------------------------------------------------------------
-// One CTA's share of a panel (a sample's column tile): a slice of its rows.
+// One CTA's share of a panel (a sample's column tile): a slice of its rows;
+// and a thread's place in it.
 struct GnUnit {
   int n, tile, slice;
-  int c0, c1;            // channels of the tile
+  int c0, nc;            // first channel, number of channels of the tile
   int g0, ng;            // its groups
-  int64_t r0, r1;        // rows of the slice
+  int64_t r0, nr;        // rows of the slice
+  int tc;                // channels of a full tile
+  int TY;                // row lanes
+  int tx, ty;            // the thread's vector and row lane
+  int rows;              // its rows
+  bool on;               // it has a vector
 };
 template <int VEC>
 __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice) {
@@ -105,134 +172,159 @@ __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice)
   u.n = panel / a.tiles;
   u.tile = panel - u.n * a.tiles;
   u.slice = slice;
-  u.c0 = u.tile * a.tw * VEC;
-  u.c1 = min(a.channels, u.c0 + a.tw * VEC);
+  u.tc = a.tw * VEC;
+  u.c0 = u.tile * u.tc;
+  u.nc = min(a.channels - u.c0, u.tc);
   u.g0 = u.c0 / a.cpg;
-  u.ng = (u.c1 - 1) / a.cpg - u.g0 + 1;
+  u.ng = (u.c0 + u.nc - 1) / a.cpg - u.g0 + 1;
   u.r0 = min(a.rows, (int64_t)slice * a.slice_rows);   // a cluster's last CTAs may have none
-  u.r1 = min(a.rows, u.r0 + a.slice_rows);
+  u.nr = min(a.rows - u.r0, a.slice_rows);
+  u.TY = kGnThreads / a.tw;
+  u.ty = threadIdx.x / a.tw;
+  u.tx = threadIdx.x - u.ty * a.tw;
+  u.on = u.ty < u.TY && u.tx * VEC < u.nc;
+  u.rows = u.on && u.nr > u.ty ? (int)((u.nr - u.ty - 1) / u.TY) + 1 : 0;
   return u;
 }
-
-// The rows a thread of row lane `ty` (of TY) takes from n rows.
-__device__ __forceinline__ int gn_lane_rows(int64_t n, int ty, int TY) {
-  return n > ty ? (int)((n - ty - 1) / TY) + 1 : 0;
-}
-
-// Channel parameters of a thread: w and beta of its VEC channels.
+// Where a thread's first row of a tensor starts.
 template <typename T, int VEC>
-__device__ __forceinline__ void gn_params(const GnArgs& a, int n, int c, float* w, float* b) {
-  float g[VEC];
-  Pack<T, VEC> p;
-  if (a.gamma != nullptr) {
-    p.load(static_cast<const T*>(a.gamma) + n * a.param_sample + c);
-    p.get(g);
-  }
-#pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    w[i] = a.gamma == nullptr ? 1.f : (a.zero_centered ? 1.f + g[i] : g[i]);
-  if (a.beta != nullptr) {
-    p.load(static_cast<const T*>(a.beta) + n * a.param_sample + c);
-    p.get(b);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) b[i] = 0.f;
-  }
+__device__ __forceinline__ int64_t gn_at(const GnUnit& u, int64_t sample, int64_t row) {
+  return u.n * sample + (u.r0 + u.ty) * row + u.c0 + u.tx * VEC;
 }
 
-struct GnSmem {
-  float a[kGnThreads * 8];
-  float b[kGnThreads * 8];
-  float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
-  float g1[kGnMaxTileCh];       // rstd, or c2
-};
+// gamma (as w) or beta of one channel of the tile.
+template <typename T>
+__device__ __forceinline__ float gn_weight(const GnArgs& a, const GnUnit& u, int col) {
+  if (a.gamma == nullptr) return 1.f;
+  const float g = to_f(static_cast<const T*>(a.gamma)[u.n * a.param_sample + u.c0 + col]);
+  return a.zero_centered ? 1.f + g : g;
+}
+template <typename T>
+__device__ __forceinline__ float gn_bias(const GnArgs& a, const GnUnit& u, int col) {
+  if (a.beta == nullptr) return 0.f;
+  return to_f(static_cast<const T*>(a.beta)[u.n * a.param_sample + u.c0 + col]);
+}
+
+// ---- column sums ------------------------------------------------------------------
+// Add up two quantities of every column over the row lanes: each column's
+// lanes are dealt to as many threads as there are, then those parts are
+// added; the order depends on the launch's shape only. Returns with the
+// totals of column `col` in sm.ca, sm.cb after the caller's next barrier, via
+// `done(col, a, b)`.
+template <int VEC, typename F>
+__device__ __forceinline__ void gn_columns(const GnUnit& u, GnSmem& sm, const float2* va,
+                                           const float2* vb, F&& done) {
+  if (u.on) {
+    put_pairs<VEC>(sm.lane.a + u.ty * u.tc + u.tx * VEC, va);
+    put_pairs<VEC>(sm.lane.b + u.ty * u.tc + u.tx * VEC, vb);
+  }
+  __syncthreads();
+  const int parts = kGnThreads / u.tc;   // threads a column
+  if (parts > 1) {
+    const int part = threadIdx.x / u.tc, col = threadIdx.x - part * u.tc;
+    if (part < parts && col < u.nc) {
+      float sa = 0.f, sb = 0.f;
+      for (int y = part; y < u.TY; y += parts) {
+        sa += sm.lane.a[y * u.tc + col];
+        sb += sm.lane.b[y * u.tc + col];
+      }
+      sm.ca[threadIdx.x] = sa;
+      sm.cb[threadIdx.x] = sb;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+      float sa = 0.f, sb = 0.f;
+      for (int p = 0; p < parts; ++p) {
+        sa += sm.ca[p * u.tc + c];
+        sb += sm.cb[p * u.tc + c];
+      }
+      done(c, sa, sb);
+    }
+  } else {
+    for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+      float sa = 0.f, sb = 0.f;
+      for (int y = 0; y < u.TY; ++y) {
+        sa += sm.lane.a[y * u.tc + c];
+        sb += sm.lane.b[y * u.tc + c];
+      }
+      done(c, sa, sb);
+    }
+  }
+}
 
 // ---- forward: partial statistics of one unit -------------------------------------
-// Each thread sums d = x - K and d^2 per channel, K the channel's first value
-// in its rows. K is one of the data, so (mean - K)^2 is itself a term of the
-// variance: with n_t rows a thread, cancellation in s2 - s1^2 / n_t costs at
-// most about n_t * 2^-24 of the group's sum of squares, whatever the mean.
-// The threads' (mean, M2) are merged by the parallel-variance identity
-// M2 = sum M2_i + n_i (mean_i - mean)^2.
-template <typename T, int VEC>
+// Each column is summed as d = x - k and d^2, k the column's value in the
+// slice's first row. k is one of the data, so (mean - k)^2 is itself a term
+// of the variance: with n rows a slice, cancellation in s2 - s1^2 / n costs
+// at most about n * 2^-24 of the group's sum of squares, whatever the mean.
+// Columns, and later slices, are merged by the parallel-variance identity
+// M2 = sum M2_i + n_i (mean_i - mean)^2. The first HOLD rows stay in `held`.
+template <typename T, int VEC, int HOLD>
 __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              float2* out) {
-  const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
-  const int c = u.c0 + tx * VEC;
-  const bool on = ty < TY && c < u.c1;
-  const int64_t n_rows = u.r1 - u.r0;
-  if (on) {
-    const T* p = static_cast<const T*>(a.x) + (int64_t)u.n * a.x_sample + (u.r0 + ty) * a.x_row + c;
-    const int64_t step = (int64_t)TY * a.x_row;
-    const int rows = gn_lane_rows(n_rows, ty, TY);
-    float k[VEC], s1[VEC], s2[VEC], v[VEC];
+                                              Pack<T, VEC>* held, float2* out) {
+  constexpr int NP = Pack<T, VEC>::NP;
+  float2 k[NP], s1[NP], s2[NP], v[NP];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) k[i] = s1[i] = s2[i] = 0.f;
-    if (rows > 0) {
-      Pack<T, VEC> q;
-      q.load(p);
-      q.get(k);
-    }
-    int r = 0;
-    for (; r + 4 <= rows; r += 4) {
-      Pack<T, VEC> q[4];
+  for (int i = 0; i < NP; ++i) k[i] = s1[i] = s2[i] = splat2(0.f);
+  const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+  const int64_t step = (int64_t)u.TY * a.x_row;
+  if (u.rows > 0) {
+    Pack<T, VEC> first;
+    first.load(p - u.ty * a.x_row);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) q[j].load(p + j * step);
-      p += 4 * step;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j].get(v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float d = v[i] - k[i];
-          s1[i] += d;
-          s2[i] = fmaf(d, d, s2[i]);
-        }
-      }
-    }
-    for (; r < rows; ++r, p += step) {
-      Pack<T, VEC> q;
-      q.load(p);
+    for (int j = 0; j < HOLD; ++j)
+      if (j < u.rows) held[j].load(p + j * step);
+    first.get(k);
+    auto add = [&](const Pack<T, VEC>& q) {
       q.get(v);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float d = v[i] - k[i];
-        s1[i] += d;
-        s2[i] = fmaf(d, d, s2[i]);
+      for (int i = 0; i < NP; ++i) {
+        const float2 d = fma2(k[i], splat2(-1.f), v[i]);
+        s1[i] = add2(s1[i], d);
+        s2[i] = fma2(d, d, s2[i]);
       }
-    }
-    const float inv = rows > 0 ? 1.f / (float)rows : 0.f;
-    const int at = ty * (a.tw * VEC) + tx * VEC;
+    };
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const float m = s1[i] * inv;
-      sm.a[at + i] = k[i] + m;
-      sm.b[at + i] = s2[i] - s1[i] * m;
+    for (int j = 0; j < HOLD; ++j)
+      if (j < u.rows) add(held[j]);
+    int r = HOLD;
+    p += HOLD * step;
+    constexpr int UN = HOLD > 0 ? 4 : 8;
+    for (; r + UN <= u.rows; r += UN, p += UN * step) {
+      Pack<T, VEC> q[UN];
+#pragma unroll
+      for (int j = 0; j < UN; ++j) q[j].load(p + j * step);
+#pragma unroll
+      for (int j = 0; j < UN; ++j) add(q[j]);
+    }
+    for (; r < u.rows; ++r, p += step) {
+      Pack<T, VEC> q;
+      q.load(p);
+      add(q);
     }
   }
+  if (u.on && u.ty == 0) put_pairs<VEC>(sm.k + u.tx * VEC, k);
+  const float n = (float)u.nr, inv = u.nr > 0 ? 1.f / n : 0.f;
+  gn_columns<VEC>(u, sm, s1, s2, [&](int c, float sa, float sb) {
+    const float m = sa * inv;
+    sm.ca[c] = sm.k[c] + m;    // the part this thread has just read, or nobody's
+    sm.cb[c] = fmaf(-sa, m, sb);
+  });
   __syncthreads();
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
-    const int cs = max((u.g0 + lg) * a.cpg, u.c0) - u.c0;
-    const int ce = min((u.g0 + lg + 1) * a.cpg, u.c1) - u.c0;
-    const int nc = ce - cs, total = nc * TY;
+    const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
+    const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     // Means are averaged as differences from one of them, which keeps a
     // constant group's mean exact and a large common mean out of the sum.
-    const float base = sm.a[cs];
+    const float base = sm.ca[cs];
     float s = 0.f;
-    for (int e = lane; e < total; e += 32) {
-      const int y = e / nc, at = y * (a.tw * VEC) + cs + (e - y * nc);
-      const int k = gn_lane_rows(n_rows, y, TY);
-      if (k > 0) s = fmaf((float)k, sm.a[at] - base, s);
-    }
-    s = group_sum<32>(s);
-    const float m = n_rows > 0 ? base + s / ((float)n_rows * (float)nc) : 0.f;
+    for (int c = cs + lane; c < ce; c += 32) s += sm.ca[c] - base;
+    const float m = base + group_sum<32>(s) / (float)(ce - cs);
     s = 0.f;
-    for (int e = lane; e < total; e += 32) {
-      const int y = e / nc, at = y * (a.tw * VEC) + cs + (e - y * nc);
-      const int k = gn_lane_rows(n_rows, y, TY);
-      const float d = sm.a[at] - m;
-      if (k > 0) s += fmaf((float)k * d, d, sm.b[at]);
+    for (int c = cs + lane; c < ce; c += 32) {
+      const float d = sm.ca[c] - m;
+      s += fmaf(n * d, d, sm.cb[c]);
     }
     s = group_sum<32>(s);
     if (lane == 0) out[lg] = make_float2(m, s);
@@ -261,20 +353,21 @@ __device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSm
 // Merge the partials of the unit's groups into sm.g0 = mean, sm.g1 = rstd
 // (forward) or into sm.g0 = c1, sm.g1 = c2 (backward): one warp a group, the
 // slices dealt to its lanes, the same order in every CTA.
-template <int VEC, bool BWD>
+template <bool BWD>
 __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
   const int lane = threadIdx.x & 31;
-  const int tc = a.tw * VEC;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
     const int g = u.g0 + lg, ch0 = g * a.cpg, ch1 = ch0 + a.cpg;
-    const int t0 = ch0 / tc, t1 = (ch1 - 1) / tc;
+    const int t0 = ch0 / u.tc, t1 = (ch1 - 1) / u.tc;
     float s0 = 0.f, s1 = 0.f, base = 0.f;
     if (!BWD)   // the mean of the first slice of the group's first tile
-      base = a.part[((int64_t)u.n * a.tiles + t0) * a.slices * a.max_groups + g - t0 * tc / a.cpg].x;
+      base = a.part[((int64_t)u.n * a.tiles + t0) * a.slices * a.max_groups + g -
+                    t0 * u.tc / a.cpg].x;
     for (int t = t0; t <= t1; ++t) {
-      const int nc = min(ch1, (t + 1) * tc) - max(ch0, t * tc);
+      const int nc = min(ch1, (t + 1) * u.tc) - max(ch0, t * u.tc);
       const float2* p = a.part + ((int64_t)u.n * a.tiles + t) * a.slices * a.max_groups +
-                        (g - t * tc / a.cpg);
+                        (g - t * u.tc / a.cpg);
+#pragma unroll 4
       for (int i = lane; i < a.slices; i += 32) {
         const float2 v = p[(int64_t)i * a.max_groups];
         if (BWD) {
@@ -291,9 +384,10 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
       s1 = group_sum<32>(s1) * a.inv_m;
     } else {
       for (int t = t0; t <= t1; ++t) {
-        const int nc = min(ch1, (t + 1) * tc) - max(ch0, t * tc);
+        const int nc = min(ch1, (t + 1) * u.tc) - max(ch0, t * u.tc);
         const float2* p = a.part + ((int64_t)u.n * a.tiles + t) * a.slices * a.max_groups +
-                          (g - t * tc / a.cpg);
+                          (g - t * u.tc / a.cpg);
+#pragma unroll 4
         for (int i = lane; i < a.slices; i += 32) {
           const float2 v = p[(int64_t)i * a.max_groups];
           const int64_t nr = min(a.slice_rows, a.rows - i * a.slice_rows);
@@ -322,7 +416,10 @@ __device__ __forceinline__ float2 cluster_read(const float2* p, int rank) {
   unsigned far;
   float2 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(far) : "memory");
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(far)
+               : "memory");
   return v;
 }
 
@@ -341,10 +438,11 @@ __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit
     } else {
       const float base = __shfl_sync(0xffffffffu, v.x, 0);
       const int64_t nr = min(a.slice_rows, a.rows - lane * a.slice_rows);
-      const float cnt = lane < a.slices && nr > 0 ? (float)nr * (float)a.cpg : 0.f;
-      s0 = base + group_sum<32>(cnt * (lane < a.slices ? v.x - base : 0.f)) * a.inv_m;
+      const bool some = lane < a.slices && nr > 0;
+      const float cnt = some ? (float)nr * (float)a.cpg : 0.f;
+      s0 = base + group_sum<32>(some ? cnt * (v.x - base) : 0.f) * a.inv_m;
       const float d = v.x - s0;
-      s1 = group_sum<32>(lane < a.slices ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
+      s1 = group_sum<32>(some ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
     }
     if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0);
   }
@@ -352,140 +450,165 @@ __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit
 }
 
 // ---- forward: normalize one unit -------------------------------------------------
-template <typename T, int VEC, int ACT>
-__device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
-  const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
-  const int c = u.c0 + tx * VEC;
-  if (ty < TY && c < u.c1) {
-    float m[VEC], w[VEC], b[VEC], v[VEC];
-    gn_params<T, VEC>(a, u.n, c, w, b);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int lg = (c + i) / a.cpg - u.g0;
-      m[i] = sm.g0[lg];
-      w[i] *= sm.g1[lg];
-    }
-    const T* p = static_cast<const T*>(a.x) + (int64_t)u.n * a.x_sample + (u.r0 + ty) * a.x_row + c;
-    T* o = static_cast<T*>(a.out) + (int64_t)u.n * a.out_sample + (u.r0 + ty) * a.out_row + c;
-    const int64_t step = (int64_t)TY * a.x_row, ostep = (int64_t)TY * a.out_row;
-    const int rows = gn_lane_rows(u.r1 - u.r0, ty, TY);
-    int r = 0;
-    for (; r + 4 <= rows; r += 4) {
-      Pack<T, VEC> q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) q[j].load(p + j * step);
-      p += 4 * step;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j].get(v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = act_f<ACT>(fmaf(v[i] - m[i], w[i], b[i]));
-        q[j].set(v);
-        q[j].store(o + j * ostep);
-      }
-      o += 4 * ostep;
-    }
-    for (; r < rows; ++r, p += step, o += ostep) {
-      Pack<T, VEC> q;
-      q.load(p);
-      q.get(v);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = act_f<ACT>(fmaf(v[i] - m[i], w[i], b[i]));
-      q.set(v);
-      q.store(o);
-    }
+template <typename T, int VEC, int ACT, int HOLD>
+__device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                              const Pack<T, VEC>* held) {
+  constexpr int NP = Pack<T, VEC>::NP;
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+    const int lg = (u.c0 + c) / a.cpg - u.g0;
+    sm.par[0][c] = -sm.g0[lg];
+    sm.par[1][c] = gn_weight<T>(a, u, c) * sm.g1[lg];
+    sm.par[2][c] = gn_bias<T>(a, u, c);
   }
   __syncthreads();
+  if (u.rows > 0) {
+    float2 m[NP], w[NP], b[NP], v[NP];
+    get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
+    get_pairs<VEC>(sm.par[1] + u.tx * VEC, w);
+    get_pairs<VEC>(sm.par[2] + u.tx * VEC, b);
+    const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+    T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
+    const int64_t step = (int64_t)u.TY * a.x_row, ostep = (int64_t)u.TY * a.out_row;
+    auto put = [&](const Pack<T, VEC>& q, T* to) {
+      q.get(v);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) v[i] = act2<ACT>(fma2(add2(v[i], m[i]), w[i], b[i]));
+      Pack<T, VEC> r;
+      r.set(v);
+      r.store(to);
+    };
+#pragma unroll
+    for (int j = 0; j < HOLD; ++j)
+      if (j < u.rows) put(held[j], o + j * ostep);
+    int r = HOLD;
+    p += HOLD * step;
+    o += HOLD * ostep;
+    constexpr int UN = 4;
+    for (; r + UN <= u.rows; r += UN, p += UN * step, o += UN * ostep) {
+      Pack<T, VEC> q[UN];
+#pragma unroll
+      for (int j = 0; j < UN; ++j) q[j].load(p + j * step);
+#pragma unroll
+      for (int j = 0; j < UN; ++j) put(q[j], o + j * ostep);
+    }
+    for (; r < u.rows; ++r, p += step, o += ostep) {
+      Pack<T, VEC> q;
+      q.load(p);
+      put(q, o);
+    }
+  }
 }
 
-// ---- backward: sums of one unit ----------------------------------------------------
-template <typename T, int VEC, int ACT>
+// ---- backward ------------------------------------------------------------------------
+// What a thread keeps of its first rows: x, and dz in fp32 (dy itself where
+// there is no activation), so that the activation's slope is not taken twice.
+template <typename T, int VEC, int ACT> struct Held {
+  Pack<T, VEC> x;
+  float2 dz[Pack<T, VEC>::NP];
+};
+template <typename T, int VEC> struct Held<T, VEC, kActNone> {
+  Pack<T, VEC> x, dy;
+};
+
+// mean, rstd, w and beta of the unit's columns.
+template <typename T>
+__device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+    const int64_t g = (int64_t)u.n * a.groups + (u.c0 + c) / a.cpg;
+    sm.par[0][c] = -a.mean[g];
+    sm.par[1][c] = a.rstd[g];
+    sm.par[2][c] = gn_weight<T>(a, u, c);
+    sm.par[3][c] = gn_bias<T>(a, u, c);
+  }
+}
+
+// Sums of one unit.
+template <typename T, int VEC, int ACT, int HOLD>
 __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  float2* out) {
-  const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
-  const int tc = a.tw * VEC;
-  const int c = u.c0 + tx * VEC;
-  const bool on = ty < TY && c < u.c1;
-  if (on) {
-    float m[VEC], rs[VEC], w[VEC], b[VEC], sa[VEC], sb[VEC], v[VEC], d[VEC];
-    gn_params<T, VEC>(a, u.n, c, w, b);
+                                                  Held<T, VEC, ACT>* held, float2* out) {
+  constexpr int NP = Pack<T, VEC>::NP;
+  float2 sa[NP], sb[NP];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int64_t g = (int64_t)u.n * a.groups + (c + i) / a.cpg;
-      m[i] = a.mean[g];
-      rs[i] = a.rstd[g];
-      sa[i] = sb[i] = 0.f;
+  for (int i = 0; i < NP; ++i) sa[i] = sb[i] = splat2(0.f);
+  const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+  const T* q = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
+  const int64_t ps = (int64_t)u.TY * a.x_row, qs = (int64_t)u.TY * a.dy_row;
+  Pack<T, VEC> hd[HOLD > 0 ? HOLD : 1];
+#pragma unroll
+  for (int j = 0; j < HOLD; ++j)
+    if (j < u.rows) {
+      held[j].x.load(p + j * ps);
+      hd[j].load(q + j * qs);
     }
-    const T* p = static_cast<const T*>(a.x) + (int64_t)u.n * a.x_sample + (u.r0 + ty) * a.x_row + c;
-    const T* q = static_cast<const T*>(a.dy) + (int64_t)u.n * a.dy_sample + (u.r0 + ty) * a.dy_row + c;
-    const int64_t ps = (int64_t)TY * a.x_row, qs = (int64_t)TY * a.dy_row;
-    const int rows = gn_lane_rows(u.r1 - u.r0, ty, TY);
-    int r = 0;
-    auto add = [&](const Pack<T, VEC>& px, const Pack<T, VEC>& pd) {
+  gn_bwd_params<T>(a, u, sm);
+  __syncthreads();
+  if (u.rows > 0) {
+    float2 m[NP], rs[NP], w[NP], b[NP], v[NP], d[NP];
+    get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
+    get_pairs<VEC>(sm.par[1] + u.tx * VEC, rs);
+    get_pairs<VEC>(sm.par[2] + u.tx * VEC, w);
+    get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
+    auto add = [&](const Pack<T, VEC>& px, const Pack<T, VEC>& pd) {   // leaves dz in d
       px.get(v);
       pd.get(d);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float xh = (v[i] - m[i]) * rs[i];
-        const float dz = d[i] * act_grad_f<ACT>(fmaf(xh, w[i], b[i]));
-        sa[i] += dz;
-        sb[i] = fmaf(dz, xh, sb[i]);
+      for (int i = 0; i < NP; ++i) {
+        const float2 xh = mul2(add2(v[i], m[i]), rs[i]);
+        if (ACT != kActNone) d[i] = mul2(d[i], act_grad2<ACT>(fma2(xh, w[i], b[i])));
+        sa[i] = add2(sa[i], d[i]);
+        sb[i] = fma2(d[i], xh, sb[i]);
       }
     };
-    for (; r + 2 <= rows; r += 2) {
-      Pack<T, VEC> px[2], pd[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < HOLD; ++j)
+      if (j < u.rows) {
+        add(held[j].x, hd[j]);
+        if constexpr (ACT == kActNone) {
+          held[j].dy = hd[j];
+        } else {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) held[j].dz[i] = d[i];
+        }
+      }
+    int r = HOLD;
+    p += HOLD * ps;
+    q += HOLD * qs;
+    constexpr int UN = 4;
+    for (; r + UN <= u.rows; r += UN, p += UN * ps, q += UN * qs) {
+      Pack<T, VEC> px[UN], pd[UN];
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
         px[j].load(p + j * ps);
         pd[j].load(q + j * qs);
       }
-      p += 2 * ps;
-      q += 2 * qs;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) add(px[j], pd[j]);
+      for (int j = 0; j < UN; ++j) add(px[j], pd[j]);
     }
-    if (r < rows) {
+    for (; r < u.rows; ++r, p += ps, q += qs) {
       Pack<T, VEC> px, pd;
       px.load(p);
       pd.load(q);
       add(px, pd);
     }
-    const int at = ty * tc + tx * VEC;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      sm.a[at + i] = sa[i];
-      sm.b[at + i] = sb[i];
-    }
   }
-  __syncthreads();
-  // Column sums over the row lanes, in their order; the first row of the
-  // arrays then holds the columns' totals.
-  float* cols = a.cols + ((int64_t)u.n * a.slices + u.slice) * 2 * a.channels;
-  for (int k = threadIdx.x; k < u.c1 - u.c0; k += kGnThreads) {
-    float ta = 0.f, tb = 0.f;
-    for (int y = 0; y < TY; ++y) {
-      ta += sm.a[y * tc + k];
-      tb += sm.b[y * tc + k];
-    }
-    cols[u.c0 + k] = tb;
-    cols[a.channels + u.c0 + k] = ta;
-    float w = 1.f;
-    if (a.gamma != nullptr) {
-      w = to_f(static_cast<const T*>(a.gamma)[u.n * a.param_sample + u.c0 + k]);
-      if (a.zero_centered) w += 1.f;
-    }
-    sm.a[k] = w * ta;
-    sm.b[k] = w * tb;
-  }
+  __syncthreads();   // the parameters give way to the sums
+  float* cols = a.cols + ((int64_t)u.n * a.slices + u.slice) * 2 * a.channels + u.c0;
+  gn_columns<VEC>(u, sm, sa, sb, [&](int c, float ta, float tb) {
+    cols[c] = tb;
+    cols[a.channels + c] = ta;
+    const float w = gn_weight<T>(a, u, c);
+    sm.ca[c] = w * ta;
+    sm.cb[c] = w * tb;
+  });
   __syncthreads();
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
-    const int cs = max((u.g0 + lg) * a.cpg, u.c0) - u.c0;
-    const int ce = min((u.g0 + lg + 1) * a.cpg, u.c1) - u.c0;
+    const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
+    const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     float2 s = make_float2(0.f, 0.f);
-    for (int k = cs + lane; k < ce; k += 32) {
-      s.x += sm.a[k];
-      s.y += sm.b[k];
+    for (int c = cs + lane; c < ce; c += 32) {
+      s.x += sm.ca[c];
+      s.y += sm.cb[c];
     }
     s = group_sum2<32>(s);
     if (lane == 0) out[lg] = s;
@@ -493,66 +616,83 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
   __syncthreads();
 }
 
-// ---- backward: dx of one unit --------------------------------------------------------
-template <typename T, int VEC, int ACT>
-__device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
-  const int tx = threadIdx.x % a.tw, ty = threadIdx.x / a.tw, TY = kGnThreads / a.tw;
-  const int c = u.c0 + tx * VEC;
-  if (ty < TY && c < u.c1) {
-    float m[VEC], rs[VEC], w[VEC], b[VEC], c1[VEC], c2[VEC], v[VEC], d[VEC];
-    gn_params<T, VEC>(a, u.n, c, w, b);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int lg = (c + i) / a.cpg - u.g0;
-      const int64_t g = (int64_t)u.n * a.groups + u.g0 + lg;
-      m[i] = a.mean[g];
-      rs[i] = a.rstd[g];
-      c1[i] = sm.g0[lg];
-      c2[i] = sm.g1[lg];
-    }
-    const T* p = static_cast<const T*>(a.x) + (int64_t)u.n * a.x_sample + (u.r0 + ty) * a.x_row + c;
-    const T* q = static_cast<const T*>(a.dy) + (int64_t)u.n * a.dy_sample + (u.r0 + ty) * a.dy_row + c;
-    T* o = static_cast<T*>(a.out) + (int64_t)u.n * a.out_sample + (u.r0 + ty) * a.out_row + c;
-    const int64_t ps = (int64_t)TY * a.x_row, qs = (int64_t)TY * a.dy_row,
-                  os = (int64_t)TY * a.out_row;
-    const int rows = gn_lane_rows(u.r1 - u.r0, ty, TY);
-    auto put = [&](const Pack<T, VEC>& px, const Pack<T, VEC>& pd, T* to) {
+// dx of one unit.
+template <typename T, int VEC, int ACT, int HOLD>
+__device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                                  const Held<T, VEC, ACT>* held) {
+  constexpr int NP = Pack<T, VEC>::NP;
+  gn_bwd_params<T>(a, u, sm);
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+    const int lg = (u.c0 + c) / a.cpg - u.g0;
+    sm.par[4][c] = -sm.g0[lg];
+    sm.par[5][c] = -sm.g1[lg];
+  }
+  __syncthreads();
+  if (u.rows > 0) {
+    float2 m[NP], rs[NP], w[NP], b[NP], c1[NP], c2[NP], v[NP], d[NP];
+    get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
+    get_pairs<VEC>(sm.par[1] + u.tx * VEC, rs);
+    get_pairs<VEC>(sm.par[2] + u.tx * VEC, w);
+    get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
+    get_pairs<VEC>(sm.par[4] + u.tx * VEC, c1);
+    get_pairs<VEC>(sm.par[5] + u.tx * VEC, c2);
+    const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+    const T* q = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
+    T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
+    const int64_t ps = (int64_t)u.TY * a.x_row, qs = (int64_t)u.TY * a.dy_row,
+                  os = (int64_t)u.TY * a.out_row;
+    // The product w dz is rounded before c1 is taken off (no fma): in a group
+    // of one value c1 is that very product and dx is exactly 0.
+    auto put = [&](const Pack<T, VEC>& px, T* to, bool have_dz) {
       px.get(v);
-      pd.get(d);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float xh = (v[i] - m[i]) * rs[i];
-        const float dz = d[i] * act_grad_f<ACT>(fmaf(xh, w[i], b[i]));
-        // The product is rounded before c1 is taken off (no fma): in a group
-        // of one value c1 is that very product and dx is exactly 0.
-        v[i] = rs[i] * fmaf(-xh, c2[i], __fmul_rn(w[i], dz) - c1[i]);
+      for (int i = 0; i < NP; ++i) {
+        const float2 xh = mul2(add2(v[i], m[i]), rs[i]);
+        if (ACT != kActNone && !have_dz) d[i] = mul2(d[i], act_grad2<ACT>(fma2(xh, w[i], b[i])));
+        const float2 g = make_float2(__fmul_rn(w[i].x, d[i].x), __fmul_rn(w[i].y, d[i].y));
+        v[i] = mul2(rs[i], fma2(xh, c2[i], add2(g, c1[i])));
       }
-      Pack<T, VEC> po;
-      po.set(v);
-      po.store(to);
+      Pack<T, VEC> r;
+      r.set(v);
+      r.store(to);
     };
-    int r = 0;
-    for (; r + 2 <= rows; r += 2) {
-      Pack<T, VEC> px[2], pd[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < HOLD; ++j)
+      if (j < u.rows) {
+        if constexpr (ACT == kActNone) {
+          held[j].dy.get(d);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) d[i] = held[j].dz[i];
+        }
+        put(held[j].x, o + j * os, true);
+      }
+    int r = HOLD;
+    p += HOLD * ps;
+    q += HOLD * qs;
+    o += HOLD * os;
+    constexpr int UN = 2;
+    for (; r + UN <= u.rows; r += UN, p += UN * ps, q += UN * qs, o += UN * os) {
+      Pack<T, VEC> px[UN], pd[UN];
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
         px[j].load(p + j * ps);
         pd[j].load(q + j * qs);
       }
-      p += 2 * ps;
-      q += 2 * qs;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) put(px[j], pd[j], o + j * os);
-      o += 2 * os;
+      for (int j = 0; j < UN; ++j) {
+        pd[j].get(d);
+        put(px[j], o + j * os, false);
+      }
     }
-    if (r < rows) {
+    for (; r < u.rows; ++r, p += ps, q += qs, o += os) {
       Pack<T, VEC> px, pd;
       px.load(p);
       pd.load(q);
-      put(px, pd, o);
+      pd.get(d);
+      put(px, o, false);
     }
   }
-  __syncthreads();
 }
 
 // ---- kernels ----------------------------------------------------------------------
@@ -569,13 +709,13 @@ __global__ void __launch_bounds__(kGnThreads)
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
-    gn_stats_unit<T, VEC>(a, u, sm, gn_part(a, u));
+    gn_stats_unit<T, VEC, 0>(a, u, sm, nullptr, gn_part(a, u));
   }
   if (app0 + p < app1) {
     const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_combine<VEC, false>(a, u, sm);
-    gn_apply_unit<T, VEC, ACT>(a, u, sm);
+    gn_combine<false>(a, u, sm);
+    gn_apply_unit<T, VEC, ACT, 0>(a, u, sm, nullptr);
   }
 }
 
@@ -586,45 +726,48 @@ __global__ void __launch_bounds__(kGnThreads)
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
-    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, gn_part(a, u));
+    gn_bwd_stats_unit<T, VEC, ACT, 0>(a, u, sm, nullptr, gn_part(a, u));
   }
   if (app0 + p < app1) {
     const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_combine<VEC, true>(a, u, sm);
-    gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm);
+    gn_combine<true>(a, u, sm);
+    gn_bwd_apply_unit<T, VEC, ACT, 0>(a, u, sm, nullptr);
   }
 }
 
 // A panel a cluster, in one launch: the statistics, a barrier of the
-// cluster, and the rows again, out of the L2 cache.
+// cluster, and the rows again: those that are held, then the others out of
+// the L2 cache.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads) gn_fwd_cluster_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a) {
   __shared__ GnSmem sm;
   __shared__ float2 part[kGnMaxTileCh];
   const int p = blockIdx.x / a.slices;
   const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
-  gn_stats_unit<T, VEC>(a, u, sm, part);
+  Pack<T, VEC> held[kGnFwdHold];
+  gn_stats_unit<T, VEC, kGnFwdHold>(a, u, sm, held, part);
   cluster_arrive();
   cluster_wait();
   gn_combine_cluster<false>(a, u, sm, part);
   cluster_arrive();
-  gn_apply_unit<T, VEC, ACT>(a, u, sm);
+  gn_apply_unit<T, VEC, ACT, kGnFwdHold>(a, u, sm, held);
   cluster_wait();   // no CTA leaves while another reads its partials
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_cluster_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a) {
   __shared__ GnSmem sm;
   __shared__ float2 part[kGnMaxTileCh];
   const int p = blockIdx.x / a.slices;
   const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
-  gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, part);
+  Held<T, VEC, ACT> held[kGnBwdHold];
+  gn_bwd_stats_unit<T, VEC, ACT, kGnBwdHold>(a, u, sm, held, part);
   cluster_arrive();
   cluster_wait();
   gn_combine_cluster<true>(a, u, sm, part);
   cluster_arrive();
-  gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm);
+  gn_bwd_apply_unit<T, VEC, ACT, kGnBwdHold>(a, u, sm, held);
   cluster_wait();
 }
 
