@@ -171,6 +171,9 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
   const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, act)
                    : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, act)
                                         : gn_table_f16(bwd, p.cluster, vec, act);
+  const size_t smem = vec ? (size_t)kGnRingBytes * (bwd ? 2 : 1) : 0;
+  const cudaError_t opt = (cudaError_t)allow_dyn_smem(fn, smem);
+  if (opt != cudaSuccess) return cuda_fail(opt);
   if (p.cluster) {
     if (p.slices > 8) {
       const cudaError_t e =
@@ -180,6 +183,7 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.panels * p.slices));
     cfg.blockDim = dim3(kGnThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -202,6 +206,7 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n * p.slices));
     cfg.blockDim = dim3(kGnThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

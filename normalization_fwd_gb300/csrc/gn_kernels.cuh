@@ -21,8 +21,9 @@ namespace nf {
 constexpr int kGnThreads = 256;
 constexpr int kGnWarps = kGnThreads / 32;
 constexpr int kGnMaxTileCh = 512;   // most channels of a column tile
-constexpr int kGnFwdHold = 8;       // rows a thread keeps in registers in one launch
-constexpr int kGnBwdHold = 4;
+constexpr int kGnRing = 8;          // rows a thread has in flight, or keeps
+constexpr int kGnStep = 2;          // rows of one step
+constexpr int kGnRingBytes = kGnRing * kGnThreads * 16;   // of one tensor
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
@@ -252,57 +253,153 @@ __device__ __forceinline__ void gn_columns(const GnUnit& u, GnSmem& sm, const fl
   }
 }
 
+// ---- rows in flight -----------------------------------------------------------------
+// A thread streams its vectors of one or two tensors through slots of shared
+// memory that nobody else touches (so no barrier is needed, only a wait for
+// its own copies): kGnRing rows are on their way at any time, in steps of
+// kGnStep rows. Of a pass over more rows than that the last kGnRing stay in
+// the slots, and a second pass starts with those while it fetches the others
+// again. Without slots (VEC = 1) rows go straight to registers.
+__device__ __forceinline__ void copy_async16(unsigned dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T, int VEC, int TENSORS> struct Rows {
+  static constexpr int NG = kGnRing / kGnStep;   // steps in flight
+  const T* p[TENSORS];
+  int64_t step[TENSORS];    // between the thread's rows
+  int rows, steps;
+  unsigned slots;           // this thread's first slot
+  Pack<T, VEC> v[TENSORS][kGnStep];
+
+  __device__ __forceinline__ void init(int n, void* ring) {
+    rows = n;
+    steps = (n + kGnStep - 1) / kGnStep;
+    slots = (unsigned)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  }
+  __device__ __forceinline__ void fetch(int g, int slot) {
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t)
+#pragma unroll
+      for (int j = 0; j < kGnStep; ++j) {
+        const int r = g * kGnStep + j;
+        if (r < rows)
+          copy_async16(slots + (t * kGnRing + slot * kGnStep + j) * (kGnThreads * 16),
+                       p[t] + r * step[t]);
+      }
+  }
+  __device__ __forceinline__ void take(int slot) {
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t)
+#pragma unroll
+      for (int j = 0; j < kGnStep; ++j) {
+        uint4& u = v[t][j].v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "r"(slots + (t * kGnRing + slot * kGnStep + j) * (kGnThreads * 16)));
+      }
+  }
+  // Start the first pass (or the only one).
+  __device__ __forceinline__ void start() {
+    if constexpr (VEC > 1) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if (g < steps) fetch(g, g);
+        copy_commit();
+      }
+    }
+  }
+  // body(j, row) for every row, j its place in v.
+  template <typename F> __device__ __forceinline__ void pass(F&& body) {
+    if constexpr (VEC > 1) {
+      for (int g = 0; g < steps; ++g) {
+        copy_wait<NG - 1>();
+        take(g % NG);
+#pragma unroll
+        for (int j = 0; j < kGnStep; ++j)
+          if (g * kGnStep + j < rows) body(j, g * kGnStep + j);
+        if (g + NG < steps) fetch(g + NG, g % NG);
+        copy_commit();
+      }
+    } else {
+      direct(body);
+    }
+  }
+  // The second pass over the same rows, those in the slots first.
+  template <typename F> __device__ __forceinline__ void again(F&& body) {
+    if constexpr (VEC > 1) {
+      const int far = steps > NG ? steps - NG : 0;   // steps that have left the slots
+      const int kept = steps - far;
+      for (int q = 0; q < steps; ++q) {
+        const int slot = (far + q) % NG, g = q < kept ? far + q : q - kept;
+        copy_wait<NG - 1>();
+        take(slot);
+#pragma unroll
+        for (int j = 0; j < kGnStep; ++j)
+          if (g * kGnStep + j < rows) body(j, g * kGnStep + j);
+        if (q < far) fetch(q, slot);
+        copy_commit();
+      }
+    } else {
+      direct(body);
+    }
+  }
+  template <typename F> __device__ __forceinline__ void direct(F&& body) {
+    constexpr int UN = 8 / TENSORS;
+    int r = 0;
+    for (; r + UN <= rows; r += UN) {
+      Pack<T, VEC> q[TENSORS][UN];
+#pragma unroll
+      for (int j = 0; j < UN; ++j)
+#pragma unroll
+        for (int t = 0; t < TENSORS; ++t) q[t][j].load(p[t] + (r + j) * step[t]);
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
+#pragma unroll
+        for (int t = 0; t < TENSORS; ++t) v[t][0] = q[t][j];
+        body(0, r + j);
+      }
+    }
+    for (; r < rows; ++r) {
+#pragma unroll
+      for (int t = 0; t < TENSORS; ++t) v[t][0].load(p[t] + r * step[t]);
+      body(0, r);
+    }
+  }
+};
+
 // ---- forward: partial statistics of one unit -------------------------------------
 // Each column is summed as d = x - k and d^2, k the column's value in the
 // slice's first row. k is one of the data, so (mean - k)^2 is itself a term
 // of the variance: with n rows a slice, cancellation in s2 - s1^2 / n costs
 // at most about n * 2^-24 of the group's sum of squares, whatever the mean.
 // Columns, and later slices, are merged by the parallel-variance identity
-// M2 = sum M2_i + n_i (mean_i - mean)^2. The first HOLD rows stay in `held`.
-template <typename T, int VEC, int HOLD>
+// M2 = sum M2_i + n_i (mean_i - mean)^2.
+template <typename T, int VEC>
 __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              Pack<T, VEC>* held, float2* out) {
+                                              Rows<T, VEC, 1>& rows, float2* out) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 k[NP], s1[NP], s2[NP], v[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) k[i] = s1[i] = s2[i] = splat2(0.f);
-  const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
-  const int64_t step = (int64_t)u.TY * a.x_row;
   if (u.rows > 0) {
     Pack<T, VEC> first;
-    first.load(p - u.ty * a.x_row);
-#pragma unroll
-    for (int j = 0; j < HOLD; ++j)
-      if (j < u.rows) held[j].load(p + j * step);
+    first.load(rows.p[0] - u.ty * a.x_row);
     first.get(k);
-    auto add = [&](const Pack<T, VEC>& q) {
-      q.get(v);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 d = fma2(k[i], splat2(-1.f), v[i]);
-        s1[i] = add2(s1[i], d);
-        s2[i] = fma2(d, d, s2[i]);
-      }
-    };
-#pragma unroll
-    for (int j = 0; j < HOLD; ++j)
-      if (j < u.rows) add(held[j]);
-    int r = HOLD;
-    p += HOLD * step;
-    constexpr int UN = HOLD > 0 ? 4 : 8;
-    for (; r + UN <= u.rows; r += UN, p += UN * step) {
-      Pack<T, VEC> q[UN];
-#pragma unroll
-      for (int j = 0; j < UN; ++j) q[j].load(p + j * step);
-#pragma unroll
-      for (int j = 0; j < UN; ++j) add(q[j]);
-    }
-    for (; r < u.rows; ++r, p += step) {
-      Pack<T, VEC> q;
-      q.load(p);
-      add(q);
-    }
   }
+  rows.pass([&](int j, int) {
+    rows.v[0][j].get(v);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 d = fma2(k[i], splat2(-1.f), v[i]);
+      s1[i] = add2(s1[i], d);
+      s2[i] = fma2(d, d, s2[i]);
+    }
+  });
   if (u.on && u.ty == 0) put_pairs<VEC>(sm.k + u.tx * VEC, k);
   const float n = (float)u.nr, inv = u.nr > 0 ? 1.f / n : 0.f;
   gn_columns<VEC>(u, sm, s1, s2, [&](int c, float sa, float sb) {
@@ -450,9 +547,9 @@ __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit
 }
 
 // ---- forward: normalize one unit -------------------------------------------------
-template <typename T, int VEC, int ACT, int HOLD>
+template <typename T, int VEC, int ACT, bool AGAIN>
 __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              const Pack<T, VEC>* held) {
+                                              Rows<T, VEC, 1>& rows) {
   constexpr int NP = Pack<T, VEC>::NP;
   for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
     const int lg = (u.c0 + c) / a.cpg - u.g0;
@@ -466,50 +563,22 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
     get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
     get_pairs<VEC>(sm.par[1] + u.tx * VEC, w);
     get_pairs<VEC>(sm.par[2] + u.tx * VEC, b);
-    const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
     T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
-    const int64_t step = (int64_t)u.TY * a.x_row, ostep = (int64_t)u.TY * a.out_row;
-    auto put = [&](const Pack<T, VEC>& q, T* to) {
-      q.get(v);
+    const int64_t ostep = (int64_t)u.TY * a.out_row;
+    auto body = [&](int j, int r) {
+      rows.v[0][j].get(v);
 #pragma unroll
       for (int i = 0; i < NP; ++i) v[i] = act2<ACT>(fma2(add2(v[i], m[i]), w[i], b[i]));
-      Pack<T, VEC> r;
-      r.set(v);
-      r.store(to);
+      Pack<T, VEC> y;
+      y.set(v);
+      y.store(o + r * ostep);
     };
-#pragma unroll
-    for (int j = 0; j < HOLD; ++j)
-      if (j < u.rows) put(held[j], o + j * ostep);
-    int r = HOLD;
-    p += HOLD * step;
-    o += HOLD * ostep;
-    constexpr int UN = 4;
-    for (; r + UN <= u.rows; r += UN, p += UN * step, o += UN * ostep) {
-      Pack<T, VEC> q[UN];
-#pragma unroll
-      for (int j = 0; j < UN; ++j) q[j].load(p + j * step);
-#pragma unroll
-      for (int j = 0; j < UN; ++j) put(q[j], o + j * ostep);
-    }
-    for (; r < u.rows; ++r, p += step, o += ostep) {
-      Pack<T, VEC> q;
-      q.load(p);
-      put(q, o);
-    }
+    if (AGAIN) rows.again(body);
+    else rows.pass(body);
   }
 }
 
 // ---- backward ------------------------------------------------------------------------
-// What a thread keeps of its first rows: x, and dz in fp32 (dy itself where
-// there is no activation), so that the activation's slope is not taken twice.
-template <typename T, int VEC, int ACT> struct Held {
-  Pack<T, VEC> x;
-  float2 dz[Pack<T, VEC>::NP];
-};
-template <typename T, int VEC> struct Held<T, VEC, kActNone> {
-  Pack<T, VEC> x, dy;
-};
-
 // mean, rstd, w and beta of the unit's columns.
 template <typename T>
 __device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
@@ -523,23 +592,13 @@ __device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, 
 }
 
 // Sums of one unit.
-template <typename T, int VEC, int ACT, int HOLD>
+template <typename T, int VEC, int ACT>
 __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  Held<T, VEC, ACT>* held, float2* out) {
+                                                  Rows<T, VEC, 2>& rows, float2* out) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 sa[NP], sb[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) sa[i] = sb[i] = splat2(0.f);
-  const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
-  const T* q = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
-  const int64_t ps = (int64_t)u.TY * a.x_row, qs = (int64_t)u.TY * a.dy_row;
-  Pack<T, VEC> hd[HOLD > 0 ? HOLD : 1];
-#pragma unroll
-  for (int j = 0; j < HOLD; ++j)
-    if (j < u.rows) {
-      held[j].x.load(p + j * ps);
-      hd[j].load(q + j * qs);
-    }
   gn_bwd_params<T>(a, u, sm);
   __syncthreads();
   if (u.rows > 0) {
@@ -548,9 +607,9 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
     get_pairs<VEC>(sm.par[1] + u.tx * VEC, rs);
     get_pairs<VEC>(sm.par[2] + u.tx * VEC, w);
     get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
-    auto add = [&](const Pack<T, VEC>& px, const Pack<T, VEC>& pd) {   // leaves dz in d
-      px.get(v);
-      pd.get(d);
+    rows.pass([&](int j, int) {
+      rows.v[0][j].get(v);
+      rows.v[1][j].get(d);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float2 xh = mul2(add2(v[i], m[i]), rs[i]);
@@ -558,38 +617,7 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
         sa[i] = add2(sa[i], d[i]);
         sb[i] = fma2(d[i], xh, sb[i]);
       }
-    };
-#pragma unroll
-    for (int j = 0; j < HOLD; ++j)
-      if (j < u.rows) {
-        add(held[j].x, hd[j]);
-        if constexpr (ACT == kActNone) {
-          held[j].dy = hd[j];
-        } else {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) held[j].dz[i] = d[i];
-        }
-      }
-    int r = HOLD;
-    p += HOLD * ps;
-    q += HOLD * qs;
-    constexpr int UN = 4;
-    for (; r + UN <= u.rows; r += UN, p += UN * ps, q += UN * qs) {
-      Pack<T, VEC> px[UN], pd[UN];
-#pragma unroll
-      for (int j = 0; j < UN; ++j) {
-        px[j].load(p + j * ps);
-        pd[j].load(q + j * qs);
-      }
-#pragma unroll
-      for (int j = 0; j < UN; ++j) add(px[j], pd[j]);
-    }
-    for (; r < u.rows; ++r, p += ps, q += qs) {
-      Pack<T, VEC> px, pd;
-      px.load(p);
-      pd.load(q);
-      add(px, pd);
-    }
+    });
   }
   __syncthreads();   // the parameters give way to the sums
   float* cols = a.cols + ((int64_t)u.n * a.slices + u.slice) * 2 * a.channels + u.c0;
@@ -617,9 +645,9 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
 }
 
 // dx of one unit.
-template <typename T, int VEC, int ACT, int HOLD>
+template <typename T, int VEC, int ACT, bool AGAIN>
 __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  const Held<T, VEC, ACT>* held) {
+                                                  Rows<T, VEC, 2>& rows) {
   constexpr int NP = Pack<T, VEC>::NP;
   gn_bwd_params<T>(a, u, sm);
   for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
@@ -636,62 +664,26 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
     get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
     get_pairs<VEC>(sm.par[4] + u.tx * VEC, c1);
     get_pairs<VEC>(sm.par[5] + u.tx * VEC, c2);
-    const T* p = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
-    const T* q = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
     T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
-    const int64_t ps = (int64_t)u.TY * a.x_row, qs = (int64_t)u.TY * a.dy_row,
-                  os = (int64_t)u.TY * a.out_row;
+    const int64_t ostep = (int64_t)u.TY * a.out_row;
     // The product w dz is rounded before c1 is taken off (no fma): in a group
     // of one value c1 is that very product and dx is exactly 0.
-    auto put = [&](const Pack<T, VEC>& px, T* to, bool have_dz) {
-      px.get(v);
+    auto body = [&](int j, int r) {
+      rows.v[0][j].get(v);
+      rows.v[1][j].get(d);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float2 xh = mul2(add2(v[i], m[i]), rs[i]);
-        if (ACT != kActNone && !have_dz) d[i] = mul2(d[i], act_grad2<ACT>(fma2(xh, w[i], b[i])));
+        if (ACT != kActNone) d[i] = mul2(d[i], act_grad2<ACT>(fma2(xh, w[i], b[i])));
         const float2 g = make_float2(__fmul_rn(w[i].x, d[i].x), __fmul_rn(w[i].y, d[i].y));
         v[i] = mul2(rs[i], fma2(xh, c2[i], add2(g, c1[i])));
       }
-      Pack<T, VEC> r;
-      r.set(v);
-      r.store(to);
+      Pack<T, VEC> y;
+      y.set(v);
+      y.store(o + r * ostep);
     };
-#pragma unroll
-    for (int j = 0; j < HOLD; ++j)
-      if (j < u.rows) {
-        if constexpr (ACT == kActNone) {
-          held[j].dy.get(d);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) d[i] = held[j].dz[i];
-        }
-        put(held[j].x, o + j * os, true);
-      }
-    int r = HOLD;
-    p += HOLD * ps;
-    q += HOLD * qs;
-    o += HOLD * os;
-    constexpr int UN = 2;
-    for (; r + UN <= u.rows; r += UN, p += UN * ps, q += UN * qs, o += UN * os) {
-      Pack<T, VEC> px[UN], pd[UN];
-#pragma unroll
-      for (int j = 0; j < UN; ++j) {
-        px[j].load(p + j * ps);
-        pd[j].load(q + j * qs);
-      }
-#pragma unroll
-      for (int j = 0; j < UN; ++j) {
-        pd[j].get(d);
-        put(px[j], o + j * os, false);
-      }
-    }
-    for (; r < u.rows; ++r, p += ps, q += qs, o += os) {
-      Pack<T, VEC> px, pd;
-      px.load(p);
-      pd.load(q);
-      pd.get(d);
-      put(px, o, false);
-    }
+    if (AGAIN) rows.again(body);
+    else rows.pass(body);
   }
 }
 
@@ -699,59 +691,86 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
 __device__ __forceinline__ float2* gn_part(const GnArgs& a, const GnUnit& u) {
   return a.part + (((int64_t)u.n * a.tiles + u.tile) * a.slices + u.slice) * a.max_groups;
 }
+extern __shared__ __align__(16) unsigned char gn_ring[];
+
+// A unit's rows, on their way.
+template <typename T, int VEC>
+__device__ __forceinline__ Rows<T, VEC, 1> gn_fwd_rows(const GnArgs& a, const GnUnit& u) {
+  Rows<T, VEC, 1> r;
+  r.p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+  r.step[0] = (int64_t)u.TY * a.x_row;
+  r.init(u.rows, gn_ring);
+  r.start();
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Rows<T, VEC, 2> gn_bwd_rows(const GnArgs& a, const GnUnit& u) {
+  Rows<T, VEC, 2> r;
+  r.p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+  r.step[0] = (int64_t)u.TY * a.x_row;
+  r.p[1] = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
+  r.step[1] = (int64_t)u.TY * a.dy_row;
+  r.init(u.rows, gn_ring);
+  r.start();
+  return r;
+}
 
 // One launch takes the statistics of the panels [stat0, stat1) and applies
 // those of [app0, app1), which an earlier launch gathered.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads)
+__global__ void __launch_bounds__(kGnThreads, 3)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
-    gn_stats_unit<T, VEC, 0>(a, u, sm, nullptr, gn_part(a, u));
+    Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
+    gn_stats_unit<T, VEC>(a, u, sm, rows, gn_part(a, u));
   }
   if (app0 + p < app1) {
     const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
+    Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     gn_combine<false>(a, u, sm);
-    gn_apply_unit<T, VEC, ACT, 0>(a, u, sm, nullptr);
+    gn_apply_unit<T, VEC, ACT, false>(a, u, sm, rows);
   }
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads)
+__global__ void __launch_bounds__(kGnThreads, 2)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
-    gn_bwd_stats_unit<T, VEC, ACT, 0>(a, u, sm, nullptr, gn_part(a, u));
+    Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
+    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, gn_part(a, u));
   }
   if (app0 + p < app1) {
     const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
+    Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     gn_combine<true>(a, u, sm);
-    gn_bwd_apply_unit<T, VEC, ACT, 0>(a, u, sm, nullptr);
+    gn_bwd_apply_unit<T, VEC, ACT, false>(a, u, sm, rows);
   }
 }
 
 // A panel a cluster, in one launch: the statistics, a barrier of the
-// cluster, and the rows again: those that are held, then the others out of
-// the L2 cache.
+// cluster, and the rows again: those still in the slots, then the others out
+// of the L2 cache.
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a) {
   __shared__ GnSmem sm;
   __shared__ float2 part[kGnMaxTileCh];
   const int p = blockIdx.x / a.slices;
   const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
-  Pack<T, VEC> held[kGnFwdHold];
-  gn_stats_unit<T, VEC, kGnFwdHold>(a, u, sm, held, part);
+  Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
+  gn_stats_unit<T, VEC>(a, u, sm, rows, part);
   cluster_arrive();
   cluster_wait();
   gn_combine_cluster<false>(a, u, sm, part);
   cluster_arrive();
-  gn_apply_unit<T, VEC, ACT, kGnFwdHold>(a, u, sm, held);
+  gn_apply_unit<T, VEC, ACT, true>(a, u, sm, rows);
   cluster_wait();   // no CTA leaves while another reads its partials
 }
 
@@ -761,13 +780,13 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a)
   __shared__ float2 part[kGnMaxTileCh];
   const int p = blockIdx.x / a.slices;
   const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
-  Held<T, VEC, ACT> held[kGnBwdHold];
-  gn_bwd_stats_unit<T, VEC, ACT, kGnBwdHold>(a, u, sm, held, part);
+  Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
+  gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, part);
   cluster_arrive();
   cluster_wait();
   gn_combine_cluster<true>(a, u, sm, part);
   cluster_arrive();
-  gn_bwd_apply_unit<T, VEC, ACT, kGnBwdHold>(a, u, sm, held);
+  gn_bwd_apply_unit<T, VEC, ACT, true>(a, u, sm, rows);
   cluster_wait();
 }
 
