@@ -101,7 +101,8 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
       p->batch = b < step ? step : b;
       if (p->batch > p->panels) p->batch = p->panels;
     }
-    int64_t slices = ((int64_t)sms * 4 + p->batch - 1) / p->batch;
+    int64_t slices = ((int64_t)sms * (bwd ? 2 : 3) + p->batch - 1) / p->batch;
+    if (slices > kGnMaxSlices) slices = kGnMaxSlices;
     const int64_t least = 4 * TY;       // rows of a slice: four a thread
     if (slices > (rows + least - 1) / least) slices = (rows + least - 1) / least;
     if (slices < 1) slices = 1;

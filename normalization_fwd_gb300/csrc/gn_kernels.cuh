@@ -23,6 +23,7 @@ constexpr int kGnWarps = kGnThreads / 32;
 constexpr int kGnMaxTileCh = 512;   // most channels of a column tile
 constexpr int kGnRing = 8;          // rows a thread has in flight, or keeps
 constexpr int kGnStep = 2;          // rows of one step
+constexpr int kGnMaxSlices = 512;   // most slices of a panel
 constexpr int kGnRingBytes = kGnRing * kGnThreads * 16;   // of one tensor
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
@@ -65,31 +66,82 @@ __device__ __forceinline__ float rcpf(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 1 / (1 + e^-z) by the hardware's exponential and reciprocal (each good to
-// about 2^-23, relative); an e^-z that overflows gives 0.
-__device__ __forceinline__ float2 sigmoid2(float2 z) {
-  const float2 t = mul2(z, splat2(-1.4426950408889634f));
-  const float2 d = add2(make_float2(ex2f(t.x), ex2f(t.y)), splat2(1.f));
-  return make_float2(rcpf(d.x), rcpf(d.y));
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
-template <int ACT> __device__ __forceinline__ float2 act2(float2 z) {
-  if (ACT == kActSilu) return mul2(z, sigmoid2(z));
+// 1 / (1 + e^-z) of NP pairs. The special-function unit takes 16 lanes a
+// cycle and would bound the kernels with an exponential and a reciprocal for
+// each value, so four values share a reciprocal: with d = 1 + e^-z,
+// 1 / d0 = d1 d2 d3 / (d0 d1 d2 d3). The product stays finite while every d
+// is below 2^31 (z > -21); a thread with a lower z, or a NaN that the others
+// must not get, takes the reciprocals one by one. The exponential and the reciprocal are good to about 2^-23,
+// relative; an e^-z that overflows gives 0.
+template <int NP> __device__ __forceinline__ void sigmoid(const float2* z, float2* s) {
+  float2 t[NP], d[NP];
+  float top = -1.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    t[i] = mul2(z[i], splat2(-1.4426950408889634f));
+    top = max_nan(top, max_nan(t[i].x, t[i].y));
+  }
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    d[i] = add2(make_float2(ex2f(t[i].x), ex2f(t[i].y)), splat2(1.f));
+  if (NP % 2 == 0 && top < 30.f) {
+#pragma unroll
+    for (int i = 0; i + 1 < NP; i += 2) {
+      const float2 p = mul2(d[i], d[i + 1]);           // (d0 d2, d1 d3)
+      const float r = rcpf(p.x * p.y);
+      const float2 q = mul2(make_float2(p.y, p.x), splat2(r));   // 1 / p
+      s[i] = mul2(q, d[i + 1]);
+      s[i + 1] = mul2(q, d[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) s[i] = make_float2(rcpf(d[i].x), rcpf(d[i].y));
+  }
+}
+// z -> act(z) of NP pairs.
+template <int ACT, int NP> __device__ __forceinline__ void activate(float2* z) {
+  if (ACT == kActSilu) {
+    float2 s[NP];
+    sigmoid<NP>(z, s);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) z[i] = mul2(z[i], s[i]);
+  }
   // normcdff keeps relative accuracy in the lower tail, where (1 + erf) / 2
   // cancels.
-  if (ACT == kActGelu) return mul2(z, make_float2(normcdff(z.x), normcdff(z.y)));
-  return z;
+  if (ACT == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      z[i].x *= normcdff(z[i].x);
+      z[i].y *= normcdff(z[i].y);
+    }
+  }
 }
 __device__ __forceinline__ float gelu_grad(float z) {
   return normcdff(z) + z * 0.3989422804f * __expf(-0.5f * z * z);
 }
-template <int ACT> __device__ __forceinline__ float2 act_grad2(float2 z) {
+// d -> d * act'(z) of NP pairs.
+template <int ACT, int NP> __device__ __forceinline__ void through(float2* d, const float2* z) {
   if (ACT == kActSilu) {
-    const float2 s = sigmoid2(z);
-    const float2 o = fma2(s, splat2(-1.f), splat2(1.f));   // 1 - s
-    return mul2(s, fma2(z, o, splat2(1.f)));
+    float2 s[NP];
+    sigmoid<NP>(z, s);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 o = fma2(s[i], splat2(-1.f), splat2(1.f));   // 1 - s
+      d[i] = mul2(d[i], mul2(s[i], fma2(z[i], o, splat2(1.f))));
+    }
   }
-  if (ACT == kActGelu) return make_float2(gelu_grad(z.x), gelu_grad(z.y));
-  return splat2(1.f);
+  if (ACT == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      d[i].x *= gelu_grad(z[i].x);
+      d[i].y *= gelu_grad(z[i].y);
+    }
+  }
 }
 
 // ---- a thread's VEC elements, as NP pairs ---------------------------------------
@@ -270,29 +322,27 @@ template <int N> __device__ __forceinline__ void copy_wait() {
 
 template <typename T, int VEC, int TENSORS> struct Rows {
   static constexpr int NG = kGnRing / kGnStep;   // steps in flight
-  const T* p[TENSORS];
-  int64_t step[TENSORS];    // between the thread's rows
+  const T* p[TENSORS];      // the thread's first row
+  int64_t step[TENSORS];    // from one of its rows to the next
+  const T* next[TENSORS];   // the next one to fetch
   int rows, steps;
   unsigned slots;           // this thread's first slot
   Pack<T, VEC> v[TENSORS][kGnStep];
 
-  __device__ __forceinline__ void init(int n, void* ring) {
-    rows = n;
-    steps = (n + kGnStep - 1) / kGnStep;
-    slots = (unsigned)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
-  }
-  __device__ __forceinline__ void fetch(int g, int slot) {
+  __device__ __forceinline__ void fetch(int g, int place) {   // step g, into place's slots
+    const unsigned at = slots + (unsigned)place % NG * (kGnStep * kGnThreads * 16);
 #pragma unroll
-    for (int t = 0; t < TENSORS; ++t)
+    for (int j = 0; j < kGnStep; ++j)
+      if (g * kGnStep + j < rows) {
 #pragma unroll
-      for (int j = 0; j < kGnStep; ++j) {
-        const int r = g * kGnStep + j;
-        if (r < rows)
-          copy_async16(slots + (t * kGnRing + slot * kGnStep + j) * (kGnThreads * 16),
-                       p[t] + r * step[t]);
+        for (int t = 0; t < TENSORS; ++t) {
+          copy_async16(at + t * kGnRingBytes + j * (kGnThreads * 16), next[t]);
+          next[t] += step[t];
+        }
       }
   }
-  __device__ __forceinline__ void take(int slot) {
+  __device__ __forceinline__ void take(int g) {
+    const unsigned at = slots + (unsigned)g % NG * (kGnStep * kGnThreads * 16);
 #pragma unroll
     for (int t = 0; t < TENSORS; ++t)
 #pragma unroll
@@ -300,55 +350,70 @@ template <typename T, int VEC, int TENSORS> struct Rows {
         uint4& u = v[t][j].v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "r"(slots + (t * kGnRing + slot * kGnStep + j) * (kGnThreads * 16)));
+                     : "r"(at + t * kGnRingBytes + j * (kGnThreads * 16)));
       }
   }
-  // Start the first pass (or the only one).
-  __device__ __forceinline__ void start() {
+  // Start the first pass (or the only one) over n rows.
+  __device__ __forceinline__ void start(int n, void* ring) {
+    rows = n;
+    steps = (n + kGnStep - 1) / kGnStep;
+    slots = (unsigned)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
     if constexpr (VEC > 1) {
 #pragma unroll
+      for (int t = 0; t < TENSORS; ++t) next[t] = p[t];
+#pragma unroll
       for (int g = 0; g < NG; ++g) {
-        if (g < steps) fetch(g, g);
+        fetch(g, g);
         copy_commit();
       }
     }
   }
-  // body(j, row) for every row, j its place in v.
-  template <typename F> __device__ __forceinline__ void pass(F&& body) {
+  // body(j, to) for every row, j its place in v, `to` its place in an output
+  // whose first row is at `o`.
+  template <typename F> __device__ __forceinline__ void pass(T* o, int64_t ostep, F&& body) {
     if constexpr (VEC > 1) {
       for (int g = 0; g < steps; ++g) {
         copy_wait<NG - 1>();
-        take(g % NG);
+        take(g);
 #pragma unroll
-        for (int j = 0; j < kGnStep; ++j)
-          if (g * kGnStep + j < rows) body(j, g * kGnStep + j);
-        if (g + NG < steps) fetch(g + NG, g % NG);
+        for (int j = 0; j < kGnStep; ++j) {
+          if (g * kGnStep + j < rows) body(j, o);
+          o += ostep;
+        }
+        fetch(g + NG, g);
         copy_commit();
       }
     } else {
-      direct(body);
+      direct(o, ostep, body);
     }
   }
   // The second pass over the same rows, those in the slots first.
-  template <typename F> __device__ __forceinline__ void again(F&& body) {
+  template <typename F> __device__ __forceinline__ void again(T* o, int64_t ostep, F&& body) {
     if constexpr (VEC > 1) {
       const int far = steps > NG ? steps - NG : 0;   // steps that have left the slots
-      const int kept = steps - far;
-      for (int q = 0; q < steps; ++q) {
-        const int slot = (far + q) % NG, g = q < kept ? far + q : q - kept;
-        copy_wait<NG - 1>();
-        take(slot);
 #pragma unroll
-        for (int j = 0; j < kGnStep; ++j)
-          if (g * kGnStep + j < rows) body(j, g * kGnStep + j);
-        if (q < far) fetch(q, slot);
+      for (int t = 0; t < TENSORS; ++t) next[t] = p[t];
+      T* const first = o;
+      o += far * kGnStep * ostep;
+      // Steps far, ..., steps - 1 out of their slots, which take 0, 1, ... after them.
+      for (int q = 0; q < steps; ++q) {
+        const int g = far + q < steps ? far + q : far + q - steps;
+        if (g == 0) o = first;
+        copy_wait<NG - 1>();
+        take(far + q);
+#pragma unroll
+        for (int j = 0; j < kGnStep; ++j) {
+          if (g * kGnStep + j < rows) body(j, o);
+          o += ostep;
+        }
+        if (q < far) fetch(q, far + q);
         copy_commit();
       }
     } else {
-      direct(body);
+      direct(o, ostep, body);
     }
   }
-  template <typename F> __device__ __forceinline__ void direct(F&& body) {
+  template <typename F> __device__ __forceinline__ void direct(T* o, int64_t ostep, F&& body) {
     constexpr int UN = 8 / TENSORS;
     int r = 0;
     for (; r + UN <= rows; r += UN) {
@@ -361,13 +426,15 @@ template <typename T, int VEC, int TENSORS> struct Rows {
       for (int j = 0; j < UN; ++j) {
 #pragma unroll
         for (int t = 0; t < TENSORS; ++t) v[t][0] = q[t][j];
-        body(0, r + j);
+        body(0, o);
+        o += ostep;
       }
     }
     for (; r < rows; ++r) {
 #pragma unroll
       for (int t = 0; t < TENSORS; ++t) v[t][0].load(p[t] + r * step[t]);
-      body(0, r);
+      body(0, o);
+      o += ostep;
     }
   }
 };
@@ -391,7 +458,7 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
     first.load(rows.p[0] - u.ty * a.x_row);
     first.get(k);
   }
-  rows.pass([&](int j, int) {
+  rows.pass(static_cast<T*>(nullptr), 0, [&](int j, T*) {
     rows.v[0][j].get(v);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -449,51 +516,54 @@ __device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSm
 
 // Merge the partials of the unit's groups into sm.g0 = mean, sm.g1 = rstd
 // (forward) or into sm.g0 = c1, sm.g1 = c2 (backward): one warp a group, the
-// slices dealt to its lanes, the same order in every CTA.
+// slices dealt to its lanes, the same order in every CTA. A lane has all its
+// partials of a tile on their way at once and keeps them for the second sum.
 template <bool BWD>
 __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
+  constexpr int N = kGnMaxSlices / 32;
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
     const int g = u.g0 + lg, ch0 = g * a.cpg, ch1 = ch0 + a.cpg;
     const int t0 = ch0 / u.tc, t1 = (ch1 - 1) / u.tc;
     float s0 = 0.f, s1 = 0.f, base = 0.f;
-    if (!BWD)   // the mean of the first slice of the group's first tile
-      base = a.part[((int64_t)u.n * a.tiles + t0) * a.slices * a.max_groups + g -
-                    t0 * u.tc / a.cpg].x;
-    for (int t = t0; t <= t1; ++t) {
-      const int nc = min(ch1, (t + 1) * u.tc) - max(ch0, t * u.tc);
+    float2 v[N];
+    const auto fetch = [&](int t) {
       const float2* p = a.part + ((int64_t)u.n * a.tiles + t) * a.slices * a.max_groups +
                         (g - t * u.tc / a.cpg);
-#pragma unroll 4
-      for (int i = lane; i < a.slices; i += 32) {
-        const float2 v = p[(int64_t)i * a.max_groups];
-        if (BWD) {
-          s0 += v.x;
-          s1 += v.y;
-        } else {
-          const int64_t nr = min(a.slice_rows, a.rows - i * a.slice_rows);
-          s0 = fmaf((float)nr * (float)nc, v.x - base, s0);
-        }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        v[j] = make_float2(0.f, 0.f);
+        if (lane + 32 * j < a.slices) v[j] = p[(int64_t)(lane + 32 * j) * a.max_groups];
       }
+    };
+    // values of the group in slice i of tile t
+    const auto count = [&](int t, int i) {
+      const int nc = min(ch1, (t + 1) * u.tc) - max(ch0, t * u.tc);
+      return (float)min(a.slice_rows, a.rows - i * a.slice_rows) * (float)nc;
+    };
+    for (int t = t0; t <= t1; ++t) {
+      fetch(t);
+      if (!BWD && t == t0) base = __shfl_sync(0xffffffffu, v[0].x, 0);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (lane + 32 * j < a.slices) {
+          s0 = BWD ? s0 + v[j].x : fmaf(count(t, lane + 32 * j), v[j].x - base, s0);
+          if (BWD) s1 += v[j].y;
+        }
     }
     s0 = base + group_sum<32>(s0) * a.inv_m;
-    if (BWD) {
-      s1 = group_sum<32>(s1) * a.inv_m;
-    } else {
+    if (!BWD) {
       for (int t = t0; t <= t1; ++t) {
-        const int nc = min(ch1, (t + 1) * u.tc) - max(ch0, t * u.tc);
-        const float2* p = a.part + ((int64_t)u.n * a.tiles + t) * a.slices * a.max_groups +
-                          (g - t * u.tc / a.cpg);
-#pragma unroll 4
-        for (int i = lane; i < a.slices; i += 32) {
-          const float2 v = p[(int64_t)i * a.max_groups];
-          const int64_t nr = min(a.slice_rows, a.rows - i * a.slice_rows);
-          const float d = v.x - s0;
-          s1 += fmaf((float)nr * (float)nc * d, d, v.y);
-        }
+        if (t1 > t0) fetch(t);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (lane + 32 * j < a.slices) {
+            const float d = v[j].x - s0;
+            s1 += fmaf(count(t, lane + 32 * j) * d, d, v[j].y);
+          }
       }
-      s1 = group_sum<32>(s1) * a.inv_m;
     }
+    s1 = group_sum<32>(s1) * a.inv_m;
     if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0 && u.tile == t0);
   }
   __syncthreads();
@@ -565,16 +635,17 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
     get_pairs<VEC>(sm.par[2] + u.tx * VEC, b);
     T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
     const int64_t ostep = (int64_t)u.TY * a.out_row;
-    auto body = [&](int j, int r) {
+    auto body = [&](int j, T* to) {
       rows.v[0][j].get(v);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) v[i] = act2<ACT>(fma2(add2(v[i], m[i]), w[i], b[i]));
+      for (int i = 0; i < NP; ++i) v[i] = fma2(add2(v[i], m[i]), w[i], b[i]);
+      activate<ACT, NP>(v);
       Pack<T, VEC> y;
       y.set(v);
-      y.store(o + r * ostep);
+      y.store(to);
     };
-    if (AGAIN) rows.again(body);
-    else rows.pass(body);
+    if (AGAIN) rows.again(o, ostep, body);
+    else rows.pass(o, ostep, body);
   }
 }
 
@@ -607,15 +678,20 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
     get_pairs<VEC>(sm.par[1] + u.tx * VEC, rs);
     get_pairs<VEC>(sm.par[2] + u.tx * VEC, w);
     get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
-    rows.pass([&](int j, int) {
+    rows.pass(static_cast<T*>(nullptr), 0, [&](int j, T*) {
       rows.v[0][j].get(v);
       rows.v[1][j].get(d);
+      float2 z[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const float2 xh = mul2(add2(v[i], m[i]), rs[i]);
-        if (ACT != kActNone) d[i] = mul2(d[i], act_grad2<ACT>(fma2(xh, w[i], b[i])));
+        v[i] = mul2(add2(v[i], m[i]), rs[i]);
+        z[i] = fma2(v[i], w[i], b[i]);
+      }
+      through<ACT, NP>(d, z);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
         sa[i] = add2(sa[i], d[i]);
-        sb[i] = fma2(d[i], xh, sb[i]);
+        sb[i] = fma2(d[i], v[i], sb[i]);
       }
     });
   }
@@ -668,22 +744,27 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
     const int64_t ostep = (int64_t)u.TY * a.out_row;
     // The product w dz is rounded before c1 is taken off (no fma): in a group
     // of one value c1 is that very product and dx is exactly 0.
-    auto body = [&](int j, int r) {
+    auto body = [&](int j, T* to) {
       rows.v[0][j].get(v);
       rows.v[1][j].get(d);
+      float2 z[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const float2 xh = mul2(add2(v[i], m[i]), rs[i]);
-        if (ACT != kActNone) d[i] = mul2(d[i], act_grad2<ACT>(fma2(xh, w[i], b[i])));
+        v[i] = mul2(add2(v[i], m[i]), rs[i]);
+        z[i] = fma2(v[i], w[i], b[i]);
+      }
+      through<ACT, NP>(d, z);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
         const float2 g = make_float2(__fmul_rn(w[i].x, d[i].x), __fmul_rn(w[i].y, d[i].y));
-        v[i] = mul2(rs[i], fma2(xh, c2[i], add2(g, c1[i])));
+        v[i] = mul2(rs[i], fma2(v[i], c2[i], add2(g, c1[i])));
       }
       Pack<T, VEC> y;
       y.set(v);
-      y.store(o + r * ostep);
+      y.store(to);
     };
-    if (AGAIN) rows.again(body);
-    else rows.pass(body);
+    if (AGAIN) rows.again(o, ostep, body);
+    else rows.pass(o, ostep, body);
   }
 }
 
@@ -699,8 +780,7 @@ __device__ __forceinline__ Rows<T, VEC, 1> gn_fwd_rows(const GnArgs& a, const Gn
   Rows<T, VEC, 1> r;
   r.p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
   r.step[0] = (int64_t)u.TY * a.x_row;
-  r.init(u.rows, gn_ring);
-  r.start();
+  r.start(u.rows, gn_ring);
   return r;
 }
 template <typename T, int VEC>
@@ -710,8 +790,7 @@ __device__ __forceinline__ Rows<T, VEC, 2> gn_bwd_rows(const GnArgs& a, const Gn
   r.step[0] = (int64_t)u.TY * a.x_row;
   r.p[1] = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
   r.step[1] = (int64_t)u.TY * a.dy_row;
-  r.init(u.rows, gn_ring);
-  r.start();
+  r.start(u.rows, gn_ring);
   return r;
 }
 
@@ -722,6 +801,7 @@ __global__ void __launch_bounds__(kGnThreads, 3)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
     Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
@@ -741,6 +821,7 @@ __global__ void __launch_bounds__(kGnThreads, 2)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
   const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
     Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
