@@ -112,7 +112,7 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
     p->part_bytes = (p->part_bytes + 15) / 16 * 16;
   }
   p->cols_bytes = bwd ? (size_t)samples * p->slices * 2 * channels * sizeof(float) : 0;
-  return p->panels * p->slices <= INT32_MAX;
+  return p->panels * p->slices <= INT32_MAX && p->slice_rows <= INT32_MAX;
 }
 
 struct GnCall {
@@ -167,6 +167,12 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
   a.tiles = p.tiles;
   a.tw = p.tw;
   a.max_groups = p.max_groups;
+  a.by_slices.set(p.slices);
+  a.by_tiles.set(p.tiles);
+  a.by_tw.set(p.tw);
+  a.by_tc.set(p.tw * (vec ? (int)(16 / elem_size(c.dtype)) : 1));
+  a.by_ty.set(kGnThreads / p.tw);
+  a.by_cpg.set(a.cpg);
   a.rows = c.rows;
   a.inv_m = (float)(1.0 / ((double)c.rows * a.cpg));
   const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, act)

@@ -28,6 +28,20 @@ constexpr int kGnRingBytes = kGnRing * kGnThreads * 16;   // of one tensor
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
+// Division of n < 2^31 by a number fixed for the launch: with s = ceil(log2 d)
+// and m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n m) + n) >> s.
+struct FastDiv {
+  unsigned d, m, s;
+  void set(unsigned v) {
+    d = v;
+    for (s = 0; (1ull << s) < v; ++s) {}
+    m = (unsigned)(((1ull << 32) * ((1ull << s) - v)) / v + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi((unsigned)n, m) + (unsigned)n) >> s);
+  }
+};
+
 // Arguments of the group norm kernels (validated on the host).
 struct GnArgs {
   const void* x;
@@ -50,6 +64,7 @@ struct GnArgs {
   int tiles;             // column tiles
   int tw;                // vectors of a column tile
   int max_groups;        // most groups that meet one tile
+  FastDiv by_slices, by_tiles, by_tw, by_tc, by_ty, by_cpg;
   float eps;
   float inv_m;           // 1 / (rows * cpg)
   int zero_centered;
@@ -66,35 +81,32 @@ __device__ __forceinline__ float rcpf(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN wins
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 // 1 / (1 + e^-z) of NP pairs. The special-function unit takes 16 lanes a
 // cycle and would bound the kernels with an exponential and a reciprocal for
 // each value, so four values share a reciprocal: with d = 1 + e^-z,
-// 1 / d0 = d1 d2 d3 / (d0 d1 d2 d3). The product stays finite while every d
-// is below 2^31 (z > -21); a thread with a lower z, or a NaN that the others
-// must not get, takes the reciprocals one by one. The exponential and the reciprocal are good to about 2^-23,
-// relative; an e^-z that overflows gives 0.
+// 1 / d0 = d1 d2 d3 / (d0 d1 d2 d3). Where that product passes 2^126 (every z
+// below -21, say), or a NaN is among the four that the others must not get,
+// the thread takes the reciprocals one by one. The exponential and the
+// reciprocal are good to about 2^-23, relative; an e^-z that overflows gives 0.
 template <int NP> __device__ __forceinline__ void sigmoid(const float2* z, float2* s) {
-  float2 t[NP], d[NP];
-  float top = -1.f;
+  float2 d[NP];
+  float prod[NP / 2 + 1];
+  bool fine = NP % 2 == 0;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    t[i] = mul2(z[i], splat2(-1.4426950408889634f));
-    top = max_nan(top, max_nan(t[i].x, t[i].y));
+    const float2 t = mul2(z[i], splat2(-1.4426950408889634f));
+    d[i] = add2(make_float2(ex2f(t.x), ex2f(t.y)), splat2(1.f));
   }
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
-    d[i] = add2(make_float2(ex2f(t[i].x), ex2f(t[i].y)), splat2(1.f));
-  if (NP % 2 == 0 && top < 30.f) {
+  for (int i = 0; i + 1 < NP; i += 2) {
+    s[i] = mul2(d[i], d[i + 1]);   // (d0 d2, d1 d3)
+    prod[i / 2] = s[i].x * s[i].y;
+    fine = fine && prod[i / 2] < 0x1p126f;
+  }
+  if (fine) {
 #pragma unroll
     for (int i = 0; i + 1 < NP; i += 2) {
-      const float2 p = mul2(d[i], d[i + 1]);           // (d0 d2, d1 d3)
-      const float r = rcpf(p.x * p.y);
-      const float2 q = mul2(make_float2(p.y, p.x), splat2(r));   // 1 / p
+      const float2 q = mul2(make_float2(s[i].y, s[i].x), splat2(rcpf(prod[i / 2])));
       s[i] = mul2(q, d[i + 1]);
       s[i + 1] = mul2(q, d[i]);
     }
@@ -169,14 +181,10 @@ template <typename T> struct Pack<T, 1> {
 // place, afterwards, the parameters of the tile's columns.
 struct GnSmem {
   union {
-    struct {
-      float a[kGnThreads * 8];
-      float b[kGnThreads * 8];
-    } lane;
+    float2 lane[kGnThreads * 8];
     float par[6][kGnMaxTileCh];
   };
-  float ca[2 * kGnMaxTileCh];   // column sums, in parts, then whole
-  float cb[2 * kGnMaxTileCh];
+  float2 col[kGnMaxTileCh];     // column sums, in parts, then whole
   float k[kGnMaxTileCh];        // forward: what the columns are shifted by
   float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
   float g1[kGnMaxTileCh];       // rstd, or c2
@@ -222,21 +230,21 @@ struct GnUnit {
 template <int VEC>
 __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice) {
   GnUnit u;
-  u.n = panel / a.tiles;
+  u.n = a.by_tiles.div(panel);
   u.tile = panel - u.n * a.tiles;
   u.slice = slice;
   u.tc = a.tw * VEC;
   u.c0 = u.tile * u.tc;
   u.nc = min(a.channels - u.c0, u.tc);
-  u.g0 = u.c0 / a.cpg;
-  u.ng = (u.c0 + u.nc - 1) / a.cpg - u.g0 + 1;
+  u.g0 = a.by_cpg.div(u.c0);
+  u.ng = a.by_cpg.div(u.c0 + u.nc - 1) - u.g0 + 1;
   u.r0 = min(a.rows, (int64_t)slice * a.slice_rows);   // a cluster's last CTAs may have none
   u.nr = min(a.rows - u.r0, a.slice_rows);
-  u.TY = kGnThreads / a.tw;
-  u.ty = threadIdx.x / a.tw;
+  u.TY = a.by_tw.div(kGnThreads);
+  u.ty = a.by_tw.div(threadIdx.x);
   u.tx = threadIdx.x - u.ty * a.tw;
   u.on = u.ty < u.TY && u.tx * VEC < u.nc;
-  u.rows = u.on && u.nr > u.ty ? (int)((u.nr - u.ty - 1) / u.TY) + 1 : 0;
+  u.rows = u.on && u.nr > u.ty ? a.by_ty.div((int)(u.nr - u.ty - 1)) + 1 : 0;
   return u;
 }
 // Where a thread's first row of a tensor starts.
@@ -261,46 +269,44 @@ __device__ __forceinline__ float gn_bias(const GnArgs& a, const GnUnit& u, int c
 // ---- column sums ------------------------------------------------------------------
 // Add up two quantities of every column over the row lanes: each column's
 // lanes are dealt to as many threads as there are, then those parts are
-// added; the order depends on the launch's shape only. Returns with the
-// totals of column `col` in sm.ca, sm.cb after the caller's next barrier, via
-// `done(col, a, b)`.
+// added; the order depends on the launch's shape only. done(col, sums) gets
+// the totals; where it writes sm.col[col] no other thread reads that place.
 template <int VEC, typename F>
-__device__ __forceinline__ void gn_columns(const GnUnit& u, GnSmem& sm, const float2* va,
-                                           const float2* vb, F&& done) {
+__device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                           const float2* va, const float2* vb, F&& done) {
   if (u.on) {
-    put_pairs<VEC>(sm.lane.a + u.ty * u.tc + u.tx * VEC, va);
-    put_pairs<VEC>(sm.lane.b + u.ty * u.tc + u.tx * VEC, vb);
+    float2* to = sm.lane + u.ty * u.tc + u.tx * VEC;
+    if (VEC == 1) {
+      to[0] = make_float2(va[0].x, vb[0].x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i)
+        reinterpret_cast<float4*>(to)[i] = make_float4(va[i].x, vb[i].x, va[i].y, vb[i].y);
+    }
   }
   __syncthreads();
-  const int parts = kGnThreads / u.tc;   // threads a column
+  const int parts = a.by_tc.div(kGnThreads);   // threads a column
   if (parts > 1) {
-    const int part = threadIdx.x / u.tc, col = threadIdx.x - part * u.tc;
+    const int part = a.by_tc.div(threadIdx.x), col = threadIdx.x - part * u.tc;
     if (part < parts && col < u.nc) {
-      float sa = 0.f, sb = 0.f;
-      for (int y = part; y < u.TY; y += parts) {
-        sa += sm.lane.a[y * u.tc + col];
-        sb += sm.lane.b[y * u.tc + col];
-      }
-      sm.ca[threadIdx.x] = sa;
-      sm.cb[threadIdx.x] = sb;
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int y = part; y < u.TY; y += parts) s = add2(s, sm.lane[y * u.tc + col]);
+      sm.col[threadIdx.x] = s;
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-      float sa = 0.f, sb = 0.f;
-      for (int p = 0; p < parts; ++p) {
-        sa += sm.ca[p * u.tc + c];
-        sb += sm.cb[p * u.tc + c];
-      }
-      done(c, sa, sb);
+    if (threadIdx.x < u.nc) {
+      float2 s = sm.col[threadIdx.x];
+#pragma unroll 2
+      for (int p = 1; p < parts; ++p) s = add2(s, sm.col[p * u.tc + threadIdx.x]);
+      done(threadIdx.x, s);
     }
   } else {
     for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-      float sa = 0.f, sb = 0.f;
-      for (int y = 0; y < u.TY; ++y) {
-        sa += sm.lane.a[y * u.tc + c];
-        sb += sm.lane.b[y * u.tc + c];
-      }
-      done(c, sa, sb);
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int y = 0; y < u.TY; ++y) s = add2(s, sm.lane[y * u.tc + c]);
+      done(c, s);
     }
   }
 }
@@ -469,10 +475,9 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
   });
   if (u.on && u.ty == 0) put_pairs<VEC>(sm.k + u.tx * VEC, k);
   const float n = (float)u.nr, inv = u.nr > 0 ? 1.f / n : 0.f;
-  gn_columns<VEC>(u, sm, s1, s2, [&](int c, float sa, float sb) {
-    const float m = sa * inv;
-    sm.ca[c] = sm.k[c] + m;    // the part this thread has just read, or nobody's
-    sm.cb[c] = fmaf(-sa, m, sb);
+  gn_columns<VEC>(a, u, sm, s1, s2, [&](int c, float2 s) {
+    const float m = s.x * inv;
+    sm.col[c] = make_float2(sm.k[c] + m, fmaf(-s.x, m, s.y));   // mean, M2
   });
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -481,14 +486,15 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
     const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     // Means are averaged as differences from one of them, which keeps a
     // constant group's mean exact and a large common mean out of the sum.
-    const float base = sm.ca[cs];
+    const float base = sm.col[cs].x;
     float s = 0.f;
-    for (int c = cs + lane; c < ce; c += 32) s += sm.ca[c] - base;
+    for (int c = cs + lane; c < ce; c += 32) s += sm.col[c].x - base;
     const float m = base + group_sum<32>(s) / (float)(ce - cs);
     s = 0.f;
     for (int c = cs + lane; c < ce; c += 32) {
-      const float d = sm.ca[c] - m;
-      s += fmaf(n * d, d, sm.cb[c]);
+      const float2 v = sm.col[c];
+      const float d = v.x - m;
+      s += fmaf(n * d, d, v.y);
     }
     s = group_sum<32>(s);
     if (lane == 0) out[lg] = make_float2(m, s);
@@ -524,12 +530,12 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
     const int g = u.g0 + lg, ch0 = g * a.cpg, ch1 = ch0 + a.cpg;
-    const int t0 = ch0 / u.tc, t1 = (ch1 - 1) / u.tc;
+    const int t0 = a.by_tc.div(ch0), t1 = a.by_tc.div(ch1 - 1);
     float s0 = 0.f, s1 = 0.f, base = 0.f;
     float2 v[N];
     const auto fetch = [&](int t) {
       const float2* p = a.part + ((int64_t)u.n * a.tiles + t) * a.slices * a.max_groups +
-                        (g - t * u.tc / a.cpg);
+                        (g - a.by_cpg.div(t * u.tc));
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         v[j] = make_float2(0.f, 0.f);
@@ -622,7 +628,7 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
                                               Rows<T, VEC, 1>& rows) {
   constexpr int NP = Pack<T, VEC>::NP;
   for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-    const int lg = (u.c0 + c) / a.cpg - u.g0;
+    const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
     sm.par[0][c] = -sm.g0[lg];
     sm.par[1][c] = gn_weight<T>(a, u, c) * sm.g1[lg];
     sm.par[2][c] = gn_bias<T>(a, u, c);
@@ -654,7 +660,7 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
 template <typename T>
 __device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
   for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-    const int64_t g = (int64_t)u.n * a.groups + (u.c0 + c) / a.cpg;
+    const int64_t g = (int64_t)u.n * a.groups + a.by_cpg.div(u.c0 + c);
     sm.par[0][c] = -a.mean[g];
     sm.par[1][c] = a.rstd[g];
     sm.par[2][c] = gn_weight<T>(a, u, c);
@@ -697,12 +703,11 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
   }
   __syncthreads();   // the parameters give way to the sums
   float* cols = a.cols + ((int64_t)u.n * a.slices + u.slice) * 2 * a.channels + u.c0;
-  gn_columns<VEC>(u, sm, sa, sb, [&](int c, float ta, float tb) {
-    cols[c] = tb;
-    cols[a.channels + c] = ta;
+  gn_columns<VEC>(a, u, sm, sa, sb, [&](int c, float2 s) {
+    cols[c] = s.y;
+    cols[a.channels + c] = s.x;
     const float w = gn_weight<T>(a, u, c);
-    sm.ca[c] = w * ta;
-    sm.cb[c] = w * tb;
+    sm.col[c] = make_float2(w * s.x, w * s.y);
   });
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -710,10 +715,7 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
     const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
     const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     float2 s = make_float2(0.f, 0.f);
-    for (int c = cs + lane; c < ce; c += 32) {
-      s.x += sm.ca[c];
-      s.y += sm.cb[c];
-    }
+    for (int c = cs + lane; c < ce; c += 32) s = add2(s, sm.col[c]);
     s = group_sum2<32>(s);
     if (lane == 0) out[lg] = s;
   }
@@ -727,7 +729,7 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
   constexpr int NP = Pack<T, VEC>::NP;
   gn_bwd_params<T>(a, u, sm);
   for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-    const int lg = (u.c0 + c) / a.cpg - u.g0;
+    const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
     sm.par[4][c] = -sm.g0[lg];
     sm.par[5][c] = -sm.g1[lg];
   }
@@ -800,7 +802,7 @@ template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGnThreads, 3)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
-  const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
+  const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
@@ -820,7 +822,7 @@ template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGnThreads, 2)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   __shared__ GnSmem sm;
-  const int p = blockIdx.x / a.slices, s = blockIdx.x - p * a.slices;
+  const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
@@ -843,7 +845,7 @@ template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a) {
   __shared__ GnSmem sm;
   __shared__ float2 part[kGnMaxTileCh];
-  const int p = blockIdx.x / a.slices;
+  const int p = a.by_slices.div(blockIdx.x);
   const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
   Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
   gn_stats_unit<T, VEC>(a, u, sm, rows, part);
@@ -859,7 +861,7 @@ template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a) {
   __shared__ GnSmem sm;
   __shared__ float2 part[kGnMaxTileCh];
-  const int p = blockIdx.x / a.slices;
+  const int p = a.by_slices.div(blockIdx.x);
   const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
   Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
   gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, part);
