@@ -9,9 +9,9 @@
 
 namespace nf {
 
-const void* gn_table_f32(bool bwd, bool cluster, bool vec, int act);
-const void* gn_table_bf16(bool bwd, bool cluster, bool vec, int act);
-const void* gn_table_f16(bool bwd, bool cluster, bool vec, int act);
+const void* gn_table_f32(bool bwd, bool cluster, bool vec, int threads, int act);
+const void* gn_table_bf16(bool bwd, bool cluster, bool vec, int threads, int act);
+const void* gn_table_f16(bool bwd, bool cluster, bool vec, int threads, int act);
 
 namespace {
 
@@ -34,6 +34,8 @@ int gcd(int a, int b) {
 // tile).
 struct GnPlan {
   bool cluster;            // one launch, a cluster a panel
+  int threads;             // of a CTA
+  int clusters;            // of the launch
   int tiles, tw, max_groups, slices;
   int64_t slice_rows;
   int64_t panels, batch;   // all panels, and those of one launch
@@ -80,16 +82,24 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
   const int lv = cpg / gcd(cpg, V);
   const int target = kTileBytes / vb < most ? kTileBytes / vb : most;
   const bool whole = gn_tiles(nv, lv, target, most, p);
-  const int tc = p->tw * V, TY = kGnThreads / p->tw;
+  const int tc = p->tw * V;
   p->panels = samples * p->tiles;
   p->max_groups = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
   if (p->max_groups > groups) p->max_groups = groups;
   const double slab = (double)rows * tc * es * (bwd ? 2 : 1);   // what a panel reads
   p->cluster = whole && slab <= (double)kSlabBytes;
+  p->threads = 256;
+  p->clusters = 0;
   if (p->cluster) {
     int s = 1;
-    while (s < 16 && p->panels * s < (int64_t)sms * kClusterCtas && rows > (int64_t)s * TY * 2) s *= 2;
+    const int per_sm = bwd ? 2 : 3;   // resident CTAs of 256 threads
+    const int64_t TY = 256 / p->tw;
+    while (s < 16 && p->panels * s < (int64_t)sms * per_sm && rows > s * TY * 4) s *= 2;
+    // Too few CTAs for every SM to hold as many as it can: larger ones.
+    if (vec && p->panels * s < (int64_t)sms * per_sm / 2 && rows > s * TY * 2) p->threads = 512;
     p->slices = s;
+    p->clusters = (int)(p->panels * s <= (int64_t)sms * per_sm ? p->panels
+                                                               : (int64_t)sms * per_sm / s);
     p->slice_rows = (rows + s - 1) / s;
     p->batch = p->panels;
     p->part_bytes = 0;
@@ -101,6 +111,7 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
       p->batch = b < step ? step : b;
       if (p->batch > p->panels) p->batch = p->panels;
     }
+    const int64_t TY = 256 / p->tw;
     int64_t slices = ((int64_t)sms * (bwd ? 2 : 3) + p->batch - 1) / p->batch;
     if (slices > kGnMaxSlices) slices = kGnMaxSlices;
     const int64_t least = 4 * TY;       // rows of a slice: four a thread
@@ -171,14 +182,16 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
   a.by_tiles.set(p.tiles);
   a.by_tw.set(p.tw);
   a.by_tc.set(p.tw * (vec ? (int)(16 / elem_size(c.dtype)) : 1));
-  a.by_ty.set(kGnThreads / p.tw);
+  a.by_ty.set(p.threads / p.tw);
   a.by_cpg.set(a.cpg);
   a.rows = c.rows;
   a.inv_m = (float)(1.0 / ((double)c.rows * a.cpg));
-  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, act)
-                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, act)
-                                        : gn_table_f16(bwd, p.cluster, vec, act);
-  const size_t smem = vec ? (size_t)kGnRingBytes * (bwd ? 2 : 1) : 0;
+  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, p.threads, act)
+                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, p.threads, act)
+                                        : gn_table_f16(bwd, p.cluster, vec, p.threads, act);
+  const int tensors = !vec ? 0 : bwd ? 2 : 1;
+  const size_t smem = p.threads == 512 ? gn_smem_bytes<512>(tensors, p.cluster)
+                                       : gn_smem_bytes<256>(tensors, p.cluster);
   const cudaError_t opt = (cudaError_t)allow_dyn_smem(fn, smem);
   if (opt != cudaSuccess) return cuda_fail(opt);
   if (p.cluster) {
@@ -188,8 +201,8 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
       if (e != cudaSuccess) return cuda_fail(e);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.panels * p.slices));
-    cfg.blockDim = dim3(kGnThreads);
+    cfg.gridDim = dim3((unsigned)(p.clusters * p.slices));
+    cfg.blockDim = dim3(p.threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -198,7 +211,8 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void* args[] = {&a};
+    int panels = (int)p.panels;
+    void* args[] = {&a, &panels};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
     return e == cudaSuccess ? LN_OK : cuda_fail(e);
   }
@@ -212,7 +226,7 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
     const int n = s1 - s0 > a1 - a0 ? s1 - s0 : a1 - a0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n * p.slices));
-    cfg.blockDim = dim3(kGnThreads);
+    cfg.blockDim = dim3(p.threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

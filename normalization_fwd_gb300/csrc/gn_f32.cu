@@ -2,7 +2,7 @@
 #include "gn_table.cuh"
 
 namespace nf {
-const void* gn_table_f32(bool bwd, bool cluster, bool vec, int act) {
-  return vec ? gn_table<float, Vec<float>::N>(bwd, cluster, act) : gn_table<float, 1>(bwd, cluster, act);
+const void* gn_table_f32(bool bwd, bool cluster, bool vec, int threads, int act) {
+  return gn_table<float>(bwd, cluster, vec, threads, act);
 }
 }  // namespace nf

@@ -18,13 +18,10 @@
 
 namespace nf {
 
-constexpr int kGnThreads = 256;
-constexpr int kGnWarps = kGnThreads / 32;
 constexpr int kGnMaxTileCh = 512;   // most channels of a column tile
 constexpr int kGnRing = 8;          // rows a thread has in flight, or keeps
 constexpr int kGnStep = 2;          // rows of one step
 constexpr int kGnMaxSlices = 512;   // most slices of a panel
-constexpr int kGnRingBytes = kGnRing * kGnThreads * 16;   // of one tensor
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
@@ -179,12 +176,12 @@ template <typename T> struct Pack<T, 1> {
 
 // Shared memory: the row lanes' sums before they are added up, and in their
 // place, afterwards, the parameters of the tile's columns.
-struct GnSmem {
+template <int TH> struct alignas(16) GnSmem {
   union {
-    float2 lane[kGnThreads * 8];
+    float2 lane[TH * 8];
     float par[6][kGnMaxTileCh];
   };
-  float2 col[kGnMaxTileCh];     // column sums, in parts, then whole
+  float2 col[TH > kGnMaxTileCh ? TH : kGnMaxTileCh];   // column sums, in parts, then whole
   float k[kGnMaxTileCh];        // forward: what the columns are shifted by
   float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
   float g1[kGnMaxTileCh];       // rstd, or c2
@@ -227,7 +224,7 @@ struct GnUnit {
   int rows;              // its rows
   bool on;               // it has a vector
 };
-template <int VEC>
+template <int VEC, int TH>
 __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice) {
   GnUnit u;
   u.n = a.by_tiles.div(panel);
@@ -240,7 +237,7 @@ __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice)
   u.ng = a.by_cpg.div(u.c0 + u.nc - 1) - u.g0 + 1;
   u.r0 = min(a.rows, (int64_t)slice * a.slice_rows);   // a cluster's last CTAs may have none
   u.nr = min(a.rows - u.r0, a.slice_rows);
-  u.TY = a.by_tw.div(kGnThreads);
+  u.TY = a.by_tw.div(TH);
   u.ty = a.by_tw.div(threadIdx.x);
   u.tx = threadIdx.x - u.ty * a.tw;
   u.on = u.ty < u.TY && u.tx * VEC < u.nc;
@@ -271,8 +268,8 @@ __device__ __forceinline__ float gn_bias(const GnArgs& a, const GnUnit& u, int c
 // lanes are dealt to as many threads as there are, then those parts are
 // added; the order depends on the launch's shape only. done(col, sums) gets
 // the totals; where it writes sm.col[col] no other thread reads that place.
-template <int VEC, typename F>
-__device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+template <int VEC, int TH, typename F>
+__device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
                                            const float2* va, const float2* vb, F&& done) {
   if (u.on) {
     float2* to = sm.lane + u.ty * u.tc + u.tx * VEC;
@@ -285,7 +282,7 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
     }
   }
   __syncthreads();
-  const int parts = a.by_tc.div(kGnThreads);   // threads a column
+  const int parts = a.by_tc.div(TH);   // threads a column
   if (parts > 1) {
     const int part = a.by_tc.div(threadIdx.x), col = threadIdx.x - part * u.tc;
     if (part < parts && col < u.nc) {
@@ -302,7 +299,7 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
       done(threadIdx.x, s);
     }
   } else {
-    for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+    for (int c = threadIdx.x; c < u.nc; c += TH) {
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int y = 0; y < u.TY; ++y) s = add2(s, sm.lane[y * u.tc + c]);
@@ -326,29 +323,35 @@ template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int VEC, int TENSORS> struct Rows {
+template <typename T, int VEC, int TH, int TENSORS> struct Rows {
   static constexpr int NG = kGnRing / kGnStep;   // steps in flight
   const T* p[TENSORS];      // the thread's first row
   int64_t step[TENSORS];    // from one of its rows to the next
   const T* next[TENSORS];   // the next one to fetch
   int rows, steps;
+  unsigned place;           // in the ring, of step 0
   unsigned slots;           // this thread's first slot
   Pack<T, VEC> v[TENSORS][kGnStep];
 
-  __device__ __forceinline__ void fetch(int g, int place) {   // step g, into place's slots
-    const unsigned at = slots + (unsigned)place % NG * (kGnStep * kGnThreads * 16);
+  __device__ __forceinline__ unsigned at(unsigned place) const {
+    return slots + place % NG * (kGnStep * TH * 16);
+  }
+  // Step g of n rows, into a place of the ring.
+  __device__ __forceinline__ void fetch(int g, int n, unsigned place) {
+    const unsigned to = at(place);
 #pragma unroll
     for (int j = 0; j < kGnStep; ++j)
-      if (g * kGnStep + j < rows) {
+      if (g * kGnStep + j < n) {
 #pragma unroll
         for (int t = 0; t < TENSORS; ++t) {
-          copy_async16(at + t * kGnRingBytes + j * (kGnThreads * 16), next[t]);
+          copy_async16(to + t * (kGnRing * TH * 16) + j * (TH * 16), next[t]);
           next[t] += step[t];
         }
       }
+    copy_commit();
   }
-  __device__ __forceinline__ void take(int g) {
-    const unsigned at = slots + (unsigned)g % NG * (kGnStep * kGnThreads * 16);
+  __device__ __forceinline__ void take(unsigned place) {
+    const unsigned from = at(place);
 #pragma unroll
     for (int t = 0; t < TENSORS; ++t)
 #pragma unroll
@@ -356,22 +359,26 @@ template <typename T, int VEC, int TENSORS> struct Rows {
         uint4& u = v[t][j].v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "r"(at + t * kGnRingBytes + j * (kGnThreads * 16)));
+                     : "r"(from + t * (kGnRing * TH * 16) + j * (TH * 16)));
       }
+  }
+  __device__ __forceinline__ void rewind() {
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t) next[t] = p[t];
+  }
+  __device__ __forceinline__ void take_rows(int n) {
+    rows = n;
+    steps = (n + kGnStep - 1) / kGnStep;
   }
   // Start the first pass (or the only one) over n rows.
   __device__ __forceinline__ void start(int n, void* ring) {
-    rows = n;
-    steps = (n + kGnStep - 1) / kGnStep;
+    take_rows(n);
+    place = 0;
     slots = (unsigned)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
     if constexpr (VEC > 1) {
+      rewind();
 #pragma unroll
-      for (int t = 0; t < TENSORS; ++t) next[t] = p[t];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        fetch(g, g);
-        copy_commit();
-      }
+      for (int g = 0; g < NG; ++g) fetch(g, rows, g);
     }
   }
   // body(j, to) for every row, j its place in v, `to` its place in an output
@@ -380,44 +387,60 @@ template <typename T, int VEC, int TENSORS> struct Rows {
     if constexpr (VEC > 1) {
       for (int g = 0; g < steps; ++g) {
         copy_wait<NG - 1>();
-        take(g);
+        take(place + g);
 #pragma unroll
         for (int j = 0; j < kGnStep; ++j) {
           if (g * kGnStep + j < rows) body(j, o);
           o += ostep;
         }
-        fetch(g + NG, g);
-        copy_commit();
+        fetch(g + NG, rows, place + g);
       }
     } else {
       direct(o, ostep, body);
     }
   }
-  // The second pass over the same rows, those in the slots first.
-  template <typename F> __device__ __forceinline__ void again(T* o, int64_t ostep, F&& body) {
+  // The second pass over the same rows, those in the slots first; places that
+  // it has no more rows for take the first ones of another unit's n rows at q.
+  template <typename F>
+  __device__ __forceinline__ void again(T* o, int64_t ostep, F&& body, const T* const* q, int n) {
     if constexpr (VEC > 1) {
       const int far = steps > NG ? steps - NG : 0;   // steps that have left the slots
-#pragma unroll
-      for (int t = 0; t < TENSORS; ++t) next[t] = p[t];
+      rewind();
       T* const first = o;
       o += far * kGnStep * ostep;
+      place += far;
       // Steps far, ..., steps - 1 out of their slots, which take 0, 1, ... after them.
-      for (int q = 0; q < steps; ++q) {
-        const int g = far + q < steps ? far + q : far + q - steps;
+      for (int k = 0; k < steps; ++k) {
+        const int g = far + k < steps ? far + k : far + k - steps;
         if (g == 0) o = first;
         copy_wait<NG - 1>();
-        take(far + q);
+        take(place + k);
 #pragma unroll
         for (int j = 0; j < kGnStep; ++j) {
           if (g * kGnStep + j < rows) body(j, o);
           o += ostep;
         }
-        if (q < far) fetch(q, far + q);
-        copy_commit();
+        if (k == far) {
+#pragma unroll
+          for (int t = 0; t < TENSORS; ++t) next[t] = q[t];
+        }
+        if (k < far) fetch(k, rows, place + k);
+        else fetch(k - far, n, place + k);
       }
+      if (steps == 0) {
+#pragma unroll
+        for (int t = 0; t < TENSORS; ++t) next[t] = q[t];
+      }
+      place += far;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        if (g >= steps) fetch(g, n, place + g);
     } else {
       direct(o, ostep, body);
     }
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t) p[t] = q[t];
+    take_rows(n);
   }
   template <typename F> __device__ __forceinline__ void direct(T* o, int64_t ostep, F&& body) {
     constexpr int UN = 8 / TENSORS;
@@ -452,9 +475,9 @@ template <typename T, int VEC, int TENSORS> struct Rows {
 // at most about n * 2^-24 of the group's sum of squares, whatever the mean.
 // Columns, and later slices, are merged by the parallel-variance identity
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
-template <typename T, int VEC>
-__device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              Rows<T, VEC, 1>& rows, float2* out) {
+template <typename T, int VEC, int TH>
+__device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
+                                              Rows<T, VEC, TH, 1>& rows, float2* out) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 k[NP], s1[NP], s2[NP], v[NP];
 #pragma unroll
@@ -475,13 +498,13 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
   });
   if (u.on && u.ty == 0) put_pairs<VEC>(sm.k + u.tx * VEC, k);
   const float n = (float)u.nr, inv = u.nr > 0 ? 1.f / n : 0.f;
-  gn_columns<VEC>(a, u, sm, s1, s2, [&](int c, float2 s) {
+  gn_columns<VEC, TH>(a, u, sm, s1, s2, [&](int c, float2 s) {
     const float m = s.x * inv;
     sm.col[c] = make_float2(sm.k[c] + m, fmaf(-s.x, m, s.y));   // mean, M2
   });
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
     const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
     const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     // Means are averaged as differences from one of them, which keeps a
@@ -504,8 +527,8 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
 
 // What the merged sums become: mean and rstd (forward, stored by one CTA of
 // the group's), or c1 and c2.
-template <bool BWD>
-__device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSmem& sm, int lg,
+template <bool BWD, int TH>
+__device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm, int lg,
                                           float s0, float s1, bool store) {
   if (!BWD) {
     if (s1 < 0.f) s1 = 0.f;   // rounding alone; a NaN stays one
@@ -524,11 +547,11 @@ __device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSm
 // (forward) or into sm.g0 = c1, sm.g1 = c2 (backward): one warp a group, the
 // slices dealt to its lanes, the same order in every CTA. A lane has all its
 // partials of a tile on their way at once and keeps them for the second sum.
-template <bool BWD>
-__device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
+template <bool BWD, int TH>
+__device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm) {
   constexpr int N = kGnMaxSlices / 32;
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
     const int g = u.g0 + lg, ch0 = g * a.cpg, ch1 = ch0 + a.cpg;
     const int t0 = a.by_tc.div(ch0), t1 = a.by_tc.div(ch1 - 1);
     float s0 = 0.f, s1 = 0.f, base = 0.f;
@@ -570,7 +593,7 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
       }
     }
     s1 = group_sum<32>(s1) * a.inv_m;
-    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0 && u.tile == t0);
+    if (lane == 0) gn_merged<BWD, TH>(a, u, sm, lg, s0, s1, u.slice == 0 && u.tile == t0);
   }
   __syncthreads();
 }
@@ -597,11 +620,11 @@ __device__ __forceinline__ float2 cluster_read(const float2* p, int rank) {
 }
 
 // The merge of gn_combine over the cluster's CTAs: a lane a CTA.
-template <bool BWD>
-__device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+template <bool BWD, int TH>
+__device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
                                                    const float2* part) {
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
     float2 v = make_float2(0.f, 0.f);
     if (lane < a.slices) v = cluster_read(part + lg, lane);
     float s0, s1;
@@ -617,49 +640,46 @@ __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit
       const float d = v.x - s0;
       s1 = group_sum<32>(some ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
     }
-    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0);
+    if (lane == 0) gn_merged<BWD, TH>(a, u, sm, lg, s0, s1, u.slice == 0);
   }
   __syncthreads();
 }
 
 // ---- forward: normalize one unit -------------------------------------------------
-template <typename T, int VEC, int ACT, bool AGAIN>
-__device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              Rows<T, VEC, 1>& rows) {
+template <typename T, int VEC, int TH, int ACT, typename W>
+__device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
+                                              Rows<T, VEC, TH, 1>& rows, W&& walk) {
   constexpr int NP = Pack<T, VEC>::NP;
-  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+  for (int c = threadIdx.x; c < u.nc; c += TH) {
     const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
     sm.par[0][c] = -sm.g0[lg];
     sm.par[1][c] = gn_weight<T>(a, u, c) * sm.g1[lg];
     sm.par[2][c] = gn_bias<T>(a, u, c);
   }
   __syncthreads();
-  if (u.rows > 0) {
-    float2 m[NP], w[NP], b[NP], v[NP];
-    get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
-    get_pairs<VEC>(sm.par[1] + u.tx * VEC, w);
-    get_pairs<VEC>(sm.par[2] + u.tx * VEC, b);
-    T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
-    const int64_t ostep = (int64_t)u.TY * a.out_row;
-    auto body = [&](int j, T* to) {
-      rows.v[0][j].get(v);
+  float2 m[NP], w[NP], b[NP], v[NP];
+  get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
+  get_pairs<VEC>(sm.par[1] + u.tx * VEC, w);
+  get_pairs<VEC>(sm.par[2] + u.tx * VEC, b);
+  T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
+  const int64_t ostep = (int64_t)u.TY * a.out_row;
+  auto body = [&](int j, T* to) {
+    rows.v[0][j].get(v);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) v[i] = fma2(add2(v[i], m[i]), w[i], b[i]);
-      activate<ACT, NP>(v);
-      Pack<T, VEC> y;
-      y.set(v);
-      y.store(to);
-    };
-    if (AGAIN) rows.again(o, ostep, body);
-    else rows.pass(o, ostep, body);
-  }
+    for (int i = 0; i < NP; ++i) v[i] = fma2(add2(v[i], m[i]), w[i], b[i]);
+    activate<ACT, NP>(v);
+    Pack<T, VEC> y;
+    y.set(v);
+    y.store(to);
+  };
+  walk(o, ostep, body);
 }
 
 // ---- backward ------------------------------------------------------------------------
 // mean, rstd, w and beta of the unit's columns.
-template <typename T>
-__device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
-  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+template <typename T, int TH>
+__device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm) {
+  for (int c = threadIdx.x; c < u.nc; c += TH) {
     const int64_t g = (int64_t)u.n * a.groups + a.by_cpg.div(u.c0 + c);
     sm.par[0][c] = -a.mean[g];
     sm.par[1][c] = a.rstd[g];
@@ -669,14 +689,14 @@ __device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, 
 }
 
 // Sums of one unit.
-template <typename T, int VEC, int ACT>
-__device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  Rows<T, VEC, 2>& rows, float2* out) {
+template <typename T, int VEC, int TH, int ACT>
+__device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
+                                                  Rows<T, VEC, TH, 2>& rows, float2* out) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 sa[NP], sb[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) sa[i] = sb[i] = splat2(0.f);
-  gn_bwd_params<T>(a, u, sm);
+  gn_bwd_params<T, TH>(a, u, sm);
   __syncthreads();
   if (u.rows > 0) {
     float2 m[NP], rs[NP], w[NP], b[NP], v[NP], d[NP];
@@ -703,7 +723,7 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
   }
   __syncthreads();   // the parameters give way to the sums
   float* cols = a.cols + ((int64_t)u.n * a.slices + u.slice) * 2 * a.channels + u.c0;
-  gn_columns<VEC>(a, u, sm, sa, sb, [&](int c, float2 s) {
+  gn_columns<VEC, TH>(a, u, sm, sa, sb, [&](int c, float2 s) {
     cols[c] = s.y;
     cols[a.channels + c] = s.x;
     const float w = gn_weight<T>(a, u, c);
@@ -711,7 +731,7 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
   });
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnWarps) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
     const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
     const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     float2 s = make_float2(0.f, 0.f);
@@ -723,153 +743,205 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
 }
 
 // dx of one unit.
-template <typename T, int VEC, int ACT, bool AGAIN>
-__device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  Rows<T, VEC, 2>& rows) {
+template <typename T, int VEC, int TH, int ACT, typename W>
+__device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
+                                                  Rows<T, VEC, TH, 2>& rows, W&& walk) {
   constexpr int NP = Pack<T, VEC>::NP;
-  gn_bwd_params<T>(a, u, sm);
-  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
+  gn_bwd_params<T, TH>(a, u, sm);
+  for (int c = threadIdx.x; c < u.nc; c += TH) {
     const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
     sm.par[4][c] = -sm.g0[lg];
     sm.par[5][c] = -sm.g1[lg];
   }
   __syncthreads();
-  if (u.rows > 0) {
-    float2 m[NP], rs[NP], w[NP], b[NP], c1[NP], c2[NP], v[NP], d[NP];
-    get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
-    get_pairs<VEC>(sm.par[1] + u.tx * VEC, rs);
-    get_pairs<VEC>(sm.par[2] + u.tx * VEC, w);
-    get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
-    get_pairs<VEC>(sm.par[4] + u.tx * VEC, c1);
-    get_pairs<VEC>(sm.par[5] + u.tx * VEC, c2);
-    T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
-    const int64_t ostep = (int64_t)u.TY * a.out_row;
-    // The product w dz is rounded before c1 is taken off (no fma): in a group
-    // of one value c1 is that very product and dx is exactly 0.
-    auto body = [&](int j, T* to) {
-      rows.v[0][j].get(v);
-      rows.v[1][j].get(d);
-      float2 z[NP];
+  float2 m[NP], rs[NP], w[NP], b[NP], c1[NP], c2[NP], v[NP], d[NP];
+  get_pairs<VEC>(sm.par[0] + u.tx * VEC, m);
+  get_pairs<VEC>(sm.par[1] + u.tx * VEC, rs);
+  get_pairs<VEC>(sm.par[2] + u.tx * VEC, w);
+  get_pairs<VEC>(sm.par[3] + u.tx * VEC, b);
+  get_pairs<VEC>(sm.par[4] + u.tx * VEC, c1);
+  get_pairs<VEC>(sm.par[5] + u.tx * VEC, c2);
+  T* o = static_cast<T*>(a.out) + gn_at<T, VEC>(u, a.out_sample, a.out_row);
+  const int64_t ostep = (int64_t)u.TY * a.out_row;
+  // The product w dz is rounded before c1 is taken off (no fma): in a group
+  // of one value c1 is that very product and dx is exactly 0.
+  auto body = [&](int j, T* to) {
+    rows.v[0][j].get(v);
+    rows.v[1][j].get(d);
+    float2 z[NP];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        v[i] = mul2(add2(v[i], m[i]), rs[i]);
-        z[i] = fma2(v[i], w[i], b[i]);
-      }
-      through<ACT, NP>(d, z);
+    for (int i = 0; i < NP; ++i) {
+      v[i] = mul2(add2(v[i], m[i]), rs[i]);
+      z[i] = fma2(v[i], w[i], b[i]);
+    }
+    through<ACT, NP>(d, z);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 g = make_float2(__fmul_rn(w[i].x, d[i].x), __fmul_rn(w[i].y, d[i].y));
-        v[i] = mul2(rs[i], fma2(v[i], c2[i], add2(g, c1[i])));
-      }
-      Pack<T, VEC> y;
-      y.set(v);
-      y.store(to);
-    };
-    if (AGAIN) rows.again(o, ostep, body);
-    else rows.pass(o, ostep, body);
-  }
+    for (int i = 0; i < NP; ++i) {
+      const float2 g = make_float2(__fmul_rn(w[i].x, d[i].x), __fmul_rn(w[i].y, d[i].y));
+      v[i] = mul2(rs[i], fma2(v[i], c2[i], add2(g, c1[i])));
+    }
+    Pack<T, VEC> y;
+    y.set(v);
+    y.store(to);
+  };
+  walk(o, ostep, body);
 }
 
 // ---- kernels ----------------------------------------------------------------------
 __device__ __forceinline__ float2* gn_part(const GnArgs& a, const GnUnit& u) {
   return a.part + (((int64_t)u.n * a.tiles + u.tile) * a.slices + u.slice) * a.max_groups;
 }
-extern __shared__ __align__(16) unsigned char gn_ring[];
-
-// A unit's rows, on their way.
-template <typename T, int VEC>
-__device__ __forceinline__ Rows<T, VEC, 1> gn_fwd_rows(const GnArgs& a, const GnUnit& u) {
-  Rows<T, VEC, 1> r;
-  r.p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
-  r.step[0] = (int64_t)u.TY * a.x_row;
-  r.start(u.rows, gn_ring);
-  return r;
+// Dynamic shared memory: GnSmem, a cluster's partials, then the slots.
+extern __shared__ __align__(16) unsigned char gn_dynamic[];
+struct GnParts {
+  float2 part[2][kGnMaxTileCh];
+};
+template <int TH> __host__ __device__ constexpr size_t gn_smem_bytes(int tensors, bool cluster) {
+  return sizeof(GnSmem<TH>) + (cluster ? sizeof(GnParts) : 0) +
+         (size_t)tensors * kGnRing * TH * 16;
 }
-template <typename T, int VEC>
-__device__ __forceinline__ Rows<T, VEC, 2> gn_bwd_rows(const GnArgs& a, const GnUnit& u) {
-  Rows<T, VEC, 2> r;
-  r.p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
-  r.step[0] = (int64_t)u.TY * a.x_row;
-  r.p[1] = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
-  r.step[1] = (int64_t)u.TY * a.dy_row;
-  r.start(u.rows, gn_ring);
-  return r;
+
+// Where a unit's first rows are.
+template <typename T, int VEC, int TH>
+__device__ __forceinline__ void gn_fwd_rows(const GnArgs& a, const GnUnit& u, const T** p) {
+  p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+}
+template <typename T, int VEC, int TH>
+__device__ __forceinline__ void gn_bwd_rows(const GnArgs& a, const GnUnit& u, const T** p) {
+  p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
+  p[1] = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
 }
 
 // One launch takes the statistics of the panels [stat0, stat1) and applies
 // those of [app0, app1), which an earlier launch gathered.
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads, 3)
+template <typename T, int VEC, int TH, int ACT>
+__global__ void __launch_bounds__(TH, 768 / TH)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
-  __shared__ GnSmem sm;
+  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
+  void* const ring = gn_dynamic + sizeof(GnSmem<TH>);
   const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Rows<T, VEC, TH, 1> rows;
   if (stat0 + p < stat1) {
-    const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
-    Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
-    gn_stats_unit<T, VEC>(a, u, sm, rows, gn_part(a, u));
+    const GnUnit u = gn_unit<VEC, TH>(a, stat0 + p, s);
+    gn_fwd_rows<T, VEC, TH>(a, u, rows.p);
+    rows.step[0] = (int64_t)u.TY * a.x_row;
+    rows.start(u.rows, ring);
+    gn_stats_unit<T, VEC, TH>(a, u, sm, rows, gn_part(a, u));
   }
   if (app0 + p < app1) {
-    const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
-    Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
+    const GnUnit u = gn_unit<VEC, TH>(a, app0 + p, s);
+    gn_fwd_rows<T, VEC, TH>(a, u, rows.p);
+    rows.step[0] = (int64_t)u.TY * a.x_row;
+    rows.start(u.rows, ring);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_combine<false>(a, u, sm);
-    gn_apply_unit<T, VEC, ACT, false>(a, u, sm, rows);
+    gn_combine<false, TH>(a, u, sm);
+    gn_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+      rows.pass(o, ostep, body);
+    });
   }
 }
 
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads, 2)
+template <typename T, int VEC, int TH, int ACT>
+__global__ void __launch_bounds__(TH, 512 / TH)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
-  __shared__ GnSmem sm;
+  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
+  void* const ring = gn_dynamic + sizeof(GnSmem<TH>);
   const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Rows<T, VEC, TH, 2> rows;
   if (stat0 + p < stat1) {
-    const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
-    Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
-    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, gn_part(a, u));
+    const GnUnit u = gn_unit<VEC, TH>(a, stat0 + p, s);
+    gn_bwd_rows<T, VEC, TH>(a, u, rows.p);
+    rows.step[0] = (int64_t)u.TY * a.x_row;
+    rows.step[1] = (int64_t)u.TY * a.dy_row;
+    rows.start(u.rows, ring);
+    gn_bwd_stats_unit<T, VEC, TH, ACT>(a, u, sm, rows, gn_part(a, u));
   }
   if (app0 + p < app1) {
-    const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
-    Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
+    const GnUnit u = gn_unit<VEC, TH>(a, app0 + p, s);
+    gn_bwd_rows<T, VEC, TH>(a, u, rows.p);
+    rows.step[0] = (int64_t)u.TY * a.x_row;
+    rows.step[1] = (int64_t)u.TY * a.dy_row;
+    rows.start(u.rows, ring);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_combine<true>(a, u, sm);
-    gn_bwd_apply_unit<T, VEC, ACT, false>(a, u, sm, rows);
+    gn_combine<true, TH>(a, u, sm);
+    gn_bwd_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+      rows.pass(o, ostep, body);
+    });
   }
 }
 
-// A panel a cluster, in one launch: the statistics, a barrier of the
-// cluster, and the rows again: those still in the slots, then the others out
-// of the L2 cache.
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a) {
-  __shared__ GnSmem sm;
-  __shared__ float2 part[kGnMaxTileCh];
-  const int p = a.by_slices.div(blockIdx.x);
-  const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
-  Rows<T, VEC, 1> rows = gn_fwd_rows<T, VEC>(a, u);
-  gn_stats_unit<T, VEC>(a, u, sm, rows, part);
-  cluster_arrive();
+// A panel a cluster: the statistics, a barrier of the cluster, and the rows
+// again: those still in the slots, then the others out of the L2 cache. A
+// cluster takes one panel after another and has the first rows of the next
+// one on their way while it finishes this one. The partials have two places
+// in turn: one is written again only after the barrier of the panel between,
+// which every CTA reaches after it has read them.
+template <typename T, int VEC, int TH, int ACT>
+__global__ void __launch_bounds__(TH, 768 / TH) gn_fwd_cluster_kernel(GnArgs a, int panels) {
+  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
+  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem<TH>))->part;
+  void* const ring = gn_dynamic + sizeof(GnSmem<TH>) + sizeof(GnParts);
+  int p = a.by_slices.div(blockIdx.x), turn = 0;
+  const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
+  GnUnit u = gn_unit<VEC, TH>(a, p, rank);
+  Rows<T, VEC, TH, 1> rows;
+  gn_fwd_rows<T, VEC, TH>(a, u, rows.p);
+  rows.step[0] = (int64_t)u.TY * a.x_row;
+  rows.start(u.rows, ring);
+  while (true) {
+    gn_stats_unit<T, VEC, TH>(a, u, sm, rows, part[turn]);
+    cluster_arrive();
+    cluster_wait();
+    gn_combine_cluster<false, TH>(a, u, sm, part[turn]);
+    p += clusters;
+    const GnUnit v = gn_unit<VEC, TH>(a, p < panels ? p : 0, rank);
+    const T* q[1];
+    gn_fwd_rows<T, VEC, TH>(a, v, q);
+    gn_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+      rows.again(o, ostep, body, q, p < panels ? v.rows : 0);
+    });
+    if (p >= panels) break;
+    u = v;
+    turn ^= 1;
+    __syncthreads();   // the parameters give way to the next sums
+  }
+  cluster_arrive();    // no CTA leaves while another reads its partials
   cluster_wait();
-  gn_combine_cluster<false>(a, u, sm, part);
-  cluster_arrive();
-  gn_apply_unit<T, VEC, ACT, true>(a, u, sm, rows);
-  cluster_wait();   // no CTA leaves while another reads its partials
 }
 
-template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a) {
-  __shared__ GnSmem sm;
-  __shared__ float2 part[kGnMaxTileCh];
-  const int p = a.by_slices.div(blockIdx.x);
-  const GnUnit u = gn_unit<VEC>(a, p, blockIdx.x - p * a.slices);
-  Rows<T, VEC, 2> rows = gn_bwd_rows<T, VEC>(a, u);
-  gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, part);
+template <typename T, int VEC, int TH, int ACT>
+__global__ void __launch_bounds__(TH, 512 / TH) gn_bwd_cluster_kernel(GnArgs a, int panels) {
+  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
+  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem<TH>))->part;
+  void* const ring = gn_dynamic + sizeof(GnSmem<TH>) + sizeof(GnParts);
+  int p = a.by_slices.div(blockIdx.x), turn = 0;
+  const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
+  GnUnit u = gn_unit<VEC, TH>(a, p, rank);
+  Rows<T, VEC, TH, 2> rows;
+  gn_bwd_rows<T, VEC, TH>(a, u, rows.p);
+  rows.step[0] = (int64_t)u.TY * a.x_row;
+  rows.step[1] = (int64_t)u.TY * a.dy_row;
+  rows.start(u.rows, ring);
+  while (true) {
+    gn_bwd_stats_unit<T, VEC, TH, ACT>(a, u, sm, rows, part[turn]);
+    cluster_arrive();
+    cluster_wait();
+    gn_combine_cluster<true, TH>(a, u, sm, part[turn]);
+    p += clusters;
+    const GnUnit v = gn_unit<VEC, TH>(a, p < panels ? p : 0, rank);
+    const T* q[2];
+    gn_bwd_rows<T, VEC, TH>(a, v, q);
+    gn_bwd_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+      rows.again(o, ostep, body, q, p < panels ? v.rows : 0);
+    });
+    if (p >= panels) break;
+    u = v;
+    turn ^= 1;
+    __syncthreads();
+  }
   cluster_arrive();
-  cluster_wait();
-  gn_combine_cluster<true>(a, u, sm, part);
-  cluster_arrive();
-  gn_bwd_apply_unit<T, VEC, ACT, true>(a, u, sm, rows);
   cluster_wait();
 }
 
