@@ -25,7 +25,8 @@ struct Shape {
   ln_dtype dtype;
 };
 
-constexpr int kBwdBlocksPerSm = 4;   // backward CTAs an SM, each with a row of partials
+constexpr int kBwdBlocksPerSm = 2;   // backward CTAs an SM, each with a row of partials
+constexpr int kRopeItems = 8;        // heads of a tile for each group of threads
 
 Strided strided(const void* p, const int64_t* st, int64_t heads, const Shape& c) {
   const int64_t es = (int64_t)elem_size(c.dtype);
@@ -123,24 +124,40 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
   if (p->fn == nullptr) return LN_ERR_UNSUPPORTED;
   p->lanes = lanes;
   const int per_cta = kRopeThreads / lanes;
-  // A unit's heads share its cos and sin; fewer heads a unit where there
-  // would not be a unit for every group of threads.
+  a->lanes = lanes;
+  a->row = (dim / 2 + 3) / 4 * 4;
+  a->wide = 1;
+  while (a->wide < rot / 2) a->wide *= 2;
   const int64_t toks = c.batch * c.tokens;
   const int total = a->side[0].heads + a->side[1].heads;
-  int hpu = 8;
-  const int64_t want = (int64_t)sms * 4 * per_cta;
-  while (hpu > 1 && toks * ((total + hpu - 1) / hpu) < want) hpu /= 2;
-  a->heads_per_unit = hpu;
-  a->lanes = lanes;
+  int most_tile = kRopeMaxTable / a->row;
+  if (most_tile > kRopeMaxTile) most_tile = kRopeMaxTile;
   for (int s = 0; s < 2; ++s) {
-    a->side[s].chunks = (a->side[s].heads + hpu - 1) / hpu;
-    const int64_t need = (toks * a->side[s].chunks + per_cta - 1) / per_cta;
+    RopeSide& d = a->side[s];
+    if (d.heads == 0) {
+      a->blocks[s] = 0;
+      d.tile = 1;
+      d.tiles = 0;
+      continue;
+    }
+    // Tokens of a tile: kRopeItems heads for every group, fewer where the
+    // device would not have a CTA for each of its places.
+    int64_t tile = ((int64_t)kRopeItems * per_cta + d.heads - 1) / d.heads;
+    const int64_t places = (int64_t)sms * 3 * d.heads / total;
+    const int64_t even = toks / (places > 0 ? places : 1);
+    if (tile > even) tile = even;
+    const int64_t fill = (per_cta + d.heads - 1) / d.heads;   // one head a group at least
+    if (tile < fill && toks / fill >= sms / 4) tile = fill;
+    if (tile > most_tile) tile = most_tile;
+    if (tile < 1) tile = 1;
+    d.tile = (int)tile;
+    d.tiles = (toks + tile - 1) / tile;
     int64_t most = 1 << 30;
     if (bwd) {
-      most = (int64_t)sms * kBwdBlocksPerSm * a->side[s].heads / total;
+      most = (int64_t)sms * kBwdBlocksPerSm * d.heads / total;
       if (most < 1) most = 1;
     }
-    a->blocks[s] = (int)(need < most ? need : most);
+    a->blocks[s] = (int)(d.tiles < most ? d.tiles : most);
   }
   p->grid = a->blocks[0] + a->blocks[1];
   p->smem = bwd && a->ws != nullptr ? (size_t)per_cta * dim * sizeof(float) : 0;

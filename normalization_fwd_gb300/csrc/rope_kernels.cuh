@@ -22,6 +22,9 @@ namespace nf {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 512;
+constexpr int kRopeMaxTile = 32;      // tokens of a tile
+constexpr int kRopeMaxTable = 2048;   // floats of a tile's cosines, and of its sines
+constexpr int kRopeAhead = 2;         // heads that a thread has on their way
 constexpr int kRopeMaxAxes = 4;
 
 // One of the tensors a call takes (queries or keys).
@@ -31,7 +34,8 @@ struct RopeSide {
   void* out;             // y, or dx
   const void* gamma;     // nullable: no norm
   int heads;             // 0: absent
-  int chunks;            // ceil(heads / heads_per_unit)
+  int tile;              // tokens of a tile
+  int64_t tiles;         // ceil(all tokens / tile)
   int64_t in_s[3], x_s[3], out_s[3];   // strides of batch, token, head (elements)
 };
 
@@ -47,48 +51,51 @@ struct RopeArgs {
   int pos64, axes;
   int dim, rot;
   int lanes;             // threads of one head, a power of two <= 32
-  int heads_per_unit;
+  int row;               // floats of a token's row in the table, a multiple of 4
+  int wide;              // threads that work out a token's angles, a power of two
   float scale, eps, inv_dim;
   int zero_centered;
 };
 
-// VEC elements from memory; ALIGNED: one access of VEC * sizeof(T) bytes.
-template <typename T, int VEC, bool ALIGNED>
-__device__ __forceinline__ void rope_load(const T* p, float* f) {
-  constexpr int B = VEC * (int)sizeof(T);
+// VEC elements as they are in memory; ALIGNED: one access of all of them.
+template <typename T, int VEC, bool ALIGNED> struct RopeRaw {
+  static constexpr int B = VEC * (int)sizeof(T);
   union {
     uint4 q;
     uint2 d;
     unsigned w;
     T t[VEC];
   } u;
-  if (ALIGNED && B == 16) u.q = *reinterpret_cast<const uint4*>(p);
-  else if (ALIGNED && B == 8) u.d = *reinterpret_cast<const uint2*>(p);
-  else if (ALIGNED && B == 4) u.w = *reinterpret_cast<const unsigned*>(p);
-  else {
+  __device__ __forceinline__ RopeRaw() {}
+  __device__ __forceinline__ void load(const T* p) {
+    if (ALIGNED && B == 16) u.q = *reinterpret_cast<const uint4*>(p);
+    else if (ALIGNED && B == 8) u.d = *reinterpret_cast<const uint2*>(p);
+    else if (ALIGNED && B == 4) u.w = *reinterpret_cast<const unsigned*>(p);
+    else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) u.t[i] = p[i];
+      for (int i = 0; i < VEC; ++i) u.t[i] = p[i];
+    }
   }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) f[i] = to_f(u.t[i]);
-}
+    for (int i = 0; i < VEC; ++i) u.t[i] = from_f<T>(0.f);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = to_f(u.t[i]);
+  }
+};
 template <typename T, int VEC, bool ALIGNED>
 __device__ __forceinline__ void rope_store(T* p, const float* f) {
-  constexpr int B = VEC * (int)sizeof(T);
-  union {
-    uint4 q;
-    uint2 d;
-    unsigned w;
-    T t[VEC];
-  } u;
+  RopeRaw<T, VEC, ALIGNED> r;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) u.t[i] = from_f<T>(f[i]);
-  if (ALIGNED && B == 16) *reinterpret_cast<uint4*>(p) = u.q;
-  else if (ALIGNED && B == 8) *reinterpret_cast<uint2*>(p) = u.d;
-  else if (ALIGNED && B == 4) *reinterpret_cast<unsigned*>(p) = u.w;
+  for (int i = 0; i < VEC; ++i) r.u.t[i] = from_f<T>(f[i]);
+  if (ALIGNED && r.B == 16) *reinterpret_cast<uint4*>(p) = r.u.q;
+  else if (ALIGNED && r.B == 8) *reinterpret_cast<uint2*>(p) = r.u.d;
+  else if (ALIGNED && r.B == 4) *reinterpret_cast<unsigned*>(p) = r.u.w;
   else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = u.t[i];
+    for (int i = 0; i < VEC; ++i) p[i] = r.u.t[i];
   }
 }
 
@@ -189,95 +196,168 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   return v;
 }
 
-// A group of `lanes` threads takes a unit: one token and up to
-// heads_per_unit of its heads, whose cos and sin it works out once. A CTA
-// works on the queries or on the keys.
+// N consecutive floats of the table.
+template <int N> __device__ __forceinline__ void rope_table_get(const float* t, float* f) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(t)[i];
+      f[4 * i] = v.x;
+      f[4 * i + 1] = v.y;
+      f[4 * i + 2] = v.z;
+      f[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = t[i];
+  }
+}
+
+// A CTA takes the queries or the keys of a tile of tokens. It works out the
+// cosines and sines of the tile's tokens once, into shared memory, and goes
+// through the tokens' heads with a group of `lanes` threads a head, the next
+// kRopeAhead heads of a group always on their way. Forward: a tile a CTA;
+// backward: a CTA takes tile after tile and keeps its share of dgamma in
+// registers.
 template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs A) {
+__global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArgs A) {
+  using Raw = RopeRaw<T, VEC, ALIGNED>;
+  __shared__ __align__(16) float tab_c[kRopeMaxTable], tab_s[kRopeMaxTable];
+  __shared__ int64_t off_in[kRopeMaxTile], off_out[kRopeMaxTile], off_x[kRopeMaxTile];
+  extern __shared__ float red[];
   const int L = A.lanes, per_cta = kRopeThreads / L;
   const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
+  const int side = (int)blockIdx.x >= A.blocks[0] ? 1 : 0;
+  const int blk = blockIdx.x - (side ? A.blocks[0] : 0), blks = A.blocks[side];
+  const RopeSide& S = A.side[side];
+  const bool norm = S.gamma != nullptr;
   RopeSlot slot[NS];
 #pragma unroll
   for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER>(l + n * L, A.dim, A.rot);
-  extern __shared__ float red[];
-  const int side = (int)blockIdx.x >= A.blocks[0] ? 1 : 0;
-  const int blk = blockIdx.x - (side ? A.blocks[0] : 0), blks = A.blocks[side];
-  {
-    const RopeSide& S = A.side[side];
-    const bool norm = S.gamma != nullptr;
-    float w[NS][2][VEC], acc[NS][2][VEC];
+  float w[NS][2][VEC], acc[NS][2][VEC];
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+  for (int n = 0; n < NS; ++n)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      w[n][0][i] = w[n][1][i] = 1.f;
+      acc[n][0][i] = acc[n][1][i] = 0.f;
+    }
+  if (norm) {
+    const T* gm = static_cast<const T*>(S.gamma);
+    const float add = A.zero_centered ? 1.f : 0.f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        w[n][0][i] = w[n][1][i] = 1.f;
-        acc[n][0][i] = acc[n][1][i] = 0.f;
-      }
-    if (norm) {
-      const T* gm = static_cast<const T*>(S.gamma);
-      const float add = A.zero_centered ? 1.f : 0.f;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          if (slot[n].on) w[n][0][i] = to_f(gm[slot[n].a + i]) + add;
-          if (slot[n].on_b) w[n][1][i] = to_f(gm[slot[n].b + i]) + add;
-        }
+        if (slot[n].on) w[n][0][i] = to_f(gm[slot[n].a + i]) + add;
+        if (slot[n].on_b) w[n][1][i] = to_f(gm[slot[n].b + i]) + add;
       }
     }
-    const int64_t units = A.units_tokens * S.chunks;
-    // Whole warps run the loop, so that every lane reaches the shuffles.
-    const int64_t steps = (units + (int64_t)blks * per_cta - 1) / ((int64_t)blks * per_cta);
-    for (int64_t st = 0; st < steps; ++st) {
-      const int64_t u = (st * blks + blk) * per_cta + grp;
-      const bool live = u < units;
-      const int64_t tok = live ? u / S.chunks : 0;
-      const int h0 = live ? (int)(u - tok * S.chunks) * A.heads_per_unit : 0;
-      const int nh = live ? min(A.heads_per_unit, S.heads - h0) : 0;
-      const int64_t bi = tok / A.tokens, ti = tok - bi * A.tokens;
-      float cs[NS][VEC], sn[NS][VEC];
+  }
+  const int j = threadIdx.x & (A.wide - 1);      // this thread's pair
+  unsigned long long turns = 0;
+  if (A.axes == 1 && j < A.rot / 2) turns = turns_of(A.freqs[j]);
+
+  for (int64_t tile = blk; tile < S.tiles; tile += blks) {
+    const int64_t tok0 = tile * S.tile;
+    const int toks = (int)min((int64_t)S.tile, A.units_tokens - tok0);
+    if (BWD) __syncthreads();   // the last tile's table gives way
+    for (int t = threadIdx.x; t < toks; t += kRopeThreads) {
+      const int64_t b = (tok0 + t) / A.tokens, k = tok0 + t - b * A.tokens;
+      off_in[t] = b * S.in_s[0] + k * S.in_s[1];
+      off_out[t] = b * S.out_s[0] + k * S.out_s[1];
+      if (BWD) off_x[t] = b * S.x_s[0] + k * S.x_s[1];
+    }
+    if (j < A.rot / 2)
+      for (int t = threadIdx.x / A.wide; t < toks; t += kRopeThreads / A.wide) {
+        const int64_t b = (tok0 + t) / A.tokens, k = tok0 + t - b * A.tokens;
+        unsigned long long sum = 0;
+        for (int ax = 0; ax < A.axes; ++ax) {
+          const int64_t at = ax * A.pos_s[0] + b * A.pos_s[1] + k * A.pos_s[2];
+          const int64_t p = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
+                                    : (int64_t)static_cast<const int*>(A.pos)[at];
+          if (A.axes > 1) turns = turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
+          sum += (unsigned long long)p * turns;
+        }
+        const int top = (int)((sum + 0x80000000ull) >> 32);   // signed 2^-32 turns
+        float s, c;
+        sincospif((float)top * 0x1p-31f, &s, &c);
+        tab_c[t * A.row + j] = c * A.scale;
+        tab_s[t * A.row + j] = s * A.scale;
+      }
+    __syncthreads();
+
+    // Heads of the tile in order, dealt to the groups. Whole warps run the
+    // loop, so that every lane reaches the shuffles.
+    const int items = toks * S.heads;
+    const int steps = (items + per_cta - 1) / per_cta;
+    Raw v0[kRopeAhead][NS][2], x0[BWD ? kRopeAhead : 1][NS][2];
+    int ft = 0, fh = grp;       // token and head of the next item to fetch
+    const auto settle = [&](int& t, int& h) {
+      while (h >= S.heads && t < toks) {
+        h -= S.heads;
+        ++t;
+      }
+    };
+    settle(ft, fh);
+    const auto fetch = [&](Raw (&v)[NS][2], Raw (&x)[NS][2]) {
+      const bool have = ft < toks;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        if (have && slot[n].on) {
+          const T* p = static_cast<const T*>(S.in) + off_in[ft] + (int64_t)fh * S.in_s[2];
+          v[n][0].load(p + slot[n].a);
+          if (slot[n].on_b) v[n][1].load(p + slot[n].b);
+          if (BWD && norm) {
+            const T* q = static_cast<const T*>(S.x) + off_x[ft] + (int64_t)fh * S.x_s[2];
+            x[n][0].load(q + slot[n].a);
+            if (slot[n].on_b) x[n][1].load(q + slot[n].b);
+          }
+        }
+      }
+      fh += per_cta;
+      settle(ft, fh);
+    };
+#pragma unroll
+    for (int d = 0; d < kRopeAhead; ++d) {
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const int j = rope_pair<VEC, INTER>(slot[n], i);
-          cs[n][i] = 1.f;
-          sn[n][i] = 0.f;
-          if (live && (slot[n].turned >> i & 1)) {
-            unsigned long long t = 0;
-            for (int ax = 0; ax < A.axes; ++ax) {
-              const int64_t at = ax * A.pos_s[0] + bi * A.pos_s[1] + ti * A.pos_s[2];
-              const int64_t p = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
-                                        : (int64_t)static_cast<const int*>(A.pos)[at];
-              t += (unsigned long long)p * turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
-            }
-            const int top = (int)((t + 0x80000000ull) >> 32);   // signed 2^-32 turns
-            float s, c;
-            sincospif((float)top * 0x1p-31f, &s, &c);
-            cs[n][i] = c * A.scale;
-            sn[n][i] = s * A.scale;
-          }
+        for (int k = 0; k < 2; ++k) {
+          v0[d][n][k].clear();
+          if (BWD) x0[d][n][k].clear();
         }
-      const int most = __reduce_max_sync(0xffffffffu, nh);
-      for (int h = 0; h < most; ++h) {
-        const bool act = h < nh;
-        const int64_t in_at = bi * S.in_s[0] + ti * S.in_s[1] + (int64_t)(h0 + h) * S.in_s[2];
-        const int64_t out_at = bi * S.out_s[0] + ti * S.out_s[1] + (int64_t)(h0 + h) * S.out_s[2];
-        const T* in = static_cast<const T*>(S.in) + in_at;
-        T* out = static_cast<T*>(S.out) + out_at;
-        float v[NS][2][VEC], xv[BWD ? NS : 1][2][VEC];
-        float ss = 0.f, gs = 0.f;
+      fetch(v0[d], x0[BWD ? d : 0]);
+    }
+    int t = 0, h = grp;
+    settle(t, h);
+    for (int st = 0; st < steps; st += kRopeAhead) {
+#pragma unroll
+      for (int d = 0; d < kRopeAhead; ++d) {
+        if (st + d >= steps) break;
+        const bool act = t < toks;
+        float v[NS][2][VEC], cs[NS][VEC], sn[NS][VEC], ss = 0.f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[n][0][i] = v[n][1][i] = 0.f;
-          if (act && slot[n].on) {
-            rope_load<T, VEC, ALIGNED>(in + slot[n].a, v[n][0]);
-            if (slot[n].on_b) rope_load<T, VEC, ALIGNED>(in + slot[n].b, v[n][1]);
+          v0[d][n][0].get(v[n][0]);
+          v0[d][n][1].get(v[n][1]);
+          const float* tc = tab_c + (act ? t : 0) * A.row;
+          const float* ts = tab_s + (act ? t : 0) * A.row;
+          if (INTER) {
+            constexpr int H = VEC > 1 ? VEC / 2 : 1;
+            rope_table_get<H>(tc + slot[n].a / 2, cs[n]);
+            rope_table_get<H>(ts + slot[n].a / 2, sn[n]);
+            const int b = slot[n].on_b ? slot[n].b / 2 : 0;
+            rope_table_get<H>(tc + b, cs[n] + VEC / 2);
+            rope_table_get<H>(ts + b, sn[n] + VEC / 2);
+          } else {
+            const int at = slot[n].turned ? slot[n].a : 0;
+            rope_table_get<VEC>(tc + at, cs[n]);
+            rope_table_get<VEC>(ts + at, sn[n]);
           }
         }
         if (!BWD) {
-          float rstd = 1.f;
+          fetch(v0[d], x0[0]);
           if (norm) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -287,88 +367,87 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs A) {
                 ss = fmaf(v[n][1][i], v[n][1][i], ss);
               }
             ss = lanes_sum(ss, L);
-            rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
-          }
+            const float rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
 #pragma unroll
-          for (int n = 0; n < NS; ++n) {
-            if (norm) {
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int i = 0; i < VEC; ++i) {
                 v[n][0][i] = v[n][0][i] * rstd * w[n][0][i];
                 v[n][1][i] = v[n][1][i] * rstd * w[n][1][i];
               }
-            }
-            rope_rotate<VEC, INTER, false>(v[n], cs[n], sn[n], slot[n].turned);
           }
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+            rope_rotate<VEC, INTER, false>(v[n], cs[n], sn[n], slot[n].turned);
         } else {
-          const T* xp = static_cast<const T*>(S.x) + bi * S.x_s[0] + ti * S.x_s[1] +
-                        (int64_t)(h0 + h) * S.x_s[2];
+          float xv[NS][2][VEC], gs = 0.f;
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) xv[n][0][i] = xv[n][1][i] = 0.f;
-            if (norm && act && slot[n].on) {
-              rope_load<T, VEC, ALIGNED>(xp + slot[n].a, xv[n][0]);
-              if (slot[n].on_b) rope_load<T, VEC, ALIGNED>(xp + slot[n].b, xv[n][1]);
-            }
-            rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
+            x0[d][n][0].get(xv[n][0]);
+            x0[d][n][1].get(xv[n][1]);
           }
+          fetch(v0[d], x0[d]);
+#pragma unroll
+          for (int n = 0; n < NS; ++n)
+            rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
           if (norm) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) ss = fmaf(xv[n][k][i], xv[n][k][i], ss);
+                for (int i = 0; i < VEC; ++i) {
+                  ss = fmaf(xv[n][k][i], xv[n][k][i], ss);
+                  gs = fmaf(v[n][k][i] * w[n][k][i], xv[n][k][i], gs);
+                }
+            // sum g x and sum x^2 in one go; sum g xhat = rstd sum g x
             ss = lanes_sum(ss, L);
+            gs = lanes_sum(gs, L);
             const float rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
+            gs *= rstd * A.inv_dim;
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                  xv[n][k][i] *= rstd;
-                  if (act) acc[n][k][i] = fmaf(v[n][k][i], xv[n][k][i], acc[n][k][i]);
-                  v[n][k][i] *= w[n][k][i];
-                  gs = fmaf(v[n][k][i], xv[n][k][i], gs);
+                  const float xh = xv[n][k][i] * rstd;
+                  if (act) acc[n][k][i] = fmaf(v[n][k][i], xh, acc[n][k][i]);
+                  v[n][k][i] = rstd * fmaf(-xh, gs, v[n][k][i] * w[n][k][i]);
                 }
-            gs = lanes_sum(gs, L) * A.inv_dim;
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) v[n][k][i] = rstd * fmaf(-xv[n][k][i], gs, v[n][k][i]);
           }
         }
+        if (act) {
+          T* out = static_cast<T*>(S.out) + off_out[t] + (int64_t)h * S.out_s[2];
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          if (act && slot[n].on) {
-            rope_store<T, VEC, ALIGNED>(out + slot[n].a, v[n][0]);
+          for (int n = 0; n < NS; ++n) {
+            if (slot[n].on) rope_store<T, VEC, ALIGNED>(out + slot[n].a, v[n][0]);
             if (slot[n].on_b) rope_store<T, VEC, ALIGNED>(out + slot[n].b, v[n][1]);
           }
         }
+        h += per_cta;
+        settle(t, h);
       }
     }
-    if (BWD && A.ws != nullptr) {
-      // The groups' sums, added in their order, into this CTA's partial row.
-      // The side with fewer CTAs has its other rows zeroed by the other side.
+  }
+  if (BWD && A.ws != nullptr) {
+    // The groups' sums, added in their order, into this CTA's partial row.
+    // The side with fewer CTAs has its other rows zeroed by the other side.
 #pragma unroll
-      for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          if (slot[n].on) red[grp * A.dim + slot[n].a + i] = acc[n][0][i];
-          if (slot[n].on_b) red[grp * A.dim + slot[n].b + i] = acc[n][1][i];
-        }
-      __syncthreads();
-      float* row = A.ws + (int64_t)blk * 2 * A.dim;
-      for (int d = threadIdx.x; d < A.dim; d += kRopeThreads) {
-        float t = 0.f;
-        for (int g = 0; g < per_cta; ++g) t += red[g * A.dim + d];
-        row[side * A.dim + d] = t;
-        if (blk >= A.blocks[1 - side]) row[(1 - side) * A.dim + d] = 0.f;
+      for (int i = 0; i < VEC; ++i) {
+        if (slot[n].on) red[grp * A.dim + slot[n].a + i] = acc[n][0][i];
+        if (slot[n].on_b) red[grp * A.dim + slot[n].b + i] = acc[n][1][i];
       }
+    __syncthreads();
+    float* row = A.ws + (int64_t)blk * 2 * A.dim;
+    for (int d = threadIdx.x; d < A.dim; d += kRopeThreads) {
+      float t = 0.f;
+#pragma unroll 4
+      for (int g = 0; g < per_cta; ++g) t += red[g * A.dim + d];
+      row[side * A.dim + d] = t;
+      if (blk >= A.blocks[1 - side]) row[(1 - side) * A.dim + d] = 0.f;
     }
   }
 }
