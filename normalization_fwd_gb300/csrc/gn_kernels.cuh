@@ -15,6 +15,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fastdiv.h"
 
 namespace nf {
 
@@ -24,20 +25,6 @@ constexpr int kGnStep = 2;          // rows of one step
 constexpr int kGnMaxSlices = 512;   // most slices of a panel
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
-
-// Division of n < 2^31 by a number fixed for the launch: with s = ceil(log2 d)
-// and m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n m) + n) >> s.
-struct FastDiv {
-  unsigned d, m, s;
-  void set(unsigned v) {
-    d = v;
-    for (s = 0; (1ull << s) < v; ++s) {}
-    m = (unsigned)(((1ull << 32) * ((1ull << s) - v)) / v + 1);
-  }
-  __device__ __forceinline__ int div(int n) const {
-    return (int)((__umulhi((unsigned)n, m) + (unsigned)n) >> s);
-  }
-};
 
 // Arguments of the group norm kernels (validated on the host).
 struct GnArgs {

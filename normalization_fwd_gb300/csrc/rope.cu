@@ -170,6 +170,8 @@ void fill(RopeArgs* a, const Shape& c, const rope_positions* r, float eps, int z
   for (int i = 0; i < 3; ++i) a->pos_s[i] = r->stride[i];
   a->tokens = c.tokens;
   a->units_tokens = c.batch * c.tokens;
+  a->small = c.batch * c.tokens <= INT32_MAX;
+  if (a->small) a->by_tokens.set((unsigned)(c.tokens > 0 ? c.tokens : 1));
   a->pos64 = r->bits == 64;
   a->axes = (int)r->axes;
   a->dim = (int)c.dim;

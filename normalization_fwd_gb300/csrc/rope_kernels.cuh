@@ -17,6 +17,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fastdiv.h"
 
 namespace nf {
 
@@ -46,6 +47,8 @@ struct RopeArgs {
   int64_t pos_s[3];      // strides of axis, batch, token (elements)
   int64_t tokens;        // of a sequence
   int64_t units_tokens;  // batch * tokens
+  FastDiv by_tokens;     // when batch * tokens is below 2^31 (small)
+  int small;
   float* ws;             // backward: [max of blocks][2 * dim] partials, or null
   int blocks[2];         // CTAs of each side, the queries' first
   int pos64, axes;
@@ -80,24 +83,40 @@ template <typename T, int VEC, bool ALIGNED> struct RopeRaw {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) u.t[i] = from_f<T>(0.f);
   }
-  __device__ __forceinline__ void get(float* f) const {
+  // As pairs of fp32 (one element: a pair with an idle second half), and back.
+  __device__ __forceinline__ void get(float2* f) const {
+    if constexpr (B == 16) {
+      unpack2<T>(u.q, f);
+    } else if constexpr (VEC == 1) {
+      f[0] = make_float2(to_f(u.t[0]), 0.f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = to_f(u.t[i]);
+      for (int i = 0; i < VEC / 2; ++i) f[i] = make_float2(to_f(u.t[2 * i]), to_f(u.t[2 * i + 1]));
+    }
+  }
+  __device__ __forceinline__ void set(const float2* f) {
+    if constexpr (B == 16) {
+      u.q = pack2<T>(f);
+    } else if constexpr (VEC == 1) {
+      u.t[0] = from_f<T>(f[0].x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        u.t[2 * i] = from_f<T>(f[i].x);
+        u.t[2 * i + 1] = from_f<T>(f[i].y);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if (ALIGNED && B == 16) *reinterpret_cast<uint4*>(p) = u.q;
+    else if (ALIGNED && B == 8) *reinterpret_cast<uint2*>(p) = u.d;
+    else if (ALIGNED && B == 4) *reinterpret_cast<unsigned*>(p) = u.w;
+    else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = u.t[i];
+    }
   }
 };
-template <typename T, int VEC, bool ALIGNED>
-__device__ __forceinline__ void rope_store(T* p, const float* f) {
-  RopeRaw<T, VEC, ALIGNED> r;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) r.u.t[i] = from_f<T>(f[i]);
-  if (ALIGNED && r.B == 16) *reinterpret_cast<uint4*>(p) = r.u.q;
-  else if (ALIGNED && r.B == 8) *reinterpret_cast<uint2*>(p) = r.u.d;
-  else if (ALIGNED && r.B == 4) *reinterpret_cast<unsigned*>(p) = r.u.w;
-  else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = r.u.t[i];
-  }
-}
 
 // A frequency in radians as a 64-bit fraction of a turn: f * 2^64 / (2 pi)
 // modulo 2^64, by integers (double arithmetic is slow on this part). With
@@ -172,44 +191,58 @@ __device__ __forceinline__ RopeSlot rope_slot(int s, int dim, int rot) {
 }
 
 // Rotate a slot's pairs in place by (cos, sin); INV: the transposed
-// rotation. Pairs that pass through are not touched (an infinity times a
-// sine of 0 would be a NaN in its neighbour).
-template <int VEC, bool INTER, bool INV>
-__device__ __forceinline__ void rope_rotate(float (*v)[VEC], const float* cs, const float* sn,
-                                            unsigned turned) {
+// rotation. v: the slot's two vectors as pairs of neighbours. Pairs that pass
+// through are not touched (an infinity times a sine of 0 would be a NaN in
+// its neighbour).
+template <int VEC, bool INTER, bool INV, int NP>
+__device__ __forceinline__ void rope_rotate(float2 (&v)[2][NP], const float2 (&cs)[NP],
+                                            const float2 (&sn)[NP], unsigned turned) {
+  if (INTER) {
+    // cs, sn: of the first vector's pairs, then of the second's
+    constexpr int H = VEC > 1 ? VEC / 2 : 1;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    constexpr int H = VEC > 1 ? VEC / 2 : 1;   // pairs of a vector (INTER)
-    float& p = INTER ? v[i / H][2 * (i % H) % VEC] : v[0][i];
-    float& q = INTER ? v[i / H][(2 * (i % H) + 1) % VEC] : v[1][i];
-    const float c = cs[i], s = INV ? -sn[i] : sn[i];
-    const float p0 = p, q0 = q;
-    if (turned >> i & 1) {
-      p = p0 * c - q0 * s;
-      q = q0 * c + p0 * s;
+    for (int i = 0; i < VEC; ++i) {
+      float2& p = v[i / H][i % H];
+      const float c = i % 2 ? cs[i / 2].y : cs[i / 2].x;
+      const float t = i % 2 ? sn[i / 2].y : sn[i / 2].x, s = INV ? -t : t;
+      const float2 r = make_float2(p.x * c - p.y * s, p.y * c + p.x * s);
+      if (turned >> i & 1) p = r;
+    }
+  } else if (turned) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 a = v[0][i], b = v[1][i];
+      const float2 as = mul2(a, sn[i]), bs = mul2(b, sn[i]);
+      const float2 ac = mul2(a, cs[i]), bc = mul2(b, cs[i]);
+      v[0][i] = INV ? add2(ac, bs) : fma2(bs, splat2(-1.f), ac);
+      v[1][i] = INV ? fma2(as, splat2(-1.f), bc) : add2(bc, as);
     }
   }
 }
 
+// Sum over aligned groups of `lanes` lanes; the same branches in every lane.
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// N consecutive floats of the table.
-template <int N> __device__ __forceinline__ void rope_table_get(const float* t, float* f) {
-  if (N % 4 == 0) {
+// N consecutive floats of the table, from pair `at` of f on.
+template <int N, int NP>
+__device__ __forceinline__ void rope_table_get(const float* t, float2 (&f)[NP], int at) {
+  if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
       const float4 v = reinterpret_cast<const float4*>(t)[i];
-      f[4 * i] = v.x;
-      f[4 * i + 1] = v.y;
-      f[4 * i + 2] = v.z;
-      f[4 * i + 3] = v.w;
+      f[at + 2 * i] = make_float2(v.x, v.y);
+      f[at + 2 * i + 1] = make_float2(v.z, v.w);
     }
-  } else {
+  } else if constexpr (N % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = t[i];
+    for (int i = 0; i < N / 2; ++i) f[at + i] = reinterpret_cast<const float2*>(t)[i];
+  } else {
+    f[at] = make_float2(t[0], 0.f);
   }
 }
 
@@ -223,7 +256,8 @@ template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool BWD>
 __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArgs A) {
   using Raw = RopeRaw<T, VEC, ALIGNED>;
   __shared__ __align__(16) float tab_c[kRopeMaxTable], tab_s[kRopeMaxTable];
-  __shared__ int64_t off_in[kRopeMaxTile], off_out[kRopeMaxTile], off_x[kRopeMaxTile];
+  __shared__ int64_t off_in[kRopeMaxTile], off_out[kRopeMaxTile], off_x[kRopeMaxTile],
+      off_pos[kRopeMaxTile];
   extern __shared__ float red[];
   const int L = A.lanes, per_cta = kRopeThreads / L;
   const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
@@ -234,23 +268,28 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   RopeSlot slot[NS];
 #pragma unroll
   for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER>(l + n * L, A.dim, A.rot);
-  float w[NS][2][VEC], acc[NS][2][VEC];
+  constexpr int NP = (VEC + 1) / 2;
+  float2 w[NS][2][NP], acc[NS][2][NP];
 #pragma unroll
   for (int n = 0; n < NS; ++n)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      w[n][0][i] = w[n][1][i] = 1.f;
-      acc[n][0][i] = acc[n][1][i] = 0.f;
+    for (int i = 0; i < NP; ++i) {
+      w[n][0][i] = w[n][1][i] = splat2(1.f);
+      acc[n][0][i] = acc[n][1][i] = splat2(0.f);
     }
   if (norm) {
     const T* gm = static_cast<const T*>(S.gamma);
-    const float add = A.zero_centered ? 1.f : 0.f;
+    const float2 add = splat2(A.zero_centered ? 1.f : 0.f);
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (slot[n].on) w[n][0][i] = to_f(gm[slot[n].a + i]) + add;
-        if (slot[n].on_b) w[n][1][i] = to_f(gm[slot[n].b + i]) + add;
+      for (int k = 0; k < 2; ++k) {
+        RopeRaw<T, VEC, false> g;   // gamma's own alignment is not asked for
+        g.clear();
+        if (k == 0 ? slot[n].on : slot[n].on_b) g.load(gm + (k == 0 ? slot[n].a : slot[n].b));
+        g.get(w[n][k]);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) w[n][k][i] = add2(w[n][k][i], add);
       }
     }
   }
@@ -262,29 +301,15 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     const int64_t tok0 = tile * S.tile;
     const int toks = (int)min((int64_t)S.tile, A.units_tokens - tok0);
     if (BWD) __syncthreads();   // the last tile's table gives way
-    for (int t = threadIdx.x; t < toks; t += kRopeThreads) {
-      const int64_t b = (tok0 + t) / A.tokens, k = tok0 + t - b * A.tokens;
-      off_in[t] = b * S.in_s[0] + k * S.in_s[1];
-      off_out[t] = b * S.out_s[0] + k * S.out_s[1];
-      if (BWD) off_x[t] = b * S.x_s[0] + k * S.x_s[1];
+    if (threadIdx.x < toks) {
+      const int64_t tok = tok0 + threadIdx.x;
+      const int64_t b = A.small ? A.by_tokens.div((int)tok) : tok / A.tokens;
+      const int64_t k = tok - b * A.tokens;
+      off_in[threadIdx.x] = b * S.in_s[0] + k * S.in_s[1];
+      off_out[threadIdx.x] = b * S.out_s[0] + k * S.out_s[1];
+      if (BWD) off_x[threadIdx.x] = b * S.x_s[0] + k * S.x_s[1];
+      off_pos[threadIdx.x] = b * A.pos_s[1] + k * A.pos_s[2];
     }
-    if (j < A.rot / 2)
-      for (int t = threadIdx.x / A.wide; t < toks; t += kRopeThreads / A.wide) {
-        const int64_t b = (tok0 + t) / A.tokens, k = tok0 + t - b * A.tokens;
-        unsigned long long sum = 0;
-        for (int ax = 0; ax < A.axes; ++ax) {
-          const int64_t at = ax * A.pos_s[0] + b * A.pos_s[1] + k * A.pos_s[2];
-          const int64_t p = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
-                                    : (int64_t)static_cast<const int*>(A.pos)[at];
-          if (A.axes > 1) turns = turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
-          sum += (unsigned long long)p * turns;
-        }
-        const int top = (int)((sum + 0x80000000ull) >> 32);   // signed 2^-32 turns
-        float s, c;
-        sincospif((float)top * 0x1p-31f, &s, &c);
-        tab_c[t * A.row + j] = c * A.scale;
-        tab_s[t * A.row + j] = s * A.scale;
-      }
     __syncthreads();
 
     // Heads of the tile in order, dealt to the groups. Whole warps run the
@@ -329,6 +354,25 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
         }
       fetch(v0[d], x0[BWD ? d : 0]);
     }
+    // The angles, while the first heads are on their way.
+    if (j < A.rot / 2)
+      for (int t = threadIdx.x / A.wide; t < toks; t += kRopeThreads / A.wide) {
+        unsigned long long sum = 0;
+        for (int ax = 0; ax < A.axes; ++ax) {
+          const int64_t at = ax * A.pos_s[0] + off_pos[t];
+          const int64_t p = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
+                                    : (int64_t)static_cast<const int*>(A.pos)[at];
+          if (A.axes > 1) turns = turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
+          sum += (unsigned long long)p * turns;
+        }
+        const int top = (int)((sum + 0x80000000ull) >> 32);   // signed 2^-32 turns
+        float s, c;
+        sincospif((float)top * 0x1p-31f, &s, &c);
+        tab_c[t * A.row + j] = c * A.scale;
+        tab_s[t * A.row + j] = s * A.scale;
+      }
+    __syncthreads();
+
     int t = 0, h = grp;
     settle(t, h);
     for (int st = 0; st < steps; st += kRopeAhead) {
@@ -336,24 +380,29 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
       for (int d = 0; d < kRopeAhead; ++d) {
         if (st + d >= steps) break;
         const bool act = t < toks;
-        float v[NS][2][VEC], cs[NS][VEC], sn[NS][VEC], ss = 0.f;
+        float2 v[NS][2][NP], cs[NS][NP], sn[NS][NP], sum = splat2(0.f);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
           v0[d][n][0].get(v[n][0]);
           v0[d][n][1].get(v[n][1]);
           const float* tc = tab_c + (act ? t : 0) * A.row;
           const float* ts = tab_s + (act ? t : 0) * A.row;
-          if (INTER) {
-            constexpr int H = VEC > 1 ? VEC / 2 : 1;
-            rope_table_get<H>(tc + slot[n].a / 2, cs[n]);
-            rope_table_get<H>(ts + slot[n].a / 2, sn[n]);
+          if constexpr (INTER) {
+            constexpr int H = VEC / 2;
             const int b = slot[n].on_b ? slot[n].b / 2 : 0;
-            rope_table_get<H>(tc + b, cs[n] + VEC / 2);
-            rope_table_get<H>(ts + b, sn[n] + VEC / 2);
+            if constexpr (H == 1) {
+              cs[n][0] = make_float2(tc[slot[n].a / 2], tc[b]);
+              sn[n][0] = make_float2(ts[slot[n].a / 2], ts[b]);
+            } else {
+              rope_table_get<H>(tc + slot[n].a / 2, cs[n], 0);
+              rope_table_get<H>(ts + slot[n].a / 2, sn[n], 0);
+              rope_table_get<H>(tc + b, cs[n], H / 2);
+              rope_table_get<H>(ts + b, sn[n], H / 2);
+            }
           } else {
             const int at = slot[n].turned ? slot[n].a : 0;
-            rope_table_get<VEC>(tc + at, cs[n]);
-            rope_table_get<VEC>(ts + at, sn[n]);
+            rope_table_get<VEC>(tc + at, cs[n], 0);
+            rope_table_get<VEC>(ts + at, sn[n], 0);
           }
         }
         if (!BWD) {
@@ -362,25 +411,23 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                ss = fmaf(v[n][0][i], v[n][0][i], ss);
-                ss = fmaf(v[n][1][i], v[n][1][i], ss);
-              }
-            ss = lanes_sum(ss, L);
-            const float rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) sum = fma2(v[n][k][i], v[n][k][i], sum);
+            const float ss = lanes_sum(sum.x + sum.y, L);
+            const float2 rstd = splat2(rsqrtf(fmaf(ss, A.inv_dim, A.eps)));
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                v[n][0][i] = v[n][0][i] * rstd * w[n][0][i];
-                v[n][1][i] = v[n][1][i] * rstd * w[n][1][i];
-              }
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) v[n][k][i] = mul2(mul2(v[n][k][i], rstd), w[n][k][i]);
           }
 #pragma unroll
           for (int n = 0; n < NS; ++n)
             rope_rotate<VEC, INTER, false>(v[n], cs[n], sn[n], slot[n].turned);
         } else {
-          float xv[NS][2][VEC], gs = 0.f;
+          float2 xv[NS][2][NP];
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
             x0[d][n][0].get(xv[n][0]);
@@ -391,29 +438,29 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
           for (int n = 0; n < NS; ++n)
             rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
           if (norm) {
+            float2 dot = splat2(0.f);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                  ss = fmaf(xv[n][k][i], xv[n][k][i], ss);
-                  gs = fmaf(v[n][k][i] * w[n][k][i], xv[n][k][i], gs);
+                for (int i = 0; i < NP; ++i) {
+                  sum = fma2(xv[n][k][i], xv[n][k][i], sum);
+                  dot = fma2(mul2(v[n][k][i], w[n][k][i]), xv[n][k][i], dot);
                 }
-            // sum g x and sum x^2 in one go; sum g xhat = rstd sum g x
-            ss = lanes_sum(ss, L);
-            gs = lanes_sum(gs, L);
-            const float rstd = 1.f / sqrtf(fmaf(ss, A.inv_dim, A.eps));
-            gs *= rstd * A.inv_dim;
+            // sum g xhat = rstd sum g x, so one round of shuffles serves both
+            const float ss = lanes_sum(sum.x + sum.y, L), gs = lanes_sum(dot.x + dot.y, L);
+            const float rstd = rsqrtf(fmaf(ss, A.inv_dim, A.eps));
+            const float2 rs = splat2(rstd), mean = splat2(-gs * rstd * A.inv_dim);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                  const float xh = xv[n][k][i] * rstd;
-                  if (act) acc[n][k][i] = fmaf(v[n][k][i], xh, acc[n][k][i]);
-                  v[n][k][i] = rstd * fmaf(-xh, gs, v[n][k][i] * w[n][k][i]);
+                for (int i = 0; i < NP; ++i) {
+                  const float2 xh = mul2(xv[n][k][i], rs);
+                  if (act) acc[n][k][i] = fma2(v[n][k][i], xh, acc[n][k][i]);
+                  v[n][k][i] = mul2(rs, fma2(xh, mean, mul2(v[n][k][i], w[n][k][i])));
                 }
           }
         }
@@ -421,8 +468,15 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
           T* out = static_cast<T*>(S.out) + off_out[t] + (int64_t)h * S.out_s[2];
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
-            if (slot[n].on) rope_store<T, VEC, ALIGNED>(out + slot[n].a, v[n][0]);
-            if (slot[n].on_b) rope_store<T, VEC, ALIGNED>(out + slot[n].b, v[n][1]);
+            Raw r;
+            if (slot[n].on) {
+              r.set(v[n][0]);
+              r.store(out + slot[n].a);
+            }
+            if (slot[n].on_b) {
+              r.set(v[n][1]);
+              r.store(out + slot[n].b);
+            }
           }
         }
         h += per_cta;
@@ -437,8 +491,9 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        if (slot[n].on) red[grp * A.dim + slot[n].a + i] = acc[n][0][i];
-        if (slot[n].on_b) red[grp * A.dim + slot[n].b + i] = acc[n][1][i];
+        const float2 p = acc[n][0][i / 2], q = acc[n][1][i / 2];
+        if (slot[n].on) red[grp * A.dim + slot[n].a + i] = i % 2 ? p.y : p.x;
+        if (slot[n].on_b) red[grp * A.dim + slot[n].b + i] = i % 2 ? q.y : q.x;
       }
     __syncthreads();
     float* row = A.ws + (int64_t)blk * 2 * A.dim;
