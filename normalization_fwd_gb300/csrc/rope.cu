@@ -9,9 +9,9 @@
 
 namespace nf {
 
-const void* rope_table_f32(int vec, int ns, bool inter, bool aligned, bool bwd);
-const void* rope_table_bf16(int vec, int ns, bool inter, bool aligned, bool bwd);
-const void* rope_table_f16(int vec, int ns, bool inter, bool aligned, bool bwd);
+const void* rope_table_f32(int vec, int ns, bool inter, bool aligned, bool full, bool bwd);
+const void* rope_table_bf16(int vec, int ns, bool inter, bool aligned, bool full, bool bwd);
+const void* rope_table_f16(int vec, int ns, bool inter, bool aligned, bool full, bool bwd);
 
 namespace {
 
@@ -26,6 +26,7 @@ struct Shape {
 };
 
 constexpr int kBwdBlocksPerSm = 2;   // backward CTAs an SM, each with a row of partials
+constexpr int kFwdBlocksPerSm = 3;
 constexpr int kRopeItems = 8;        // heads of a tile for each group of threads
 
 Strided strided(const void* p, const int64_t* st, int64_t heads, const Shape& c) {
@@ -118,9 +119,10 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
   const int ns = slots <= 32 ? 1 : 8 / v;
   int lanes = 1;
   while (lanes * ns < slots) lanes *= 2;
-  p->fn = c.dtype == LN_F32    ? rope_table_f32(v, ns, inter, al, bwd)
-          : c.dtype == LN_BF16 ? rope_table_bf16(v, ns, inter, al, bwd)
-                               : rope_table_f16(v, ns, inter, al, bwd);
+  const bool full = rot == dim && slots == lanes * ns && dim == 2 * v * lanes * ns;
+  p->fn = c.dtype == LN_F32    ? rope_table_f32(v, ns, inter, al, full, bwd)
+          : c.dtype == LN_BF16 ? rope_table_bf16(v, ns, inter, al, full, bwd)
+                               : rope_table_f16(v, ns, inter, al, full, bwd);
   if (p->fn == nullptr) return LN_ERR_UNSUPPORTED;
   p->lanes = lanes;
   const int per_cta = kRopeThreads / lanes;
@@ -152,11 +154,8 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
     if (tile < 1) tile = 1;
     d.tile = (int)tile;
     d.tiles = (toks + tile - 1) / tile;
-    int64_t most = 1 << 30;
-    if (bwd) {
-      most = (int64_t)sms * kBwdBlocksPerSm * d.heads / total;
-      if (most < 1) most = 1;
-    }
+    int64_t most = (int64_t)sms * (bwd ? kBwdBlocksPerSm : kFwdBlocksPerSm) * d.heads / total;
+    if (most < 1) most = 1;
     a->blocks[s] = (int)(d.tiles < most ? d.tiles : most);
   }
   p->grid = a->blocks[0] + a->blocks[1];

@@ -22,10 +22,11 @@
 namespace nf {
 
 constexpr int kRopeThreads = 256;
+// Heads that a thread has on their way.
+constexpr int kRopeAheadFwd = 2, kRopeAheadBwd = 1;
 constexpr int kRopeMaxDim = 512;
 constexpr int kRopeMaxTile = 32;      // tokens of a tile
 constexpr int kRopeMaxTable = 2048;   // floats of a tile's cosines, and of its sines
-constexpr int kRopeAhead = 2;         // heads that a thread has on their way
 constexpr int kRopeMaxAxes = 4;
 
 // One of the tensors a call takes (queries or keys).
@@ -157,10 +158,18 @@ template <int VEC, bool INTER> __device__ __forceinline__ int rope_pair(const Ro
   if (!INTER) return r.a + i;
   return i < VEC / 2 ? r.a / 2 + i : r.b / 2 + i - VEC / 2;
 }
-template <int VEC, bool INTER>
+// FULL: every slot is there and all of it is rotated.
+template <int VEC, bool INTER, bool FULL>
 __device__ __forceinline__ RopeSlot rope_slot(int s, int dim, int rot) {
   RopeSlot r;
   const int nv = dim / VEC;
+  if (FULL) {
+    r.on = r.on_b = true;
+    r.turned = (1u << VEC) - 1;
+    r.a = s * VEC;
+    r.b = r.a + dim / 2;
+    return r;
+  }
   if (INTER) {
     const int n2 = (nv + 1) / 2;
     r.on = s < n2;
@@ -248,13 +257,14 @@ __device__ __forceinline__ void rope_table_get(const float* t, float2 (&f)[NP], 
 
 // A CTA takes the queries or the keys of a tile of tokens. It works out the
 // cosines and sines of the tile's tokens once, into shared memory, and goes
-// through the tokens' heads with a group of `lanes` threads a head, the next
-// kRopeAhead heads of a group always on their way. Forward: a tile a CTA;
-// backward: a CTA takes tile after tile and keeps its share of dgamma in
-// registers.
-template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool BWD>
+// through the tokens' heads with a group of `lanes` threads a head, a group's
+// next heads always on their way. A CTA takes tile after tile; in the
+// backward it keeps its share of dgamma in registers. FULL: each lane has a
+// whole slot and all of the head is rotated.
+template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool FULL, bool BWD>
 __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArgs A) {
   using Raw = RopeRaw<T, VEC, ALIGNED>;
+  constexpr int kAhead = BWD ? kRopeAheadBwd : kRopeAheadFwd;
   __shared__ __align__(16) float tab_c[kRopeMaxTable], tab_s[kRopeMaxTable];
   __shared__ int64_t off_in[kRopeMaxTile], off_out[kRopeMaxTile], off_x[kRopeMaxTile],
       off_pos[kRopeMaxTile];
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   const bool norm = S.gamma != nullptr;
   RopeSlot slot[NS];
 #pragma unroll
-  for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER>(l + n * L, A.dim, A.rot);
+  for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER, FULL>(l + n * L, A.dim, A.rot);
   constexpr int NP = (VEC + 1) / 2;
   float2 w[NS][2][NP], acc[NS][2][NP];
 #pragma unroll
@@ -300,7 +310,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   for (int64_t tile = blk; tile < S.tiles; tile += blks) {
     const int64_t tok0 = tile * S.tile;
     const int toks = (int)min((int64_t)S.tile, A.units_tokens - tok0);
-    if (BWD) __syncthreads();   // the last tile's table gives way
+    __syncthreads();   // the last tile's table gives way
     if (threadIdx.x < toks) {
       const int64_t tok = tok0 + threadIdx.x;
       const int64_t b = A.small ? A.by_tokens.div((int)tok) : tok / A.tokens;
@@ -316,7 +326,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     // loop, so that every lane reaches the shuffles.
     const int items = toks * S.heads;
     const int steps = (items + per_cta - 1) / per_cta;
-    Raw v0[kRopeAhead][NS][2], x0[BWD ? kRopeAhead : 1][NS][2];
+    Raw v0[kAhead][NS][2], x0[BWD ? kAhead : 1][NS][2];
     int ft = 0, fh = grp;       // token and head of the next item to fetch
     const auto settle = [&](int& t, int& h) {
       while (h >= S.heads && t < toks) {
@@ -344,7 +354,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
       settle(ft, fh);
     };
 #pragma unroll
-    for (int d = 0; d < kRopeAhead; ++d) {
+    for (int d = 0; d < kAhead; ++d) {
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -375,10 +385,9 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
 
     int t = 0, h = grp;
     settle(t, h);
-    for (int st = 0; st < steps; st += kRopeAhead) {
+    for (int st = 0; st < steps; st += kAhead) {
 #pragma unroll
-      for (int d = 0; d < kRopeAhead; ++d) {
-        if (st + d >= steps) break;
+      for (int d = 0; d < kAhead; ++d) {
         const bool act = t < toks;
         float2 v[NS][2][NP], cs[NS][NP], sn[NS][NP], sum = splat2(0.f);
 #pragma unroll

@@ -7,27 +7,31 @@
 
 namespace nf {
 
-template <typename T, int VEC, int NS, bool INTER, bool ALIGNED>
+template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool FULL>
 const void* rope_dir(bool bwd) {
-  return bwd ? (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, true>
-             : (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, false>;
+  return bwd ? (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, true>
+             : (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, false>;
 }
-template <typename T, int VEC, bool INTER, bool ALIGNED> const void* rope_ns(int ns, bool bwd) {
-  if (ns == 1) return rope_dir<T, VEC, 1, INTER, ALIGNED>(bwd);
-  if (VEC < 8 && ns == 8 / VEC) return rope_dir<T, VEC, 8 / VEC, INTER, ALIGNED>(bwd);
+template <typename T, int VEC, bool INTER, bool ALIGNED>
+const void* rope_ns(int ns, bool full, bool bwd) {
+  // Heads of 64, 128 and 256 elements that are rotated whole, in vectors.
+  if constexpr (VEC == Vec<T>::N && ALIGNED)
+    if (ns == 1 && full) return rope_dir<T, VEC, 1, INTER, ALIGNED, true>(bwd);
+  if (ns == 1) return rope_dir<T, VEC, 1, INTER, ALIGNED, false>(bwd);
+  if (VEC < 8 && ns == 8 / VEC) return rope_dir<T, VEC, 8 / VEC, INTER, ALIGNED, false>(bwd);
   return nullptr;
 }
-template <typename T, bool INTER> const void* rope_vec(int vec, int ns, bool aligned, bool bwd) {
-  if (vec == Vec<T>::N) return rope_ns<T, Vec<T>::N, INTER, true>(ns, bwd);
-  if (Vec<T>::N == 8 && vec == 4) return rope_ns<T, 4, INTER, true>(ns, bwd);
-  if (vec == 2 && aligned) return rope_ns<T, 2, INTER, true>(ns, bwd);
-  if (INTER) return vec == 2 ? rope_ns<T, 2, INTER, false>(ns, bwd) : nullptr;
-  return vec == 1 ? rope_ns<T, 1, false, false>(ns, bwd) : nullptr;
+template <typename T, bool INTER> const void* rope_vec(int vec, int ns, bool aligned, bool full, bool bwd) {
+  if (vec == Vec<T>::N) return rope_ns<T, Vec<T>::N, INTER, true>(ns, full, bwd);
+  if (Vec<T>::N == 8 && vec == 4) return rope_ns<T, 4, INTER, true>(ns, full, bwd);
+  if (vec == 2 && aligned) return rope_ns<T, 2, INTER, true>(ns, full, bwd);
+  if (INTER) return vec == 2 ? rope_ns<T, 2, INTER, false>(ns, full, bwd) : nullptr;
+  return vec == 1 ? rope_ns<T, 1, false, false>(ns, full, bwd) : nullptr;
 }
 template <typename T>
-const void* rope_table(int vec, int ns, bool inter, bool aligned, bool bwd) {
-  return inter ? rope_vec<T, true>(vec, ns, aligned, bwd)
-               : rope_vec<T, false>(vec, ns, aligned, bwd);
+const void* rope_table(int vec, int ns, bool inter, bool aligned, bool full, bool bwd) {
+  return inter ? rope_vec<T, true>(vec, ns, aligned, full, bwd)
+               : rope_vec<T, false>(vec, ns, aligned, full, bwd);
 }
 
 }  // namespace nf
