@@ -422,8 +422,7 @@ ln_status gn_workspace_bytes(int64_t samples, int64_t rows, int64_t channels, in
  * with the RMSNorm of each head in front where a gamma is given.
  *
  * A tensor is [batch, tokens, heads, head_dim], head_dim contiguous, with
- * strides in elements for batch, token and head: slices of a packed
- * projection, [batch, heads, tokens, head_dim] in memory and expanded inputs
+ * strides in elements for batch, token and head: slices of a packed projection, [batch, heads, tokens, head_dim] in memory and expanded inputs
  * are all given that way. The first `rot` elements of a head form rot / 2
  * pairs: (j, j + rot / 2) for ROPE_HALF, (2j, 2j + 1) for ROPE_INTERLEAVED;
  * the elements after them pass through. Per head, in fp32:

@@ -126,36 +126,38 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
   if (p->fn == nullptr) return LN_ERR_UNSUPPORTED;
   p->lanes = lanes;
   const int per_cta = kRopeThreads / lanes;
+  const int per_sm = bwd ? kBwdBlocksPerSm : kFwdBlocksPerSm;
   a->lanes = lanes;
   a->row = (dim / 2 + 3) / 4 * 4;
   a->wide = 1;
   while (a->wide < rot / 2) a->wide *= 2;
-  const int64_t toks = c.batch * c.tokens;
   const int total = a->side[0].heads + a->side[1].heads;
   int most_tile = kRopeMaxTable / a->row;
   if (most_tile > kRopeMaxTile) most_tile = kRopeMaxTile;
   for (int s = 0; s < 2; ++s) {
     RopeSide& d = a->side[s];
-    if (d.heads == 0) {
-      a->blocks[s] = 0;
-      d.tile = 1;
-      d.tiles = 0;
-      continue;
-    }
-    // Tokens of a tile: kRopeItems heads for every group, fewer where the
+    d.head_lanes = d.heads < per_cta ? (d.heads > 0 ? d.heads : 1) : per_cta;
+    d.token_lanes = per_cta / d.head_lanes;
+    d.tile = 1;
+    d.row_tiles = d.tiles = 0;
+    a->blocks[s] = 0;
+    if (d.heads == 0) continue;
+    // Tokens of a tile: kRopeItems rows for every group, fewer where the
     // device would not have a CTA for each of its places.
-    int64_t tile = ((int64_t)kRopeItems * per_cta + d.heads - 1) / d.heads;
-    const int64_t places = (int64_t)sms * 3 * d.heads / total;
-    const int64_t even = toks / (places > 0 ? places : 1);
+    const int64_t rounds = (d.heads + d.head_lanes - 1) / d.head_lanes;
+    int64_t tile = (kRopeItems + rounds - 1) / rounds * d.token_lanes;
+    const int64_t places = (int64_t)sms * per_sm * d.heads / total;
+    const int64_t even = a->batch * a->tokens / (places > 0 ? places : 1);
     if (tile > even) tile = even;
-    const int64_t fill = (per_cta + d.heads - 1) / d.heads;   // one head a group at least
-    if (tile < fill && toks / fill >= sms / 4) tile = fill;
+    if (tile < d.token_lanes && a->batch * a->tokens >= d.token_lanes * (int64_t)sms / 4)
+      tile = d.token_lanes;
+    if (tile > a->tokens) tile = a->tokens;
     if (tile > most_tile) tile = most_tile;
     if (tile < 1) tile = 1;
     d.tile = (int)tile;
-    d.tiles = (toks + tile - 1) / tile;
-    int64_t most = (int64_t)sms * (bwd ? kBwdBlocksPerSm : kFwdBlocksPerSm) * d.heads / total;
-    if (most < 1) most = 1;
+    d.row_tiles = (a->tokens + tile - 1) / tile;
+    d.tiles = a->batch * d.row_tiles;
+    const int64_t most = places > 0 ? places : 1;
     a->blocks[s] = (int)(d.tiles < most ? d.tiles : most);
   }
   p->grid = a->blocks[0] + a->blocks[1];
@@ -167,10 +169,27 @@ void fill(RopeArgs* a, const Shape& c, const rope_positions* r, float eps, int z
   a->pos = r->pos;
   a->freqs = r->freqs;
   for (int i = 0; i < 3; ++i) a->pos_s[i] = r->stride[i];
+  // Sequences that lie one behind the other in every tensor, and single
+  // tokens, are one sequence.
+  a->batch = c.batch;
   a->tokens = c.tokens;
-  a->units_tokens = c.batch * c.tokens;
-  a->small = c.batch * c.tokens <= INT32_MAX;
-  if (a->small) a->by_tokens.set((unsigned)(c.tokens > 0 ? c.tokens : 1));
+  bool flat = c.tokens == 1 || c.batch == 1 || r->stride[1] == c.tokens * r->stride[2];
+  for (RopeSide& d : a->side)
+    if (d.heads > 0 && c.tokens > 1 && c.batch > 1)
+      flat = flat && d.in_s[0] == c.tokens * d.in_s[1] && d.out_s[0] == c.tokens * d.out_s[1] &&
+             (d.x == nullptr || d.x_s[0] == c.tokens * d.x_s[1]);
+  if (flat && c.batch > 1) {
+    if (c.tokens == 1) {
+      a->pos_s[2] = a->pos_s[1];
+      for (RopeSide& d : a->side) {
+        d.in_s[1] = d.in_s[0];
+        d.out_s[1] = d.out_s[0];
+        d.x_s[1] = d.x_s[0];
+      }
+    }
+    a->tokens = c.batch * c.tokens;
+    a->batch = 1;
+  }
   a->pos64 = r->bits == 64;
   a->axes = (int)r->axes;
   a->dim = (int)c.dim;
@@ -181,7 +200,9 @@ void fill(RopeArgs* a, const Shape& c, const rope_positions* r, float eps, int z
   a->zero_centered = zero_centered ? 1 : 0;
 }
 
-bool strides_ok(const int64_t* s) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
+bool strides_ok(const int64_t* s) {
+  return s[0] >= 0 && s[1] >= 0 && s[2] >= 0;
+}
 
 }  // namespace
 }  // namespace nf
@@ -245,7 +266,7 @@ ln_status rope_fwd(const rope_heads* q, const rope_heads* k, const rope_position
   const size_t es = elem_size(dtype);
   const bool some = batch > 0 && tokens > 0;
   Strided in[2], out[2], all[4];
-  Range small[4];
+  Range small[4] = {};
   RopeArgs a = {};
   for (int i = 0; i < 2; ++i) {
     const rope_heads* h = sides[i];

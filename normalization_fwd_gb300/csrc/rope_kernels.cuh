@@ -12,8 +12,8 @@
 // Angles: a position times a frequency passes fp32's precision at a few
 // thousand radians. A frequency is turned into a 64-bit fraction of a turn,
 // the product with the integer position is taken modulo 2^64, which is
-// modulo one turn exactly, and its top 32 bits go to sincospi. The error is
-// that of the frequency itself times the position, plus 2^-32 turns.
+// modulo one turn exactly, and its top 32 bits give sine and cosine. The error
+// is that of the frequency itself times the position, plus 2^-33 turns.
 #pragma once
 
 #include "common.cuh"
@@ -36,8 +36,11 @@ struct RopeSide {
   void* out;             // y, or dx
   const void* gamma;     // nullable: no norm
   int heads;             // 0: absent
+  int head_lanes;        // heads that a CTA works on at a time
+  int token_lanes;       // tokens, each by head_lanes groups of threads
   int tile;              // tokens of a tile
-  int64_t tiles;         // ceil(all tokens / tile)
+  int64_t row_tiles;     // tiles of a sequence, ceil(tokens / tile)
+  int64_t tiles;         // of all sequences
   int64_t in_s[3], x_s[3], out_s[3];   // strides of batch, token, head (elements)
 };
 
@@ -46,10 +49,7 @@ struct RopeArgs {
   const void* pos;
   const double* freqs;   // [axes][rot / 2] radians a position
   int64_t pos_s[3];      // strides of axis, batch, token (elements)
-  int64_t tokens;        // of a sequence
-  int64_t units_tokens;  // batch * tokens
-  FastDiv by_tokens;     // when batch * tokens is below 2^31 (small)
-  int small;
+  int64_t batch, tokens; // sequences, and the tokens of one
   float* ws;             // backward: [max of blocks][2 * dim] partials, or null
   int blocks[2];         // CTAs of each side, the queries' first
   int pos64, axes;
@@ -141,6 +141,27 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
   else if (sh == 0) t = w1;
   else t = sh > -64 ? (w1 << -sh) | (w0 >> (64 + sh)) : 0;
   return (long long)bits < 0 ? 0ull - t : t;
+}
+
+// Sine and cosine of t 2^-32 turns: the nearest quarter turn, then the Taylor
+// series of the rest, at most pi / 4, to x^9 and x^10 (the next terms are
+// below 2^-29 and 2^-31); about 1 ulp in all.
+__device__ __forceinline__ void sincos_turns(unsigned t, float* sine, float* cosine) {
+  const unsigned q = (t + 0x20000000u) >> 30;
+  const float x = (float)(int)(t - (q << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float z = x * x;
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+  s = fmaf(z, s, 8.3333333e-3f);
+  s = fmaf(z, s, -1.6666667e-1f);
+  s = fmaf(x * z, s, x);
+  float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  c = fmaf(z, c, -1.3888889e-3f);
+  c = fmaf(z, c, 4.1666667e-2f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.f);
+  const float a = q & 1 ? c : s, b = q & 1 ? s : c;
+  *sine = __uint_as_float(__float_as_uint(a) ^ (q & 2) << 30);
+  *cosine = __uint_as_float(__float_as_uint(b) ^ ((q + 1) & 2) << 30);
 }
 
 // Which vectors a head's lane slot s holds. The first `rot` elements make
@@ -255,10 +276,11 @@ __device__ __forceinline__ void rope_table_get(const float* t, float2 (&f)[NP], 
   }
 }
 
-// A CTA takes the queries or the keys of a tile of tokens. It works out the
-// cosines and sines of the tile's tokens once, into shared memory, and goes
-// through the tokens' heads with a group of `lanes` threads a head, a group's
-// next heads always on their way. A CTA takes tile after tile; in the
+// A CTA takes the queries or the keys of a tile of one sequence's tokens. It
+// works out the cosines and sines of those tokens once, into shared memory.
+// A group of `lanes` threads has a head and goes through the tile's tokens
+// with it, so that it steps its pointers and does little else; the next rows
+// of a group are always on their way. A CTA takes tile after tile; in the
 // backward it keeps its share of dgamma in registers. FULL: each lane has a
 // whole slot and all of the head is rotated.
 template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool FULL, bool BWD>
@@ -266,8 +288,6 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   using Raw = RopeRaw<T, VEC, ALIGNED>;
   constexpr int kAhead = BWD ? kRopeAheadBwd : kRopeAheadFwd;
   __shared__ __align__(16) float tab_c[kRopeMaxTable], tab_s[kRopeMaxTable];
-  __shared__ int64_t off_in[kRopeMaxTile], off_out[kRopeMaxTile], off_x[kRopeMaxTile],
-      off_pos[kRopeMaxTile];
   extern __shared__ float red[];
   const int L = A.lanes, per_cta = kRopeThreads / L;
   const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
@@ -275,6 +295,10 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   const int blk = blockIdx.x - (side ? A.blocks[0] : 0), blks = A.blocks[side];
   const RopeSide& S = A.side[side];
   const bool norm = S.gamma != nullptr;
+  const T* const in = static_cast<const T*>(S.in);
+  const T* const xin = static_cast<const T*>(S.x);
+  T* const out = static_cast<T*>(S.out);
+  const int heads = S.heads, tl = grp / S.head_lanes, hl = grp - tl * S.head_lanes;
   RopeSlot slot[NS];
 #pragma unroll
   for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER, FULL>(l + n * L, A.dim, A.rot);
@@ -307,189 +331,174 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   unsigned long long turns = 0;
   if (A.axes == 1 && j < A.rot / 2) turns = turns_of(A.freqs[j]);
 
+  const int64_t in_step = S.token_lanes * S.in_s[1], out_step = S.token_lanes * S.out_s[1],
+                x_step = BWD ? S.token_lanes * S.x_s[1] : 0;
   for (int64_t tile = blk; tile < S.tiles; tile += blks) {
-    const int64_t tok0 = tile * S.tile;
-    const int toks = (int)min((int64_t)S.tile, A.units_tokens - tok0);
-    __syncthreads();   // the last tile's table gives way
-    if (threadIdx.x < toks) {
-      const int64_t tok = tok0 + threadIdx.x;
-      const int64_t b = A.small ? A.by_tokens.div((int)tok) : tok / A.tokens;
-      const int64_t k = tok - b * A.tokens;
-      off_in[threadIdx.x] = b * S.in_s[0] + k * S.in_s[1];
-      off_out[threadIdx.x] = b * S.out_s[0] + k * S.out_s[1];
-      if (BWD) off_x[threadIdx.x] = b * S.x_s[0] + k * S.x_s[1];
-      off_pos[threadIdx.x] = b * A.pos_s[1] + k * A.pos_s[2];
-    }
-    __syncthreads();
-
-    // Heads of the tile in order, dealt to the groups. Whole warps run the
-    // loop, so that every lane reaches the shuffles.
-    const int items = toks * S.heads;
-    const int steps = (items + per_cta - 1) / per_cta;
-    Raw v0[kAhead][NS][2], x0[BWD ? kAhead : 1][NS][2];
-    int ft = 0, fh = grp;       // token and head of the next item to fetch
-    const auto settle = [&](int& t, int& h) {
-      while (h >= S.heads && t < toks) {
-        h -= S.heads;
-        ++t;
-      }
-    };
-    settle(ft, fh);
-    const auto fetch = [&](Raw (&v)[NS][2], Raw (&x)[NS][2]) {
-      const bool have = ft < toks;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        if (have && slot[n].on) {
-          const T* p = static_cast<const T*>(S.in) + off_in[ft] + (int64_t)fh * S.in_s[2];
-          v[n][0].load(p + slot[n].a);
-          if (slot[n].on_b) v[n][1].load(p + slot[n].b);
-          if (BWD && norm) {
-            const T* q = static_cast<const T*>(S.x) + off_x[ft] + (int64_t)fh * S.x_s[2];
-            x[n][0].load(q + slot[n].a);
-            if (slot[n].on_b) x[n][1].load(q + slot[n].b);
-          }
-        }
-      }
-      fh += per_cta;
-      settle(ft, fh);
-    };
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          v0[d][n][k].clear();
-          if (BWD) x0[d][n][k].clear();
-        }
-      fetch(v0[d], x0[BWD ? d : 0]);
-    }
-    // The angles, while the first heads are on their way.
-    if (j < A.rot / 2)
-      for (int t = threadIdx.x / A.wide; t < toks; t += kRopeThreads / A.wide) {
-        unsigned long long sum = 0;
-        for (int ax = 0; ax < A.axes; ++ax) {
-          const int64_t at = ax * A.pos_s[0] + off_pos[t];
-          const int64_t p = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
-                                    : (int64_t)static_cast<const int*>(A.pos)[at];
-          if (A.axes > 1) turns = turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
-          sum += (unsigned long long)p * turns;
-        }
-        const int top = (int)((sum + 0x80000000ull) >> 32);   // signed 2^-32 turns
-        float s, c;
-        sincospif((float)top * 0x1p-31f, &s, &c);
-        tab_c[t * A.row + j] = c * A.scale;
-        tab_s[t * A.row + j] = s * A.scale;
-      }
-    __syncthreads();
-
-    int t = 0, h = grp;
-    settle(t, h);
-    for (int st = 0; st < steps; st += kAhead) {
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        const bool act = t < toks;
-        float2 v[NS][2][NP], cs[NS][NP], sn[NS][NP], sum = splat2(0.f);
+    const int64_t b = tile / S.row_tiles, tok0 = (tile - b * S.row_tiles) * S.tile;
+    const int toks = (int)min((int64_t)S.tile, A.tokens - tok0);
+    // Whole warps run the loops below, so that every lane reaches the shuffles.
+    const int steps = (toks + S.token_lanes - 1) / S.token_lanes;
+    const int mine = tl < S.token_lanes && toks > tl ? (toks - tl - 1) / S.token_lanes + 1 : 0;
+    for (int h0 = 0; h0 < heads; h0 += S.head_lanes) {
+      const int h = h0 + hl, n_rows = h < heads ? mine : 0;
+      const T* p = in + b * S.in_s[0] + (tok0 + tl) * S.in_s[1] + h * S.in_s[2];
+      const T* q = BWD ? xin + b * S.x_s[0] + (tok0 + tl) * S.x_s[1] + h * S.x_s[2] : nullptr;
+      T* dst = out + b * S.out_s[0] + (tok0 + tl) * S.out_s[1] + h * S.out_s[2];
+      Raw v0[kAhead][NS][2], x0[BWD ? kAhead : 1][NS][2];
+      const auto fetch = [&](int d, int r) {   // row r of the group
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          v0[d][n][0].get(v[n][0]);
-          v0[d][n][1].get(v[n][1]);
-          const float* tc = tab_c + (act ? t : 0) * A.row;
-          const float* ts = tab_s + (act ? t : 0) * A.row;
-          if constexpr (INTER) {
-            constexpr int H = VEC / 2;
-            const int b = slot[n].on_b ? slot[n].b / 2 : 0;
-            if constexpr (H == 1) {
-              cs[n][0] = make_float2(tc[slot[n].a / 2], tc[b]);
-              sn[n][0] = make_float2(ts[slot[n].a / 2], ts[b]);
+          if (r < n_rows && slot[n].on) {
+            v0[d][n][0].load(p + slot[n].a);
+            if (slot[n].on_b) v0[d][n][1].load(p + slot[n].b);
+            if (BWD && norm) {
+              x0[d][n][0].load(q + slot[n].a);
+              if (slot[n].on_b) x0[d][n][1].load(q + slot[n].b);
+            }
+          }
+        }
+        p += in_step;
+        if (BWD) q += x_step;
+      };
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            v0[d][n][k].clear();
+            if (BWD) x0[d][n][k].clear();
+          }
+        fetch(d, d);
+      }
+      if (h0 == 0) {
+        // The angles, while the first rows are on their way.
+        __syncthreads();   // the last tile's table gives way
+        if (j < A.rot / 2)
+          for (int t = threadIdx.x / A.wide; t < toks; t += kRopeThreads / A.wide) {
+            unsigned long long sum = 0;
+            for (int ax = 0; ax < A.axes; ++ax) {
+              const int64_t at = ax * A.pos_s[0] + b * A.pos_s[1] + (tok0 + t) * A.pos_s[2];
+              const int64_t pos = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
+                                          : (int64_t)static_cast<const int*>(A.pos)[at];
+              if (A.axes > 1) turns = turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
+              sum += (unsigned long long)pos * turns;
+            }
+            float s, c;
+            sincos_turns((unsigned)((sum + 0x80000000ull) >> 32), &s, &c);
+            tab_c[t * A.row + j] = c * A.scale;
+            tab_s[t * A.row + j] = s * A.scale;
+          }
+        __syncthreads();
+      }
+      const float* tc = tab_c + tl * A.row;
+      const float* ts = tab_s + tl * A.row;
+      for (int st = 0; st < steps; st += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const bool act = st + d < n_rows;
+          float2 v[NS][2][NP], cs[NS][NP], sn[NS][NP], sum = splat2(0.f);
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+            v0[d][n][0].get(v[n][0]);
+            v0[d][n][1].get(v[n][1]);
+            if constexpr (INTER) {
+              constexpr int H = VEC / 2;
+              const int sb = slot[n].on_b ? slot[n].b / 2 : 0;
+              if constexpr (H == 1) {
+                cs[n][0] = make_float2(tc[slot[n].a / 2], tc[sb]);
+                sn[n][0] = make_float2(ts[slot[n].a / 2], ts[sb]);
+              } else {
+                rope_table_get<H>(tc + slot[n].a / 2, cs[n], 0);
+                rope_table_get<H>(ts + slot[n].a / 2, sn[n], 0);
+                rope_table_get<H>(tc + sb, cs[n], H / 2);
+                rope_table_get<H>(ts + sb, sn[n], H / 2);
+              }
             } else {
-              rope_table_get<H>(tc + slot[n].a / 2, cs[n], 0);
-              rope_table_get<H>(ts + slot[n].a / 2, sn[n], 0);
-              rope_table_get<H>(tc + b, cs[n], H / 2);
-              rope_table_get<H>(ts + b, sn[n], H / 2);
+              const int at = slot[n].turned ? slot[n].a : 0;
+              rope_table_get<VEC>(tc + at, cs[n], 0);
+              rope_table_get<VEC>(ts + at, sn[n], 0);
             }
+          }
+          if (!BWD) {
+            fetch(d, st + d + kAhead);
+            if (norm) {
+#pragma unroll
+              for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) sum = fma2(v[n][k][i], v[n][k][i], sum);
+              const float ss = lanes_sum(sum.x + sum.y, L);
+              const float2 rstd = splat2(rsqrtf(fmaf(ss, A.inv_dim, A.eps)));
+#pragma unroll
+              for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) v[n][k][i] = mul2(mul2(v[n][k][i], rstd), w[n][k][i]);
+            }
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+              rope_rotate<VEC, INTER, false>(v[n], cs[n], sn[n], slot[n].turned);
           } else {
-            const int at = slot[n].turned ? slot[n].a : 0;
-            rope_table_get<VEC>(tc + at, cs[n], 0);
-            rope_table_get<VEC>(ts + at, sn[n], 0);
-          }
-        }
-        if (!BWD) {
-          fetch(v0[d], x0[0]);
-          if (norm) {
+            float2 xv[NS][2][NP];
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) sum = fma2(v[n][k][i], v[n][k][i], sum);
-            const float ss = lanes_sum(sum.x + sum.y, L);
-            const float2 rstd = splat2(rsqrtf(fmaf(ss, A.inv_dim, A.eps)));
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) v[n][k][i] = mul2(mul2(v[n][k][i], rstd), w[n][k][i]);
-          }
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-            rope_rotate<VEC, INTER, false>(v[n], cs[n], sn[n], slot[n].turned);
-        } else {
-          float2 xv[NS][2][NP];
-#pragma unroll
-          for (int n = 0; n < NS; ++n) {
-            x0[d][n][0].get(xv[n][0]);
-            x0[d][n][1].get(xv[n][1]);
-          }
-          fetch(v0[d], x0[d]);
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-            rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
-          if (norm) {
-            float2 dot = splat2(0.f);
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                  sum = fma2(xv[n][k][i], xv[n][k][i], sum);
-                  dot = fma2(mul2(v[n][k][i], w[n][k][i]), xv[n][k][i], dot);
-                }
-            // sum g xhat = rstd sum g x, so one round of shuffles serves both
-            const float ss = lanes_sum(sum.x + sum.y, L), gs = lanes_sum(dot.x + dot.y, L);
-            const float rstd = rsqrtf(fmaf(ss, A.inv_dim, A.eps));
-            const float2 rs = splat2(rstd), mean = splat2(-gs * rstd * A.inv_dim);
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                  const float2 xh = mul2(xv[n][k][i], rs);
-                  if (act) acc[n][k][i] = fma2(v[n][k][i], xh, acc[n][k][i]);
-                  v[n][k][i] = mul2(rs, fma2(xh, mean, mul2(v[n][k][i], w[n][k][i])));
-                }
-          }
-        }
-        if (act) {
-          T* out = static_cast<T*>(S.out) + off_out[t] + (int64_t)h * S.out_s[2];
-#pragma unroll
-          for (int n = 0; n < NS; ++n) {
-            Raw r;
-            if (slot[n].on) {
-              r.set(v[n][0]);
-              r.store(out + slot[n].a);
+            for (int n = 0; n < NS; ++n) {
+              x0[d][n][0].get(xv[n][0]);
+              x0[d][n][1].get(xv[n][1]);
             }
-            if (slot[n].on_b) {
-              r.set(v[n][1]);
-              r.store(out + slot[n].b);
+            fetch(d, st + d + kAhead);
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+              rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
+            if (norm) {
+              float2 dot = splat2(0.f);
+#pragma unroll
+              for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) {
+                    sum = fma2(xv[n][k][i], xv[n][k][i], sum);
+                    dot = fma2(mul2(v[n][k][i], w[n][k][i]), xv[n][k][i], dot);
+                  }
+              // sum g xhat = rstd sum g x, so one round of shuffles serves both
+              const float ss = lanes_sum(sum.x + sum.y, L), gs = lanes_sum(dot.x + dot.y, L);
+              const float rstd = rsqrtf(fmaf(ss, A.inv_dim, A.eps));
+              const float2 rs = splat2(rstd), mean = splat2(-gs * rstd * A.inv_dim);
+#pragma unroll
+              for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) {
+                    const float2 xh = mul2(xv[n][k][i], rs);
+                    if (act) acc[n][k][i] = fma2(v[n][k][i], xh, acc[n][k][i]);
+                    v[n][k][i] = mul2(rs, fma2(xh, mean, mul2(v[n][k][i], w[n][k][i])));
+                  }
             }
           }
+          if (act) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+              Raw r;
+              if (slot[n].on) {
+                r.set(v[n][0]);
+                r.store(dst + slot[n].a);
+              }
+              if (slot[n].on_b) {
+                r.set(v[n][1]);
+                r.store(dst + slot[n].b);
+              }
+            }
+          }
+          dst += out_step;
+          if (st + d + 1 < n_rows) {   // stay inside the table behind the last row
+            tc += S.token_lanes * A.row;
+            ts += S.token_lanes * A.row;
+          }
         }
-        h += per_cta;
-        settle(t, h);
       }
     }
   }
