@@ -153,11 +153,20 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
       tile = d.token_lanes;
     if (tile > a->tokens) tile = a->tokens;
     if (tile > most_tile) tile = most_tile;
+    if (bwd && tile > d.token_lanes && places > 0) {
+      // Whole rounds of the CTAs that there are places for.
+      const int64_t rows = a->batch * a->tokens, rounds_of = (rows + places * tile - 1) / (places * tile);
+      const int64_t need = (rows + places * rounds_of - 1) / (places * rounds_of);
+      const int64_t even_tile = (need + d.token_lanes - 1) / d.token_lanes * d.token_lanes;
+      if (even_tile < tile) tile = even_tile;
+    }
     if (tile < 1) tile = 1;
     d.tile = (int)tile;
     d.row_tiles = (a->tokens + tile - 1) / tile;
     d.tiles = a->batch * d.row_tiles;
-    const int64_t most = places > 0 ? places : 1;
+    // Forward: a CTA a tile, so that the device deals them out; backward: no
+    // more than a CTA for each place, which leave a row of partials each.
+    const int64_t most = !bwd ? 1 << 30 : places > 0 ? places : 1;
     a->blocks[s] = (int)(d.tiles < most ? d.tiles : most);
   }
   p->grid = a->blocks[0] + a->blocks[1];

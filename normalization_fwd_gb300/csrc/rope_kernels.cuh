@@ -293,57 +293,59 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
   const int side = (int)blockIdx.x >= A.blocks[0] ? 1 : 0;
   const int blk = blockIdx.x - (side ? A.blocks[0] : 0), blks = A.blocks[side];
-  const RopeSide& S = A.side[side];
-  const bool norm = S.gamma != nullptr;
-  const T* const in = static_cast<const T*>(S.in);
-  const T* const xin = static_cast<const T*>(S.x);
-  T* const out = static_cast<T*>(S.out);
-  const int heads = S.heads, tl = grp / S.head_lanes, hl = grp - tl * S.head_lanes;
+  const RopeSide &q0 = A.side[0], &k0 = A.side[1];
+  // Taken once: a side indexed at run time would be read anew at every use.
+#define NF_SIDE(field) (side ? k0.field : q0.field)
+  const bool norm = NF_SIDE(gamma) != nullptr;
+  const T* const in = static_cast<const T*>(NF_SIDE(in));
+  const T* const xin = static_cast<const T*>(NF_SIDE(x));
+  T* const out = static_cast<T*>(NF_SIDE(out));
+  const int heads = NF_SIDE(heads), head_lanes = NF_SIDE(head_lanes);
+  const int token_lanes = NF_SIDE(token_lanes), tile_rows = NF_SIDE(tile);
+  const int64_t row_tiles = NF_SIDE(row_tiles), tiles = NF_SIDE(tiles);
+  const int64_t in_b = NF_SIDE(in_s[0]), in_t = NF_SIDE(in_s[1]), in_h = NF_SIDE(in_s[2]);
+  const int64_t out_b = NF_SIDE(out_s[0]), out_t = NF_SIDE(out_s[1]), out_h = NF_SIDE(out_s[2]);
+  const int64_t x_b = BWD ? NF_SIDE(x_s[0]) : 0, x_t = BWD ? NF_SIDE(x_s[1]) : 0,
+                x_h = BWD ? NF_SIDE(x_s[2]) : 0;
+  const T* const gm = static_cast<const T*>(NF_SIDE(gamma));
+#undef NF_SIDE
+  const int tl = grp / head_lanes, hl = grp - tl * head_lanes;
   RopeSlot slot[NS];
 #pragma unroll
   for (int n = 0; n < NS; ++n) slot[n] = rope_slot<VEC, INTER, FULL>(l + n * L, A.dim, A.rot);
   constexpr int NP = (VEC + 1) / 2;
-  float2 w[NS][2][NP], acc[NS][2][NP];
+  RopeRaw<T, VEC, false> gamma[NS][2];   // as it is in memory, to save registers
+  float2 acc[BWD ? NS : 1][2][NP];
+  const float2 add = splat2(A.zero_centered ? 1.f : 0.f);
 #pragma unroll
   for (int n = 0; n < NS; ++n)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      w[n][0][i] = w[n][1][i] = splat2(1.f);
-      acc[n][0][i] = acc[n][1][i] = splat2(0.f);
-    }
-  if (norm) {
-    const T* gm = static_cast<const T*>(S.gamma);
-    const float2 add = splat2(A.zero_centered ? 1.f : 0.f);
+    for (int k = 0; k < 2; ++k) {
+      gamma[n][k].clear();
+      if (norm && (k == 0 ? slot[n].on : slot[n].on_b))
+        gamma[n][k].load(gm + (k == 0 ? slot[n].a : slot[n].b));
+      if (BWD) {
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        RopeRaw<T, VEC, false> g;   // gamma's own alignment is not asked for
-        g.clear();
-        if (k == 0 ? slot[n].on : slot[n].on_b) g.load(gm + (k == 0 ? slot[n].a : slot[n].b));
-        g.get(w[n][k]);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) w[n][k][i] = add2(w[n][k][i], add);
+        for (int i = 0; i < NP; ++i) acc[n][k][i] = splat2(0.f);
       }
     }
-  }
   const int j = threadIdx.x & (A.wide - 1);      // this thread's pair
   unsigned long long turns = 0;
   if (A.axes == 1 && j < A.rot / 2) turns = turns_of(A.freqs[j]);
 
-  const int64_t in_step = S.token_lanes * S.in_s[1], out_step = S.token_lanes * S.out_s[1],
-                x_step = BWD ? S.token_lanes * S.x_s[1] : 0;
-  for (int64_t tile = blk; tile < S.tiles; tile += blks) {
-    const int64_t b = tile / S.row_tiles, tok0 = (tile - b * S.row_tiles) * S.tile;
-    const int toks = (int)min((int64_t)S.tile, A.tokens - tok0);
+  const int64_t in_step = token_lanes * in_t, out_step = token_lanes * out_t,
+                x_step = token_lanes * x_t;
+  for (int64_t tile = blk; tile < tiles; tile += blks) {
+    const int64_t b = tile / row_tiles, tok0 = (tile - b * row_tiles) * tile_rows;
+    const int toks = (int)min((int64_t)tile_rows, A.tokens - tok0);
     // Whole warps run the loops below, so that every lane reaches the shuffles.
-    const int steps = (toks + S.token_lanes - 1) / S.token_lanes;
-    const int mine = tl < S.token_lanes && toks > tl ? (toks - tl - 1) / S.token_lanes + 1 : 0;
-    for (int h0 = 0; h0 < heads; h0 += S.head_lanes) {
+    const int steps = (toks + token_lanes - 1) / token_lanes;
+    const int mine = tl < token_lanes && toks > tl ? (toks - tl - 1) / token_lanes + 1 : 0;
+    for (int h0 = 0; h0 < heads; h0 += head_lanes) {
       const int h = h0 + hl, n_rows = h < heads ? mine : 0;
-      const T* p = in + b * S.in_s[0] + (tok0 + tl) * S.in_s[1] + h * S.in_s[2];
-      const T* q = BWD ? xin + b * S.x_s[0] + (tok0 + tl) * S.x_s[1] + h * S.x_s[2] : nullptr;
-      T* dst = out + b * S.out_s[0] + (tok0 + tl) * S.out_s[1] + h * S.out_s[2];
+      const T* p = in + b * in_b + (tok0 + tl) * in_t + h * in_h;
+      const T* q = BWD ? xin + b * x_b + (tok0 + tl) * x_t + h * x_h : nullptr;
+      T* dst = out + b * out_b + (tok0 + tl) * out_t + h * out_h;
       Raw v0[kAhead][NS][2], x0[BWD ? kAhead : 1][NS][2];
       const auto fetch = [&](int d, int r) {   // row r of the group
 #pragma unroll
@@ -434,9 +436,13 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
 #pragma unroll
               for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < 2; ++k) {
+                  float2 w[NP];
+                  gamma[n][k].get(w);
 #pragma unroll
-                  for (int i = 0; i < NP; ++i) v[n][k][i] = mul2(mul2(v[n][k][i], rstd), w[n][k][i]);
+                  for (int i = 0; i < NP; ++i)
+                    v[n][k][i] = mul2(mul2(v[n][k][i], rstd), add2(w[i], add));
+                }
             }
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -453,16 +459,22 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
             for (int n = 0; n < NS; ++n)
               rope_rotate<VEC, INTER, true>(v[n], cs[n], sn[n], slot[n].turned);
             if (norm) {
-              float2 dot = splat2(0.f);
+              float2 dot = splat2(0.f), vx[NS][2][NP];   // g' x, then v = g
 #pragma unroll
               for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < 2; ++k) {
+                  float2 w[NP];
+                  gamma[n][k].get(w);
 #pragma unroll
                   for (int i = 0; i < NP; ++i) {
+                    w[i] = add2(w[i], add);
                     sum = fma2(xv[n][k][i], xv[n][k][i], sum);
-                    dot = fma2(mul2(v[n][k][i], w[n][k][i]), xv[n][k][i], dot);
+                    vx[n][k][i] = mul2(v[n][k][i], xv[n][k][i]);
+                    dot = fma2(vx[n][k][i], w[i], dot);
+                    v[n][k][i] = mul2(v[n][k][i], w[i]);
                   }
+                }
               // sum g xhat = rstd sum g x, so one round of shuffles serves both
               const float ss = lanes_sum(sum.x + sum.y, L), gs = lanes_sum(dot.x + dot.y, L);
               const float rstd = rsqrtf(fmaf(ss, A.inv_dim, A.eps));
@@ -473,9 +485,8 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                   for (int i = 0; i < NP; ++i) {
-                    const float2 xh = mul2(xv[n][k][i], rs);
-                    if (act) acc[n][k][i] = fma2(v[n][k][i], xh, acc[n][k][i]);
-                    v[n][k][i] = mul2(rs, fma2(xh, mean, mul2(v[n][k][i], w[n][k][i])));
+                    if (act) acc[n][k][i] = fma2(vx[n][k][i], rs, acc[n][k][i]);
+                    v[n][k][i] = mul2(rs, fma2(mul2(xv[n][k][i], rs), mean, v[n][k][i]));
                   }
             }
           }
@@ -495,8 +506,8 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
           }
           dst += out_step;
           if (st + d + 1 < n_rows) {   // stay inside the table behind the last row
-            tc += S.token_lanes * A.row;
-            ts += S.token_lanes * A.row;
+            tc += token_lanes * A.row;
+            ts += token_lanes * A.row;
           }
         }
       }
