@@ -12,7 +12,9 @@ PyTorch is used for device memory and streams only.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -481,51 +483,46 @@ def fused_norm_bwd(dy, x_sum, gamma, mean, rstd, *, mode="layernorm", zero_cente
 # stream that they launch on, so that a buffer of theirs is not handed out again
 # while the launch is using it.
 
-def _on_device(where: str, first, *others) -> torch.device:
-    """The CUDA device that all given tensors live on."""
-    for t in (first, *others):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{where}: expected a torch.Tensor or None, got {type(t).__name__}")
-        if not t.is_cuda:
-            raise ValueError(f"{where}: tensors passed to the CUDA library must live on a CUDA "
-                             "device")
-        if t.device != first.device:
-            raise ValueError(f"{where}: tensors on {first.device} and {t.device}")
-    return first.device
+def _device_of(where: str, first, *others) -> int:
+    """Number of the CUDA device that all given tensors live on."""
+    try:
+        device = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != device:
+                raise ValueError(f"{where}: tensors on {first.device} and {t.device}")
+    except AttributeError:
+        for t in (first, *others):
+            if t is not None and not isinstance(t, torch.Tensor):
+                raise TypeError(f"{where}: expected a torch.Tensor or None, got "
+                                f"{type(t).__name__}") from None
+        raise
+    if device < 0:
+        raise ValueError(f"{where}: tensors passed to the CUDA library must live on a CUDA device")
+    return device
 
 
-class _Launch:
-    """Makes ``device`` and ``stream`` (None: torch's current stream of that
-    device) current, where they are not, and gives the raw stream."""
+def _elsewhere(device: int, stream) -> bool:
+    """Whether a call has to make its device or stream current first."""
+    return stream is not None or device != torch.cuda.current_device()
 
-    __slots__ = ("raw", "_guards")
 
-    def __init__(self, device, stream):
-        self._guards = ()
-        if device.index != torch.cuda.current_device():
-            self._guards = (torch.cuda.device(device),)
+@contextlib.contextmanager
+def _current(device: int, stream):
+    """Make ``device`` and ``stream`` (a torch stream, a raw one or None)
+    current, so that what the call allocates belongs to the stream that it
+    launches on."""
+    with torch.cuda.device(device):
         if stream is None:
-            self.raw = torch.cuda.current_stream(device).cuda_stream
+            yield
             return
         if not isinstance(stream, torch.cuda.Stream):
             # 0 is the legacy default stream, torch's own default
-            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
-                      else torch.cuda.default_stream(device))
-        if stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        self.raw = stream.cuda_stream
-        self._guards += (torch.cuda.stream(stream),)
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+            stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
+                      else torch.cuda.default_stream())
+        if stream.device.index != device:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{device}")
+        with torch.cuda.stream(stream):
+            yield
 
 
 def _dense_last(t, name):
@@ -535,10 +532,12 @@ def _dense_last(t, name):
 
 def _rows_of(t, name):
     """(samples, rows, channels, sample stride, row stride) of [N, ..., C]."""
-    if t.dim() < 2:
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 2:
         raise ValueError(f"{name}: expected [samples, ..., channels]")
     _dense_last(t, name)
-    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        return shape[0], shape[1], shape[2], stride[0], stride[1] if shape[1] > 1 else 0
     rows, row = 1, 0
     for n, s in zip(shape[-2:0:-1], stride[-2:0:-1]):
         if n == 1:
@@ -604,15 +603,31 @@ def gn_workspace_bytes(samples, rows, channels, groups, dtype, backward=False) -
     return int(out.value)
 
 
+# The answer depends on the shape and the device alone.
+@functools.lru_cache(maxsize=4096)
+def _gn_need(device, samples, rows, channels, groups, dtype, backward):
+    return gn_workspace_bytes(samples, rows, channels, groups, dtype, backward)
+
+
+@functools.lru_cache(maxsize=4096)
+def _rope_need(device, head_dim):
+    return rope_bwd_workspace_bytes(head_dim)
+
+
 def _workspace(workspace, need, device):
+    """(tensor to hold on to, address, bytes) of a call's workspace of `need`
+    bytes: the caller's, or one for this call."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     if isinstance(workspace, Workspace):
         workspace = workspace.take(need)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace is None or not workspace.numel():
+    if not workspace.numel():
         return None, None, 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -626,27 +641,25 @@ def gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean
     ``Workspace`` (one is allocated for the call when None). See ``gn_fwd`` in
     include/normfuse.h.
     """
+    device = _device_of("gn_fwd", x, gamma, beta, y, mean, rstd)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean,
+                          rstd, workspace=workspace)
     lib = _lib or load_library()
-    device = _on_device("gn_fwd", x, gamma, beta, y, mean, rstd)
     dt = _dtype(x)
     N, R, C, xs, xr = _rows_of(x, "gn_fwd: x")
     _same("gn_fwd", "y", y, x)
     _, _, _, ys, yr = _rows_of(y, "gn_fwd: y")
     ps = _affines("gn_fwd", gamma, beta, N, C, x.dtype)
     _check_stats("gn_fwd", mean, rstd, N, groups, True)
-    act = _activation(activation)
-    with _Launch(device, stream) as raw:
-        if workspace is None or isinstance(workspace, Workspace):
-            need = gn_workspace_bytes(N, R, C, groups, dt)
-        else:
-            need = 0
-        _held, ws, ws_bytes = _workspace(workspace, need, device)
-        st = lib.gn_fwd(x.data_ptr() or None, xs, xr, None if gamma is None else gamma.data_ptr(),
-                        None if beta is None else beta.data_ptr(), ps, eps, act,
-                        1 if zero_centered_gamma else 0, y.data_ptr() or None, ys, yr,
-                        None if mean is None else mean.data_ptr(),
-                        None if rstd is None else rstd.data_ptr(), raw or None, N, R, C, groups,
-                        dt, ws, ws_bytes)
+    held, ws, ws_bytes = _workspace(workspace, _gn_need(device, N, R, C, groups, dt, False), device)
+    st = lib.gn_fwd(x.data_ptr() or None, xs, xr, None if gamma is None else gamma.data_ptr(),
+                    None if beta is None else beta.data_ptr(), ps, eps, _activation(activation),
+                    1 if zero_centered_gamma else 0, y.data_ptr() or None, ys, yr,
+                    None if mean is None else mean.data_ptr(),
+                    None if rstd is None else rstd.data_ptr(), _stream(None), N, R, C, groups, dt,
+                    ws, ws_bytes)
     if st:
         raise NormError(st, "gn_fwd")
 
@@ -656,8 +669,12 @@ def gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rs
     """Enqueue the backward of ``gn_fwd``: dx, and dgamma and dbeta (contiguous,
     the shape of gamma, one dtype of float32, bfloat16 or float16; may be
     None). See ``gn_bwd`` in include/normfuse.h."""
+    device = _device_of("gn_bwd", x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd,
+                          dx, dgamma, dbeta, workspace=workspace)
     lib = _lib or load_library()
-    device = _on_device("gn_bwd", x, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta)
     dt = _dtype(x)
     N, R, C, xs, xr = _rows_of(x, "gn_bwd: x")
     _same("gn_bwd", "dy", dy, x)
@@ -672,22 +689,15 @@ def gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rs
                 or g.dtype != grads[0].dtype):
             raise ValueError("gn_bwd: dgamma and dbeta must be contiguous, of the shape of gamma "
                              "and of one dtype")
-    gdt = _dtype(grads[0]) if grads else LN_F32
-    act = _activation(activation)
-    with _Launch(device, stream) as raw:
-        if workspace is None or isinstance(workspace, Workspace):
-            need = gn_workspace_bytes(N, R, C, groups, dt, True)
-        else:
-            need = 0
-        _held, ws, ws_bytes = _workspace(workspace, need, device)
-        st = lib.gn_bwd(dy.data_ptr() or None, ds, dr, x.data_ptr() or None, xs, xr,
-                        None if gamma is None else gamma.data_ptr(),
-                        None if beta is None else beta.data_ptr(), ps, act,
-                        1 if zero_centered_gamma else 0, mean.data_ptr() or None,
-                        rstd.data_ptr() or None, dx.data_ptr() or None, os_, or_,
-                        None if dgamma is None else dgamma.data_ptr(),
-                        None if dbeta is None else dbeta.data_ptr(), raw or None, N, R, C, groups,
-                        dt, gdt, ws, ws_bytes)
+    held, ws, ws_bytes = _workspace(workspace, _gn_need(device, N, R, C, groups, dt, True), device)
+    st = lib.gn_bwd(dy.data_ptr() or None, ds, dr, x.data_ptr() or None, xs, xr,
+                    None if gamma is None else gamma.data_ptr(),
+                    None if beta is None else beta.data_ptr(), ps, _activation(activation),
+                    1 if zero_centered_gamma else 0, mean.data_ptr() or None,
+                    rstd.data_ptr() or None, dx.data_ptr() or None, os_, or_,
+                    None if dgamma is None else dgamma.data_ptr(),
+                    None if dbeta is None else dbeta.data_ptr(), _stream(None), N, R, C, groups,
+                    dt, _dtype(grads[0]) if grads else LN_F32, ws, ws_bytes)
     if st:
         raise NormError(st, "gn_bwd")
 
@@ -703,12 +713,17 @@ def fused_group_norm_fwd(x, groups, gamma=None, beta=None, *, eps=1e-5, activati
     shift of each sample. ``x`` and ``out`` may be slices of the channels of
     wider tensors.
     """
-    device = _on_device("fused_group_norm_fwd", x)
-    with _Launch(device, stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
-        mean, rstd = torch.empty((2, x.shape[0], groups), dtype=torch.float32, device=device)
-        gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
-               None, workspace=workspace)
+    device = _device_of("fused_group_norm_fwd", x)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return fused_group_norm_fwd(x, groups, gamma, beta, eps=eps, activation=activation,
+                                        zero_centered_gamma=zero_centered_gamma, out=out,
+                                        workspace=workspace)
+    y = torch.empty_like(x) if out is None else out
+    mean = torch.empty((x.shape[0], groups), dtype=torch.float32, device=device)
+    rstd = torch.empty_like(mean)
+    gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
+           workspace=workspace)
     return {"y": y, "mean": mean, "rstd": rstd}
 
 
@@ -718,16 +733,18 @@ def fused_group_norm_bwd(dy, x, groups, gamma, beta, mean, rstd, *, activation="
     """The backward of ``fused_group_norm_fwd`` from its x and statistics;
     returns a dict with ``dx``, ``dgamma`` and ``dbeta`` (None where gamma or
     beta is None)."""
-    device = _on_device("fused_group_norm_bwd", x)
-    with _Launch(device, stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
-        dgamma = dbeta = None
-        if gamma is not None:
-            dgamma = torch.empty(gamma.shape, dtype=grad_dtype, device=device)
-        if beta is not None:
-            dbeta = torch.empty(beta.shape, dtype=grad_dtype, device=device)
-        gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx, dgamma,
-               dbeta, None, workspace=workspace)
+    device = _device_of("fused_group_norm_bwd", x)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return fused_group_norm_bwd(dy, x, groups, gamma, beta, mean, rstd,
+                                        activation=activation,
+                                        zero_centered_gamma=zero_centered_gamma,
+                                        grad_dtype=grad_dtype, workspace=workspace)
+    dx = torch.empty_like(x)
+    dgamma = None if gamma is None else torch.empty(gamma.shape, dtype=grad_dtype, device=device)
+    dbeta = None if beta is None else torch.empty(beta.shape, dtype=grad_dtype, device=device)
+    gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx, dgamma,
+           dbeta, workspace=workspace)
     return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
@@ -822,8 +839,12 @@ def rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
     RMSNorm of each head where its gamma is given. Tensors are
     [batch, tokens, heads, dim] or [tokens, heads, dim] of any strides; an
     output may be its input. See ``rope_fwd`` in include/normfuse.h."""
+    device = _device_of("rope_fwd", q, k, positions, freqs, q_gamma, k_gamma, out_q, out_k)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+                            interleaved, scale, out_q, out_k)
     lib = _lib or load_library()
-    device = _on_device("rope_fwd", q, k, positions, freqs, q_gamma, k_gamma, out_q, out_k)
     shape, xs = _heads(q, "rope_fwd: q")
     _, ys = _heads(out_q, "rope_fwd: out_q", q)
     D = shape[3]
@@ -839,9 +860,8 @@ def rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
                               _gamma_ptr(k_gamma, "rope_fwd: k_gamma", D, q.dtype), kshape[2], *xs,
                               *ys)
     pos = _positions("rope_fwd", positions, freqs, interleaved, scale, shape, q.dim())
-    with _Launch(device, stream) as raw:
-        st = lib.rope_fwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, raw or None, shape[0],
-                          shape[1], D, _dtype(q))
+    st = lib.rope_fwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, _stream(None), shape[0],
+                      shape[1], D, _dtype(q))
     if st:
         raise NormError(st, "rope_fwd")
 
@@ -863,9 +883,14 @@ def rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centere
     of its outputs, ``out_dq`` and ``out_dk`` those of its inputs (an output
     may be its gradient). q and k are needed with a gamma only; dq_gamma and
     dk_gamma ([dim], one dtype) may be None."""
-    lib = _lib or load_library()
-    device = _on_device("rope_bwd", dq, dk, q, k, positions, freqs, q_gamma, k_gamma, out_dq,
+    device = _device_of("rope_bwd", dq, dk, q, k, positions, freqs, q_gamma, k_gamma, out_dq,
                         out_dk, dq_gamma, dk_gamma)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps,
+                            zero_centered_gamma, interleaved, scale, out_dq, out_dk, dq_gamma,
+                            dk_gamma, workspace=workspace)
+    lib = _lib or load_library()
     shape, _ = _heads(dq, "rope_bwd: dq")
     D = shape[3]
     grads = [g for g in (dq_gamma, dk_gamma) if g is not None]
@@ -895,13 +920,9 @@ def rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centere
     qs = side(dq, q, q_gamma, out_dq, dq_gamma, "q")
     ks = side(dk, k, k_gamma, out_dk, dk_gamma, "k")
     pos = _positions("rope_bwd", positions, freqs, interleaved, scale, shape, dq.dim())
-    with _Launch(device, stream) as raw:
-        need = rope_bwd_workspace_bytes(D) if grads and (
-            workspace is None or isinstance(workspace, Workspace)) else 0
-        _held, ws, ws_bytes = _workspace(workspace, need, device)
-        st = lib.rope_bwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, raw or None, shape[0],
-                          shape[1], D, _dtype(dq), _dtype(grads[0]) if grads else LN_F32, ws,
-                          ws_bytes)
+    held, ws, ws_bytes = _workspace(workspace, _rope_need(device, D) if grads else 0, device)
+    st = lib.rope_bwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, _stream(None), shape[0],
+                      shape[1], D, _dtype(dq), _dtype(grads[0]) if grads else LN_F32, ws, ws_bytes)
     if st:
         raise NormError(st, "rope_bwd")
 
@@ -918,14 +939,18 @@ def fused_rope_fwd(q, k, positions, freqs, *, q_gamma=None, k_gamma=None, eps=1e
     rotated, the others pass through), or [axes, pairs] from ``rope_axes``
     with positions of [axes, ...]. ``out_q=q`` and ``out_k=k`` work in place.
     """
-    device = _on_device("fused_rope_fwd", q)
-    with _Launch(device, stream):
-        if out_q is None:
-            out_q = torch.empty_like(q)
-        if out_k is None and k is not None:
-            out_k = torch.empty_like(k)
-        rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma, interleaved,
-                 scale, out_q, out_k, None)
+    device = _device_of("fused_rope_fwd", q)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return fused_rope_fwd(q, k, positions, freqs, q_gamma=q_gamma, k_gamma=k_gamma,
+                                  eps=eps, zero_centered_gamma=zero_centered_gamma,
+                                  interleaved=interleaved, scale=scale, out_q=out_q, out_k=out_k)
+    if out_q is None:
+        out_q = torch.empty_like(q)
+    if out_k is None and k is not None:
+        out_k = torch.empty_like(k)
+    rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma, interleaved, scale,
+             out_q, out_k)
     return {"q": out_q, "k": out_k}
 
 
@@ -935,14 +960,20 @@ def fused_rope_bwd(dq, dk, positions, freqs, *, q=None, k=None, q_gamma=None, k_
     """The backward of ``fused_rope_fwd``; ``q`` and ``k`` are its inputs,
     needed with a gamma. Returns a dict with ``dq``, ``dk``, ``dq_gamma`` and
     ``dk_gamma`` (None where there is none)."""
-    device = _on_device("fused_rope_bwd", dq)
-    with _Launch(device, stream):
-        out_dq = torch.empty_like(dq)
-        out_dk = torch.empty_like(dk) if dk is not None else None
-        D = dq.shape[-1]
-        gq = torch.empty(D, dtype=grad_dtype, device=device) if q_gamma is not None else None
-        gk = (torch.empty(D, dtype=grad_dtype, device=device)
-              if k_gamma is not None and dk is not None else None)
-        rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
-                 interleaved, scale, out_dq, out_dk, gq, gk, None, workspace=workspace)
+    device = _device_of("fused_rope_bwd", dq)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return fused_rope_bwd(dq, dk, positions, freqs, q=q, k=k, q_gamma=q_gamma,
+                                  k_gamma=k_gamma, eps=eps,
+                                  zero_centered_gamma=zero_centered_gamma,
+                                  interleaved=interleaved, scale=scale, grad_dtype=grad_dtype,
+                                  workspace=workspace)
+    out_dq = torch.empty_like(dq)
+    out_dk = torch.empty_like(dk) if dk is not None else None
+    D = dq.shape[-1]
+    gq = torch.empty(D, dtype=grad_dtype, device=device) if q_gamma is not None else None
+    gk = (torch.empty(D, dtype=grad_dtype, device=device)
+          if k_gamma is not None and dk is not None else None)
+    rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+             interleaved, scale, out_dq, out_dk, gq, gk, workspace=workspace)
     return {"dq": out_dq, "dk": out_dk, "dq_gamma": gq, "dk_gamma": gk}
