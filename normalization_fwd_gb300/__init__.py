@@ -501,9 +501,16 @@ def _device_of(where: str, first, *others) -> int:
     return device
 
 
+# torch's own fast paths to the current device and the raw current stream of a
+# device, where it has them: the public calls take a few microseconds each.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
 def _elsewhere(device: int, stream) -> bool:
     """Whether a call has to make its device or stream current first."""
-    return stream is not None or device != torch.cuda.current_device()
+    return stream is not None or device != _get_device()
 
 
 @contextlib.contextmanager
@@ -535,7 +542,8 @@ def _rows_of(t, name):
     shape, stride = t.shape, t.stride()
     if len(shape) < 2:
         raise ValueError(f"{name}: expected [samples, ..., channels]")
-    _dense_last(t, name)
+    if stride[-1] != 1:
+        _dense_last(t, name)
     if len(shape) == 3:
         return shape[0], shape[1], shape[2], stride[0], stride[1] if shape[1] > 1 else 0
     rows, row = 1, 0
@@ -646,6 +654,12 @@ def gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean
         with _current(device, stream):
             return gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean,
                           rstd, workspace=workspace)
+    _gn_fwd(device, x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
+            workspace)
+
+
+def _gn_fwd(device, x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
+            workspace):
     lib = _lib or load_library()
     dt = _dtype(x)
     N, R, C, xs, xr = _rows_of(x, "gn_fwd: x")
@@ -658,7 +672,8 @@ def gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean
                     None if beta is None else beta.data_ptr(), ps, eps, _activation(activation),
                     1 if zero_centered_gamma else 0, y.data_ptr() or None, ys, yr,
                     None if mean is None else mean.data_ptr(),
-                    None if rstd is None else rstd.data_ptr(), _stream(None), N, R, C, groups, dt,
+                    None if rstd is None else rstd.data_ptr(), _raw_stream(device) or None, N, R,
+                    C, groups, dt,
                     ws, ws_bytes)
     if st:
         raise NormError(st, "gn_fwd")
@@ -674,6 +689,12 @@ def gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rs
         with _current(device, stream):
             return gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd,
                           dx, dgamma, dbeta, workspace=workspace)
+    _gn_bwd(device, dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx,
+            dgamma, dbeta, workspace)
+
+
+def _gn_bwd(device, dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx,
+            dgamma, dbeta, workspace):
     lib = _lib or load_library()
     dt = _dtype(x)
     N, R, C, xs, xr = _rows_of(x, "gn_bwd: x")
@@ -696,8 +717,8 @@ def gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rs
                     1 if zero_centered_gamma else 0, mean.data_ptr() or None,
                     rstd.data_ptr() or None, dx.data_ptr() or None, os_, or_,
                     None if dgamma is None else dgamma.data_ptr(),
-                    None if dbeta is None else dbeta.data_ptr(), _stream(None), N, R, C, groups,
-                    dt, _dtype(grads[0]) if grads else LN_F32, ws, ws_bytes)
+                    None if dbeta is None else dbeta.data_ptr(), _raw_stream(device) or None, N, R,
+                    C, groups, dt, _dtype(grads[0]) if grads else LN_F32, ws, ws_bytes)
     if st:
         raise NormError(st, "gn_bwd")
 
@@ -713,7 +734,7 @@ def fused_group_norm_fwd(x, groups, gamma=None, beta=None, *, eps=1e-5, activati
     shift of each sample. ``x`` and ``out`` may be slices of the channels of
     wider tensors.
     """
-    device = _device_of("fused_group_norm_fwd", x)
+    device = _device_of("fused_group_norm_fwd", x, gamma, beta, out)
     if _elsewhere(device, stream):
         with _current(device, stream):
             return fused_group_norm_fwd(x, groups, gamma, beta, eps=eps, activation=activation,
@@ -722,8 +743,8 @@ def fused_group_norm_fwd(x, groups, gamma=None, beta=None, *, eps=1e-5, activati
     y = torch.empty_like(x) if out is None else out
     mean = torch.empty((x.shape[0], groups), dtype=torch.float32, device=device)
     rstd = torch.empty_like(mean)
-    gn_fwd(x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
-           workspace=workspace)
+    _gn_fwd(device, x, groups, gamma, beta, eps, activation, zero_centered_gamma, y, mean, rstd,
+            workspace)
     return {"y": y, "mean": mean, "rstd": rstd}
 
 
@@ -733,7 +754,7 @@ def fused_group_norm_bwd(dy, x, groups, gamma, beta, mean, rstd, *, activation="
     """The backward of ``fused_group_norm_fwd`` from its x and statistics;
     returns a dict with ``dx``, ``dgamma`` and ``dbeta`` (None where gamma or
     beta is None)."""
-    device = _device_of("fused_group_norm_bwd", x)
+    device = _device_of("fused_group_norm_bwd", x, dy, gamma, beta, mean, rstd)
     if _elsewhere(device, stream):
         with _current(device, stream):
             return fused_group_norm_bwd(dy, x, groups, gamma, beta, mean, rstd,
@@ -743,8 +764,8 @@ def fused_group_norm_bwd(dy, x, groups, gamma, beta, mean, rstd, *, activation="
     dx = torch.empty_like(x)
     dgamma = None if gamma is None else torch.empty(gamma.shape, dtype=grad_dtype, device=device)
     dbeta = None if beta is None else torch.empty(beta.shape, dtype=grad_dtype, device=device)
-    gn_bwd(dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx, dgamma,
-           dbeta, workspace=workspace)
+    _gn_bwd(device, dy, x, groups, gamma, beta, activation, zero_centered_gamma, mean, rstd, dx,
+            dgamma, dbeta, workspace)
     return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
@@ -784,16 +805,21 @@ def rope_axes(*frequencies):
 
 
 def _heads(t, name, like=None):
-    """(batch, tokens, heads, dim) and the strides of the first three, of
+    """Shape [batch, tokens, heads, dim] and the strides of the first three, of
     [tokens, heads, dim] or [batch, tokens, heads, dim]."""
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{name}: expected [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    _dense_last(t, name)
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+    shape, st = t.shape, t.stride()
+    if like is not None and (shape != like.shape or t.dtype != like.dtype):
         raise ValueError(f"{name}: expected {list(like.shape)} of {like.dtype}")
-    if t.dim() == 3:
-        return (1, *t.shape), (0, *t.stride()[:2])
-    return tuple(t.shape), t.stride()[:3]
+    if st[-1:] != (1,):
+        if len(shape) not in (3, 4):
+            raise ValueError(f"{name}: expected [tokens, heads, dim] or "
+                             "[batch, tokens, heads, dim]")
+        _dense_last(t, name)
+    if len(shape) == 4:
+        return shape, st[:3]
+    if len(shape) == 3:
+        return (1, *shape), (0, *st[:2])
+    raise ValueError(f"{name}: expected [tokens, heads, dim] or [batch, tokens, heads, dim]")
 
 
 def _positions(where, positions, freqs, interleaved, scale, shape, dims):
@@ -844,6 +870,12 @@ def rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
         with _current(device, stream):
             return rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
                             interleaved, scale, out_q, out_k)
+    _rope_fwd(device, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+              interleaved, scale, out_q, out_k)
+
+
+def _rope_fwd(device, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+              interleaved, scale, out_q, out_k):
     lib = _lib or load_library()
     shape, xs = _heads(q, "rope_fwd: q")
     _, ys = _heads(out_q, "rope_fwd: out_q", q)
@@ -860,7 +892,8 @@ def rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
                               _gamma_ptr(k_gamma, "rope_fwd: k_gamma", D, q.dtype), kshape[2], *xs,
                               *ys)
     pos = _positions("rope_fwd", positions, freqs, interleaved, scale, shape, q.dim())
-    st = lib.rope_fwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, _stream(None), shape[0],
+    st = lib.rope_fwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0,
+                      _raw_stream(device) or None, shape[0],
                       shape[1], D, _dtype(q))
     if st:
         raise NormError(st, "rope_fwd")
@@ -890,6 +923,12 @@ def rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centere
             return rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps,
                             zero_centered_gamma, interleaved, scale, out_dq, out_dk, dq_gamma,
                             dk_gamma, workspace=workspace)
+    _rope_bwd(device, dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+              interleaved, scale, out_dq, out_dk, dq_gamma, dk_gamma, workspace)
+
+
+def _rope_bwd(device, dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+              interleaved, scale, out_dq, out_dk, dq_gamma, dk_gamma, workspace):
     lib = _lib or load_library()
     shape, _ = _heads(dq, "rope_bwd: dq")
     D = shape[3]
@@ -921,7 +960,8 @@ def rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centere
     ks = side(dk, k, k_gamma, out_dk, dk_gamma, "k")
     pos = _positions("rope_bwd", positions, freqs, interleaved, scale, shape, dq.dim())
     held, ws, ws_bytes = _workspace(workspace, _rope_need(device, D) if grads else 0, device)
-    st = lib.rope_bwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0, _stream(None), shape[0],
+    st = lib.rope_bwd(qs, ks, pos, eps, 1 if zero_centered_gamma else 0,
+                      _raw_stream(device) or None, shape[0],
                       shape[1], D, _dtype(dq), _dtype(grads[0]) if grads else LN_F32, ws, ws_bytes)
     if st:
         raise NormError(st, "rope_bwd")
@@ -939,7 +979,7 @@ def fused_rope_fwd(q, k, positions, freqs, *, q_gamma=None, k_gamma=None, eps=1e
     rotated, the others pass through), or [axes, pairs] from ``rope_axes``
     with positions of [axes, ...]. ``out_q=q`` and ``out_k=k`` work in place.
     """
-    device = _device_of("fused_rope_fwd", q)
+    device = _device_of("fused_rope_fwd", q, k, positions, freqs, q_gamma, k_gamma, out_q, out_k)
     if _elsewhere(device, stream):
         with _current(device, stream):
             return fused_rope_fwd(q, k, positions, freqs, q_gamma=q_gamma, k_gamma=k_gamma,
@@ -949,8 +989,8 @@ def fused_rope_fwd(q, k, positions, freqs, *, q_gamma=None, k_gamma=None, eps=1e
         out_q = torch.empty_like(q)
     if out_k is None and k is not None:
         out_k = torch.empty_like(k)
-    rope_fwd(q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma, interleaved, scale,
-             out_q, out_k)
+    _rope_fwd(device, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+              interleaved, scale, out_q, out_k)
     return {"q": out_q, "k": out_k}
 
 
@@ -960,7 +1000,7 @@ def fused_rope_bwd(dq, dk, positions, freqs, *, q=None, k=None, q_gamma=None, k_
     """The backward of ``fused_rope_fwd``; ``q`` and ``k`` are its inputs,
     needed with a gamma. Returns a dict with ``dq``, ``dk``, ``dq_gamma`` and
     ``dk_gamma`` (None where there is none)."""
-    device = _device_of("fused_rope_bwd", dq)
+    device = _device_of("fused_rope_bwd", dq, dk, positions, freqs, q, k, q_gamma, k_gamma)
     if _elsewhere(device, stream):
         with _current(device, stream):
             return fused_rope_bwd(dq, dk, positions, freqs, q=q, k=k, q_gamma=q_gamma,
@@ -974,6 +1014,6 @@ def fused_rope_bwd(dq, dk, positions, freqs, *, q=None, k=None, q_gamma=None, k_
     gq = torch.empty(D, dtype=grad_dtype, device=device) if q_gamma is not None else None
     gk = (torch.empty(D, dtype=grad_dtype, device=device)
           if k_gamma is not None and dk is not None else None)
-    rope_bwd(dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
-             interleaved, scale, out_dq, out_dk, gq, gk, workspace=workspace)
+    _rope_bwd(device, dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
+              interleaved, scale, out_dq, out_dk, gq, gk, workspace)
     return {"dq": out_dq, "dk": out_dk, "dq_gamma": gq, "dk_gamma": gk}
