@@ -9,9 +9,9 @@
 
 namespace nf {
 
-const void* gn_table_f32(bool bwd, bool cluster, bool vec, int threads, int act);
-const void* gn_table_bf16(bool bwd, bool cluster, bool vec, int threads, int act);
-const void* gn_table_f16(bool bwd, bool cluster, bool vec, int threads, int act);
+const void* gn_table_f32(bool bwd, bool cluster, bool vec, int act);
+const void* gn_table_bf16(bool bwd, bool cluster, bool vec, int act);
+const void* gn_table_f16(bool bwd, bool cluster, bool vec, int act);
 
 namespace {
 
@@ -34,7 +34,6 @@ int gcd(int a, int b) {
 // tile).
 struct GnPlan {
   bool cluster;            // one launch, a cluster a panel
-  int threads;             // of a CTA
   int clusters;            // of the launch
   int tiles, tw, max_groups, slices;
   int64_t slice_rows;
@@ -43,15 +42,15 @@ struct GnPlan {
   size_t bytes() const { return part_bytes + cols_bytes; }
 };
 
-constexpr int64_t kBatchBytes = 48ll << 20;
-constexpr int kTileBytes = 128;
-constexpr int kClusterCtas = 4;              // CTAs an SM that clusters aim for
+constexpr int kPerSm[2] = {3, 2};            // resident CTAs, forward and backward
+constexpr int64_t kBatchBytes[2] = {68ll << 20, 90ll << 20};
 constexpr int64_t kSlabBytes = 4ll << 20;
 
-// Column tiles of about `target` vectors. Whole groups and whole vectors
-// where `lv`, the vectors that both fill, is no more than `most`; false when
-// a tile may end inside a group.
-bool gn_tiles(int nv, int lv, int target, int most, GnPlan* p) {
+// Column tiles of about `bytes`, of whole groups and whole vectors where lv,
+// the vectors that both fill, is no more than `most`; false when a tile may
+// end inside a group. A vector has vb bytes.
+bool gn_tiles(int nv, int lv, int bytes, int vb, int most, GnPlan* p) {
+  const int target = bytes / vb < most ? (bytes / vb > 0 ? bytes / vb : 1) : most;
   int tw = nv;
   bool whole = true;
   if (nv > target) {
@@ -78,41 +77,56 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
   const int V = vec ? (int)(16 / es) : 1;
   const int nv = channels / V, cpg = channels / groups;
   const int most = vec ? 64 : 256;
-  const int vb = V * (int)es;                       // bytes of a vector
+  const int vb = V * (int)es;
   const int lv = cpg / gcd(cpg, V);
-  const int target = kTileBytes / vb < most ? kTileBytes / vb : most;
-  const bool whole = gn_tiles(nv, lv, target, most, p);
-  const int tc = p->tw * V;
+  const int64_t places = (int64_t)sms * kPerSm[bwd];
+  const auto max_groups = [&](bool whole) {
+    const int tc = p->tw * V;
+    const int m = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
+    return m < groups ? m : groups;
+  };
+  // One launch, a cluster a panel. What a CTA does besides its rows costs as
+  // much as some eight rows of each thread, so there are no more CTAs than it
+  // takes to give every SM one and most a second (1.5 an SM): narrow tiles
+  // first, which make more panels, then clusters of more CTAs.
+  bool whole = gn_tiles(nv, lv, 128, vb, most, p);
+  while (whole && samples * p->tiles * 8 < (int64_t)sms * 3 / 2 && p->tw > lv &&
+         (p->tw - lv) * vb >= 64)
+    whole = gn_tiles(nv, lv, (p->tw - lv) * vb, vb, most, p);
   p->panels = samples * p->tiles;
-  p->max_groups = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
-  if (p->max_groups > groups) p->max_groups = groups;
-  const double slab = (double)rows * tc * es * (bwd ? 2 : 1);   // what a panel reads
+  p->max_groups = max_groups(whole);
+  double slab = (double)rows * p->tw * vb * (bwd ? 2 : 1);   // what a panel reads
   p->cluster = whole && slab <= (double)kSlabBytes;
-  p->threads = 256;
   p->clusters = 0;
   if (p->cluster) {
+    const int64_t TY = kGnThreads / p->tw;
     int s = 1;
-    const int per_sm = bwd ? 2 : 3;   // resident CTAs of 256 threads
-    const int64_t TY = 256 / p->tw;
-    while (s < 16 && p->panels * s < (int64_t)sms * per_sm && rows > s * TY * 4) s *= 2;
-    // Too few CTAs for every SM to hold as many as it can: larger ones.
-    if (vec && p->panels * s < (int64_t)sms * per_sm / 2 && rows > s * TY * 2) p->threads = 512;
+    // Clusters of 16 need 16 free places in one part of the chip: fewer of
+    // them fit than the SMs would hold CTAs.
+    while (s < 16 && p->panels * s < (int64_t)sms * 3 / 2 && rows > s * TY * 2 &&
+           !(s == 8 && p->panels > sms / (bwd ? 12 : 8)))
+      s *= 2;
     p->slices = s;
-    p->clusters = (int)(p->panels * s <= (int64_t)sms * per_sm ? p->panels
-                                                               : (int64_t)sms * per_sm / s);
+    p->clusters = (int)(p->panels * s <= places ? p->panels : places / s);
     p->slice_rows = (rows + s - 1) / s;
     p->batch = p->panels;
     p->part_bytes = 0;
   } else {
+    // Batches whose rows stay in the L2 cache from the launch that sums them
+    // to the one that applies them.
+    whole = gn_tiles(nv, lv, 128, vb, most, p);
+    p->panels = samples * p->tiles;
+    p->max_groups = max_groups(whole);
+    slab = (double)rows * p->tw * vb * (bwd ? 2 : 1);
     p->batch = p->panels;
-    if (slab * p->panels > (double)kBatchBytes) {
+    if (slab * p->panels > (double)kBatchBytes[bwd]) {
       const int64_t step = whole ? 1 : p->tiles;
-      int64_t b = (int64_t)(kBatchBytes / slab) / step * step;
+      int64_t b = (int64_t)(kBatchBytes[bwd] / slab) / step * step;
       p->batch = b < step ? step : b;
       if (p->batch > p->panels) p->batch = p->panels;
     }
-    const int64_t TY = 256 / p->tw;
-    int64_t slices = ((int64_t)sms * (bwd ? 2 : 3) + p->batch - 1) / p->batch;
+    const int64_t TY = kGnThreads / p->tw;
+    int64_t slices = (places + p->batch - 1) / p->batch;
     if (slices > kGnMaxSlices) slices = kGnMaxSlices;
     const int64_t least = 4 * TY;       // rows of a slice: four a thread
     if (slices > (rows + least - 1) / least) slices = (rows + least - 1) / least;
@@ -182,16 +196,15 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
   a.by_tiles.set(p.tiles);
   a.by_tw.set(p.tw);
   a.by_tc.set(p.tw * (vec ? (int)(16 / elem_size(c.dtype)) : 1));
-  a.by_ty.set(p.threads / p.tw);
+  a.by_ty.set(kGnThreads / p.tw);
   a.by_cpg.set(a.cpg);
   a.rows = c.rows;
   a.inv_m = (float)(1.0 / ((double)c.rows * a.cpg));
-  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, p.threads, act)
-                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, p.threads, act)
-                                        : gn_table_f16(bwd, p.cluster, vec, p.threads, act);
+  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, act)
+                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, act)
+                                        : gn_table_f16(bwd, p.cluster, vec, act);
   const int tensors = !vec ? 0 : bwd ? 2 : 1;
-  const size_t smem = p.threads == 512 ? gn_smem_bytes<512>(tensors, p.cluster)
-                                       : gn_smem_bytes<256>(tensors, p.cluster);
+  const size_t smem = gn_smem_bytes(tensors, p.cluster);
   const cudaError_t opt = (cudaError_t)allow_dyn_smem(fn, smem);
   if (opt != cudaSuccess) return cuda_fail(opt);
   if (p.cluster) {
@@ -202,7 +215,7 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.clusters * p.slices));
-    cfg.blockDim = dim3(p.threads);
+    cfg.blockDim = dim3(kGnThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -226,7 +239,7 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
     const int n = s1 - s0 > a1 - a0 ? s1 - s0 : a1 - a0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n * p.slices));
-    cfg.blockDim = dim3(p.threads);
+    cfg.blockDim = dim3(kGnThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

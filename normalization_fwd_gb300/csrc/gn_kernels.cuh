@@ -19,6 +19,7 @@
 
 namespace nf {
 
+constexpr int kGnThreads = 256;
 constexpr int kGnMaxTileCh = 512;   // most channels of a column tile
 constexpr int kGnRing = 8;          // rows a thread has in flight, or keeps
 constexpr int kGnStep = 2;          // rows of one step
@@ -35,7 +36,7 @@ struct GnArgs {
   void* out;             // y, or dx
   float* mean;           // [samples, groups]; forward: output, nullable
   float* rstd;
-  float2* part;          // [panel][slice][max_groups] partials of the groups
+  float2* part;          // [panel][max_groups][slice] partials of the groups
   float* cols;           // backward: [sample][slice][2 * channels] B, then A
   int64_t x_sample, x_row, dy_sample, dy_row, out_sample, out_row;   // elements
   int64_t param_sample;  // elements between samples of gamma / beta, 0 = shared
@@ -163,12 +164,12 @@ template <typename T> struct Pack<T, 1> {
 
 // Shared memory: the row lanes' sums before they are added up, and in their
 // place, afterwards, the parameters of the tile's columns.
-template <int TH> struct alignas(16) GnSmem {
+struct alignas(16) GnSmem {
   union {
-    float2 lane[TH * 8];
+    float2 lane[kGnThreads * 8];
     float par[6][kGnMaxTileCh];
   };
-  float2 col[TH > kGnMaxTileCh ? TH : kGnMaxTileCh];   // column sums, in parts, then whole
+  float2 col[kGnMaxTileCh];   // column sums, in parts, then whole
   float k[kGnMaxTileCh];        // forward: what the columns are shifted by
   float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
   float g1[kGnMaxTileCh];       // rstd, or c2
@@ -211,7 +212,7 @@ struct GnUnit {
   int rows;              // its rows
   bool on;               // it has a vector
 };
-template <int VEC, int TH>
+template <int VEC>
 __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice) {
   GnUnit u;
   u.n = a.by_tiles.div(panel);
@@ -224,7 +225,7 @@ __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice)
   u.ng = a.by_cpg.div(u.c0 + u.nc - 1) - u.g0 + 1;
   u.r0 = min(a.rows, (int64_t)slice * a.slice_rows);   // a cluster's last CTAs may have none
   u.nr = min(a.rows - u.r0, a.slice_rows);
-  u.TY = a.by_tw.div(TH);
+  u.TY = a.by_tw.div(kGnThreads);
   u.ty = a.by_tw.div(threadIdx.x);
   u.tx = threadIdx.x - u.ty * a.tw;
   u.on = u.ty < u.TY && u.tx * VEC < u.nc;
@@ -255,8 +256,8 @@ __device__ __forceinline__ float gn_bias(const GnArgs& a, const GnUnit& u, int c
 // lanes are dealt to as many threads as there are, then those parts are
 // added; the order depends on the launch's shape only. done(col, sums) gets
 // the totals; where it writes sm.col[col] no other thread reads that place.
-template <int VEC, int TH, typename F>
-__device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
+template <int VEC, typename F>
+__device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnSmem& sm,
                                            const float2* va, const float2* vb, F&& done) {
   if (u.on) {
     float2* to = sm.lane + u.ty * u.tc + u.tx * VEC;
@@ -269,7 +270,7 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
     }
   }
   __syncthreads();
-  const int parts = a.by_tc.div(TH);   // threads a column
+  const int parts = a.by_tc.div(kGnThreads);   // threads a column
   if (parts > 1) {
     const int part = a.by_tc.div(threadIdx.x), col = threadIdx.x - part * u.tc;
     if (part < parts && col < u.nc) {
@@ -286,7 +287,7 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
       done(threadIdx.x, s);
     }
   } else {
-    for (int c = threadIdx.x; c < u.nc; c += TH) {
+    for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int y = 0; y < u.TY; ++y) s = add2(s, sm.lane[y * u.tc + c]);
@@ -310,7 +311,7 @@ template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int VEC, int TH, int TENSORS> struct Rows {
+template <typename T, int VEC, int TENSORS> struct Rows {
   static constexpr int NG = kGnRing / kGnStep;   // steps in flight
   const T* p[TENSORS];      // the thread's first row
   int64_t step[TENSORS];    // from one of its rows to the next
@@ -321,7 +322,7 @@ template <typename T, int VEC, int TH, int TENSORS> struct Rows {
   Pack<T, VEC> v[TENSORS][kGnStep];
 
   __device__ __forceinline__ unsigned at(unsigned place) const {
-    return slots + place % NG * (kGnStep * TH * 16);
+    return slots + place % NG * (kGnStep * kGnThreads * 16);
   }
   // Step g of n rows, into a place of the ring.
   __device__ __forceinline__ void fetch(int g, int n, unsigned place) {
@@ -331,7 +332,7 @@ template <typename T, int VEC, int TH, int TENSORS> struct Rows {
       if (g * kGnStep + j < n) {
 #pragma unroll
         for (int t = 0; t < TENSORS; ++t) {
-          copy_async16(to + t * (kGnRing * TH * 16) + j * (TH * 16), next[t]);
+          copy_async16(to + t * (kGnRing * kGnThreads * 16) + j * (kGnThreads * 16), next[t]);
           next[t] += step[t];
         }
       }
@@ -346,7 +347,7 @@ template <typename T, int VEC, int TH, int TENSORS> struct Rows {
         uint4& u = v[t][j].v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "r"(from + t * (kGnRing * TH * 16) + j * (TH * 16)));
+                     : "r"(from + t * (kGnRing * kGnThreads * 16) + j * (kGnThreads * 16)));
       }
   }
   __device__ __forceinline__ void rewind() {
@@ -462,9 +463,10 @@ template <typename T, int VEC, int TH, int TENSORS> struct Rows {
 // at most about n * 2^-24 of the group's sum of squares, whatever the mean.
 // Columns, and later slices, are merged by the parallel-variance identity
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
-template <typename T, int VEC, int TH>
-__device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
-                                              Rows<T, VEC, TH, 1>& rows, float2* out) {
+template <typename T, int VEC>
+__device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                              Rows<T, VEC, 1>& rows, float2* out,
+                                              int stride) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 k[NP], s1[NP], s2[NP], v[NP];
 #pragma unroll
@@ -485,13 +487,13 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
   });
   if (u.on && u.ty == 0) put_pairs<VEC>(sm.k + u.tx * VEC, k);
   const float n = (float)u.nr, inv = u.nr > 0 ? 1.f / n : 0.f;
-  gn_columns<VEC, TH>(a, u, sm, s1, s2, [&](int c, float2 s) {
+  gn_columns<VEC>(a, u, sm, s1, s2, [&](int c, float2 s) {
     const float m = s.x * inv;
     sm.col[c] = make_float2(sm.k[c] + m, fmaf(-s.x, m, s.y));   // mean, M2
   });
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
     const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     // Means are averaged as differences from one of them, which keeps a
@@ -507,15 +509,15 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
       s += fmaf(n * d, d, v.y);
     }
     s = group_sum<32>(s);
-    if (lane == 0) out[lg] = make_float2(m, s);
+    if (lane == 0) out[(int64_t)lg * stride] = make_float2(m, s);
   }
   __syncthreads();
 }
 
 // What the merged sums become: mean and rstd (forward, stored by one CTA of
 // the group's), or c1 and c2.
-template <bool BWD, int TH>
-__device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm, int lg,
+template <bool BWD>
+__device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSmem& sm, int lg,
                                           float s0, float s1, bool store) {
   if (!BWD) {
     if (s1 < 0.f) s1 = 0.f;   // rounding alone; a NaN stays one
@@ -534,22 +536,22 @@ __device__ __forceinline__ void gn_merged(const GnArgs& a, const GnUnit& u, GnSm
 // (forward) or into sm.g0 = c1, sm.g1 = c2 (backward): one warp a group, the
 // slices dealt to its lanes, the same order in every CTA. A lane has all its
 // partials of a tile on their way at once and keeps them for the second sum.
-template <bool BWD, int TH>
-__device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm) {
+template <bool BWD>
+__device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
   constexpr int N = kGnMaxSlices / 32;
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     const int g = u.g0 + lg, ch0 = g * a.cpg, ch1 = ch0 + a.cpg;
     const int t0 = a.by_tc.div(ch0), t1 = a.by_tc.div(ch1 - 1);
     float s0 = 0.f, s1 = 0.f, base = 0.f;
     float2 v[N];
     const auto fetch = [&](int t) {
-      const float2* p = a.part + ((int64_t)u.n * a.tiles + t) * a.slices * a.max_groups +
-                        (g - a.by_cpg.div(t * u.tc));
+      const float2* p = a.part + (((int64_t)u.n * a.tiles + t) * a.max_groups +
+                                  (g - a.by_cpg.div(t * u.tc))) * a.slices;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         v[j] = make_float2(0.f, 0.f);
-        if (lane + 32 * j < a.slices) v[j] = p[(int64_t)(lane + 32 * j) * a.max_groups];
+        if (lane + 32 * j < a.slices) v[j] = p[lane + 32 * j];
       }
     };
     // values of the group in slice i of tile t
@@ -580,7 +582,7 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
       }
     }
     s1 = group_sum<32>(s1) * a.inv_m;
-    if (lane == 0) gn_merged<BWD, TH>(a, u, sm, lg, s0, s1, u.slice == 0 && u.tile == t0);
+    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0 && u.tile == t0);
   }
   __syncthreads();
 }
@@ -607,11 +609,11 @@ __device__ __forceinline__ float2 cluster_read(const float2* p, int rank) {
 }
 
 // The merge of gn_combine over the cluster's CTAs: a lane a CTA.
-template <bool BWD, int TH>
-__device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
+template <bool BWD>
+__device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit& u, GnSmem& sm,
                                                    const float2* part) {
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     float2 v = make_float2(0.f, 0.f);
     if (lane < a.slices) v = cluster_read(part + lg, lane);
     float s0, s1;
@@ -627,17 +629,17 @@ __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit
       const float d = v.x - s0;
       s1 = group_sum<32>(some ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
     }
-    if (lane == 0) gn_merged<BWD, TH>(a, u, sm, lg, s0, s1, u.slice == 0);
+    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0);
   }
   __syncthreads();
 }
 
 // ---- forward: normalize one unit -------------------------------------------------
-template <typename T, int VEC, int TH, int ACT, typename W>
-__device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
-                                              Rows<T, VEC, TH, 1>& rows, W&& walk) {
+template <typename T, int VEC, int ACT, typename W>
+__device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                              Rows<T, VEC, 1>& rows, W&& walk) {
   constexpr int NP = Pack<T, VEC>::NP;
-  for (int c = threadIdx.x; c < u.nc; c += TH) {
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
     const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
     sm.par[0][c] = -sm.g0[lg];
     sm.par[1][c] = gn_weight<T>(a, u, c) * sm.g1[lg];
@@ -664,9 +666,9 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
 
 // ---- backward ------------------------------------------------------------------------
 // mean, rstd, w and beta of the unit's columns.
-template <typename T, int TH>
-__device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm) {
-  for (int c = threadIdx.x; c < u.nc; c += TH) {
+template <typename T>
+__device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
     const int64_t g = (int64_t)u.n * a.groups + a.by_cpg.div(u.c0 + c);
     sm.par[0][c] = -a.mean[g];
     sm.par[1][c] = a.rstd[g];
@@ -676,14 +678,15 @@ __device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, 
 }
 
 // Sums of one unit.
-template <typename T, int VEC, int TH, int ACT>
-__device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
-                                                  Rows<T, VEC, TH, 2>& rows, float2* out) {
+template <typename T, int VEC, int ACT>
+__device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                                  Rows<T, VEC, 2>& rows, float2* out,
+                                                  int stride) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 sa[NP], sb[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) sa[i] = sb[i] = splat2(0.f);
-  gn_bwd_params<T, TH>(a, u, sm);
+  gn_bwd_params<T>(a, u, sm);
   __syncthreads();
   if (u.rows > 0) {
     float2 m[NP], rs[NP], w[NP], b[NP], v[NP], d[NP];
@@ -710,7 +713,7 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
   }
   __syncthreads();   // the parameters give way to the sums
   float* cols = a.cols + ((int64_t)u.n * a.slices + u.slice) * 2 * a.channels + u.c0;
-  gn_columns<VEC, TH>(a, u, sm, sa, sb, [&](int c, float2 s) {
+  gn_columns<VEC>(a, u, sm, sa, sb, [&](int c, float2 s) {
     cols[c] = s.y;
     cols[a.channels + c] = s.x;
     const float w = gn_weight<T>(a, u, c);
@@ -718,24 +721,24 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
   });
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += TH / 32) {
+  for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
     const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
     float2 s = make_float2(0.f, 0.f);
     for (int c = cs + lane; c < ce; c += 32) s = add2(s, sm.col[c]);
     s = group_sum2<32>(s);
-    if (lane == 0) out[lg] = s;
+    if (lane == 0) out[(int64_t)lg * stride] = s;
   }
   __syncthreads();
 }
 
 // dx of one unit.
-template <typename T, int VEC, int TH, int ACT, typename W>
-__device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem<TH>& sm,
-                                                  Rows<T, VEC, TH, 2>& rows, W&& walk) {
+template <typename T, int VEC, int ACT, typename W>
+__device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                                  Rows<T, VEC, 2>& rows, W&& walk) {
   constexpr int NP = Pack<T, VEC>::NP;
-  gn_bwd_params<T, TH>(a, u, sm);
-  for (int c = threadIdx.x; c < u.nc; c += TH) {
+  gn_bwd_params<T>(a, u, sm);
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
     const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
     sm.par[4][c] = -sm.g0[lg];
     sm.par[5][c] = -sm.g1[lg];
@@ -776,24 +779,24 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
 
 // ---- kernels ----------------------------------------------------------------------
 __device__ __forceinline__ float2* gn_part(const GnArgs& a, const GnUnit& u) {
-  return a.part + (((int64_t)u.n * a.tiles + u.tile) * a.slices + u.slice) * a.max_groups;
+  return a.part + ((int64_t)u.n * a.tiles + u.tile) * a.max_groups * a.slices + u.slice;
 }
 // Dynamic shared memory: GnSmem, a cluster's partials, then the slots.
 extern __shared__ __align__(16) unsigned char gn_dynamic[];
 struct GnParts {
   float2 part[2][kGnMaxTileCh];
 };
-template <int TH> __host__ __device__ constexpr size_t gn_smem_bytes(int tensors, bool cluster) {
-  return sizeof(GnSmem<TH>) + (cluster ? sizeof(GnParts) : 0) +
-         (size_t)tensors * kGnRing * TH * 16;
+constexpr size_t gn_smem_bytes(int tensors, bool cluster) {
+  return sizeof(GnSmem) + (cluster ? sizeof(GnParts) : 0) +
+         (size_t)tensors * kGnRing * kGnThreads * 16;
 }
 
 // Where a unit's first rows are.
-template <typename T, int VEC, int TH>
+template <typename T, int VEC>
 __device__ __forceinline__ void gn_fwd_rows(const GnArgs& a, const GnUnit& u, const T** p) {
   p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
 }
-template <typename T, int VEC, int TH>
+template <typename T, int VEC>
 __device__ __forceinline__ void gn_bwd_rows(const GnArgs& a, const GnUnit& u, const T** p) {
   p[0] = static_cast<const T*>(a.x) + gn_at<T, VEC>(u, a.x_sample, a.x_row);
   p[1] = static_cast<const T*>(a.dy) + gn_at<T, VEC>(u, a.dy_sample, a.dy_row);
@@ -801,59 +804,59 @@ __device__ __forceinline__ void gn_bwd_rows(const GnArgs& a, const GnUnit& u, co
 
 // One launch takes the statistics of the panels [stat0, stat1) and applies
 // those of [app0, app1), which an earlier launch gathered.
-template <typename T, int VEC, int TH, int ACT>
-__global__ void __launch_bounds__(TH, 768 / TH)
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnThreads, 3)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
-  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
-  void* const ring = gn_dynamic + sizeof(GnSmem<TH>);
+  GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
+  void* const ring = gn_dynamic + sizeof(GnSmem);
   const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Rows<T, VEC, TH, 1> rows;
+  Rows<T, VEC, 1> rows;
   if (stat0 + p < stat1) {
-    const GnUnit u = gn_unit<VEC, TH>(a, stat0 + p, s);
-    gn_fwd_rows<T, VEC, TH>(a, u, rows.p);
+    const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
+    gn_fwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
     rows.start(u.rows, ring);
-    gn_stats_unit<T, VEC, TH>(a, u, sm, rows, gn_part(a, u));
+    gn_stats_unit<T, VEC>(a, u, sm, rows, gn_part(a, u), a.slices);
   }
   if (app0 + p < app1) {
-    const GnUnit u = gn_unit<VEC, TH>(a, app0 + p, s);
-    gn_fwd_rows<T, VEC, TH>(a, u, rows.p);
+    const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
+    gn_fwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
     rows.start(u.rows, ring);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_combine<false, TH>(a, u, sm);
-    gn_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+    gn_combine<false>(a, u, sm);
+    gn_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
       rows.pass(o, ostep, body);
     });
   }
 }
 
-template <typename T, int VEC, int TH, int ACT>
-__global__ void __launch_bounds__(TH, 512 / TH)
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnThreads, 2)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
-  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
-  void* const ring = gn_dynamic + sizeof(GnSmem<TH>);
+  GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
+  void* const ring = gn_dynamic + sizeof(GnSmem);
   const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Rows<T, VEC, TH, 2> rows;
+  Rows<T, VEC, 2> rows;
   if (stat0 + p < stat1) {
-    const GnUnit u = gn_unit<VEC, TH>(a, stat0 + p, s);
-    gn_bwd_rows<T, VEC, TH>(a, u, rows.p);
+    const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
+    gn_bwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
     rows.step[1] = (int64_t)u.TY * a.dy_row;
     rows.start(u.rows, ring);
-    gn_bwd_stats_unit<T, VEC, TH, ACT>(a, u, sm, rows, gn_part(a, u));
+    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, gn_part(a, u), a.slices);
   }
   if (app0 + p < app1) {
-    const GnUnit u = gn_unit<VEC, TH>(a, app0 + p, s);
-    gn_bwd_rows<T, VEC, TH>(a, u, rows.p);
+    const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
+    gn_bwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
     rows.step[1] = (int64_t)u.TY * a.dy_row;
     rows.start(u.rows, ring);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    gn_combine<true, TH>(a, u, sm);
-    gn_bwd_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+    gn_combine<true>(a, u, sm);
+    gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
       rows.pass(o, ostep, body);
     });
   }
@@ -865,28 +868,28 @@ __global__ void __launch_bounds__(TH, 512 / TH)
 // one on their way while it finishes this one. The partials have two places
 // in turn: one is written again only after the barrier of the panel between,
 // which every CTA reaches after it has read them.
-template <typename T, int VEC, int TH, int ACT>
-__global__ void __launch_bounds__(TH, 768 / TH) gn_fwd_cluster_kernel(GnArgs a, int panels) {
-  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
-  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem<TH>))->part;
-  void* const ring = gn_dynamic + sizeof(GnSmem<TH>) + sizeof(GnParts);
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a, int panels) {
+  GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
+  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem))->part;
+  void* const ring = gn_dynamic + sizeof(GnSmem) + sizeof(GnParts);
   int p = a.by_slices.div(blockIdx.x), turn = 0;
   const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
-  GnUnit u = gn_unit<VEC, TH>(a, p, rank);
-  Rows<T, VEC, TH, 1> rows;
-  gn_fwd_rows<T, VEC, TH>(a, u, rows.p);
+  GnUnit u = gn_unit<VEC>(a, p, rank);
+  Rows<T, VEC, 1> rows;
+  gn_fwd_rows<T, VEC>(a, u, rows.p);
   rows.step[0] = (int64_t)u.TY * a.x_row;
   rows.start(u.rows, ring);
   while (true) {
-    gn_stats_unit<T, VEC, TH>(a, u, sm, rows, part[turn]);
+    gn_stats_unit<T, VEC>(a, u, sm, rows, part[turn], 1);
     cluster_arrive();
     cluster_wait();
-    gn_combine_cluster<false, TH>(a, u, sm, part[turn]);
+    gn_combine_cluster<false>(a, u, sm, part[turn]);
     p += clusters;
-    const GnUnit v = gn_unit<VEC, TH>(a, p < panels ? p : 0, rank);
+    const GnUnit v = gn_unit<VEC>(a, p < panels ? p : 0, rank);
     const T* q[1];
-    gn_fwd_rows<T, VEC, TH>(a, v, q);
-    gn_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+    gn_fwd_rows<T, VEC>(a, v, q);
+    gn_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
       rows.again(o, ostep, body, q, p < panels ? v.rows : 0);
     });
     if (p >= panels) break;
@@ -898,29 +901,29 @@ __global__ void __launch_bounds__(TH, 768 / TH) gn_fwd_cluster_kernel(GnArgs a, 
   cluster_wait();
 }
 
-template <typename T, int VEC, int TH, int ACT>
-__global__ void __launch_bounds__(TH, 512 / TH) gn_bwd_cluster_kernel(GnArgs a, int panels) {
-  GnSmem<TH>& sm = *reinterpret_cast<GnSmem<TH>*>(gn_dynamic);
-  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem<TH>))->part;
-  void* const ring = gn_dynamic + sizeof(GnSmem<TH>) + sizeof(GnParts);
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a, int panels) {
+  GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
+  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem))->part;
+  void* const ring = gn_dynamic + sizeof(GnSmem) + sizeof(GnParts);
   int p = a.by_slices.div(blockIdx.x), turn = 0;
   const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
-  GnUnit u = gn_unit<VEC, TH>(a, p, rank);
-  Rows<T, VEC, TH, 2> rows;
-  gn_bwd_rows<T, VEC, TH>(a, u, rows.p);
+  GnUnit u = gn_unit<VEC>(a, p, rank);
+  Rows<T, VEC, 2> rows;
+  gn_bwd_rows<T, VEC>(a, u, rows.p);
   rows.step[0] = (int64_t)u.TY * a.x_row;
   rows.step[1] = (int64_t)u.TY * a.dy_row;
   rows.start(u.rows, ring);
   while (true) {
-    gn_bwd_stats_unit<T, VEC, TH, ACT>(a, u, sm, rows, part[turn]);
+    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, part[turn], 1);
     cluster_arrive();
     cluster_wait();
-    gn_combine_cluster<true, TH>(a, u, sm, part[turn]);
+    gn_combine_cluster<true>(a, u, sm, part[turn]);
     p += clusters;
-    const GnUnit v = gn_unit<VEC, TH>(a, p < panels ? p : 0, rank);
+    const GnUnit v = gn_unit<VEC>(a, p < panels ? p : 0, rank);
     const T* q[2];
-    gn_bwd_rows<T, VEC, TH>(a, v, q);
-    gn_bwd_apply_unit<T, VEC, TH, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
+    gn_bwd_rows<T, VEC>(a, v, q);
+    gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
       rows.again(o, ostep, body, q, p < panels ? v.rows : 0);
     });
     if (p >= panels) break;
