@@ -131,7 +131,13 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
   a->row = (dim / 2 + 3) / 4 * 4;
   a->wide = 1;
   while (a->wide < rot / 2) a->wide *= 2;
-  const int total = a->side[0].heads + a->side[1].heads;
+  // What a token costs a side: its heads' rows, and its angles, which cost a
+  // thread about a sixth of a row.
+  int64_t cost[2], all = 0;
+  for (int s = 0; s < 2; ++s) {
+    cost[s] = a->side[s].heads > 0 ? (int64_t)a->side[s].heads * lanes * 6 + rot / 2 : 0;
+    all += cost[s];
+  }
   int most_tile = kRopeMaxTable / a->row;
   if (most_tile > kRopeMaxTile) most_tile = kRopeMaxTile;
   for (int s = 0; s < 2; ++s) {
@@ -146,7 +152,7 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
     // device would not have a CTA for each of its places.
     const int64_t rounds = (d.heads + d.head_lanes - 1) / d.head_lanes;
     int64_t tile = (kRopeItems + rounds - 1) / rounds * d.token_lanes;
-    const int64_t places = (int64_t)sms * per_sm * d.heads / total;
+    const int64_t places = sms * per_sm * cost[s] / all;
     const int64_t even = a->batch * a->tokens / (places > 0 ? places : 1);
     if (tile > even) tile = even;
     if (tile < d.token_lanes && a->batch * a->tokens >= d.token_lanes * (int64_t)sms / 4)
