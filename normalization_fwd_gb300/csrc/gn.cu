@@ -9,9 +9,9 @@
 
 namespace nf {
 
-const void* gn_table_f32(bool bwd, bool cluster, bool vec, int act);
-const void* gn_table_bf16(bool bwd, bool cluster, bool vec, int act);
-const void* gn_table_f16(bool bwd, bool cluster, bool vec, int act);
+const void* gn_table_f32(bool bwd, bool cluster, bool fine, int act);
+const void* gn_table_bf16(bool bwd, bool cluster, bool fine, int act);
+const void* gn_table_f16(bool bwd, bool cluster, bool fine, int act);
 
 namespace {
 
@@ -35,53 +35,55 @@ int gcd(int a, int b) {
 struct GnPlan {
   bool cluster;            // one launch, a cluster a panel
   int clusters;            // of the launch
-  int tiles, tw, max_groups, slices;
+  int tiles, tile_ch, tw, max_groups, slices;
   int64_t slice_rows;
   int64_t panels, batch;   // all panels, and those of one launch
   size_t part_bytes, cols_bytes;
   size_t bytes() const { return part_bytes + cols_bytes; }
 };
 
+constexpr int kGnMaxVecs = 64;                 // most vectors of a tile
 constexpr int kPerSm[2] = {3, 2};            // resident CTAs, forward and backward
 constexpr int64_t kBatchBytes[2] = {68ll << 20, 90ll << 20};
 constexpr int64_t kSlabBytes = 4ll << 20;
 
-// Column tiles of about `bytes`, of whole groups and whole vectors where lv,
-// the vectors that both fill, is no more than `most`; false when a tile may
-// end inside a group. A vector has vb bytes.
-bool gn_tiles(int nv, int lv, int bytes, int vb, int most, GnPlan* p) {
-  const int target = bytes / vb < most ? (bytes / vb > 0 ? bytes / vb : 1) : most;
-  int tw = nv;
-  bool whole = true;
-  if (nv > target) {
-    if (lv <= most) {
-      const int units = nv / lv;
-      int per = (target + lv - 1) / lv;
-      if (per * lv > most) per = most / lv;
+// Column tiles of about `bytes`: of whole groups that start on the rows'
+// alignment, in units of `unit` channels, where a tile can be that wide; false
+// when a tile may end inside a group.
+bool gn_tiles(int channels, int unit, int bytes, int es, GnPlan* p) {
+  const int V = 16 / es, most = kGnMaxVecs * V;
+  int target = bytes / es;
+  if (target > most) target = most;
+  int ch = channels;
+  bool whole = channels <= most;
+  if (channels > target) {
+    if (unit <= most) {
+      whole = true;
+      const int units = (channels + unit - 1) / unit;
+      int per = (target + unit - 1) / unit;
+      if (per * unit > most) per = most / unit;
       if (per > units) per = units;
       const int t = (units + per - 1) / per;
-      tw = (units + t - 1) / t * lv;
-    } else {
-      const int t = (nv + target - 1) / target;
-      tw = (nv + t - 1) / t;
-      whole = false;
+      ch = (units + t - 1) / t * unit;
+      if (ch > channels) ch = channels;
+    } else if (!whole) {
+      const int t = (channels + target - 1) / target;
+      ch = ((channels + t - 1) / t + V - 1) / V * V;
     }
   }
-  p->tw = tw;
-  p->tiles = (nv + tw - 1) / tw;
+  p->tile_ch = ch;
+  p->tw = (ch + V - 1) / V;
+  p->tiles = (channels + ch - 1) / ch;
   return whole;
 }
 
-bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es, bool bwd, bool vec,
-             int sms, GnPlan* p) {
-  const int V = vec ? (int)(16 / es) : 1;
-  const int nv = channels / V, cpg = channels / groups;
-  const int most = vec ? 64 : 256;
-  const int vb = V * (int)es;
-  const int lv = cpg / gcd(cpg, V);
+bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t elem, bool bwd,
+             int grain, int sms, GnPlan* p) {
+  const int es = (int)elem, cpg = channels / groups;
+  const int unit = cpg * (grain / gcd(cpg * es, grain));
   const int64_t places = (int64_t)sms * kPerSm[bwd];
   const auto max_groups = [&](bool whole) {
-    const int tc = p->tw * V;
+    const int tc = p->tile_ch;
     const int m = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
     return m < groups ? m : groups;
   };
@@ -89,13 +91,16 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
   // much as some eight rows of each thread, so there are no more CTAs than it
   // takes to give every SM one and most a second (1.5 an SM): narrow tiles
   // first, which make more panels, then clusters of more CTAs.
-  bool whole = gn_tiles(nv, lv, 128, vb, most, p);
-  while (whole && samples * p->tiles * 8 < (int64_t)sms * 3 / 2 && p->tw > lv &&
-         (p->tw - lv) * vb >= 64)
-    whole = gn_tiles(nv, lv, (p->tw - lv) * vb, vb, most, p);
+  bool whole = gn_tiles(channels, unit, 128, es, p);
+  while (whole && samples * p->tiles * 8 < (int64_t)sms * 3 / 2 && p->tile_ch > unit &&
+         (p->tile_ch - unit) * es >= 64) {
+    const int was = p->tile_ch;
+    whole = gn_tiles(channels, unit, (was - unit) * es, es, p);
+    if (p->tile_ch >= was) break;
+  }
   p->panels = samples * p->tiles;
   p->max_groups = max_groups(whole);
-  double slab = (double)rows * p->tw * vb * (bwd ? 2 : 1);   // what a panel reads
+  double slab = (double)rows * p->tile_ch * es * (bwd ? 2 : 1);   // what a panel reads
   p->cluster = whole && slab <= (double)kSlabBytes;
   p->clusters = 0;
   if (p->cluster) {
@@ -114,10 +119,10 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t es,
   } else {
     // Batches whose rows stay in the L2 cache from the launch that sums them
     // to the one that applies them.
-    whole = gn_tiles(nv, lv, 128, vb, most, p);
+    whole = gn_tiles(channels, unit, 128, es, p);
     p->panels = samples * p->tiles;
     p->max_groups = max_groups(whole);
-    slab = (double)rows * p->tw * vb * (bwd ? 2 : 1);
+    slab = (double)rows * p->tile_ch * es * (bwd ? 2 : 1);
     p->batch = p->panels;
     if (slab * p->panels > (double)kBatchBytes[bwd]) {
       const int64_t step = whole ? 1 : p->tiles;
@@ -166,23 +171,27 @@ Strided tensor(const void* p, int64_t sample, int64_t row, const GnCall& c) {
   return s;
 }
 
-bool vec_ok(const void* p, int64_t sample, int64_t row, size_t es) {
-  return aligned(p, 16) && (sample * (int64_t)es) % 16 == 0 && (row * (int64_t)es) % 16 == 0;
+// The bytes that a tensor's rows are aligned to, `most` at most.
+int grain_of(const Strided& s, int most) {
+  if (s.empty()) return most;
+  while (most > 1 &&
+         (!aligned(s.p, most) || s.width % most != 0 || (s.n[0] > 1 && s.stride[0] % most != 0) ||
+          (s.n[1] > 1 && s.stride[1] % most != 0)))
+    most /= 2;
+  return most;
 }
 
-// The plan of a call whose pointers allow vectors or not; the vector plan
-// and the scalar plan differ in their need of workspace.
-ln_status plan_call(const GnCall& c, bool bwd, bool vec, GnPlan* p) {
+ln_status plan_call(const GnCall& c, bool bwd, int grain, GnPlan* p) {
   int sms = 0;
   const cudaError_t e = (cudaError_t)device_sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
-  return gn_plan(c.samples, c.rows, (int)c.channels, (int)c.groups, elem_size(c.dtype), bwd, vec,
+  return gn_plan(c.samples, c.rows, (int)c.channels, (int)c.groups, elem_size(c.dtype), bwd, grain,
                  sms, p)
              ? LN_OK
              : LN_ERR_SHAPE;
 }
 
-ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec, int act,
+ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, int grain, int act,
                  cudaStream_t st) {
   a.slice_rows = p.slice_rows;
   a.slices = p.slices;
@@ -190,21 +199,23 @@ ln_status launch(const GnCall& c, const GnPlan& p, GnArgs a, bool bwd, bool vec,
   a.groups = (int)c.groups;
   a.cpg = (int)(c.channels / c.groups);
   a.tiles = p.tiles;
+  a.tile_ch = p.tile_ch;
   a.tw = p.tw;
+  a.grain = grain;
+  a.by_tile_ch.set(p.tile_ch);
   a.max_groups = p.max_groups;
   a.by_slices.set(p.slices);
   a.by_tiles.set(p.tiles);
   a.by_tw.set(p.tw);
-  a.by_tc.set(p.tw * (vec ? (int)(16 / elem_size(c.dtype)) : 1));
+  a.by_tc.set(p.tw * (int)(16 / elem_size(c.dtype)));
   a.by_ty.set(kGnThreads / p.tw);
   a.by_cpg.set(a.cpg);
   a.rows = c.rows;
   a.inv_m = (float)(1.0 / ((double)c.rows * a.cpg));
-  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, vec, act)
-                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, vec, act)
-                                        : gn_table_f16(bwd, p.cluster, vec, act);
-  const int tensors = !vec ? 0 : bwd ? 2 : 1;
-  const size_t smem = gn_smem_bytes(tensors, p.cluster);
+  const void* fn = c.dtype == LN_F32    ? gn_table_f32(bwd, p.cluster, grain < 16, act)
+                   : c.dtype == LN_BF16 ? gn_table_bf16(bwd, p.cluster, grain < 16, act)
+                                        : gn_table_f16(bwd, p.cluster, grain < 16, act);
+  const size_t smem = gn_smem_bytes(bwd ? 2 : 1, p.cluster);
   const cudaError_t opt = (cudaError_t)allow_dyn_smem(fn, smem);
   if (opt != cudaSuccess) return cuda_fail(opt);
   if (p.cluster) {
@@ -270,10 +281,10 @@ ln_status gn_workspace_bytes(int64_t samples, int64_t rows, int64_t channels, in
   *bytes = 0;
   if (samples == 0 || rows == 0) return LN_OK;
   size_t need = 0;
-  for (int v = 0; v < 2; ++v) {
-    if (v && (channels * (int64_t)elem_size(dtype)) % 16 != 0) continue;
+  for (int grain = 16; grain >= (int)elem_size(dtype); grain /= 2) {
+    if ((channels * (int64_t)elem_size(dtype)) % grain != 0) continue;
     GnPlan p;
-    s = plan_call(c, backward != 0, v != 0, &p);
+    s = plan_call(c, backward != 0, grain, &p);
     if (s != LN_OK) return s;
     if (p.bytes() > need) need = p.bytes();
   }
@@ -317,11 +328,9 @@ ln_status gn_fwd(const void* x, int64_t x_sample, int64_t x_row, const void* gam
     if (e == cudaSuccess && rstd) e = cudaMemsetAsync(rstd, 0, stats, stream);
     return e == cudaSuccess ? LN_OK : cuda_fail(e);
   }
-  const bool vec = (channels * (int64_t)es) % 16 == 0 && vec_ok(x, x_sample, x_row, es) &&
-                   vec_ok(y, y_sample, y_row, es) && vec_ok(gamma, param_sample, 0, es) &&
-                   vec_ok(beta, param_sample, 0, es);
+  const int grain = grain_of(sy, grain_of(sx, 16));
   GnPlan p;
-  s = plan_call(c, false, vec, &p);
+  s = plan_call(c, false, grain, &p);
   if (s != LN_OK) return s;
   if (p.bytes() > 0 &&
       (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < p.bytes()))
@@ -341,7 +350,7 @@ ln_status gn_fwd(const void* x, int64_t x_sample, int64_t x_row, const void* gam
   a.param_sample = param_sample;
   a.eps = eps;
   a.zero_centered = zero_centered_gamma ? 1 : 0;
-  return launch(c, p, a, false, vec, (int)act, stream);
+  return launch(c, p, a, false, grain, (int)act, stream);
 }
 
 ln_status gn_bwd(const void* dy, int64_t dy_sample, int64_t dy_row, const void* x,
@@ -389,11 +398,9 @@ ln_status gn_bwd(const void* dy, int64_t dy_sample, int64_t dy_row, const void* 
     return e == cudaSuccess ? LN_OK : cuda_fail(e);
   }
   if (grad_rows > 65535) return LN_ERR_SHAPE;   // rows of the finalize's grid
-  const bool vec = (channels * (int64_t)es) % 16 == 0 && vec_ok(x, x_sample, x_row, es) &&
-                   vec_ok(dy, dy_sample, dy_row, es) && vec_ok(dx, dx_sample, dx_row, es) &&
-                   vec_ok(gamma, param_sample, 0, es) && vec_ok(beta, param_sample, 0, es);
+  const int grain = grain_of(so, grain_of(sd, grain_of(sx, 16)));
   GnPlan p;
-  s = plan_call(c, true, vec, &p);
+  s = plan_call(c, true, grain, &p);
   if (s != LN_OK) return s;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < p.bytes())
     return LN_ERR_WORKSPACE;
@@ -415,7 +422,7 @@ ln_status gn_bwd(const void* dy, int64_t dy_sample, int64_t dy_row, const void* 
   a.out_row = dx_row;
   a.param_sample = param_sample;
   a.zero_centered = zero_centered_gamma ? 1 : 0;
-  s = launch(c, p, a, true, vec, (int)act, stream);
+  s = launch(c, p, a, true, grain, (int)act, stream);
   if (s != LN_OK || (dgamma == nullptr && dbeta == nullptr)) return s;
   const int H = (int)channels;
   const int64_t P = (param_sample != 0 ? 1 : samples) * p.slices;

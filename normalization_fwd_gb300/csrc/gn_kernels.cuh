@@ -7,9 +7,8 @@
 // from which c1 = sum_{c in group} w A / M, c2 = sum_{c in group} w B / M,
 //   dx = rstd * (w dz - c1 - xhat c2), dgamma = sum_n B, dbeta = sum_n A.
 //
-// A thread owns one 16-byte vector of channels (one element where rows are
-// not 16-byte aligned) for the whole launch, so every sum over rows stays in
-// its registers; the CTA then adds up its columns in shared memory, and one
+// A thread owns 16 bytes of channels for the whole launch, so every sum over
+// rows stays in its registers; the CTA then adds up its columns in shared memory, and one
 // warp a group merges the columns. Sums are fp32. Values go in pairs, which
 // this part adds, multiplies and fmas in one instruction.
 #pragma once
@@ -47,9 +46,11 @@ struct GnArgs {
   int cpg;               // channels of a group
   int groups;
   int tiles;             // column tiles
-  int tw;                // vectors of a column tile
+  int tile_ch;           // channels of a tile
+  int tw;                // vectors of a tile, the last of which may be in part
+  int grain;             // bytes of an access: 16, 8, 4 or 2, what rows are aligned to
   int max_groups;        // most groups that meet one tile
-  FastDiv by_slices, by_tiles, by_tw, by_tc, by_ty, by_cpg;
+  FastDiv by_slices, by_tiles, by_tile_ch, by_tw, by_tc, by_ty, by_cpg;
   float eps;
   float inv_m;           // 1 / (rows * cpg)
   int zero_centered;
@@ -142,24 +143,53 @@ template <int ACT, int NP> __device__ __forceinline__ void through(float2* d, co
 }
 
 // ---- a thread's VEC elements, as NP pairs ---------------------------------------
-// A vector of 16 bytes, or one element (whose pair has an idle second half).
+// Sixteen bytes in registers, and one access in memory. FINE: rows that are
+// not aligned to 16 bytes are moved `grain` bytes at a time, what they are
+// aligned to, and the first `valid` elements only (all but a row's last
+// vector have all of them).
 template <typename T, int VEC> struct Pack {
-  static constexpr int NP = VEC / 2;
-  uint4 v;
-  __device__ __forceinline__ void load(const T* p) { v = ld_vec(p); }
-  __device__ __forceinline__ void store(T* p) const { st_vec(p, v); }
+  static constexpr int NP = VEC / 2, B = (int)sizeof(T);
+  union {
+    uint4 v;
+    uint2 d[2];
+    unsigned w[4];
+    T t[VEC];
+  };
+  __device__ __forceinline__ Pack() {}
+  template <bool FINE> __device__ __forceinline__ void load(const T* p, int grain, int valid) {
+    if (!FINE) {
+      v = ld_vec(p);
+    } else if (B == 4 || grain > 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * (4 / B) < valid) w[i] = reinterpret_cast<const unsigned*>(p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i < valid) t[i] = p[i];
+    }
+  }
+  template <bool FINE>
+  __device__ __forceinline__ void store(T* p, int grain, int valid) const {
+    if (!FINE) {
+      st_vec(p, v);
+    } else if (grain == 8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (i * (8 / B) < valid) reinterpret_cast<uint2*>(p)[i] = d[i];
+    } else if (B == 4 || grain == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * (4 / B) < valid) reinterpret_cast<unsigned*>(p)[i] = w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i < valid) p[i] = t[i];
+    }
+  }
   __device__ __forceinline__ void get(float2* f) const { unpack2<T>(v, f); }
   __device__ __forceinline__ void set(const float2* f) { v = pack2<T>(f); }
   __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
-};
-template <typename T> struct Pack<T, 1> {
-  static constexpr int NP = 1;
-  T v;
-  __device__ __forceinline__ void load(const T* p) { v = *p; }
-  __device__ __forceinline__ void store(T* p) const { *p = v; }
-  __device__ __forceinline__ void get(float2* f) const { f[0] = make_float2(to_f(v), 0.f); }
-  __device__ __forceinline__ void set(const float2* f) { v = from_f<T>(f[0].x); }
-  __device__ __forceinline__ void clear() { v = from_f<T>(0.f); }
 };
 
 // Shared memory: the row lanes' sums before they are added up, and in their
@@ -176,25 +206,17 @@ struct alignas(16) GnSmem {
 };
 
 template <int VEC> __device__ __forceinline__ void put_pairs(float* s, const float2* f) {
-  if (VEC == 1) {
-    s[0] = f[0].x;
-  } else {
 #pragma unroll
-    for (int i = 0; i < VEC / 4; ++i)
-      reinterpret_cast<float4*>(s)[i] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x,
-                                                    f[2 * i + 1].y);
-  }
+  for (int i = 0; i < VEC / 4; ++i)
+    reinterpret_cast<float4*>(s)[i] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x,
+                                                  f[2 * i + 1].y);
 }
 template <int VEC> __device__ __forceinline__ void get_pairs(const float* s, float2* f) {
-  if (VEC == 1) {
-    f[0] = make_float2(s[0], 0.f);
-  } else {
 #pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-      const float4 v = reinterpret_cast<const float4*>(s)[i];
-      f[2 * i] = make_float2(v.x, v.y);
-      f[2 * i + 1] = make_float2(v.z, v.w);
-    }
+  for (int i = 0; i < VEC / 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(s)[i];
+    f[2 * i] = make_float2(v.x, v.y);
+    f[2 * i + 1] = make_float2(v.z, v.w);
   }
 }
 
@@ -206,11 +228,12 @@ struct GnUnit {
   int c0, nc;            // first channel, number of channels of the tile
   int g0, ng;            // its groups
   int64_t r0, nr;        // rows of the slice
-  int tc;                // channels of a full tile
+  int tc;                // places of a tile's channels, tw * VEC
   int TY;                // row lanes
   int tx, ty;            // the thread's vector and row lane
   int rows;              // its rows
-  bool on;               // it has a vector
+  int valid;             // elements of its vector
+  bool on;               // it has one
 };
 template <int VEC>
 __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice) {
@@ -219,8 +242,8 @@ __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice)
   u.tile = panel - u.n * a.tiles;
   u.slice = slice;
   u.tc = a.tw * VEC;
-  u.c0 = u.tile * u.tc;
-  u.nc = min(a.channels - u.c0, u.tc);
+  u.c0 = u.tile * a.tile_ch;
+  u.nc = min(a.channels - u.c0, a.tile_ch);
   u.g0 = a.by_cpg.div(u.c0);
   u.ng = a.by_cpg.div(u.c0 + u.nc - 1) - u.g0 + 1;
   u.r0 = min(a.rows, (int64_t)slice * a.slice_rows);   // a cluster's last CTAs may have none
@@ -228,7 +251,8 @@ __device__ __forceinline__ GnUnit gn_unit(const GnArgs& a, int panel, int slice)
   u.TY = a.by_tw.div(kGnThreads);
   u.ty = a.by_tw.div(threadIdx.x);
   u.tx = threadIdx.x - u.ty * a.tw;
-  u.on = u.ty < u.TY && u.tx * VEC < u.nc;
+  u.valid = min(u.nc - u.tx * VEC, VEC);
+  u.on = u.ty < u.TY && u.valid > 0;
   u.rows = u.on && u.nr > u.ty ? a.by_ty.div((int)(u.nr - u.ty - 1)) + 1 : 0;
   return u;
 }
@@ -261,13 +285,9 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
                                            const float2* va, const float2* vb, F&& done) {
   if (u.on) {
     float2* to = sm.lane + u.ty * u.tc + u.tx * VEC;
-    if (VEC == 1) {
-      to[0] = make_float2(va[0].x, vb[0].x);
-    } else {
 #pragma unroll
-      for (int i = 0; i < VEC / 2; ++i)
-        reinterpret_cast<float4*>(to)[i] = make_float4(va[i].x, vb[i].x, va[i].y, vb[i].y);
-    }
+    for (int i = 0; i < VEC / 2; ++i)
+      reinterpret_cast<float4*>(to)[i] = make_float4(va[i].x, vb[i].x, va[i].y, vb[i].y);
   }
   __syncthreads();
   const int parts = a.by_tc.div(kGnThreads);   // threads a column
@@ -302,27 +322,55 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
 // its own copies): kGnRing rows are on their way at any time, in steps of
 // kGnStep rows. Of a pass over more rows than that the last kGnRing stay in
 // the slots, and a second pass starts with those while it fetches the others
-// again. Without slots (VEC = 1) rows go straight to registers.
+// again. Copies are of 16, 8 or 4 bytes, by the rows' alignment; rows that are
+// aligned to 2 bytes pass through registers.
 __device__ __forceinline__ void copy_async16(unsigned dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N> __device__ __forceinline__ void copy_async(unsigned dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int VEC, int TENSORS> struct Rows {
+template <typename T, int VEC, int TENSORS, bool FINE> struct Rows {
   static constexpr int NG = kGnRing / kGnStep;   // steps in flight
   const T* p[TENSORS];      // the thread's first row
   int64_t step[TENSORS];    // from one of its rows to the next
   const T* next[TENSORS];   // the next one to fetch
   int rows, steps;
+  int grain, valid;         // of the copies
+  int held;                 // valid elements of what is in the slots
   unsigned place;           // in the ring, of step 0
   unsigned slots;           // this thread's first slot
   Pack<T, VEC> v[TENSORS][kGnStep];
 
   __device__ __forceinline__ unsigned at(unsigned place) const {
     return slots + place % NG * (kGnStep * kGnThreads * 16);
+  }
+  // A vector, from memory into a slot.
+  __device__ __forceinline__ void copy(unsigned to, const T* from) const {
+    constexpr int B = (int)sizeof(T);
+    if (!FINE) {
+      copy_async16(to, from);
+    } else if (B == 2 && grain == 2) {
+      Pack<T, VEC> x;
+      x.template load<true>(from, 2, valid);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(x.v.x), "r"(x.v.y),
+                   "r"(x.v.z), "r"(x.v.w)
+                   : "memory");
+    } else if (grain == 8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (i * (8 / B) < valid) copy_async<8>(to + 8 * i, from + i * (8 / B));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * (4 / B) < valid) copy_async<4>(to + 4 * i, from + i * (4 / B));
+    }
   }
   // Step g of n rows, into a place of the ring.
   __device__ __forceinline__ void fetch(int g, int n, unsigned place) {
@@ -332,7 +380,7 @@ template <typename T, int VEC, int TENSORS> struct Rows {
       if (g * kGnStep + j < n) {
 #pragma unroll
         for (int t = 0; t < TENSORS; ++t) {
-          copy_async16(to + t * (kGnRing * kGnThreads * 16) + j * (kGnThreads * 16), next[t]);
+          copy(to + t * (kGnRing * kGnThreads * 16) + j * (kGnThreads * 16), next[t]);
           next[t] += step[t];
         }
       }
@@ -348,6 +396,14 @@ template <typename T, int VEC, int TENSORS> struct Rows {
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                      : "r"(from + t * (kGnRing * kGnThreads * 16) + j * (kGnThreads * 16)));
+        // What is behind the row counts as 0: it shares reciprocals with the rest.
+        if (FINE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int left = held * (int)sizeof(T) - 4 * i;
+            v[t][j].w[i] &= left >= 4 ? ~0u : left == 2 ? 0xffffu : 0u;
+          }
+        }
       }
   }
   __device__ __forceinline__ void rewind() {
@@ -358,101 +414,73 @@ template <typename T, int VEC, int TENSORS> struct Rows {
     rows = n;
     steps = (n + kGnStep - 1) / kGnStep;
   }
-  // Start the first pass (or the only one) over n rows.
-  __device__ __forceinline__ void start(int n, void* ring) {
-    take_rows(n);
+  // Start the first pass (or the only one) over a unit's rows.
+  __device__ __forceinline__ void start(const GnArgs& a, const GnUnit& u, void* ring) {
+    take_rows(u.rows);
+    grain = a.grain;
+    valid = held = u.valid;
     place = 0;
     slots = (unsigned)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
-    if constexpr (VEC > 1) {
-      rewind();
+    rewind();
 #pragma unroll
-      for (int g = 0; g < NG; ++g) fetch(g, rows, g);
-    }
+    for (int g = 0; g < NG; ++g) fetch(g, rows, g);
   }
   // body(j, to) for every row, j its place in v, `to` its place in an output
   // whose first row is at `o`.
   template <typename F> __device__ __forceinline__ void pass(T* o, int64_t ostep, F&& body) {
-    if constexpr (VEC > 1) {
-      for (int g = 0; g < steps; ++g) {
-        copy_wait<NG - 1>();
-        take(place + g);
+    for (int g = 0; g < steps; ++g) {
+      copy_wait<NG - 1>();
+      take(place + g);
 #pragma unroll
-        for (int j = 0; j < kGnStep; ++j) {
-          if (g * kGnStep + j < rows) body(j, o);
-          o += ostep;
-        }
-        fetch(g + NG, rows, place + g);
+      for (int j = 0; j < kGnStep; ++j) {
+        if (g * kGnStep + j < rows) body(j, o);
+        o += ostep;
       }
-    } else {
-      direct(o, ostep, body);
+      fetch(g + NG, rows, place + g);
     }
   }
   // The second pass over the same rows, those in the slots first; places that
-  // it has no more rows for take the first ones of another unit's n rows at q.
+  // it has no more rows for take the first ones of another unit at q.
   template <typename F>
-  __device__ __forceinline__ void again(T* o, int64_t ostep, F&& body, const T* const* q, int n) {
-    if constexpr (VEC > 1) {
-      const int far = steps > NG ? steps - NG : 0;   // steps that have left the slots
-      rewind();
-      T* const first = o;
-      o += far * kGnStep * ostep;
-      place += far;
-      // Steps far, ..., steps - 1 out of their slots, which take 0, 1, ... after them.
-      for (int k = 0; k < steps; ++k) {
-        const int g = far + k < steps ? far + k : far + k - steps;
-        if (g == 0) o = first;
-        copy_wait<NG - 1>();
-        take(place + k);
+  __device__ __forceinline__ void again(T* o, int64_t ostep, F&& body, const T* const* q, int n,
+                                        int n_valid) {
+    const int far = steps > NG ? steps - NG : 0;   // steps that have left the slots
+    rewind();
+    T* const first = o;
+    o += far * kGnStep * ostep;
+    place += far;
+    // Steps far, ..., steps - 1 out of their slots, which take 0, 1, ... after them.
+    for (int k = 0; k < steps; ++k) {
+      const int g = far + k < steps ? far + k : far + k - steps;
+      if (g == 0) o = first;
+      copy_wait<NG - 1>();
+      take(place + k);
 #pragma unroll
-        for (int j = 0; j < kGnStep; ++j) {
-          if (g * kGnStep + j < rows) body(j, o);
-          o += ostep;
-        }
-        if (k == far) {
-#pragma unroll
-          for (int t = 0; t < TENSORS; ++t) next[t] = q[t];
-        }
-        if (k < far) fetch(k, rows, place + k);
-        else fetch(k - far, n, place + k);
+      for (int j = 0; j < kGnStep; ++j) {
+        if (g * kGnStep + j < rows) body(j, o);
+        o += ostep;
       }
-      if (steps == 0) {
+      if (k == far) {
 #pragma unroll
         for (int t = 0; t < TENSORS; ++t) next[t] = q[t];
       }
-      place += far;
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-        if (g >= steps) fetch(g, n, place + g);
-    } else {
-      direct(o, ostep, body);
+      valid = k < far ? held : n_valid;
+      if (k < far) fetch(k, rows, place + k);
+      else fetch(k - far, n, place + k);
     }
+    if (steps == 0) {
+#pragma unroll
+      for (int t = 0; t < TENSORS; ++t) next[t] = q[t];
+    }
+    valid = n_valid;
+    place += far;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      if (g >= steps) fetch(g, n, place + g);
 #pragma unroll
     for (int t = 0; t < TENSORS; ++t) p[t] = q[t];
     take_rows(n);
-  }
-  template <typename F> __device__ __forceinline__ void direct(T* o, int64_t ostep, F&& body) {
-    constexpr int UN = 8 / TENSORS;
-    int r = 0;
-    for (; r + UN <= rows; r += UN) {
-      Pack<T, VEC> q[TENSORS][UN];
-#pragma unroll
-      for (int j = 0; j < UN; ++j)
-#pragma unroll
-        for (int t = 0; t < TENSORS; ++t) q[t][j].load(p[t] + (r + j) * step[t]);
-#pragma unroll
-      for (int j = 0; j < UN; ++j) {
-#pragma unroll
-        for (int t = 0; t < TENSORS; ++t) v[t][0] = q[t][j];
-        body(0, o);
-        o += ostep;
-      }
-    }
-    for (; r < rows; ++r) {
-#pragma unroll
-      for (int t = 0; t < TENSORS; ++t) v[t][0].load(p[t] + r * step[t]);
-      body(0, o);
-      o += ostep;
-    }
+    held = n_valid;
   }
 };
 
@@ -463,9 +491,9 @@ template <typename T, int VEC, int TENSORS> struct Rows {
 // at most about n * 2^-24 of the group's sum of squares, whatever the mean.
 // Columns, and later slices, are merged by the parallel-variance identity
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
-template <typename T, int VEC>
+template <typename T, int VEC, bool FINE>
 __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              Rows<T, VEC, 1>& rows, float2* out,
+                                              Rows<T, VEC, 1, FINE>& rows, float2* out,
                                               int stride) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 k[NP], s1[NP], s2[NP], v[NP];
@@ -473,7 +501,8 @@ __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, 
   for (int i = 0; i < NP; ++i) k[i] = s1[i] = s2[i] = splat2(0.f);
   if (u.rows > 0) {
     Pack<T, VEC> first;
-    first.load(rows.p[0] - u.ty * a.x_row);
+    first.clear();
+    first.template load<FINE>(rows.p[0] - u.ty * a.x_row, a.grain, u.valid);
     first.get(k);
   }
   rows.pass(static_cast<T*>(nullptr), 0, [&](int j, T*) {
@@ -542,12 +571,12 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     const int g = u.g0 + lg, ch0 = g * a.cpg, ch1 = ch0 + a.cpg;
-    const int t0 = a.by_tc.div(ch0), t1 = a.by_tc.div(ch1 - 1);
+    const int t0 = a.by_tile_ch.div(ch0), t1 = a.by_tile_ch.div(ch1 - 1);
     float s0 = 0.f, s1 = 0.f, base = 0.f;
     float2 v[N];
     const auto fetch = [&](int t) {
       const float2* p = a.part + (((int64_t)u.n * a.tiles + t) * a.max_groups +
-                                  (g - a.by_cpg.div(t * u.tc))) * a.slices;
+                                  (g - a.by_cpg.div(t * a.tile_ch))) * a.slices;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         v[j] = make_float2(0.f, 0.f);
@@ -556,7 +585,7 @@ __device__ __forceinline__ void gn_combine(const GnArgs& a, const GnUnit& u, GnS
     };
     // values of the group in slice i of tile t
     const auto count = [&](int t, int i) {
-      const int nc = min(ch1, (t + 1) * u.tc) - max(ch0, t * u.tc);
+      const int nc = min(ch1, (t + 1) * a.tile_ch) - max(ch0, t * a.tile_ch);
       return (float)min(a.slice_rows, a.rows - i * a.slice_rows) * (float)nc;
     };
     for (int t = t0; t <= t1; ++t) {
@@ -635,15 +664,19 @@ __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit
 }
 
 // ---- forward: normalize one unit -------------------------------------------------
-template <typename T, int VEC, int ACT, typename W>
+template <typename T, int VEC, int ACT, bool FINE, typename W>
 __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                              Rows<T, VEC, 1>& rows, W&& walk) {
+                                              Rows<T, VEC, 1, FINE>& rows, W&& walk) {
   constexpr int NP = Pack<T, VEC>::NP;
-  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-    const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
-    sm.par[0][c] = -sm.g0[lg];
-    sm.par[1][c] = gn_weight<T>(a, u, c) * sm.g1[lg];
-    sm.par[2][c] = gn_bias<T>(a, u, c);
+  for (int c = threadIdx.x; c < u.tc; c += kGnThreads) {
+    if (c < u.nc) {
+      const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
+      sm.par[0][c] = -sm.g0[lg];
+      sm.par[1][c] = gn_weight<T>(a, u, c) * sm.g1[lg];
+      sm.par[2][c] = gn_bias<T>(a, u, c);
+    } else {
+      sm.par[0][c] = sm.par[1][c] = sm.par[2][c] = 0.f;
+    }
   }
   __syncthreads();
   float2 m[NP], w[NP], b[NP], v[NP];
@@ -659,7 +692,7 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
     activate<ACT, NP>(v);
     Pack<T, VEC> y;
     y.set(v);
-    y.store(to);
+    y.template store<FINE>(to, a.grain, u.valid);
   };
   walk(o, ostep, body);
 }
@@ -668,19 +701,23 @@ __device__ __forceinline__ void gn_apply_unit(const GnArgs& a, const GnUnit& u, 
 // mean, rstd, w and beta of the unit's columns.
 template <typename T>
 __device__ __forceinline__ void gn_bwd_params(const GnArgs& a, const GnUnit& u, GnSmem& sm) {
-  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-    const int64_t g = (int64_t)u.n * a.groups + a.by_cpg.div(u.c0 + c);
-    sm.par[0][c] = -a.mean[g];
-    sm.par[1][c] = a.rstd[g];
-    sm.par[2][c] = gn_weight<T>(a, u, c);
-    sm.par[3][c] = gn_bias<T>(a, u, c);
+  for (int c = threadIdx.x; c < u.tc; c += kGnThreads) {
+    if (c < u.nc) {
+      const int64_t g = (int64_t)u.n * a.groups + a.by_cpg.div(u.c0 + c);
+      sm.par[0][c] = -a.mean[g];
+      sm.par[1][c] = a.rstd[g];
+      sm.par[2][c] = gn_weight<T>(a, u, c);
+      sm.par[3][c] = gn_bias<T>(a, u, c);
+    } else {
+      sm.par[0][c] = sm.par[1][c] = sm.par[2][c] = sm.par[3][c] = 0.f;
+    }
   }
 }
 
 // Sums of one unit.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool FINE>
 __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  Rows<T, VEC, 2>& rows, float2* out,
+                                                  Rows<T, VEC, 2, FINE>& rows, float2* out,
                                                   int stride) {
   constexpr int NP = Pack<T, VEC>::NP;
   float2 sa[NP], sb[NP];
@@ -733,13 +770,13 @@ __device__ __forceinline__ void gn_bwd_stats_unit(const GnArgs& a, const GnUnit&
 }
 
 // dx of one unit.
-template <typename T, int VEC, int ACT, typename W>
+template <typename T, int VEC, int ACT, bool FINE, typename W>
 __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
-                                                  Rows<T, VEC, 2>& rows, W&& walk) {
+                                                  Rows<T, VEC, 2, FINE>& rows, W&& walk) {
   constexpr int NP = Pack<T, VEC>::NP;
   gn_bwd_params<T>(a, u, sm);
-  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) {
-    const int lg = a.by_cpg.div(u.c0 + c) - u.g0;
+  for (int c = threadIdx.x; c < u.tc; c += kGnThreads) {
+    const int lg = a.by_cpg.div(u.c0 + min(c, u.nc - 1)) - u.g0;
     sm.par[4][c] = -sm.g0[lg];
     sm.par[5][c] = -sm.g1[lg];
   }
@@ -772,7 +809,7 @@ __device__ __forceinline__ void gn_bwd_apply_unit(const GnArgs& a, const GnUnit&
     }
     Pack<T, VEC> y;
     y.set(v);
-    y.store(to);
+    y.template store<FINE>(to, a.grain, u.valid);
   };
   walk(o, ostep, body);
 }
@@ -804,26 +841,26 @@ __device__ __forceinline__ void gn_bwd_rows(const GnArgs& a, const GnUnit& u, co
 
 // One launch takes the statistics of the panels [stat0, stat1) and applies
 // those of [app0, app1), which an earlier launch gathered.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool FINE>
 __global__ void __launch_bounds__(kGnThreads, 3)
     gn_fwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
   void* const ring = gn_dynamic + sizeof(GnSmem);
   const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Rows<T, VEC, 1> rows;
+  Rows<T, VEC, 1, FINE> rows;
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
     gn_fwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
-    rows.start(u.rows, ring);
+    rows.start(a, u, ring);
     gn_stats_unit<T, VEC>(a, u, sm, rows, gn_part(a, u), a.slices);
   }
   if (app0 + p < app1) {
     const GnUnit u = gn_unit<VEC>(a, app0 + p, s);
     gn_fwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
-    rows.start(u.rows, ring);
+    rows.start(a, u, ring);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     gn_combine<false>(a, u, sm);
     gn_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
@@ -832,20 +869,20 @@ __global__ void __launch_bounds__(kGnThreads, 3)
   }
 }
 
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool FINE>
 __global__ void __launch_bounds__(kGnThreads, 2)
     gn_bwd_kernel(GnArgs a, int stat0, int stat1, int app0, int app1) {
   GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
   void* const ring = gn_dynamic + sizeof(GnSmem);
   const int p = a.by_slices.div(blockIdx.x), s = blockIdx.x - p * a.slices;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Rows<T, VEC, 2> rows;
+  Rows<T, VEC, 2, FINE> rows;
   if (stat0 + p < stat1) {
     const GnUnit u = gn_unit<VEC>(a, stat0 + p, s);
     gn_bwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
     rows.step[1] = (int64_t)u.TY * a.dy_row;
-    rows.start(u.rows, ring);
+    rows.start(a, u, ring);
     gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, gn_part(a, u), a.slices);
   }
   if (app0 + p < app1) {
@@ -853,7 +890,7 @@ __global__ void __launch_bounds__(kGnThreads, 2)
     gn_bwd_rows<T, VEC>(a, u, rows.p);
     rows.step[0] = (int64_t)u.TY * a.x_row;
     rows.step[1] = (int64_t)u.TY * a.dy_row;
-    rows.start(u.rows, ring);
+    rows.start(a, u, ring);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     gn_combine<true>(a, u, sm);
     gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
@@ -868,7 +905,7 @@ __global__ void __launch_bounds__(kGnThreads, 2)
 // one on their way while it finishes this one. The partials have two places
 // in turn: one is written again only after the barrier of the panel between,
 // which every CTA reaches after it has read them.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool FINE>
 __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a, int panels) {
   GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
   auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem))->part;
@@ -876,10 +913,10 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a,
   int p = a.by_slices.div(blockIdx.x), turn = 0;
   const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
   GnUnit u = gn_unit<VEC>(a, p, rank);
-  Rows<T, VEC, 1> rows;
+  Rows<T, VEC, 1, FINE> rows;
   gn_fwd_rows<T, VEC>(a, u, rows.p);
   rows.step[0] = (int64_t)u.TY * a.x_row;
-  rows.start(u.rows, ring);
+  rows.start(a, u, ring);
   while (true) {
     gn_stats_unit<T, VEC>(a, u, sm, rows, part[turn], 1);
     cluster_arrive();
@@ -890,7 +927,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a,
     const T* q[1];
     gn_fwd_rows<T, VEC>(a, v, q);
     gn_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
-      rows.again(o, ostep, body, q, p < panels ? v.rows : 0);
+      rows.again(o, ostep, body, q, p < panels ? v.rows : 0, v.valid);
     });
     if (p >= panels) break;
     u = v;
@@ -901,7 +938,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a,
   cluster_wait();
 }
 
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool FINE>
 __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a, int panels) {
   GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
   auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem))->part;
@@ -909,11 +946,11 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a,
   int p = a.by_slices.div(blockIdx.x), turn = 0;
   const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
   GnUnit u = gn_unit<VEC>(a, p, rank);
-  Rows<T, VEC, 2> rows;
+  Rows<T, VEC, 2, FINE> rows;
   gn_bwd_rows<T, VEC>(a, u, rows.p);
   rows.step[0] = (int64_t)u.TY * a.x_row;
   rows.step[1] = (int64_t)u.TY * a.dy_row;
-  rows.start(u.rows, ring);
+  rows.start(a, u, ring);
   while (true) {
     gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, part[turn], 1);
     cluster_arrive();
@@ -924,7 +961,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a,
     const T* q[2];
     gn_bwd_rows<T, VEC>(a, v, q);
     gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
-      rows.again(o, ostep, body, q, p < panels ? v.rows : 0);
+      rows.again(o, ostep, body, q, p < panels ? v.rows : 0, v.valid);
     });
     if (p >= panels) break;
     u = v;

@@ -160,6 +160,14 @@ SHAPES = [
     ("bf16", 1, 4099, 40, 4, "silu"),     # many rows, ragged
     ("f16", 1, 16384, 16, 2, "silu"),
     ("f32", 2, 301, 512, 512, "none"),    # as many groups as a tile has channels
+    ("bf16", 2, 333, 250, 5, "silu"),     # rows aligned to 4 and to 8 bytes, last vectors in part
+    ("f16", 3, 65, 20, 4, "gelu"),
+    ("bf16", 1, 700, 6, 3, "silu"),
+    ("f32", 2, 129, 10, 5, "silu"),
+    ("f32", 1, 50, 7, 7, "none"),
+    ("bf16", 2, 40, 650, 13, "none"),     # tiles of whole groups, the last one narrower
+    ("f16", 1, 29, 1026, 2, "silu"),      # groups wider than a tile, rows aligned to 4 bytes
+    ("bf16", 1, 21, 1035, 5, "gelu"),     # and to 2
 ]
 
 
