@@ -138,8 +138,7 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
     cost[s] = a->side[s].heads > 0 ? (int64_t)a->side[s].heads * lanes * 6 + rot / 2 : 0;
     all += cost[s];
   }
-  int most_tile = kRopeMaxTable / a->row;
-  if (most_tile > kRopeMaxTile) most_tile = kRopeMaxTile;
+  const int most_tile = kRopeMaxTable / a->row;
   for (int s = 0; s < 2; ++s) {
     RopeSide& d = a->side[s];
     d.head_lanes = d.heads < per_cta ? (d.heads > 0 ? d.heads : 1) : per_cta;
@@ -209,7 +208,7 @@ void fill(RopeArgs* a, const Shape& c, const rope_positions* r, float eps, int z
   a->axes = (int)r->axes;
   a->dim = (int)c.dim;
   a->rot = (int)r->rot;
-  a->scale = r->scale;
+  a->scale_c = a->scale_s = r->scale;
   a->eps = eps;
   a->inv_dim = 1.0f / (float)c.dim;
   a->zero_centered = zero_centered ? 1 : 0;
@@ -425,8 +424,11 @@ ln_status rope_bwd(const rope_heads_grad* q, const rope_heads_grad* k,
     all[2 + i] = x[i];
     all[4 + i] = out[i];
   }
+  // Without any gamma it is the forward of dy with the angles turned round.
+  const bool norm = a.side[0].gamma != nullptr || a.side[1].gamma != nullptr;
+  if (!norm) a.scale_s = -a.scale_s;
   RopePlan p;
-  s = plan(c, positions, all, 6, true, &a, &p);
+  s = plan(c, positions, all, 6, norm, &a, &p);
   if (s != LN_OK) return s;
   const int rows = a.blocks[0] > a.blocks[1] ? a.blocks[0] : a.blocks[1];
   if (sums && workspace_bytes < (size_t)rows * 2 * head_dim * sizeof(float))

@@ -25,7 +25,6 @@ constexpr int kRopeThreads = 256;
 // Heads that a thread has on their way.
 constexpr int kRopeAheadFwd = 2, kRopeAheadBwd = 1;
 constexpr int kRopeMaxDim = 512;
-constexpr int kRopeMaxTile = 32;      // tokens of a tile
 constexpr int kRopeMaxTable = 2048;   // floats of a tile's cosines, and of its sines
 constexpr int kRopeMaxAxes = 4;
 
@@ -57,7 +56,8 @@ struct RopeArgs {
   int lanes;             // threads of one head, a power of two <= 32
   int row;               // floats of a token's row in the table, a multiple of 4
   int wide;              // threads that work out a token's angles, a power of two
-  float scale, eps, inv_dim;
+  float scale_c, scale_s;  // of the cosines and the sines; the sines' sign turns it round
+  float eps, inv_dim;
   int zero_centered;
 };
 
@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
             }
             float s, c;
             sincos_turns((unsigned)((sum + 0x80000000ull) >> 32), &s, &c);
-            tab_c[t * A.row + j] = c * A.scale;
-            tab_s[t * A.row + j] = s * A.scale;
+            tab_c[t * A.row + j] = c * A.scale_c;
+            tab_s[t * A.row + j] = s * A.scale_s;
           }
         __syncthreads();
       }
