@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   using Raw = RopeRaw<T, VEC, ALIGNED>;
   constexpr int kAhead = BWD ? kRopeAheadBwd : kRopeAheadFwd;
   __shared__ __align__(16) float tab_c[kRopeMaxTable], tab_s[kRopeMaxTable];
+  __shared__ unsigned long long tab_t[kRopeMaxAxes * kRopeMaxDim / 2];   // several axes only
   extern __shared__ float red[];
   const int L = A.lanes, per_cta = kRopeThreads / L;
   const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
@@ -331,7 +332,13 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     }
   const int j = threadIdx.x & (A.wide - 1);      // this thread's pair
   unsigned long long turns = 0;
-  if (A.axes == 1 && j < A.rot / 2) turns = turns_of(A.freqs[j]);
+  if (A.axes == 1) {
+    if (j < A.rot / 2) turns = turns_of(A.freqs[j]);
+  } else {
+    // Read behind the barrier before the first tile's angles.
+    for (int i = threadIdx.x; i < A.axes * (A.rot / 2); i += kRopeThreads)
+      tab_t[i] = turns_of(A.freqs[i]);
+  }
 
   const int64_t in_step = token_lanes * in_t, out_step = token_lanes * out_t,
                 x_step = token_lanes * x_t;
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
               const int64_t at = ax * A.pos_s[0] + b * A.pos_s[1] + (tok0 + t) * A.pos_s[2];
               const int64_t pos = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
                                           : (int64_t)static_cast<const int*>(A.pos)[at];
-              if (A.axes > 1) turns = turns_of(A.freqs[(int64_t)ax * (A.rot / 2) + j]);
+              if (A.axes > 1) turns = tab_t[ax * (A.rot / 2) + j];
               sum += (unsigned long long)pos * turns;
             }
             float s, c;
