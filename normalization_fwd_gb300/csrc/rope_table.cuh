@@ -1,6 +1,6 @@
 // (vector width, slots a lane, layout, direction) -> rotary kernel of one
 // dtype. A lane holds at most 8 pairs, so a head of up to 512 elements takes
-// one slot of VEC pairs a lane, or 8 / VEC of them.
+// 1, 2, ... or 8 / VEC slots of VEC pairs a lane (backward: 1 or 8 / VEC).
 #pragma once
 
 #include "rope_kernels.cuh"
@@ -9,8 +9,10 @@ namespace nf {
 
 template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool FULL>
 const void* rope_dir(bool bwd) {
-  return bwd ? (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, true>
-             : (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, false>;
+  if (!bwd) return (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, false>;
+  if constexpr (NS == 1 || NS == 8 / VEC)
+    return (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, true>;
+  return nullptr;
 }
 template <typename T, int VEC, bool INTER, bool ALIGNED>
 const void* rope_ns(int ns, bool full, bool bwd) {
@@ -18,7 +20,12 @@ const void* rope_ns(int ns, bool full, bool bwd) {
   if constexpr (VEC == Vec<T>::N && ALIGNED)
     if (ns == 1 && full) return rope_dir<T, VEC, 1, INTER, ALIGNED, true>(bwd);
   if (ns == 1) return rope_dir<T, VEC, 1, INTER, ALIGNED, false>(bwd);
-  if (VEC < 8 && ns == 8 / VEC) return rope_dir<T, VEC, 8 / VEC, INTER, ALIGNED, false>(bwd);
+  if constexpr (VEC <= 4)
+    if (ns == 2) return rope_dir<T, VEC, 2, INTER, ALIGNED, false>(bwd);
+  if constexpr (VEC <= 2)
+    if (ns == 4) return rope_dir<T, VEC, 4, INTER, ALIGNED, false>(bwd);
+  if constexpr (VEC == 1)
+    if (ns == 8) return rope_dir<T, VEC, 8, INTER, ALIGNED, false>(bwd);
   return nullptr;
 }
 template <typename T, bool INTER> const void* rope_vec(int vec, int ns, bool aligned, bool full, bool bwd) {
