@@ -101,6 +101,30 @@ template <int NP> __device__ __forceinline__ void sigmoid(const float2* z, float
     for (int i = 0; i < NP; ++i) s[i] = make_float2(rcpf(d[i].x), rcpf(d[i].y));
   }
 }
+// The normal distribution function of a pair, and e^(-z^2/2). Its lower tail
+// is e^(-z^2/2) R(|z|), where R falls from 1/2 like 1 / (sqrt(2 pi) |z|): a
+// polynomial of t = 1 / (1 + p |z|), nine terms without a constant, fitted to
+// the least relative error over [0, 14.5] (2^-26). In fp32 it is good to
+// 12 + 1.5 z^2 roundings, relative, in the lower tail (where (1 + erf) / 2
+// would cancel). A backward over 3 x 85374 x 250 bf16 takes 266 us with it, and
+// took 540 with CUDA's normcdff and an exponential.
+__device__ __forceinline__ void gauss(float2 z, float2* cdf, float2* e) {
+  const float2 d = fma2(make_float2(fabsf(z.x), fabsf(z.y)), splat2(0.26499999f), splat2(1.f));
+  const float2 t = make_float2(rcpf(d.x), rcpf(d.y));
+  const float2 h = mul2(mul2(z, z), splat2(-0.72134752f));
+  *e = make_float2(ex2f(h.x), ex2f(h.y));
+  float2 r = fma2(t, splat2(0.030624436f), splat2(-0.14330049f));
+  r = fma2(r, t, splat2(0.21595012f));
+  r = fma2(r, t, splat2(-0.11428611f));
+  r = fma2(r, t, splat2(0.13655469f));
+  r = fma2(r, t, splat2(0.060895126f));
+  r = fma2(r, t, splat2(0.10255506f));
+  r = fma2(r, t, splat2(0.10526678f));
+  r = fma2(r, t, splat2(0.10574039f));
+  const float2 low = mul2(mul2(r, t), *e);
+  const float2 up = fma2(low, splat2(-1.f), splat2(1.f));
+  *cdf = make_float2(z.x < 0.f ? low.x : up.x, z.y < 0.f ? low.y : up.y);
+}
 // z -> act(z) of NP pairs.
 template <int ACT, int NP> __device__ __forceinline__ void activate(float2* z) {
   if (ACT == kActSilu) {
@@ -109,18 +133,14 @@ template <int ACT, int NP> __device__ __forceinline__ void activate(float2* z) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) z[i] = mul2(z[i], s[i]);
   }
-  // normcdff keeps relative accuracy in the lower tail, where (1 + erf) / 2
-  // cancels.
   if (ACT == kActGelu) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      z[i].x *= normcdff(z[i].x);
-      z[i].y *= normcdff(z[i].y);
+      float2 c, e;
+      gauss(z[i], &c, &e);
+      z[i] = mul2(z[i], c);
     }
   }
-}
-__device__ __forceinline__ float gelu_grad(float z) {
-  return normcdff(z) + z * 0.3989422804f * __expf(-0.5f * z * z);
 }
 // d -> d * act'(z) of NP pairs.
 template <int ACT, int NP> __device__ __forceinline__ void through(float2* d, const float2* z) {
@@ -136,8 +156,9 @@ template <int ACT, int NP> __device__ __forceinline__ void through(float2* d, co
   if (ACT == kActGelu) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      d[i].x *= gelu_grad(z[i].x);
-      d[i].y *= gelu_grad(z[i].y);
+      float2 c, e;
+      gauss(z[i], &c, &e);
+      d[i] = mul2(d[i], fma2(mul2(z[i], splat2(0.39894228f)), e, c));
     }
   }
 }
