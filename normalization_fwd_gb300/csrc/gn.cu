@@ -127,11 +127,14 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t ele
     if (slab * p->panels > (double)kBatchBytes[bwd]) {
       const int64_t step = whole ? 1 : p->tiles;
       int64_t b = (int64_t)(kBatchBytes[bwd] / slab) / step * step;
-      p->batch = b < step ? step : b;
-      if (p->batch > p->panels) p->batch = p->panels;
+      if (b < step) b = step;
+      // As many batches, of about one size.
+      const int64_t n = (p->panels + b - 1) / b;
+      b = ((p->panels + n - 1) / n + step - 1) / step * step;
+      p->batch = b < p->panels ? b : p->panels;
     }
     const int64_t TY = kGnThreads / p->tw;
-    int64_t slices = (places + p->batch - 1) / p->batch;
+    int64_t slices = places / p->batch;   // not a CTA more than fit at a time
     if (slices > kGnMaxSlices) slices = kGnMaxSlices;
     const int64_t least = 4 * TY;       // rows of a slice: four a thread
     if (slices > (rows + least - 1) / least) slices = (rows + least - 1) / least;
