@@ -178,7 +178,7 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
     d.tiles = a->batch * d.row_tiles;
     // Forward: a CTA a tile, so that the device deals them out; backward: no
     // more than a CTA for each place, which leave a row of partials each.
-    const int64_t most = !bwd ? 1 << 30 : places > 0 ? places : 1;
+    const int64_t most = !bwd ? (1 << 30) - 1 : places > 0 ? places : 1;
     a->blocks[s] = (int)(d.tiles < most ? d.tiles : most);
   }
   p->grid = a->blocks[0] + a->blocks[1];
