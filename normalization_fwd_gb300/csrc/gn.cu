@@ -45,7 +45,7 @@ struct GnPlan {
 constexpr int kGnMaxVecs = 64;                 // most vectors of a tile
 constexpr int kPerSm[2] = {3, 2};            // resident CTAs, forward and backward
 constexpr int64_t kBatchBytes[2] = {68ll << 20, 90ll << 20};
-constexpr int64_t kSlabBytes = 4ll << 20;
+constexpr int64_t kSlabBytes = 2ll << 20;
 
 // Column tiles of about `bytes`: of whole groups that start on the rows'
 // alignment, in units of `unit` channels, where a tile can be that wide; false
@@ -87,42 +87,60 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t ele
     const int m = whole ? (tc + cpg - 1) / cpg : (tc - 2 > 0 ? (tc - 2) / cpg : 0) + 2;
     return m < groups ? m : groups;
   };
-  // One launch, a cluster a panel. What a CTA does besides its rows costs as
-  // much as some eight rows of each thread, so there are no more CTAs than it
-  // takes to give every SM one and most a second (1.5 an SM): narrow tiles
-  // first, which make more panels, then clusters of more CTAs.
-  bool whole = gn_tiles(channels, unit, 128, es, p);
-  while (whole && samples * p->tiles * 8 < (int64_t)sms * 3 / 2 && p->tile_ch > unit &&
-         (p->tile_ch - unit) * es >= 64) {
-    const int was = p->tile_ch;
-    whole = gn_tiles(channels, unit, (was - unit) * es, es, p);
-    if (p->tile_ch >= was) break;
-  }
-  p->panels = samples * p->tiles;
-  p->max_groups = max_groups(whole);
-  double slab = (double)rows * p->tile_ch * es * (bwd ? 2 : 1);   // what a panel reads
-  p->cluster = whole && slab <= (double)kSlabBytes;
+  // Forward: one launch, a cluster a panel, where a thread's rows all stay in
+  // its slots (4 x 205 x 192 bf16 6.3 us, two launches 10.0), and for vectors
+  // where panels are small and clusters of 16 fill the SMs (16 x 1024 x 1280
+  // bf16 26 us against 32, 2 x 4096 x 320 fp16 10 against 13; but with a
+  // panel of 3 MB, 2 x 39760 x 160 fp16, 28 against 24, and with 64 CTAs, 4 x
+  // 12708 x 104, 17 against 12). The backward, whose rows take twice the
+  // shared memory and registers, has its two launches always: one launch of
+  // clusters took 22 us for 2 x 4096 x 640 fp16 (two 20), 62 for 13 x 9961 x
+  // 40 bf16 (36).
+  // What a CTA does besides its rows costs as much as some eight rows of each
+  // thread, so there are no more CTAs than it takes to give every SM one and
+  // most a second (1.5 an SM; with 3 an SM 16 x 1024 x 1280 took 29 us):
+  // narrow tiles first, which make more panels, then clusters of more CTAs.
+  bool whole = false;
+  int s = 1;
+  p->cluster = false;
   p->clusters = 0;
-  if (p->cluster) {
+  if (!bwd) {
+    whole = gn_tiles(channels, unit, 128, es, p);
+    while (whole && samples * p->tiles * 8 < (int64_t)sms * 3 / 2 && p->tile_ch > unit &&
+           (p->tile_ch - unit) * es >= 64) {
+      const int was = p->tile_ch;
+      whole = gn_tiles(channels, unit, (was - unit) * es, es, p);
+      if (p->tile_ch >= was) break;
+    }
+  }
+  if (whole) {
+    p->panels = samples * p->tiles;
+    p->max_groups = max_groups(whole);
     const int64_t TY = kGnThreads / p->tw;
-    int s = 1;
     // Clusters of 16 need 16 free places in one part of the chip: fewer of
     // them fit than the SMs would hold CTAs.
     while (s < 16 && p->panels * s < (int64_t)sms * 3 / 2 && rows > s * TY * 2 &&
-           !(s == 8 && p->panels > sms / (bwd ? 12 : 8)))
+           !(s == 8 && p->panels > sms / 8))
       s *= 2;
+    p->cluster = rows <= s * TY * kGnRing ||
+                 (grain == 16 && (double)rows * p->tile_ch * es <= (double)kSlabBytes &&
+                  p->panels * s >= (int64_t)sms * 3 / 4);
+  }
+  if (p->cluster) {
     p->slices = s;
     p->clusters = (int)(p->panels * s <= places ? p->panels : places / s);
     p->slice_rows = (rows + s - 1) / s;
     p->batch = p->panels;
     p->part_bytes = 0;
   } else {
-    // Batches whose rows stay in the L2 cache from the launch that sums them
-    // to the one that applies them.
+    // Batches whose rows stay in the L2 cache (129 MB) from the launch that
+    // sums them to the one that applies them, with the outputs beside them
+    // (2 x 262144 x 256 bf16: 139 us, with batches of half the size 155; 8 x
+    // 16384 x 320 backward 82 and 90; with twice the size 141 and 80).
     whole = gn_tiles(channels, unit, 128, es, p);
     p->panels = samples * p->tiles;
     p->max_groups = max_groups(whole);
-    slab = (double)rows * p->tile_ch * es * (bwd ? 2 : 1);
+    const double slab = (double)rows * p->tile_ch * es * (bwd ? 2 : 1);   // what a panel reads
     p->batch = p->panels;
     if (slab * p->panels > (double)kBatchBytes[bwd]) {
       const int64_t step = whole ? 1 : p->tiles;

@@ -659,27 +659,20 @@ __device__ __forceinline__ float2 cluster_read(const float2* p, int rank) {
 }
 
 // The merge of gn_combine over the cluster's CTAs: a lane a CTA.
-template <bool BWD>
 __device__ __forceinline__ void gn_combine_cluster(const GnArgs& a, const GnUnit& u, GnSmem& sm,
                                                    const float2* part) {
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     float2 v = make_float2(0.f, 0.f);
     if (lane < a.slices) v = cluster_read(part + lg, lane);
-    float s0, s1;
-    if (BWD) {
-      s0 = group_sum<32>(v.x) * a.inv_m;
-      s1 = group_sum<32>(v.y) * a.inv_m;
-    } else {
-      const float base = __shfl_sync(0xffffffffu, v.x, 0);
-      const int64_t nr = min(a.slice_rows, a.rows - lane * a.slice_rows);
-      const bool some = lane < a.slices && nr > 0;
-      const float cnt = some ? (float)nr * (float)a.cpg : 0.f;
-      s0 = base + group_sum<32>(some ? cnt * (v.x - base) : 0.f) * a.inv_m;
-      const float d = v.x - s0;
-      s1 = group_sum<32>(some ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
-    }
-    if (lane == 0) gn_merged<BWD>(a, u, sm, lg, s0, s1, u.slice == 0);
+    const float base = __shfl_sync(0xffffffffu, v.x, 0);
+    const int64_t nr = min(a.slice_rows, a.rows - lane * a.slice_rows);
+    const bool some = lane < a.slices && nr > 0;
+    const float cnt = some ? (float)nr * (float)a.cpg : 0.f;
+    const float mean = base + group_sum<32>(some ? cnt * (v.x - base) : 0.f) * a.inv_m;
+    const float d = v.x - mean;
+    const float var = group_sum<32>(some ? fmaf(cnt * d, d, v.y) : 0.f) * a.inv_m;
+    if (lane == 0) gn_merged<false>(a, u, sm, lg, mean, var, u.slice == 0);
   }
   __syncthreads();
 }
@@ -942,7 +935,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a,
     gn_stats_unit<T, VEC>(a, u, sm, rows, part[turn], 1);
     cluster_arrive();
     cluster_wait();
-    gn_combine_cluster<false>(a, u, sm, part[turn]);
+    gn_combine_cluster(a, u, sm, part[turn]);
     p += clusters;
     const GnUnit v = gn_unit<VEC>(a, p < panels ? p : 0, rank);
     const T* q[1];
@@ -956,40 +949,6 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_fwd_cluster_kernel(GnArgs a,
     __syncthreads();   // the parameters give way to the next sums
   }
   cluster_arrive();    // no CTA leaves while another reads its partials
-  cluster_wait();
-}
-
-template <typename T, int VEC, int ACT, bool FINE>
-__global__ void __launch_bounds__(kGnThreads, 2) gn_bwd_cluster_kernel(GnArgs a, int panels) {
-  GnSmem& sm = *reinterpret_cast<GnSmem*>(gn_dynamic);
-  auto& part = reinterpret_cast<GnParts*>(gn_dynamic + sizeof(GnSmem))->part;
-  void* const ring = gn_dynamic + sizeof(GnSmem) + sizeof(GnParts);
-  int p = a.by_slices.div(blockIdx.x), turn = 0;
-  const int rank = blockIdx.x - p * a.slices, clusters = a.by_slices.div(gridDim.x);
-  GnUnit u = gn_unit<VEC>(a, p, rank);
-  Rows<T, VEC, 2, FINE> rows;
-  gn_bwd_rows<T, VEC>(a, u, rows.p);
-  rows.step[0] = (int64_t)u.TY * a.x_row;
-  rows.step[1] = (int64_t)u.TY * a.dy_row;
-  rows.start(a, u, ring);
-  while (true) {
-    gn_bwd_stats_unit<T, VEC, ACT>(a, u, sm, rows, part[turn], 1);
-    cluster_arrive();
-    cluster_wait();
-    gn_combine_cluster<true>(a, u, sm, part[turn]);
-    p += clusters;
-    const GnUnit v = gn_unit<VEC>(a, p < panels ? p : 0, rank);
-    const T* q[2];
-    gn_bwd_rows<T, VEC>(a, v, q);
-    gn_bwd_apply_unit<T, VEC, ACT>(a, u, sm, rows, [&](T* o, int64_t ostep, auto& body) {
-      rows.again(o, ostep, body, q, p < panels ? v.rows : 0, v.valid);
-    });
-    if (p >= panels) break;
-    u = v;
-    turn ^= 1;
-    __syncthreads();
-  }
-  cluster_arrive();
   cluster_wait();
 }
 

@@ -7,11 +7,9 @@ namespace nf {
 
 template <typename T, int ACT, bool FINE> const void* gn_form(bool bwd, bool cluster) {
   constexpr int V = Vec<T>::N;
-  if (cluster)
-    return bwd ? (const void*)gn_bwd_cluster_kernel<T, V, ACT, FINE>
-               : (const void*)gn_fwd_cluster_kernel<T, V, ACT, FINE>;
-  return bwd ? (const void*)gn_bwd_kernel<T, V, ACT, FINE>
-             : (const void*)gn_fwd_kernel<T, V, ACT, FINE>;
+  if (bwd) return (const void*)gn_bwd_kernel<T, V, ACT, FINE>;
+  return cluster ? (const void*)gn_fwd_cluster_kernel<T, V, ACT, FINE>
+                 : (const void*)gn_fwd_kernel<T, V, ACT, FINE>;
 }
 template <typename T, bool FINE> const void* gn_act(bool bwd, bool cluster, int act) {
   if (act == kActSilu) return gn_form<T, kActSilu, FINE>(bwd, cluster);
