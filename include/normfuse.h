@@ -351,10 +351,10 @@ ln_status ln_softmax_fwd(const void* x, void* y, cudaStream_t stream, int64_t ro
  *
  * Everything else is as above: device pointers owned by the caller, one
  * dtype for x, gamma, beta, y, dy and dx, fp32 arithmetic, work enqueued on
- * `stream`, a status for an answer, nothing touched on a refusal. Rows that
- * are not 16-byte aligned (base, strides, channels * sizeof(dtype)) take
- * kernels of one element an access, with the same results up to the order of
- * the sums. The results depend on the arguments and the number of SMs only.
+ * `stream`, a status for an answer, nothing touched on a refusal. Rows are
+ * read and written 16, 8, 4 or 2 bytes at a time, by what all the call's rows
+ * are aligned to (base, strides, channels * sizeof(dtype)). The results depend
+ * on the arguments, that alignment and the number of SMs only.
  */
 #define GN_MAX_CHANNELS 65536
 
@@ -373,9 +373,9 @@ typedef enum { GN_ACT_NONE = 0, GN_ACT_SILU = 1, GN_ACT_GELU = 2 } gn_act;
  * mean, rstd [samples, groups] fp32, NULL = not stored; the backward reads
  *            them. rows = 0 stores zeros.
  * groups     divides channels, else LN_ERR_SHAPE.
- * workspace  gn_workspace_bytes(..., backward = 0), 16-byte aligned, owned by
- *            the caller, not initialised; calls that may run at the same time
- *            need one each.
+ * workspace  gn_workspace_bytes(..., backward = 0), which may be 0 (NULL is
+ *            fine then), 16-byte aligned, owned by the caller, not
+ *            initialised; calls that may run at the same time need one each.
  */
 ln_status gn_fwd(const void* x, int64_t x_sample, int64_t x_row, const void* gamma,
                  const void* beta, int64_t param_sample, float eps, gn_act act,
@@ -422,7 +422,8 @@ ln_status gn_workspace_bytes(int64_t samples, int64_t rows, int64_t channels, in
  * with the RMSNorm of each head in front where a gamma is given.
  *
  * A tensor is [batch, tokens, heads, head_dim], head_dim contiguous, with
- * strides in elements for batch, token and head: slices of a packed projection, [batch, heads, tokens, head_dim] in memory and expanded inputs
+ * strides in elements for batch, token and head: slices of a packed
+ * projection, [batch, heads, tokens, head_dim] in memory and expanded inputs
  * are all given that way. The first `rot` elements of a head form rot / 2
  * pairs: (j, j + rot / 2) for ROPE_HALF, (2j, 2j + 1) for ROPE_INTERLEAVED;
  * the elements after them pass through. Per head, in fp32:

@@ -27,7 +27,9 @@ struct Shape {
 
 constexpr int kBwdBlocksPerSm = 2;   // backward CTAs an SM, each with a row of partials
 constexpr int kFwdBlocksPerSm = 3;
-constexpr int kRopeItems = 8;        // heads of a tile for each group of threads
+// Heads of a tile for each group of threads: with 4 the forward over 1 x 16384
+// tokens takes 72 us for 64, with 16 the one over 3 x 1023 takes 22 for 18.
+constexpr int kRopeItems = 8;
 
 Strided strided(const void* p, const int64_t* st, int64_t heads, const Shape& c) {
   const int64_t es = (int64_t)elem_size(c.dtype);

@@ -14,6 +14,16 @@
 // the product with the integer position is taken modulo 2^64, which is
 // modulo one turn exactly, and its top 32 bits give sine and cosine. The error
 // is that of the frequency itself times the position, plus 2^-33 turns.
+//
+// Every tensor is read and written once. What bounds the kernel is the
+// arithmetic beside the loads: norm, rotation, conversions and addresses issue
+// in 50 % of the cycles of the forward (half of them pairs, which take the pipe
+// two) with 24 warps an SM, which its 80 registers allow, and too few loads in
+// flight to cover the rest. Measured, back to back, with norm:
+//   forward  1 x 16384 tokens, 32 + 8 heads of 128, bf16   64 us, 5.2 TB/s
+//            64 x 1 token                                   3.9 us (latency)
+//   backward 4 x 4096 tokens, bf16                         41.5 us, 3.0 TB/s:
+//            two CTAs an SM (120 registers with dgamma's sums)
 #pragma once
 
 #include "common.cuh"
@@ -22,7 +32,9 @@
 namespace nf {
 
 constexpr int kRopeThreads = 256;
-// Heads that a thread has on their way.
+// Heads that a thread has on their way. Forward: with one 1 x 16384 tokens take
+// 71 us for 64. Backward: two do not pay for their registers (41.1 us for 41.5
+// over 4 x 4096 tokens, 29.8 for 29.4 over 2 x 4096 with two axes).
 constexpr int kRopeAheadFwd = 2, kRopeAheadBwd = 1;
 constexpr int kRopeMaxDim = 512;
 constexpr int kRopeMaxTable = 2048;   // floats of a tile's cosines, and of its sines
