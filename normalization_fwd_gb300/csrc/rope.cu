@@ -92,7 +92,6 @@ bool can(const Strided& s, int64_t bytes) {
 struct RopePlan {
   const void* fn = nullptr;
   int lanes = 0, grid = 0;
-  size_t smem = 0;
 };
 
 ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, int n_tensors,
@@ -184,7 +183,6 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
     a->blocks[s] = (int)(d.tiles < most ? d.tiles : most);
   }
   p->grid = a->blocks[0] + a->blocks[1];
-  p->smem = bwd && a->ws != nullptr ? (size_t)per_cta * dim * sizeof(float) : 0;
   return LN_OK;
 }
 
@@ -332,7 +330,7 @@ ln_status rope_fwd(const rope_heads* q, const rope_heads* k, const rope_position
   s = plan(c, positions, all, 4, false, &a, &p);
   if (s != LN_OK) return s;
   void* args[] = {&a};
-  const cudaError_t e = cudaLaunchKernel(p.fn, dim3(p.grid), dim3(kRopeThreads), args, p.smem,
+  const cudaError_t e = cudaLaunchKernel(p.fn, dim3(p.grid), dim3(kRopeThreads), args, 0,
                                          stream);
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }
@@ -443,7 +441,7 @@ ln_status rope_bwd(const rope_heads_grad* q, const rope_heads_grad* k,
   if (sums && workspace_bytes < (size_t)rows * 2 * head_dim * sizeof(float))
     return LN_ERR_WORKSPACE;
   void* args[] = {&a};
-  cudaError_t e = cudaLaunchKernel(p.fn, dim3(p.grid), dim3(kRopeThreads), args, p.smem, stream);
+  cudaError_t e = cudaLaunchKernel(p.fn, dim3(p.grid), dim3(kRopeThreads), args, 0, stream);
   if (e == cudaSuccess && sums)
     e = launch_bwd_finalize(a.ws, rows, 2 * (int)head_dim, (int)head_dim, true,
                             const_cast<void*>(grads[0].p), const_cast<void*>(grads[1].p), nullptr,

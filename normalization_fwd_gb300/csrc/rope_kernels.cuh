@@ -299,9 +299,10 @@ template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool FULL, bool
 __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArgs A) {
   using Raw = RopeRaw<T, VEC, ALIGNED>;
   constexpr int kAhead = BWD ? kRopeAheadBwd : kRopeAheadFwd;
-  __shared__ __align__(16) float tab_c[kRopeMaxTable], tab_s[kRopeMaxTable];
+  // Cosines and sines, of two tiles in turn: a warp may write the next tile's
+  // while others still read, so a tile takes one barrier.
+  __shared__ __align__(16) float tab[2][2][kRopeMaxTable];
   __shared__ unsigned long long tab_t[kRopeMaxAxes * kRopeMaxDim / 2];   // several axes only
-  extern __shared__ float red[];
   const int L = A.lanes, per_cta = kRopeThreads / L;
   const int l = threadIdx.x & (L - 1), grp = threadIdx.x / L;
   const int side = (int)blockIdx.x >= A.blocks[0] ? 1 : 0;
@@ -347,14 +348,17 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
   if (A.axes == 1) {
     if (j < A.rot / 2) turns = turns_of(A.freqs[j]);
   } else {
-    // Read behind the barrier before the first tile's angles.
     for (int i = threadIdx.x; i < A.axes * (A.rot / 2); i += kRopeThreads)
       tab_t[i] = turns_of(A.freqs[i]);
+    __syncthreads();
   }
 
   const int64_t in_step = token_lanes * in_t, out_step = token_lanes * out_t,
                 x_step = token_lanes * x_t;
-  for (int64_t tile = blk; tile < tiles; tile += blks) {
+  int turn = 0;
+  for (int64_t tile = blk; tile < tiles; tile += blks, turn ^= 1) {
+    float* const tab_c = tab[turn][0];
+    float* const tab_s = tab[turn][1];
     const int64_t b = tile / row_tiles, tok0 = (tile - b * row_tiles) * tile_rows;
     const int toks = (int)min((int64_t)tile_rows, A.tokens - tok0);
     // Whole warps run the loops below, so that every lane reaches the shuffles.
@@ -393,23 +397,39 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
         fetch(d, d);
       }
       if (h0 == 0) {
-        // The angles, while the first rows are on their way.
-        __syncthreads();   // the last tile's table gives way
-        if (j < A.rot / 2)
-          for (int t = threadIdx.x / A.wide; t < toks; t += kRopeThreads / A.wide) {
-            unsigned long long sum = 0;
+        // The angles, while the first rows are on their way; positions are
+        // loaded four at a time.
+        if (j < A.rot / 2) {
+          const int step = kRopeThreads / A.wide;
+          for (int t0 = threadIdx.x / A.wide; t0 < toks; t0 += 4 * step) {
+            unsigned long long sum[4] = {0, 0, 0, 0};
             for (int ax = 0; ax < A.axes; ++ax) {
-              const int64_t at = ax * A.pos_s[0] + b * A.pos_s[1] + (tok0 + t) * A.pos_s[2];
-              const int64_t pos = A.pos64 ? static_cast<const int64_t*>(A.pos)[at]
-                                          : (int64_t)static_cast<const int*>(A.pos)[at];
+              const int64_t at = ax * A.pos_s[0] + b * A.pos_s[1] + (tok0 + t0) * A.pos_s[2];
+              long long pos[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                pos[i] = 0;
+                const int64_t from = at + i * step * A.pos_s[2];
+                if (t0 + i * step < toks)
+                  pos[i] = A.pos64 ? static_cast<const long long*>(A.pos)[from]
+                                   : (long long)static_cast<const int*>(A.pos)[from];
+              }
               if (A.axes > 1) turns = tab_t[ax * (A.rot / 2) + j];
-              sum += (unsigned long long)pos * turns;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[i] += (unsigned long long)pos[i] * turns;
             }
-            float s, c;
-            sincos_turns((unsigned)((sum + 0x80000000ull) >> 32), &s, &c);
-            tab_c[t * A.row + j] = c * A.scale_c;
-            tab_s[t * A.row + j] = s * A.scale_s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = t0 + i * step;
+              if (t < toks) {
+                float s, c;
+                sincos_turns((unsigned)((sum[i] + 0x80000000ull) >> 32), &s, &c);
+                tab_c[t * A.row + j] = c * A.scale_c;
+                tab_s[t * A.row + j] = s * A.scale_s;
+              }
+            }
           }
+        }
         __syncthreads();
       }
       const float* tc = tab_c + tl * A.row;
@@ -533,8 +553,11 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     }
   }
   if (BWD && A.ws != nullptr) {
-    // The groups' sums, added in their order, into this CTA's partial row.
-    // The side with fewer CTAs has its other rows zeroed by the other side.
+    // The groups' sums, added in their order, into this CTA's partial row, by
+    // way of the tables' memory (a group's head each: 4096 floats at most). The
+    // side with fewer CTAs has its other rows zeroed by the other side.
+    float* const red = tab[0][0];
+    __syncthreads();   // the tables give way
 #pragma unroll
     for (int n = 0; n < NS; ++n)
 #pragma unroll
