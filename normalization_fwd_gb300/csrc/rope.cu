@@ -117,13 +117,15 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
   }
   const int nv = dim / v;
   const int slots = inter ? (nv + 1) / 2 : rot / 2 / v + (nv - rot / v + 1) / 2;
-  // Heads of more than 32 slots. Forward: as few a lane as 32 lanes take, so
-  // that neighbouring lanes' accesses are neighbours (fp16 heads of 98
-  // elements, 15 x 3804 tokens: 264 us, with 8 slots a lane 372). Backward: as
-  // many as a lane holds, because fewer lanes have less to do besides (fp16
-  // heads of 170, 53 x 248 tokens: 190 us, with 2 slots a lane 248).
+  // Heads of more than 32 slots: as few a lane as 32 lanes take, so that
+  // neighbouring lanes' accesses are neighbours and registers last (element by
+  // element, fp16: heads of 98, 15 x 3804 tokens forward 264 us, with 8 slots a
+  // lane 372; heads of 128, 21 x 8322 tokens backward 299 and 792). The
+  // backward in pairs of elements takes as many as a lane holds, four, because
+  // fewer lanes have less to do besides (fp16 heads of 170, 53 x 248 tokens: 190
+  // us, with two a lane 248).
   int ns = 1;
-  if (slots > 32 && bwd) ns = 8 / v;
+  if (slots > 32 && bwd && v > 1) ns = 8 / v;
   while (32 * ns < slots) ns *= 2;
   int lanes = 1;
   while (lanes * ns < slots) lanes *= 2;

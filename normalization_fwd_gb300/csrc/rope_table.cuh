@@ -1,6 +1,6 @@
 // (vector width, slots a lane, layout, direction) -> rotary kernel of one
 // dtype. A lane holds at most 8 pairs, so a head of up to 512 elements takes
-// 1, 2, ... or 8 / VEC slots of VEC pairs a lane (backward: 1 or 8 / VEC).
+// 1, 2, ... or 8 / VEC slots of VEC pairs a lane (backward in vectors: 1 or 8 / VEC).
 #pragma once
 
 #include "rope_kernels.cuh"
@@ -10,7 +10,7 @@ namespace nf {
 template <typename T, int VEC, int NS, bool INTER, bool ALIGNED, bool FULL>
 const void* rope_dir(bool bwd) {
   if (!bwd) return (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, false>;
-  if constexpr (NS == 1 || NS == 8 / VEC)
+  if constexpr (NS == 1 || NS == 8 / VEC || VEC == 1)
     return (const void*)rope_kernel<T, VEC, NS, INTER, ALIGNED, FULL, true>;
   return nullptr;
 }

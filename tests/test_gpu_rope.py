@@ -144,6 +144,19 @@ def test_head_sizes(cuda_lib, D, rot, interleaved, norm):
         check(cuda_lib, dtype, 2, 5, 3, 2, D, rot, interleaved, norm)
 
 
+# heads that take 2, 4 and 8 slots a lane: element by element, in pairs and in fours of elements
+WIDE = [(140, 140), (160, 150), (256, 70), (134, 134), (258, 258), (500, 402), (510, 30), (460, 460),
+        (264, 264)]
+
+
+@pytest.mark.parametrize("D,rot", WIDE)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_wide_heads(cuda_lib, D, rot, interleaved, dtype):
+    check(cuda_lib, dtype, 2, 37, 3, 1, D, rot, interleaved, True)
+    check(cuda_lib, dtype, 1, 6, 2, 2, D, rot, interleaved, False, offset=1)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("storage", ["separate", "heads", "packed"])
 @pytest.mark.parametrize("interleaved", [False, True])
