@@ -28,7 +28,7 @@ struct Shape {
 constexpr int kBwdBlocksPerSm = 2;   // backward CTAs an SM, each with a row of partials
 constexpr int kFwdBlocksPerSm = 3;
 // Heads of a tile for each group of threads: with 4 the forward over 1 x 16384
-// tokens takes 72 us for 64, with 16 the one over 3 x 1023 takes 22 for 18.
+// tokens takes 71 us for 62, with 16 the one over 3 x 1023 takes 18 for 17.
 constexpr int kRopeItems = 8;
 
 Strided strided(const void* p, const int64_t* st, int64_t heads, const Shape& c) {
@@ -91,7 +91,7 @@ bool can(const Strided& s, int64_t bytes) {
 
 struct RopePlan {
   const void* fn = nullptr;
-  int lanes = 0, grid = 0;
+  int grid = 0;
 };
 
 ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, int n_tensors,
@@ -134,7 +134,6 @@ ln_status plan(const Shape& c, const rope_positions* r, const Strided* tensors, 
           : c.dtype == LN_BF16 ? rope_table_bf16(v, ns, inter, al, full, bwd)
                                : rope_table_f16(v, ns, inter, al, full, bwd);
   if (p->fn == nullptr) return LN_ERR_UNSUPPORTED;
-  p->lanes = lanes;
   const int per_cta = kRopeThreads / lanes;
   const int per_sm = bwd ? kBwdBlocksPerSm : kFwdBlocksPerSm;
   a->lanes = lanes;

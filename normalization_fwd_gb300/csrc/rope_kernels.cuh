@@ -20,9 +20,9 @@
 // in 50 % of the cycles of the forward (half of them pairs, which take the pipe
 // two) with 24 warps an SM, which its 80 registers allow, and too few loads in
 // flight to cover the rest. Measured, back to back, with norm:
-//   forward  1 x 16384 tokens, 32 + 8 heads of 128, bf16   64 us, 5.2 TB/s
+//   forward  1 x 16384 tokens, 32 + 8 heads of 128, bf16   62 us, 5.4 TB/s
 //            64 x 1 token                                   3.9 us (latency)
-//   backward 4 x 4096 tokens, bf16                         41.5 us, 3.0 TB/s:
+//   backward 4 x 4096 tokens, 16 + 4 heads of 64, bf16      36 us, 3.5 TB/s:
 //            two CTAs an SM (120 registers with dgamma's sums)
 #pragma once
 
@@ -33,8 +33,9 @@ namespace nf {
 
 constexpr int kRopeThreads = 256;
 // Heads that a thread has on their way. Forward: with one 1 x 16384 tokens take
-// 71 us for 64. Backward: two do not pay for their registers (41.1 us for 41.5
-// over 4 x 4096 tokens, 29.8 for 29.4 over 2 x 4096 with two axes).
+// 69 us for 62, with three 77. Backward: two do not pay for their registers
+// (37.4 us for 36.8 over 4 x 4096 tokens, 22.8 for 21.1 over 2 x 4096 with two
+// axes).
 constexpr int kRopeAheadFwd = 2, kRopeAheadBwd = 1;
 constexpr int kRopeMaxDim = 512;
 constexpr int kRopeMaxTable = 2048;   // floats of a tile's cosines, and of its sines
@@ -557,6 +558,8 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     // way of the tables' memory (a group's head each: 4096 floats at most). The
     // side with fewer CTAs has its other rows zeroed by the other side.
     float* const red = tab[0][0];
+    // The finalize may be scheduled while the last CTAs work; it waits for them.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();   // the tables give way
 #pragma unroll
     for (int n = 0; n < NS; ++n)
