@@ -400,11 +400,15 @@ def softmax_fwd(x, *, out=None, stream=None):
 
 
 class Workspace:
-    """A reusable backward workspace, grown on demand (allocated through torch)."""
+    """A reusable workspace, grown on demand (allocated through torch). Calls
+    that may run at the same time, replays of captured graphs among them, need
+    one each. A buffer that it has outgrown is kept: a graph captured with it
+    writes there at every replay."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = torch.empty(0, dtype=torch.uint8, device=self.device)
+        self.outgrown = []
 
     def get(self, rows: int, hidden: int, dtype, mode) -> torch.Tensor:
         return self.take(ln_bwd_workspace_bytes(rows, hidden, dtype, mode))
@@ -412,6 +416,8 @@ class Workspace:
     def take(self, need: int) -> torch.Tensor:
         """A buffer of at least ``need`` bytes."""
         if self.buf.numel() < need:
+            if self.buf.numel():
+                self.outgrown.append(self.buf)
             self.buf = torch.empty(need, dtype=torch.uint8, device=self.device)
         return self.buf
 

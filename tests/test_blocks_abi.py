@@ -3,10 +3,12 @@ points, refusals on the host (no call below reaches the GPU), the binding's
 own checks, and the frequencies."""
 
 import ctypes
+import gc
 import math
 import os
 import re
 import struct
+import weakref
 
 import numpy as np
 import pytest
@@ -324,3 +326,13 @@ def test_rows_of_strided_tensors():
     for bad in (x[:, :, :5], x.transpose(1, 2), x.permute(0, 3, 1, 2), torch.empty(8)):
         with pytest.raises(ValueError):
             rows(bad, "x")
+
+
+def test_an_outgrown_workspace_buffer_stays():
+    """A graph captured with the smaller buffer still writes to it."""
+    w = nf.Workspace("cpu")
+    small = weakref.ref(w.take(64))
+    at = w.take(32).data_ptr()
+    assert w.take(4096).numel() == 4096 and w.take(64).numel() == 4096
+    gc.collect()
+    assert small() is not None and small().data_ptr() == at != w.take(64).data_ptr()
