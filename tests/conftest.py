@@ -21,6 +21,21 @@ def pytest_configure(config):
         "markers", "gpu: needs a CUDA GPU (sm_103a); runs the CUDA library through its C ABI")
 
 
+# Tests without a GPU mark whose calls the C library accepts, on addresses that
+# are no memory: they end at the missing device, and would launch on one.
+MADE_UP_ADDRESSES = ("test_gn_fwd_slices_of_one_buffer", "test_rope_overlap_of_packed_heads")
+
+
+def pytest_collection_modifyitems(items):
+    import torch
+    if not torch.cuda.is_available():
+        return
+    for item in items:
+        if getattr(item, "originalname", None) in MADE_UP_ADDRESSES:
+            item.add_marker(pytest.mark.skip(
+                reason="a GPU is visible: the call would be launched on made-up addresses"))
+
+
 @pytest.fixture(scope="session")
 def cuda_lib(request):
     """The CUDA library, built in-tree; the GPU tests fail loudly without it."""

@@ -1,0 +1,69 @@
+"""What calls of the group norm and the rotary positions would launch where
+there is a device, seen without one (tests/_fake_device.py)."""
+
+import inspect
+
+import pytest
+import torch
+
+import _fake_device
+import conftest
+import test_blocks_abi as abi
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    return _fake_device.load(tmp_path_factory.mktemp("fake"))
+
+
+def refusals():
+    """(name, call, arguments, status) of every host-side refusal in test_blocks_abi."""
+    for fn, call in ((abi.test_gn_fwd_rejects_on_host, abi.gn_fwd),
+                     (abi.test_gn_bwd_rejects_on_host, abi.gn_bwd),
+                     (abi.test_rope_fwd_rejects_on_host, abi.rope),
+                     (abi.test_rope_bwd_rejects_on_host, abi.rope_b)):
+        (mark,) = [m for m in fn.pytestmark if m.name == "parametrize"]
+        for i, (kw, want) in enumerate(mark.args[1]):
+            yield pytest.param(call, kw, want, id=f"{fn.__name__}-{i}")
+
+
+@pytest.mark.parametrize("call,kw,want", list(refusals()))
+def test_refusals_come_before_any_launch(lib, call, kw, want):
+    """With a device, too: their addresses are made up."""
+    lib.fake_reset(152)
+    assert call(lib, **kw) == want
+    assert _fake_device.counts(lib)["launches"] == 0
+
+
+class Item:
+    """A collected test, as far as the hook looks at one."""
+
+    def __init__(self, name):
+        self.originalname, self.marks = name, []
+
+    def add_marker(self, mark):
+        self.marks.append(mark.name)
+
+
+def test_accepted_calls_on_made_up_addresses_need_a_machine_without_gpu(lib, monkeypatch):
+    """The unmarked tests that go through the C library without a refusal are
+    those that would launch, and a visible GPU skips them."""
+    launch = []
+    for name, fn in inspect.getmembers(abi, inspect.isfunction):
+        if not name.startswith("test_") or list(inspect.signature(fn).parameters) != ["lib"]:
+            continue
+        lib.fake_reset(152)
+        try:
+            fn(lib)
+        except AssertionError:
+            pass        # it expects to end at the missing device
+        if _fake_device.counts(lib)["launches"]:
+            launch.append(name)
+    assert launch == ["test_gn_fwd_slices_of_one_buffer", "test_rope_overlap_of_packed_heads"]
+    items = [Item(n) for n in launch + ["test_gn_fwd_rejects_on_host"]]
+    conftest.pytest_collection_modifyitems(items)
+    assert not any(i.marks for i in items) or torch.cuda.is_available()
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    items = [Item(n) for n in launch + ["test_gn_fwd_rejects_on_host"]]
+    conftest.pytest_collection_modifyitems(items)
+    assert [i.marks for i in items] == [["skip"], ["skip"], []]
