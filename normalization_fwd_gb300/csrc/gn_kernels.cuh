@@ -232,8 +232,8 @@ struct alignas(16) GnSmem {
     float2 lane[kGnThreads * 8];
     float par[6][kGnMaxTileCh];
   };
-  float2 col[kGnMaxTileCh];   // column sums, in parts, then whole
-  float k[kGnMaxTileCh];        // forward: what the columns are shifted by
+  float2 col[kGnMaxTileCh];   // column sums, in parts, then whole (backward)
+  float n[kGnThreads / 4];      // forward: rows of the parts
   float g0[kGnMaxTileCh];       // merged: mean, or c1, of the tile's groups
   float g1[kGnMaxTileCh];       // rstd, or c2
 };
@@ -460,9 +460,17 @@ template <typename T, int VEC, int TENSORS, bool FINE> struct Rows {
 #pragma unroll
     for (int g = 0; g < NG; ++g) fetch(g, rows, g);
   }
+  // The thread's first row (zeros where it has none).
+  __device__ __forceinline__ void first(float2* f) {
+    copy_wait<NG - 1>();
+    take(place);
+    if (rows == 0) v[0][0].clear();
+    v[0][0].get(f);
+  }
   // body(j, to) for every row, j its place in v, `to` its place in an output
-  // whose first row is at `o`.
-  template <typename F> __device__ __forceinline__ void pass(T* o, int64_t ostep, F&& body) {
+  // whose first row is at `o`; end(g) after step g.
+  template <typename F, typename E>
+  __device__ __forceinline__ void pass(T* o, int64_t ostep, F&& body, E&& end) {
     for (int g = 0; g < steps; ++g) {
       copy_wait<NG - 1>();
       take(place + g);
@@ -472,7 +480,11 @@ template <typename T, int VEC, int TENSORS, bool FINE> struct Rows {
         o += ostep;
       }
       fetch(g + NG, rows, place + g);
+      end(g);
     }
+  }
+  template <typename F> __device__ __forceinline__ void pass(T* o, int64_t ostep, F&& body) {
+    pass(o, ostep, body, [](int) {});
   }
   // The second pass over the same rows, those in the slots first; places that
   // it has no more rows for take the first ones of another unit at q.
@@ -520,58 +532,134 @@ template <typename T, int VEC, int TENSORS, bool FINE> struct Rows {
 };
 
 // ---- forward: partial statistics of one unit -------------------------------------
-// Each column is summed as d = x - k and d^2, k the column's value in the
-// slice's first row. k is one of the data, so (mean - k)^2 is itself a term
-// of the variance: with n rows a slice, cancellation in s2 - s1^2 / n costs
-// at most about n * 2^-24 of the group's sum of squares, whatever the mean.
-// Columns, and later slices, are merged by the parallel-variance identity
-// M2 = sum M2_i + n_i (mean_i - mean)^2.
+// A thread sums a column of its rows as d = x - k and d^2 about a k that it
+// moves to the mean of its rows so far: after 8 and 32 rows, then every 32.
+// With s1, s2 the sums of a block of rows, N the rows so far and t the move,
+// about s1 / N, what is left is s1 - N t, and the block adds s2 - t (2 s1 - N t)
+// to the column's sum of squares M2. No row is special: k begins as the
+// thread's own first row, so the first block's s2 is at most 8 M2, and with b
+// rows a later block Cauchy's inequality gives s1^2 / N <= s2 b / N, b / N <= 3/4,
+// so that the later ones come to at most 4 M2, whatever the data. M2 is good
+// to 8 * 10 + 4 * 34 roundings and one more a block, relative; measured, rstd
+// is off by 9 roundings at most over rows that begin with an outlier or padding. One shift for all rows, the slice's first one, was off by 1e-3
+// after an outlier and 16384 rows; it saved 0.7 us of 2 x 4096 x 320 fp16's
+// 10.7 and nothing of 2 x 262144 x 256 bf16's 137.
+// Row lanes, columns and slices are merged by the parallel-variance identity
+// M2 = sum M2_i + n_i (mean_i - mean)^2, the mean first.
+__device__ __forceinline__ bool gn_moves(int g) { return g == 3 || g % 16 == 15; }
+
+// Merge the columns' (mean, M2) over the row lanes: each column's lanes are
+// dealt to as many threads as there are, part p of column c into
+// sm.col[p * tc + c] and its rows into sm.n[p]. The order depends on the
+// launch's shape only. Returns the parts.
+template <int VEC>
+__device__ __forceinline__ int gn_merge_lanes(const GnArgs& a, const GnUnit& u, GnSmem& sm,
+                                              const float2* mean, const float2* m2) {
+  if (u.on) {
+    float2* to = sm.lane + u.ty * u.tc + u.tx * VEC;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i)
+      reinterpret_cast<float4*>(to)[i] = make_float4(mean[i].x, m2[i].x, mean[i].y, m2[i].y);
+  }
+  __syncthreads();
+  const int each = a.by_ty.div((int)u.nr), more = (int)u.nr - each * u.TY;
+  const auto merge = [&](int part, int parts, int col) {
+    const auto rows = [&](int y) { return (float)(each + (y < more ? 1 : 0)); };
+    const float base = sm.lane[part * u.tc + col].x;
+    float n = 0.f, s = 0.f, q = 0.f;
+#pragma unroll 4
+    for (int y = part; y < u.TY; y += parts) {
+      n += rows(y);
+      s = fmaf(rows(y), sm.lane[y * u.tc + col].x - base, s);
+    }
+    const float m = n > 0.f ? fmaf(s, rcpf(n), base) : base;
+#pragma unroll 4
+    for (int y = part; y < u.TY; y += parts) {
+      const float2 v = sm.lane[y * u.tc + col];
+      const float d = v.x - m;
+      q += fmaf(rows(y) * d, d, v.y);
+    }
+    sm.col[part * u.tc + col] = make_float2(m, q);
+    if (col == 0) sm.n[part] = n;
+  };
+  const int parts = a.by_tc.div(kGnThreads);   // threads a column
+  if (parts > 1) {
+    const int part = a.by_tc.div(threadIdx.x), col = threadIdx.x - part * u.tc;
+    if (part < parts && col < u.nc) merge(part, parts, col);
+    return parts;
+  }
+  for (int c = threadIdx.x; c < u.nc; c += kGnThreads) merge(0, 1, c);
+  return 1;
+}
+
 template <typename T, int VEC, bool FINE>
 __device__ __forceinline__ void gn_stats_unit(const GnArgs& a, const GnUnit& u, GnSmem& sm,
                                               Rows<T, VEC, 1, FINE>& rows, float2* out,
                                               int stride) {
   constexpr int NP = Pack<T, VEC>::NP;
-  float2 k[NP], s1[NP], s2[NP], v[NP];
+  float2 k[NP], s1[NP], s2[NP], m2[NP], v[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) k[i] = s1[i] = s2[i] = splat2(0.f);
-  if (u.rows > 0) {
-    Pack<T, VEC> first;
-    first.clear();
-    first.template load<FINE>(rows.p[0] - u.ty * a.x_row, a.grain, u.valid);
-    first.get(k);
-  }
-  rows.pass(static_cast<T*>(nullptr), 0, [&](int j, T*) {
-    rows.v[0][j].get(v);
+  for (int i = 0; i < NP; ++i) s1[i] = s2[i] = m2[i] = splat2(0.f);
+  rows.first(k);
+  const auto move = [&](int n) {
+    const float2 inv = splat2(rcpf((float)n)), neg = splat2(-(float)n);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const float2 d = fma2(k[i], splat2(-1.f), v[i]);
-      s1[i] = add2(s1[i], d);
-      s2[i] = fma2(d, d, s2[i]);
+      const float2 to = fma2(s1[i], inv, k[i]);
+      const float2 t = fma2(k[i], splat2(-1.f), to);
+      const float2 left = fma2(neg, t, s1[i]);
+      const float2 sum = add2(s1[i], left);
+      m2[i] = add2(m2[i], fma2(mul2(t, splat2(-1.f)), sum, s2[i]));
+      k[i] = to;
+      s1[i] = left;
+      s2[i] = splat2(0.f);
     }
-  });
-  if (u.on && u.ty == 0) put_pairs<VEC>(sm.k + u.tx * VEC, k);
-  const float n = (float)u.nr, inv = u.nr > 0 ? 1.f / n : 0.f;
-  gn_columns<VEC>(a, u, sm, s1, s2, [&](int c, float2 s) {
-    const float m = s.x * inv;
-    sm.col[c] = make_float2(sm.k[c] + m, fmaf(-s.x, m, s.y));   // mean, M2
-  });
+  };
+  rows.pass(
+      static_cast<T*>(nullptr), 0,
+      [&](int j, T*) {
+        rows.v[0][j].get(v);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float2 d = fma2(k[i], splat2(-1.f), v[i]);
+          s1[i] = add2(s1[i], d);
+          s2[i] = fma2(d, d, s2[i]);
+        }
+      },
+      [&](int g) {
+        if (gn_moves(g) && (g + 1) * kGnStep < rows.rows) move((g + 1) * kGnStep);
+      });
+  if (rows.rows > 0) move(rows.rows);
+  const int parts = gn_merge_lanes<VEC>(a, u, sm, k, m2);
   __syncthreads();
   const int lane = threadIdx.x & 31;
   for (int lg = threadIdx.x >> 5; lg < u.ng; lg += kGnThreads / 32) {
     const int cs = max((u.g0 + lg) * a.cpg - u.c0, 0);
-    const int ce = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc);
-    // Means are averaged as differences from one of them, which keeps a
-    // constant group's mean exact and a large common mean out of the sum.
+    const int width = min((u.g0 + lg + 1) * a.cpg - u.c0, u.nc) - cs;
+    // The group's columns and parts, dealt to the lanes as one list. Means are
+    // averaged as differences from one of them, which keeps a constant
+    // group's mean exact and a large common mean out of the sum.
+    const int dp = 32 / width, dc = 32 - dp * width, p0 = lane / width, c0 = lane - p0 * width;
+    const auto walk = [&](auto&& body) {
+      for (int p = p0, c = c0; p < parts;) {
+        body(sm.n[p], sm.col[p * u.tc + cs + c]);
+        p += dp;
+        c += dc;
+        if (c >= width) {
+          c -= width;
+          ++p;
+        }
+      }
+    };
     const float base = sm.col[cs].x;
     float s = 0.f;
-    for (int c = cs + lane; c < ce; c += 32) s += sm.col[c].x - base;
-    const float m = base + group_sum<32>(s) / (float)(ce - cs);
+    walk([&](float n, float2 v) { s = fmaf(n, v.x - base, s); });
+    const float m = base + group_sum<32>(s) / ((float)u.nr * (float)width);
     s = 0.f;
-    for (int c = cs + lane; c < ce; c += 32) {
-      const float2 v = sm.col[c];
+    walk([&](float n, float2 v) {
       const float d = v.x - m;
       s += fmaf(n * d, d, v.y);
-    }
+    });
     s = group_sum<32>(s);
     if (lane == 0) out[(int64_t)lg * stride] = make_float2(m, s);
   }
