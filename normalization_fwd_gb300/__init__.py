@@ -402,8 +402,10 @@ def softmax_fwd(x, *, out=None, stream=None):
 class Workspace:
     """A reusable workspace, grown on demand (allocated through torch). Calls
     that may run at the same time, replays of captured graphs among them, need
-    one each. A buffer that it has outgrown is kept: a graph captured with it
-    writes there at every replay."""
+    one each. A buffer that it has outgrown is kept, as a graph captured with
+    it writes there at every replay; each buffer is at least twice the one
+    before, so that what is kept is less than the newest one. ``release`` lets
+    go of it."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
@@ -415,11 +417,18 @@ class Workspace:
 
     def take(self, need: int) -> torch.Tensor:
         """A buffer of at least ``need`` bytes."""
-        if self.buf.numel() < need:
-            if self.buf.numel():
+        have = self.buf.numel()
+        if have < need:
+            if have:
                 self.outgrown.append(self.buf)
-            self.buf = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self.buf = torch.empty(max(need, 2 * have), dtype=torch.uint8, device=self.device)
         return self.buf
+
+    def release(self) -> None:
+        """Let go of the buffers that it has outgrown: for when no graph
+        captured with one of them will be replayed again and no call that was
+        given one is still running."""
+        self.outgrown.clear()
 
 
 def fused_norm_fwd(x, gamma, beta=None, *, bias=None, residual=None, eps=1e-5,
