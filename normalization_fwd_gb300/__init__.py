@@ -585,13 +585,21 @@ def _affine(p, name, N, C, dtype):
     raise ValueError(f"{name}: expected [{C}] or [{N}, {C}], got {list(p.shape)}")
 
 
-def _affines(where, gamma, beta, N, C, dtype):
-    steps = [_affine(p, f"{where}: {n}", N, C, dtype) for p, n in ((gamma, "gamma"), (beta, "beta"))
-             if p is not None]
-    if len(set(steps)) > 1:
-        raise ValueError(f"{where}: gamma and beta must both be shared or both per sample, with "
-                         "the same stride")
-    return steps[0] if steps else 0
+def _affines(where, gamma, beta, N, C, dtype, grads=False):
+    """gamma, beta and their stride between samples (0: shared). Parameters of
+    each sample that are one row expanded over the samples work as shared ones;
+    with ``grads`` each sample has a gradient of its own, so they are laid out,
+    as are two whose strides differ."""
+    given = [p for p in (gamma, beta) if p is not None]
+    steps = {_affine(p, f"{where}: {n}", N, C, dtype)
+             for p, n in ((gamma, "gamma"), (beta, "beta")) if p is not None}
+    each = [p.dim() == 2 for p in given]
+    if len(steps) > 1 or (grads and N > 1 and 0 in steps and any(each)):
+        if not all(each):
+            raise ValueError(f"{where}: gamma and beta must both be shared or both per sample")
+        gamma, beta = (None if p is None else p.contiguous() for p in (gamma, beta))
+        steps = {C}
+    return gamma, beta, steps.pop() if steps else 0
 
 
 def _activation(act) -> int:
@@ -680,7 +688,7 @@ def _gn_fwd(device, x, groups, gamma, beta, eps, activation, zero_centered_gamma
     N, R, C, xs, xr = _rows_of(x, "gn_fwd: x")
     _same("gn_fwd", "y", y, x)
     _, _, _, ys, yr = _rows_of(y, "gn_fwd: y")
-    ps = _affines("gn_fwd", gamma, beta, N, C, x.dtype)
+    gamma, beta, ps = _affines("gn_fwd", gamma, beta, N, C, x.dtype)
     _check_stats("gn_fwd", mean, rstd, N, groups, True)
     held, ws, ws_bytes = _workspace(workspace, _gn_need(device, N, R, C, groups, dt, False), device)
     st = lib.gn_fwd(x.data_ptr() or None, xs, xr, None if gamma is None else gamma.data_ptr(),
@@ -717,7 +725,7 @@ def _gn_bwd(device, dy, x, groups, gamma, beta, activation, zero_centered_gamma,
     _same("gn_bwd", "dx", dx, x)
     _, _, _, ds, dr = _rows_of(dy, "gn_bwd: dy")
     _, _, _, os_, or_ = _rows_of(dx, "gn_bwd: dx")
-    ps = _affines("gn_bwd", gamma, beta, N, C, x.dtype)
+    gamma, beta, ps = _affines("gn_bwd", gamma, beta, N, C, x.dtype, grads=True)
     _check_stats("gn_bwd", mean, rstd, N, groups, False)
     grads = [g for g in (dgamma, dbeta) if g is not None]
     for g in grads:
