@@ -418,7 +418,8 @@ ln_status gn_bwd(const void* dy, int64_t dy_sample, int64_t dy_row, const void* 
     if (e == cudaSuccess && dbeta && grads) e = cudaMemsetAsync(dbeta, 0, grads, stream);
     return e == cudaSuccess ? LN_OK : cuda_fail(e);
   }
-  if (grad_rows > 65535) return LN_ERR_SHAPE;   // rows of the finalize's grid
+  if (grad_rows > 65535 && (dgamma != nullptr || dbeta != nullptr))
+    return LN_ERR_SHAPE;   // rows of the finalize's grid
   const int grain = grain_of(so, grain_of(sd, grain_of(sx, 16)));
   GnPlan p;
   s = plan_call(c, true, grain, &p);

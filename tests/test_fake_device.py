@@ -67,3 +67,18 @@ def test_accepted_calls_on_made_up_addresses_need_a_machine_without_gpu(lib, mon
     items = [Item(n) for n in launch + ["test_gn_fwd_rejects_on_host"]]
     conftest.pytest_collection_modifyitems(items)
     assert [i.marks for i in items] == [["skip"], ["skip"], []]
+
+
+def test_many_samples_without_gradients_of_their_parameters(lib):
+    """The limit of 65535 samples is that of the gradients' sums."""
+    many = dict(ps=64, N=70000, rows=1, xs=0, ds=0, os_=64, wb=1 << 30)
+    # the statistics and the workspace would lie in one another
+    far = dict(m=1 << 48, r=1 << 49, ws=1 << 50, dg=None, db=None)
+    lib.fake_reset(152)
+    assert abi.gn_bwd(lib, **many, **far) == abi.OK
+    counts = _fake_device.counts(lib)
+    assert counts["launches"] > 0 and counts["finalizes"] == 0
+    lib.fake_reset(152)
+    for grad in ("dg", "db"):
+        assert abi.gn_bwd(lib, **many, **{**far, grad: 1 << 51}) == abi.SHAPE
+    assert _fake_device.counts(lib)["launches"] == 0

@@ -58,3 +58,16 @@ def test_halves_of_one_projection(cuda_lib):
     want = run(cuda_lib, x, dy, g.contiguous(), b.contiguous())
     for got in (run(cuda_lib, x, dy, g, b), run(cuda_lib, x, dy, g.contiguous(), b)):
         assert all(torch.equal(a, w) for a, w in zip(got, want))
+
+
+def test_dx_of_many_samples(cuda_lib):
+    """More samples than the parameters' gradients can have, without those."""
+    nf = cuda_lib
+    x, dy, g, b = tensors((70000, 2, 8), (70000, 2, 8), (70000, 8), (70000, 8))
+    f = nf.fused_group_norm_fwd(x, 2, g, b, activation="silu")
+    dx = torch.empty_like(x)
+    nf.gn_bwd(dy, x, 2, g, b, "silu", False, f["mean"], f["rstd"], dx, None, None)
+    for n in (slice(0, 3), slice(65534, 65538), slice(69990, 70000)):
+        r = nf.fused_group_norm_bwd(dy[n], x[n], 2, g[n], b[n], f["mean"][n], f["rstd"][n],
+                                    activation="silu")
+        assert torch.equal(dx[n], r["dx"])
