@@ -354,7 +354,8 @@ ln_status ln_softmax_fwd(const void* x, void* y, cudaStream_t stream, int64_t ro
  * `stream`, a status for an answer, nothing touched on a refusal. Rows are
  * read and written 16, 8, 4 or 2 bytes at a time, by what all the call's rows
  * are aligned to (base, strides, channels * sizeof(dtype)). The results depend
- * on the arguments, that alignment and the number of SMs only.
+ * on the arguments, that alignment, the number of SMs and the largest
+ * thread-block cluster that the device places only.
  */
 #define GN_MAX_CHANNELS 65536
 

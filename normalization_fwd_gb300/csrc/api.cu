@@ -23,6 +23,7 @@ ln_status cuda_fail(cudaError_t e) {
 
 constexpr int kMaxDevices = 64;
 int g_sm_count[kMaxDevices] = {0};
+std::atomic<int> g_cluster_limit[kMaxDevices];
 std::mutex g_mu;
 
 struct OccEntry {
@@ -116,6 +117,39 @@ int allow_dyn_smem(const void* fn, size_t smem) {
   if (smem + static_bytes > optin) return (int)cudaErrorInvalidValue;
   return (int)cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)(optin - static_bytes));
+}
+
+int cluster_limit(const void* fn, int block, size_t smem, int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  const bool kept = dev >= 0 && dev < kMaxDevices;
+  *out = kept ? g_cluster_limit[dev].load(std::memory_order_relaxed) : 0;
+  if (*out > 0) return (int)cudaSuccess;
+  e = (cudaError_t)allow_dyn_smem(fn, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return (int)e;
+  int s = 16;
+  for (; s > 1; s /= 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    if (e != cudaSuccess) return (int)e;
+    if (n > 0) break;
+  }
+  if (kept) g_cluster_limit[dev].store(s, std::memory_order_relaxed);
+  *out = s;
+  return (int)cudaSuccess;
 }
 
 int resident_blocks(const void* fn, int block, size_t smem, int* out) {

@@ -78,7 +78,7 @@ bool gn_tiles(int channels, int unit, int bytes, int es, GnPlan* p) {
 }
 
 bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t elem, bool bwd,
-             int grain, int sms, GnPlan* p) {
+             int grain, int sms, int most_cluster, GnPlan* p) {
   const int es = (int)elem, cpg = channels / groups;
   const int unit = cpg * (grain / gcd(cpg * es, grain));
   const int64_t places = (int64_t)sms * kPerSm[bwd];
@@ -118,8 +118,9 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t ele
     p->max_groups = max_groups(whole);
     const int64_t TY = kGnThreads / p->tw;
     // Clusters of 16 need 16 free places in one part of the chip: fewer of
-    // them fit than the SMs would hold CTAs.
-    while (s < 16 && p->panels * s < (int64_t)sms * 3 / 2 && rows > s * TY * 2 &&
+    // them fit than the SMs would hold CTAs. most_cluster: what the device
+    // places at all.
+    while (s < most_cluster && p->panels * s < (int64_t)sms * 3 / 2 && rows > s * TY * 2 &&
            !(s == 8 && p->panels > sms / 8))
       s *= 2;
     p->cluster = rows <= s * TY * kGnRing ||
@@ -203,11 +204,14 @@ int grain_of(const Strided& s, int most) {
 }
 
 ln_status plan_call(const GnCall& c, bool bwd, int grain, GnPlan* p) {
-  int sms = 0;
-  const cudaError_t e = (cudaError_t)device_sm_count(&sms);
+  int sms = 0, most_cluster = 1;
+  cudaError_t e = (cudaError_t)device_sm_count(&sms);
+  if (e == cudaSuccess && !bwd)
+    e = (cudaError_t)cluster_limit(gn_table_f32(false, true, true, kActNone), kGnThreads,
+                                   gn_smem_bytes(1, true), &most_cluster);
   if (e != cudaSuccess) return cuda_fail(e);
   return gn_plan(c.samples, c.rows, (int)c.channels, (int)c.groups, elem_size(c.dtype), bwd, grain,
-                 sms, p)
+                 sms, most_cluster, p)
              ? LN_OK
              : LN_ERR_SHAPE;
 }

@@ -41,6 +41,10 @@ int resident_blocks(const void* fn, int block, size_t smem, int* out);  // retur
 // Opt `fn` in to `smem` bytes of dynamic shared memory when that plus its
 // static shared memory passes the default 48 KiB (cached per kernel).
 int allow_dyn_smem(const void* fn, size_t smem);  // returns cudaError_t
+// Most CTAs of a thread-block cluster that the device (or the part of it that
+// the process has) places: 16, 8, 4, 2 or 1. `fn` stands for all kernels that
+// are launched in clusters, of `block` threads and `smem` bytes; asked once a device.
+int cluster_limit(const void* fn, int block, size_t smem, int* out);  // returns cudaError_t
 
 // Kernel family per direction (api.cu): 0 = the default for each shape,
 // 1 = the bulk-copy ring kernels wherever they apply. Only the testing hook

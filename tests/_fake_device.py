@@ -31,6 +31,11 @@ def load(folder):
     return lib
 
 
+def reset(lib, sms=152, most_cluster=16):
+    """A device of so many SMs that places clusters of so many CTAs."""
+    lib.fake_reset(sms, most_cluster)
+
+
 def counts(lib):
     """What was launched since the last reset."""
     out = (ctypes.c_int * len(COUNTS))()

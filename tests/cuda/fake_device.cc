@@ -7,7 +7,7 @@
 #include <stddef.h>
 
 namespace {
-int g_sms = 152;
+int g_sms = 152, g_most_cluster = 16;
 int g_launches, g_grid, g_cluster, g_finalizes, g_memsets;
 const int kKernel = 0;   // stands for every kernel
 
@@ -22,6 +22,10 @@ cudaError_t launched(dim3 grid, int cluster) {
 namespace nf {
 int device_sm_count(int* sms) {
   *sms = g_sms;
+  return (int)cudaSuccess;
+}
+int cluster_limit(const void*, int, size_t, int* out) {
+  *out = g_most_cluster;
   return (int)cudaSuccess;
 }
 int allow_dyn_smem(const void*, size_t) { return (int)cudaSuccess; }
@@ -47,6 +51,7 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* cfg, const void*, void
   for (unsigned i = 0; i < cfg->numAttrs; ++i)
     if (cfg->attrs[i].id == cudaLaunchAttributeClusterDimension)
       cluster = (int)cfg->attrs[i].val.clusterDim.x;
+  if (cluster > g_most_cluster) return cudaErrorInvalidClusterSize;
   return launched(cfg->gridDim, cluster);
 }
 cudaError_t cudaLaunchKernel(const void*, dim3 grid, dim3, void**, size_t, cudaStream_t) {
@@ -63,8 +68,9 @@ void __cudaUnregisterFatBinary(void**) {}
 
 // The test's part. out: kernel launches, the last one's grid and cluster,
 // finalize launches, memsets.
-void fake_reset(int sms) {
+void fake_reset(int sms, int most_cluster) {
   g_sms = sms;
+  g_most_cluster = most_cluster;
   g_launches = g_grid = g_cluster = g_finalizes = g_memsets = 0;
 }
 void fake_counts(int* out) {
