@@ -906,6 +906,8 @@ def _rope_fwd(device, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_center
     qs = _ROPE_HEADS.pack(q.data_ptr(), out_q.data_ptr(),
                           _gamma_ptr(q_gamma, "rope_fwd: q_gamma", D, q.dtype), shape[2], *xs, *ys)
     ks = None
+    if (k is None) != (out_k is None):
+        raise ValueError("rope_fwd: k and out_k go together")
     if k is not None:
         kshape, xs = _heads(k, "rope_fwd: k")
         _, ys = _heads(out_k, "rope_fwd: out_k", k)
@@ -955,6 +957,8 @@ def _rope_bwd(device, dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zer
     lib = _lib or load_library()
     shape, _ = _heads(dq, "rope_bwd: dq")
     D = shape[3]
+    if (dk is None) != (out_dk is None) or (dk is None and dk_gamma is not None):
+        raise ValueError("rope_bwd: dk, out_dk and dk_gamma go together")
     grads = [g for g in (dq_gamma, dk_gamma) if g is not None]
     for g in grads:
         if g.shape != (D,) or not g.is_contiguous() or g.dtype != grads[0].dtype:
