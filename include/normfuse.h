@@ -434,7 +434,8 @@ ln_status gn_workspace_bytes(int64_t samples, int64_t rows, int64_t channels, in
  *   y0 = scale * (u0 cos t - u1 sin t), y1 = scale * (u1 cos t + u0 sin t);
  * y is rounded once, to dtype. Angles are exact modulo one turn (the
  * frequency as a 64-bit fraction of a turn times the integer position), so
- * positions of any size, negative ones too, lose nothing to fp32.
+ * positions of any size, negative ones too, lose nothing to fp32. A frequency
+ * that is infinite or NaN makes its pair's results NaN, at position 0 too.
  *
  * An output may be its own input (same pointer and strides); apart from that
  * outputs overlap neither inputs nor each other nor themselves. Interleaved

@@ -27,7 +27,6 @@
 #pragma once
 
 #include "common.cuh"
-#include "fastdiv.h"
 
 namespace nf {
 
@@ -141,7 +140,7 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
   const unsigned long long k1 = 0xa2f9836e4e441529ull, k0 = 0xfc2757d1f534ddc1ull;
   const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
   const int ex = (int)(bits >> 52) & 0x7ff;
-  if (ex == 0 || ex == 0x7ff) return 0;   // zero, below 2^-1022, or not finite
+  if (ex == 0 || ex == 0x7ff) return 0;   // zero, below 2^-1022, or not finite (see finite_turns)
   const unsigned long long m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
   // m * K = (w2, w1, w0)
   const unsigned long long w0 = m * k0, w1 = m * k1 + __umul64hi(m, k0);
@@ -154,6 +153,12 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
   else if (sh == 0) t = w1;
   else t = sh > -64 ? (w1 << -sh) | (w0 >> (64 + sh)) : 0;
   return (long long)bits < 0 ? 0ull - t : t;
+}
+
+// An infinity or a NaN has no fraction of a turn: its pair's cosines and sines
+// are NaN, as the definition gives them for any position.
+__device__ __forceinline__ bool finite_turns(double f) {
+  return ((unsigned long long)__double_as_longlong(f) >> 52 & 0x7ff) != 0x7ff;
 }
 
 // Sine and cosine of t 2^-32 turns: the nearest quarter turn, then the Taylor
@@ -346,9 +351,17 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
     }
   const int j = threadIdx.x & (A.wide - 1);      // this thread's pair
   unsigned long long turns = 0;
+  bool finite = true;                            // all of its frequencies are
   if (A.axes == 1) {
-    if (j < A.rot / 2) turns = turns_of(A.freqs[j]);
+    if (j < A.rot / 2) {
+      const double f = A.freqs[j];
+      turns = turns_of(f);
+      finite = finite_turns(f);
+    }
   } else {
+#pragma unroll
+    for (int ax = 0; ax < kRopeMaxAxes; ++ax)
+      if (j < A.rot / 2 && ax < A.axes) finite &= finite_turns(A.freqs[ax * (A.rot / 2) + j]);
     for (int i = threadIdx.x; i < A.axes * (A.rot / 2); i += kRopeThreads)
       tab_t[i] = turns_of(A.freqs[i]);
     __syncthreads();
@@ -423,10 +436,11 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(RopeArg
             for (int i = 0; i < 4; ++i) {
               const int t = t0 + i * step;
               if (t < toks) {
+                const float kNaN = __int_as_float(0x7fffffff);
                 float s, c;
                 sincos_turns((unsigned)((sum[i] + 0x80000000ull) >> 32), &s, &c);
-                tab_c[t * A.row + j] = c * A.scale_c;
-                tab_s[t * A.row + j] = s * A.scale_s;
+                tab_c[t * A.row + j] = finite ? c * A.scale_c : kNaN;
+                tab_s[t * A.row + j] = finite ? s * A.scale_s : kNaN;
               }
             }
           }
