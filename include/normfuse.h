@@ -367,7 +367,9 @@ typedef enum { GN_ACT_NONE = 0, GN_ACT_SILU = 1, GN_ACT_GELU = 2 } gn_act;
  * 1 + gamma; act: none, z / (1 + e^-z), or z * Phi(z) (the exact GELU).
  *
  * x          [samples, rows, channels], required. rows up to 2^40, samples
- *            below 2^31.
+ *            below 2^31; LN_ERR_SHAPE too where samples times the column
+ *            tiles (64 bytes of channels and more) or times the slices of
+ *            the rows reach 2^31, which no y below 128 GiB does.
  * gamma      NULL = 1; beta NULL = 0.
  * eps        >= 0 and finite.
  * y          as x, required; overlaps no input and not itself.

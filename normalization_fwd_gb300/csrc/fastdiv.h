@@ -5,8 +5,10 @@
 
 namespace nf {
 
-// Division of n < 2^31 by a number fixed for the launch: with s = ceil(log2 d)
-// and m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n m) + n) >> s.
+// Division of n < 2^31 by a number fixed for the launch, by a product and a
+// shift (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (hi32(n m) + n) >> s.
 struct FastDiv {
   unsigned d, m, s;
   void set(unsigned v) {

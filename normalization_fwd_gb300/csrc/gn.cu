@@ -88,11 +88,15 @@ bool gn_plan(int64_t samples, int64_t rows, int channels, int groups, size_t ele
     return m < groups ? m : groups;
   };
   // Forward: one launch, a cluster a panel, where a thread's rows all stay in
-  // its slots (4 x 205 x 192 bf16 6.3 us, two launches 10.0), and for vectors
+  // its slots (4 x 205 x 192 bf16 5.8 us, two launches 9.3), and for vectors
   // where panels are small and clusters of 16 fill the SMs (16 x 1024 x 1280
-  // bf16 26 us against 32, 2 x 4096 x 320 fp16 10 against 13; but with a
-  // panel of 3 MB, 2 x 39760 x 160 fp16, 28 against 24, and with 64 CTAs, 4 x
-  // 12708 x 104, 17 against 12). The backward, whose rows take twice the
+  // bf16 26 us against 32, 2 x 4096 x 320 fp16 10.6 against 13.2; but with a
+  // panel of 3 MB, 2 x 39760 x 160 fp16, 30 against 26, and with 64 CTAs, 4 x
+  // 12708 x 104, 18 against 15). How much all panels at a time are is not in
+  // the rule: past the L2 cache the rows come out of DRAM twice, which costs
+  // less than the second launch for 64 x 4096 x 320 fp16 (168 MB of rows at a
+  // time, 89 us against 95) and more for 64 x 4096 x 640 (299 MB, 189 against
+  // 172). The backward, whose rows take twice the
   // shared memory and registers, has its two launches always: one launch of
   // clusters took 22 us for 2 x 4096 x 640 fp16 (two 20), 62 for 13 x 9961 x
   // 40 bf16 (36).

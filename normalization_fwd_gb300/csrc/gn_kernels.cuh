@@ -13,14 +13,19 @@
 // pairs, which this part adds, multiplies and fmas in one instruction.
 //
 // Statistics and result need two passes over the rows. The second comes out of
-// the thread's slots in shared memory or the L2 cache, so DRAM sees each tensor
-// once; what bounds the kernels is the arithmetic of two passes (some 100
-// instructions for 16 bytes of bf16 with SiLU, half of them pairs that take the
-// pipe two cycles: issue active 50 %, and math pipe and not-selected stalls
-// next to those on memory). Measured, SiLU, back to back:
-//   forward  2 x 262144 x 256 bf16   139 us, 3.9 TB/s
+// the thread's slots in shared memory or the L2 cache, so that DRAM sees each
+// tensor once, except where the panels that clusters work on at a time are
+// more than the cache holds (64 x 4096 x 320 fp16: 168 MB of rows at a time,
+// 327 MB read for 168). No unit is full in the large cases: DRAM 56 % of its
+// peak, the FMA pipe 38 % (its heavy half 45 %) in the forward and 45 % (50 %)
+// in the backward, with a third and a quarter of the warps that an SM could
+// have. The kernels wait, for memory and for the results of their own
+// instructions, with too few warps to cover it: 80 registers and 58 KB of
+// shared memory a CTA in the forward, 126 registers in the backward. Measured,
+// SiLU, back to back:
+//   forward  2 x 262144 x 256 bf16   137 us, 3.9 TB/s
 //            16 x 1024 x 1280 bf16    26 us, 3.2 TB/s (out of the L2 cache)
-//            2 x 4096 x 320 fp16      10 us: latency of load, merge and store
+//            2 x 4096 x 320 fp16      10.6 us: latency of load, merge and store
 //   backward 8 x 16384 x 320 bf16     82 us, 3.1 TB/s
 //            2 x 4096 x 640 fp16      20 us, 1.5 TB/s
 #pragma once
@@ -357,7 +362,7 @@ __device__ __forceinline__ void gn_columns(const GnArgs& a, const GnUnit& u, GnS
 // the slots, and a second pass starts with those while it fetches the others
 // again. Copies are of 16, 8 or 4 bytes, by the rows' alignment; rows that are
 // aligned to 2 bytes pass through registers. Eight rows: with four 16 x 1024 x
-// 1280 bf16 takes 29 us for 26 and 2 x 262144 x 256 takes 147 for 139; with
+// 1280 bf16 took 29 us for 26 and 2 x 262144 x 256 took 147 for 139; with
 // sixteen a CTA fewer fits an SM.
 __device__ __forceinline__ void copy_async16(unsigned dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

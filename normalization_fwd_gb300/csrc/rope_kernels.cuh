@@ -15,11 +15,11 @@
 // modulo one turn exactly, and its top 32 bits give sine and cosine. The error
 // is that of the frequency itself times the position, plus 2^-33 turns.
 //
-// Every tensor is read and written once. What bounds the kernel is the
-// arithmetic beside the loads: norm, rotation, conversions and addresses issue
-// in 50 % of the cycles of the forward (half of them pairs, which take the pipe
-// two) with 24 warps an SM, which its 80 registers allow, and too few loads in
-// flight to cover the rest. Measured, back to back, with norm:
+// Every tensor is read and written once. The forward reaches 0.80 of the copy
+// rate; neither DRAM (61 % of its peak) nor the FMA pipe (34 %, its heavy half
+// 44 %) is full: norm, rotation, conversions and addresses issue in half of the
+// cycles, and 24 warps an SM, which its 80 registers allow, have too few loads
+// in flight to cover the rest. Measured, back to back, with norm:
 //   forward  1 x 16384 tokens, 32 + 8 heads of 128, bf16   62 us, 5.4 TB/s
 //            64 x 1 token                                   3.9 us (latency)
 //   backward 4 x 4096 tokens, 16 + 4 heads of 64, bf16      36 us, 3.5 TB/s:

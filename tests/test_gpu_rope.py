@@ -5,8 +5,8 @@ Bounds, with u = 2^-24 and half the step of the output format on top:
 
 * the angle: the frequency as a 64-bit fraction of a turn is off by 2^-64
   turns a position, its top 32 bits by 2^-33 turns: 2^-30 radians with the
-  fp32 rounding of the fraction at most 2^-24 pi; sincospi is good to 2 ulp.
-  12 u of the pair's size together.
+  fp32 rounding of the fraction at most 2^-24 pi; the Taylor series of the rest
+  to the nearest quarter turn are good to 2 ulp. 12 u of the pair's size together.
 * u = x rstd w: 512 squares at most, 16 in a thread and the rest by a tree:
   32 u relative, with the root, the quotient and two products.
 * the rotation: two products and a sum, 4 u of the pair's size.
