@@ -535,6 +535,115 @@ ln_status rope_frequencies(int64_t rot, double base, rope_scaling scaling, doubl
                            int64_t original, double turns_fast, double turns_slow,
                            double* freqs, float* scale);
 
+/*
+ * Matrices in 8 and 4 bits with scales, the norms that end in them and the
+ * product that starts from them.
+ *
+ * ln_fwd_ex casts y with one scale that the caller has from an earlier step.
+ * Here the scales are found in the same pass, for a row or a block of columns:
+ *   MX_FP8_ROW   E4M3 codes, one fp32 scale a row
+ *   MX_FP8_BLOCK E4M3 codes, one fp32 scale for 128 columns of a row
+ *   MX_MXFP8     E4M3 codes, one E8M0 scale (2^(byte - 127)) for 32 columns
+ *   MX_MXFP4     E2M1 codes, one E8M0 scale for 32 columns
+ *   MX_NVFP4     E2M1 codes, one E4M3 scale for 16 columns, of the values times
+ *                *mul
+ * The formats of the last three are those of the OCP microscaling
+ * specification (2023) and NVIDIA's NVFP4. With amax the largest |v| of a row or
+ * block, all in fp32, round to nearest even:
+ *   fp32 scale   a = max(amax, 2^-100), scale = a / 448, code = E4M3(v * (448 / a))
+ *   E8M0         scale = the least 2^e, e >= -127, with amax <= M 2^e (M = 448 or
+ *                6), code = E4M3 or E2M1(v / 2^e)
+ *   E4M3         u = v * *mul, scale = E4M3(amax(u) / 6), at most 448,
+ *                code = E2M1(u / scale), at most 6; 0 where the scale is 0
+ * so a value is code * scale (MX_NVFP4: / *mul). A row or block that holds an
+ * infinity or a NaN has a NaN for its scale and codes of 0. The blocks begin at
+ * column 0; the last one of a row may be narrower.
+ *
+ * Layout. MX_FP8_ROW and MX_FP8_BLOCK: codes [rows, cols] bytes, scales [rows]
+ * or [rows, ceil(cols / 128)] fp32. The microscaled formats: a row of codes is
+ * padded with zero codes to 32 columns; E2M1 codes go two a byte, the first in
+ * the low half. Their scales lie in tiles of 128 rows by 4 blocks, 512 bytes,
+ * the tiles of 128 rows one after the other: block b of row r is at
+ *   ((r / 128) * ceil(blocks / 4) + b / 4) * 512 + (r % 32) * 16 +
+ *   (r % 128 / 32) * 4 + b % 4,
+ * and bytes of rows or blocks that the matrix does not have are 0. That is the
+ * layout that block-scaled matrix products of this GPU generation take.
+ */
+typedef enum {
+  MX_FP8_ROW = 0,
+  MX_FP8_BLOCK = 1,
+  MX_MXFP8 = 2,
+  MX_MXFP4 = 3,
+  MX_NVFP4 = 4
+} mx_format;
+
+typedef struct {
+  void* codes;       /* device; microscaled formats: 16-byte aligned */
+  void* scales;      /* device; 4-byte, microscaled formats 16-byte aligned */
+  const float* mul;  /* MX_NVFP4: one positive finite fp32 on the device (commonly
+                        2688 / amax of the matrix), NULL = 1; else ignored */
+  mx_format format;
+  int64_t rows;      /* 0 .. 2^31 - 129 */
+  int64_t cols;      /* 1 .. 2^31 - 129 */
+} mx_matrix;
+
+/* Bytes of a matrix's codes and of its scales. */
+ln_status mx_matrix_bytes(mx_format format, int64_t rows, int64_t cols, size_t* codes,
+                          size_t* scales);
+
+/*
+ * mx_norm_fwd: ln_fwd with its result quantised into `q` ([rows, hidden]): the
+ * fp32 result, not one rounded to dtype first. out_sum, mean and rstd are what
+ * ln_bwd takes, so the backward is that of the norm with the gradient of the
+ * dequantised result passed straight through.
+ *
+ * y    [rows, hidden] dtype, NULL = not stored.
+ * q    overlaps no other tensor of the call.
+ * Other arguments, alignment, limits of hidden and errors are those of ln_fwd
+ * (q's codes count as a tensor pointer for the vectorised path); rows stay
+ * below 2^31 - 128.
+ */
+ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, const void* gamma,
+                      const void* beta, float eps, ln_mode mode, int zero_centered_gamma,
+                      void* out_sum, void* y, float* mean, float* rstd, const mx_matrix* q,
+                      cudaStream_t stream, ln_dtype dtype);
+
+/*
+ * mx_quantize: x, or with `transpose` its transpose, into q. x is [q.rows,
+ * q.cols] ([q.cols, q.rows] with transpose), columns contiguous, x_row >= 0
+ * elements from one row to the next. A transposed operand is what a product's
+ * gradients need: they contract over the rows.
+ */
+ln_status mx_quantize(const void* x, int64_t x_row, int transpose, const mx_matrix* q,
+                      cudaStream_t stream, ln_dtype dtype);
+
+/* mx_dequantize: the values of q, rounded to dtype, into y [rows, cols], y_row
+ * >= cols elements from one row to the next. */
+ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t stream,
+                        ln_dtype dtype);
+
+/*
+ * mx_product: out[m, n] = alpha * sum over k of A[m, k] * B[n, k] + bias[n] +
+ * residual[m, n], A and B the values of two matrices of one microscaled format
+ * with the same number of columns (for a projection: activations by rows and
+ * weights by output features). Products are exact, sums fp32 in the tensor
+ * cores, the scales' included; the rest is fp32, rounded once to dtype.
+ *
+ * bias      [N] dtype, NULL = none.
+ * residual  [M, N] dtype, residual_row elements a row, NULL = none; may be out
+ *           itself (same row stride), overlaps it in no other way.
+ * out       [M, N] dtype, out_row >= N elements a row.
+ * psum, psq [M, ceil(N / 128)] fp32 or NULL (both or none): sums of the stored
+ *           rows over tiles of 128 columns and their squares about the tile's
+ *           mean: what ln_fwd_from_partials takes as LN_PARTIALS_SUM_M2 with
+ *           tile_cols = 128.
+ * The result does not depend on how often or where the call runs on one GPU
+ * model: sums that are split are joined in a fixed order.
+ */
+ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const void* bias,
+                     const void* residual, int64_t residual_row, void* out, int64_t out_row,
+                     float* psum, float* psq, cudaStream_t stream, ln_dtype dtype);
+
 /* Static, human-readable name of a status code. */
 const char* ln_status_string(ln_status status);
 

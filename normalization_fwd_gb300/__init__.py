@@ -18,6 +18,7 @@ import functools
 import os
 import struct
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -38,6 +39,9 @@ __all__ = [
     "fused_group_norm_fwd", "fused_group_norm_bwd",
     "ROPE_HALF", "ROPE_INTERLEAVED", "rope_fwd", "rope_bwd", "rope_bwd_workspace_bytes",
     "rope_frequencies", "rope_axes", "fused_rope_fwd", "fused_rope_bwd",
+    "MX_FP8_ROW", "MX_FP8_BLOCK", "MX_MXFP8", "MX_MXFP4", "MX_NVFP4", "Quantized",
+    "quantized_empty", "mx_matrix_bytes", "mx_norm_fwd", "mx_quantize", "mx_dequantize",
+    "mx_product", "fused_norm_quant_fwd", "quantize", "dequantize", "scaled_product",
 ]
 
 # Mirrors of include/normfuse.h (a CPU test checks them against the header).
@@ -62,6 +66,11 @@ _SCALING_CODES = {"none": 0, None: 0, "linear": 1, "ntk": 2, "yarn": 3}
 _ROPE_HEADS = struct.Struct("@PPPq3q3q")
 _ROPE_HEADS_GRAD = struct.Struct("@PPPPPq3q3q3q")
 _ROPE_POSITIONS = struct.Struct("@Piq3qPqif")
+MX_FP8_ROW, MX_FP8_BLOCK, MX_MXFP8, MX_MXFP4, MX_NVFP4 = range(5)
+_FORMAT_CODES = {"fp8_row": MX_FP8_ROW, "fp8_block": MX_FP8_BLOCK, "mxfp8": MX_MXFP8,
+                 "mxfp4": MX_MXFP4, "nvfp4": MX_NVFP4}
+# The C struct mx_matrix.
+_MX_MATRIX = struct.Struct("@PPPiqq")
 
 _lib = None
 _lock = threading.Lock()
@@ -141,18 +150,30 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                          ctypes.c_double, ctypes.c_double, vp,
                                          ctypes.POINTER(f32)]
         lib.rope_frequencies.restype = ci
+        lib.mx_matrix_bytes.argtypes = [ci, i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        lib.mx_matrix_bytes.restype = ci
+        lib.mx_norm_fwd.argtypes = [vp, vp, vp, vp, vp, f32, ci, ci, vp, vp, vp, vp, vp, vp, ci]
+        lib.mx_norm_fwd.restype = ci
+        lib.mx_quantize.argtypes = [vp, i64, ci, vp, vp, ci]
+        lib.mx_quantize.restype = ci
+        lib.mx_dequantize.argtypes = [vp, vp, i64, vp, ci]
+        lib.mx_dequantize.restype = ci
+        lib.mx_product.argtypes = [vp, vp, f32, vp, vp, i64, vp, i64, vp, vp, vp, ci]
+        lib.mx_product.restype = ci
         _lib = lib
         return lib
 
 
 def exported_symbols(prefix: str = "ln_") -> list[str]:
     """Names of the C entry points this binding wraps that start with
-    ``prefix``: "ln_", "gn_" (group norm) or "rope_" (rotary positions)."""
+    ``prefix``: "ln_", "gn_" (group norm), "rope_" (rotary positions) or "mx_"
+    (quantised matrices)."""
     names = ["ln_fwd", "ln_fwd_ex", "ln_bwd", "ln_bwd_ex", "ln_bwd_workspace_bytes",
              "ln_status_string", "ln_last_cuda_error", "ln_device_error", "ln_bwd_noalloc",
              "ln_softmax_fwd", "ln_testing_select_kernels", "ln_fwd_from_partials",
              "ln_testing_plan", "gn_fwd", "gn_bwd", "gn_workspace_bytes", "rope_fwd", "rope_bwd",
-             "rope_bwd_workspace_bytes", "rope_frequencies"]
+             "rope_bwd_workspace_bytes", "rope_frequencies", "mx_matrix_bytes", "mx_norm_fwd",
+             "mx_quantize", "mx_dequantize", "mx_product"]
     return [n for n in names if n.startswith(prefix)]
 
 
@@ -1044,3 +1065,286 @@ def fused_rope_bwd(dq, dk, positions, freqs, *, q=None, k=None, q_gamma=None, k_
     _rope_bwd(device, dq, dk, q, k, positions, freqs, q_gamma, k_gamma, eps, zero_centered_gamma,
               interleaved, scale, out_dq, out_dk, gq, gk, workspace)
     return {"dq": out_dq, "dk": out_dk, "dq_gamma": gq, "dk_gamma": gk}
+
+
+# ---- quantised matrices ----------------------------------------------------------
+
+class Quantized(NamedTuple):
+    """A matrix in 8 or 4 bits with scales (``mx_matrix`` in include/normfuse.h).
+
+    ``format`` is "fp8_row", "fp8_block", "mxfp8", "mxfp4" or "nvfp4". ``codes``
+    [rows, columns] are float8_e4m3fn, of the 4-bit formats uint8 with two codes a
+    byte; microscaled rows are padded to 32 columns. ``scales`` are float32 [rows]
+    or [rows, blocks], of the microscaled formats [rows / 128, blocks / 4, 32, 4, 4]
+    (rounded up) of float8_e8m0fnu or, for nvfp4, float8_e4m3fn. ``mul`` is the
+    float32 that nvfp4's values were multiplied by (one element; None: 1).
+    """
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    format: str
+    rows: int
+    cols: int
+    mul: torch.Tensor | None = None
+
+
+def _format(format) -> int:
+    try:
+        return _FORMAT_CODES[format]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown format {format!r}") from None
+
+
+def mx_matrix_bytes(format, rows, cols) -> tuple[int, int]:
+    """Bytes of a quantised matrix's codes and of its scales."""
+    lib = load_library()
+    codes, scales = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    st = lib.mx_matrix_bytes(_format(format), int(rows), int(cols), ctypes.byref(codes),
+                             ctypes.byref(scales))
+    if st:
+        raise NormError(st, "mx_matrix_bytes")
+    return int(codes.value), int(scales.value)
+
+
+@functools.lru_cache(maxsize=4096)
+def _quantized_layout(fmt, rows, cols):
+    """(shape and type of the codes, of the scales, bytes of either)."""
+    e4m3 = torch.float8_e4m3fn
+    bytes_of = mx_matrix_bytes(fmt, rows, cols)
+    if fmt in ("fp8_row", "fp8_block"):
+        scales = (rows,) if fmt == "fp8_row" else (rows, -(-cols // 128))
+        return (rows, cols), e4m3, scales, torch.float32, bytes_of
+    pitch = bytes_of[0] // rows if rows else -(-cols // 32) * (32 if fmt == "mxfp8" else 16)
+    blocks = -(-cols // (16 if fmt == "nvfp4" else 32))
+    return ((rows, pitch), e4m3 if fmt == "mxfp8" else torch.uint8,
+            (-(-rows // 128), -(-blocks // 4), 32, 4, 4),
+            e4m3 if fmt == "nvfp4" else torch.float8_e8m0fnu, bytes_of)
+
+
+def quantized_empty(rows, cols, format, *, mul=None, device="cuda") -> Quantized:
+    """A matrix with room for codes and scales, not initialised."""
+    _format(format)
+    cshape, ctype, sshape, stype, _ = _quantized_layout(format, int(rows), int(cols))
+    return Quantized(torch.empty(cshape, dtype=ctype, device=device),
+                     torch.empty(sshape, dtype=stype, device=device), format, int(rows), int(cols),
+                     mul)
+
+
+def _matrix(where, q):
+    """The packed mx_matrix struct of ``q``."""
+    if not isinstance(q, Quantized):
+        raise TypeError(f"{where}: expected a Quantized, got {type(q).__name__}")
+    code = _format(q.format)
+    need = _quantized_layout(q.format, q.rows, q.cols)[4]
+    for t, name, n in ((q.codes, "codes", need[0]), (q.scales, "scales", need[1])):
+        if t.numel() * t.element_size() != n or not t.is_contiguous():
+            raise ValueError(f"{where}: the {name} of {q.rows} x {q.cols} {q.format} must be "
+                             f"contiguous, of {n} bytes")
+    mul = q.mul if q.format == "nvfp4" else None
+    if mul is not None and (mul.numel() != 1 or mul.dtype != torch.float32):
+        raise ValueError(f"{where}: mul must be one float32")
+    return _MX_MATRIX.pack(q.codes.data_ptr(), q.scales.data_ptr(),
+                           0 if mul is None else mul.data_ptr(), code, q.rows, q.cols)
+
+
+def _vector(where, name, t, n, dtype):
+    if t is None:
+        return None
+    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous [{n}] of {dtype}")
+    return t.data_ptr()
+
+
+def _whole(where, name, t, ref):
+    if t is None:
+        return None
+    if t.shape != ref.shape or t.dtype != ref.dtype or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous, of the shape and dtype of x")
+    return t.data_ptr() or None
+
+
+def mx_norm_fwd(x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma, out_sum, y, mean,
+                rstd, q, stream=None) -> None:
+    """Enqueue the fused forward of ``ln_fwd`` with its result in ``q`` (a
+    ``Quantized`` of [rows, hidden]); y may be None. See ``mx_norm_fwd`` in
+    include/normfuse.h."""
+    device = _device_of("mx_norm_fwd", x, bias, residual, gamma, beta, out_sum, y, mean, rstd,
+                        q.codes, q.scales, q.mul)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return mx_norm_fwd(x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma,
+                               out_sum, y, mean, rstd, q)
+    where = "mx_norm_fwd"
+    lib = _lib or load_library()
+    rows, hidden = _shape(x)
+    if (q.rows, q.cols) != (rows, hidden):
+        raise ValueError(f"{where}: q must be {rows} x {hidden}, is {q.rows} x {q.cols}")
+    if not x.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    stats = [_vector(where, n, t, rows, torch.float32) for n, t in (("mean", mean), ("rstd", rstd))]
+    st = lib.mx_norm_fwd(
+        x.data_ptr() or None, _vector(where, "bias", bias, hidden, x.dtype),
+        _whole(where, "residual", residual, x), _vector(where, "gamma", gamma, hidden, x.dtype),
+        _vector(where, "beta", beta, hidden, x.dtype), eps, _mode(mode),
+        1 if zero_centered_gamma else 0, _whole(where, "out_sum", out_sum, x),
+        _whole(where, "y", y, x), *stats, _matrix(where, q), _raw_stream(device) or None, _dtype(x))
+    if st:
+        raise NormError(st, where)
+
+
+def _plane(where, name, t, shape=None, dtype=None):
+    """Row stride of a matrix [rows, cols] whose columns are contiguous."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape) or (dtype and t.dtype != dtype):
+        raise ValueError(f"{where}: {name} must be "
+                         + (f"{list(shape)} of {dtype}" if shape is not None else "a matrix"))
+    _dense_last(t, f"{where}: {name}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def mx_quantize(x, q, *, transpose=False, stream=None) -> None:
+    """Enqueue the quantisation of the matrix ``x`` (its transpose with
+    ``transpose``) into ``q``; the rows of x may be any distance apart."""
+    device = _device_of("mx_quantize", x, q.codes, q.scales, q.mul)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return mx_quantize(x, q, transpose=transpose)
+    lib = _lib or load_library()
+    row = _plane("mx_quantize", "x", x)
+    if (tuple(x.shape[::-1]) if transpose else tuple(x.shape)) != (q.rows, q.cols):
+        raise ValueError(f"mx_quantize: x of {list(x.shape)} into {q.rows} x {q.cols}")
+    st = lib.mx_quantize(x.data_ptr() or None, row, 1 if transpose else 0,
+                         _matrix("mx_quantize", q), _raw_stream(device) or None, _dtype(x))
+    if st:
+        raise NormError(st, "mx_quantize")
+
+
+def mx_dequantize(q, y, stream=None) -> None:
+    """Enqueue the values of ``q`` into the matrix ``y``."""
+    device = _device_of("mx_dequantize", q.codes, q.scales, q.mul, y)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return mx_dequantize(q, y)
+    lib = _lib or load_library()
+    row = _plane("mx_dequantize", "y", y, (q.rows, q.cols), y.dtype)
+    st = lib.mx_dequantize(_matrix("mx_dequantize", q), y.data_ptr() or None, max(row, q.cols)
+                           if q.rows <= 1 else row, _raw_stream(device) or None, _dtype(y))
+    if st:
+        raise NormError(st, "mx_dequantize")
+
+
+def mx_product(a, b, alpha, bias, residual, out, psum, psq, stream=None) -> None:
+    """Enqueue out = alpha * a @ b.T + bias + residual of two microscaled
+    matrices; psum and psq (float32 [rows, ceil(columns / 128)], or None) take
+    the statistics of 128-column tiles for ``ln_fwd_from_partials``. See
+    ``mx_product`` in include/normfuse.h."""
+    device = _device_of("mx_product", out, a.codes, a.scales, a.mul, b.codes, b.scales, b.mul, bias,
+                        residual, psum, psq)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return mx_product(a, b, alpha, bias, residual, out, psum, psq)
+    where = "mx_product"
+    lib = _lib or load_library()
+    shape = (a.rows, b.rows)
+    row = _plane(where, "out", out, shape, out.dtype)
+    res_row = row if residual is None else _plane(where, "residual", residual, shape, out.dtype)
+    for t in (psum, psq):
+        if t is not None and (t.shape != (a.rows, -(-b.rows // 128)) or t.dtype != torch.float32
+                              or not t.is_contiguous()):
+            raise ValueError(f"{where}: psum and psq must be contiguous float32 "
+                             f"[{a.rows}, {-(-b.rows // 128)}]")
+    st = lib.mx_product(_matrix(where, a), _matrix(where, b), alpha,
+                        _vector(where, "bias", bias, b.rows, out.dtype),
+                        None if residual is None else residual.data_ptr() or None, res_row,
+                        out.data_ptr() or None, row, None if psum is None else psum.data_ptr() or None,
+                        None if psq is None else psq.data_ptr() or None, _raw_stream(device) or None,
+                        _dtype(out))
+    if st:
+        raise NormError(st, where)
+
+
+def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, residual=None,
+                         eps=1e-5, mode="layernorm", zero_centered_gamma=False, store_sum=None,
+                         store_y=False, stream=None):
+    """The fused forward of ``fused_norm_fwd`` with its result quantised: returns
+    a dict with ``q`` (a ``Quantized`` of [rows, hidden]), ``sum`` (or None),
+    ``y`` (in x's dtype, with ``store_y``), ``mean`` (LayerNorm) and ``rstd``.
+
+    ``fused_norm_bwd`` on ``sum`` (or x), ``mean`` and ``rstd`` is its backward,
+    the gradient of the dequantised result passed straight through. ``mul`` is
+    nvfp4's factor (one float32 on the device, commonly 2688 over the largest
+    magnitude seen).
+    """
+    device = _device_of("fused_norm_quant_fwd", x, gamma, beta, mul, bias, residual)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return fused_norm_quant_fwd(x, gamma, beta, format=format, mul=mul, bias=bias,
+                                        residual=residual, eps=eps, mode=mode,
+                                        zero_centered_gamma=zero_centered_gamma,
+                                        store_sum=store_sum, store_y=store_y)
+    rows, hidden = _shape(x)
+    if store_sum is None:
+        store_sum = bias is not None or residual is not None
+    rms = _mode(mode) == LN_RMSNORM
+    q = quantized_empty(rows, hidden, format, mul=mul, device=x.device)
+    out_sum = torch.empty_like(x) if store_sum else None
+    y = torch.empty_like(x) if store_y else None
+    mean = None if rms else torch.empty(rows, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    mx_norm_fwd(x, bias, residual, gamma, None if rms else beta, eps, mode, zero_centered_gamma,
+                out_sum, y, mean, rstd, q)
+    return {"q": q, "sum": out_sum, "y": y, "mean": mean, "rstd": rstd}
+
+
+def quantize(x, format, *, mul=None, transpose=False, stream=None) -> Quantized:
+    """The matrix ``x``, or its transpose, in 8 or 4 bits with scales. Rows of x
+    may be any distance apart (a slice of a wider tensor)."""
+    device = _device_of("quantize", x, mul)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return quantize(x, format, mul=mul, transpose=transpose)
+    if x.dim() != 2:
+        raise ValueError("quantize: x must be a matrix")
+    rows, cols = x.shape[::-1] if transpose else x.shape
+    q = quantized_empty(rows, cols, format, mul=mul, device=x.device)
+    mx_quantize(x, q, transpose=transpose)
+    return q
+
+
+def dequantize(q, dtype=torch.float32, *, out=None, stream=None):
+    """The values of ``q`` as a [rows, cols] tensor of ``dtype``."""
+    device = _device_of("dequantize", q.codes, q.scales, q.mul, out)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return dequantize(q, dtype, out=out)
+    if out is None:
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+    mx_dequantize(q, out)
+    return out
+
+
+def scaled_product(a, b, *, alpha=1.0, bias=None, residual=None, dtype=torch.bfloat16, out=None,
+                   partials=False, stream=None):
+    """alpha * a @ b.T + bias + residual of two ``Quantized`` matrices of one
+    microscaled format with equal columns (activations and a projection's
+    weights); returns a dict with ``out`` [a.rows, b.rows] and, with
+    ``partials``, ``psum``, ``psq`` and ``tile_cols`` for
+    ``fused_norm_fwd_from_partials(..., kind="sum_m2")``.
+
+    ``bias`` [b.rows] and ``residual`` [a.rows, b.rows] are of the output's
+    dtype; ``out`` may be the residual itself. Its gradients are products, too:
+    quantise the output's gradient and the weights (transpose=True) for the
+    input's, both operands transposed for the weights'.
+    """
+    device = _device_of("scaled_product", a.codes, a.scales, b.codes, b.scales, bias, residual, out)
+    if _elsewhere(device, stream):
+        with _current(device, stream):
+            return scaled_product(a, b, alpha=alpha, bias=bias, residual=residual, dtype=dtype,
+                                  out=out, partials=partials)
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
+    psum = psq = None
+    if partials:
+        psum, psq = torch.empty((2, a.rows, -(-b.rows // 128)), dtype=torch.float32,
+                                device=a.codes.device)
+    mx_product(a, b, alpha, bias, residual, out, psum, psq)
+    return {"out": out, "psum": psum, "psq": psq, "tile_cols": 128}

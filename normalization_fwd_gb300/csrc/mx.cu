@@ -1,0 +1,241 @@
+// Norms with quantised results, the quantiser and its inverse: C entry points,
+// argument checks and launch plan.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/normfuse.h"
+#include "launch.h"
+#include "mx_check.h"
+#include "mx_norm_kernels.cuh"
+#include "mx_quantize_kernels.cuh"
+#include "validate.h"
+
+namespace nf {
+
+const void* mx_norm_table_f32(int cls, int lanes, int n);
+const void* mx_norm_table_bf16(int cls, int lanes, int n);
+const void* mx_norm_table_f16(int cls, int lanes, int n);
+
+namespace {
+
+ln_status cuda_fail(cudaError_t e) {
+  nf_set_last_cuda_error((int)e);
+  return LN_ERR_CUDA;
+}
+
+int class_of(int fmt) { return fmt == MX_FP8_ROW ? 0 : mx_four(fmt) ? 2 : 1; }
+
+// Lanes a row (0: a CTA), vectors a lane and threads for rows of `slots` 16-byte
+// vectors, room for codes included. As in the 16-bit forward: lane groups up to
+// 160 vectors, four vectors a lane where the row splits evenly, then a CTA
+// fitted to the row. A block of 128 columns needs 16 lanes (32 for fp32).
+struct NormPlan {
+  int lanes = -1, n = 0, block = kScalarCta;
+};
+NormPlan norm_plan(int slots, int least_lanes) {
+  NormPlan p;
+  if (slots <= 160) {
+    for (int n : {4, 3, 5, 2, 1}) {
+      const int lanes = slots / n;
+      if (slots % n == 0 && (lanes == 8 || lanes == 16 || lanes == 32) && lanes >= least_lanes)
+        return {lanes, n, kBulkThreads};
+    }
+    int idle = 1 << 30;
+    for (int lanes : {32, 16, 8}) {
+      const int n = (slots + lanes - 1) / lanes;
+      if (lanes < least_lanes || n > 5 || lanes * n - slots >= idle) continue;
+      idle = lanes * n - slots;
+      p = {lanes, n, kBulkThreads};
+    }
+    return p;
+  }
+  int idle = 1 << 30;
+  for (int n : {4, 5, 3, 6, 8, 2}) {
+    const int nt = std::max(64, (slots + 32 * n - 1) / (32 * n) * 32);
+    if (nt > kMaxFitThreads || nt * n - slots >= idle) continue;
+    idle = nt * n - slots;
+    p = {0, n, nt};
+  }
+  return p;
+}
+
+int64_t padded_rows(const QuantOut& q) { return mx_tiled(q.fmt) ? (q.rows + 127) / 128 * 128 : q.rows; }
+
+template <typename T>
+cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStream_t st) {
+  const QuantOut& q = a.q;
+  const int cls = class_of(q.fmt);
+  if (transpose) {
+    const int64_t rows = std::max(a.padded_rows, q.rows);
+    const int64_t x = (rows + kTrRows - 1) / kTrRows, tiles = (q.cols + kTrCols - 1) / kTrCols;
+    const dim3 grid((unsigned)x, cls == 0 ? 1u : (unsigned)std::min<int64_t>(tiles, 65535));
+    if (cls == 0) quant_transpose_kernel<T, 0><<<grid, kQuantThreads, 0, st>>>(a);
+    else if (cls == 1) quant_transpose_kernel<T, 1><<<grid, kQuantThreads, 0, st>>>(a);
+    else quant_transpose_kernel<T, 2><<<grid, kQuantThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  if (cls == 0) {
+    quant_row_kernel<T><<<(unsigned)std::min<int64_t>(q.rows, 1 << 20), kQuantThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const int64_t chunks = (q.cols + 255) / 256;
+  const int64_t ctas = (a.padded_rows * chunks + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 8 * 16);
+  if (cls == 1) quant_block_kernel<T, 1><<<grid, kQuantThreads, 0, st>>>(a, chunks);
+  else quant_block_kernel<T, 2><<<grid, kQuantThreads, 0, st>>>(a, chunks);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace nf
+
+using namespace nf;
+
+extern "C" {
+
+ln_status mx_matrix_bytes(mx_format format, int64_t rows, int64_t cols, size_t* codes,
+                          size_t* scales) {
+  if (codes == nullptr || scales == nullptr) return LN_ERR_NULL;
+  if (!known_format(format)) return LN_ERR_UNSUPPORTED;
+  if (!fits(rows, cols)) return LN_ERR_SHAPE;
+  *codes = code_bytes(format, rows, cols);
+  *scales = scale_bytes(format, rows, cols);
+  return LN_OK;
+}
+
+ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, const void* gamma,
+                      const void* beta, float eps, ln_mode mode, int zero_centered_gamma,
+                      void* out_sum, void* y, float* mean, float* rstd, const mx_matrix* q,
+                      cudaStream_t stream, ln_dtype dtype) {
+  if (q == nullptr) return LN_ERR_NULL;
+  if (!known_dtype(dtype) || !known_format(q->format)) return LN_ERR_UNSUPPORTED;
+  if (mode != LN_LAYERNORM && mode != LN_RMSNORM) return LN_ERR_UNSUPPORTED;
+  const int64_t rows = q->rows, hidden = q->cols;
+  if (rows < 0 || hidden < 1 || rows > INT32_MAX - 128) return LN_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return LN_ERR_INVALID;
+  const bool rms = mode == LN_RMSNORM;
+  if (rms) {
+    beta = nullptr;
+    mean = nullptr;
+  }
+  if (gamma == nullptr) return LN_ERR_NULL;
+  if (rows > 0 && x == nullptr) return LN_ERR_NULL;
+  ln_status st = check_matrix(*q);
+  if (st != LN_OK) return st;
+  const size_t es = elem_size(dtype);
+  const void* tensors[] = {x, bias, residual, gamma, beta, out_sum, y};
+  for (const void* p : tensors)
+    if (!aligned(p, es)) return LN_ERR_ALIGN;
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return LN_ERR_ALIGN;
+  bool vec = (hidden * (int64_t)es) % 16 == 0;
+  for (const void* p : tensors)
+    if (!aligned(p, 16)) vec = false;
+  if (!aligned(q->codes, 16)) vec = false;
+  if (vec && hidden > (int64_t)(16 / es) * kMaxVecSlots) vec = false;
+  if (!vec && hidden > kMaxHiddenScalar) return LN_ERR_SHAPE;
+  const size_t mat = (size_t)rows * (size_t)hidden * es, vecb = (size_t)hidden * es;
+  const Range outs[] = {{out_sum, mat}, {y, mat}, {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4},
+                        codes_range(*q), scales_range(*q)};
+  const Range ins[] = {{x, mat}, {residual, mat}, {bias, vecb}, {gamma, vecb}, {beta, vecb},
+                       mul_range(*q)};
+  if (any_overlap(outs, 6, ins, 6)) return LN_ERR_INVALID;
+  if (rows == 0) return LN_OK;
+
+  MxNormArgs a = {};
+  a.f.x = x;
+  a.f.bias = bias;
+  a.f.residual = residual;
+  a.f.gamma = gamma;
+  a.f.beta = beta;
+  a.f.out_sum = out_sum;
+  a.f.y = y;
+  a.f.mean = mean;
+  a.f.rstd = rstd;
+  a.f.rows = rows;
+  a.f.hidden = (int)hidden;
+  a.f.eps = eps;
+  a.f.rms = rms ? 1 : 0;
+  a.f.zero_centered = zero_centered_gamma ? 1 : 0;
+  a.q = quant_out(*q);
+  a.padded_rows = padded_rows(a.q);
+  const int cls = class_of(q->format), per = (int)(16 / es);
+  NormPlan p;
+  if (vec) {
+    const int64_t wide = mx_tiled(q->format) ? (hidden + 31) / 32 * 32 : hidden;
+    p = norm_plan((int)((wide + per - 1) / per), q->format == MX_FP8_BLOCK ? 128 / per : 8);
+  }
+  const void* fn = dtype == LN_F32 ? mx_norm_table_f32(cls, p.lanes, p.n)
+                   : dtype == LN_BF16 ? mx_norm_table_bf16(cls, p.lanes, p.n)
+                                      : mx_norm_table_f16(cls, p.lanes, p.n);
+  int64_t grid = a.padded_rows;
+  size_t smem = 0;
+  if (p.lanes > 0) grid = (a.padded_rows + 256 / p.lanes - 1) / (256 / p.lanes);
+  if (p.lanes < 0) smem = (size_t)(hidden + 127) / 128 * 512;
+  void* args[] = {&a};
+  const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(p.block), args, smem, stream);
+  return e == cudaSuccess ? LN_OK : cuda_fail(e);
+}
+
+ln_status mx_quantize(const void* x, int64_t x_row, int transpose, const mx_matrix* q,
+                      cudaStream_t stream, ln_dtype dtype) {
+  if (q == nullptr) return LN_ERR_NULL;
+  if (!known_dtype(dtype) || !known_format(q->format)) return LN_ERR_UNSUPPORTED;
+  ln_status st = check_matrix(*q);
+  if (st != LN_OK) return st;
+  const int64_t rows = transpose ? q->cols : q->rows, cols = transpose ? q->rows : q->cols;
+  const size_t es = elem_size(dtype);
+  if (q->rows > 0 && x == nullptr) return LN_ERR_NULL;
+  if (x_row < 0 || (rows > 1 && x_row > INT64_MAX / 16 / rows)) return LN_ERR_INVALID;
+  if (!aligned(x, es)) return LN_ERR_ALIGN;
+  const size_t span = q->rows > 0 ? (size_t)((rows - 1) * x_row + cols) * es : 0;
+  const Range outs[] = {codes_range(*q), scales_range(*q)};
+  const Range ins[] = {{x, span}, mul_range(*q)};
+  if (any_overlap(outs, 2, ins, 2)) return LN_ERR_INVALID;
+  if (q->rows == 0) return LN_OK;
+  int sms = 0;
+  cudaError_t e = (cudaError_t)device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  QuantArgs a = {};
+  a.x = x;
+  a.x_row = x_row;
+  a.q = quant_out(*q);
+  a.vec = aligned(x, 16) && (rows == 1 || (x_row * es) % 16 == 0);
+  a.vec_codes = aligned(q->codes, 16);
+  a.padded_rows = padded_rows(a.q);
+  e = by_dtype(dtype, [&](auto t) { return launch_quantize<decltype(t)>(a, transpose, sms, stream); });
+  return e == cudaSuccess ? LN_OK : cuda_fail(e);
+}
+
+ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t stream,
+                        ln_dtype dtype) {
+  if (q == nullptr) return LN_ERR_NULL;
+  if (!known_dtype(dtype) || !known_format(q->format)) return LN_ERR_UNSUPPORTED;
+  ln_status st = check_matrix(*q);
+  if (st != LN_OK) return st;
+  const size_t es = elem_size(dtype);
+  if (q->rows > 0 && y == nullptr) return LN_ERR_NULL;
+  if (y_row < q->cols || (q->rows > 1 && y_row > INT64_MAX / 16 / q->rows)) return LN_ERR_INVALID;
+  if (!aligned(y, es)) return LN_ERR_ALIGN;
+  const size_t span = q->rows > 0 ? (size_t)((q->rows - 1) * y_row + q->cols) * es : 0;
+  const Range outs[] = {{y, span}};
+  const Range ins[] = {codes_range(*q), scales_range(*q), mul_range(*q)};
+  if (any_overlap(outs, 1, ins, 3)) return LN_ERR_INVALID;
+  if (q->rows == 0) return LN_OK;
+  int sms = 0;
+  cudaError_t e = (cudaError_t)device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const QuantOut o = quant_out(*q);
+  const bool vec = aligned(y, 16) && (q->rows == 1 || (y_row * es) % 16 == 0);
+  const int64_t chunks = (q->cols + 7) / 8;
+  const int64_t ctas = (q->rows * chunks + kQuantThreads - 1) / kQuantThreads;
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 8 * 16);
+  e = by_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    dequant_kernel<T><<<grid, kQuantThreads, 0, stream>>>(o, static_cast<T*>(y), y_row, vec, chunks);
+    return cudaGetLastError();
+  });
+  return e == cudaSuccess ? LN_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,225 @@
+// 8- and 4-bit formats with scales: layouts, and the device functions that
+// turn fp32 values into codes and scales and back.
+//
+//   format      code   scale              covers        value
+//   MX_FP8_ROW   E4M3  fp32               a row         code * scale
+//   MX_FP8_BLOCK E4M3  fp32               128 columns   code * scale
+//   MX_MXFP8     E4M3  E8M0 (2^(b - 127)) 32 columns    code * scale
+//   MX_MXFP4     E2M1  E8M0               32 columns    code * scale
+//   MX_NVFP4     E2M1  E4M3               16 columns    code * scale / mul
+//
+// The last three are the microscaled ones. Their rows of codes are padded with
+// zeros to 32 columns (so that a row starts on 16 bytes), and their scales lie
+// in tiles of 128 rows by 4 blocks, 512 bytes each: the scale of row r, block
+// b of a tile is byte (r % 32) * 16 + (r / 32) * 4 + b. That is how the tensor
+// cores take them (32 lanes of 16 bytes), so a tile goes there as it lies.
+// Tiles run along a row first; what lies behind the last row or block is 0.
+#pragma once
+
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "../../include/normfuse.h"
+#include "common.cuh"
+
+namespace nf {
+
+constexpr unsigned kInfBits = 0x7f800000u;
+constexpr float kLeastAmax = 0x1p-100f;   // fp8_row, fp8_block: smaller ones count as this
+
+inline __host__ __device__ bool mx_tiled(int fmt) { return fmt >= MX_MXFP8; }
+inline __host__ __device__ bool mx_four(int fmt) { return fmt >= MX_MXFP4; }
+// Columns of a block; a row's (MX_FP8_ROW) is given as 0.
+inline __host__ __device__ int mx_block(int fmt) {
+  return fmt == MX_NVFP4 ? 16 : fmt == MX_FP8_BLOCK ? 128 : fmt == MX_FP8_ROW ? 0 : 32;
+}
+inline __host__ __device__ int64_t mx_pitch(int fmt, int64_t cols) {   // bytes of a row of codes
+  if (!mx_tiled(fmt)) return cols;
+  const int64_t padded = (cols + 31) / 32 * 32;
+  return mx_four(fmt) ? padded / 2 : padded;
+}
+inline __host__ __device__ int64_t mx_blocks(int fmt, int64_t cols) {
+  const int b = mx_block(fmt);
+  return b == 0 ? 1 : (cols + b - 1) / b;
+}
+
+// Where a call writes a quantised matrix.
+struct QuantOut {
+  unsigned char* codes;
+  void* scales;          // float, or bytes in tiles
+  const float* mul;      // MX_NVFP4: factor of the values before, null = 1
+  int64_t rows;
+  int64_t cols;
+  int64_t pitch;         // bytes of a row of codes
+  int64_t blocks;        // of a row
+  int fmt;
+};
+
+// Offset of a block's scale byte in the tiles.
+__host__ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t block, int64_t blocks) {
+  return ((row >> 7) * ((blocks + 3) >> 2) + (block >> 2)) * 512 + (row & 31) * 16 +
+         ((row >> 5) & 3) * 4 + (block & 3);
+}
+
+// A scale and the factor that goes with it: codes are those of v * factor
+// (for MX_NVFP4: v / scale, see quotient2). `bits` of a block's largest |v|;
+// infinite or NaN makes the scale NaN and the codes 0.
+struct BlockScale {
+  float factor;          // 0: all codes are 0
+  float scale;           // MX_NVFP4: the scale's value; fp32 formats: the scale
+  unsigned byte;         // microscaled formats
+};
+
+// E8M0: the least power of two 2^e, e >= -127, with amax <= MOST * 2^e, by the
+// bits of amax: its exponent less that of MOST (8 or 2), one more where its
+// fraction is larger than that of MOST (448 = 1.75 * 2^8, 6 = 1.5 * 2^2). No
+// value saturates.
+template <bool FOUR>
+__device__ __forceinline__ BlockScale scale_e8m0(unsigned bits) {
+  constexpr unsigned kRound = FOUR ? 0x3fffffu : 0x1fffffu;
+  constexpr int kTop = FOUR ? 2 : 8;
+  BlockScale s;
+  const int e = max((int)((bits + kRound) >> 23) - kTop, 0);
+  const bool odd = bits >= kInfBits;
+  s.byte = odd ? 0xffu : (unsigned)e;
+  s.factor = odd ? 0.f : __uint_as_float((unsigned)(254 - e) << 23);
+  s.scale = 0.f;
+  return s;
+}
+
+// E4M3 scale of a block of MX_NVFP4: amax / 6, rounded to E4M3 (448 at most).
+__device__ __forceinline__ BlockScale scale_e4m3(unsigned bits) {
+  BlockScale s;
+  if (bits >= kInfBits) return {0.f, 0.f, 0x7fu};
+  const float t = __uint_as_float(bits) / 6.0f;
+  s.byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+  s.scale = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s.byte, __NV_E4M3)));
+  s.factor = s.byte ? 1.0f / s.scale : 0.f;
+  return s;
+}
+
+// fp32 scale: amax / 448, with amax no less than 2^-100 (so that 448 / amax is
+// finite and the scale normal).
+__device__ __forceinline__ BlockScale scale_fp32(unsigned bits) {
+  if (bits >= kInfBits) return {0.f, __uint_as_float(0x7fffffffu), 0u};
+  const float a = fmaxf(__uint_as_float(bits), kLeastAmax);
+  return {448.0f / a, a / 448.0f, 0u};
+}
+
+// v / s, correctly rounded, from r = 1 / s rounded to nearest: q = v r is
+// within a rounding or two, and the remainder v - q s, exact in one fma, gives
+// the correction (Markstein 1990). E2M1 has only eight magnitudes, 16-bit
+// values often lie on the middle between two of them, and a quotient that is
+// off by a rounding would fall to the wrong side.
+__device__ __forceinline__ float2 quotient2(float2 v, float s, float r) {
+  const float2 q = mul2(v, splat2(r));
+  const float2 rem = fma2(make_float2(-q.x, -q.y), splat2(s), v);
+  return fma2(rem, splat2(r), q);
+}
+
+// Codes of 2P values. FOUR: 2P / 2 bytes, else 2P bytes, the first value lowest.
+template <int P>
+__device__ __forceinline__ void codes_e4m3(const float2* v, float factor, unsigned* out) {
+  const float2 f = splat2(factor);
+#pragma unroll
+  for (int i = 0; i < P; i += 2) out[i / 2] = (unsigned)fp8x2(v[i], f) | ((unsigned)fp8x2(v[i + 1], f) << 16);
+  if (factor == 0.f) {   // an infinity times 0 is not 0
+#pragma unroll
+    for (int i = 0; i < P; i += 2) out[i / 2] = 0u;
+  }
+}
+__device__ __forceinline__ unsigned fp4x2(float2 v) {
+  return (unsigned)__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest);
+}
+// 2P / 2 bytes in the low end of the result (P = 2, 4).
+template <int P>
+__device__ __forceinline__ unsigned codes_e2m1(const float2* v, const BlockScale& s, bool nvfp4) {
+  unsigned out = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const float2 q = nvfp4 ? quotient2(v[i], s.scale, s.factor) : mul2(v[i], splat2(s.factor));
+    out |= fp4x2(q) << (8 * i);
+  }
+  return s.factor == 0.f ? 0u : out;
+}
+
+// Largest |v| of 2P values as bits (NaN wins).
+template <int P>
+__device__ __forceinline__ unsigned amax_of(const float2* v) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) m = max(m, max(abs_bits(v[i].x), abs_bits(v[i].y)));
+  return m;
+}
+// Largest over aligned groups of `lanes` lanes (a power of two), by all lanes of the warp.
+__device__ __forceinline__ unsigned lanes_max(unsigned m, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// Store VEC codes of the columns from `col` on (col a multiple of VEC).
+template <int VEC>
+__device__ __forceinline__ void put_codes(unsigned char* p, const unsigned* c, bool four) {
+  if (four) {
+    if (VEC == 8) *reinterpret_cast<unsigned*>(p) = c[0];
+    else *reinterpret_cast<unsigned short*>(p) = (unsigned short)c[0];
+  } else {
+    if (VEC == 8) *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
+    else *reinterpret_cast<unsigned*>(p) = c[0];
+  }
+}
+
+// Scale and codes of a block whose values lie in `lanes` neighbouring lanes,
+// VEC each, in columns col .. col + VEC - 1 of the lane (values behind the
+// last column are 0). All lanes of the warp call it; `live` lanes write.
+// CLS: 1 E4M3, 2 E2M1.
+template <int VEC, int CLS>
+__device__ __forceinline__ void put_block(const QuantOut& q, int64_t row, int64_t col, bool live,
+                                          float2* v, float mul, bool bytes_only = false) {
+  constexpr int P = VEC / 2;
+  const int width = mx_block(q.fmt);
+  if (CLS == 2 && q.fmt == MX_NVFP4) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], splat2(mul));
+  }
+  const unsigned m = lanes_max(amax_of<P>(v), width / VEC);
+  unsigned c[VEC / 4 > 0 ? VEC / 4 : 1];
+  BlockScale s;
+  if (CLS == 1) {
+    s = q.fmt == MX_MXFP8 ? scale_e8m0<false>(m) : scale_fp32(m);
+    codes_e4m3<P>(v, s.factor, c);
+  } else {
+    s = q.fmt == MX_MXFP4 ? scale_e8m0<true>(m) : scale_e4m3(m);
+    c[0] = codes_e2m1<P>(v, s, q.fmt == MX_NVFP4);
+  }
+  if (!live) return;
+  unsigned char* row_codes = q.codes + row * q.pitch;
+  if (CLS == 2) {
+    put_codes<VEC>(row_codes + col / 2, c, true);
+  } else if (!bytes_only) {
+    put_codes<VEC>(row_codes + col, c, false);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (col + i < q.pitch) row_codes[col + i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
+  }
+  if (col % width == 0 && col < q.cols) {
+    const int64_t b = col / width;
+    if (CLS == 1 && q.fmt == MX_FP8_BLOCK) static_cast<float*>(q.scales)[row * q.blocks + b] = s.scale;
+    else static_cast<unsigned char*>(q.scales)[scale_at(row, b, q.blocks)] = (unsigned char)s.byte;
+  }
+}
+
+// The scale bytes behind a row's last block, and all of a row behind the last
+// row, are 0. `t` of `n` threads.
+__device__ __forceinline__ void put_padding(const QuantOut& q, int64_t row, int t, int n) {
+  const int64_t first = row < q.rows ? q.blocks : 0;
+  for (int64_t b = first + t; b < (q.blocks + 3) / 4 * 4; b += n)
+    static_cast<unsigned char*>(q.scales)[scale_at(row, b, q.blocks)] = 0;
+}
+
+__device__ __forceinline__ float mul_of(const QuantOut& q) {
+  return q.fmt == MX_NVFP4 && q.mul != nullptr ? *q.mul : 1.0f;
+}
+
+}  // namespace nf

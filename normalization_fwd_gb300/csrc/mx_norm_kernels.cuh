@@ -1,0 +1,294 @@
+// The fused block's forward (bias + residual addition, LayerNorm or RMSNorm)
+// with its result in 8 or 4 bits and scales (mx_formats.cuh).
+//
+// A row stays in registers from its one read to its codes, as in the 16-bit
+// forward: sum and its rounding, mean, centred squares, then y in fp32, which
+// is quantised as it is (rounding it to the I/O type first would round twice).
+// A block's values lie in 2 to 32 neighbouring lanes, so its largest magnitude
+// takes 1 to 5 shuffles; a row's goes through the CTA as the sums do.
+// Bound by HBM: x and residual read, the sum and 0.5 to 1 bytes a value written.
+#pragma once
+
+#include "bulk.cuh"
+#include "common.cuh"
+#include "mx_formats.cuh"
+
+namespace nf {
+
+struct MxNormArgs {
+  FwdArgs f;       // y may be null; amax and y_fp8 are not used
+  QuantOut q;
+  int64_t padded_rows;   // rows whose scales are written: a multiple of 128 in tiles
+};
+
+// Rows in registers. CLS: 0 a scale a row, 1 blocks of E4M3, 2 blocks of E2M1.
+// G0 > 0: a group of G0 lanes a row; 0: the CTA.
+template <typename T, int G0, int N, int CLS, typename Sum, typename Max>
+__device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, int t, Sum reduce,
+                                            Max row_max) {
+  constexpr int VEC = Vec<T>::N;
+  constexpr int P = VEC / 2;
+  const FwdArgs& f = a.f;
+  const int G = G0 > 0 ? G0 : (int)blockDim.x;
+  const bool row_ok = row < f.rows;
+  const int H = f.hidden;
+  const int V = H / VEC;
+  const int64_t off = row * (int64_t)H;
+  const T* x = static_cast<const T*>(f.x) + off;
+  const T* res = f.residual ? static_cast<const T*>(f.residual) + off : nullptr;
+  uint4 xr[N], rr[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int v = k * G + t;
+    if (row_ok && v < V) {
+      xr[k] = ld_vec(x + v * VEC);
+      if (res) rr[k] = ld_vec(res + v * VEC);
+    }
+  }
+  if (CLS != 0 && mx_tiled(a.q.fmt) && row < a.padded_rows) put_padding(a.q, row, t, G);
+
+  float2 s[N][P];
+  float2 t1 = splat2(0.f);
+  T* sum_row = f.out_sum ? static_cast<T*>(f.out_sum) + off : nullptr;
+  const ParamRow<T> w_row = {nullptr, static_cast<const T*>(f.gamma), H, f.zero_centered != 0};
+  const ParamRow<T> bias_row = {nullptr, static_cast<const T*>(f.bias), H, false};
+  const ParamRow<T> beta_row = {nullptr, static_cast<const T*>(f.beta), H, false};
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int v = k * G + t;
+#pragma unroll
+    for (int i = 0; i < P; ++i) s[k][i] = splat2(0.f);
+    if (row_ok && v < V) {
+      unpack2<T>(xr[k], s[k]);
+      if (bias_row.g) {
+        float2 b[P];
+        bias_row.template load2<false>(v, b);
+#pragma unroll
+        for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], b[i]);
+      }
+      if (res) {
+        float2 r[P];
+        unpack2<T>(rr[k], r);
+#pragma unroll
+        for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], r[i]);
+      }
+      const uint4 packed = pack2<T>(s[k]);
+      if (sum_row) st_vec(sum_row + v * VEC, packed);
+      unpack2<T>(packed, s[k]);
+#pragma unroll
+      for (int i = 0; i < P; ++i) t1 = add2(t1, s[k][i]);
+    }
+  }
+  const float mean = f.rms ? 0.f : reduce(t1.x + t1.y) / (float)H;
+  const float2 neg_mean = splat2(-mean);
+  float2 t2 = splat2(0.f);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (row_ok && (k * G + t) < V) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        s[k][i] = add2(s[k][i], neg_mean);
+        t2 = fma2(s[k][i], s[k][i], t2);
+      }
+    }
+  }
+  const float rstd = 1.0f / sqrtf(reduce(t2.x + t2.y) / (float)H + f.eps);
+  if (row_ok && t == 0) {
+    if (f.mean) f.mean[row] = mean;
+    if (f.rstd) f.rstd[row] = rstd;
+  }
+
+  const float2 r2 = splat2(rstd);
+  const float mul = CLS == 2 ? mul_of(a.q) : 1.0f;
+  const int64_t wide = a.q.pitch * (CLS == 2 ? 2 : 1);   // columns with room for codes
+  unsigned m = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int v = k * G + t;
+    if (row_ok && v < V) {
+      float2 w[P], o[P];
+      w_row.template load2<false>(v, w);
+      if (beta_row.g) {
+        beta_row.template load2<false>(v, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = splat2(0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) s[k][i] = fma2(mul2(s[k][i], r2), w[i], o[i]);
+      if (f.y) st_vec(static_cast<T*>(f.y) + off + v * VEC, pack2<T>(s[k]));
+      if (CLS == 0) m = max(m, amax_of<P>(s[k]));
+    }
+    if (CLS != 0)
+      put_block<VEC, CLS>(a.q, row, (int64_t)v * VEC, row_ok && (int64_t)v * VEC < wide, s[k], mul);
+  }
+  if (CLS == 0) {
+    const BlockScale b = scale_fp32(row_max(m));
+    if (row_ok && t == 0) static_cast<float*>(a.q.scales)[row] = b.scale;
+    unsigned char* codes = a.q.codes + off;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int v = k * G + t;
+      if (row_ok && v < V) {
+        unsigned c[VEC / 4];
+        codes_e4m3<P>(s[k], b.factor, c);
+        put_codes<VEC>(codes + v * VEC, c, false);
+      }
+    }
+  }
+}
+
+// A tile of 8 * (32 / LANES) rows a CTA, a lane group a row.
+template <typename T, int LANES, int N, int CLS>
+__global__ void __launch_bounds__(kBulkThreads, N <= 3 ? 4 : 2) mx_norm_tile_kernel(const MxNormArgs a) {
+  constexpr int RPW = 32 / LANES;
+  const int lane = threadIdx.x & 31;
+  const int64_t row =
+      ((int64_t)blockIdx.x * kConsumerWarps + (threadIdx.x >> 5)) * RPW + lane / LANES;
+  mx_norm_row<T, LANES, N, CLS>(
+      a, row, lane % LANES, [](float v) { return group_sum<LANES>(v); },
+      [](unsigned v) { return lanes_max(v, LANES); });
+}
+
+// A CTA a row, blockDim.x * N vectors.
+template <typename T, int N, int CLS>
+__global__ void __launch_bounds__(kMaxFitThreads) __maxnreg__(N <= 4 ? 64 : 128) mx_norm_cta_kernel(const MxNormArgs a) {
+  __shared__ float red[2][kMaxFitWarps];
+  __shared__ unsigned red_max[kMaxFitWarps];
+  if (blockIdx.x >= a.f.rows) {    // the scales behind the last row
+    if (CLS != 0) put_padding(a.q, blockIdx.x, threadIdx.x, blockDim.x);
+    return;
+  }
+  int parity = 0;
+  mx_norm_row<T, 0, N, CLS>(
+      a, blockIdx.x, threadIdx.x, [&](float v) { return cta_sum_db_fit(v, red, parity); },
+      [&](unsigned v) {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if ((threadIdx.x & 31) == 0) red_max[threadIdx.x >> 5] = v;
+        __syncthreads();
+        unsigned m = 0;
+        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) m = max(m, red_max[i]);
+        return m;
+      });
+}
+
+// Any hidden size and alignment: a CTA a row, the row in shared memory, four
+// columns a lane when it comes to the codes. Dynamic shared memory: hidden
+// floats, rounded up to 128.
+template <typename T>
+__global__ void __launch_bounds__(kScalarCta) mx_norm_scalar_kernel(const MxNormArgs a) {
+  extern __shared__ float srow[];
+  __shared__ float red[kScalarCta / 32];
+  __shared__ unsigned red_max[kScalarCta / 32];
+  const FwdArgs& f = a.f;
+  const int H = f.hidden;
+  const T* x = static_cast<const T*>(f.x);
+  const T* res = static_cast<const T*>(f.residual);
+  const T* bias = static_cast<const T*>(f.bias);
+  const T* gamma = static_cast<const T*>(f.gamma);
+  const T* beta = static_cast<const T*>(f.beta);
+  T* out_sum = static_cast<T*>(f.out_sum);
+  T* y = static_cast<T*>(f.y);
+  const float mul = mul_of(a.q);
+  const int chunks = (H + 127) / 128;
+  for (int64_t row = blockIdx.x; row < a.padded_rows; row += gridDim.x) {
+    if (mx_tiled(a.q.fmt)) put_padding(a.q, row, threadIdx.x, kScalarCta);
+    if (row >= f.rows) continue;
+    const int64_t off = row * (int64_t)H;
+    float t1 = 0.f;
+    for (int j = threadIdx.x; j < H; j += kScalarCta) {
+      float s = to_f(x[off + j]);
+      if (bias) s += to_f(bias[j]);
+      if (res) s += to_f(res[off + j]);
+      const T st = from_f<T>(s);
+      if (out_sum) out_sum[off + j] = st;
+      s = to_f(st);
+      srow[j] = s;
+      t1 += s;
+    }
+    const float mean = f.rms ? 0.f : cta_sum<kScalarCta>(t1, red) / (float)H;
+    float t2 = 0.f;
+    for (int j = threadIdx.x; j < H; j += kScalarCta) {
+      const float d = srow[j] - mean;
+      t2 = fmaf(d, d, t2);
+    }
+    const float rstd = 1.0f / sqrtf(cta_sum<kScalarCta>(t2, red) / (float)H + f.eps);
+    if (threadIdx.x == 0) {
+      if (f.mean) f.mean[row] = mean;
+      if (f.rstd) f.rstd[row] = rstd;
+    }
+    unsigned m = 0;
+    for (int j = threadIdx.x; j < chunks * 128; j += kScalarCta) {
+      float o = 0.f;
+      if (j < H) {
+        const float w = f.zero_centered ? 1.0f + to_f(gamma[j]) : to_f(gamma[j]);
+        o = fmaf((srow[j] - mean) * rstd, w, beta ? to_f(beta[j]) : 0.f);
+        if (y) y[off + j] = from_f<T>(o);
+      }
+      srow[j] = o;
+      m = max(m, abs_bits(o));
+    }
+    if (a.q.fmt == MX_FP8_ROW) {
+      m = __reduce_max_sync(0xffffffffu, m);
+      if ((threadIdx.x & 31) == 0) red_max[threadIdx.x >> 5] = m;
+    }
+    __syncthreads();
+    if (a.q.fmt == MX_FP8_ROW) {
+      m = 0;
+      for (int i = 0; i < kScalarCta / 32; ++i) m = max(m, red_max[i]);
+      const BlockScale b = scale_fp32(m);
+      if (threadIdx.x == 0) static_cast<float*>(a.q.scales)[row] = b.scale;
+      for (int j = threadIdx.x; j < H; j += kScalarCta)
+        a.q.codes[off + j] = b.factor == 0.f ? 0 : fp8_one(srow[j], b.factor);
+    } else {
+      const int lane = threadIdx.x & 31;
+      for (int c = threadIdx.x >> 5; c < chunks; c += kScalarCta / 32) {
+        const int64_t col = c * 128 + lane * 4;
+        float2 v[2] = {make_float2(srow[col], srow[col + 1]), make_float2(srow[col + 2], srow[col + 3])};
+        if (mx_four(a.q.fmt))
+          put_block<4, 2>(a.q, row, col, col < a.q.pitch * 2, v, mul);
+        else
+          put_block<4, 1>(a.q, row, col, col < a.q.pitch, v, mul, !mx_tiled(a.q.fmt));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int LANES, int CLS> const void* mx_norm_tile_of(int n) {
+  switch (n) {
+    case 1: return (const void*)mx_norm_tile_kernel<T, LANES, 1, CLS>;
+    case 2: return (const void*)mx_norm_tile_kernel<T, LANES, 2, CLS>;
+    case 3: return (const void*)mx_norm_tile_kernel<T, LANES, 3, CLS>;
+    case 4: return (const void*)mx_norm_tile_kernel<T, LANES, 4, CLS>;
+    case 5: return (const void*)mx_norm_tile_kernel<T, LANES, 5, CLS>;
+    default: return nullptr;
+  }
+}
+template <typename T, int CLS> const void* mx_norm_cta_of(int n) {
+  switch (n) {
+    case 2: return (const void*)mx_norm_cta_kernel<T, 2, CLS>;
+    case 3: return (const void*)mx_norm_cta_kernel<T, 3, CLS>;
+    case 4: return (const void*)mx_norm_cta_kernel<T, 4, CLS>;
+    case 5: return (const void*)mx_norm_cta_kernel<T, 5, CLS>;
+    case 6: return (const void*)mx_norm_cta_kernel<T, 6, CLS>;
+    case 8: return (const void*)mx_norm_cta_kernel<T, 8, CLS>;
+    default: return nullptr;
+  }
+}
+// lanes 8, 16, 32: a lane group a row; 0: a CTA a row; -1: the scalar kernel.
+template <typename T, int CLS> const void* mx_norm_cls(int lanes, int n) {
+  switch (lanes) {
+    case 8: return mx_norm_tile_of<T, 8, CLS>(n);
+    case 16: return mx_norm_tile_of<T, 16, CLS>(n);
+    case 32: return mx_norm_tile_of<T, 32, CLS>(n);
+    default: return mx_norm_cta_of<T, CLS>(n);
+  }
+}
+template <typename T> const void* mx_norm_table(int cls, int lanes, int n) {
+  if (lanes < 0) return (const void*)mx_norm_scalar_kernel<T>;
+  return cls == 0 ? mx_norm_cls<T, 0>(lanes, n) : cls == 1 ? mx_norm_cls<T, 1>(lanes, n)
+                                                          : mx_norm_cls<T, 2>(lanes, n);
+}
+
+}  // namespace nf
