@@ -1,6 +1,9 @@
-// The product of two microscaled matrices: C entry point, argument checks and
-// launch plan.
+// The product of two microscaled matrices: C entry point, argument checks,
+// tensor maps and launch plan.
 #include <math.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "../../include/normfuse.h"
 #include "launch.h"
@@ -8,11 +11,123 @@
 #include "mx_product_kernels.cuh"
 
 namespace nf {
+
+cudaError_t take_error_product(cudaStream_t st, unsigned* out) { return take_tu_error(st, out); }
+
 namespace {
 
 ln_status cuda_fail(cudaError_t e) {
   nf_set_last_cuda_error((int)e);
   return LN_ERR_CUDA;
+}
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+
+cudaError_t encoder(Encode* out) {
+  static std::atomic<void*> kept{nullptr};
+  void* fn = kept.load(std::memory_order_relaxed);
+  if (fn == nullptr) {
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+    kept.store(fn, std::memory_order_relaxed);
+  }
+  *out = reinterpret_cast<Encode>(fn);
+  return cudaSuccess;
+}
+
+// Codes as rows of bytes, boxes of 128 bytes by `rows`, swizzled.
+cudaError_t codes_map(Encode encode, const QuantOut& q, int rows, CUtensorMap* map) {
+  const cuuint64_t dims[2] = {(cuuint64_t)q.pitch, (cuuint64_t)q.rows}, strides[1] = {(cuuint64_t)q.pitch};
+  const cuuint32_t box[2] = {kChunkBytes, (cuuint32_t)rows}, step[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.codes, dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// Scales as tiles of 128 words, [row tiles, tiles of a row], boxes of
+// `row_tiles` by `tiles`.
+cudaError_t scales_map(Encode encode, const QuantOut& q, int tiles, int row_tiles, CUtensorMap* map) {
+  const cuuint64_t across = (cuuint64_t)(q.blocks + 3) / 4;
+  const cuuint64_t dims[3] = {128, across, (cuuint64_t)(q.rows + 127) / 128}, strides[2] = {512, across * 512};
+  const cuuint32_t box[3] = {128, (cuuint32_t)tiles, (cuuint32_t)row_tiles}, step[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, q.scales, dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr uint32_t kSmemTarget = 200 * 1024;
+
+template <typename T, int FMT, bool SWAP>
+cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
+  const QuantOut &lanes = SWAP ? p.b : p.a, &columns = SWAP ? p.a : p.b;
+  const void* fn = (const void*)product_tile_kernel<T, FMT, SWAP>;
+  p.lane_tiles = (int)((lanes.rows + kTileLanes - 1) / kTileLanes);
+  const int64_t tiles = p.lane_tiles * ((columns.rows + p.cols - 1) / p.cols);
+  // K over so many CTAs as fill the SMs, each with two chunks at least.
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= sms && p.chunks >= p.splits * 4) p.splits *= 2;
+  const uint32_t stage = stage_bytes<FMT>(p.cols);
+  p.stages = (int)std::min<uint32_t>(kMaxStages, kSmemTarget / stage);
+  const size_t smem = std::max<size_t>((size_t)p.stages * stage, (SWAP ? p.cols : kTileLanes) * kResultPitch * 4) + 1024;
+  p.idesc = instr_desc(FMT, kTileLanes, p.cols);
+  if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
+
+  CUtensorMap maps[4];
+  Encode encode;
+  cudaError_t e = encoder(&encode);
+  if (e == cudaSuccess) e = codes_map(encode, lanes, kTileLanes, &maps[0]);
+  if (e == cudaSuccess) e = scales_map(encode, lanes, chunk_tiles<FMT>(), 1, &maps[1]);
+  if (e == cudaSuccess) e = codes_map(encode, columns, p.cols, &maps[2]);
+  if (e == cudaSuccess) e = scales_map(encode, columns, chunk_tiles<FMT>(), 1, &maps[3]);
+  if (e == cudaSuccess) e = (cudaError_t)allow_dyn_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  for (;; p.splits /= 2) {     // no larger clusters than the device places
+    cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+    attr[0].val.clusterDim.x = p.splits;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    int n = 1;
+    if (p.splits > 1) e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n > 0) break;
+  }
+  void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <typename T, int FMT>
+cudaError_t launch_format(ProductArgs p, int sms, cudaStream_t st) {
+  p.chunks = (int)((p.a.pitch + kChunkBytes - 1) / kChunkBytes);
+  p.steps = (int)((p.a.pitch + 31) / 32);
+  if (p.a.rows <= 64) {
+    p.cols = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64;
+    return launch_tiles<T, FMT, true>(p, sms, st);
+  }
+  p.cols = 128;
+  return launch_tiles<T, FMT, false>(p, sms, st);
+}
+
+template <typename T>
+cudaError_t launch_product(const ProductArgs& p, int sms, cudaStream_t st) {
+  switch (p.a.fmt) {
+    case MX_MXFP8: return launch_format<T, MX_MXFP8>(p, sms, st);
+    case MX_MXFP4: return launch_format<T, MX_MXFP4>(p, sms, st);
+    default: return launch_format<T, MX_NVFP4>(p, sms, st);
+  }
 }
 
 }  // namespace
@@ -49,6 +164,9 @@ ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const 
                        mul_range(*b), {bias, (size_t)N * es},
                        {in_place ? nullptr : residual, (size_t)((M - 1) * residual_row + N) * es}};
   if (any_overlap(outs, 3, ins, 8)) return LN_ERR_INVALID;
+  int sms = 0;
+  cudaError_t e = (cudaError_t)device_sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
   ProductArgs p = {};
   p.a = quant_out(*a);
   p.b = quant_out(*b);
@@ -60,7 +178,9 @@ ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const 
   p.out_row = out_row;
   p.psum = psum;
   p.psq = psq;
-  const cudaError_t e = by_dtype(dtype, [&](auto t) { return product_launch<decltype(t)>(p, stream); });
+  const auto four = [&](const void* t, int64_t row) { return aligned(t, 4 * es) && (M == 1 || row % 4 == 0); };
+  p.vec = four(out, out_row) && (residual == nullptr || four(residual, residual_row));
+  e = by_dtype(dtype, [&](auto t) { return launch_product<decltype(t)>(p, sms, stream); });
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }
 

@@ -1,14 +1,35 @@
-// The product of two microscaled matrices, simplest form: 64 x 64 results a
-// CTA, values of 32 columns at a time in shared memory, 4 x 4 results a thread.
+// The product of two microscaled matrices on the tensor cores.
+//
+// A tile of results has 128 lanes of tensor memory by `cols` columns. One of the
+// operands lies along the lanes (128 of its rows), the other along the columns.
+// With few rows of A (SWAP) the lanes are B's rows (a projection's output
+// features) and the columns A's: 16, 32 or 64 tokens cost a tile of that width
+// and not one of 128. Otherwise lanes are A's rows and the 128 columns B's.
+//
+// K goes by in chunks of 128 bytes of codes a row (256 E2M1 or 128 E4M3): one
+// thread copies a chunk's codes and scales to a ring of stages (tensor maps;
+// the codes in the swizzle that the matrix instructions read, the scales as
+// they lie, which is how tensor memory wants them), another one moves the scales
+// on to tensor memory and issues four instructions of 32 bytes of K. Scales
+// have four buffers there, and a buffer is only written again when the
+// instructions that read it are known to be done.
+//
+// Few tiles: K is split over the CTAs of a cluster. Each gets the tile's rows
+// of results that it is to finish from all others through distributed shared
+// memory and adds them in the order of the ranks.
+//
+// Every wait gives up after a second, reports it (ln_device_error) and lets the
+// kernel end; barriers of the cluster are passed by every thread in any case.
 #pragma once
 
 #include "common.cuh"
 #include "mx_formats.cuh"
+#include "tcgen05.cuh"
 
 namespace nf {
 
 struct ProductArgs {
-  QuantOut a, b;
+  QuantOut a, b;         // A [M, K], B [N, K]
   float alpha;
   const void* bias;
   const void* residual;
@@ -16,76 +37,241 @@ struct ProductArgs {
   void* out;
   int64_t out_row;
   float *psum, *psq;
+  int cols;              // columns of a tile
+  int lane_tiles;        // tiles along the lanes' operand; the grid's x is lane_tiles * column tiles
+  int splits;            // CTAs of a cluster, each with its share of the chunks
+  int chunks;            // of K
+  int steps;             // instructions along all of K
+  int stages;
+  int vec;               // out and residual can be accessed four at a time
+  uint32_t idesc;
 };
 
-__device__ __forceinline__ float mx_value(const QuantOut& q, int64_t row, int64_t col) {
-  if (row >= q.rows || col >= q.cols) return 0.f;
-  const unsigned b = static_cast<const unsigned char*>(q.scales)[scale_at(row, col / mx_block(q.fmt), q.blocks)];
-  const float s = q.fmt == MX_NVFP4 ? __half2float(__half(__nv_cvt_fp8_to_halfraw((unsigned char)b, __NV_E4M3)))
-                  : b == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 1u << 22);
-  const unsigned char* codes = q.codes + row * q.pitch;
-  if (q.fmt == MX_MXFP8) return s * __half2float(__half(__nv_cvt_fp8_to_halfraw(codes[col], __NV_E4M3)));
-  const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(codes[col / 2], __NV_E2M1));
-  return s * __half2float(col & 1 ? __high2half(h) : __low2half(h));
+constexpr int kTileLanes = 128;
+constexpr int kTileThreads = 256;
+constexpr int kChunkBytes = 128;
+constexpr int kScaleBufs = 4;
+constexpr int kTmemCols = 256;      // 128 of results, 4 buffers of 32 for scales
+constexpr int kScaleCol = 128;
+constexpr int kResultPitch = 132;   // floats of a row of results in shared memory
+constexpr int kMaxStages = 10;
+
+// 512-byte tiles of scales that a chunk takes.
+template <int FMT> __host__ __device__ constexpr int chunk_tiles() { return FMT == MX_NVFP4 ? 4 : FMT == MX_MXFP4 ? 2 : 1; }
+template <int FMT> __host__ __device__ constexpr uint32_t stage_bytes(int cols) {
+  return (uint32_t)(kTileLanes + cols) * kChunkBytes + 2u * chunk_tiles<FMT>() * 512u;
 }
 
+// Rounding of a row of up to 128 results, four a lane, and its statistics.
 template <typename T>
-__global__ void __launch_bounds__(256) product_simple_kernel(const ProductArgs p) {
-  __shared__ float as[32][65], bs[32][65];
-  const int64_t m0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < p.a.cols; k0 += 32) {
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-      as[i & 31][i >> 5] = mx_value(p.a, m0 + (i >> 5), k0 + (i & 31));
-      bs[i & 31][i >> 5] = mx_value(p.b, n0 + (i >> 5), k0 + (i & 31));
-    }
-    __syncthreads();
-    for (int k = 0; k < 32; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+__device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int64_t n0, float4 acc,
+                                           float f) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n = n0 + lane * 4;
+  const int live = (int)max((int64_t)0, min((int64_t)4, p.b.rows - n));
+  float v[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
+  const T* res = p.residual ? static_cast<const T*>(p.residual) + m * p.residual_row + n : nullptr;
+  T* out = static_cast<T*>(p.out) + m * p.out_row + n;
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < live) v[i] += to_f(static_cast<const T*>(p.bias)[n + i]);
   }
-  const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= p.a.rows || n >= p.b.rows) continue;
-      float v = acc[i][j] * f;
-      if (p.bias) v += to_f(static_cast<const T*>(p.bias)[n]);
-      if (p.residual) v += to_f(static_cast<const T*>(p.residual)[m * p.residual_row + n]);
-      static_cast<T*>(p.out)[m * p.out_row + n] = from_f<T>(v);
+  T o[4];
+  if (p.vec && live == 4) {
+    if (res) {
+      T r[4];
+      if (sizeof(T) == 4) *reinterpret_cast<uint4*>(r) = *reinterpret_cast<const uint4*>(res);
+      else *reinterpret_cast<uint2*>(r) = *reinterpret_cast<const uint2*>(res);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += to_f(r[i]);
     }
-}
-
-// Sums of the stored rows over 128 columns, a warp a tile.
-template <typename T>
-__global__ void __launch_bounds__(256) product_partials_kernel(const ProductArgs p) {
-  const int64_t tiles = (p.b.rows + 127) / 128, i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= p.a.rows * tiles) return;
-  const int64_t m = i / tiles, n0 = i % tiles * 128;
-  const int n = (int)min((int64_t)128, p.b.rows - n0), lane = threadIdx.x & 31;
-  const T* row = static_cast<const T*>(p.out) + m * p.out_row + n0;
-  float s = 0.f, q = 0.f;
-  for (int j = lane; j < n; j += 32) s += to_f(row[j]);
-  s = group_sum<32>(s);
-  for (int j = lane; j < n; j += 32) {
-    const float d = to_f(row[j]) - s / (float)n;
-    q = fmaf(d, d, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = from_f<T>(v[i]);
+    if (sizeof(T) == 4) *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(o);
+    else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = from_f<T>(0.f);
+      if (i < live) {
+        if (res) v[i] += to_f(res[i]);
+        o[i] = from_f<T>(v[i]);
+        out[i] = o[i];
+      }
+    }
   }
-  q = group_sum<32>(q);
-  if (lane == 0) p.psum[i] = s, p.psq[i] = q;
-}
-
-template <typename T>
-cudaError_t product_launch(const ProductArgs& p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.a.rows + 63) / 64), (unsigned)((p.b.rows + 63) / 64));
-  product_simple_kernel<T><<<grid, 256, 0, st>>>(p);
   if (p.psum) {
-    const int64_t tiles = p.a.rows * ((p.b.rows + 127) / 128);
-    product_partials_kernel<T><<<(unsigned)((tiles + 7) / 8), 256, 0, st>>>(p);
+    const int n_tile = (int)min((int64_t)128, p.b.rows - n0);
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += i < live ? to_f(o[i]) : 0.f;
+    s = group_sum<32>(s);
+    const float mean = s / (float)n_tile;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float d = i < live ? to_f(o[i]) - mean : 0.f;
+      q = fmaf(d, d, q);
+    }
+    q = group_sum<32>(q);
+    if (lane == 0) {
+      const int64_t at = m * ((p.b.rows + 127) / 128) + n0 / 128;
+      p.psum[at] = s;
+      p.psq[at] = q;
+    }
   }
-  return cudaGetLastError();
+}
+
+template <typename T, int FMT, bool SWAP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    product_tile_kernel(const __grid_constant__ CUtensorMap lane_codes,
+                        const __grid_constant__ CUtensorMap lane_scales,
+                        const __grid_constant__ CUtensorMap col_codes,
+                        const __grid_constant__ CUtensorMap col_scales, const ProductArgs p) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+  __shared__ uint32_t tmem_at;
+  constexpr int kTiles = chunk_tiles<FMT>();
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cols = SWAP ? p.cols : 128;
+  const uint32_t rank = p.splits > 1 ? cluster_rank() : 0u;
+  const int tile = blockIdx.x / p.splits;
+  const int lane_row = tile % p.lane_tiles * kTileLanes, col_row = tile / p.lane_tiles * cols;
+  const int c0 = (int)((int64_t)p.chunks * rank / p.splits);
+  const int c1 = (int)((int64_t)p.chunks * (rank + 1) / p.splits);
+  const uint32_t stage_size = stage_bytes<FMT>(cols);
+
+  if (warp == 2) tmem_alloc<kTmemCols>(&tmem_at);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
+    fence_mbar_init();
+    tma_prefetch(&lane_codes);
+    tma_prefetch(&lane_scales);
+    tma_prefetch(&col_codes);
+    tma_prefetch(&col_scales);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+
+  if (warp == 0 && lane == 0) {
+    bool ok = true;
+    int st = 0, round = 0, c = c0;
+    for (; c < c1; ++c) {
+      if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const uint32_t at = base + st * stage_size, bar = smem_addr(&full[st]);
+      mbar_arrive_expect_tx(&full[st], stage_size);
+      const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
+      tma_load_2d(at, &lane_codes, c * kChunkBytes, lane_row, bar);
+      tma_load_2d(at + kTileLanes * kChunkBytes, &col_codes, c * kChunkBytes, col_row, bar);
+      tma_load_3d(sc, &lane_scales, 0, c * kTiles, lane_row / 128, bar);
+      tma_load_3d(sc + kTiles * 512, &col_scales, 0, c * kTiles, col_row / 128, bar);
+      if (++st == p.stages) {
+        st = 0;
+        ++round;
+      }
+    }
+    if (!ok) {   // copies in flight land before the CTA ends
+      atomicOr(&g_tu_error, kErrWaitTimeout);
+      for (int i = max(c0, c - p.stages); i < c; ++i)
+        mbar_wait(&full[(i - c0) % p.stages], ((i - c0) / p.stages) & 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    bool ok = true;
+    int st = 0, round = 0;
+    for (int c = c0; c < c1 && ok; ++c) {
+      const int i = c - c0;
+      if (i >= kScaleBufs) {    // the scales' buffer is free
+        const int e = i - kScaleBufs;
+        ok = mbar_wait(&empty[e % p.stages], (e / p.stages) & 1);
+      }
+      ok = ok && mbar_wait(&full[st], round & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t at = base + st * stage_size;
+      const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
+      const uint32_t sa = tmem + kScaleCol + (i % kScaleBufs) * 32, sb = sa + 16;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        tc_copy_scales(sa + 4 * t, scales_desc(sc + 512 * t));
+        tc_copy_scales(sb + 4 * t, scales_desc(sc + (kTiles + t) * 512));
+      }
+      const uint64_t da = operand_desc(at), db = operand_desc(at + kTileLanes * kChunkBytes);
+      const int steps = min(4, p.steps - 4 * c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= steps) break;
+        // scales of the step: a tile of 4 a row serves 1, 2 or 4 steps
+        const uint32_t col = 4 * (k * kTiles / 4), id = FMT == MX_NVFP4 ? 0 : FMT == MX_MXFP4 ? (k & 1) * 2 : k;
+        tc_mma<FMT>(tmem, da + 2 * k, db + 2 * k, p.idesc | (id << 29) | (id << 4), sa + col, sb + col,
+                    i > 0 || k > 0);
+      }
+      tc_commit(smem_addr(&empty[st]));
+      if (++st == p.stages) {
+        st = 0;
+        ++round;
+      }
+    }
+    if (!ok) atomicOr(&g_tu_error, kErrWaitTimeout);
+    tc_commit(smem_addr(&done));
+  }
+  __syncwarp();
+  if (!mbar_wait(&done, 0)) atomicOr(&g_tu_error, kErrWaitTimeout);
+  __syncwarp();
+  tc_fence_after();
+  // The stages are read and become the place of the results: of all CTAs of the cluster.
+  if (p.splits > 1) cluster_sync();
+  else __syncthreads();
+
+  const int tile_rows = SWAP ? cols : kTileLanes;          // rows of results
+  const int rows_each = tile_rows / p.splits;              // that a CTA finishes
+  const uint32_t lane_base = (uint32_t)(warp & 3) * 32;    // the warp's lanes of tensor memory
+  const int half = warp >> 2;                              // of the columns
+  for (int j = half * 16; j < cols; j += 32) {
+    float v[16];
+    tmem_load16(tmem + (lane_base << 16) + j, v);
+    if (SWAP) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = j + i, to = r / rows_each;
+        const uint32_t at = base + (((rank * rows_each + r - to * rows_each) * kResultPitch) + lane_base + lane) * 4;
+        st_cluster(map_to_rank(at, to), v[i]);
+      }
+    } else {
+      const int r = lane_base + lane, to = r / rows_each;
+      const uint32_t at = map_to_rank(base + (((rank * rows_each + r - to * rows_each) * kResultPitch) + j) * 4, to);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) st_cluster4(at + 4 * i, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+    }
+  }
+  tc_fence_before();
+  if (p.splits > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_free<kTmemCols>(tmem);
+  }
+
+  const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
+  const int64_t m0 = (SWAP ? col_row : lane_row) + (int64_t)rank * rows_each, n0 = SWAP ? lane_row : col_row;
+  for (int r = warp; r < rows_each; r += kTileThreads / 32) {
+    if (m0 + r >= p.a.rows) break;
+    float4 s = lds_f4(base + (r * kResultPitch + lane * 4) * 4);
+    for (int q = 1; q < p.splits; ++q) {
+      const float4 t = lds_f4(base + ((q * rows_each + r) * kResultPitch + lane * 4) * 4);
+      s = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
+    }
+    finish_row<T>(p, m0 + r, n0, s, f);
+  }
 }
 
 }  // namespace nf
