@@ -62,6 +62,7 @@ cudaError_t scales_map(Encode encode, const QuantOut& q, int tiles, int row_tile
 }
 
 constexpr uint32_t kSmemTarget = 200 * 1024;
+constexpr uint32_t kPairSmem = 224 * 1024;
 
 template <typename T, int FMT, bool SWAP>
 cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
@@ -109,6 +110,41 @@ cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+template <typename T, int FMT, int WN>
+cudaError_t launch_pairs(ProductArgs p, int sms, cudaStream_t st) {
+  const void* fn = (const void*)product_pair_kernel<T, FMT, WN>;
+  p.tiles_m = (int)((p.a.rows + 255) / 256);
+  p.tiles_n = (int)((p.b.rows + WN - 1) / WN);
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  constexpr uint32_t kStage = pair_stage_step<FMT>(WN);
+  p.stages = (int)std::min<uint32_t>(kMaxStages, kPairSmem / kStage);
+  const size_t smem = (size_t)p.stages * kStage + 1024;
+  p.idesc = instr_desc(FMT, 256, WN);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  CUtensorMap maps[4];
+  Encode encode;
+  cudaError_t e = encoder(&encode);
+  if (e == cudaSuccess) e = codes_map(encode, p.a, 128, &maps[0]);
+  if (e == cudaSuccess) e = scales_map(encode, p.a, chunk_tiles<FMT>(), 1, &maps[1]);
+  if (e == cudaSuccess) e = codes_map(encode, p.b, WN / 2, &maps[2]);
+  if (e == cudaSuccess) e = scales_map(encode, p.b, chunk_tiles<FMT>(), WN / 128, &maps[3]);
+  if (e == cudaSuccess) e = (cudaError_t)allow_dyn_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(2 * tiles, sms / 2 * 2));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
 template <typename T, int FMT>
 cudaError_t launch_format(ProductArgs p, int sms, cudaStream_t st) {
   p.chunks = (int)((p.a.pitch + kChunkBytes - 1) / kChunkBytes);
@@ -116,6 +152,14 @@ cudaError_t launch_format(ProductArgs p, int sms, cudaStream_t st) {
   if (p.a.rows <= 64) {
     p.cols = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64;
     return launch_tiles<T, FMT, true>(p, sms, st);
+  }
+  // Pairs of CTAs from where single tiles are more than the SMs; tiles of 256
+  // columns where they take no more rounds than twice as many of half the width.
+  const int64_t tm = (p.a.rows + 255) / 256, tn = (p.b.rows + 127) / 128, pairs = sms / 2;
+  if (p.a.rows > 128 && pairs > 0 && tm * tn * 2 > sms) {
+    const int64_t narrow = (tm * tn + pairs - 1) / pairs, wide = (tm * ((tn + 1) / 2) + pairs - 1) / pairs;
+    if (wide * 8 <= narrow * 5) return launch_pairs<T, FMT, 256>(p, sms, st);
+    return launch_pairs<T, FMT, 128>(p, sms, st);
   }
   p.cols = 128;
   return launch_tiles<T, FMT, false>(p, sms, st);
@@ -180,6 +224,8 @@ ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const 
   p.psq = psq;
   const auto four = [&](const void* t, int64_t row) { return aligned(t, 4 * es) && (M == 1 || row % 4 == 0); };
   p.vec = four(out, out_row) && (residual == nullptr || four(residual, residual_row));
+  const auto wide = [&](const void* t, int64_t row) { return aligned(t, 16) && (M == 1 || row * es % 16 == 0); };
+  p.wide = wide(out, out_row) && (residual == nullptr || wide(residual, residual_row));
   e = by_dtype(dtype, [&](auto t) { return launch_product<decltype(t)>(p, sms, stream); });
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }

@@ -45,6 +45,8 @@ struct ProductArgs {
   int stages;
   int vec;               // out and residual can be accessed four at a time
   uint32_t idesc;
+  int tiles_m, tiles_n;  // pairs of CTAs: tiles of 256 rows of A, of 128 or 256 of B
+  int wide;              // out and residual can be accessed 16 bytes at a time
 };
 
 constexpr int kTileLanes = 128;
@@ -271,6 +273,251 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       s = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
     }
     finish_row<T>(p, m0 + r, n0, s, f);
+  }
+}
+
+// ---- pairs of CTAs ------------------------------------------------------------
+//
+// Tiles of 256 by WN results (WN = 128 or 256) by pairs of CTAs that stay and
+// take one tile after another. A step of the pair reads 128 rows of A and WN / 2
+// of B from each CTA's shared memory, so that a chunk costs half the copies a
+// result of two single tiles. Warps: 0 copies, 1 issues (in the first CTA of the
+// pair), 2 has the tensor memory, 4 to 11 finish results. WN = 256: the results
+// fill one half of tensor memory, the eight warps take 128 columns a thread into
+// registers and hand it back at once; WN = 128: two buffers, four warps each.
+constexpr int kPairThreads = 384;
+constexpr int kPairTmem = 512;
+
+template <int FMT> __host__ __device__ constexpr uint32_t pair_stage_bytes(int wn) {
+  return (uint32_t)(128 + wn / 2) * kChunkBytes + (uint32_t)(1 + wn / 128) * chunk_tiles<FMT>() * 512u;
+}
+
+// The same, up to where the next stage may begin.
+template <int FMT> __host__ __device__ constexpr uint32_t pair_stage_step(int wn) {
+  return (pair_stage_bytes<FMT>(wn) + 1023u) / 1024u * 1024u;
+}
+
+// Tile t in an order that keeps what runs at a time in few rows of A and B:
+// groups of 8 tiles of A's rows, all of B's columns in each.
+__device__ __forceinline__ void pair_tile(const ProductArgs& p, int t, int* tm, int* tn) {
+  const int per = 8 * p.tiles_n, g = t / per, rest = t - g * per;
+  const int rows = min(8, p.tiles_m - g * 8);
+  *tn = rest / rows;
+  *tm = g * 8 + rest - *tn * rows;
+}
+
+// 16 neighbouring results: the epilogue of a row's columns n .. n + 15.
+template <typename T>
+__device__ __forceinline__ void finish16(const ProductArgs& p, int64_t m, int64_t n, uint32_t* acc, float f) {
+  const int live = (int)max((int64_t)0, min((int64_t)16, p.b.rows - n));
+  float* v = reinterpret_cast<float*>(acc);
+  const T* bias = static_cast<const T*>(p.bias);
+  const T* res = p.residual ? static_cast<const T*>(p.residual) + m * p.residual_row + n : nullptr;
+  T* out = static_cast<T*>(p.out) + m * p.out_row + n;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= f;
+  if (live == 16) {
+    if (bias) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += to_f(bias[n + i]);
+    }
+    if (p.wide) {
+      constexpr int N = Vec<T>::N;
+      if (res) {
+#pragma unroll
+        for (int k = 0; k < 16 / N; ++k) {
+          float r[N];
+          unpack<T>(*reinterpret_cast<const uint4*>(res + k * N), r);
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[k * N + i] += r[i];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 16 / N; ++k) {
+        const uint4 o = pack<T>(v + k * N);
+        st_vec(out + k * N, o);
+        if (p.psum) unpack<T>(o, v + k * N);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (i < live) {
+      if (live != 16 && bias) v[i] += to_f(bias[n + i]);
+      if (res) v[i] += to_f(res[i]);
+      const T o = from_f<T>(v[i]);
+      out[i] = o;
+      v[i] = to_f(o);
+    } else {
+      v[i] = 0.f;
+    }
+  }
+}
+
+template <typename T, int FMT, int WN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    product_pair_kernel(const __grid_constant__ CUtensorMap a_codes,
+                        const __grid_constant__ CUtensorMap a_scales,
+                        const __grid_constant__ CUtensorMap b_codes,
+                        const __grid_constant__ CUtensorMap b_scales, const ProductArgs p) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], ready[2], drained[2];
+  __shared__ uint32_t tmem_at;
+  constexpr int kTiles = chunk_tiles<FMT>();
+  constexpr int kBufs = 256 / WN;                        // of results
+  constexpr int kRowTiles = WN / 128;                    // of B's scales
+  constexpr uint32_t kStage = pair_stage_step<FMT>(WN);
+  constexpr int kScaleStep = 16 + 16 * kRowTiles;        // columns of a buffer of scales
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = p.tiles_m * p.tiles_n;
+
+  if (warp == 2) tmem_alloc_pair<kPairTmem>(&tmem_at);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ready[i], 1);
+      mbar_init(&drained[i], 2 * (WN == 256 ? 8 : 4));   // warps of both CTAs
+    }
+    fence_mbar_init();
+    tma_prefetch(&a_codes);
+    tma_prefetch(&a_scales);
+    tma_prefetch(&b_codes);
+    tma_prefetch(&b_scales);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+
+  if (warp == 0 && lane == 0) {
+    bool ok = true;
+    int i = 0;                                           // chunks copied
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      int tm, tn;
+      pair_tile(p, t, &tm, &tn);
+      const int a_row = tm * 256 + (int)rank * 128, b_row = tn * WN;
+      for (int c = 0; c < p.chunks; ++c, ++i) {
+        const int st = i % p.stages;
+        if (i >= p.stages && !mbar_wait_cluster(&empty[st], (i / p.stages - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t at = base + st * kStage, sc = at + (128 + WN / 2) * kChunkBytes;
+        const uint32_t bar = map_to_rank(smem_addr(&full[st]), 0);
+        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * pair_stage_bytes<FMT>(WN));
+        tma_load_2d_pair(at, &a_codes, c * kChunkBytes, a_row, bar);
+        tma_load_2d_pair(at + 128 * kChunkBytes, &b_codes, c * kChunkBytes, b_row + (int)rank * (WN / 2), bar);
+        tma_load_3d_pair(sc, &a_scales, 0, c * kTiles, a_row / 128, bar);
+        tma_load_3d_pair(sc + kTiles * 512, &b_scales, 0, c * kTiles, b_row / 128, bar);
+      }
+    }
+    if (!ok) atomicOr(&g_tu_error, kErrWaitTimeout);
+    // What is in flight has landed when the first CTA's barriers say so, which
+    // its issuing thread waits for; after a wait that gave up, for a second more.
+    if (!ok && rank == 0)
+      for (int k = max(0, i - p.stages); k < i; ++k) mbar_wait_cluster(&full[k % p.stages], (k / p.stages) & 1);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    bool ok = true;
+    int i = 0, n = 0;                                    // chunks and tiles so far
+    for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+      const int buf = n % kBufs;
+      if (n >= kBufs) ok = mbar_wait_cluster(&drained[buf], (n / kBufs - 1) & 1);
+      tc_fence_after();
+      for (int c = 0; c < p.chunks && ok; ++c, ++i) {
+        const int st = i % p.stages;
+        if (i >= kScaleBufs) {
+          const int e = i - kScaleBufs;
+          ok = mbar_wait_cluster(&empty[e % p.stages], (e / p.stages) & 1);
+        }
+        ok = ok && mbar_wait_cluster(&full[st], (i / p.stages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = base + st * kStage, sc = at + (128 + WN / 2) * kChunkBytes;
+        const uint32_t sa = tmem + 256 + (i % kScaleBufs) * kScaleStep, sb = sa + 16;
+#pragma unroll
+        for (int k = 0; k < kTiles; ++k) {
+          tc_copy_scales_pair(sa + 4 * k, scales_desc(sc + 512 * k));
+#pragma unroll
+          for (int r = 0; r < kRowTiles; ++r)
+            tc_copy_scales_pair(sb + 4 * (k * kRowTiles + r), scales_desc(sc + (kTiles * (1 + r) + k) * 512));
+        }
+        const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * kChunkBytes);
+        const int steps = min(4, p.steps - 4 * c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= steps) break;
+          const uint32_t tile = k * kTiles / 4, id = FMT == MX_NVFP4 ? 0 : FMT == MX_MXFP4 ? (k & 1) * 2 : k;
+          tc_mma_pair<FMT>(tmem + buf * WN, da + 2 * k, db + 2 * k, p.idesc | (id << 29) | (id << 4),
+                           sa + 4 * tile, sb + 4 * tile * kRowTiles, c > 0 || k > 0);
+        }
+        tc_commit_pair(smem_addr(&empty[st]));
+      }
+      tc_commit_pair(smem_addr(&ready[buf]));
+    }
+    if (!ok) atomicOr(&g_tu_error, kErrWaitTimeout);
+    // all that was issued is done before tensor memory goes back
+    for (int e = max(0, i - p.stages); e < i; ++e) mbar_wait_cluster(&empty[e % p.stages], (e / p.stages) & 1);
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, group = (warp - 4) >> 2;
+    const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
+    int n = 0;
+    for (int t = pair; t < tiles; t += pairs, ++n) {
+      const int buf = n % kBufs;
+      if (WN == 128 && buf != group) continue;
+      int tm, tn;
+      pair_tile(p, t, &tm, &tn);
+      const bool ok = mbar_wait_cluster(&ready[buf], (n / kBufs) & 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
+        break;
+      }
+      tc_fence_after();
+      uint32_t v[128];
+      const int col = WN == 256 ? group * 128 : 0;
+      const uint32_t at = tmem + ((uint32_t)quarter << 21) + buf * WN + col;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_load32(at + 32 * j, v + 32 * j);
+      tmem_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&drained[buf]), 0));
+      const int64_t m = (int64_t)tm * 256 + rank * 128 + quarter * 32 + lane, n0 = (int64_t)tn * WN + col;
+      if (m < p.a.rows && n0 < p.b.rows) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) finish16<T>(p, m, n0 + 16 * j, v + 16 * j, f);
+        if (p.psum) {
+          const int width = (int)min((int64_t)128, p.b.rows - n0);
+          const float* o = reinterpret_cast<const float*>(v);
+          float s = 0.f, q = 0.f;
+#pragma unroll
+          for (int j = 0; j < 128; ++j) s += o[j];
+          const float mean = s / (float)width;
+#pragma unroll
+          for (int j = 0; j < 128; ++j) {
+            const float d = j < width ? o[j] - mean : 0.f;
+            q = fmaf(d, d, q);
+          }
+          const int64_t to = m * ((p.b.rows + 127) / 128) + n0 / 128;
+          p.psum[to] = s;
+          p.psq[to] = q;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_free_pair<kPairTmem>(tmem);
   }
 }
 

@@ -105,9 +105,8 @@ def tile(stored):
     """Scale bytes [rows, blocks] in tiles of 128 rows by 4 blocks."""
     rows, n = stored.shape
     out = np.zeros((-(-rows // 128), -(-n // 4), 32, 4, 4), np.uint8)
-    for r in range(rows):
-        for b in range(n):
-            out[r // 128, b // 4, r % 32, r % 128 // 32, b % 4] = stored[r, b]
+    r, b = np.arange(rows)[:, None], np.arange(n)[None, :]
+    out[r // 128, b // 4, r % 32, r % 128 // 32, b % 4] = stored
     return out
 
 

@@ -38,6 +38,13 @@ def test_whole_numbers_are_exact(cuda_lib, M, N, K, fmt):
     assert out.intact()
 
 
+# More results than single tiles on all SMs hold: pairs of CTAs, both widths.
+@pytest.mark.parametrize("fmt", TILED)
+@pytest.mark.parametrize("M,N,K", [(2600, 2000, 96), (4100, 4100, 160), (9001, 515, 1000), (3900, 2048, 2100), (140, 20001, 320)])
+def test_whole_numbers_are_exact_in_pairs(cuda_lib, M, N, K, fmt):
+    test_whole_numbers_are_exact(cuda_lib, M, N, K, fmt)
+
+
 def bound(want, size, K, dtype):
     """A partial sum is rounded (or cut) once for 16 terms at most often, to 24
     bits, in an order of the hardware's; then the factor, the bias, the residual
@@ -47,7 +54,7 @@ def bound(want, size, K, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("fmt", TILED)
-@pytest.mark.parametrize("M,N,K", [(1, 200, 1000), (16, 1024, 4096), (77, 300, 640), (300, 257, 1165), (512, 384, 8192)])
+@pytest.mark.parametrize("M,N,K", [(1, 200, 1000), (16, 1024, 4096), (77, 300, 640), (300, 257, 1165), (512, 384, 8192), (2100, 2300, 800), (5000, 4000, 500)])
 def test_values(cuda_lib, M, N, K, fmt, dtype):
     nf = cuda_lib
     rng = np.random.default_rng(K)
