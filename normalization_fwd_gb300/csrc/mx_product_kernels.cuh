@@ -162,72 +162,82 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_at;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     bool ok = true;
     int st = 0, round = 0, c = c0;
     for (; c < c1; ++c) {
-      if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1)) {
+      if (round > 0 && !mbar_wait_cluster(&empty[st], (round - 1) & 1)) {
         ok = false;
         break;
       }
       const uint32_t at = base + st * stage_size, bar = smem_addr(&full[st]);
-      mbar_arrive_expect_tx(&full[st], stage_size);
       const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
-      tma_load_2d(at, &lane_codes, c * kChunkBytes, lane_row, bar);
-      tma_load_2d(at + kTileLanes * kChunkBytes, &col_codes, c * kChunkBytes, col_row, bar);
-      tma_load_3d(sc, &lane_scales, 0, c * kTiles, lane_row / 128, bar);
-      tma_load_3d(sc + kTiles * 512, &col_scales, 0, c * kTiles, col_row / 128, bar);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[st], stage_size);
+        tma_load_2d(at, &lane_codes, c * kChunkBytes, lane_row, bar);
+        tma_load_2d(at + kTileLanes * kChunkBytes, &col_codes, c * kChunkBytes, col_row, bar);
+        tma_load_3d(sc, &lane_scales, 0, c * kTiles, lane_row / 128, bar);
+        tma_load_3d(sc + kTiles * 512, &col_scales, 0, c * kTiles, col_row / 128, bar);
+      }
+      __syncwarp();
       if (++st == p.stages) {
         st = 0;
         ++round;
       }
     }
     if (!ok) {   // copies in flight land before the CTA ends
-      atomicOr(&g_tu_error, kErrWaitTimeout);
+      if (lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
       for (int i = max(c0, c - p.stages); i < c; ++i)
-        mbar_wait(&full[(i - c0) % p.stages], ((i - c0) / p.stages) & 1);
+        mbar_wait_cluster(&full[(i - c0) % p.stages], ((i - c0) / p.stages) & 1);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     bool ok = true;
-    int st = 0, round = 0;
-    for (int c = c0; c < c1 && ok; ++c) {
+    int st = 0, round = 0, est = 0, eround = 0;
+    for (int c = c0; c < c1; ++c) {
       const int i = c - c0;
       if (i >= kScaleBufs) {    // the scales' buffer is free
-        const int e = i - kScaleBufs;
-        ok = mbar_wait(&empty[e % p.stages], (e / p.stages) & 1);
+        ok = mbar_wait_cluster(&empty[est], eround & 1);
+        if (++est == p.stages) {
+          est = 0;
+          ++eround;
+        }
       }
-      ok = ok && mbar_wait(&full[st], round & 1);
+      ok = ok && mbar_wait_cluster(&full[st], round & 1);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t at = base + st * stage_size;
       const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
       const uint32_t sa = tmem + kScaleCol + (i % kScaleBufs) * 32, sb = sa + 16;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        tc_copy_scales(sa + 4 * t, scales_desc(sc + 512 * t));
-        tc_copy_scales(sb + 4 * t, scales_desc(sc + (kTiles + t) * 512));
-      }
-      const uint64_t da = operand_desc(at), db = operand_desc(at + kTileLanes * kChunkBytes);
+      const uint64_t da = operand_desc(at), db = operand_desc(at + kTileLanes * kChunkBytes), ds = scales_desc(sc);
       const int steps = min(4, p.steps - 4 * c);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k >= steps) break;
-        // scales of the step: a tile of 4 a row serves 1, 2 or 4 steps
-        const uint32_t col = 4 * (k * kTiles / 4), id = FMT == MX_NVFP4 ? 0 : FMT == MX_MXFP4 ? (k & 1) * 2 : k;
-        tc_mma<FMT>(tmem, da + 2 * k, db + 2 * k, p.idesc | (id << 29) | (id << 4), sa + col, sb + col,
-                    i > 0 || k > 0);
+        for (int t = 0; t < kTiles; ++t) {
+          tc_copy_scales(sa + 4 * t, ds + 32 * t);
+          tc_copy_scales(sb + 4 * t, ds + 32 * (kTiles + t));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // scales of the step: a tile of 4 a row serves 1, 2 or 4 steps
+          const uint32_t col = 4 * (k * kTiles / 4), id = FMT == MX_NVFP4 ? 0 : FMT == MX_MXFP4 ? (k & 1) * 2 : k;
+          if (k < steps)
+            tc_mma<FMT>(tmem, da + 2 * k, db + 2 * k, p.idesc | (id << 29) | (id << 4), sa + col, sb + col,
+                        i > 0 || k > 0);
+        }
+        tc_commit(smem_addr(&empty[st]));
       }
-      tc_commit(smem_addr(&empty[st]));
+      __syncwarp();
       if (++st == p.stages) {
         st = 0;
         ++round;
       }
     }
-    if (!ok) atomicOr(&g_tu_error, kErrWaitTimeout);
-    tc_commit(smem_addr(&done));
+    if (!ok && lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
+    if (elect_one()) tc_commit(smem_addr(&done));
   }
   __syncwarp();
-  if (!mbar_wait(&done, 0)) atomicOr(&g_tu_error, kErrWaitTimeout);
+  if (!mbar_wait_cluster(&done, 0)) atomicOr(&g_tu_error, kErrWaitTimeout);
   __syncwarp();
   tc_fence_after();
   // The stages are read and become the place of the results: of all CTAs of the cluster.
@@ -396,72 +406,90 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_at;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     bool ok = true;
-    int i = 0;                                           // chunks copied
+    int i = 0, st = 0, round = 0;                        // chunks copied, stage and its use
     for (int t = pair; t < tiles && ok; t += pairs) {
       int tm, tn;
       pair_tile(p, t, &tm, &tn);
       const int a_row = tm * 256 + (int)rank * 128, b_row = tn * WN;
       for (int c = 0; c < p.chunks; ++c, ++i) {
-        const int st = i % p.stages;
-        if (i >= p.stages && !mbar_wait_cluster(&empty[st], (i / p.stages - 1) & 1)) {
+        if (round > 0 && !mbar_wait_cluster(&empty[st], (round - 1) & 1)) {
           ok = false;
           break;
         }
         const uint32_t at = base + st * kStage, sc = at + (128 + WN / 2) * kChunkBytes;
         const uint32_t bar = map_to_rank(smem_addr(&full[st]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * pair_stage_bytes<FMT>(WN));
-        tma_load_2d_pair(at, &a_codes, c * kChunkBytes, a_row, bar);
-        tma_load_2d_pair(at + 128 * kChunkBytes, &b_codes, c * kChunkBytes, b_row + (int)rank * (WN / 2), bar);
-        tma_load_3d_pair(sc, &a_scales, 0, c * kTiles, a_row / 128, bar);
-        tma_load_3d_pair(sc + kTiles * 512, &b_scales, 0, c * kTiles, b_row / 128, bar);
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * pair_stage_bytes<FMT>(WN));
+          tma_load_2d_pair(at, &a_codes, c * kChunkBytes, a_row, bar);
+          tma_load_2d_pair(at + 128 * kChunkBytes, &b_codes, c * kChunkBytes, b_row + (int)rank * (WN / 2), bar);
+          tma_load_3d_pair(sc, &a_scales, 0, c * kTiles, a_row / 128, bar);
+          tma_load_3d_pair(sc + kTiles * 512, &b_scales, 0, c * kTiles, b_row / 128, bar);
+        }
+        __syncwarp();
+        if (++st == p.stages) {
+          st = 0;
+          ++round;
+        }
       }
     }
-    if (!ok) atomicOr(&g_tu_error, kErrWaitTimeout);
+    if (!ok && lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
     // What is in flight has landed when the first CTA's barriers say so, which
-    // its issuing thread waits for; after a wait that gave up, for a second more.
+    // its issuing warp waits for; after a wait that gave up, for a second more.
     if (!ok && rank == 0)
       for (int k = max(0, i - p.stages); k < i; ++k) mbar_wait_cluster(&full[k % p.stages], (k / p.stages) & 1);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     bool ok = true;
     int i = 0, n = 0;                                    // chunks and tiles so far
+    int st = 0, round = 0, est = 0, eround = 0;
     for (int t = pair; t < tiles && ok; t += pairs, ++n) {
       const int buf = n % kBufs;
-      if (n >= kBufs) ok = mbar_wait_cluster(&drained[buf], (n / kBufs - 1) & 1);
+      if (n >= kBufs) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&drained[buf], (n / kBufs - 1) & 1));
       tc_fence_after();
       for (int c = 0; c < p.chunks && ok; ++c, ++i) {
-        const int st = i % p.stages;
         if (i >= kScaleBufs) {
-          const int e = i - kScaleBufs;
-          ok = mbar_wait_cluster(&empty[e % p.stages], (e / p.stages) & 1);
+          ok = mbar_wait_cluster(&empty[est], eround & 1);
+          if (++est == p.stages) {
+            est = 0;
+            ++eround;
+          }
         }
-        ok = ok && mbar_wait_cluster(&full[st], (i / p.stages) & 1);
+        ok = ok && mbar_wait_cluster(&full[st], round & 1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t at = base + st * kStage, sc = at + (128 + WN / 2) * kChunkBytes;
         const uint32_t sa = tmem + 256 + (i % kScaleBufs) * kScaleStep, sb = sa + 16;
-#pragma unroll
-        for (int k = 0; k < kTiles; ++k) {
-          tc_copy_scales_pair(sa + 4 * k, scales_desc(sc + 512 * k));
-#pragma unroll
-          for (int r = 0; r < kRowTiles; ++r)
-            tc_copy_scales_pair(sb + 4 * (k * kRowTiles + r), scales_desc(sc + (kTiles * (1 + r) + k) * 512));
-        }
-        const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * kChunkBytes);
+        const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * kChunkBytes), ds = scales_desc(sc);
         const int steps = min(4, p.steps - 4 * c);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k >= steps) break;
-          const uint32_t tile = k * kTiles / 4, id = FMT == MX_NVFP4 ? 0 : FMT == MX_MXFP4 ? (k & 1) * 2 : k;
-          tc_mma_pair<FMT>(tmem + buf * WN, da + 2 * k, db + 2 * k, p.idesc | (id << 29) | (id << 4),
-                           sa + 4 * tile, sb + 4 * tile * kRowTiles, c > 0 || k > 0);
+          for (int k = 0; k < kTiles; ++k) {
+            tc_copy_scales_pair(sa + 4 * k, ds + 32 * k);
+#pragma unroll
+            for (int r = 0; r < kRowTiles; ++r)
+              tc_copy_scales_pair(sb + 4 * (k * kRowTiles + r), ds + 32 * (kTiles * (1 + r) + k));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t tile = k * kTiles / 4, id = FMT == MX_NVFP4 ? 0 : FMT == MX_MXFP4 ? (k & 1) * 2 : k;
+            if (k < steps)
+              tc_mma_pair<FMT>(tmem + buf * WN, da + 2 * k, db + 2 * k, p.idesc | (id << 29) | (id << 4),
+                               sa + 4 * tile, sb + 4 * tile * kRowTiles, c > 0 || k > 0);
+          }
+          tc_commit_pair(smem_addr(&empty[st]));
         }
-        tc_commit_pair(smem_addr(&empty[st]));
+        __syncwarp();
+        if (++st == p.stages) {
+          st = 0;
+          ++round;
+        }
       }
-      tc_commit_pair(smem_addr(&ready[buf]));
+      if (elect_one()) tc_commit_pair(smem_addr(&ready[buf]));
+      __syncwarp();
     }
-    if (!ok) atomicOr(&g_tu_error, kErrWaitTimeout);
+    if (!ok && lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
     // all that was issued is done before tensor memory goes back
     for (int e = max(0, i - p.stages); e < i; ++e) mbar_wait_cluster(&empty[e % p.stages], (e / p.stages) & 1);
   } else if (warp >= 4) {

@@ -9,6 +9,18 @@
 
 namespace nf {
 
+// One lane of a converged warp, the same one each time. The assembler knows that
+// one lane passes, and issues the tensor-core instructions behind it once; behind
+// `lane == 0` it made each a loop over the warp's lanes (70 cycles each, 4096 x
+// 4096 x 8192 nvfp4 147 us).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---- tensor-map copies ------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -207,23 +219,32 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
       : "memory");
 }
 // Arrival on a barrier of any CTA of the cluster, and a wait that sees what
-// came before arrivals of other CTAs.
+// came before arrivals of other CTAs. The waits of one thread follow each other
+// every few hundred cycles here, so their limit is counted in cycles (about a
+// second): reading the global timer in each held up the ring by a microsecond
+// a chunk (4096 x 4096 x 8192: 147 us with it).
+constexpr long long kWaitLimitCycles = 2000000000ll;
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = global_ns();
-  uint32_t done;
-  do {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
-        : "memory");
-  } while (!done && global_ns() - t0 <= kWaitLimitNs);
-  return done != 0;
+  const uint32_t at = smem_addr(bar);
+  if (mbar_test_cluster(at, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_test_cluster(at, parity))
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  return true;
 }
 
 // ---- clusters -------------------------------------------------------------------
