@@ -43,10 +43,9 @@ struct ProductArgs {
   int chunks;            // of K
   int steps;             // instructions along all of K
   int stages;
-  int vec;               // out and residual can be accessed four at a time
+  int vec;               // out and residual can be accessed 16 bytes at a time
   uint32_t idesc;
   int tiles_m, tiles_n;  // pairs of CTAs: tiles of 256 rows of A, of 128 or 256 of B
-  int wide;              // out and residual can be accessed 16 bytes at a time
 };
 
 constexpr int kTileLanes = 128;
@@ -316,52 +315,108 @@ __device__ __forceinline__ void pair_tile(const ProductArgs& p, int t, int* tm, 
   *tm = g * 8 + rest - *tn * rows;
 }
 
-// 16 neighbouring results: the epilogue of a row's columns n .. n + 15.
+// A warp's 32 rows by 128 columns of results, a row a lane in `v`. A lane scales,
+// rounds and sums its own row; 64 bytes of each row at a time change places
+// through shared memory, so that rows of the residual and the output are read
+// and written in runs of 64 bytes (straight from a row a lane, 4099 x 1165 x 1280,
+// whose 16-bit rows start anywhere, took 78 us).
+constexpr int kPiecePitch = 80;      // bytes: 16-byte accesses of 8 rows meet no bank twice
+constexpr int kPieceBytes = 32 * kPiecePitch;
+
+// Row r, 16-byte part c of a piece whose first column is n: `live` of its
+// values are there.
 template <typename T>
-__device__ __forceinline__ void finish16(const ProductArgs& p, int64_t m, int64_t n, uint32_t* acc, float f) {
-  const int live = (int)max((int64_t)0, min((int64_t)16, p.b.rows - n));
-  float* v = reinterpret_cast<float*>(acc);
-  const T* bias = static_cast<const T*>(p.bias);
-  const T* res = p.residual ? static_cast<const T*>(p.residual) + m * p.residual_row + n : nullptr;
-  T* out = static_cast<T*>(p.out) + m * p.out_row + n;
+__device__ __forceinline__ uint4 piece_load(const T* row, int live, bool vec) {
+  constexpr int N = Vec<T>::N;
+  if (vec && live == N) return *reinterpret_cast<const uint4*>(row);
+  T t[N];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] *= f;
-  if (live == 16) {
-    if (bias) {
+  for (int i = 0; i < N; ++i) t[i] = i < live ? row[i] : from_f<T>(0.f);
+  return *reinterpret_cast<const uint4*>(t);
+}
+
+template <typename T, bool RES, bool SUMS>
+__device__ __forceinline__ void finish_pieces(const ProductArgs& p, int64_t m0, int64_t n0, uint32_t* v,
+                                              float f, uint32_t piece) {
+  constexpr int N = Vec<T>::N, kCols = 4 * N, kPieces = 128 / kCols;
+  const int lane = threadIdx.x & 31, part = lane & 3;
+  const int rows = (int)min((int64_t)32, p.a.rows - m0), width = (int)min((int64_t)128, p.b.rows - n0);
+  const uint32_t own = piece + lane * kPiecePitch, other = piece + (lane >> 2) * kPiecePitch + part * 16;
+  const T* res = static_cast<const T*>(p.residual) + m0 * p.residual_row + n0;
+  T* out = static_cast<T*>(p.out) + m0 * p.out_row + n0;
+  const T* bias = p.bias ? static_cast<const T*>(p.bias) + n0 : nullptr;
+  float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] += to_f(bias[n + i]);
+  for (int j = 0; j < kPieces; ++j) {
+    const int col = j * kCols;
+    if (col >= width) break;
+    if (RES) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        uint4 t = make_uint4(0, 0, 0, 0);
+        if (r < rows) t = piece_load(res + r * p.residual_row + col + part * N, width - col - part * N, p.vec);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(other + 8 * i * kPiecePitch), "r"(t.x), "r"(t.y), "r"(t.z), "r"(t.w) : "memory");
+      }
+      __syncwarp();
     }
-    if (p.wide) {
-      constexpr int N = Vec<T>::N;
-      if (res) {
 #pragma unroll
-        for (int k = 0; k < 16 / N; ++k) {
-          float r[N];
-          unpack<T>(*reinterpret_cast<const uint4*>(res + k * N), r);
+    for (int c = 0; c < 4; ++c) {
+      float o[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) v[k * N + i] += r[i];
+      for (int i = 0; i < N; ++i) o[i] = __uint_as_float(v[col + c * N + i]) * f;
+      if (bias) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (col + c * N + i < width) o[i] += to_f(bias[col + c * N + i]);
+      }
+      if (RES) {
+        float r[N];
+        unpack<T>(lds_u4(own + c * 16), r);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] += r[i];
+      }
+      const uint4 t = pack<T>(o);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(own + c * 16), "r"(t.x), "r"(t.y), "r"(t.z), "r"(t.w) : "memory");
+      if (SUMS) {
+        unpack<T>(t, o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (col + c * N + i < width) sum += o[i];
+          v[col + c * N + i] = __float_as_uint(o[i]);
         }
       }
+    }
+    __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 16 / N; ++k) {
-        const uint4 o = pack<T>(v + k * N);
-        st_vec(out + k * N, o);
-        if (p.psum) unpack<T>(o, v + k * N);
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), live = width - col - part * N;
+      const uint4 t = lds_u4(other + 8 * i * kPiecePitch);
+      if (r < rows) {
+        T* to = out + r * p.out_row + col + part * N;
+        if (p.vec && live >= N) {
+          st_vec(to, t);
+        } else {
+          const T* e = reinterpret_cast<const T*>(&t);
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            if (k < live) to[k] = e[k];
+        }
       }
-      return;
     }
+    __syncwarp();
   }
+  if (SUMS && lane < rows) {
+    const float mean = sum / (float)width;
+    float q = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (i < live) {
-      if (live != 16 && bias) v[i] += to_f(bias[n + i]);
-      if (res) v[i] += to_f(res[i]);
-      const T o = from_f<T>(v[i]);
-      out[i] = o;
-      v[i] = to_f(o);
-    } else {
-      v[i] = 0.f;
+    for (int j = 0; j < 128; ++j) {
+      const float d = j < width ? __uint_as_float(v[j]) - mean : 0.f;
+      q = fmaf(d, d, q);
     }
+    const int64_t at = (m0 + lane) * ((p.b.rows + 127) / 128) + n0 / 128;
+    p.psum[at] = sum;
+    p.psq[at] = q;
   }
 }
 
@@ -495,6 +550,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3, group = (warp - 4) >> 2;
     const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
+    const uint32_t piece = base + p.stages * kStage + (warp - 4) * kPieceBytes;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const int buf = n % kBufs;
@@ -516,25 +572,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&drained[buf]), 0));
-      const int64_t m = (int64_t)tm * 256 + rank * 128 + quarter * 32 + lane, n0 = (int64_t)tn * WN + col;
-      if (m < p.a.rows && n0 < p.b.rows) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) finish16<T>(p, m, n0 + 16 * j, v + 16 * j, f);
+      const int64_t m0 = (int64_t)tm * 256 + rank * 128 + quarter * 32, n0 = (int64_t)tn * WN + col;
+      if (m0 < p.a.rows && n0 < p.b.rows) {
         if (p.psum) {
-          const int width = (int)min((int64_t)128, p.b.rows - n0);
-          const float* o = reinterpret_cast<const float*>(v);
-          float s = 0.f, q = 0.f;
-#pragma unroll
-          for (int j = 0; j < 128; ++j) s += o[j];
-          const float mean = s / (float)width;
-#pragma unroll
-          for (int j = 0; j < 128; ++j) {
-            const float d = j < width ? o[j] - mean : 0.f;
-            q = fmaf(d, d, q);
-          }
-          const int64_t to = m * ((p.b.rows + 127) / 128) + n0 / 128;
-          p.psum[to] = s;
-          p.psq[to] = q;
+          if (p.residual) finish_pieces<T, true, true>(p, m0, n0, v, f, piece);
+          else finish_pieces<T, false, true>(p, m0, n0, v, f, piece);
+        } else {
+          if (p.residual) finish_pieces<T, true, false>(p, m0, n0, v, f, piece);
+          else finish_pieces<T, false, false>(p, m0, n0, v, f, piece);
         }
       }
     }
