@@ -75,6 +75,7 @@ cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
   while (p.splits < 8 && tiles * p.splits * 2 <= sms && p.chunks >= p.splits * 4) p.splits *= 2;
   const uint32_t stage = stage_bytes<FMT>(p.cols);
   p.stages = (int)std::min<uint32_t>(kMaxStages, kSmemTarget / stage);
+  static_assert(kScaleCol + kMaxStages * 8 * chunk_tiles<FMT>() <= kTmemCols, "scales' buffers");
   const size_t smem = std::max<size_t>((size_t)p.stages * stage, (SWAP ? p.cols : kTileLanes) * kResultPitch * 4) + 1024;
   p.idesc = instr_desc(FMT, kTileLanes, p.cols);
   if (tiles * p.splits > INT32_MAX) return cudaErrorInvalidValue;
@@ -118,6 +119,8 @@ cudaError_t launch_pairs(ProductArgs p, int sms, cudaStream_t st) {
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   constexpr uint32_t kStage = pair_stage_step<FMT>(WN);
   p.stages = (int)std::min<uint32_t>(kMaxStages, (kPairSmem - 8 * kPieceBytes) / kStage);
+  static_assert(256 + std::min<uint32_t>(kMaxStages, (kPairSmem - 8 * kPieceBytes) / kStage) * 4 *
+                          chunk_tiles<FMT>() * (1 + WN / 128) <= kTmemCols, "scales' buffers");
   const size_t smem = (size_t)p.stages * kStage + 8 * kPieceBytes + 1024;
   p.idesc = instr_desc(FMT, 256, WN);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;

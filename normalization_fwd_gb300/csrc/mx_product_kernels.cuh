@@ -11,8 +11,10 @@
 // the codes in the swizzle that the matrix instructions read, the scales as
 // they lie, which is how tensor memory wants them), another one moves the scales
 // on to tensor memory and issues four instructions of 32 bytes of K. Scales
-// have four buffers there, and a buffer is only written again when the
-// instructions that read it are known to be done.
+// have a buffer there for each stage: a stage that is full again says that the
+// instructions on what it held before are done, and so are those that read that
+// buffer. The issuing warp is what bounds a chunk (512 cycles of instructions
+// against some 400 to issue them), so it asks for the next stage before it issues.
 //
 // Few tiles: K is split over the CTAs of a cluster. Each gets the tile's rows
 // of results that it is to finish from all others through distributed shared
@@ -51,8 +53,7 @@ struct ProductArgs {
 constexpr int kTileLanes = 128;
 constexpr int kTileThreads = 256;
 constexpr int kChunkBytes = 128;
-constexpr int kScaleBufs = 4;
-constexpr int kTmemCols = 256;      // 128 of results, 4 buffers of 32 for scales
+constexpr int kTmemCols = 512;      // 128 or 256 of results, then scales
 constexpr int kScaleCol = 128;
 constexpr int kResultPitch = 132;   // floats of a row of results in shared memory
 constexpr int kMaxStages = 10;
@@ -190,24 +191,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_wait_cluster(&full[(i - c0) % p.stages], ((i - c0) / p.stages) & 1);
     }
   } else if (warp == 1) {
-    bool ok = true;
-    int st = 0, round = 0, est = 0, eround = 0;
+    bool ok = true, here = mbar_test_cluster(smem_addr(&full[0]), 0);
+    int st = 0, round = 0;
     for (int c = c0; c < c1; ++c) {
       const int i = c - c0;
-      if (i >= kScaleBufs) {    // the scales' buffer is free
-        ok = mbar_wait_cluster(&empty[est], eround & 1);
-        if (++est == p.stages) {
-          est = 0;
-          ++eround;
-        }
-      }
-      ok = ok && mbar_wait_cluster(&full[st], round & 1);
+      ok = here || mbar_wait_cluster(&full[st], round & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      const int next = st + 1 == p.stages ? 0 : st + 1;
+      here = c + 1 < c1 && mbar_test_cluster(smem_addr(&full[next]), (next == 0 ? round + 1 : round) & 1);
       const uint32_t at = base + st * stage_size;
       const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
-      const uint32_t sa = tmem + kScaleCol + (i % kScaleBufs) * 32, sb = sa + 16;
+      const uint32_t sa = tmem + kScaleCol + st * 8 * kTiles, sb = sa + 4 * kTiles;
       const uint64_t da = operand_desc(at), db = operand_desc(at + kTileLanes * kChunkBytes), ds = scales_desc(sc);
       const int steps = min(4, p.steps - 4 * c);
       if (elect_one()) {
@@ -227,10 +223,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_commit(smem_addr(&empty[st]));
       }
       __syncwarp();
-      if (++st == p.stages) {
-        st = 0;
-        ++round;
-      }
+      st = next;
+      if (next == 0) ++round;
     }
     if (!ok && lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
     if (elect_one()) tc_commit(smem_addr(&done));
@@ -295,7 +289,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // fill one half of tensor memory, the eight warps take 128 columns a thread into
 // registers and hand it back at once; WN = 128: two buffers, four warps each.
 constexpr int kPairThreads = 384;
-constexpr int kPairTmem = 512;
 
 template <int FMT> __host__ __device__ constexpr uint32_t pair_stage_bytes(int wn) {
   return (uint32_t)(128 + wn / 2) * kChunkBytes + (uint32_t)(1 + wn / 128) * chunk_tiles<FMT>() * 512u;
@@ -433,13 +426,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   constexpr int kBufs = 256 / WN;                        // of results
   constexpr int kRowTiles = WN / 128;                    // of B's scales
   constexpr uint32_t kStage = pair_stage_step<FMT>(WN);
-  constexpr int kScaleStep = 16 + 16 * kRowTiles;        // columns of a buffer of scales
+  constexpr int kScaleStep = 4 * kTiles * (1 + kRowTiles);   // columns of a stage's scales
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = p.tiles_m * p.tiles_n;
 
-  if (warp == 2) tmem_alloc_pair<kPairTmem>(&tmem_at);
+  if (warp == 2) tmem_alloc_pair<kTmemCols>(&tmem_at);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 1);
@@ -497,25 +490,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1 && rank == 0) {
     bool ok = true;
     int i = 0, n = 0;                                    // chunks and tiles so far
-    int st = 0, round = 0, est = 0, eround = 0;
+    int st = 0, round = 0;
+    bool here = mbar_test_cluster(smem_addr(&full[0]), 0);
     for (int t = pair; t < tiles && ok; t += pairs, ++n) {
       const int buf = n % kBufs;
       if (n >= kBufs) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&drained[buf], (n / kBufs - 1) & 1));
       tc_fence_after();
       for (int c = 0; c < p.chunks && ok; ++c, ++i) {
-        if (i >= kScaleBufs) {
-          ok = mbar_wait_cluster(&empty[est], eround & 1);
-          if (++est == p.stages) {
-            est = 0;
-            ++eround;
-          }
-        }
-        ok = ok && mbar_wait_cluster(&full[st], round & 1);
+        ok = here || mbar_wait_cluster(&full[st], round & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        const int next = st + 1 == p.stages ? 0 : st + 1;
+        here = mbar_test_cluster(smem_addr(&full[next]), (next == 0 ? round + 1 : round) & 1);
         const uint32_t at = base + st * kStage, sc = at + (128 + WN / 2) * kChunkBytes;
-        const uint32_t sa = tmem + 256 + (i % kScaleBufs) * kScaleStep, sb = sa + 16;
+        const uint32_t sa = tmem + 256 + st * kScaleStep, sb = sa + 4 * kTiles;
         const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * kChunkBytes), ds = scales_desc(sc);
         const int steps = min(4, p.steps - 4 * c);
         if (elect_one()) {
@@ -536,10 +525,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           tc_commit_pair(smem_addr(&empty[st]));
         }
         __syncwarp();
-        if (++st == p.stages) {
-          st = 0;
-          ++round;
-        }
+        st = next;
+        if (next == 0) ++round;
       }
       if (elect_one()) tc_commit_pair(smem_addr(&ready[buf]));
       __syncwarp();
@@ -590,7 +577,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   if (warp == 2) {
     tc_fence_after();
-    tmem_free_pair<kPairTmem>(tmem);
+    tmem_free_pair<kTmemCols>(tmem);
   }
 }
 
