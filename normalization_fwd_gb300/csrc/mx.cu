@@ -62,28 +62,34 @@ NormPlan norm_plan(int slots, int least_lanes) {
 
 int64_t padded_rows(const QuantOut& q) { return mx_tiled(q.fmt) ? (q.rows + 127) / 128 * 128 : q.rows; }
 
-template <typename T>
+// Lanes a row of `cols` columns takes at 8 a lane (`least` at least), and the grid
+// of CTAs that deal rows to them: about 16 CTAs an SM, so that each lane's rows
+// are enough to keep one on its way.
+int row_lanes(int64_t cols, int least) {
+  int lanes = least;
+  while (lanes < 32 && lanes * 8 < cols) lanes *= 2;
+  return lanes;
+}
+dim3 row_grid(int64_t rows, int64_t cols, int lanes, int sms) {
+  const int64_t x = (cols + 255) / 256, per = (int64_t)(kQuantThreads / 32) * (32 / lanes);
+  const int64_t most = std::max<int64_t>(1, (int64_t)sms * 16 / x);
+  return dim3((unsigned)x, (unsigned)std::min<int64_t>(std::min<int64_t>((rows + per - 1) / per, most), 65535));
+}
+
+template <typename T, int FMT>
 cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStream_t st) {
   const QuantOut& q = a.q;
-  const int cls = class_of(q.fmt);
   if (transpose) {
-    const int64_t rows = std::max(a.padded_rows, q.rows);
-    const int64_t x = (rows + kTrRows - 1) / kTrRows, tiles = (q.cols + kTrCols - 1) / kTrCols;
-    const dim3 grid((unsigned)x, cls == 0 ? 1u : (unsigned)std::min<int64_t>(tiles, 65535));
-    if (cls == 0) quant_transpose_kernel<T, 0><<<grid, kQuantThreads, 0, st>>>(a);
-    else if (cls == 1) quant_transpose_kernel<T, 1><<<grid, kQuantThreads, 0, st>>>(a);
-    else quant_transpose_kernel<T, 2><<<grid, kQuantThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  if (cls == 0) {
+    const int64_t x = (a.padded_rows + TrRows<T>::N - 1) / TrRows<T>::N, tiles = (q.cols + kTrCols - 1) / kTrCols;
+    const dim3 grid((unsigned)x, FMT == MX_FP8_ROW ? 1u : (unsigned)std::min<int64_t>(tiles, 65535));
+    quant_transpose_kernel<T, FMT><<<grid, kQuantThreads, 0, st>>>(a);
+  } else if constexpr (FMT == MX_FP8_ROW) {
     quant_row_kernel<T><<<(unsigned)std::min<int64_t>(q.rows, 1 << 20), kQuantThreads, 0, st>>>(a);
-    return cudaGetLastError();
+  } else {
+    // room for codes included
+    const int lanes = row_lanes(mx_tiled(FMT) ? (q.cols + 31) / 32 * 32 : q.cols, mx_block(FMT) / 8);
+    quant_block_kernel<T, FMT><<<row_grid(a.padded_rows, q.cols, lanes, sms), kQuantThreads, 0, st>>>(a, lanes);
   }
-  const int64_t chunks = (q.cols + 255) / 256;
-  const int64_t ctas = (a.padded_rows * chunks + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 8 * 16);
-  if (cls == 1) quant_block_kernel<T, 1><<<grid, kQuantThreads, 0, st>>>(a, chunks);
-  else quant_block_kernel<T, 2><<<grid, kQuantThreads, 0, st>>>(a, chunks);
   return cudaGetLastError();
 }
 
@@ -203,7 +209,16 @@ ln_status mx_quantize(const void* x, int64_t x_row, int transpose, const mx_matr
   a.vec = aligned(x, 16) && (rows == 1 || (x_row * es) % 16 == 0);
   a.vec_codes = aligned(q->codes, 16);
   a.padded_rows = padded_rows(a.q);
-  e = by_dtype(dtype, [&](auto t) { return launch_quantize<decltype(t)>(a, transpose, sms, stream); });
+  e = by_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    switch (q->format) {
+      case MX_FP8_ROW: return launch_quantize<T, MX_FP8_ROW>(a, transpose, sms, stream);
+      case MX_FP8_BLOCK: return launch_quantize<T, MX_FP8_BLOCK>(a, transpose, sms, stream);
+      case MX_MXFP8: return launch_quantize<T, MX_MXFP8>(a, transpose, sms, stream);
+      case MX_MXFP4: return launch_quantize<T, MX_MXFP4>(a, transpose, sms, stream);
+      default: return launch_quantize<T, MX_NVFP4>(a, transpose, sms, stream);
+    }
+  });
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }
 
@@ -227,12 +242,12 @@ ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t
   if (e != cudaSuccess) return cuda_fail(e);
   const QuantOut o = quant_out(*q);
   const bool vec = aligned(y, 16) && (q->rows == 1 || (y_row * es) % 16 == 0);
-  const int64_t chunks = (q->cols + 7) / 8;
-  const int64_t ctas = (q->rows * chunks + kQuantThreads - 1) / kQuantThreads;
-  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 8 * 16);
+  const bool vec_codes = o.pitch % 8 == 0 && aligned(q->codes, 8);
+  const int lanes = row_lanes(q->cols, 1);
+  const dim3 grid = row_grid(q->rows, q->cols, lanes, sms);
   e = by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    dequant_kernel<T><<<grid, kQuantThreads, 0, stream>>>(o, static_cast<T*>(y), y_row, vec, chunks);
+    dequant_kernel<T><<<grid, kQuantThreads, 0, stream>>>(o, static_cast<T*>(y), y_row, vec, vec_codes, lanes);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? LN_OK : cuda_fail(e);

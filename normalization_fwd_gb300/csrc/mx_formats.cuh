@@ -43,6 +43,9 @@ inline __host__ __device__ int64_t mx_blocks(int fmt, int64_t cols) {
   return b == 0 ? 1 : (cols + b - 1) / b;
 }
 
+// A format as a type.
+template <int F> struct Format { static constexpr int value = F; };
+
 // Where a call writes a quantised matrix.
 struct QuantOut {
   unsigned char* codes;
@@ -87,14 +90,24 @@ __device__ __forceinline__ BlockScale scale_e8m0(unsigned bits) {
   return s;
 }
 
-// E4M3 scale of a block of MX_NVFP4: amax / 6, rounded to E4M3 (448 at most).
+// v / d for a constant d, correctly rounded: see quotient2.
+template <int D> __device__ __forceinline__ float over(float v) {
+  constexpr float kInv = 1.0f / (float)D;
+  const float q = v * kInv;
+  return fmaf(fmaf(-q, (float)D, v), kInv, q);
+}
+
+// E4M3 scale of a block of MX_NVFP4: amax / 6, rounded to E4M3 (448 at most), and
+// 1 / scale, correctly rounded: one Newton step from the approximation, which
+// the eight fractions that E4M3 has all reach (the tests see every one).
 __device__ __forceinline__ BlockScale scale_e4m3(unsigned bits) {
   BlockScale s;
   if (bits >= kInfBits) return {0.f, 0.f, 0x7fu};
-  const float t = __uint_as_float(bits) / 6.0f;
-  s.byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+  const float t = over<6>(__uint_as_float(bits));
+  s.byte = fp8x2(make_float2(t, 0.f), splat2(1.0f)) & 0xffu;
   s.scale = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s.byte, __NV_E4M3)));
-  s.factor = s.byte ? 1.0f / s.scale : 0.f;
+  const float r = __fdividef(1.0f, s.scale);
+  s.factor = s.byte ? fmaf(fmaf(-s.scale, r, 1.0f), r, r) : 0.f;
   return s;
 }
 
@@ -103,7 +116,7 @@ __device__ __forceinline__ BlockScale scale_e4m3(unsigned bits) {
 __device__ __forceinline__ BlockScale scale_fp32(unsigned bits) {
   if (bits >= kInfBits) return {0.f, __uint_as_float(0x7fffffffu), 0u};
   const float a = fmaxf(__uint_as_float(bits), kLeastAmax);
-  return {448.0f / a, a / 448.0f, 0u};
+  return {448.0f / a, over<448>(a), 0u};
 }
 
 // v / s, correctly rounded, from r = 1 / s rounded to nearest: q = v r is
@@ -143,17 +156,24 @@ __device__ __forceinline__ unsigned codes_e2m1(const float2* v, const BlockScale
   return s.factor == 0.f ? 0u : out;
 }
 
-// Largest |v| of 2P values as bits (NaN wins).
-template <int P>
-__device__ __forceinline__ unsigned amax_of(const float2* v) {
-  unsigned m = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) m = max(m, max(abs_bits(v[i].x), abs_bits(v[i].y)));
+// Larger magnitude of two values as a magnitude; NaN wins.
+__device__ __forceinline__ float abs_max(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
   return m;
 }
-// Largest over aligned groups of `lanes` lanes (a power of two), by all lanes of the warp.
-__device__ __forceinline__ unsigned lanes_max(unsigned m, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+// Largest |v| of 2P values as bits (NaN wins: its bits are above those of inf).
+template <int P>
+__device__ __forceinline__ unsigned amax_of(const float2* v) {
+  float m = abs_max(v[0].x, v[0].y);
+#pragma unroll
+  for (int i = 1; i < P; ++i) m = abs_max(m, abs_max(v[i].x, v[i].y));
+  return __float_as_uint(m);
+}
+// Largest over aligned groups of LANES lanes, by all lanes of the warp.
+template <int LANES> __device__ __forceinline__ unsigned lanes_max(unsigned m) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
@@ -169,43 +189,39 @@ __device__ __forceinline__ void put_codes(unsigned char* p, const unsigned* c, b
   }
 }
 
-// Scale and codes of a block whose values lie in `lanes` neighbouring lanes,
-// VEC each, in columns col .. col + VEC - 1 of the lane (values behind the
-// last column are 0). All lanes of the warp call it; `live` lanes write.
-// CLS: 1 E4M3, 2 E2M1.
-template <int VEC, int CLS>
+// Scale and codes of a block whose values lie in neighbouring lanes, VEC each, in
+// columns col .. col + VEC - 1 of the lane (values behind the last column are
+// 0). All lanes of the warp call it; `live` lanes write, `bytes_only` a byte at a
+// time and no further than the row of codes goes.
+template <int VEC, int FMT>
 __device__ __forceinline__ void put_block(const QuantOut& q, int64_t row, int64_t col, bool live,
                                           float2* v, float mul, bool bytes_only = false) {
   constexpr int P = VEC / 2;
-  const int width = mx_block(q.fmt);
-  if (CLS == 2 && q.fmt == MX_NVFP4) {
+  constexpr bool FOUR = FMT >= MX_MXFP4;
+  constexpr int kWidth = FMT == MX_NVFP4 ? 16 : FMT == MX_FP8_BLOCK ? 128 : 32;
+  if (FMT == MX_NVFP4) {
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = mul2(v[i], splat2(mul));
   }
-  const unsigned m = lanes_max(amax_of<P>(v), width / VEC);
-  unsigned c[VEC / 4 > 0 ? VEC / 4 : 1];
-  BlockScale s;
-  if (CLS == 1) {
-    s = q.fmt == MX_MXFP8 ? scale_e8m0<false>(m) : scale_fp32(m);
-    codes_e4m3<P>(v, s.factor, c);
-  } else {
-    s = q.fmt == MX_MXFP4 ? scale_e8m0<true>(m) : scale_e4m3(m);
-    c[0] = codes_e2m1<P>(v, s, q.fmt == MX_NVFP4);
-  }
+  const unsigned m = lanes_max<kWidth / VEC>(amax_of<P>(v));
+  unsigned c[VEC / 4];
+  const BlockScale s = FMT == MX_NVFP4 ? scale_e4m3(m) : FMT == MX_FP8_BLOCK ? scale_fp32(m) : scale_e8m0<FOUR>(m);
+  if (FOUR) c[0] = codes_e2m1<P>(v, s, FMT == MX_NVFP4);
+  else codes_e4m3<P>(v, s.factor, c);
   if (!live) return;
   unsigned char* row_codes = q.codes + row * q.pitch;
-  if (CLS == 2) {
+  if (FOUR) {
     put_codes<VEC>(row_codes + col / 2, c, true);
-  } else if (!bytes_only) {
+  } else if (FMT == MX_MXFP8 || !bytes_only) {
     put_codes<VEC>(row_codes + col, c, false);
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       if (col + i < q.pitch) row_codes[col + i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
   }
-  if (col % width == 0 && col < q.cols) {
-    const int64_t b = col / width;
-    if (CLS == 1 && q.fmt == MX_FP8_BLOCK) static_cast<float*>(q.scales)[row * q.blocks + b] = s.scale;
+  if (col % kWidth == 0 && col < q.cols) {
+    const int64_t b = col / kWidth;
+    if (FMT == MX_FP8_BLOCK) static_cast<float*>(q.scales)[row * q.blocks + b] = s.scale;
     else static_cast<unsigned char*>(q.scales)[scale_at(row, b, q.blocks)] = (unsigned char)s.byte;
   }
 }

@@ -102,8 +102,8 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
   const float mul = CLS == 2 ? mul_of(a.q) : 1.0f;
   const int64_t wide = a.q.pitch * (CLS == 2 ? 2 : 1);   // columns with room for codes
   unsigned m = 0;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
+  // y of slot k, in fp32
+  const auto norm = [&](int k) {
     const int v = k * G + t;
     if (row_ok && v < V) {
       float2 w[P], o[P];
@@ -119,8 +119,27 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
       if (f.y) st_vec(static_cast<T*>(f.y) + off + v * VEC, pack2<T>(s[k]));
       if (CLS == 0) m = max(m, amax_of<P>(s[k]));
     }
-    if (CLS != 0)
-      put_block<VEC, CLS>(a.q, row, (int64_t)v * VEC, row_ok && (int64_t)v * VEC < wide, s[k], mul);
+  };
+  if constexpr (CLS == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) norm(k);
+  } else {
+    const auto blocks = [&](auto fmt) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        norm(k);
+        const int col = (k * G + t) * VEC;
+        put_block<VEC, decltype(fmt)::value>(a.q, row, col, row_ok && col < wide, s[k], mul);
+      }
+    };
+    // one format a loop: its shuffles and conversions are known then
+    if (CLS == 1) {
+      if (a.q.fmt == MX_MXFP8) blocks(Format<MX_MXFP8>());
+      else blocks(Format<MX_FP8_BLOCK>());
+    } else {
+      if (a.q.fmt == MX_MXFP4) blocks(Format<MX_MXFP4>());
+      else blocks(Format<MX_NVFP4>());
+    }
   }
   if (CLS == 0) {
     const BlockScale b = scale_fp32(row_max(m));
@@ -147,7 +166,7 @@ __global__ void __launch_bounds__(kBulkThreads, N <= 3 ? 4 : 2) mx_norm_tile_ker
       ((int64_t)blockIdx.x * kConsumerWarps + (threadIdx.x >> 5)) * RPW + lane / LANES;
   mx_norm_row<T, LANES, N, CLS>(
       a, row, lane % LANES, [](float v) { return group_sum<LANES>(v); },
-      [](unsigned v) { return lanes_max(v, LANES); });
+      [](unsigned v) { return lanes_max<LANES>(v); });
 }
 
 // A CTA a row, blockDim.x * N vectors.
@@ -245,10 +264,10 @@ __global__ void __launch_bounds__(kScalarCta) mx_norm_scalar_kernel(const MxNorm
       for (int c = threadIdx.x >> 5; c < chunks; c += kScalarCta / 32) {
         const int64_t col = c * 128 + lane * 4;
         float2 v[2] = {make_float2(srow[col], srow[col + 1]), make_float2(srow[col + 2], srow[col + 3])};
-        if (mx_four(a.q.fmt))
-          put_block<4, 2>(a.q, row, col, col < a.q.pitch * 2, v, mul);
-        else
-          put_block<4, 1>(a.q, row, col, col < a.q.pitch, v, mul, !mx_tiled(a.q.fmt));
+        if (a.q.fmt == MX_NVFP4) put_block<4, MX_NVFP4>(a.q, row, col, col < a.q.pitch * 2, v, mul);
+        else if (a.q.fmt == MX_MXFP4) put_block<4, MX_MXFP4>(a.q, row, col, col < a.q.pitch * 2, v, mul);
+        else if (a.q.fmt == MX_MXFP8) put_block<4, MX_MXFP8>(a.q, row, col, col < a.q.pitch, v, mul);
+        else put_block<4, MX_FP8_BLOCK>(a.q, row, col, col < a.q.pitch, v, mul, true);
       }
     }
     __syncthreads();

@@ -2,8 +2,8 @@
 // back to values.
 //
 // Bound by HBM: each value read once, 0.5 to 1 bytes of code written for it.
-// The transpose goes through a tile in shared memory: 64 columns of x (rows of
-// the result) by 128 rows, read along x's rows and written along the result's.
+// The transpose goes through a tile in shared memory: 128 bytes of 256 rows of
+// x, read along x's rows and written along the result's.
 #pragma once
 
 #include "common.cuh"
@@ -39,174 +39,301 @@ __device__ __forceinline__ void load8(const T* row, int64_t col, int64_t n, bool
   }
 }
 
-// Blocks of 16, 32 or 128 columns: 8 columns a lane, `kTiles` warps' worth (256
-// columns each) a warp. CLS: 1 E4M3, 2 E2M1.
-template <typename T, int CLS>
-__global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantArgs a, int64_t chunks) {
+// Rows are dealt to lanes: `lanes` (a power of two from 2 on) a row, 8 columns
+// each, so that narrow matrices leave few of a warp idle; the grid's x covers
+// columns, y rows, which go on a grid apart.
+struct LaneRows {
+  int64_t row, step, col;
+  __device__ __forceinline__ LaneRows(int lanes) {
+    const int per = 32 / lanes, lane = threadIdx.x & 31;
+    row = ((int64_t)blockIdx.y * (kQuantThreads / 32) + (threadIdx.x >> 5)) * per + lane / lanes;
+    step = (int64_t)gridDim.y * (kQuantThreads / 32) * per;
+    col = (int64_t)blockIdx.x * 256 + lane % lanes * 8;
+  }
+};
+
+// Blocks of 16, 32 or 128 columns. A warp's rows end
+// together (padded_rows is a multiple of what a warp has, or the loop's test is
+// by its first row), as its lanes work on blocks together.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantArgs a, int lanes) {
+  constexpr bool FOUR = FMT >= MX_MXFP4;
   const QuantOut& q = a.q;
-  const int lane = threadIdx.x & 31;
-  const float mul = CLS == 2 ? mul_of(q) : 1.0f;
-  const int64_t wide = q.pitch * (CLS == 2 ? 2 : 1);
-  const int64_t all = a.padded_rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); i < all;
-       i += (int64_t)gridDim.x * (kQuantThreads / 32)) {
-    const int64_t row = i / chunks, chunk = i - row * chunks;
-    if (chunk == 0 && mx_tiled(q.fmt)) put_padding(q, row, lane, 32);
-    if (row >= q.rows) continue;
-    const int64_t col = chunk * 256 + lane * 8;
-    float2 v[4];
-    load8<T>(static_cast<const T*>(a.x) + row * a.x_row, col, q.cols, a.vec != 0, v);
-    put_block<8, CLS>(q, row, col, col < wide, v, mul, CLS == 1 && (q.pitch % 8 != 0 || !a.vec_codes));
+  const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
+  const int64_t wide = q.pitch * (FOUR ? 2 : 1);
+  const LaneRows at(lanes);
+  const int t = (threadIdx.x & 31) % lanes;
+  const bool bytes = FMT == MX_FP8_BLOCK && (q.pitch % 8 != 0 || !a.vec_codes);
+  int64_t row = at.row;
+  const auto load = [&](int64_t r, float2* v) {
+    load8<T>(static_cast<const T*>(a.x) + r * a.x_row, at.col, r < q.rows ? q.cols : 0, a.vec != 0, v);
+  };
+  float2 v[4], next[4];
+  load(row, v);
+  for (; __any_sync(0xffffffffu, row < a.padded_rows); row += at.step) {
+    load(row + at.step, next);      // on its way while this row is worked on
+    if (FMT != MX_FP8_BLOCK && blockIdx.x == 0 && row < a.padded_rows) put_padding(q, row, t, lanes);
+    put_block<8, FMT>(q, row, at.col, row < q.rows && at.col < wide, v, mul, bytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = next[i];
   }
 }
 
-// A scale a row: a CTA a row, which it reads twice (the second time out of the caches).
+// A scale a row: a CTA a row. The first 8192 columns stay in registers, those
+// behind them are read again (out of the caches).
+constexpr int kRowKept = 4;
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) quant_row_kernel(const QuantArgs a) {
-  __shared__ unsigned red[kQuantThreads / 32];
+  __shared__ unsigned red[2][kQuantThreads / 32];
   const QuantOut& q = a.q;
-  for (int64_t row = blockIdx.x; row < q.rows; row += gridDim.x) {
+  const bool vec_codes = q.pitch % 8 == 0 && a.vec_codes;
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < q.rows; row += gridDim.x, parity ^= 1) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_row;
     unsigned m = 0;
-    for (int64_t col = threadIdx.x * 8; col < q.cols; col += kQuantThreads * 8) {
-      float2 v[4];
-      load8<T>(x, col, q.cols, a.vec != 0, v);
-      m = max(m, amax_of<4>(v));
+    float2 v[kRowKept][4];
+#pragma unroll
+    for (int k = 0; k < kRowKept; ++k) {
+      load8<T>(x, (k * kQuantThreads + (int)threadIdx.x) * 8, q.cols, a.vec != 0, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowKept; ++k) m = max(m, amax_of<4>(v[k]));
+    for (int64_t col = ((int64_t)kRowKept * kQuantThreads + threadIdx.x) * 8; col < q.cols; col += kQuantThreads * 8) {
+      float2 w[4];
+      load8<T>(x, col, q.cols, a.vec != 0, w);
+      m = max(m, amax_of<4>(w));
     }
     m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = m;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, red[i]);
+    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, red[parity][i]);
     const BlockScale s = scale_fp32(m);
     if (threadIdx.x == 0) static_cast<float*>(q.scales)[row] = s.scale;
     unsigned char* codes = q.codes + row * q.pitch;
-    for (int64_t col = threadIdx.x * 8; col < q.cols; col += kQuantThreads * 8) {
-      float2 v[4];
+    const auto put = [&](int64_t col, const float2* w) {
       unsigned c[2];
-      load8<T>(x, col, q.cols, a.vec != 0, v);
-      codes_e4m3<4>(v, s.factor, c);
-      if (q.pitch % 8 == 0 && a.vec_codes && col + 8 <= q.cols) {
+      if (col >= q.cols) return;
+      codes_e4m3<4>(w, s.factor, c);
+      if (vec_codes && col + 8 <= q.cols) {
         put_codes<8>(codes + col, c, false);
       } else {
-        for (int i = 0; i < 8 && col + i < q.cols; ++i) codes[col + i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col + i < q.cols) codes[col + i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
       }
+    };
+#pragma unroll
+    for (int k = 0; k < kRowKept; ++k) put((k * kQuantThreads + (int)threadIdx.x) * 8, v[k]);
+    for (int64_t col = ((int64_t)kRowKept * kQuantThreads + threadIdx.x) * 8; col < q.cols; col += kQuantThreads * 8) {
+      float2 w[4];
+      load8<T>(x, col, q.cols, a.vec != 0, w);
+      put(col, w);
     }
   }
 }
 
-// The transpose. A CTA has 64 rows of the result (columns of x) and, for the
-// block formats, 128 columns of it (rows of x) a tile; with a scale a row it
-// goes over all tiles of its rows twice.
-constexpr int kTrRows = 64;     // columns of x
-constexpr int kTrCols = 128;    // rows of x
+// The transpose. A tile is 32 words (32 fp32 or 64 16-bit columns of x: rows of
+// the result) by 256 rows of x; a lane has a word's one or two rows, a warp 32 of
+// the result's columns. With a scale a row a CTA goes over all tiles of its rows
+// twice.
+constexpr int kTrCols = 256;
+constexpr int kTrPitch = 33;
+template <typename T> struct TrRows { static constexpr int N = 32 * 4 / sizeof(T); };
 
 template <typename T>
-__device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t row0, int64_t col0,
-                                          T (*tile)[kTrRows + 2]) {
+__device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t row0, int64_t col0, unsigned* tile) {
+  constexpr int V = Vec<T>::N;                  // of 16 bytes, 8 of them a row of the tile
   const int64_t rows = a.q.rows, cols = a.q.cols;
-  for (int i = threadIdx.x; i < kTrCols * (kTrRows / 8); i += kQuantThreads) {
-    const int c = i / (kTrRows / 8), r = i % (kTrRows / 8) * 8;
-    float2 v[4];
+  uint4 w[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = splat2(0.f);
-    if (col0 + c < cols) load8<T>(static_cast<const T*>(a.x) + (col0 + c) * a.x_row, row0 + r, rows, a.vec != 0, v);
-    const float* f = reinterpret_cast<const float*>(v);
+  for (int i = 0; i < 8; ++i) {
+    const int at = i * kQuantThreads + threadIdx.x, c = at >> 3, r = (at & 7) * V;
+    const T* x = static_cast<const T*>(a.x) + (col0 + c) * a.x_row + row0 + r;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (col0 + c < cols) {
+      if (a.vec && row0 + r + V <= rows) {
+        w[i] = ld_vec(x);
+      } else {
+        T t[V];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tile[c][r + j] = from_f<T>(f[j]);   // what was read: exact
+        for (int j = 0; j < V; ++j) t[j] = row0 + r + j < rows ? x[j] : from_f<T>(0.f);
+        w[i] = *reinterpret_cast<const uint4*>(t);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int at = i * kQuantThreads + threadIdx.x;
+    unsigned* p = tile + (at >> 3) * kTrPitch + (at & 7) * 4;
+    p[0] = w[i].x;
+    p[1] = w[i].y;
+    p[2] = w[i].z;
+    p[3] = w[i].w;
   }
 }
 
-// CLS: 0 a scale a row, 1 blocks of E4M3, 2 blocks of E2M1.
-template <typename T, int CLS>
-__global__ void __launch_bounds__(kQuantThreads) quant_transpose_kernel(const QuantArgs a) {
-  __shared__ T tile[kTrCols][kTrRows + 2];
-  __shared__ unsigned red[kTrRows][4];
+// Value h (0, or 1 of 16-bit types) of a word.
+template <typename T> __device__ __forceinline__ float word_value(unsigned w, int h);
+template <> __device__ __forceinline__ float word_value<float>(unsigned w, int) { return __uint_as_float(w); }
+template <> __device__ __forceinline__ float word_value<bf16>(unsigned w, int h) {
+  return __uint_as_float(h ? w & 0xffff0000u : w << 16);
+}
+template <> __device__ __forceinline__ float word_value<f16>(unsigned w, int h) {
+  return __half2float(__ushort_as_half((unsigned short)(h ? w >> 16 : w & 0xffffu)));
+}
+
+// Largest |value| of n words, of each of a word's rows, as fp32 bits. 16-bit
+// values are compared as they lie, two at a time.
+template <typename T, int N> __device__ __forceinline__ void words_amax(const unsigned* w, unsigned* m) {
+  if (sizeof(T) == 4) {
+    m[0] = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[0] = max(m[0], w[i] & 0x7fffffffu);
+  } else {
+    unsigned b = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) b = __vmaxu2(b, w[i] & 0x7fff7fffu);
+    m[0] = __float_as_uint(word_value<T>(b, 0));
+    m[sizeof(T) == 2] = __float_as_uint(word_value<T>(b, 1));
+  }
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kQuantThreads, 3) quant_transpose_kernel(const QuantArgs a) {
+  __shared__ unsigned tile[kTrCols * kTrPitch];
+  constexpr int W = 4 / sizeof(T);             // rows of a lane
+  constexpr bool FOUR = FMT >= MX_MXFP4, TILED = FMT >= MX_MXFP8;
+  __shared__ unsigned red[8][32][W];
   const QuantOut& q = a.q;
-  const int64_t row0 = (int64_t)blockIdx.x * kTrRows;
-  const int r = threadIdx.x & (kTrRows - 1), part = threadIdx.x / kTrRows;   // 32 columns each
-  const int64_t row = row0 + r;
-  const float mul = CLS == 2 ? mul_of(q) : 1.0f;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * TrRows<T>::N, row = row0 + lane * W;
+  const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
   const int64_t tiles = (q.cols + kTrCols - 1) / kTrCols;
-  if (CLS != 0 && mx_tiled(q.fmt) && blockIdx.y == 0 && row < a.padded_rows) put_padding(q, row, part, 4);
-  unsigned m = 0;
-  if (CLS == 0) {
+  const unsigned* mine = tile + part * 32 * kTrPitch + lane;
+  if (TILED && blockIdx.y == 0)
+    for (int h = 0; h < W; ++h)
+      if (row + h < a.padded_rows) put_padding(q, row + h, part, 8);
+  unsigned m[W] = {};
+  BlockScale s[W];
+  if (FMT == MX_FP8_ROW) {
     for (int64_t t = 0; t < tiles; ++t) {
       __syncthreads();
       load_tile<T>(a, row0, t * kTrCols, tile);
       __syncthreads();
-      for (int i = 0; i < 32; ++i) m = max(m, abs_bits(to_f(tile[part * 32 + i][r])));
+      unsigned w[32], b[W];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = mine[i * kTrPitch];
+      words_amax<T, 32>(w, b);
+#pragma unroll
+      for (int h = 0; h < W; ++h) m[h] = max(m[h], b[h]);
     }
-    red[r][part] = m;
+#pragma unroll
+    for (int h = 0; h < W; ++h) red[part][lane][h] = m[h];
     __syncthreads();
-    m = max(max(red[r][0], red[r][1]), max(red[r][2], red[r][3]));
+#pragma unroll
+    for (int h = 0; h < W; ++h) {
+      for (int i = 0; i < 8; ++i) m[h] = max(m[h], red[i][lane][h]);
+      s[h] = scale_fp32(m[h]);
+      if (part == 0 && row + h < q.rows) static_cast<float*>(q.scales)[row + h] = s[h].scale;
+    }
   }
-  BlockScale s = scale_fp32(m);
-  if (CLS == 0 && part == 0 && row < q.rows) static_cast<float*>(q.scales)[row] = s.scale;
   for (int64_t t = blockIdx.y; t < tiles; t += gridDim.y) {
     __syncthreads();
     load_tile<T>(a, row0, t * kTrCols, tile);
     __syncthreads();
     const int64_t col = t * kTrCols + part * 32;
-    float2 v[16];
-    m = 0;
+    unsigned w[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      v[i] = make_float2(to_f(tile[part * 32 + 2 * i][r]), to_f(tile[part * 32 + 2 * i + 1][r]));
-      if (CLS == 2 && q.fmt == MX_NVFP4) v[i] = mul2(v[i], splat2(mul));
-    }
-    if (CLS == 1) {
-      m = amax_of<16>(v);
-      if (q.fmt == MX_FP8_BLOCK) {
-        red[r][part] = m;
-        __syncthreads();
-        m = max(max(red[r][0], red[r][1]), max(red[r][2], red[r][3]));
-        s = scale_fp32(m);
-      } else {
-        s = scale_e8m0<false>(m);
+    for (int i = 0; i < 32; ++i) w[i] = mine[i * kTrPitch];
+    if (FMT == MX_FP8_BLOCK) {                    // four warps have a block
+      words_amax<T, 32>(w, m);
+#pragma unroll
+      for (int h = 0; h < W; ++h) red[part][lane][h] = m[h];
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < W; ++h) {
+        unsigned b = 0;
+        for (int i = 0; i < 4; ++i) b = max(b, red[(part & 4) + i][lane][h]);
+        s[h] = scale_fp32(b);
       }
     }
-    if (row >= q.rows || col >= q.cols) continue;    // the barriers are at the loop's head
-    if (CLS == 2) {
-      unsigned w[4];
+    if (col >= q.cols) continue;                  // the barriers are at the loop's head
+    unsigned m2[W];
+    if (FMT == MX_NVFP4) {
+      words_amax<T, 16>(w, m);
+      words_amax<T, 16>(w + 16, m2);
+    } else if (TILED) {
+      words_amax<T, 32>(w, m);
+    }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        s = q.fmt == MX_NVFP4 ? scale_e4m3(amax_of<8>(v + 8 * h)) : scale_e8m0<true>(amax_of<16>(v));
-        w[2 * h] = codes_e2m1<4>(v + 8 * h, s, q.fmt == MX_NVFP4);
-        w[2 * h + 1] = codes_e2m1<4>(v + 8 * h + 4, s, q.fmt == MX_NVFP4);
-        const int64_t b = q.fmt == MX_NVFP4 ? col / 16 + h : col / 32;
-        if (b < q.blocks) static_cast<unsigned char*>(q.scales)[scale_at(row, b, q.blocks)] = (unsigned char)s.byte;
-      }
-      *reinterpret_cast<uint4*>(q.codes + row * q.pitch + col / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      unsigned w[8];
-      codes_e4m3<16>(v, s.factor, w);
-      unsigned char* p = q.codes + row * q.pitch + col;
-      if (a.vec_codes && q.pitch % 16 == 0 && col + 32 <= q.pitch) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int h = 0; h < W; ++h) {
+      if (row + h >= q.rows) break;
+      unsigned char* scales = static_cast<unsigned char*>(q.scales);
+      if (FOUR) {
+        unsigned c[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          BlockScale b;
+          if (FMT == MX_NVFP4) {
+            // the largest product is that of the largest value: products round monotonically
+            b = scale_e4m3(__float_as_uint(fabsf(__uint_as_float(k ? m2[h] : m[h]) * mul)));
+            if (col / 16 + k < q.blocks) scales[scale_at(row + h, col / 16 + k, q.blocks)] = (unsigned char)b.byte;
+          } else {
+            b = scale_e8m0<true>(m[h]);
+            if (k == 0) scales[scale_at(row + h, col / 32, q.blocks)] = (unsigned char)b.byte;
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = 16 * k + 8 * g + 2 * i;
+              v[i] = make_float2(word_value<T>(w[at], h), word_value<T>(w[at + 1], h));
+              if (FMT == MX_NVFP4) v[i] = mul2(v[i], splat2(mul));
+            }
+            c[2 * k + g] = codes_e2m1<4>(v, b, FMT == MX_NVFP4);
+          }
+        }
+        *reinterpret_cast<uint4*>(q.codes + (row + h) * q.pitch + col / 2) = make_uint4(c[0], c[1], c[2], c[3]);
       } else {
+        if (FMT == MX_MXFP8) {
+          s[h] = scale_e8m0<false>(m[h]);
+          scales[scale_at(row + h, col / 32, q.blocks)] = (unsigned char)s[h].byte;
+        } else if (FMT == MX_FP8_BLOCK && part % 4 == 0) {
+          static_cast<float*>(q.scales)[(row + h) * q.blocks + col / 128] = s[h].scale;
+        }
+        unsigned c[8];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (col + i < q.pitch) p[i] = (unsigned char)(w[i / 4] >> (8 * (i % 4)));
-      }
-      if (CLS == 1 && q.fmt == MX_FP8_BLOCK) {
-        if (part == 0) static_cast<float*>(q.scales)[row * q.blocks + t] = s.scale;
-      } else if (CLS == 1) {
-        static_cast<unsigned char*>(q.scales)[scale_at(row, col / 32, q.blocks)] = (unsigned char)s.byte;
+        for (int i = 0; i < 8; ++i) {
+          const float2 v[2] = {make_float2(word_value<T>(w[4 * i], h), word_value<T>(w[4 * i + 1], h)),
+                               make_float2(word_value<T>(w[4 * i + 2], h), word_value<T>(w[4 * i + 3], h))};
+          codes_e4m3<2>(v, s[h].factor, c + i);
+        }
+        unsigned char* p = q.codes + (row + h) * q.pitch + col;
+        if (TILED || (a.vec_codes && q.pitch % 16 == 0 && col + 32 <= q.pitch)) {
+          *reinterpret_cast<uint4*>(p) = make_uint4(c[0], c[1], c[2], c[3]);
+          *reinterpret_cast<uint4*>(p + 16) = make_uint4(c[4], c[5], c[6], c[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + i < q.pitch) p[i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
+        }
       }
     }
   }
 }
 
-// Values of 8 columns a thread.
+// Values, 8 columns a lane.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q, T* y, int64_t y_row,
-                                                                bool vec, int64_t chunks) {
-  const int64_t all = q.rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < all;
-       i += (int64_t)gridDim.x * kQuantThreads) {
-    const int64_t row = i / chunks, col = (i - row * chunks) * 8;
+                                                                bool vec, bool vec_codes, int lanes) {
+  const LaneRows at(lanes);
+  const int64_t col = at.col;
+  if (col >= q.cols) return;
+  const float mul = mul_of(q), r_mul = 1.0f / mul;
+  const bool divide = q.fmt == MX_NVFP4 && q.mul != nullptr;
+  const int64_t block = mx_block(q.fmt) ? col / mx_block(q.fmt) : 0;
+  for (int64_t row = at.row; row < q.rows; row += at.step) {
     const unsigned char* codes = q.codes + row * q.pitch;
     float2 v[4];
     if (mx_four(q.fmt)) {
@@ -215,36 +342,46 @@ __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q
       for (int j = 0; j < 4; ++j)
         v[j] = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * j)), __NV_E2M1)));
     } else {
-      float* f = reinterpret_cast<float*>(v);
+      unsigned w[2] = {0, 0};
+      if (vec_codes) {
+        const uint2 u = *reinterpret_cast<const uint2*>(codes + col);
+        w[0] = u.x;
+        w[1] = u.y;
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f[j] = __half2float(__half(__nv_cvt_fp8_to_halfraw(col + j < q.pitch ? codes[col + j] : (unsigned char)0, __NV_E4M3)));
+        for (int j = 0; j < 8; ++j)
+          if (col + j < q.pitch) w[j / 4] |= (unsigned)codes[col + j] << (8 * (j % 4));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j / 2] >> (16 * (j % 2))), __NV_E4M3)));
     }
     float s;
-    if (q.fmt == MX_FP8_ROW) {
-      s = static_cast<const float*>(q.scales)[row];
-    } else if (q.fmt == MX_FP8_BLOCK) {
-      s = static_cast<const float*>(q.scales)[row * q.blocks + col / 128];
+    if (!mx_tiled(q.fmt)) {
+      s = static_cast<const float*>(q.scales)[row * q.blocks + block];
     } else {
-      const unsigned b = static_cast<const unsigned char*>(q.scales)[scale_at(row, col / mx_block(q.fmt), q.blocks)];
+      const unsigned b = static_cast<const unsigned char*>(q.scales)[scale_at(row, block, q.blocks)];
       if (q.fmt == MX_NVFP4)
         s = __half2float(__half(__nv_cvt_fp8_to_halfraw((unsigned char)b, __NV_E4M3)));
       else
         s = b == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 1u << 22);
     }
-    const float mul = mul_of(q);
-    float* f = reinterpret_cast<float*>(v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = f[j] * s;
-    if (q.fmt == MX_NVFP4 && q.mul != nullptr) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] / mul;
+    for (int j = 0; j < 4; ++j) {
+      v[j] = mul2(v[j], splat2(s));
+      if (divide) {
+        const float2 d = quotient2(v[j], mul, r_mul);
+        // past the largest fp32 number the correction would be inf - inf
+        v[j] = make_float2(fabsf(v[j].x * r_mul) <= 0x1.fp127f ? d.x : v[j].x / mul,
+                           fabsf(v[j].y * r_mul) <= 0x1.fp127f ? d.y : v[j].y / mul);
+      }
     }
     T* out = y + row * y_row + col;
     if (vec && col + 8 <= q.cols) {
 #pragma unroll
       for (int j = 0; j < 8 / Vec<T>::N; ++j) st_vec(out + j * Vec<T>::N, pack2<T>(v + j * Vec<T>::N / 2));
     } else {
+      const float* f = reinterpret_cast<const float*>(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (col + j < q.cols) out[j] = from_f<T>(f[j]);
