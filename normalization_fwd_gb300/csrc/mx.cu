@@ -62,17 +62,17 @@ NormPlan norm_plan(int slots, int least_lanes) {
 
 int64_t padded_rows(const QuantOut& q) { return mx_tiled(q.fmt) ? (q.rows + 127) / 128 * 128 : q.rows; }
 
-// Lanes a row of `cols` columns takes at 8 a lane (`least` at least), and the grid
-// of CTAs that deal rows to them: about 16 CTAs an SM, so that each lane's rows
-// are enough to keep one on its way.
-int row_lanes(int64_t cols, int least) {
-  int lanes = least;
-  while (lanes < 32 && lanes * 8 < cols) lanes *= 2;
-  return lanes;
+// Lanes a row of `cols` columns takes at 8 a lane (`least` at least), as a power
+// of two, and the grid of CTAs that deal rows to them: about 12 an SM, so that a
+// lane has rows enough to have one on its way.
+int row_shift(int64_t cols, int least) {
+  int shift = 0;
+  while (shift < 5 && ((1 << shift) < least || (8 << shift) < cols)) ++shift;
+  return shift;
 }
-dim3 row_grid(int64_t rows, int64_t cols, int lanes, int sms) {
-  const int64_t x = (cols + 255) / 256, per = (int64_t)(kQuantThreads / 32) * (32 / lanes);
-  const int64_t most = std::max<int64_t>(1, (int64_t)sms * 16 / x);
+dim3 row_grid(int64_t rows, int64_t cols, int shift, int sms) {
+  const int64_t x = (cols + 255) / 256, per = (int64_t)(kQuantThreads / 32) << (5 - shift);
+  const int64_t most = std::max<int64_t>(1, (int64_t)sms * 12 / x);
   return dim3((unsigned)x, (unsigned)std::min<int64_t>(std::min<int64_t>((rows + per - 1) / per, most), 65535));
 }
 
@@ -87,8 +87,8 @@ cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStre
     quant_row_kernel<T><<<(unsigned)std::min<int64_t>(q.rows, 1 << 20), kQuantThreads, 0, st>>>(a);
   } else {
     // room for codes included
-    const int lanes = row_lanes(mx_tiled(FMT) ? (q.cols + 31) / 32 * 32 : q.cols, mx_block(FMT) / 8);
-    quant_block_kernel<T, FMT><<<row_grid(a.padded_rows, q.cols, lanes, sms), kQuantThreads, 0, st>>>(a, lanes);
+    const int shift = row_shift(mx_tiled(FMT) ? (q.cols + 31) / 32 * 32 : q.cols, mx_block(FMT) / 8);
+    quant_block_kernel<T, FMT><<<row_grid(a.padded_rows, q.cols, shift, sms), kQuantThreads, 0, st>>>(a, shift);
   }
   return cudaGetLastError();
 }
@@ -243,12 +243,21 @@ ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t
   const QuantOut o = quant_out(*q);
   const bool vec = aligned(y, 16) && (q->rows == 1 || (y_row * es) % 16 == 0);
   const bool vec_codes = o.pitch % 8 == 0 && aligned(q->codes, 8);
-  const int lanes = row_lanes(q->cols, 1);
-  const dim3 grid = row_grid(q->rows, q->cols, lanes, sms);
+  const int shift = row_shift(q->cols, 1);
+  const dim3 grid = row_grid(q->rows, q->cols, shift, sms);
   e = by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    dequant_kernel<T><<<grid, kQuantThreads, 0, stream>>>(o, static_cast<T*>(y), y_row, vec, vec_codes, lanes);
-    return cudaGetLastError();
+    const auto run = [&](auto fmt) {
+      dequant_kernel<T, decltype(fmt)::value><<<grid, kQuantThreads, 0, stream>>>(o, static_cast<T*>(y), y_row, vec,
+                                                                                  vec_codes, shift);
+      return cudaGetLastError();
+    };
+    switch (q->format) {
+      case MX_MXFP8: return run(Format<MX_MXFP8>());
+      case MX_MXFP4: return run(Format<MX_MXFP4>());
+      case MX_NVFP4: return run(Format<MX_NVFP4>());
+      default: return run(Format<MX_FP8_ROW>());
+    }
   });
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }

@@ -16,7 +16,6 @@
 // Tiles run along a row first; what lies behind the last row or block is 0.
 #pragma once
 
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include "../../include/normfuse.h"
@@ -44,7 +43,11 @@ inline __host__ __device__ int64_t mx_blocks(int fmt, int64_t cols) {
 }
 
 // A format as a type.
-template <int F> struct Format { static constexpr int value = F; };
+template <int F> struct Format {
+  static constexpr int value = F;
+  static constexpr bool four = F >= MX_MXFP4;
+  static constexpr int width = F == MX_NVFP4 ? 16 : F == MX_FP8_BLOCK ? 128 : 32;
+};
 
 // Where a call writes a quantised matrix.
 struct QuantOut {
@@ -58,10 +61,13 @@ struct QuantOut {
   int fmt;
 };
 
-// Offset of a block's scale byte in the tiles.
+// Offset of a block's scale byte in the tiles: a row's part and a block's.
+__host__ __device__ __forceinline__ int64_t scale_row(int64_t row, int64_t blocks) {
+  return (row >> 7) * ((blocks + 3) >> 2) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+__host__ __device__ __forceinline__ int64_t scale_block(int64_t block) { return (block >> 2) * 512 + (block & 3); }
 __host__ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t block, int64_t blocks) {
-  return ((row >> 7) * ((blocks + 3) >> 2) + (block >> 2)) * 512 + (row & 31) * 16 +
-         ((row >> 5) & 3) * 4 + (block & 3);
+  return scale_row(row, blocks) + scale_block(block);
 }
 
 // A scale and the factor that goes with it: codes are those of v * factor
@@ -141,18 +147,50 @@ __device__ __forceinline__ void codes_e4m3(const float2* v, float factor, unsign
     for (int i = 0; i < P; i += 2) out[i / 2] = 0u;
   }
 }
-__device__ __forceinline__ unsigned fp4x2(float2 v) {
-  return (unsigned)__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest);
+// E2M1 codes of four or eight values, to nearest even, 6 at most.
+__device__ __forceinline__ unsigned fp4x4(float2 a, float2 b) {
+  unsigned o;
+  asm("{\n\t.reg .b8 b0, b1, z;\n\tmov.b16 {z, z}, 0;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "mov.b32 %0, {b0, b1, z, z};\n\t}"
+      : "=r"(o)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return o;
+}
+__device__ __forceinline__ unsigned fp4x8(const float2* v) {
+  unsigned o;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(o)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x),
+        "f"(v[3].y));
+  return o;
+}
+// The eight values of four bytes of E2M1 codes.
+__device__ __forceinline__ void fp4_values(unsigned w, float2* v) {
+  unsigned h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f16x2_to_f2(h[i]);
 }
 // 2P / 2 bytes in the low end of the result (P = 2, 4).
 template <int P>
 __device__ __forceinline__ unsigned codes_e2m1(const float2* v, const BlockScale& s, bool nvfp4) {
-  unsigned out = 0;
+  float2 q[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const float2 q = nvfp4 ? quotient2(v[i], s.scale, s.factor) : mul2(v[i], splat2(s.factor));
-    out |= fp4x2(q) << (8 * i);
-  }
+  for (int i = 0; i < P; ++i) q[i] = nvfp4 ? quotient2(v[i], s.scale, s.factor) : mul2(v[i], splat2(s.factor));
+  unsigned out;
+  if constexpr (P == 4) out = fp4x8(q);
+  else out = fp4x4(q[0], q[1]);
   return s.factor == 0.f ? 0u : out;
 }
 
@@ -189,13 +227,13 @@ __device__ __forceinline__ void put_codes(unsigned char* p, const unsigned* c, b
   }
 }
 
-// Scale and codes of a block whose values lie in neighbouring lanes, VEC each, in
-// columns col .. col + VEC - 1 of the lane (values behind the last column are
-// 0). All lanes of the warp call it; `live` lanes write, `bytes_only` a byte at a
-// time and no further than the row of codes goes.
+// Scale and codes of a block whose values lie in neighbouring lanes, VEC each (0
+// behind the last column). All lanes of the warp call it; a lane's codes go to
+// `codes`, the block's scale to `scale` (fp32 or a byte) where these are not
+// null. `bytes` (MX_FP8_BLOCK): a byte at a time, `most` of them.
 template <int VEC, int FMT>
-__device__ __forceinline__ void put_block(const QuantOut& q, int64_t row, int64_t col, bool live,
-                                          float2* v, float mul, bool bytes_only = false) {
+__device__ __forceinline__ void put_block(float2* v, float mul, unsigned char* codes, void* scale,
+                                          int most = VEC, bool bytes = false) {
   constexpr int P = VEC / 2;
   constexpr bool FOUR = FMT >= MX_MXFP4;
   constexpr int kWidth = FMT == MX_NVFP4 ? 16 : FMT == MX_FP8_BLOCK ? 128 : 32;
@@ -208,22 +246,29 @@ __device__ __forceinline__ void put_block(const QuantOut& q, int64_t row, int64_
   const BlockScale s = FMT == MX_NVFP4 ? scale_e4m3(m) : FMT == MX_FP8_BLOCK ? scale_fp32(m) : scale_e8m0<FOUR>(m);
   if (FOUR) c[0] = codes_e2m1<P>(v, s, FMT == MX_NVFP4);
   else codes_e4m3<P>(v, s.factor, c);
-  if (!live) return;
-  unsigned char* row_codes = q.codes + row * q.pitch;
-  if (FOUR) {
-    put_codes<VEC>(row_codes + col / 2, c, true);
-  } else if (FMT == MX_MXFP8 || !bytes_only) {
-    put_codes<VEC>(row_codes + col, c, false);
-  } else {
+  if (codes) {
+    if (FMT != MX_FP8_BLOCK || !bytes) {
+      put_codes<VEC>(codes, c, FOUR);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      if (col + i < q.pitch) row_codes[col + i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
+      for (int i = 0; i < VEC; ++i)
+        if (i < most) codes[i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
+    }
   }
-  if (col % kWidth == 0 && col < q.cols) {
-    const int64_t b = col / kWidth;
-    if (FMT == MX_FP8_BLOCK) static_cast<float*>(q.scales)[row * q.blocks + b] = s.scale;
-    else static_cast<unsigned char*>(q.scales)[scale_at(row, b, q.blocks)] = (unsigned char)s.byte;
+  if (scale) {
+    if (FMT == MX_FP8_BLOCK) *static_cast<float*>(scale) = s.scale;
+    else *static_cast<unsigned char*>(scale) = (unsigned char)s.byte;
   }
+}
+
+// Where the scale of a row's block goes, by the row's part of its place.
+template <int FMT>
+__device__ __forceinline__ void* scale_place(const QuantOut& q, int64_t row_part, int64_t block) {
+  return FMT == MX_FP8_BLOCK ? (void*)(static_cast<float*>(q.scales) + row_part + block)
+                             : (void*)(static_cast<unsigned char*>(q.scales) + row_part + scale_block(block));
+}
+template <int FMT> __device__ __forceinline__ int64_t scale_row_part(const QuantOut& q, int64_t row) {
+  return FMT == MX_FP8_BLOCK ? row * q.blocks : scale_row(row, q.blocks);
 }
 
 // The scale bytes behind a row's last block, and all of a row behind the last

@@ -100,7 +100,7 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
 
   const float2 r2 = splat2(rstd);
   const float mul = CLS == 2 ? mul_of(a.q) : 1.0f;
-  const int64_t wide = a.q.pitch * (CLS == 2 ? 2 : 1);   // columns with room for codes
+  const int wide = (int)a.q.pitch * (CLS == 2 ? 2 : 1);   // columns with room for codes
   unsigned m = 0;
   // y of slot k, in fp32
   const auto norm = [&](int k) {
@@ -125,11 +125,16 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
     for (int k = 0; k < N; ++k) norm(k);
   } else {
     const auto blocks = [&](auto fmt) {
+      using F = decltype(fmt);
+      const int64_t part = scale_row_part<F::value>(a.q, row);
+      unsigned char* codes = a.q.codes + row * a.q.pitch;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         norm(k);
         const int col = (k * G + t) * VEC;
-        put_block<VEC, decltype(fmt)::value>(a.q, row, col, row_ok && col < wide, s[k], mul);
+        const bool first = row_ok && col % F::width == 0 && col < H;
+        put_block<VEC, F::value>(s[k], mul, row_ok && col < wide ? codes + (F::four ? col / 2 : col) : nullptr,
+                                 first ? scale_place<F::value>(a.q, part, col / F::width) : nullptr);
       }
     };
     // one format a loop: its shuffles and conversions are known then
@@ -261,14 +266,22 @@ __global__ void __launch_bounds__(kScalarCta) mx_norm_scalar_kernel(const MxNorm
         a.q.codes[off + j] = b.factor == 0.f ? 0 : fp8_one(srow[j], b.factor);
     } else {
       const int lane = threadIdx.x & 31;
-      for (int c = threadIdx.x >> 5; c < chunks; c += kScalarCta / 32) {
-        const int64_t col = c * 128 + lane * 4;
-        float2 v[2] = {make_float2(srow[col], srow[col + 1]), make_float2(srow[col + 2], srow[col + 3])};
-        if (a.q.fmt == MX_NVFP4) put_block<4, MX_NVFP4>(a.q, row, col, col < a.q.pitch * 2, v, mul);
-        else if (a.q.fmt == MX_MXFP4) put_block<4, MX_MXFP4>(a.q, row, col, col < a.q.pitch * 2, v, mul);
-        else if (a.q.fmt == MX_MXFP8) put_block<4, MX_MXFP8>(a.q, row, col, col < a.q.pitch, v, mul);
-        else put_block<4, MX_FP8_BLOCK>(a.q, row, col, col < a.q.pitch, v, mul, true);
-      }
+      const auto blocks = [&](auto fmt) {
+        using F = decltype(fmt);
+        const int64_t part = scale_row_part<F::value>(a.q, row);
+        const int wide = (int)a.q.pitch * (F::four ? 2 : 1);
+        for (int c = threadIdx.x >> 5; c < chunks; c += kScalarCta / 32) {
+          const int col = c * 128 + lane * 4;
+          float2 v[2] = {make_float2(srow[col], srow[col + 1]), make_float2(srow[col + 2], srow[col + 3])};
+          put_block<4, F::value>(v, mul, col < wide ? a.q.codes + row * a.q.pitch + (F::four ? col / 2 : col) : nullptr,
+                                 col % F::width == 0 && col < H ? scale_place<F::value>(a.q, part, col / F::width) : nullptr,
+                                 min(4, wide - col), true);   // rows of MX_FP8_BLOCK start anywhere
+        }
+      };
+      if (a.q.fmt == MX_NVFP4) blocks(Format<MX_NVFP4>());
+      else if (a.q.fmt == MX_MXFP4) blocks(Format<MX_MXFP4>());
+      else if (a.q.fmt == MX_MXFP8) blocks(Format<MX_MXFP8>());
+      else blocks(Format<MX_FP8_BLOCK>());
     }
     __syncthreads();
   }

@@ -39,43 +39,66 @@ __device__ __forceinline__ void load8(const T* row, int64_t col, int64_t n, bool
   }
 }
 
-// Rows are dealt to lanes: `lanes` (a power of two from 2 on) a row, 8 columns
-// each, so that narrow matrices leave few of a warp idle; the grid's x covers
-// columns, y rows, which go on a grid apart.
+// Rows are dealt to lanes: 2^shift lanes a row, 8 columns each, so that narrow
+// matrices leave few of a warp idle; the grid's x covers columns, y rows, which
+// go on a grid apart.
 struct LaneRows {
   int64_t row, step, col;
-  __device__ __forceinline__ LaneRows(int lanes) {
-    const int per = 32 / lanes, lane = threadIdx.x & 31;
-    row = ((int64_t)blockIdx.y * (kQuantThreads / 32) + (threadIdx.x >> 5)) * per + lane / lanes;
-    step = (int64_t)gridDim.y * (kQuantThreads / 32) * per;
-    col = (int64_t)blockIdx.x * 256 + lane % lanes * 8;
+  __device__ __forceinline__ LaneRows(int shift) {
+    const int per = 5 - shift, lane = threadIdx.x & 31;      // rows of a warp, as a power of two
+    row = (((int64_t)blockIdx.y * (kQuantThreads / 32) + (threadIdx.x >> 5)) << per) + (lane >> shift);
+    step = ((int64_t)gridDim.y * (kQuantThreads / 32)) << per;
+    col = (int64_t)blockIdx.x * 256 + (lane & ((1 << shift) - 1)) * 8;
   }
 };
 
-// Blocks of 16, 32 or 128 columns. A warp's rows end
-// together (padded_rows is a multiple of what a warp has, or the loop's test is
-// by its first row), as its lanes work on blocks together.
+// Blocks of 16, 32 or 128 columns. A warp's rows end together (the loop's test is
+// by all of them), as its lanes work on blocks together. Two rows at a time, so
+// that one is on its way while the other is worked on.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantArgs a, int lanes) {
-  constexpr bool FOUR = FMT >= MX_MXFP4;
+__global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantArgs a, int shift) {
+  using F = Format<FMT>;
   const QuantOut& q = a.q;
   const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
-  const int64_t wide = q.pitch * (FOUR ? 2 : 1);
-  const LaneRows at(lanes);
-  const int t = (threadIdx.x & 31) % lanes;
+  const LaneRows at(shift);
+  const int64_t col = at.col, wide = q.pitch * (F::four ? 2 : 1);
+  const bool room = col < wide, first = col % F::width == 0 && col < q.cols;
+  const bool pads = FMT != MX_FP8_BLOCK && blockIdx.x == 0;
   const bool bytes = FMT == MX_FP8_BLOCK && (q.pitch % 8 != 0 || !a.vec_codes);
+  const int most = (int)min((int64_t)8, q.cols - col);
+  const bool vec = a.vec != 0 && col + 8 <= q.cols;
+  const int64_t x_step = at.step * a.x_row, code_step = at.step * q.pitch;
   int64_t row = at.row;
-  const auto load = [&](int64_t r, float2* v) {
-    load8<T>(static_cast<const T*>(a.x) + r * a.x_row, at.col, r < q.rows ? q.cols : 0, a.vec != 0, v);
-  };
-  float2 v[4], next[4];
-  load(row, v);
-  for (; __any_sync(0xffffffffu, row < a.padded_rows); row += at.step) {
-    load(row + at.step, next);      // on its way while this row is worked on
-    if (FMT != MX_FP8_BLOCK && blockIdx.x == 0 && row < a.padded_rows) put_padding(q, row, t, lanes);
-    put_block<8, FMT>(q, row, at.col, row < q.rows && at.col < wide, v, mul, bytes);
+  const T* x = static_cast<const T*>(a.x) + row * a.x_row + col;
+  unsigned char* codes = q.codes + row * q.pitch + (F::four ? col / 2 : col);
+  const auto load = [&](int64_t r, const T* p, float2* v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = next[i];
+    for (int i = 0; i < 4; ++i) v[i] = splat2(0.f);
+    if (r >= q.rows) return;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < 8 / Vec<T>::N; ++i) unpack2<T>(ld_vec(p + i * Vec<T>::N), v + i * Vec<T>::N / 2);
+    } else {
+      float* f = reinterpret_cast<float*>(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < most) f[i] = to_f(p[i]);
+    }
+  };
+  const auto put = [&](int64_t r, unsigned char* c, float2* v) {
+    const bool ok = r < q.rows;
+    put_block<8, FMT>(v, mul, ok && room ? c : nullptr,
+                      ok && first ? scale_place<FMT>(q, scale_row_part<FMT>(q, r), col / F::width) : nullptr, most, bytes);
+    if (pads && r < a.padded_rows) put_padding(q, r, (threadIdx.x & 31) & ((1 << shift) - 1), 1 << shift);
+  };
+  for (; __any_sync(0xffffffffu, row < a.padded_rows); row += 2 * at.step) {
+    float2 v[4], w[4];
+    load(row, x, v);
+    load(row + at.step, x + x_step, w);
+    put(row, codes, v);
+    if (__any_sync(0xffffffffu, row + at.step < a.padded_rows)) put(row + at.step, codes + code_step, w);
+    x += 2 * x_step;
+    codes += 2 * code_step;
   }
 }
 
@@ -323,68 +346,76 @@ __global__ void __launch_bounds__(kQuantThreads, 3) quant_transpose_kernel(const
   }
 }
 
-// Values, 8 columns a lane.
-template <typename T>
+// Values, 8 columns a lane. FMT 0: the formats with fp32 scales.
+template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q, T* y, int64_t y_row,
-                                                                bool vec, bool vec_codes, int lanes) {
-  const LaneRows at(lanes);
+                                                                bool vec, bool vec_codes, int shift) {
+  constexpr bool FOUR = FMT >= MX_MXFP4;
+  const LaneRows at(shift);
   const int64_t col = at.col;
   if (col >= q.cols) return;
-  const float mul = mul_of(q), r_mul = 1.0f / mul;
-  const bool divide = q.fmt == MX_NVFP4 && q.mul != nullptr;
-  const int64_t block = mx_block(q.fmt) ? col / mx_block(q.fmt) : 0;
+  const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f, r_mul = 1.0f / mul;
+  const int64_t block = FMT == MX_FP8_ROW ? (q.fmt == MX_FP8_ROW ? 0 : col >> 7) : col / Format<FMT>::width;
+  const int most = (int)min((int64_t)8, q.cols - col);
+  vec = vec && most == 8;
+#pragma unroll 2
   for (int64_t row = at.row; row < q.rows; row += at.step) {
-    const unsigned char* codes = q.codes + row * q.pitch;
+    const unsigned char* codes = q.codes + row * q.pitch + (FOUR ? col / 2 : col);
     float2 v[4];
-    if (mx_four(q.fmt)) {
-      const unsigned w = *reinterpret_cast<const unsigned*>(codes + col / 2);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * j)), __NV_E2M1)));
+    float s;
+    if (FMT == MX_FP8_ROW) {
+      s = static_cast<const float*>(q.scales)[row * q.blocks + block];
+    } else {
+      const unsigned b = static_cast<const unsigned char*>(q.scales)[scale_at(row, block, q.blocks)];
+      if (FMT == MX_NVFP4)
+        s = __half2float(__half(__nv_cvt_fp8_to_halfraw((unsigned char)b, __NV_E4M3)));
+      else
+        s = b == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 1u << 22);
+    }
+    if (FOUR) {
+      fp4_values(*reinterpret_cast<const unsigned*>(codes), v);
     } else {
       unsigned w[2] = {0, 0};
       if (vec_codes) {
-        const uint2 u = *reinterpret_cast<const uint2*>(codes + col);
+        const uint2 u = *reinterpret_cast<const uint2*>(codes);
         w[0] = u.x;
         w[1] = u.y;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (col + j < q.pitch) w[j / 4] |= (unsigned)codes[col + j] << (8 * (j % 4));
+          if (j < most) w[j / 4] |= (unsigned)codes[j] << (8 * (j % 4));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         v[j] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j / 2] >> (16 * (j % 2))), __NV_E4M3)));
     }
-    float s;
-    if (!mx_tiled(q.fmt)) {
-      s = static_cast<const float*>(q.scales)[row * q.blocks + block];
-    } else {
-      const unsigned b = static_cast<const unsigned char*>(q.scales)[scale_at(row, block, q.blocks)];
-      if (q.fmt == MX_NVFP4)
-        s = __half2float(__half(__nv_cvt_fp8_to_halfraw((unsigned char)b, __NV_E4M3)));
-      else
-        s = b == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 1u << 22);
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = mul2(v[j], splat2(s));
-      if (divide) {
-        const float2 d = quotient2(v[j], mul, r_mul);
-        // past the largest fp32 number the correction would be inf - inf
-        v[j] = make_float2(fabsf(v[j].x * r_mul) <= 0x1.fp127f ? d.x : v[j].x / mul,
-                           fabsf(v[j].y * r_mul) <= 0x1.fp127f ? d.y : v[j].y / mul);
+    for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], splat2(s));
+    if (FMT == MX_NVFP4 && q.mul != nullptr) {
+      float2 d[4];
+      float all = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = quotient2(v[j], mul, r_mul);
+        all += d[j].x + d[j].y;
+      }
+      if (all != all || isinf(all)) {     // past the largest number the correction is inf - inf
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x / mul, v[j].y / mul);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = d[j];
       }
     }
     T* out = y + row * y_row + col;
-    if (vec && col + 8 <= q.cols) {
+    if (vec) {
 #pragma unroll
       for (int j = 0; j < 8 / Vec<T>::N; ++j) st_vec(out + j * Vec<T>::N, pack2<T>(v + j * Vec<T>::N / 2));
     } else {
       const float* f = reinterpret_cast<const float*>(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (col + j < q.cols) out[j] = from_f<T>(f[j]);
+        if (j < most) out[j] = from_f<T>(f[j]);
     }
   }
 }
