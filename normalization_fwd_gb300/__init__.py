@@ -250,7 +250,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(_get_device()) or None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream or None
     return int(stream) or None
@@ -1109,6 +1109,7 @@ def mx_matrix_bytes(format, rows, cols) -> tuple[int, int]:
 @functools.lru_cache(maxsize=4096)
 def _quantized_layout(fmt, rows, cols):
     """(shape and type of the codes, of the scales, bytes of either)."""
+    rows, cols = int(rows), int(cols)
     e4m3 = torch.float8_e4m3fn
     bytes_of = mx_matrix_bytes(fmt, rows, cols)
     if fmt in ("fp8_row", "fp8_block"):
@@ -1123,44 +1124,26 @@ def _quantized_layout(fmt, rows, cols):
 
 def quantized_empty(rows, cols, format, *, mul=None, device="cuda") -> Quantized:
     """A matrix with room for codes and scales, not initialised."""
-    _format(format)
-    cshape, ctype, sshape, stype, _ = _quantized_layout(format, int(rows), int(cols))
+    cshape, ctype, sshape, stype, _ = _quantized_layout(format, rows, cols)
     return Quantized(torch.empty(cshape, dtype=ctype, device=device),
-                     torch.empty(sshape, dtype=stype, device=device), format, int(rows), int(cols),
-                     mul)
+                     torch.empty(sshape, dtype=stype, device=device), format, rows, cols, mul)
 
 
 def _matrix(where, q):
     """The packed mx_matrix struct of ``q``."""
-    if not isinstance(q, Quantized):
-        raise TypeError(f"{where}: expected a Quantized, got {type(q).__name__}")
-    code = _format(q.format)
-    need = _quantized_layout(q.format, q.rows, q.cols)[4]
-    for t, name, n in ((q.codes, "codes", need[0]), (q.scales, "scales", need[1])):
-        if t.numel() * t.element_size() != n or not t.is_contiguous():
-            raise ValueError(f"{where}: the {name} of {q.rows} x {q.cols} {q.format} must be "
-                             f"contiguous, of {n} bytes")
-    mul = q.mul if q.format == "nvfp4" else None
-    if mul is not None and (mul.numel() != 1 or mul.dtype != torch.float32):
+    codes, scales, format, rows, cols, mul = q
+    need = _quantized_layout(format, rows, cols)[4]
+    if (codes.nbytes != need[0] or scales.nbytes != need[1] or not codes.is_contiguous()
+            or not scales.is_contiguous()):
+        raise ValueError(f"{where}: codes and scales of {rows} x {cols} {format} must be "
+                         f"contiguous, of {need[0]} and {need[1]} bytes")
+    if mul is None or format != "nvfp4":
+        return _MX_MATRIX.pack(codes.data_ptr(), scales.data_ptr(), 0, _FORMAT_CODES[format], rows,
+                               cols)
+    if mul.numel() != 1 or mul.dtype != torch.float32:
         raise ValueError(f"{where}: mul must be one float32")
-    return _MX_MATRIX.pack(q.codes.data_ptr(), q.scales.data_ptr(),
-                           0 if mul is None else mul.data_ptr(), code, q.rows, q.cols)
-
-
-def _vector(where, name, t, n, dtype):
-    if t is None:
-        return None
-    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be a contiguous [{n}] of {dtype}")
-    return t.data_ptr()
-
-
-def _whole(where, name, t, ref):
-    if t is None:
-        return None
-    if t.shape != ref.shape or t.dtype != ref.dtype or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be contiguous, of the shape and dtype of x")
-    return t.data_ptr() or None
+    return _MX_MATRIX.pack(codes.data_ptr(), scales.data_ptr(), mul.data_ptr(), MX_NVFP4, rows,
+                           cols)
 
 
 def mx_norm_fwd(x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma, out_sum, y, mean,
@@ -1174,31 +1157,58 @@ def mx_norm_fwd(x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma, 
         with _current(device, stream):
             return mx_norm_fwd(x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma,
                                out_sum, y, mean, rstd, q)
-    where = "mx_norm_fwd"
-    lib = _lib or load_library()
     rows, hidden = _shape(x)
     if (q.rows, q.cols) != (rows, hidden):
-        raise ValueError(f"{where}: q must be {rows} x {hidden}, is {q.rows} x {q.cols}")
+        raise ValueError(f"mx_norm_fwd: q must be {rows} x {hidden}, is {q.rows} x {q.cols}")
+    for n, t in (("out_sum", out_sum), ("y", y)):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or not t.is_contiguous()):
+            raise ValueError(f"mx_norm_fwd: {n} must be contiguous, of the shape and dtype of x")
+    for n, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None and (t.shape != (rows,) or t.dtype != torch.float32
+                              or not t.is_contiguous()):
+            raise ValueError(f"mx_norm_fwd: {n} must be a contiguous float32 [{rows}]")
+    _mx_norm_fwd(device, x, bias, residual, gamma, beta, eps, _mode(mode), zero_centered_gamma,
+                 out_sum, y, mean, rstd, q)
+
+
+def _mx_norm_fwd(device, x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma, out_sum,
+                 y, mean, rstd, q):
+    """The call itself; outputs and q's shape are as they should be."""
+    lib = _lib or load_library()
+    dt = _dtype(x)
     if not x.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    stats = [_vector(where, n, t, rows, torch.float32) for n, t in (("mean", mean), ("rstd", rstd))]
+        raise ValueError("mx_norm_fwd: x must be contiguous")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
+                                 or not residual.is_contiguous()):
+        raise ValueError("mx_norm_fwd: residual must be contiguous, of the shape and dtype of x")
+    n = q.cols
+    for name, t in (("gamma", gamma), ("beta", beta), ("bias", bias)):
+        if t is not None and (t.numel() != n or t.dtype != x.dtype or not t.is_contiguous()):
+            raise ValueError(f"mx_norm_fwd: {name} must be a contiguous [{n}] of {x.dtype}")
     st = lib.mx_norm_fwd(
-        x.data_ptr() or None, _vector(where, "bias", bias, hidden, x.dtype),
-        _whole(where, "residual", residual, x), _vector(where, "gamma", gamma, hidden, x.dtype),
-        _vector(where, "beta", beta, hidden, x.dtype), eps, _mode(mode),
-        1 if zero_centered_gamma else 0, _whole(where, "out_sum", out_sum, x),
-        _whole(where, "y", y, x), *stats, _matrix(where, q), _raw_stream(device) or None, _dtype(x))
+        x.data_ptr() or None, None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr() or None,
+        None if gamma is None else gamma.data_ptr(), None if beta is None else beta.data_ptr(),
+        eps, mode, 1 if zero_centered_gamma else 0,
+        None if out_sum is None else out_sum.data_ptr() or None,
+        None if y is None else y.data_ptr() or None,
+        None if mean is None else mean.data_ptr() or None,
+        None if rstd is None else rstd.data_ptr() or None, _matrix("mx_norm_fwd", q),
+        _raw_stream(device) or None, dt)
     if st:
-        raise NormError(st, where)
+        raise NormError(st, "mx_norm_fwd")
 
 
 def _plane(where, name, t, shape=None, dtype=None):
     """Row stride of a matrix [rows, cols] whose columns are contiguous."""
-    if t.dim() != 2 or (shape is not None and t.shape != shape) or (dtype and t.dtype != dtype):
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape) or (dtype and t.dtype != dtype):
         raise ValueError(f"{where}: {name} must be "
                          + (f"{list(shape)} of {dtype}" if shape is not None else "a matrix"))
-    _dense_last(t, f"{where}: {name}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    row, col = t.stride()
+    if col != 1 and size[1] > 1:
+        raise ValueError(f"{where}: {name}: the last dimension must be contiguous")
+    return row if size[0] > 1 else size[1]
 
 
 def mx_quantize(x, q, *, transpose=False, stream=None) -> None:
@@ -1208,10 +1218,12 @@ def mx_quantize(x, q, *, transpose=False, stream=None) -> None:
     if _elsewhere(device, stream):
         with _current(device, stream):
             return mx_quantize(x, q, transpose=transpose)
+    _mx_quantize(device, x, q, transpose)
+
+
+def _mx_quantize(device, x, q, transpose):
     lib = _lib or load_library()
-    row = _plane("mx_quantize", "x", x)
-    if (tuple(x.shape[::-1]) if transpose else tuple(x.shape)) != (q.rows, q.cols):
-        raise ValueError(f"mx_quantize: x of {list(x.shape)} into {q.rows} x {q.cols}")
+    row = _plane("mx_quantize", "x", x, (q.cols, q.rows) if transpose else (q.rows, q.cols), x.dtype)
     st = lib.mx_quantize(x.data_ptr() or None, row, 1 if transpose else 0,
                          _matrix("mx_quantize", q), _raw_stream(device) or None, _dtype(x))
     if st:
@@ -1224,10 +1236,14 @@ def mx_dequantize(q, y, stream=None) -> None:
     if _elsewhere(device, stream):
         with _current(device, stream):
             return mx_dequantize(q, y)
+    _mx_dequantize(device, q, y)
+
+
+def _mx_dequantize(device, q, y):
     lib = _lib or load_library()
     row = _plane("mx_dequantize", "y", y, (q.rows, q.cols), y.dtype)
-    st = lib.mx_dequantize(_matrix("mx_dequantize", q), y.data_ptr() or None, max(row, q.cols)
-                           if q.rows <= 1 else row, _raw_stream(device) or None, _dtype(y))
+    st = lib.mx_dequantize(_matrix("mx_dequantize", q), y.data_ptr() or None, row,
+                           _raw_stream(device) or None, _dtype(y))
     if st:
         raise NormError(st, "mx_dequantize")
 
@@ -1242,22 +1258,30 @@ def mx_product(a, b, alpha, bias, residual, out, psum, psq, stream=None) -> None
     if _elsewhere(device, stream):
         with _current(device, stream):
             return mx_product(a, b, alpha, bias, residual, out, psum, psq)
-    where = "mx_product"
+    _mx_product(device, a, b, alpha, bias, residual, out, psum, psq)
+
+
+def _mx_product(device, a, b, alpha, bias, residual, out, psum, psq):
     lib = _lib or load_library()
-    shape = (a.rows, b.rows)
-    row = _plane(where, "out", out, shape, out.dtype)
-    res_row = row if residual is None else _plane(where, "residual", residual, shape, out.dtype)
+    where, rows, cols, dtype = "mx_product", a.rows, b.rows, out.dtype
+    shape = (rows, cols)
+    row = _plane(where, "out", out, shape, dtype)
+    res_row = row if residual is None else _plane(where, "residual", residual, shape, dtype)
+    if bias is not None and (bias.numel() != cols or bias.dtype != dtype
+                             or not bias.is_contiguous()):
+        raise ValueError(f"{where}: bias must be a contiguous [{cols}] of {dtype}")
     for t in (psum, psq):
-        if t is not None and (t.shape != (a.rows, -(-b.rows // 128)) or t.dtype != torch.float32
+        if t is not None and (t.shape != (rows, -(-cols // 128)) or t.dtype != torch.float32
                               or not t.is_contiguous()):
             raise ValueError(f"{where}: psum and psq must be contiguous float32 "
-                             f"[{a.rows}, {-(-b.rows // 128)}]")
+                             f"[{rows}, {-(-cols // 128)}]")
     st = lib.mx_product(_matrix(where, a), _matrix(where, b), alpha,
-                        _vector(where, "bias", bias, b.rows, out.dtype),
+                        None if bias is None else bias.data_ptr() or None,
                         None if residual is None else residual.data_ptr() or None, res_row,
-                        out.data_ptr() or None, row, None if psum is None else psum.data_ptr() or None,
-                        None if psq is None else psq.data_ptr() or None, _raw_stream(device) or None,
-                        _dtype(out))
+                        out.data_ptr() or None, row,
+                        None if psum is None else psum.data_ptr() or None,
+                        None if psq is None else psq.data_ptr() or None,
+                        _raw_stream(device) or None, _dtype(out))
     if st:
         raise NormError(st, where)
 
@@ -1284,14 +1308,15 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
     rows, hidden = _shape(x)
     if store_sum is None:
         store_sum = bias is not None or residual is not None
-    rms = _mode(mode) == LN_RMSNORM
-    q = quantized_empty(rows, hidden, format, mul=mul, device=x.device)
+    mode = _mode(mode)
+    rms = mode == LN_RMSNORM
+    q = quantized_empty(rows, hidden, format, mul=mul, device=device)
     out_sum = torch.empty_like(x) if store_sum else None
     y = torch.empty_like(x) if store_y else None
-    mean = None if rms else torch.empty(rows, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    mx_norm_fwd(x, bias, residual, gamma, None if rms else beta, eps, mode, zero_centered_gamma,
-                out_sum, y, mean, rstd, q)
+    mean = None if rms else torch.empty(rows, dtype=torch.float32, device=device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    _mx_norm_fwd(device, x, bias, residual, gamma, None if rms else beta, eps, mode,
+                 zero_centered_gamma, out_sum, y, mean, rstd, q)
     return {"q": q, "sum": out_sum, "y": y, "mean": mean, "rstd": rstd}
 
 
@@ -1305,8 +1330,8 @@ def quantize(x, format, *, mul=None, transpose=False, stream=None) -> Quantized:
     if x.dim() != 2:
         raise ValueError("quantize: x must be a matrix")
     rows, cols = x.shape[::-1] if transpose else x.shape
-    q = quantized_empty(rows, cols, format, mul=mul, device=x.device)
-    mx_quantize(x, q, transpose=transpose)
+    q = quantized_empty(rows, cols, format, mul=mul, device=device)
+    _mx_quantize(device, x, q, transpose)
     return q
 
 
@@ -1317,8 +1342,8 @@ def dequantize(q, dtype=torch.float32, *, out=None, stream=None):
         with _current(device, stream):
             return dequantize(q, dtype, out=out)
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    mx_dequantize(q, out)
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=device)
+    _mx_dequantize(device, q, out)
     return out
 
 
@@ -1335,16 +1360,18 @@ def scaled_product(a, b, *, alpha=1.0, bias=None, residual=None, dtype=torch.bfl
     quantise the output's gradient and the weights (transpose=True) for the
     input's, both operands transposed for the weights'.
     """
-    device = _device_of("scaled_product", a.codes, a.scales, b.codes, b.scales, bias, residual, out)
+    device = _device_of("scaled_product", a.codes, a.scales, a.mul, b.codes, b.scales, b.mul, bias,
+                        residual, out)
     if _elsewhere(device, stream):
         with _current(device, stream):
             return scaled_product(a, b, alpha=alpha, bias=bias, residual=residual, dtype=dtype,
                                   out=out, partials=partials)
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=device)
     psum = psq = None
     if partials:
-        psum, psq = torch.empty((2, a.rows, -(-b.rows // 128)), dtype=torch.float32,
-                                device=a.codes.device)
-    mx_product(a, b, alpha, bias, residual, out, psum, psq)
+        shape = (a.rows, -(-b.rows // 128))
+        psum = torch.empty(shape, dtype=torch.float32, device=device)
+        psq = torch.empty(shape, dtype=torch.float32, device=device)
+    _mx_product(device, a, b, alpha, bias, residual, out, psum, psq)
     return {"out": out, "psum": psum, "psq": psq, "tile_cols": 128}

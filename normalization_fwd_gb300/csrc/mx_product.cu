@@ -4,6 +4,8 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
+#include <vector>
 
 #include "../../include/normfuse.h"
 #include "launch.h"
@@ -61,6 +63,33 @@ cudaError_t scales_map(Encode encode, const QuantOut& q, int tiles, int row_tile
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Whether the device places clusters of `cfg`'s shape; asked once for a kernel,
+// a device and a size.
+cudaError_t places(const void* fn, const cudaLaunchConfig_t& cfg, int splits, bool* yes) {
+  struct Entry {
+    const void* fn;
+    int device, splits;
+    bool yes;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> kept;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Entry& k : kept)
+    if (k.fn == fn && k.device == dev && k.splits == splits) {
+      *yes = k.yes;
+      return cudaSuccess;
+    }
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+  if (e != cudaSuccess) return e;
+  *yes = n > 0;
+  kept.push_back({fn, dev, splits, *yes});
+  return cudaSuccess;
+}
+
 constexpr uint32_t kSmemTarget = 200 * 1024;
 constexpr uint32_t kPairSmem = 225 * 1024;   // with 1 KB for alignment and the barriers: 226.2 of 227
 
@@ -102,10 +131,10 @@ cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
     cfg.gridDim = dim3((unsigned)(tiles * p.splits));
     attr[0].val.clusterDim.x = p.splits;
     cfg.numAttrs = p.splits > 1 ? 1 : 0;
-    int n = 1;
-    if (p.splits > 1) e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    bool yes = true;
+    if (p.splits > 1) e = places(fn, cfg, p.splits, &yes);
     if (e != cudaSuccess) return e;
-    if (n > 0) break;
+    if (yes) break;
   }
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
   return cudaLaunchKernelExC(&cfg, fn, args);
