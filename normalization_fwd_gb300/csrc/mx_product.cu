@@ -255,7 +255,7 @@ ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const 
   p.psum = psum;
   p.psq = psq;
   const auto vec = [&](const void* t, int64_t row) { return aligned(t, 16) && (M == 1 || row * es % 16 == 0); };
-  p.vec = vec(out, out_row) && (residual == nullptr || vec(residual, residual_row));
+  p.vec = vec(out, out_row) && (residual == nullptr || vec(residual, residual_row)) && aligned(bias, 16);
   e = by_dtype(dtype, [&](auto t) { return launch_product<decltype(t)>(p, sms, stream); });
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }

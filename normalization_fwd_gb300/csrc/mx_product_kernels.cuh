@@ -45,7 +45,7 @@ struct ProductArgs {
   int chunks;            // of K
   int steps;             // instructions along all of K
   int stages;
-  int vec;               // out and residual can be accessed 16 bytes at a time
+  int vec;               // out, residual and bias can be accessed 16 bytes at a time
   uint32_t idesc;
   int tiles_m, tiles_n;  // pairs of CTAs: tiles of 256 rows of A, of 128 or 256 of B
 };
@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // take one tile after another. A step of the pair reads 128 rows of A and WN / 2
 // of B from each CTA's shared memory, so that a chunk costs half the copies a
 // result of two single tiles. Warps: 0 copies, 1 issues (in the first CTA of the
-// pair), 2 has the tensor memory, 4 to 11 finish results. WN = 256: the results
+// pair) and has the tensor memory, 4 to 11 finish results. WN = 256: the results
 // fill one half of tensor memory, the eight warps take 128 columns a thread into
 // registers and hand it back at once; WN = 128: two buffers, four warps each.
-constexpr int kPairThreads = 384;
+constexpr int kPairThreads = 384;   // 168 registers a thread, of which 128 hold results
 
 template <int FMT> __host__ __device__ constexpr uint32_t pair_stage_bytes(int wn) {
   return (uint32_t)(128 + wn / 2) * kChunkBytes + (uint32_t)(1 + wn / 128) * chunk_tiles<FMT>() * 512u;
@@ -308,7 +308,7 @@ __device__ __forceinline__ void pair_tile(const ProductArgs& p, int t, int* tm, 
   *tm = g * 8 + rest - *tn * rows;
 }
 
-// A warp's 32 rows by 128 columns of results, a row a lane in `v`. A lane scales,
+// A warp's 32 rows by 128 columns of results, a row a lane. A lane scales,
 // rounds and sums its own row; 64 bytes of each row at a time change places
 // through shared memory, so that rows of the residual and the output are read
 // and written in runs of 64 bytes (straight from a row a lane, 4099 x 1165 x 1280,
@@ -316,101 +316,203 @@ __device__ __forceinline__ void pair_tile(const ProductArgs& p, int t, int* tm, 
 constexpr int kPiecePitch = 80;      // bytes: 16-byte accesses of 8 rows meet no bank twice
 constexpr int kPieceBytes = 32 * kPiecePitch;
 
-// Row r, 16-byte part c of a piece whose first column is n: `live` of its
-// values are there.
-template <typename T>
-__device__ __forceinline__ uint4 piece_load(const T* row, int live, bool vec) {
-  constexpr int N = Vec<T>::N;
-  if (vec && live == N) return *reinterpret_cast<const uint4*>(row);
-  T t[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) t[i] = i < live ? row[i] : from_f<T>(0.f);
-  return *reinterpret_cast<const uint4*>(t);
+// The output is not read again by this kernel, the residual not twice: their
+// lines make way in the L2 cache for those of the operands first. Volatile, so
+// that the loads of later pieces are not moved ahead of the ones before and need
+// registers all at once.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
 }
-
-template <typename T, bool RES, bool SUMS>
-__device__ __forceinline__ void finish_pieces(const ProductArgs& p, int64_t m0, int64_t n0, uint32_t* v,
-                                              float f, uint32_t piece) {
+__device__ __forceinline__ uint4 ld_bias(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+// Tiles of 32 rows and 128 columns that can be accessed 16 bytes at a time, so
+// that nothing is asked along the way. `load` waits for the results and takes
+// them into registers; false: they did not come. The residual's first piece is
+// on its way before.
+template <typename T, bool RES, bool SUMS, typename Load>
+__device__ __forceinline__ bool finish_full(const ProductArgs& p, int64_t m0, int64_t n0, float f,
+                                            unsigned char* piece, Load load) {
   constexpr int N = Vec<T>::N, kCols = 4 * N, kPieces = 128 / kCols;
-  const int lane = threadIdx.x & 31, part = lane & 3;
-  const int rows = (int)min((int64_t)32, p.a.rows - m0), width = (int)min((int64_t)128, p.b.rows - n0);
-  const uint32_t own = piece + lane * kPiecePitch, other = piece + (lane >> 2) * kPiecePitch + part * 16;
-  const T* res = static_cast<const T*>(p.residual) + m0 * p.residual_row + n0;
-  T* out = static_cast<T*>(p.out) + m0 * p.out_row + n0;
+  const int lane = threadIdx.x & 31, part = lane & 3, row = lane >> 2;
+  uint4* own = reinterpret_cast<uint4*>(piece + lane * kPiecePitch);
+  uint4* other = reinterpret_cast<uint4*>(piece + row * kPiecePitch + part * 16);
+  constexpr int kStep = 8 * kPiecePitch / 16;
+  const int64_t res_step = 8 * p.residual_row, out_step = 8 * p.out_row;
+  const T* res = static_cast<const T*>(p.residual) + (m0 + row) * p.residual_row + n0 + part * N;
+  T* out = static_cast<T*>(p.out) + (m0 + row) * p.out_row + n0 + part * N;
   const T* bias = p.bias ? static_cast<const T*>(p.bias) + n0 : nullptr;
-  float sum = 0.f;
+  float sum = 0.f, m2 = 0.f;          // of the columns so far
+  uint4 next[4];
+  const auto fetch = [&](int col) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) next[i] = ld_stream(res + i * res_step + col);
+  };
+  if (RES) fetch(0);
+  uint32_t v[128];
+  if (!load(v)) return false;
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
     const int col = j * kCols;
-    if (col >= width) break;
     if (RES) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        uint4 t = make_uint4(0, 0, 0, 0);
-        if (r < rows) t = piece_load(res + r * p.residual_row + col + part * N, width - col - part * N, p.vec);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(other + 8 * i * kPiecePitch), "r"(t.x), "r"(t.y), "r"(t.z), "r"(t.w) : "memory");
-      }
+      for (int i = 0; i < 4; ++i) other[i * kStep] = next[i];
       __syncwarp();
     }
+    uint4 mine[4];
+    float2 s2 = splat2(0.f);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      float o[N];
+      const int at = col + c * N;
+      float2 o[N / 2];
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = __uint_as_float(v[col + c * N + i]) * f;
+      for (int i = 0; i < N / 2; ++i)
+        o[i] = mul2(make_float2(__uint_as_float(v[at + 2 * i]), __uint_as_float(v[at + 2 * i + 1])), splat2(f));
       if (bias) {
+        float2 b[N / 2];
+        unpack2<T>(ld_bias(bias + at), b);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (col + c * N + i < width) o[i] += to_f(bias[col + c * N + i]);
+        for (int i = 0; i < N / 2; ++i) o[i] = add2(o[i], b[i]);
       }
       if (RES) {
-        float r[N];
-        unpack<T>(lds_u4(own + c * 16), r);
+        float2 r[N / 2];
+        unpack2<T>(own[c], r);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] += r[i];
+        for (int i = 0; i < N / 2; ++i) o[i] = add2(o[i], r[i]);
       }
-      const uint4 t = pack<T>(o);
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(own + c * 16), "r"(t.x), "r"(t.y), "r"(t.z), "r"(t.w) : "memory");
+      mine[c] = pack2<T>(o);
+      own[c] = mine[c];
       if (SUMS) {
-        unpack<T>(t, o);
+        unpack2<T>(mine[c], o);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (col + c * N + i < width) sum += o[i];
-          v[col + c * N + i] = __float_as_uint(o[i]);
-        }
+        for (int i = 0; i < N / 2; ++i) s2 = add2(s2, o[i]);
       }
     }
+    if (RES && j + 1 < kPieces) fetch(col + kCols);     // into registers that are free now
     __syncwarp();
+    uint4 t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), live = width - col - part * N;
-      const uint4 t = lds_u4(other + 8 * i * kPiecePitch);
-      if (r < rows) {
-        T* to = out + r * p.out_row + col + part * N;
-        if (p.vec && live >= N) {
-          st_vec(to, t);
-        } else {
-          const T* e = reinterpret_cast<const T*>(&t);
+    for (int i = 0; i < 4; ++i) t[i] = other[i * kStep];
 #pragma unroll
-          for (int k = 0; k < N; ++k)
-            if (k < live) to[k] = e[k];
+    for (int i = 0; i < 4; ++i) __stcs(reinterpret_cast<uint4*>(out + i * out_step + col), t[i]);
+    if (SUMS) {
+      // the piece's sum and squares about its own mean, joined to those before
+      // (the parallel-variance identity)
+      const float s = s2.x + s2.y, mean = s * (1.0f / kCols);
+      float2 q = splat2(0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float2 o[N / 2];
+        unpack2<T>(mine[c], o);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          const float2 d = add2(o[i], splat2(-mean));
+          q = fma2(d, d, q);
         }
       }
+      m2 += q.x + q.y;
+      if (j > 0) {
+        const float d = mean - sum / (float)col;
+        m2 = fmaf(d * d, (float)col * kCols / (float)(col + kCols), m2);
+      }
+      sum += s;
     }
     __syncwarp();
   }
-  if (SUMS && lane < rows) {
-    const float mean = sum / (float)width;
-    float q = 0.f;
-#pragma unroll
-    for (int j = 0; j < 128; ++j) {
-      const float d = j < width ? __uint_as_float(v[j]) - mean : 0.f;
-      q = fmaf(d, d, q);
-    }
+  if (SUMS) {
     const int64_t at = (m0 + lane) * ((p.b.rows + 127) / 128) + n0 / 128;
     p.psum[at] = sum;
-    p.psq[at] = q;
+    p.psq[at] = m2;
   }
+  return true;
+}
+
+// Any other tile (rows or columns that the matrix does not have, rows that start
+// anywhere), 16 columns at a time as fp32 in shared memory: 16 lanes a row for
+// what is read and written.
+template <typename T, typename Load>
+__device__ __forceinline__ bool finish_ragged(const ProductArgs& p, int64_t m0, int64_t n0, float f,
+                                              unsigned char* piece, Load load) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  const int rows = (int)max((int64_t)0, min((int64_t)32, p.a.rows - m0));
+  const int width = (int)max((int64_t)0, min((int64_t)128, p.b.rows - n0));
+  float4* own = reinterpret_cast<float4*>(piece + lane * kPiecePitch);
+  float* there = reinterpret_cast<float*>(piece) + (lane >> 4) * (kPiecePitch / 4) + c;
+  const T* res = p.residual ? static_cast<const T*>(p.residual) + (m0 + (lane >> 4)) * p.residual_row + n0 + c : nullptr;
+  T* out = static_cast<T*>(p.out) + (m0 + (lane >> 4)) * p.out_row + n0 + c;
+  float sum = 0.f, m2 = 0.f;
+  uint32_t v[128];
+  if (!load(v)) return false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int col = 16 * j;
+    if (rows == 0 || col >= width) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      own[i] = make_float4(__uint_as_float(v[col + 4 * i]) * f, __uint_as_float(v[col + 4 * i + 1]) * f,
+                           __uint_as_float(v[col + 4 * i + 2]) * f, __uint_as_float(v[col + 4 * i + 3]) * f);
+    __syncwarp();
+    const bool here = col + c < width;
+    const float b = p.bias && here ? to_f(static_cast<const T*>(p.bias)[n0 + col + c]) : 0.f;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      float* x = there + 2 * i * (kPiecePitch / 4);
+      T o = from_f<T>(0.f);
+      if (here && 2 * i + (lane >> 4) < rows) {
+        float y = *x + b;
+        if (res) y += to_f(res[2 * i * p.residual_row + col]);
+        o = from_f<T>(y);
+        out[2 * i * p.out_row + col] = o;
+      }
+      if (p.psum) *x = to_f(o);
+    }
+    __syncwarp();
+    if (p.psum) {
+      const int cnt = min(16, width - col);
+      float s = 0.f, q = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += (own[i].x + own[i].y) + (own[i].z + own[i].w);   // 0 behind the last column
+      const float mean = s / (float)cnt;
+      for (int i = 0; i < cnt; ++i) {
+        const float d = reinterpret_cast<const float*>(own)[i] - mean;
+        q = fmaf(d, d, q);
+      }
+      m2 += q;
+      if (j > 0) {
+        const float d = mean - sum / (float)col;
+        m2 = fmaf(d * d, (float)col * (float)cnt / (float)(col + cnt), m2);
+      }
+      sum += s;
+    }
+    __syncwarp();
+  }
+  if (p.psum && lane < rows && width > 0) {
+    const int64_t at = (m0 + lane) * ((p.b.rows + 127) / 128) + n0 / 128;
+    p.psum[at] = sum;
+    p.psq[at] = m2;
+  }
+  return true;
+}
+
+// The lines of a warp's rows of the residual, on their way to the L2 cache while
+// the tile's results are still being worked out.
+template <typename T>
+__device__ __forceinline__ void prefetch_residual(const ProductArgs& p, int64_t m0, int64_t n0) {
+  const int64_t m = m0 + (threadIdx.x & 31);
+  if (m >= p.a.rows || n0 >= p.b.rows) return;
+  const char* at = reinterpret_cast<const char*>(static_cast<const T*>(p.residual) + m * p.residual_row + n0);
+  const int bytes = (int)min((int64_t)128, p.b.rows - n0) * (int)sizeof(T);
+  for (int b = 0; b < bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + b));
 }
 
 template <typename T, int FMT, int WN>
@@ -432,7 +534,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = p.tiles_m * p.tiles_n;
 
-  if (warp == 2) tmem_alloc_pair<kTmemCols>(&tmem_at);
+  if (warp == 1) tmem_alloc_pair<kTmemCols>(&tmem_at);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 1);
@@ -483,8 +585,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
     if (!ok && lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
-    // What is in flight has landed when the first CTA's barriers say so, which
-    // its issuing warp waits for; after a wait that gave up, for a second more.
+    // Copies in flight and arrivals from the other CTA land before this one ends:
+    // a stage that is free again has had both. After a wait that gave up, the
+    // first CTA waits a second more for what it asked for.
+    for (int k = max(0, i - p.stages); k < i && ok; ++k)
+      ok = mbar_wait_cluster(&empty[k % p.stages], (k / p.stages) & 1);
     if (!ok && rank == 0)
       for (int k = max(0, i - p.stages); k < i; ++k) mbar_wait_cluster(&full[k % p.stages], (k / p.stages) & 1);
   } else if (warp == 1 && rank == 0) {
@@ -532,42 +637,43 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       __syncwarp();
     }
     if (!ok && lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
-    // all that was issued is done before tensor memory goes back
+    // all that was issued is done before tensor memory goes back, and the other
+    // CTA's arrivals have come before this one ends
     for (int e = max(0, i - p.stages); e < i; ++e) mbar_wait_cluster(&empty[e % p.stages], (e / p.stages) & 1);
+    for (int e = max(0, n - kBufs); e < n && ok; ++e) mbar_wait_cluster(&drained[e % kBufs], (e / kBufs) & 1);
   } else if (warp >= 4) {
     const int quarter = warp & 3, group = (warp - 4) >> 2;
     const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
-    const uint32_t piece = base + p.stages * kStage + (warp - 4) * kPieceBytes;
+    unsigned char* piece = smem_raw + (base - smem_addr(smem_raw)) + p.stages * kStage + (warp - 4) * kPieceBytes;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
       const int buf = n % kBufs;
       if (WN == 128 && buf != group) continue;
       int tm, tn;
       pair_tile(p, t, &tm, &tn);
-      const bool ok = mbar_wait_cluster(&ready[buf], (n / kBufs) & 1);
-      if (!__all_sync(0xffffffffu, ok)) {
+      const int col = WN == 256 ? group * 128 : 0;
+      const int64_t m0 = (int64_t)tm * 256 + rank * 128 + quarter * 32, n0 = (int64_t)tn * WN + col;
+      if (p.residual) prefetch_residual<T>(p, m0, n0);
+      const auto load = [&](uint32_t* v) {
+        const bool here = __all_sync(0xffffffffu, mbar_wait_cluster(&ready[buf], (n / kBufs) & 1));
+        if (!here) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_load32(tmem + ((uint32_t)quarter << 21) + buf * WN + col + 32 * j, v + 32 * j);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&drained[buf]), 0));
+        return true;
+      };
+      bool ok;
+      if (!p.vec || m0 + 32 > p.a.rows || n0 + 128 > p.b.rows) ok = finish_ragged<T>(p, m0, n0, f, piece, load);
+      else if (p.psum && p.residual) ok = finish_full<T, true, true>(p, m0, n0, f, piece, load);
+      else if (p.psum) ok = finish_full<T, false, true>(p, m0, n0, f, piece, load);
+      else if (p.residual) ok = finish_full<T, true, false>(p, m0, n0, f, piece, load);
+      else ok = finish_full<T, false, false>(p, m0, n0, f, piece, load);
+      if (!ok) {
         if (lane == 0) atomicOr(&g_tu_error, kErrWaitTimeout);
         break;
-      }
-      tc_fence_after();
-      uint32_t v[128];
-      const int col = WN == 256 ? group * 128 : 0;
-      const uint32_t at = tmem + ((uint32_t)quarter << 21) + buf * WN + col;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_load32(at + 32 * j, v + 32 * j);
-      tmem_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&drained[buf]), 0));
-      const int64_t m0 = (int64_t)tm * 256 + rank * 128 + quarter * 32, n0 = (int64_t)tn * WN + col;
-      if (m0 < p.a.rows && n0 < p.b.rows) {
-        if (p.psum) {
-          if (p.residual) finish_pieces<T, true, true>(p, m0, n0, v, f, piece);
-          else finish_pieces<T, false, true>(p, m0, n0, v, f, piece);
-        } else {
-          if (p.residual) finish_pieces<T, true, false>(p, m0, n0, v, f, piece);
-          else finish_pieces<T, false, false>(p, m0, n0, v, f, piece);
-        }
       }
     }
   }
@@ -575,7 +681,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 2) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_free_pair<kTmemCols>(tmem);
   }
