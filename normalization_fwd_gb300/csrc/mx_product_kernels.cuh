@@ -450,6 +450,7 @@ __device__ __forceinline__ bool finish_ragged(const ProductArgs& p, int64_t m0, 
   float* there = reinterpret_cast<float*>(piece) + (lane >> 4) * (kPiecePitch / 4) + c;
   const T* res = p.residual ? static_cast<const T*>(p.residual) + (m0 + (lane >> 4)) * p.residual_row + n0 + c : nullptr;
   T* out = static_cast<T*>(p.out) + (m0 + (lane >> 4)) * p.out_row + n0 + c;
+  const int64_t res_step = 2 * p.residual_row, out_step = 2 * p.out_row;
   float sum = 0.f, m2 = 0.f;
   uint32_t v[128];
   if (!load(v)) return false;
@@ -462,17 +463,18 @@ __device__ __forceinline__ bool finish_ragged(const ProductArgs& p, int64_t m0, 
       own[i] = make_float4(__uint_as_float(v[col + 4 * i]) * f, __uint_as_float(v[col + 4 * i + 1]) * f,
                            __uint_as_float(v[col + 4 * i + 2]) * f, __uint_as_float(v[col + 4 * i + 3]) * f);
     __syncwarp();
-    const bool here = col + c < width;
-    const float b = p.bias && here ? to_f(static_cast<const T*>(p.bias)[n0 + col + c]) : 0.f;
-#pragma unroll 4
+    const int live = col + c < width ? (rows - (lane >> 4) + 1) / 2 : 0;    // rows of this lane's column
+    const float b = p.bias && live > 0 ? to_f(static_cast<const T*>(p.bias)[n0 + col + c]) : 0.f;
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = res && i < live ? to_f(res[i * res_step + col]) : 0.f;
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
       float* x = there + 2 * i * (kPiecePitch / 4);
       T o = from_f<T>(0.f);
-      if (here && 2 * i + (lane >> 4) < rows) {
-        float y = *x + b;
-        if (res) y += to_f(res[2 * i * p.residual_row + col]);
-        o = from_f<T>(y);
-        out[2 * i * p.out_row + col] = o;
+      if (i < live) {
+        o = from_f<T>(*x + b + y[i]);
+        out[i * out_step + col] = o;
       }
       if (p.psum) *x = to_f(o);
     }
