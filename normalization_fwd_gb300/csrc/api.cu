@@ -257,7 +257,7 @@ ln_status ln_device_error(cudaStream_t stream, unsigned* flags) {
       take_error_bwd_bulk_rms_dbias_f32, take_error_bwd_bulk_rms_dbias_bf16,
       take_error_bwd_bulk_rms_dbias_f16, take_error_softmax_f32,
       take_error_softmax_bf16,          take_error_softmax_f16,
-      take_error_product};
+      take_error_product,               take_error_quantize};
   for (auto r : readers) {
     cudaError_t e = r(stream, flags);
     if (e != cudaSuccess) return cuda_fail(e);

@@ -81,6 +81,7 @@ NF_DECLARE_TABLES(bf16)
 NF_DECLARE_TABLES(f16)
 #undef NF_DECLARE_TABLES
 cudaError_t take_error_product(cudaStream_t st, unsigned* out);
+cudaError_t take_error_quantize(cudaStream_t st, unsigned* out);
 
 // n_params: parameter rows (w, and bias / beta when given).
 template <typename T>

@@ -9,9 +9,12 @@
 #include "mx_check.h"
 #include "mx_norm_kernels.cuh"
 #include "mx_quantize_kernels.cuh"
+#include "tensor_map.h"
 #include "validate.h"
 
 namespace nf {
+
+cudaError_t take_error_quantize(cudaStream_t st, unsigned* out) { return take_tu_error(st, out); }
 
 const void* mx_norm_table_f32(int cls, int lanes, int n);
 const void* mx_norm_table_bf16(int cls, int lanes, int n);
@@ -76,11 +79,41 @@ dim3 row_grid(int64_t rows, int64_t cols, int shift, int sms) {
   return dim3((unsigned)x, (unsigned)std::min<int64_t>(std::min<int64_t>((rows + per - 1) / per, most), 65535));
 }
 
+// The transpose by tensor maps: x on 16 bytes, its rows a multiple of them apart
+// and not in one another.
+template <typename T, int FMT>
+cudaError_t launch_transpose_tma(const QuantArgs& a, int64_t x, int64_t tiles, int sms, cudaStream_t st) {
+  const void* fn = (const void*)quant_transpose_tma_kernel<T, FMT>;
+  constexpr size_t kSmem = kTrStages * kTrBytes + 1024;
+  Encode encode;
+  CUtensorMap map;
+  cudaError_t e = encoder(&encode);
+  if (e == cudaSuccess) e = (cudaError_t)allow_dyn_smem(fn, kSmem);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.q.rows, (cuuint64_t)a.q.cols}, strides[1] = {(cuuint64_t)a.x_row * sizeof(T)};
+  const cuuint32_t box[2] = {(cuuint32_t)TrRows<T>::N, (cuuint32_t)kTrCols}, step[2] = {1, 1};
+  const CUresult r = encode(&map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                            const_cast<void*>(a.x), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  int64_t all = x * tiles;
+  QuantArgs args = a;
+  void* params[] = {&map, &args, &all};
+  return cudaLaunchKernel(fn, dim3((unsigned)std::min<int64_t>(all, 2 * sms)), dim3(kQuantThreads), params, kSmem, st);
+}
+
 template <typename T, int FMT>
 cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStream_t st) {
   const QuantOut& q = a.q;
   if (transpose) {
     const int64_t x = (a.padded_rows + TrRows<T>::N - 1) / TrRows<T>::N, tiles = (q.cols + kTrCols - 1) / kTrCols;
+    // a copy each 16 bytes of x's rows: the tensor map's, from where the loop over
+    // tiles has more than one round
+    if constexpr (FMT != MX_FP8_ROW)
+      if (a.vec && a.x_row >= q.rows && a.x_row * (int64_t)sizeof(T) % 16 == 0 && a.x_row < (1ll << 37) &&
+          x * tiles > 2 * sms)
+        return launch_transpose_tma<T, FMT>(a, x, tiles, sms, st);
     const dim3 grid((unsigned)x, FMT == MX_FP8_ROW ? 1u : (unsigned)std::min<int64_t>(tiles, 65535));
     quant_transpose_kernel<T, FMT><<<grid, kQuantThreads, 0, st>>>(a);
   } else if constexpr (FMT == MX_FP8_ROW) {

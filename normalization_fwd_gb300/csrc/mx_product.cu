@@ -3,7 +3,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 #include <vector>
 
@@ -11,6 +10,7 @@
 #include "launch.h"
 #include "mx_check.h"
 #include "mx_product_kernels.cuh"
+#include "tensor_map.h"
 
 namespace nf {
 
@@ -21,25 +21,6 @@ namespace {
 ln_status cuda_fail(cudaError_t e) {
   nf_set_last_cuda_error((int)e);
   return LN_ERR_CUDA;
-}
-
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                            CUtensorMapFloatOOBfill);
-
-cudaError_t encoder(Encode* out) {
-  static std::atomic<void*> kept{nullptr};
-  void* fn = kept.load(std::memory_order_relaxed);
-  if (fn == nullptr) {
-    cudaDriverEntryPointQueryResult found;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
-    if (e != cudaSuccess) return e;
-    if (found != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
-    kept.store(fn, std::memory_order_relaxed);
-  }
-  *out = reinterpret_cast<Encode>(fn);
-  return cudaSuccess;
 }
 
 // Codes as rows of bytes, boxes of 128 bytes by `rows`, swizzled.

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "mx_formats.cuh"
+#include "tcgen05.cuh"
 
 namespace nf {
 
@@ -221,11 +222,100 @@ template <typename T, int N> __device__ __forceinline__ void words_amax(const un
   }
 }
 
+// Codes and scales of a lane's rows row .. row + W - 1 of the result, columns col
+// .. col + 31, out of 32 words. `s`: the rows' scales where they are known (fp32
+// scales); `writes`: whether this warp has a block's first columns.
+template <typename T, int FMT>
+__device__ __forceinline__ void put_columns(const QuantOut& q, int64_t row, int64_t col, const unsigned* w,
+                                            float mul, BlockScale* s, bool writes, bool vec_codes) {
+  constexpr int W = 4 / sizeof(T);
+  constexpr bool FOUR = FMT >= MX_MXFP4, TILED = FMT >= MX_MXFP8;
+  unsigned m[W], m2[W];
+  if (FMT == MX_NVFP4) {
+    words_amax<T, 16>(w, m);
+    words_amax<T, 16>(w + 16, m2);
+  } else if (TILED) {
+    words_amax<T, 32>(w, m);
+  }
+#pragma unroll
+  for (int h = 0; h < W; ++h) {
+    if (row + h >= q.rows) break;
+    unsigned char* scales = static_cast<unsigned char*>(q.scales);
+    if (FOUR) {
+      unsigned c[4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        BlockScale b;
+        if (FMT == MX_NVFP4) {
+          // the largest product is that of the largest value: products round monotonically
+          b = scale_e4m3(__float_as_uint(fabsf(__uint_as_float(k ? m2[h] : m[h]) * mul)));
+          if (col / 16 + k < q.blocks) scales[scale_at(row + h, col / 16 + k, q.blocks)] = (unsigned char)b.byte;
+        } else {
+          b = scale_e8m0<true>(m[h]);
+          if (k == 0) scales[scale_at(row + h, col / 32, q.blocks)] = (unsigned char)b.byte;
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float2 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = 16 * k + 8 * g + 2 * i;
+            v[i] = make_float2(word_value<T>(w[at], h), word_value<T>(w[at + 1], h));
+            if (FMT == MX_NVFP4) v[i] = mul2(v[i], splat2(mul));
+          }
+          c[2 * k + g] = codes_e2m1<4>(v, b, FMT == MX_NVFP4);
+        }
+      }
+      *reinterpret_cast<uint4*>(q.codes + (row + h) * q.pitch + col / 2) = make_uint4(c[0], c[1], c[2], c[3]);
+    } else {
+      if (FMT == MX_MXFP8) {
+        s[h] = scale_e8m0<false>(m[h]);
+        scales[scale_at(row + h, col / 32, q.blocks)] = (unsigned char)s[h].byte;
+      } else if (FMT == MX_FP8_BLOCK && writes) {
+        static_cast<float*>(q.scales)[(row + h) * q.blocks + col / 128] = s[h].scale;
+      }
+      unsigned c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 v[2] = {make_float2(word_value<T>(w[4 * i], h), word_value<T>(w[4 * i + 1], h)),
+                             make_float2(word_value<T>(w[4 * i + 2], h), word_value<T>(w[4 * i + 3], h))};
+        codes_e4m3<2>(v, s[h].factor, c + i);
+      }
+      unsigned char* p = q.codes + (row + h) * q.pitch + col;
+      if (TILED || (vec_codes && q.pitch % 16 == 0 && col + 32 <= q.pitch)) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(c[0], c[1], c[2], c[3]);
+        *reinterpret_cast<uint4*>(p + 16) = make_uint4(c[4], c[5], c[6], c[7]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (col + i < q.pitch) p[i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
+      }
+    }
+  }
+}
+
+// The scales of a 128-column block, whose words four warps have.
+template <typename T>
+__device__ __forceinline__ void join_blocks(const unsigned* w, unsigned (*red)[32][4 / sizeof(T)], BlockScale* s) {
+  constexpr int W = 4 / sizeof(T);
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  unsigned m[W];
+  words_amax<T, 32>(w, m);
+#pragma unroll
+  for (int h = 0; h < W; ++h) red[part][lane][h] = m[h];
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < W; ++h) {
+    unsigned b = 0;
+    for (int i = 0; i < 4; ++i) b = max(b, red[(part & 4) + i][lane][h]);
+    s[h] = scale_fp32(b);
+  }
+}
+
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads, 3) quant_transpose_kernel(const QuantArgs a) {
   __shared__ unsigned tile[kTrCols * kTrPitch];
   constexpr int W = 4 / sizeof(T);             // rows of a lane
-  constexpr bool FOUR = FMT >= MX_MXFP4, TILED = FMT >= MX_MXFP8;
   __shared__ unsigned red[8][32][W];
   const QuantOut& q = a.q;
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
@@ -233,17 +323,18 @@ __global__ void __launch_bounds__(kQuantThreads, 3) quant_transpose_kernel(const
   const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
   const int64_t tiles = (q.cols + kTrCols - 1) / kTrCols;
   const unsigned* mine = tile + part * 32 * kTrPitch + lane;
-  if (TILED && blockIdx.y == 0)
+  if (FMT >= MX_MXFP8 && blockIdx.y == 0)
     for (int h = 0; h < W; ++h)
       if (row + h < a.padded_rows) put_padding(q, row + h, part, 8);
-  unsigned m[W] = {};
   BlockScale s[W];
+  unsigned w[32];
   if (FMT == MX_FP8_ROW) {
+    unsigned m[W] = {};
     for (int64_t t = 0; t < tiles; ++t) {
       __syncthreads();
       load_tile<T>(a, row0, t * kTrCols, tile);
       __syncthreads();
-      unsigned w[32], b[W];
+      unsigned b[W];
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = mine[i * kTrPitch];
       words_amax<T, 32>(w, b);
@@ -265,82 +356,80 @@ __global__ void __launch_bounds__(kQuantThreads, 3) quant_transpose_kernel(const
     load_tile<T>(a, row0, t * kTrCols, tile);
     __syncthreads();
     const int64_t col = t * kTrCols + part * 32;
-    unsigned w[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) w[i] = mine[i * kTrPitch];
-    if (FMT == MX_FP8_BLOCK) {                    // four warps have a block
-      words_amax<T, 32>(w, m);
+    if (FMT == MX_FP8_BLOCK) join_blocks<T>(w, red, s);
+    if (col < q.cols) put_columns<T, FMT>(q, row, col, w, mul, s, part % 4 == 0, a.vec_codes != 0);
+  }
+}
+
+// The same with tiles that a tensor map copies, in a ring of kTrStages that stay
+// in flight while the ones before are worked on (with loads through registers
+// three CTAs an SM left HBM idle between them: 8192 x 8192 bf16 to mxfp8 49 us).
+// The tile's rows of 128 bytes lie in the 128-byte swizzle: 16-byte part p of row
+// c at p ^ (c % 8), so that a warp still reads a row's 32 words without conflict.
+// CTAs take tiles a grid apart, those of one column of x after another.
+constexpr int kTrStages = 3;
+constexpr uint32_t kTrBytes = kTrCols * 128;
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kQuantThreads, 2)
+    quant_transpose_tma_kernel(const __grid_constant__ CUtensorMap map, const QuantArgs a, int64_t all) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t full[kTrStages];
+  constexpr int W = 4 / sizeof(T);
+  __shared__ unsigned red[8][32][W];
+  const QuantOut& q = a.q;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
+  const int64_t tiles = (q.cols + kTrCols - 1) / kTrCols;      // along a row of the result
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTrStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const auto copy = [&](int64_t i, int st) {                   // by one thread
+    const int64_t r = i / tiles, t = i - r * tiles;
+    mbar_arrive_expect_tx(&full[st], kTrBytes);
+    tma_load_2d(base + st * kTrBytes, &map, (int)(r * TrRows<T>::N), (int)(t * kTrCols), smem_addr(&full[st]));
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < kTrStages; ++k)
+      if (blockIdx.x + (int64_t)k * gridDim.x < all) copy(blockIdx.x + (int64_t)k * gridDim.x, k);
+  int st = 0, round = 0;
+  bool ok = true;
+  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+    // all threads go on, or none: a wait that gave up has the others give up too
+    ok = __syncthreads_and(mbar_wait_cluster(&full[st], round & 1));
+    if (!ok) break;
+    const int64_t r = i / tiles, t = i - r * tiles;
+    const int64_t row = r * TrRows<T>::N + lane * W, col = t * kTrCols + part * 32;
+    if (FMT >= MX_MXFP8 && t == 0)
+      for (int h = 0; h < W; ++h)
+        if (row + h < a.padded_rows) put_padding(q, row + h, part, 8);
+    unsigned w[32];
+    const uint32_t tile = base + st * kTrBytes + part * 32 * 128;
 #pragma unroll
-      for (int h = 0; h < W; ++h) red[part][lane][h] = m[h];
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < W; ++h) {
-        unsigned b = 0;
-        for (int i = 0; i < 4; ++i) b = max(b, red[(part & 4) + i][lane][h]);
-        s[h] = scale_fp32(b);
-      }
+    for (int k = 0; k < 32; ++k)
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k]) : "r"(tile + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) + (lane & 3) * 4));
+    BlockScale s[W];
+    if (FMT == MX_FP8_BLOCK) join_blocks<T>(w, red, s);
+    __syncthreads();                                           // the stage is read
+    if (threadIdx.x == 0 && i + (int64_t)kTrStages * gridDim.x < all) copy(i + (int64_t)kTrStages * gridDim.x, st);
+    if (col < q.cols) put_columns<T, FMT>(q, row, col, w, mul, s, part % 4 == 0, a.vec_codes != 0);
+    if (++st == kTrStages) {
+      st = 0;
+      ++round;
     }
-    if (col >= q.cols) continue;                  // the barriers are at the loop's head
-    unsigned m2[W];
-    if (FMT == MX_NVFP4) {
-      words_amax<T, 16>(w, m);
-      words_amax<T, 16>(w + 16, m2);
-    } else if (TILED) {
-      words_amax<T, 32>(w, m);
-    }
-#pragma unroll
-    for (int h = 0; h < W; ++h) {
-      if (row + h >= q.rows) break;
-      unsigned char* scales = static_cast<unsigned char*>(q.scales);
-      if (FOUR) {
-        unsigned c[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          BlockScale b;
-          if (FMT == MX_NVFP4) {
-            // the largest product is that of the largest value: products round monotonically
-            b = scale_e4m3(__float_as_uint(fabsf(__uint_as_float(k ? m2[h] : m[h]) * mul)));
-            if (col / 16 + k < q.blocks) scales[scale_at(row + h, col / 16 + k, q.blocks)] = (unsigned char)b.byte;
-          } else {
-            b = scale_e8m0<true>(m[h]);
-            if (k == 0) scales[scale_at(row + h, col / 32, q.blocks)] = (unsigned char)b.byte;
-          }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float2 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = 16 * k + 8 * g + 2 * i;
-              v[i] = make_float2(word_value<T>(w[at], h), word_value<T>(w[at + 1], h));
-              if (FMT == MX_NVFP4) v[i] = mul2(v[i], splat2(mul));
-            }
-            c[2 * k + g] = codes_e2m1<4>(v, b, FMT == MX_NVFP4);
-          }
-        }
-        *reinterpret_cast<uint4*>(q.codes + (row + h) * q.pitch + col / 2) = make_uint4(c[0], c[1], c[2], c[3]);
-      } else {
-        if (FMT == MX_MXFP8) {
-          s[h] = scale_e8m0<false>(m[h]);
-          scales[scale_at(row + h, col / 32, q.blocks)] = (unsigned char)s[h].byte;
-        } else if (FMT == MX_FP8_BLOCK && part % 4 == 0) {
-          static_cast<float*>(q.scales)[(row + h) * q.blocks + col / 128] = s[h].scale;
-        }
-        unsigned c[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v[2] = {make_float2(word_value<T>(w[4 * i], h), word_value<T>(w[4 * i + 1], h)),
-                               make_float2(word_value<T>(w[4 * i + 2], h), word_value<T>(w[4 * i + 3], h))};
-          codes_e4m3<2>(v, s[h].factor, c + i);
-        }
-        unsigned char* p = q.codes + (row + h) * q.pitch + col;
-        if (TILED || (a.vec_codes && q.pitch % 16 == 0 && col + 32 <= q.pitch)) {
-          *reinterpret_cast<uint4*>(p) = make_uint4(c[0], c[1], c[2], c[3]);
-          *reinterpret_cast<uint4*>(p + 16) = make_uint4(c[4], c[5], c[6], c[7]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + i < q.pitch) p[i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
-        }
+  }
+  if (!ok && threadIdx.x == 0) {      // copies in flight land before the CTA ends
+    atomicOr(&g_tu_error, kErrWaitTimeout);
+    for (int k = 0; k < kTrStages; ++k) {
+      mbar_wait_cluster(&full[st], round & 1);
+      if (++st == kTrStages) {
+        st = 0;
+        ++round;
       }
     }
   }

@@ -42,6 +42,22 @@ def test_codes_and_scales(cuda_lib, fmt, dtype, transpose, rows, cols):
         assert g.intact()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_transposes_of_many_tiles(cuda_lib, fmt, dtype):
+    """More tiles than the SMs hold at a time, rows of x 16 bytes apart or not."""
+    nf = cuda_lib
+    rng = np.random.default_rng(8)
+    rows, cols = 1101, 5203
+    x = data(rng, cols, rows, dtype)
+    want = f64(x.T)
+    for extra in (11, 0):       # rows of 1112 and of 1101 values
+        g = Padded((cols, rows), DT[dtype], extra=extra, data=x.cuda())
+        q = nf.quantize(g.t, fmt, transpose=True)
+        check_bits(q, want, fmt)
+    assert nf.ln_device_error() == 0
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_middles_between_codes(cuda_lib, fmt):
     """Quotients that lie on the middle of two codes, for every scale's fraction."""
