@@ -239,13 +239,15 @@ def ln_device_error(stream=None) -> int:
 def _ptr(t) -> int | None:
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"expected a torch.Tensor or None, got {type(t).__name__}")
-    if t.numel() and not t.is_cuda:
+    try:
+        address, here = t.data_ptr(), t.is_cuda
+    except AttributeError:
+        raise TypeError(f"expected a torch.Tensor or None, got {type(t).__name__}") from None
+    if not here and t.numel():
         raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return t.data_ptr() or None
+    return address or None
 
 
 def _stream(stream) -> int | None:

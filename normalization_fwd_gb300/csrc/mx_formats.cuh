@@ -108,21 +108,21 @@ template <int D> __device__ __forceinline__ float over(float v) {
 // the eight fractions that E4M3 has all reach (the tests see every one).
 __device__ __forceinline__ BlockScale scale_e4m3(unsigned bits) {
   BlockScale s;
-  if (bits >= kInfBits) return {0.f, 0.f, 0x7fu};
+  const bool odd = bits >= kInfBits;
   const float t = over<6>(__uint_as_float(bits));
-  s.byte = fp8x2(make_float2(t, 0.f), splat2(1.0f)) & 0xffu;
+  s.byte = odd ? 0x7fu : fp8x2(make_float2(t, 0.f), splat2(1.0f)) & 0xffu;
   s.scale = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s.byte, __NV_E4M3)));
   const float r = __fdividef(1.0f, s.scale);
-  s.factor = s.byte ? fmaf(fmaf(-s.scale, r, 1.0f), r, r) : 0.f;
+  s.factor = s.byte && !odd ? fmaf(fmaf(-s.scale, r, 1.0f), r, r) : 0.f;
   return s;
 }
 
 // fp32 scale: amax / 448, with amax no less than 2^-100 (so that 448 / amax is
 // finite and the scale normal).
 __device__ __forceinline__ BlockScale scale_fp32(unsigned bits) {
-  if (bits >= kInfBits) return {0.f, __uint_as_float(0x7fffffffu), 0u};
-  const float a = fmaxf(__uint_as_float(bits), kLeastAmax);
-  return {448.0f / a, over<448>(a), 0u};
+  const bool odd = bits >= kInfBits;
+  const float a = fmaxf(__uint_as_float(odd ? 0u : bits), kLeastAmax);
+  return {odd ? 0.f : 448.0f / a, odd ? __uint_as_float(0x7fffffffu) : over<448>(a), 0u};
 }
 
 // v / s, correctly rounded, from r = 1 / s rounded to nearest: q = v r is
@@ -132,7 +132,7 @@ __device__ __forceinline__ BlockScale scale_fp32(unsigned bits) {
 // off by a rounding would fall to the wrong side.
 __device__ __forceinline__ float2 quotient2(float2 v, float s, float r) {
   const float2 q = mul2(v, splat2(r));
-  const float2 rem = fma2(make_float2(-q.x, -q.y), splat2(s), v);
+  const float2 rem = fma2(q, splat2(-s), v);
   return fma2(rem, splat2(r), q);
 }
 

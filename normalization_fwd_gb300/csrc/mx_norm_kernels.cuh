@@ -30,7 +30,7 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
   constexpr int P = VEC / 2;
   const FwdArgs& f = a.f;
   const int G = G0 > 0 ? G0 : (int)blockDim.x;
-  const bool row_ok = row < f.rows;
+  const bool row_ok = G0 == 0 || row < f.rows;     // a CTA without a row does not come here
   const int H = f.hidden;
   const int V = H / VEC;
   const int64_t off = row * (int64_t)H;

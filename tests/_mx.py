@@ -70,3 +70,23 @@ def check_bits(q, v, fmt, mul=None):
     else:
         s = q.scales.cpu().numpy()
         assert np.array_equal(s, stored.reshape(s.shape), equal_nan=True)
+
+
+def values_of(q):
+    """The fp64 values that the bytes of a microscaled Quantized stand for."""
+    width = mx.BLOCK[q.format]
+    n = -(-q.cols // width)
+    codes = q.codes.cpu()
+    if q.format == "mxfp8":
+        v = codes.double().numpy()
+    else:
+        c = codes.numpy()
+        c = np.stack((c & 15, c >> 4), axis=-1).reshape(q.rows, -1)
+        v = np.where(c & 8, -1.0, 1.0) * mx.E2M1[c & 7]
+    tiles = q.scales.view(torch.uint8).cpu().numpy()
+    s = tiles.transpose(0, 3, 2, 1, 4).reshape(tiles.shape[0] * 128, -1)[:q.rows, :n]
+    if q.format == "nvfp4":
+        s = torch.from_numpy(np.ascontiguousarray(s)).view(torch.float8_e4m3fn).double().numpy()
+    else:
+        s = np.where(s == 255, np.nan, 2.0 ** (s.astype(float) - 127))
+    return mx.values(v[:, :q.cols], s, q.format, None if q.mul is None else float(q.mul))
