@@ -291,7 +291,7 @@ def measured_peak():
 # Host-side sources (planning, argument checks, entry points) do not change
 # what a kernel reads or writes, so they are left out of the kernel hash.
 HOST_SOURCES = ("api.cu", "plan.cu", "noalloc.cu", "launch.h")
-OTHER_KERNELS = ("gn", "rope")   # sources of operators that no workload here runs
+OTHER_KERNELS = ("gn", "rope", "mx", "tcgen05")   # sources of operators that no workload here runs
 
 
 def source_hash() -> str:

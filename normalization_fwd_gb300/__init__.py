@@ -3,7 +3,9 @@
 The functions here have the names of the C entry points declared in
 ``include/normfuse.h`` and only marshal arguments: torch tensors become
 device pointers, the torch stream becomes a ``cudaStream_t``, and the return
-status becomes an exception. Every step of the computation runs in the CUDA
+status becomes an exception. The quantised calls that allocate their outputs
+do so in C++ (``csrc/marshal.cc``) where the call is on the current device and
+stream. Every step of the computation runs in the CUDA
 kernels of the library; there is no fallback. If the library has not been
 built, loading it raises.
 
@@ -15,6 +17,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import struct
 import threading
@@ -22,7 +26,7 @@ from typing import NamedTuple
 
 import torch
 
-from .build import LIB_PATH, build as build_library
+from .build import LIB_PATH, build as build_library, marshal_path
 
 __all__ = [
     "LN_F32", "LN_BF16", "LN_F16", "LN_LAYERNORM", "LN_RMSNORM", "NormError",
@@ -73,6 +77,7 @@ _FORMAT_CODES = {"fp8_row": MX_FP8_ROW, "fp8_block": MX_FP8_BLOCK, "mxfp8": MX_M
 _MX_MATRIX = struct.Struct("@PPPiqq")
 
 _lib = None
+_marshal = None     # the binding's C++ part (csrc/marshal.cc), loaded with the library
 _lock = threading.Lock()
 
 
@@ -89,7 +94,7 @@ class NormError(RuntimeError):
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load ``libnormfuse.so`` (built in-tree by ``build_library()``)."""
-    global _lib
+    global _lib, _marshal
     with _lock:
         if _lib is not None:
             return _lib
@@ -98,6 +103,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             raise RuntimeError(
                 f"CUDA library not built: {path} is missing. "
                 "Run `python -m normalization_fwd_gb300.build` (needs nvcc).")
+        if not os.path.isfile(marshal_path()):
+            raise RuntimeError(
+                f"the binding is not built for this torch: {marshal_path()} is missing. "
+                "Run `python -m normalization_fwd_gb300.build`.")
         lib = ctypes.CDLL(path)
         vp, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         ci = ctypes.c_int
@@ -160,6 +169,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.mx_dequantize.restype = ci
         lib.mx_product.argtypes = [vp, vp, f32, vp, vp, i64, vp, i64, vp, vp, vp, ci]
         lib.mx_product.restype = ci
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", marshal_path())
+        spec = importlib.util.spec_from_loader("_marshal", loader)
+        _marshal = importlib.util.module_from_spec(spec)
+        loader.exec_module(_marshal)
         _lib = lib
         return lib
 
@@ -481,6 +494,12 @@ def fused_norm_fwd_from_partials(x, psum, psq, tile_cols, gamma, beta=None, *, k
                                  amax=False, stream=None):
     """Allocate the outputs with torch and run ``ln_fwd_from_partials``;
     returns a dict with ``y``, ``mean`` (LayerNorm), ``rstd``, ``amax``."""
+    if stream is None and not amax and (_lib or load_library()):
+        r = _marshal.norm_from_partials(x, psum, psq, tile_cols, _PARTIAL_CODES.get(kind, -1), gamma,
+                                        beta, eps, _mode(mode), zero_centered_gamma)
+        if r is not None:
+            y, mean, rstd = _made(r, "ln_fwd_from_partials")
+            return {"y": y, "mean": mean, "rstd": rstd, "amax": None}
     rows, hidden = _shape(x)
     rms = _mode(mode) == LN_RMSNORM
     y = torch.empty_like(x)
@@ -1090,6 +1109,13 @@ class Quantized(NamedTuple):
     mul: torch.Tensor | None = None
 
 
+def _made(r, where):
+    """What a function of csrc/marshal.cc made, or the error that a status is."""
+    if isinstance(r, int):
+        raise NormError(r, where)
+    return r
+
+
 def _format(format) -> int:
     try:
         return _FORMAT_CODES[format]
@@ -1300,6 +1326,15 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
     nvfp4's factor (one float32 on the device, commonly 2688 over the largest
     magnitude seen).
     """
+    if store_sum is None:
+        store_sum = bias is not None or residual is not None
+    if stream is None and (_lib or load_library()):
+        r = _marshal.norm_quant(x, gamma, beta, bias, residual, mul, _format(format), _mode(mode),
+                                zero_centered_gamma, eps, store_sum, store_y)
+        if r is not None:
+            codes, scales, out_sum, y, mean, rstd = _made(r, "mx_norm_fwd")
+            return {"q": Quantized(codes, scales, format, codes.shape[0], x.shape[-1], mul),
+                    "sum": out_sum, "y": y, "mean": mean, "rstd": rstd}
     device = _device_of("fused_norm_quant_fwd", x, gamma, beta, mul, bias, residual)
     if _elsewhere(device, stream):
         with _current(device, stream):
@@ -1308,8 +1343,6 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
                                         zero_centered_gamma=zero_centered_gamma,
                                         store_sum=store_sum, store_y=store_y)
     rows, hidden = _shape(x)
-    if store_sum is None:
-        store_sum = bias is not None or residual is not None
     mode = _mode(mode)
     rms = mode == LN_RMSNORM
     q = quantized_empty(rows, hidden, format, mul=mul, device=device)
@@ -1325,6 +1358,12 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
 def quantize(x, format, *, mul=None, transpose=False, stream=None) -> Quantized:
     """The matrix ``x``, or its transpose, in 8 or 4 bits with scales. Rows of x
     may be any distance apart (a slice of a wider tensor)."""
+    if stream is None and (_lib or load_library()):
+        r = _marshal.quantize(x, _format(format), transpose, mul)
+        if r is not None:
+            codes, scales = _made(r, "mx_quantize")
+            return Quantized(codes, scales, format, codes.shape[0], x.shape[0 if transpose else 1],
+                             mul)
     device = _device_of("quantize", x, mul)
     if _elsewhere(device, stream):
         with _current(device, stream):
@@ -1339,6 +1378,12 @@ def quantize(x, format, *, mul=None, transpose=False, stream=None) -> Quantized:
 
 def dequantize(q, dtype=torch.float32, *, out=None, stream=None):
     """The values of ``q`` as a [rows, cols] tensor of ``dtype``."""
+    if stream is None and out is None and (_lib or load_library()):
+        codes, scales, format, rows, cols, mul = q
+        r = _marshal.dequantize(codes, scales, mul, _format(format), rows, cols,
+                                _DTYPE_CODES.get(dtype, -1))
+        if r is not None:
+            return _made(r, "mx_dequantize")
     device = _device_of("dequantize", q.codes, q.scales, q.mul, out)
     if _elsewhere(device, stream):
         with _current(device, stream):
@@ -1362,6 +1407,13 @@ def scaled_product(a, b, *, alpha=1.0, bias=None, residual=None, dtype=torch.bfl
     quantise the output's gradient and the weights (transpose=True) for the
     input's, both operands transposed for the weights'.
     """
+    if stream is None and a.format == b.format and a.cols == b.cols and (_lib or load_library()):
+        r = _marshal.product(a.codes, a.scales, a.mul, b.codes, b.scales, b.mul, _format(a.format),
+                             a.rows, b.rows, a.cols, alpha, bias, residual,
+                             _DTYPE_CODES.get(dtype, -1), out, partials)
+        if r is not None:
+            out, psum, psq = _made(r, "mx_product")
+            return {"out": out, "psum": psum, "psq": psq, "tile_cols": 128}
     device = _device_of("scaled_product", a.codes, a.scales, a.mul, b.codes, b.scales, b.mul, bias,
                         residual, out)
     if _elsewhere(device, stream):

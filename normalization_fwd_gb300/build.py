@@ -1,8 +1,11 @@
-"""Build the CUDA library ``libnormfuse.so`` in-tree for sm_103a.
+"""Build the CUDA library ``libnormfuse.so`` in-tree for sm_103a, and the
+binding's C++ part beside it.
 
 Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then the
 objects are linked into a shared library next to this file (the CUDA runtime
-is linked statically). Nothing is installed anywhere else.
+is linked statically). ``csrc/marshal.cc`` is compiled at the same time by the
+host compiler, against the headers of the torch and Python that run this; its
+file has torch's version in its name. Nothing is installed anywhere else.
 
     python -m normalization_fwd_gb300.build [--force] [--verbose] [--ptxas-info]
 """
@@ -14,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,19 +46,42 @@ def find_nvcc() -> str:
     raise RuntimeError("nvcc not found: set CUDA_HOME or put nvcc on PATH")
 
 
+def marshal_path() -> str:
+    """Where the C++ part of the binding is, for this torch and this Python."""
+    import torch
+    tag = f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}"
+    return os.path.join(PKG, f"_marshal-{tag}.so")
+
+
+def _marshal_commands(nvcc):
+    """(compile, link): the link comes after the library's."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+    dirs = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda, os.path.join(ROOT, "include")]
+    obj = os.path.join(BUILD, "marshal.o")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return (["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+             *[f"-I{d}" for d in dirs], "-c", os.path.join(CSRC, "marshal.cc"), "-o", obj],
+            ["g++", "-shared", obj, "-o", marshal_path() + ".tmp", f"-L{PKG}", f"-l:{LIB_NAME}",
+             "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+             "-ltorch_python"])
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cc")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.isfile(LIB_PATH):
+    if not os.path.isfile(LIB_PATH) or not os.path.isfile(marshal_path()):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(marshal_path()))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -76,12 +103,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
         return src, obj, r
 
     jobs = jobs or min(len(_sources()), os.cpu_count() or 4)
-    with ThreadPoolExecutor(max_workers=jobs) as ex:
+    with ThreadPoolExecutor(max_workers=jobs + 1) as ex:
+        compile_marshal, link_marshal = _marshal_commands(nvcc)
+        marshal = ex.submit(subprocess.run, compile_marshal, capture_output=True, text=True)
         results = list(ex.map(compile_one, _sources()))
+        marshal = marshal.result()
     failed = [(s, r) for s, _, r in results if r.returncode != 0]
     for s, _, r in results:
         if (verbose or ptxas_info) and (r.stdout or r.stderr):
             sys.stdout.write(r.stdout + r.stderr)
+    if marshal.returncode != 0:
+        raise RuntimeError(f"g++ failed:\n--- marshal.cc\n{marshal.stdout}{marshal.stderr}")
     if failed:
         msg = "\n".join(f"--- {s}\n{r.stdout}{r.stderr}" for s, r in failed)
         raise RuntimeError(f"nvcc failed:\n{msg}")
@@ -93,6 +125,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    r = subprocess.run(link_marshal, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
+    os.replace(marshal_path() + ".tmp", marshal_path())
     return LIB_PATH
 
 
