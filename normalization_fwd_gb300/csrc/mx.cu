@@ -32,12 +32,19 @@ int class_of(int fmt) { return fmt == MX_FP8_ROW ? 0 : mx_four(fmt) ? 2 : 1; }
 // Lanes a row (0: a CTA), vectors a lane and threads for rows of `slots` 16-byte
 // vectors, room for codes included. As in the 16-bit forward: lane groups up to
 // 160 vectors, four vectors a lane where the row splits evenly, then a CTA
-// fitted to the row. A block of 128 columns needs 16 lanes (32 for fp32).
+// fitted to the row (8192 x 5120 bf16 LayerNorm to mxfp4 56 us with four
+// vectors a thread, 58 with three, 61 with six, 73 with eight). A block of 128
+// columns needs 16 lanes (32 for fp32). `few` rows leave threads idle anyway, so
+// a row is spread over as many as there are (1024 x 320 fp16 to mxfp8 3.9 us as
+// 32 x 2 against 5.7 as 8 x 5, 512 x 1000 fp32 3.6 as a CTA of two vectors a
+// thread against 4.5 of four; 8192 x 320, which is not few, 7.3 against 6.1).
 struct NormPlan {
   int lanes = -1, n = 0, block = kScalarCta;
 };
-NormPlan norm_plan(int slots, int least_lanes) {
+NormPlan norm_plan(int slots, int least_lanes, bool few) {
   NormPlan p;
+  if (few && slots <= 64) return {32, (slots + 31) / 32, kBulkThreads};
+  if (few && slots <= 2 * kMaxFitThreads) return {0, 2, std::max(64, (slots + 63) / 64 * 32)};
   if (slots <= 160) {
     for (int n : {4, 3, 5, 2, 1}) {
       const int lanes = slots / n;
@@ -202,7 +209,11 @@ ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, con
   NormPlan p;
   if (vec) {
     const int64_t wide = mx_tiled(q->format) ? (hidden + 31) / 32 * 32 : hidden;
-    p = norm_plan((int)((wide + per - 1) / per), q->format == MX_FP8_BLOCK ? 128 / per : 8);
+    const int64_t slots = (wide + per - 1) / per;
+    int sms = 0;
+    const cudaError_t e = (cudaError_t)device_sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(e);
+    p = norm_plan((int)slots, q->format == MX_FP8_BLOCK ? 128 / per : 8, rows * slots <= (int64_t)sms * 1024);
   }
   const void* fn = dtype == LN_F32 ? mx_norm_table_f32(cls, p.lanes, p.n)
                    : dtype == LN_BF16 ? mx_norm_table_bf16(cls, p.lanes, p.n)

@@ -144,19 +144,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int c1 = (int)((int64_t)p.chunks * (rank + 1) / p.splits);
   const uint32_t stage_size = stage_bytes<FMT>(cols);
 
-  if (warp == 2) tmem_alloc<kTmemCols>(&tmem_at);
-  if (threadIdx.x == 0) {
+  // A chunk's copies, by one thread.
+  const auto copy = [&](int c, int st) {
+    const uint32_t at = base + st * stage_size, bar = smem_addr(&full[st]);
+    const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
+    mbar_arrive_expect_tx(&full[st], stage_size);
+    tma_load_2d(at, &lane_codes, c * kChunkBytes, lane_row, bar);
+    tma_load_2d(at + kTileLanes * kChunkBytes, &col_codes, c * kChunkBytes, col_row, bar);
+    tma_load_3d(sc, &lane_scales, 0, c * kTiles, lane_row / 128, bar);
+    tma_load_3d(sc + kTiles * 512, &col_scales, 0, c * kTiles, col_row / 128, bar);
+  };
+  // The ring's first round needs no one else: its copies are on their way while
+  // tensor memory is handed out.
+  const int first = min(p.stages, c1 - c0);
+  if (warp == 0 && elect_one()) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
     fence_mbar_init();
-    tma_prefetch(&lane_codes);
-    tma_prefetch(&lane_scales);
-    tma_prefetch(&col_codes);
-    tma_prefetch(&col_scales);
+    for (int i = 0; i < first; ++i) copy(c0 + i, i);
   }
+  if (warp == 2) tmem_alloc<kTmemCols>(&tmem_at);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -164,21 +174,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == 0) {
     bool ok = true;
-    int st = 0, round = 0, c = c0;
+    int st = first == p.stages ? 0 : first, round = first == p.stages ? 1 : 0, c = c0 + first;
     for (; c < c1; ++c) {
-      if (round > 0 && !mbar_wait_cluster(&empty[st], (round - 1) & 1)) {
+      if (!mbar_wait_cluster(&empty[st], (round - 1) & 1)) {
         ok = false;
         break;
       }
-      const uint32_t at = base + st * stage_size, bar = smem_addr(&full[st]);
-      const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&full[st], stage_size);
-        tma_load_2d(at, &lane_codes, c * kChunkBytes, lane_row, bar);
-        tma_load_2d(at + kTileLanes * kChunkBytes, &col_codes, c * kChunkBytes, col_row, bar);
-        tma_load_3d(sc, &lane_scales, 0, c * kTiles, lane_row / 128, bar);
-        tma_load_3d(sc + kTiles * 512, &col_scales, 0, c * kTiles, col_row / 128, bar);
-      }
+      if (elect_one()) copy(c, st);
       __syncwarp();
       if (++st == p.stages) {
         st = 0;
