@@ -229,11 +229,12 @@ __device__ __forceinline__ void put_codes(unsigned char* p, const unsigned* c, b
 
 // Scale and codes of a block whose values lie in neighbouring lanes, VEC each (0
 // behind the last column). All lanes of the warp call it; a lane's codes go to
-// `codes`, the block's scale to `scale` (fp32 or a byte) where these are not
-// null. `bytes` (MX_FP8_BLOCK): a byte at a time, `most` of them.
+// `codes` where it is `live`, the block's scale (fp32 or a byte) to `scale` where
+// it is the `first` of its block. `bytes` (MX_FP8_BLOCK): a byte at a time,
+// `most` of them.
 template <int VEC, int FMT>
-__device__ __forceinline__ void put_block(float2* v, float mul, unsigned char* codes, void* scale,
-                                          int most = VEC, bool bytes = false) {
+__device__ __forceinline__ void put_block(float2* v, float mul, unsigned char* codes, bool live, void* scale,
+                                          bool first, int most = VEC, bool bytes = false) {
   constexpr int P = VEC / 2;
   constexpr bool FOUR = FMT >= MX_MXFP4;
   constexpr int kWidth = FMT == MX_NVFP4 ? 16 : FMT == MX_FP8_BLOCK ? 128 : 32;
@@ -246,7 +247,7 @@ __device__ __forceinline__ void put_block(float2* v, float mul, unsigned char* c
   const BlockScale s = FMT == MX_NVFP4 ? scale_e4m3(m) : FMT == MX_FP8_BLOCK ? scale_fp32(m) : scale_e8m0<FOUR>(m);
   if (FOUR) c[0] = codes_e2m1<P>(v, s, FMT == MX_NVFP4);
   else codes_e4m3<P>(v, s.factor, c);
-  if (codes) {
+  if (live) {
     if (FMT != MX_FP8_BLOCK || !bytes) {
       put_codes<VEC>(codes, c, FOUR);
     } else {
@@ -255,20 +256,18 @@ __device__ __forceinline__ void put_block(float2* v, float mul, unsigned char* c
         if (i < most) codes[i] = (unsigned char)(c[i / 4] >> (8 * (i % 4)));
     }
   }
-  if (scale) {
+  if (first) {
     if (FMT == MX_FP8_BLOCK) *static_cast<float*>(scale) = s.scale;
     else *static_cast<unsigned char*>(scale) = (unsigned char)s.byte;
   }
 }
 
-// Where the scale of a row's block goes, by the row's part of its place.
-template <int FMT>
-__device__ __forceinline__ void* scale_place(const QuantOut& q, int64_t row_part, int64_t block) {
-  return FMT == MX_FP8_BLOCK ? (void*)(static_cast<float*>(q.scales) + row_part + block)
-                             : (void*)(static_cast<unsigned char*>(q.scales) + row_part + scale_block(block));
+// Where the scales of a row begin, and how far from there a block's is, in bytes.
+template <int FMT> __device__ __forceinline__ unsigned char* scales_of_row(const QuantOut& q, int64_t row) {
+  return static_cast<unsigned char*>(q.scales) + (FMT == MX_FP8_BLOCK ? row * q.blocks * 4 : scale_row(row, q.blocks));
 }
-template <int FMT> __device__ __forceinline__ int64_t scale_row_part(const QuantOut& q, int64_t row) {
-  return FMT == MX_FP8_BLOCK ? row * q.blocks : scale_row(row, q.blocks);
+template <int FMT, typename I> __device__ __forceinline__ I scale_step(I block) {
+  return FMT == MX_FP8_BLOCK ? block * 4 : (block >> 2) * 512 + (block & 3);
 }
 
 // The scale bytes behind a row's last block, and all of a row behind the last

@@ -126,15 +126,15 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
   } else {
     const auto blocks = [&](auto fmt) {
       using F = decltype(fmt);
-      const int64_t part = scale_row_part<F::value>(a.q, row);
-      unsigned char* codes = a.q.codes + row * a.q.pitch;
+      unsigned char *scales = scales_of_row<F::value>(a.q, row), *codes = a.q.codes + row * a.q.pitch;
+      // a lane is first in a block in each slot or in none: G * VEC columns are whole blocks
+      const bool first = row_ok && t * VEC % F::width == 0;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         norm(k);
         const int col = (k * G + t) * VEC;
-        const bool first = row_ok && col % F::width == 0 && col < H;
-        put_block<VEC, F::value>(s[k], mul, row_ok && col < wide ? codes + (F::four ? col / 2 : col) : nullptr,
-                                 first ? scale_place<F::value>(a.q, part, col / F::width) : nullptr);
+        put_block<VEC, F::value>(s[k], mul, codes + (F::four ? col / 2 : col), row_ok && col < wide,
+                                 scales + scale_step<F::value>(col / F::width), first && col < H);
       }
     };
     // one format a loop: its shuffles and conversions are known then
@@ -268,13 +268,13 @@ __global__ void __launch_bounds__(kScalarCta) mx_norm_scalar_kernel(const MxNorm
       const int lane = threadIdx.x & 31;
       const auto blocks = [&](auto fmt) {
         using F = decltype(fmt);
-        const int64_t part = scale_row_part<F::value>(a.q, row);
+        unsigned char *scales = scales_of_row<F::value>(a.q, row), *codes = a.q.codes + row * a.q.pitch;
         const int wide = (int)a.q.pitch * (F::four ? 2 : 1);
         for (int c = threadIdx.x >> 5; c < chunks; c += kScalarCta / 32) {
           const int col = c * 128 + lane * 4;
           float2 v[2] = {make_float2(srow[col], srow[col + 1]), make_float2(srow[col + 2], srow[col + 3])};
-          put_block<4, F::value>(v, mul, col < wide ? a.q.codes + row * a.q.pitch + (F::four ? col / 2 : col) : nullptr,
-                                 col % F::width == 0 && col < H ? scale_place<F::value>(a.q, part, col / F::width) : nullptr,
+          put_block<4, F::value>(v, mul, codes + (F::four ? col / 2 : col), col < wide,
+                                 scales + scale_step<F::value>(col / F::width), col % F::width == 0 && col < H,
                                  min(4, wide - col), true);   // rows of MX_FP8_BLOCK start anywhere
         }
       };

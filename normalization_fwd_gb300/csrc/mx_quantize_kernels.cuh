@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
   const bool bytes = FMT == MX_FP8_BLOCK && (q.pitch % 8 != 0 || !a.vec_codes);
   const int most = (int)min((int64_t)8, q.cols - col);
   const bool vec = a.vec != 0 && col + 8 <= q.cols;
+  const int64_t step = scale_step<FMT>(col / F::width);
   const int64_t x_step = at.step * a.x_row, code_step = at.step * q.pitch;
   int64_t row = at.row;
   const T* x = static_cast<const T*>(a.x) + row * a.x_row + col;
@@ -88,8 +89,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
   };
   const auto put = [&](int64_t r, unsigned char* c, float2* v) {
     const bool ok = r < q.rows;
-    put_block<8, FMT>(v, mul, ok && room ? c : nullptr,
-                      ok && first ? scale_place<FMT>(q, scale_row_part<FMT>(q, r), col / F::width) : nullptr, most, bytes);
+    put_block<8, FMT>(v, mul, c, ok && room, scales_of_row<FMT>(q, r) + step, ok && first, most, bytes);
     if (pads && r < a.padded_rows) put_padding(q, r, (threadIdx.x & 31) & ((1 << shift) - 1), 1 << shift);
   };
   for (; __any_sync(0xffffffffu, row < a.padded_rows); row += 2 * at.step) {
