@@ -128,7 +128,9 @@ cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStre
   } else {
     // room for codes included
     const int shift = row_shift(mx_tiled(FMT) ? (q.cols + 31) / 32 * 32 : q.cols, mx_block(FMT) / 8);
-    quant_block_kernel<T, FMT><<<row_grid(a.padded_rows, q.cols, shift, sms), kQuantThreads, 0, st>>>(a, shift);
+    const dim3 grid = row_grid(a.padded_rows, q.cols, shift, sms);
+    if (a.vec) quant_block_kernel<T, FMT, false><<<grid, kQuantThreads, 0, st>>>(a, shift);
+    else quant_block_kernel<T, FMT, true><<<grid, kQuantThreads, 0, st>>>(a, shift);
   }
   return cudaGetLastError();
 }
@@ -292,8 +294,10 @@ ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t
   e = by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const auto run = [&](auto fmt) {
-      dequant_kernel<T, decltype(fmt)::value><<<grid, kQuantThreads, 0, stream>>>(o, static_cast<T*>(y), y_row, vec,
-                                                                                  vec_codes, shift);
+      constexpr int FMT = decltype(fmt)::value;
+      T* out = static_cast<T*>(y);
+      if (vec) dequant_kernel<T, FMT, false><<<grid, kQuantThreads, 0, stream>>>(o, out, y_row, vec_codes, shift);
+      else dequant_kernel<T, FMT, true><<<grid, kQuantThreads, 0, stream>>>(o, out, y_row, vec_codes, shift);
       return cudaGetLastError();
     };
     switch (q->format) {

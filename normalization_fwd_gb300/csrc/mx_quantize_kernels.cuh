@@ -53,12 +53,29 @@ struct LaneRows {
   }
 };
 
+// Rows that start anywhere: a warp's 256 values, lane after lane from one element
+// to the next, through shared memory to or from the 8 of each lane (8 elements a
+// lane, each of them 16 bytes from the next lane's, take 16 sectors an access).
+// f(row, col, place) for each of a lane's eight elements in that order.
+template <typename F>
+__device__ __forceinline__ void each_element(int64_t row, int64_t col, int shift, F f) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row0 = row - (lane >> shift), col0 = col - (lane & ((1 << shift) - 1)) * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = i * 32 + lane;
+    f(row0 + (e >> (shift + 3)), col0 + (e & ((8 << shift) - 1)), e);
+  }
+}
+
 // Blocks of 16, 32 or 128 columns. A warp's rows end together (the loop's test is
 // by all of them), as its lanes work on blocks together. Two rows at a time, so
 // that one is on its way while the other is worked on.
-template <typename T, int FMT>
+template <typename T, int FMT, bool RAGGED>
 __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantArgs a, int shift) {
   using F = Format<FMT>;
+  __shared__ __align__(16) T buffer[RAGGED ? kQuantThreads / 32 : 1][RAGGED ? 256 : 8];
+  T* buf = buffer[RAGGED ? threadIdx.x >> 5 : 0];
   const QuantOut& q = a.q;
   const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
   const LaneRows at(shift);
@@ -67,13 +84,24 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
   const bool pads = FMT != MX_FP8_BLOCK && blockIdx.x == 0;
   const bool bytes = FMT == MX_FP8_BLOCK && (q.pitch % 8 != 0 || !a.vec_codes);
   const int most = (int)min((int64_t)8, q.cols - col);
-  const bool vec = a.vec != 0 && col + 8 <= q.cols;
+  const bool vec = col + 8 <= q.cols;
   const int64_t step = scale_step<FMT>(col / F::width);
   const int64_t x_step = at.step * a.x_row, code_step = at.step * q.pitch;
   int64_t row = at.row;
   const T* x = static_cast<const T*>(a.x) + row * a.x_row + col;
   unsigned char* codes = q.codes + row * q.pitch + (F::four ? col / 2 : col);
   const auto load = [&](int64_t r, const T* p, float2* v) {
+    if (RAGGED) {
+      __syncwarp();
+      each_element(r, col, shift, [&](int64_t er, int64_t ec, int e) {
+        buf[e] = er < q.rows && ec < q.cols ? static_cast<const T*>(a.x)[er * a.x_row + ec] : from_f<T>(0.f);
+      });
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8 / Vec<T>::N; ++i)
+        unpack2<T>(reinterpret_cast<const uint4*>(buf + (threadIdx.x & 31) * 8)[i], v + i * Vec<T>::N / 2);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = splat2(0.f);
     if (r >= q.rows) return;
@@ -436,23 +464,26 @@ __global__ void __launch_bounds__(kQuantThreads, 2)
 }
 
 // Values, 8 columns a lane. FMT 0: the formats with fp32 scales.
-template <typename T, int FMT>
+template <typename T, int FMT, bool RAGGED>
 __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q, T* y, int64_t y_row,
-                                                                bool vec, bool vec_codes, int shift) {
+                                                                bool vec_codes, int shift) {
   constexpr bool FOUR = FMT >= MX_MXFP4;
+  __shared__ __align__(16) T buffer[RAGGED ? kQuantThreads / 32 : 1][RAGGED ? 256 : 8];
+  T* buf = buffer[RAGGED ? threadIdx.x >> 5 : 0];
   const LaneRows at(shift);
   const int64_t col = at.col;
-  if (col >= q.cols) return;
+  if (!RAGGED && col >= q.cols) return;
   const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f, r_mul = 1.0f / mul;
   const int64_t block = FMT == MX_FP8_ROW ? (q.fmt == MX_FP8_ROW ? 0 : col >> 7) : col / Format<FMT>::width;
-  const int most = (int)min((int64_t)8, q.cols - col);
-  vec = vec && most == 8;
+  const int most = (int)max((int64_t)0, min((int64_t)8, q.cols - col));
 #pragma unroll 2
-  for (int64_t row = at.row; row < q.rows; row += at.step) {
+  for (int64_t row = at.row; RAGGED ? __any_sync(0xffffffffu, row < q.rows) : row < q.rows; row += at.step) {
+    const bool here = !RAGGED || (row < q.rows && most > 0);
     const unsigned char* codes = q.codes + row * q.pitch + (FOUR ? col / 2 : col);
     float2 v[4];
-    float s;
-    if (FMT == MX_FP8_ROW) {
+    float s = 0.f;
+    if (!here) {
+    } else if (FMT == MX_FP8_ROW) {
       s = static_cast<const float*>(q.scales)[row * q.blocks + block];
     } else {
       const unsigned b = static_cast<const unsigned char*>(q.scales)[scale_at(row, block, q.blocks)];
@@ -462,10 +493,11 @@ __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q
         s = b == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(b ? b << 23 : 1u << 22);
     }
     if (FOUR) {
-      fp4_values(*reinterpret_cast<const unsigned*>(codes), v);
+      fp4_values(here ? *reinterpret_cast<const unsigned*>(codes) : 0u, v);
     } else {
       unsigned w[2] = {0, 0};
-      if (vec_codes) {
+      if (!here) {
+      } else if (vec_codes && most == 8) {
         const uint2 u = *reinterpret_cast<const uint2*>(codes);
         w[0] = u.x;
         w[1] = u.y;
@@ -496,15 +528,26 @@ __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q
         for (int j = 0; j < 4; ++j) v[j] = d[j];
       }
     }
-    T* out = y + row * y_row + col;
-    if (vec) {
+    if (!RAGGED) {
+      T* out = y + row * y_row + col;
+      if (most == 8) {
 #pragma unroll
-      for (int j = 0; j < 8 / Vec<T>::N; ++j) st_vec(out + j * Vec<T>::N, pack2<T>(v + j * Vec<T>::N / 2));
+        for (int j = 0; j < 8 / Vec<T>::N; ++j) st_vec(out + j * Vec<T>::N, pack2<T>(v + j * Vec<T>::N / 2));
+      } else {
+        const float* f = reinterpret_cast<const float*>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < most) out[j] = from_f<T>(f[j]);
+      }
     } else {
-      const float* f = reinterpret_cast<const float*>(v);
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < most) out[j] = from_f<T>(f[j]);
+      for (int j = 0; j < 8 / Vec<T>::N; ++j)
+        reinterpret_cast<uint4*>(buf + (threadIdx.x & 31) * 8)[j] = pack2<T>(v + j * Vec<T>::N / 2);
+      __syncwarp();
+      each_element(row, col, shift, [&](int64_t er, int64_t ec, int e) {
+        if (er < q.rows && ec < q.cols) y[er * y_row + ec] = buf[e];
+      });
     }
   }
 }
