@@ -39,7 +39,7 @@ int class_of(int fmt) { return fmt == MX_FP8_ROW ? 0 : mx_four(fmt) ? 2 : 1; }
 // 32 x 2 against 5.7 as 8 x 5, 512 x 1000 fp32 3.6 as a CTA of two vectors a
 // thread against 4.5 of four; 8192 x 320, which is not few, 7.3 against 6.1).
 struct NormPlan {
-  int lanes = -1, n = 0, block = kScalarCta;
+  int lanes = -1, n = 0, block = 256;
 };
 NormPlan norm_plan(int slots, int least_lanes, bool few) {
   NormPlan p;
@@ -217,13 +217,17 @@ ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, con
     if (e != cudaSuccess) return cuda_fail(e);
     p = norm_plan((int)slots, q->format == MX_FP8_BLOCK ? 128 / per : 8, rows * slots <= (int64_t)sms * 1024);
   }
+  if (!vec && hidden > 128 * kChunks) {
+    p.lanes = -2;
+    p.block = (int)((hidden + 128 * kChunks - 1) / (128 * kChunks)) * 32;
+  }
   const void* fn = dtype == LN_F32 ? mx_norm_table_f32(cls, p.lanes, p.n)
                    : dtype == LN_BF16 ? mx_norm_table_bf16(cls, p.lanes, p.n)
                                       : mx_norm_table_f16(cls, p.lanes, p.n);
   int64_t grid = a.padded_rows;
-  size_t smem = 0;
   if (p.lanes > 0) grid = (a.padded_rows + 256 / p.lanes - 1) / (256 / p.lanes);
-  if (p.lanes < 0) smem = (size_t)(hidden + 127) / 128 * 512;
+  if (p.lanes == -1) grid = (a.padded_rows + 7) / 8;
+  const size_t smem = p.lanes < 0 && cls != 0 ? (size_t)p.block / 32 * kChunks * 128 * sizeof(float) : 0;
   void* args[] = {&a};
   const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(p.block), args, smem, stream);
   return e == cudaSuccess ? LN_OK : cuda_fail(e);

@@ -196,95 +196,146 @@ __global__ void __launch_bounds__(kMaxFitThreads) __maxnreg__(N <= 4 ? 64 : 128)
       });
 }
 
-// Any hidden size and alignment: a CTA a row, the row in shared memory, four
-// columns a lane when it comes to the codes. Dynamic shared memory: hidden
-// floats, rounded up to 128.
-template <typename T>
-__global__ void __launch_bounds__(kScalarCta) mx_norm_scalar_kernel(const MxNormArgs a) {
-  extern __shared__ float srow[];
-  __shared__ float red[kScalarCta / 32];
-  __shared__ unsigned red_max[kScalarCta / 32];
+// Rows that start anywhere, of any hidden size: element by element, a warp's lanes
+// on neighbouring columns, so that it still reads and writes runs of its lanes. A
+// warp has chunks of 128 columns, four columns 32 apart a lane, up to kChunks of
+// them. For the blocks they change places through shared memory (512 floats a
+// warp, dynamic), to 8 neighbouring columns a lane: with a scale worked out for
+// each access, a column a lane, 8192 x 5121 bf16 to nvfp4 took 442 us.
+// WARP: a warp a row (up to 512 columns), 8 rows a CTA; else a CTA a row.
+constexpr int kChunks = 4;
+
+template <typename T, bool WARP>
+__global__ void __launch_bounds__(kMaxFitThreads) mx_norm_ragged_kernel(const MxNormArgs a) {
+  extern __shared__ float turned[];
+  __shared__ float red[2][kMaxFitWarps];
+  __shared__ unsigned red_max[kMaxFitWarps];
   const FwdArgs& f = a.f;
-  const int H = f.hidden;
-  const T* x = static_cast<const T*>(f.x);
-  const T* res = static_cast<const T*>(f.residual);
-  const T* bias = static_cast<const T*>(f.bias);
-  const T* gamma = static_cast<const T*>(f.gamma);
-  const T* beta = static_cast<const T*>(f.beta);
-  T* out_sum = static_cast<T*>(f.out_sum);
-  T* y = static_cast<T*>(f.y);
-  const float mul = mul_of(a.q);
-  const int chunks = (H + 127) / 128;
-  for (int64_t row = blockIdx.x; row < a.padded_rows; row += gridDim.x) {
-    if (mx_tiled(a.q.fmt)) put_padding(a.q, row, threadIdx.x, kScalarCta);
-    if (row >= f.rows) continue;
-    const int64_t off = row * (int64_t)H;
-    float t1 = 0.f;
-    for (int j = threadIdx.x; j < H; j += kScalarCta) {
-      float s = to_f(x[off + j]);
-      if (bias) s += to_f(bias[j]);
-      if (res) s += to_f(res[off + j]);
-      const T st = from_f<T>(s);
-      if (out_sum) out_sum[off + j] = st;
-      s = to_f(st);
-      srow[j] = s;
-      t1 += s;
-    }
-    const float mean = f.rms ? 0.f : cta_sum<kScalarCta>(t1, red) / (float)H;
-    float t2 = 0.f;
-    for (int j = threadIdx.x; j < H; j += kScalarCta) {
-      const float d = srow[j] - mean;
-      t2 = fmaf(d, d, t2);
-    }
-    const float rstd = 1.0f / sqrtf(cta_sum<kScalarCta>(t2, red) / (float)H + f.eps);
-    if (threadIdx.x == 0) {
-      if (f.mean) f.mean[row] = mean;
-      if (f.rstd) f.rstd[row] = rstd;
-    }
-    unsigned m = 0;
-    for (int j = threadIdx.x; j < chunks * 128; j += kScalarCta) {
-      float o = 0.f;
-      if (j < H) {
-        const float w = f.zero_centered ? 1.0f + to_f(gamma[j]) : to_f(gamma[j]);
-        o = fmaf((srow[j] - mean) * rstd, w, beta ? to_f(beta[j]) : 0.f);
-        if (y) y[off + j] = from_f<T>(o);
-      }
-      srow[j] = o;
-      m = max(m, abs_bits(o));
-    }
-    if (a.q.fmt == MX_FP8_ROW) {
-      m = __reduce_max_sync(0xffffffffu, m);
-      if ((threadIdx.x & 31) == 0) red_max[threadIdx.x >> 5] = m;
-    }
-    __syncthreads();
-    if (a.q.fmt == MX_FP8_ROW) {
-      m = 0;
-      for (int i = 0; i < kScalarCta / 32; ++i) m = max(m, red_max[i]);
-      const BlockScale b = scale_fp32(m);
-      if (threadIdx.x == 0) static_cast<float*>(a.q.scales)[row] = b.scale;
-      for (int j = threadIdx.x; j < H; j += kScalarCta)
-        a.q.codes[off + j] = b.factor == 0.f ? 0 : fp8_one(srow[j], b.factor);
-    } else {
-      const int lane = threadIdx.x & 31;
-      const auto blocks = [&](auto fmt) {
-        using F = decltype(fmt);
-        unsigned char *scales = scales_of_row<F::value>(a.q, row), *codes = a.q.codes + row * a.q.pitch;
-        const int wide = (int)a.q.pitch * (F::four ? 2 : 1);
-        for (int c = threadIdx.x >> 5; c < chunks; c += kScalarCta / 32) {
-          const int col = c * 128 + lane * 4;
-          float2 v[2] = {make_float2(srow[col], srow[col + 1]), make_float2(srow[col + 2], srow[col + 3])};
-          put_block<4, F::value>(v, mul, codes + (F::four ? col / 2 : col), col < wide,
-                                 scales + scale_step<F::value>(col / F::width), col % F::width == 0 && col < H,
-                                 min(4, wide - col), true);   // rows of MX_FP8_BLOCK start anywhere
-        }
-      };
-      if (a.q.fmt == MX_NVFP4) blocks(Format<MX_NVFP4>());
-      else if (a.q.fmt == MX_MXFP4) blocks(Format<MX_MXFP4>());
-      else if (a.q.fmt == MX_MXFP8) blocks(Format<MX_MXFP8>());
-      else blocks(Format<MX_FP8_BLOCK>());
-    }
-    __syncthreads();
+  const QuantOut& q = a.q;
+  const int H = f.hidden, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = WARP ? 1 : (int)(blockDim.x >> 5), mine = WARP ? 0 : warp;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+  if (mx_tiled(q.fmt) && row < a.padded_rows) put_padding(q, row, mine * 32 + lane, warps * 32);
+  if (row >= f.rows) return;      // a whole warp, or a whole CTA
+  const int64_t off = row * (int64_t)H;
+  const T *x = static_cast<const T*>(f.x) + off, *res = f.residual ? static_cast<const T*>(f.residual) + off : nullptr;
+  const T *bias = static_cast<const T*>(f.bias), *gamma = static_cast<const T*>(f.gamma), *beta = static_cast<const T*>(f.beta);
+  T *out_sum = f.out_sum ? static_cast<T*>(f.out_sum) + off : nullptr, *y = f.y ? static_cast<T*>(f.y) + off : nullptr;
+  int parity = 0;
+  const auto reduce = [&](float v) { return WARP ? group_sum<32>(v) : cta_sum_db_fit(v, red, parity); };
+  // column of slot i, s
+  const auto column = [&](int i, int s) { return (i * warps + mine) * 128 + 32 * s + lane; };
+  float v[kChunks][4], u[kChunks][4];
+  float t = 0.f;
+  // each of these loops has its loads on their way together: what is stored
+  // could, as far as the compiler knows, be what is loaded next
+  const auto load = [&](const T* p, float (*to)[4]) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) to[i][s] = column(i, s) < H ? to_f(__ldg(p + column(i, s))) : 0.f;
+  };
+  load(x, v);
+  if (res) load(res, u);
+  if (bias) {
+    float b[kChunks][4];
+    load(bias, b);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[i][s] += b[i][s];
   }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int j = column(i, s);
+      const T stored = from_f<T>(res ? v[i][s] + u[i][s] : v[i][s]);
+      if (out_sum && j < H) out_sum[j] = stored;
+      v[i][s] = to_f(stored);
+      t += v[i][s];
+    }
+  const float mean = f.rms ? 0.f : reduce(t) / (float)H;
+  t = 0.f;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (column(i, s) < H) {
+        v[i][s] -= mean;
+        t = fmaf(v[i][s], v[i][s], t);
+      }
+  const float rstd = 1.0f / sqrtf(reduce(t) / (float)H + f.eps);
+  if (mine == 0 && lane == 0) {
+    if (f.mean) f.mean[row] = mean;
+    if (f.rstd) f.rstd[row] = rstd;
+  }
+  unsigned m = 0;
+  load(gamma, u);
+  if (f.zero_centered) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) u[i][s] += 1.0f;
+  }
+  float b[kChunks][4] = {};
+  if (beta) load(beta, b);
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int j = column(i, s);
+      v[i][s] = j < H ? fmaf(v[i][s] * rstd, u[i][s], b[i][s]) : 0.f;
+      if (y && j < H) y[j] = from_f<T>(v[i][s]);
+      m = max(m, abs_bits(v[i][s]));
+    }
+  if (q.fmt == MX_FP8_ROW) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (!WARP) {
+      if (lane == 0) red_max[warp] = m;
+      __syncthreads();
+      for (int i = 0; i < warps; ++i) m = max(m, red_max[i]);
+    }
+    const BlockScale b = scale_fp32(m);
+    if (mine == 0 && lane == 0) static_cast<float*>(q.scales)[row] = b.scale;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (column(i, s) < H) q.codes[off + column(i, s)] = b.factor == 0.f ? 0 : fp8_one(v[i][s], b.factor);
+    return;
+  }
+  const float mul = mul_of(q);
+  float* place = turned + warp * (kChunks * 128);
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) place[i * 128 + 32 * s + lane] = v[i][s];
+  __syncwarp();
+  const auto blocks = [&](auto fmt) {
+    using F = decltype(fmt);
+    unsigned char *scales = scales_of_row<F::value>(q, row), *codes = q.codes + row * q.pitch;
+    const int wide = (int)q.pitch * (F::four ? 2 : 1);
+#pragma unroll
+    for (int k = 0; k < kChunks / 2; ++k) {
+      if ((2 * k * warps + mine) * 128 >= H) break;
+      const int col = ((2 * k + lane / 16) * warps + mine) * 128 + lane % 16 * 8;
+      float2 o[4];
+      const float4* from = reinterpret_cast<const float4*>(place + k * 256 + lane * 8);
+      const float4 lo = from[0], hi = from[1];
+      o[0] = make_float2(lo.x, lo.y);
+      o[1] = make_float2(lo.z, lo.w);
+      o[2] = make_float2(hi.x, hi.y);
+      o[3] = make_float2(hi.z, hi.w);
+      put_block<8, F::value>(o, mul, codes + (F::four ? col / 2 : col), col < wide,
+                             scales + scale_step<F::value>(col / F::width), col % F::width == 0 && col < H,
+                             min(8, wide - col), true);
+    }
+  };
+  if (q.fmt == MX_NVFP4) blocks(Format<MX_NVFP4>());
+  else if (q.fmt == MX_MXFP4) blocks(Format<MX_MXFP4>());
+  else if (q.fmt == MX_MXFP8) blocks(Format<MX_MXFP8>());
+  else blocks(Format<MX_FP8_BLOCK>());
 }
 
 template <typename T, int LANES, int CLS> const void* mx_norm_tile_of(int n) {
@@ -308,7 +359,8 @@ template <typename T, int CLS> const void* mx_norm_cta_of(int n) {
     default: return nullptr;
   }
 }
-// lanes 8, 16, 32: a lane group a row; 0: a CTA a row; -1: the scalar kernel.
+// lanes 8, 16, 32: a lane group a row; 0: a CTA a row; -1, -2: element by element,
+// a warp or a CTA a row.
 template <typename T, int CLS> const void* mx_norm_cls(int lanes, int n) {
   switch (lanes) {
     case 8: return mx_norm_tile_of<T, 8, CLS>(n);
@@ -318,7 +370,8 @@ template <typename T, int CLS> const void* mx_norm_cls(int lanes, int n) {
   }
 }
 template <typename T> const void* mx_norm_table(int cls, int lanes, int n) {
-  if (lanes < 0) return (const void*)mx_norm_scalar_kernel<T>;
+  if (lanes == -1) return (const void*)mx_norm_ragged_kernel<T, true>;
+  if (lanes == -2) return (const void*)mx_norm_ragged_kernel<T, false>;
   return cls == 0 ? mx_norm_cls<T, 0>(lanes, n) : cls == 1 ? mx_norm_cls<T, 1>(lanes, n)
                                                           : mx_norm_cls<T, 2>(lanes, n);
 }

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
   const T* x = static_cast<const T*>(a.x) + row * a.x_row + col;
   unsigned char* codes = q.codes + row * q.pitch + (F::four ? col / 2 : col);
   const auto load = [&](int64_t r, const T* p, float2* v) {
-    if (RAGGED) {
+    if constexpr (RAGGED) {
       __syncwarp();
       each_element(r, col, shift, [&](int64_t er, int64_t ec, int e) {
         buf[e] = er < q.rows && ec < q.cols ? static_cast<const T*>(a.x)[er * a.x_row + ec] : from_f<T>(0.f);
@@ -100,19 +100,19 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
 #pragma unroll
       for (int i = 0; i < 8 / Vec<T>::N; ++i)
         unpack2<T>(reinterpret_cast<const uint4*>(buf + (threadIdx.x & 31) * 8)[i], v + i * Vec<T>::N / 2);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = splat2(0.f);
-    if (r >= q.rows) return;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < 8 / Vec<T>::N; ++i) unpack2<T>(ld_vec(p + i * Vec<T>::N), v + i * Vec<T>::N / 2);
     } else {
-      float* f = reinterpret_cast<float*>(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < most) f[i] = to_f(p[i]);
+      for (int i = 0; i < 4; ++i) v[i] = splat2(0.f);
+      if (r >= q.rows) return;
+      if (vec) {
+#pragma unroll
+        for (int i = 0; i < 8 / Vec<T>::N; ++i) unpack2<T>(ld_vec(p + i * Vec<T>::N), v + i * Vec<T>::N / 2);
+      } else {
+        float* f = reinterpret_cast<float*>(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < most) f[i] = to_f(p[i]);
+      }
     }
   };
   const auto put = [&](int64_t r, unsigned char* c, float2* v) {
