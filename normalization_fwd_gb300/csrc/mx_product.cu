@@ -121,8 +121,9 @@ cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// *placed: false where the device does not place a pair of CTAs of this size.
 template <typename T, int FMT, int WN>
-cudaError_t launch_pairs(ProductArgs p, int sms, cudaStream_t st) {
+cudaError_t launch_pairs(ProductArgs p, int sms, cudaStream_t st, bool* placed) {
   const void* fn = (const void*)product_pair_kernel<T, FMT, WN>;
   p.tiles_m = (int)((p.a.rows + 255) / 256);
   p.tiles_n = (int)((p.b.rows + WN - 1) / WN);
@@ -154,6 +155,8 @@ cudaError_t launch_pairs(ProductArgs p, int sms, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  e = places(fn, cfg, 2, placed);
+  if (e != cudaSuccess || !*placed) return e;
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
@@ -166,13 +169,17 @@ cudaError_t launch_format(ProductArgs p, int sms, cudaStream_t st) {
     p.cols = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64;
     return launch_tiles<T, FMT, true>(p, sms, st);
   }
-  // Pairs of CTAs from where single tiles are more than the SMs; tiles of 256
-  // columns where they take no more rounds than twice as many of half the width.
+  // Pairs of CTAs from where single tiles are more than the SMs (4096 x 4096 x 8192
+  // nvfp4 60 us, before that 120 as single tiles); tiles of 256 columns unless
+  // they take more than 5 rounds for 8 of half the width: a tile of 128 takes some
+  // five eighths of one of 256, as its operands are copied for half the results.
   const int64_t tm = (p.a.rows + 255) / 256, tn = (p.b.rows + 127) / 128, pairs = sms / 2;
   if (p.a.rows > 128 && pairs > 0 && tm * tn * 2 > sms) {
     const int64_t narrow = (tm * tn + pairs - 1) / pairs, wide = (tm * ((tn + 1) / 2) + pairs - 1) / pairs;
-    if (wide * 8 <= narrow * 5) return launch_pairs<T, FMT, 256>(p, sms, st);
-    return launch_pairs<T, FMT, 128>(p, sms, st);
+    bool placed = false;
+    const cudaError_t e = wide * 8 <= narrow * 5 ? launch_pairs<T, FMT, 256>(p, sms, st, &placed)
+                                                 : launch_pairs<T, FMT, 128>(p, sms, st, &placed);
+    if (e != cudaSuccess || placed) return e;
   }
   p.cols = 128;
   return launch_tiles<T, FMT, false>(p, sms, st);

@@ -1,0 +1,159 @@
+"""Quantised operators where offsets pass 2^31 elements, into buffers that hold
+something already, on expanded inputs, and the fast and the general way through
+the binding."""
+
+import numpy as np
+import pytest
+import torch
+
+from _blocks import f64
+from _mx import FORMATS, TILED, check_bits, on_gpu
+from oracle import mx
+
+pytestmark = pytest.mark.gpu
+
+
+def raw(q):
+    return q.codes.view(torch.uint8), q.scales.view(torch.uint8)
+
+
+@pytest.mark.parametrize("fmt", ["fp8_row", "mxfp8", "nvfp4"])
+def test_rows_past_2_31_elements(cuda_lib, fmt):
+    """The last rows of a matrix of 2^31 elements and more are those of the same
+    rows alone: norm, quantiser (both ways round) and inverse."""
+    nf = cuda_lib
+    rows, hidden = (1 << 18) + 133, 8192
+    x = torch.empty(rows, hidden, device="cuda", dtype=torch.bfloat16)
+    x[:] = torch.randn(hidden, device="cuda").to(torch.bfloat16)
+    x[-256:] = torch.randn(256, hidden, device="cuda").to(torch.bfloat16)
+    g = torch.ones(hidden, device="cuda", dtype=torch.bfloat16)
+    tail = x[-5:].clone()        # rows of a last, partly filled tile of 128
+    whole = nf.fused_norm_quant_fwd(x, g, format=fmt, mode="rmsnorm")["q"]
+    part = nf.fused_norm_quant_fwd(tail, g, format=fmt, mode="rmsnorm")["q"]
+    assert torch.equal(raw(whole)[0][-5:], raw(part)[0])
+    assert torch.equal(nf.dequantize(whole, torch.bfloat16)[-5:], nf.dequantize(part, torch.bfloat16))
+    del whole
+    whole, part = nf.quantize(x, fmt), nf.quantize(tail, fmt)
+    assert torch.equal(raw(whole)[0][-5:], raw(part)[0])
+    del whole
+    # 128 columns of the transpose from the last tile of x's rows
+    t = nf.dequantize(nf.quantize(x, fmt, transpose=True), torch.bfloat16)
+    if fmt != "fp8_row":         # blocks along the rows: the last ones begin at a multiple of 32
+        last = rows // 32 * 32
+        want = nf.dequantize(nf.quantize(x[last:], fmt, transpose=True), torch.bfloat16)
+        assert torch.equal(t[:, last:], want)
+
+
+@pytest.mark.parametrize("fmt", TILED)
+def test_product_past_2_31_elements(cuda_lib, fmt):
+    nf = cuda_lib
+    M, N, K = (1 << 18) + 300, 8200, 64
+    a = torch.randn(M, K, device="cuda")
+    b = nf.quantize(torch.randn(N, K, device="cuda"), fmt)
+    r = nf.scaled_product(nf.quantize(a, fmt), b, partials=True)
+    part = nf.scaled_product(nf.quantize(a[-4:], fmt), b, partials=True)
+    for k in ("out", "psum"):
+        assert torch.equal(r[k][-4:], part[k]), k
+    assert nf.ln_device_error() == 0
+
+
+@pytest.mark.parametrize("hidden", [96, 320, 1001, 2560])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_norm_writes_all_of_its_buffers_and_nothing_else(cuda_lib, fmt, hidden):
+    nf = cuda_lib
+    x, g = torch.randn(37, hidden, device="cuda"), torch.ones(hidden, device="cuda")
+    nbytes = nf.mx_matrix_bytes(fmt, 37, hidden)
+    bufs = [torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda") for n in nbytes]
+    e = nf.quantized_empty(37, hidden, fmt)
+    views = [b[32:32 + n].view(t.dtype).view(t.shape) for b, n, t in zip(bufs, nbytes, (e.codes, e.scales))]
+    q = nf.Quantized(*views, fmt, 37, hidden)
+    y, rstd = torch.empty_like(x), torch.empty(37, device="cuda")
+    nf.mx_norm_fwd(x, None, None, g, None, 1e-5, "rmsnorm", False, None, y, None, rstd, q)
+    check_bits(q, f64(y), fmt)
+    for b in bufs:
+        assert bool((b[:32] == 255).all()) and bool((b[-32:] == 255).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_expanded_input_transposed(cuda_lib, fmt):
+    nf = cuda_lib
+    x = torch.randn(1, 100, device="cuda").expand(300, 100)
+    check_bits(nf.quantize(x, fmt, transpose=True), f64(x.T), fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_both_ways_through_the_binding(cuda_lib, fmt):
+    """A call that allocates in C++ and one that goes through the checks in
+    Python (a stream given, outputs given) give the same bytes."""
+    nf = cuda_lib
+    x, r = (torch.randn(50, 320, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    g = torch.ones(320, device="cuda", dtype=torch.bfloat16)
+    b = torch.randn(320, device="cuda", dtype=torch.bfloat16)
+    mul = on_gpu(20.0) if fmt == "nvfp4" else None
+    here = torch.cuda.current_stream()
+    kw = dict(format=fmt, mul=mul, bias=b, residual=r, store_y=True)
+    one, two = (nf.fused_norm_quant_fwd(x, g, b, stream=s, **kw) for s in (None, here))
+    for k in ("sum", "y", "mean", "rstd"):
+        assert torch.equal(one[k], two[k]), k
+    assert one["q"][2:5] == two["q"][2:5]
+    for t in (False, True):
+        p, q = (nf.quantize(x, fmt, mul=mul, transpose=t, stream=s) for s in (None, here))
+        assert p.codes.shape == q.codes.shape and p.codes.dtype == q.codes.dtype and p.scales.dtype == q.scales.dtype
+        assert all(torch.equal(u, v) for u, v in zip(raw(p), raw(q)))
+        assert torch.equal(nf.dequantize(p, torch.float16), nf.dequantize(q, torch.float16, stream=here))
+    if fmt in TILED:
+        w = nf.quantize(torch.randn(70, 320, device="cuda"), fmt, mul=mul)
+        res, bias = torch.randn(50, 70, device="cuda", dtype=torch.float16), torch.randn(70, device="cuda", dtype=torch.float16)
+        kw = dict(alpha=0.5, bias=bias, residual=res, dtype=torch.float16, partials=True)
+        p, q = (nf.scaled_product(one["q"], w, stream=s, **kw) for s in (None, here))
+        for k in ("out", "psum", "psq"):
+            assert torch.equal(p[k], q[k]), k
+    out = nf.fused_norm_fwd(x, g, b)["y"]
+    psum = x.float().sum(dim=1, keepdim=True)
+    psq = ((x.float() - psum / 320) ** 2).sum(dim=1, keepdim=True)
+    p, q = (nf.fused_norm_fwd_from_partials(x, psum, psq, 320, g, b, kind="sum_m2", stream=s) for s in (None, here))
+    assert torch.equal(p["y"], q["y"]) and torch.equal(p["rstd"], q["rstd"]) and out.shape == p["y"].shape
+
+
+def test_refusals_of_the_binding_on_the_gpu(cuda_lib):
+    nf = cuda_lib
+    x = torch.randn(8, 64, device="cuda")
+    q, p = nf.quantize(x, "mxfp8"), nf.quantize(x, "mxfp4")
+    for call, what in (
+            (lambda: nf.scaled_product(q, p), nf.NormError),
+            (lambda: nf.scaled_product(q, nf.quantize(x[:, :32], "mxfp8")), nf.NormError),
+            (lambda: nf.scaled_product(nf.quantize(x, "fp8_row"), nf.quantize(x, "fp8_row")), nf.NormError),
+            (lambda: nf.scaled_product(q, q, alpha=float("nan")), nf.NormError),
+            (lambda: nf.scaled_product(q, q, bias=torch.zeros(8, device="cuda")), ValueError),      # fp32 with bf16
+            (lambda: nf.scaled_product(q, q, residual=torch.zeros(8, 9, device="cuda")), ValueError),
+            (lambda: nf.scaled_product(q, q, out=torch.zeros(8, 9, device="cuda")), ValueError),
+            (lambda: nf.scaled_product(q, q, dtype=torch.float64), TypeError),
+            (lambda: nf.dequantize(q, torch.int32), TypeError),
+            (lambda: nf.dequantize(q, out=torch.zeros(7, 64, device="cuda")), ValueError),
+            (lambda: nf.quantize(x.double(), "mxfp8"), TypeError),
+            (lambda: nf.quantize(x.T, "mxfp8"), ValueError),
+            (lambda: nf.quantize(x[None], "mxfp8"), ValueError),
+            (lambda: nf.quantize(x, "int8"), ValueError),
+            (lambda: nf.quantize(x, "nvfp4", mul=torch.ones(2, device="cuda")), ValueError),
+            (lambda: nf.fused_norm_quant_fwd(x, x[0, :32], format="mxfp8"), ValueError),
+            (lambda: nf.fused_norm_quant_fwd(x, x[0], format="mxfp8", residual=x[:4]), ValueError),
+            (lambda: nf.fused_norm_quant_fwd(x, x[0], format="mxfp8", eps=-1.0), nf.NormError),
+            (lambda: nf.fused_norm_quant_fwd(x.T, x[0], format="mxfp8"), ValueError),
+            (lambda: nf.fused_norm_quant_fwd(x, x[0].cpu(), format="mxfp8"), ValueError)):
+        with pytest.raises(what):
+            call()
+
+
+def test_overflow_and_tiny_values_come_back(cuda_lib):
+    """Values past what fp16 holds, and factors that leave fp32's range."""
+    nf = cuda_lib
+    x = torch.tensor([[3.0e38, 1.0, -2.0e38, 0.0] * 8], device="cuda")
+    q = nf.quantize(x, "mxfp8")
+    assert bool(nf.dequantize(q, torch.float16)[0, 0].isinf())
+    codes, scales, _ = mx.quantize(f64(x), "mxfp8")
+    assert np.array_equal(f64(nf.dequantize(q)), mx.values(codes, scales, "mxfp8"))
+    n = nf.quantize(torch.full((1, 32), 1e-30, device="cuda"), "nvfp4", mul=on_gpu(1e30))
+    assert torch.allclose(nf.dequantize(n), torch.full((1, 32), 1e-30, device="cuda"), rtol=0.07, atol=0)
+    big = nf.Quantized(n.codes, n.scales, "nvfp4", 1, 32, on_gpu(1e-39))
+    v = nf.dequantize(big)
+    assert bool(torch.isinf(v).all())
