@@ -6,7 +6,11 @@
 // is quantised as it is (rounding it to the I/O type first would round twice).
 // A block's values lie in 2 to 32 neighbouring lanes, so its largest magnitude
 // takes 1 to 5 shuffles; a row's goes through the CTA as the sums do.
-// Bound by HBM: x and residual read, the sum and 0.5 to 1 bytes a value written.
+//
+// What bounds it: HBM (x and residual read, the sum and 0.5 to 1 bytes a value
+// written) and, with block scales, the instructions: 16384 x 8192 bf16 RMSNorm
+// with a residual takes 138 us to fp8_row (6.8 TB/s), 145 to mxfp8 (6.5), 157 to
+// nvfp4 (5.6 TB/s, 81% of the issue slots).
 #pragma once
 
 #include "bulk.cuh"

@@ -169,10 +169,12 @@ cudaError_t launch_format(ProductArgs p, int sms, cudaStream_t st) {
     p.cols = p.a.rows <= 16 ? 16 : p.a.rows <= 32 ? 32 : 64;
     return launch_tiles<T, FMT, true>(p, sms, st);
   }
-  // Pairs of CTAs from where single tiles are more than the SMs (4096 x 4096 x 8192
-  // nvfp4 60 us, before that 120 as single tiles); tiles of 256 columns unless
-  // they take more than 5 rounds for 8 of half the width: a tile of 128 takes some
-  // five eighths of one of 256, as its operands are copied for half the results.
+  // Pairs of CTAs from where single tiles are more than the SMs (nvfp4 4096 x 4096
+  // x 8192 51 us against 98 as single tiles, 512 x 8192 x 8192 20 against 29; 256
+  // x 8192 x 8192, 128 tiles, 15.3 single against 18.7). Tiles of 256 columns
+  // unless they take more than 5 rounds for 8 of half the width (the first 51 us
+  // against 73, mxfp8 2100 x 2300 x 800 20.4 against 19.3): a tile of 128 takes
+  // some five eighths of one of 256, as its operands are copied for half the results.
   const int64_t tm = (p.a.rows + 255) / 256, tn = (p.b.rows + 127) / 128, pairs = sms / 2;
   if (p.a.rows > 128 && pairs > 0 && tm * tn * 2 > sms) {
     const int64_t narrow = (tm * tn + pairs - 1) / pairs, wide = (tm * ((tn + 1) / 2) + pairs - 1) / pairs;

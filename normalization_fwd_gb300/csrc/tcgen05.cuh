@@ -220,11 +220,10 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
       : "memory");
 }
 // Arrival on a barrier of any CTA of the cluster (it publishes no memory: with
-// release.cluster it waited for the results' stores before it, 1700 cycles a
-// tile), and a wait that sees what came before arrivals of other CTAs. The waits of one thread follow each other
-// every few hundred cycles here, so their limit is counted in cycles (about a
-// second): reading the global timer in each held up the ring by a microsecond
-// a chunk (4096 x 4096 x 8192: 147 us with it).
+// release.cluster it waited for the results' stores before it, some 1000 cycles a
+// tile), and a wait that sees what came before arrivals of other CTAs. The waits
+// of one warp follow each other every few hundred cycles here, so their limit is
+// counted in cycles (about a second).
 constexpr long long kWaitLimitCycles = 2000000000ll;
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
   uint32_t done;
