@@ -151,8 +151,9 @@ typedef enum {
  * 37, gemm_with_layernorm.h): the GEMM that produces the row (with the
  * residual added in its epilogue) also sums each row over the column tile
  * every threadblock owns, and the LayerNorm that follows combines those
- * partials into the row's mean and variance. The producing GEMM is not part
- * of this library; this is the consumer: one read of x, one write of y.
+ * partials into the row's mean and variance. This is the
+ * consumer, one read of x and one write of y; mx_product below is a producer of
+ * such partials (of quantised operands), any other GEMM may be.
  *
  * Column tiles are tile_cols wide from column 0; the last one holds the
  * hidden - (n_tiles - 1) * tile_cols columns left, n_tiles =
@@ -651,8 +652,9 @@ const char* ln_status_string(ln_status status);
 int ln_last_cuda_error(void);
 
 /*
- * Device-side failure report. The pipelined kernels wait on shared-memory
- * barriers for their bulk copies; every such wait gives up after one second,
+ * Device-side failure report. The pipelined kernels (the ring kernels, the
+ * product and the transposing quantiser) wait on shared-memory barriers for
+ * their copies and tensor-core work; every such wait gives up after about a second,
  * sets a bit in a device error word and lets the kernel finish early (its
  * outputs are then not valid). This call waits for `stream`, ORs the error
  * words of all kernels into *flags (bit 0: a wait timed out) and clears them.

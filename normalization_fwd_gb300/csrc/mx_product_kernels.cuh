@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_free<kTmemCols>(tmem);
   }
 
-  const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
+  const float f = p.alpha / mul_of(p.a) / mul_of(p.b);
   const int64_t m0 = (SWAP ? col_row : lane_row) + (int64_t)rank * rows_each, n0 = SWAP ? lane_row : col_row;
   for (int r = warp; r < rows_each; r += kTileThreads / 32) {
     if (m0 + r >= p.a.rows) break;
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int e = max(0, n - kBufs); e < n && ok; ++e) mbar_wait_cluster(&drained[e % kBufs], (e / kBufs) & 1);
   } else if (warp >= 4) {
     const int quarter = warp & 3, group = (warp - 4) >> 2;
-    const float f = p.alpha / (mul_of(p.a) * mul_of(p.b));
+    const float f = p.alpha / mul_of(p.a) / mul_of(p.b);
     unsigned char* piece = smem_raw + (base - smem_addr(smem_raw)) + p.stages * kStage + (warp - 4) * kPieceBytes;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {

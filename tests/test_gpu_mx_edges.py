@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from _blocks import f64
-from _mx import FORMATS, TILED, check_bits, on_gpu
+from _mx import FORMATS, TILED, check_bits, device_matrix, exact_operand, on_gpu
 from oracle import mx
 
 pytestmark = pytest.mark.gpu
@@ -52,8 +52,11 @@ def test_product_past_2_31_elements(cuda_lib, fmt):
     b = nf.quantize(torch.randn(N, K, device="cuda"), fmt)
     r = nf.scaled_product(nf.quantize(a, fmt), b, partials=True)
     part = nf.scaled_product(nf.quantize(a[-4:], fmt), b, partials=True)
-    for k in ("out", "psum"):
-        assert torch.equal(r[k][-4:], part[k]), k
+    assert torch.equal(r["out"][-4:], part["out"])
+    # few rows and many take kernels that add the 128 terms in orders of their own,
+    # each within 127 roundings of the sum
+    size = torch.nn.functional.pad(part["out"].double().abs(), (0, -N % 128)).view(4, -1, 128).sum(dim=2)
+    assert bool(((r["psum"][-4:] - part["psum"]).double().abs() <= 2 * 127 * 2.0 ** -24 * size).all())
     assert nf.ln_device_error() == 0
 
 
@@ -157,3 +160,50 @@ def test_overflow_and_tiny_values_come_back(cuda_lib):
     big = nf.Quantized(n.codes, n.scales, "nvfp4", 1, 32, on_gpu(1e-39))
     v = nf.dequantize(big)
     assert bool(torch.isinf(v).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("hidden", [1, 2, 3, 31, 33, 127, 129, 511, 513, 1025, 4097])
+def test_narrow_and_odd_rows(cuda_lib, fmt, hidden):
+    nf = cuda_lib
+    for rows in (1, 9, 130):
+        x = torch.randn(rows, hidden, device="cuda")
+        g = 1 + 0.1 * torch.randn(hidden, device="cuda")
+        r = nf.fused_norm_quant_fwd(x, g, format=fmt, mode="rmsnorm", store_y=True)
+        check_bits(r["q"], f64(r["y"]), fmt)
+        for t in (False, True):
+            check_bits(nf.quantize(x, fmt, transpose=t), f64(x.T if t else x), fmt)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(cuda_lib, seed):
+    """Sizes over the whole range, each drawn from its logarithm: products of
+    whole numbers exactly, codes and scales bit for bit."""
+    nf = cuda_lib
+    rng = np.random.default_rng(1000 + seed)
+
+    def size(top):
+        n = int(np.exp(rng.uniform(0, np.log(top))))
+        return max(1, n // (k := int(rng.choice([1, 1, 16, 128]))) * k)
+
+    fmt = TILED[seed % 3]
+    M, N, K = size(6000), size(3000), size(1500)
+    (ac, as_), (bc, bs) = exact_operand(rng, M, K, fmt), exact_operand(rng, N, K, fmt)
+    a, b = device_matrix(nf, ac, as_, fmt), device_matrix(nf, bc, bs, fmt)
+    bias = torch.from_numpy(rng.integers(-8, 9, N).astype(np.float32)).cuda()
+    res = torch.from_numpy(rng.integers(-8, 9, (M, N)).astype(np.float32)).cuda()
+    want, bound = mx.product(mx.values(ac, as_, fmt), mx.values(bc, bs, fmt), 1.0, f64(bias), f64(res))
+    assert bound.max() < 2 ** 19      # sums of sixteenths: fp32 numbers
+    r = nf.scaled_product(a, b, bias=bias, residual=res, dtype=torch.float32, partials=True)
+    assert np.array_equal(f64(r["out"]), want), (M, N, K, fmt)
+    for t in range(0, -(-N // 128), 3):
+        tile = want[:, 128 * t:128 * t + 128]
+        # sums of 128 sixteenths below 2^19 stay fp32 numbers as long as they are below 2^20
+        if np.abs(tile).sum(axis=1).max() < 2 ** 20:
+            assert np.array_equal(f64(r["psum"][:, t]), tile.sum(axis=1))
+    rows, cols, fmt = size(1200), size(3000), FORMATS[seed % 5]
+    x = torch.from_numpy(rng.standard_normal((rows, cols)).astype(np.float32)).to(
+        [torch.float32, torch.bfloat16, torch.float16][seed % 3]).cuda()
+    for t in (False, True):
+        check_bits(nf.quantize(x, fmt, transpose=t), f64(x.T if t else x), fmt)
+    assert nf.ln_device_error() == 0
