@@ -113,5 +113,30 @@ cudaError_t launch_bwd_finalize(const float* ws, int P, int C, int H, bool beta_
 
 }  // namespace nf
 
+namespace nf {
+
+// Launch a kernel that begins with start_after_stream() (mx_formats.cuh), in
+// clusters of so many CTAs: it may be scheduled while what is before it on the
+// stream ends.
+inline cudaError_t launch_overlapped(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
+                                     cudaStream_t st, int cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace nf
+
 // Record the cudaError_t that ln_last_cuda_error() reports (api.cu).
 extern "C" void nf_set_last_cuda_error(int e);

@@ -107,7 +107,7 @@ cudaError_t launch_transpose_tma(const QuantArgs& a, int64_t x, int64_t tiles, i
   int64_t all = x * tiles;
   QuantArgs args = a;
   void* params[] = {&map, &args, &all};
-  return cudaLaunchKernel(fn, dim3((unsigned)std::min<int64_t>(all, 2 * sms)), dim3(kQuantThreads), params, kSmem, st);
+  return launch_overlapped(fn, dim3((unsigned)std::min<int64_t>(all, 2 * sms)), dim3(kQuantThreads), params, kSmem, st);
 }
 
 template <typename T, int FMT>
@@ -122,17 +122,19 @@ cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStre
           x * tiles > 2 * sms)
         return launch_transpose_tma<T, FMT>(a, x, tiles, sms, st);
     const dim3 grid((unsigned)x, FMT == MX_FP8_ROW ? 1u : (unsigned)std::min<int64_t>(tiles, 65535));
-    quant_transpose_kernel<T, FMT><<<grid, kQuantThreads, 0, st>>>(a);
+    void* args[] = {const_cast<QuantArgs*>(&a)};
+    return launch_overlapped((const void*)quant_transpose_kernel<T, FMT>, grid, dim3(kQuantThreads), args, 0, st);
   } else if constexpr (FMT == MX_FP8_ROW) {
-    quant_row_kernel<T><<<(unsigned)std::min<int64_t>(q.rows, 1 << 20), kQuantThreads, 0, st>>>(a);
+    void* args[] = {const_cast<QuantArgs*>(&a)};
+    return launch_overlapped((const void*)quant_row_kernel<T>, dim3((unsigned)std::min<int64_t>(q.rows, 1 << 20)),
+                             dim3(kQuantThreads), args, 0, st);
   } else {
     // room for codes included
-    const int shift = row_shift(mx_tiled(FMT) ? (q.cols + 31) / 32 * 32 : q.cols, mx_block(FMT) / 8);
-    const dim3 grid = row_grid(a.padded_rows, q.cols, shift, sms);
-    if (a.vec) quant_block_kernel<T, FMT, false><<<grid, kQuantThreads, 0, st>>>(a, shift);
-    else quant_block_kernel<T, FMT, true><<<grid, kQuantThreads, 0, st>>>(a, shift);
+    int shift = row_shift(mx_tiled(FMT) ? (q.cols + 31) / 32 * 32 : q.cols, mx_block(FMT) / 8);
+    const void* fn = a.vec ? (const void*)quant_block_kernel<T, FMT, false> : (const void*)quant_block_kernel<T, FMT, true>;
+    void* args[] = {const_cast<QuantArgs*>(&a), &shift};
+    return launch_overlapped(fn, row_grid(a.padded_rows, q.cols, shift, sms), dim3(kQuantThreads), args, 0, st);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -229,7 +231,7 @@ ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, con
   if (p.lanes == -1) grid = (a.padded_rows + 7) / 8;
   const size_t smem = p.lanes < 0 && cls != 0 ? (size_t)p.block / 32 * kChunks * 128 * sizeof(float) : 0;
   void* args[] = {&a};
-  const cudaError_t e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(p.block), args, smem, stream);
+  const cudaError_t e = launch_overlapped(fn, dim3((unsigned)grid), dim3(p.block), args, smem, stream);
   return e == cudaSuccess ? LN_OK : cuda_fail(e);
 }
 
@@ -290,19 +292,18 @@ ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t
   int sms = 0;
   cudaError_t e = (cudaError_t)device_sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
-  const QuantOut o = quant_out(*q);
+  QuantOut o = quant_out(*q);
   const bool vec = aligned(y, 16) && (q->rows == 1 || (y_row * es) % 16 == 0);
-  const bool vec_codes = o.pitch % 8 == 0 && aligned(q->codes, 8);
-  const int shift = row_shift(q->cols, 1);
+  bool vec_codes = o.pitch % 8 == 0 && aligned(q->codes, 8);
+  int shift = row_shift(q->cols, 1);
   const dim3 grid = row_grid(q->rows, q->cols, shift, sms);
   e = by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const auto run = [&](auto fmt) {
       constexpr int FMT = decltype(fmt)::value;
-      T* out = static_cast<T*>(y);
-      if (vec) dequant_kernel<T, FMT, false><<<grid, kQuantThreads, 0, stream>>>(o, out, y_row, vec_codes, shift);
-      else dequant_kernel<T, FMT, true><<<grid, kQuantThreads, 0, stream>>>(o, out, y_row, vec_codes, shift);
-      return cudaGetLastError();
+      const void* fn = vec ? (const void*)dequant_kernel<T, FMT, false> : (const void*)dequant_kernel<T, FMT, true>;
+      void* args[] = {&o, &y, &y_row, &vec_codes, &shift};
+      return launch_overlapped(fn, grid, dim3(kQuantThreads), args, 0, stream);
     };
     switch (q->format) {
       case MX_MXFP8: return run(Format<MX_MXFP8>());

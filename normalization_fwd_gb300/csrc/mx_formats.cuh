@@ -42,6 +42,15 @@ inline __host__ __device__ int64_t mx_blocks(int fmt, int64_t cols) {
   return b == 0 ? 1 : (cols + b - 1) / b;
 }
 
+// The beginning of a kernel launched by launch_overlapped(): the next one on the
+// stream may be scheduled, and what was before this one has ended, its writes are
+// visible. Every thread calls it before it touches memory that another kernel
+// reads or writes, so that whoever waits for this grid has waited for that one.
+__device__ __forceinline__ void start_after_stream() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // A format as a type.
 template <int F> struct Format {
   static constexpr int value = F;

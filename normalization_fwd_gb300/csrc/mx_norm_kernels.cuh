@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kBulkThreads, N <= 3 ? 4 : 2) mx_norm_tile_ker
   const int lane = threadIdx.x & 31;
   const int64_t row =
       ((int64_t)blockIdx.x * kConsumerWarps + (threadIdx.x >> 5)) * RPW + lane / LANES;
+  start_after_stream();
   mx_norm_row<T, LANES, N, CLS>(
       a, row, lane % LANES, [](float v) { return group_sum<LANES>(v); },
       [](unsigned v) { return lanes_max<LANES>(v); });
@@ -183,6 +184,7 @@ template <typename T, int N, int CLS>
 __global__ void __launch_bounds__(kMaxFitThreads) __maxnreg__(N <= 4 ? 64 : 128) mx_norm_cta_kernel(const MxNormArgs a) {
   __shared__ float red[2][kMaxFitWarps];
   __shared__ unsigned red_max[kMaxFitWarps];
+  start_after_stream();
   if (blockIdx.x >= a.f.rows) {    // the scales behind the last row
     if (CLS != 0) put_padding(a.q, blockIdx.x, threadIdx.x, blockDim.x);
     return;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(kMaxFitThreads) mx_norm_ragged_kernel(const Mx
   extern __shared__ float turned[];
   __shared__ float red[2][kMaxFitWarps];
   __shared__ unsigned red_max[kMaxFitWarps];
+  start_after_stream();
   const FwdArgs& f = a.f;
   const QuantOut& q = a.q;
   const int H = f.hidden, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

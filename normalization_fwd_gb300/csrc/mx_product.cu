@@ -44,12 +44,13 @@ cudaError_t scales_map(Encode encode, const QuantOut& q, int tiles, int row_tile
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Whether the device places clusters of `cfg`'s shape; asked once for a kernel,
-// a device and a size.
-cudaError_t places(const void* fn, const cudaLaunchConfig_t& cfg, int splits, bool* yes) {
+// Whether the device places clusters of so many CTAs; asked once for a kernel, a
+// device, a size and the shared memory.
+cudaError_t places(const void* fn, int block, size_t smem, int cluster, bool* yes) {
   struct Entry {
     const void* fn;
-    int device, splits;
+    int device, cluster;
+    size_t smem;
     bool yes;
   };
   static std::mutex mu;
@@ -59,15 +60,25 @@ cudaError_t places(const void* fn, const cudaLaunchConfig_t& cfg, int splits, bo
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
   for (const Entry& k : kept)
-    if (k.fn == fn && k.device == dev && k.splits == splits) {
+    if (k.fn == fn && k.device == dev && k.cluster == cluster && k.smem == smem) {
       *yes = k.yes;
       return cudaSuccess;
     }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   int n = 0;
   e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
   if (e != cudaSuccess) return e;
   *yes = n > 0;
-  kept.push_back({fn, dev, splits, *yes});
+  kept.push_back({fn, dev, cluster, smem, *yes});
   return cudaSuccess;
 }
 
@@ -100,25 +111,14 @@ cudaError_t launch_tiles(ProductArgs p, int sms, cudaStream_t st) {
   if (e == cudaSuccess) e = (cudaError_t)allow_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
 
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  for (;; p.splits /= 2) {     // no larger clusters than the device places
-    cfg.gridDim = dim3((unsigned)(tiles * p.splits));
-    attr[0].val.clusterDim.x = p.splits;
-    cfg.numAttrs = p.splits > 1 ? 1 : 0;
-    bool yes = true;
-    if (p.splits > 1) e = places(fn, cfg, p.splits, &yes);
+  // no larger clusters than the device places
+  for (bool yes = false; p.splits > 1 && !yes;) {
+    e = places(fn, kTileThreads, smem, p.splits, &yes);
     if (e != cudaSuccess) return e;
-    if (yes) break;
+    if (!yes) p.splits /= 2;
   }
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  return launch_overlapped(fn, dim3((unsigned)(tiles * p.splits)), dim3(kTileThreads), args, smem, st, p.splits);
 }
 
 // *placed: false where the device does not place a pair of CTAs of this size.
@@ -144,21 +144,11 @@ cudaError_t launch_pairs(ProductArgs p, int sms, cudaStream_t st, bool* placed) 
   if (e == cudaSuccess) e = scales_map(encode, p.b, chunk_tiles<FMT>(), WN / 128, &maps[3]);
   if (e == cudaSuccess) e = (cudaError_t)allow_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(2 * tiles, sms / 2 * 2));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  e = places(fn, cfg, 2, placed);
+  e = places(fn, kPairThreads, smem, 2, placed);
   if (e != cudaSuccess || !*placed) return e;
   void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  return launch_overlapped(fn, dim3((unsigned)std::min<int64_t>(2 * tiles, sms / 2 * 2)), dim3(kPairThreads), args,
+                           smem, st, 2);
 }
 
 template <typename T, int FMT>

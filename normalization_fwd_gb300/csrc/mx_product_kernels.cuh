@@ -15,12 +15,12 @@
 // instructions on what it held before are done, and so are those that read that
 // buffer. The issuing warp asks for the next stage before it issues.
 //
-// What bounds it: few rows of A, the weights' bytes and the fixed 5 us of a launch,
-// a ring's first round and the join (16 x 8192 x 8192 nvfp4 11.9 us: 42 MB at 5.6
+// What bounds it: few rows of A, the weights' bytes and the fixed 4 us of a launch,
+// a ring's first round and the join (16 x 8192 x 8192 nvfp4 11.0 us: 42 MB at 5.6
 // TB/s on 128 SMs). Many rows, the tensor cores: a chunk's four instructions take a
 // pair of CTAs 512 cycles, moving its scales 10 cycles for each of their 12 (nvfp4),
 // 6 (mxfp4) or 3 (mxfp8) tiles, and data is always there (16384 x 8192 x 8192
-// nvfp4 336 us, 6.5 PFLOP/s, tensor pipe 66% active on a smaller case).
+// nvfp4 333 us, 6.6 PFLOP/s, tensor pipe 66% active on a smaller case).
 //
 // Few tiles: K is split over the CTAs of a cluster. Each gets the tile's rows
 // of results that it is to finish from all others through distributed shared
@@ -170,8 +170,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     mbar_init(&done, 1);
     fence_mbar_init();
-    for (int i = 0; i < first; ++i) copy(c0 + i, i);
   }
+  start_after_stream();
+  if (warp == 0 && elect_one())
+    for (int i = 0; i < first; ++i) copy(c0 + i, i);
   if (warp == 2) tmem_alloc<kTmemCols>(&tmem_at);
   tc_fence_before();
   __syncthreads();
@@ -560,6 +562,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tma_prefetch(&b_codes);
     tma_prefetch(&b_scales);
   }
+  start_after_stream();
   tc_fence_before();
   __syncthreads();
   cluster_sync();

@@ -75,6 +75,7 @@ __device__ __forceinline__ void each_element(int64_t row, int64_t col, int shift
 // that one is on its way while the other is worked on.
 template <typename T, int FMT, bool RAGGED>
 __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantArgs a, int shift) {
+  start_after_stream();
   using F = Format<FMT>;
   __shared__ __align__(16) T buffer[RAGGED ? kQuantThreads / 32 : 1][RAGGED ? 256 : 8];
   T* buf = buffer[RAGGED ? threadIdx.x >> 5 : 0];
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
 constexpr int kRowKept = 4;
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) quant_row_kernel(const QuantArgs a) {
+  start_after_stream();
   __shared__ unsigned red[2][kQuantThreads / 32];
   const QuantOut& q = a.q;
   const bool vec_codes = q.pitch % 8 == 0 && a.vec_codes;
@@ -344,6 +346,7 @@ __device__ __forceinline__ void join_blocks(const unsigned* w, unsigned (*red)[3
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads, 3) quant_transpose_kernel(const QuantArgs a) {
+  start_after_stream();
   __shared__ unsigned tile[kTrCols * kTrPitch];
   constexpr int W = 4 / sizeof(T);             // rows of a lane
   __shared__ unsigned red[8][32][W];
@@ -412,13 +415,14 @@ __global__ void __launch_bounds__(kQuantThreads, 2)
   const QuantOut& q = a.q;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
   const int64_t tiles = (q.cols + kTrCols - 1) / kTrCols;      // along a row of the result
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTrStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
+  start_after_stream();
   __syncthreads();
+  const float mul = FMT == MX_NVFP4 ? mul_of(q) : 1.0f;
   const auto copy = [&](int64_t i, int st) {                   // by one thread
     const int64_t r = i / tiles, t = i - r * tiles;
     mbar_arrive_expect_tx(&full[st], kTrBytes);
@@ -469,6 +473,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2)
 template <typename T, int FMT, bool RAGGED>
 __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const QuantOut q, T* y, int64_t y_row,
                                                                 bool vec_codes, int shift) {
+  start_after_stream();
   constexpr bool FOUR = FMT >= MX_MXFP4;
   __shared__ __align__(16) T buffer[RAGGED ? kQuantThreads / 32 : 1][RAGGED ? 256 : 8];
   T* buf = buffer[RAGGED ? threadIdx.x >> 5 : 0];
