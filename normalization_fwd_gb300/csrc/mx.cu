@@ -90,7 +90,9 @@ dim3 row_grid(int64_t rows, int64_t cols, int shift, int sms) {
 // and not in one another.
 template <typename T, int FMT>
 cudaError_t launch_transpose_tma(const QuantArgs& a, int64_t x, int64_t tiles, int sms, cudaStream_t st) {
-  const void* fn = (const void*)quant_transpose_tma_kernel<T, FMT>;
+  const void* fn;
+  if constexpr (FMT == MX_FP8_ROW) fn = (const void*)quant_transpose_row_tma_kernel<T>;
+  else fn = (const void*)quant_transpose_tma_kernel<T, FMT>;
   constexpr size_t kSmem = kTrStages * kTrBytes + 1024;
   Encode encode;
   CUtensorMap map;
@@ -104,7 +106,7 @@ cudaError_t launch_transpose_tma(const QuantArgs& a, int64_t x, int64_t tiles, i
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  int64_t all = x * tiles;
+  int64_t all = FMT == MX_FP8_ROW ? x : x * tiles;
   QuantArgs args = a;
   void* params[] = {&map, &args, &all};
   return launch_overlapped(fn, dim3((unsigned)std::min<int64_t>(all, 2 * sms)), dim3(kQuantThreads), params, kSmem, st);
@@ -117,10 +119,9 @@ cudaError_t launch_quantize(const QuantArgs& a, int transpose, int sms, cudaStre
     const int64_t x = (a.padded_rows + TrRows<T>::N - 1) / TrRows<T>::N, tiles = (q.cols + kTrCols - 1) / kTrCols;
     // a copy each 16 bytes of x's rows: the tensor map's, from where the loop over
     // tiles has more than one round
-    if constexpr (FMT != MX_FP8_ROW)
-      if (a.vec && a.x_row >= q.rows && a.x_row * (int64_t)sizeof(T) % 16 == 0 && a.x_row < (1ll << 37) &&
-          x * tiles > 2 * sms)
-        return launch_transpose_tma<T, FMT>(a, x, tiles, sms, st);
+    if (a.vec && a.x_row >= q.rows && a.x_row * (int64_t)sizeof(T) % 16 == 0 && a.x_row < (1ll << 37) &&
+        x * tiles > 2 * sms)
+      return launch_transpose_tma<T, FMT>(a, x, tiles, sms, st);
     const dim3 grid((unsigned)x, FMT == MX_FP8_ROW ? 1u : (unsigned)std::min<int64_t>(tiles, 65535));
     void* args[] = {const_cast<QuantArgs*>(&a)};
     return launch_overlapped((const void*)quant_transpose_kernel<T, FMT>, grid, dim3(kQuantThreads), args, 0, st);
