@@ -631,7 +631,7 @@ ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t
  * cores, the scales' included; the rest is fp32, rounded once to dtype.
  *
  * bias      [N] dtype, NULL = none.
- * residual  [M, N] dtype, residual_row elements a row, NULL = none; may be out
+ * residual  [M, N] dtype, residual_row >= N elements a row, NULL = none; may be out
  *           itself (same row stride), overlaps it in no other way.
  * out       [M, N] dtype, out_row >= N elements a row.
  * psum, psq [M, ceil(N / 128)] fp32 or NULL (both or none): sums of the stored

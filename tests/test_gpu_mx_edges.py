@@ -207,3 +207,49 @@ def test_random_shapes(cuda_lib, seed):
     for t in (False, True):
         check_bits(nf.quantize(x, fmt, transpose=t), f64(x.T if t else x), fmt)
     assert nf.ln_device_error() == 0
+
+
+def test_forks_and_joins_in_a_graph(cuda_lib):
+    """Kernels that may be scheduled before what is in front of them has ended:
+    behind copies, on a stream that forks from another and joins it again, into
+    buffers that the one before still reads, eager and captured."""
+    nf = cuda_lib
+    rows, hidden, n = 300, 2048, 1536
+    src = torch.randn(rows, hidden, device="cuda").to(torch.bfloat16)
+    w = torch.randn(n, hidden, device="cuda").to(torch.bfloat16)
+    g = torch.ones(hidden, device="cuda", dtype=torch.bfloat16)
+    x = torch.empty_like(src)
+    side = torch.cuda.Stream()
+
+    def step():
+        x.copy_(src)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            q = nf.quantize(w, "mxfp8")
+            q = nf.quantize(nf.dequantize(q, torch.bfloat16), "mxfp8")
+        f = nf.fused_norm_quant_fwd(x, g, format="mxfp8", mode="rmsnorm")
+        x.zero_()                                # the norm has read it
+        here.wait_stream(side)
+        out = nf.scaled_product(f["q"], q)["out"]
+        keep = out.clone()
+        nf.scaled_product(f["q"], q, residual=out, out=out)
+        return keep, out, q
+
+    want, twice, _ = (t.clone() if isinstance(t, torch.Tensor) else t for t in step())
+    torch.cuda.synchronize()
+    q = nf.quantize(nf.dequantize(nf.quantize(w, "mxfp8"), torch.bfloat16), "mxfp8")
+    ref = nf.scaled_product(nf.fused_norm_quant_fwd(src, g, format="mxfp8", mode="rmsnorm")["q"], q)["out"]
+    torch.cuda.synchronize()
+    assert torch.equal(want, ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], twice)
+    for _ in range(20):
+        again = step()
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], want) and torch.equal(again[1], twice)
