@@ -51,6 +51,14 @@ __device__ __forceinline__ void start_after_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// 16 bytes, or one value, of a tensor that the kernel in front may have written. Such
+// a kernel's lifetime begins before that one's writes, so the non-coherent loads
+// of the other kernels (ld_vec, __ldg) are not for it: they hold only where memory
+// does not change as long as the kernel lives, and the compiler may move them
+// ahead of the wait. An ordinary load is coherent and stays behind it.
+__device__ __forceinline__ uint4 ld_behind(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+template <typename T> __device__ __forceinline__ T ld_one_behind(const T* p) { return *p; }
+
 // A format as a type.
 template <int F> struct Format {
   static constexpr int value = F;

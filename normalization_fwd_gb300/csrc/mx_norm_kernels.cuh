@@ -45,8 +45,8 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
   for (int k = 0; k < N; ++k) {
     const int v = k * G + t;
     if (row_ok && v < V) {
-      xr[k] = ld_vec(x + v * VEC);
-      if (res) rr[k] = ld_vec(res + v * VEC);
+      xr[k] = ld_behind(x + v * VEC);
+      if (res) rr[k] = ld_behind(res + v * VEC);
     }
   }
   if (CLS != 0 && mx_tiled(a.q.fmt) && row < a.padded_rows) put_padding(a.q, row, t, G);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kMaxFitThreads) mx_norm_ragged_kernel(const Mx
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) to[i][s] = column(i, s) < H ? to_f(__ldg(p + column(i, s))) : 0.f;
+      for (int s = 0; s < 4; ++s) to[i][s] = column(i, s) < H ? to_f(ld_one_behind(p + column(i, s))) : 0.f;
   };
   load(x, v);
   if (res) load(res, u);

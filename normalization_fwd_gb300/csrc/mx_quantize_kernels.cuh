@@ -33,7 +33,7 @@ __device__ __forceinline__ void load8(const T* row, int64_t col, int64_t n, bool
   if (vec && col + 8 <= n) {
 #pragma unroll
     for (int i = 0; i < 8 / Vec<T>::N; ++i)
-      unpack2<T>(ld_vec(row + col + i * Vec<T>::N), v + i * Vec<T>::N / 2);
+      unpack2<T>(ld_behind(row + col + i * Vec<T>::N), v + i * Vec<T>::N / 2);
   } else {
     float* f = reinterpret_cast<float*>(v);
 #pragma unroll
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_block_kernel(const QuantA
       if (r >= q.rows) return;
       if (vec) {
 #pragma unroll
-        for (int i = 0; i < 8 / Vec<T>::N; ++i) unpack2<T>(ld_vec(p + i * Vec<T>::N), v + i * Vec<T>::N / 2);
+        for (int i = 0; i < 8 / Vec<T>::N; ++i) unpack2<T>(ld_behind(p + i * Vec<T>::N), v + i * Vec<T>::N / 2);
       } else {
         float* f = reinterpret_cast<float*>(v);
 #pragma unroll
@@ -208,7 +208,7 @@ __device__ __forceinline__ void load_tile(const QuantArgs& a, int64_t row0, int6
     w[i] = make_uint4(0, 0, 0, 0);
     if (col0 + c < cols) {
       if (a.vec && row0 + r + V <= rows) {
-        w[i] = ld_vec(x);
+        w[i] = ld_behind(x);
       } else {
         T t[V];
 #pragma unroll
