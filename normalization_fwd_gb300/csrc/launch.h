@@ -115,9 +115,9 @@ cudaError_t launch_bwd_finalize(const float* ws, int P, int C, int H, bool beta_
 
 namespace nf {
 
-// Launch a kernel that begins with start_after_stream() (mx_formats.cuh), in
-// clusters of so many CTAs: it may be scheduled while what is before it on the
-// stream ends.
+// Launch a kernel that begins with start_after_stream(), or wait_for_stream()
+// (mx_formats.cuh), in clusters of so many CTAs: it may be scheduled while what is
+// before it on the stream ends.
 inline cudaError_t launch_overlapped(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
                                      cudaStream_t st, int cluster = 1) {
   cudaLaunchConfig_t cfg = {};

@@ -42,13 +42,20 @@ inline __host__ __device__ int64_t mx_blocks(int fmt, int64_t cols) {
   return b == 0 ? 1 : (cols + b - 1) / b;
 }
 
-// The beginning of a kernel launched by launch_overlapped(): the next one on the
-// stream may be scheduled, and what was before this one has ended, its writes are
-// visible. Every thread calls it before it touches memory that another kernel
-// reads or writes, so that whoever waits for this grid has waited for that one.
+// Kernels launched by launch_overlapped() call both of these. Behind the first, what
+// was before this kernel on the stream has ended and its writes are visible: every
+// thread calls it before it touches memory that another kernel reads or writes, so
+// that whoever waits for this grid has waited for that one. After the second, the
+// next kernel on the stream may be scheduled.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// The beginning of a kernel without tensor memory. One that takes some does so
+// between the two, with a barrier behind it: it holds none while it waits for a
+// kernel in front, which might still have to take its own on this SM, and the next
+// one cannot take any, and wait with it for this one, before this one has its own.
 __device__ __forceinline__ void start_after_stream() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  wait_for_stream();
 }
 
 // 16 bytes, or one value, of a tensor that the kernel in front may have written. Such

@@ -171,13 +171,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     mbar_init(&done, 1);
     fence_mbar_init();
   }
-  start_after_stream();
+  wait_for_stream();
   if (warp == 0 && elect_one())
     for (int i = 0; i < first; ++i) copy(c0 + i, i);
   if (warp == 2) tmem_alloc<kTmemCols>(&tmem_at);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  let_next_start();
   const uint32_t tmem = tmem_at;
 
   if (warp == 0) {
@@ -546,7 +547,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = p.tiles_m * p.tiles_n;
 
-  if (warp == 1) tmem_alloc_pair<kTmemCols>(&tmem_at);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 1);
@@ -562,11 +562,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tma_prefetch(&b_codes);
     tma_prefetch(&b_scales);
   }
-  start_after_stream();
+  wait_for_stream();
+  if (warp == 1) tmem_alloc_pair<kTmemCols>(&tmem_at);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  let_next_start();
   const uint32_t tmem = tmem_at;
 
   if (warp == 0) {

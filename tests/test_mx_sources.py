@@ -55,3 +55,18 @@ def test_no_load_that_wants_memory_constant(name):
     make one."""
     found = re.findall(r"__ldg|\bld_vec\w*|ld\.global(?:\.\w+)*\.nc\b|__restrict__|__ldcs\b", SOURCES[name])
     assert not found
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_tensor_memory_is_taken_between_the_wait_and_the_signal(name):
+    """A kernel that held tensor memory while it waits for the one in front, or
+    let the next one start before it has its own, could wait for columns that
+    a kernel holds which waits for it."""
+    body = KERNELS[name]
+    if "tmem_alloc" not in body:
+        assert body.count("start_after_stream()") == 1
+        return
+    steps = ["wait_for_stream()", "tmem_alloc", "__syncthreads()", "let_next_start()"]
+    at = [body.index(s) for s in steps]
+    assert at == sorted(at) and "start_after_stream" not in body
+    assert all(body.count(s) == 1 for s in (steps[0], steps[1], steps[3]))
