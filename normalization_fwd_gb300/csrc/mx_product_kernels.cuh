@@ -70,14 +70,32 @@ template <int FMT> __host__ __device__ constexpr uint32_t stage_bytes(int cols) 
   return (uint32_t)(kTileLanes + cols) * kChunkBytes + 2u * chunk_tiles<FMT>() * 512u;
 }
 
+// What the sums are multiplied by, alpha / mul of A / mul of B: `first`, then `second`,
+// a power of two and mostly 1. As one number it need not be an fp32 one, nor alpha /
+// mul of A, where the result is (two matrices of values about 1e-19 have factors of
+// some 1e22 each): quotients of the fractions, powers of two apart.
+struct Factor {
+  float first, second;
+};
+__device__ __forceinline__ Factor factor_of(const ProductArgs& p) {
+  int e, ea, eb;
+  const float m = frexpf(p.alpha, &e) / frexpf(mul_of(p.a), &ea) / frexpf(mul_of(p.b), &eb);   // below 4
+  e -= ea + eb;
+  const int near = min(max(e, -124), 124);     // m * 2^near is a normal number
+  // past these powers the product is 0 or infinite anyway: sums are below 2^64, and
+  // with a mul (MX_NVFP4) multiples of 2^-20
+  return {ldexpf(m, near), ldexpf(1.0f, min(max(e - near, -126), 127))};
+}
+
 // Rounding of a row of up to 128 results, four a lane, and its statistics.
 template <typename T>
 __device__ __forceinline__ void finish_row(const ProductArgs& p, int64_t m, int64_t n0, float4 acc,
-                                           float f) {
+                                           Factor f) {
   const int lane = threadIdx.x & 31;
   const int64_t n = n0 + lane * 4;
   const int live = (int)max((int64_t)0, min((int64_t)4, p.b.rows - n));
-  float v[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
+  float v[4] = {acc.x * f.first * f.second, acc.y * f.first * f.second, acc.z * f.first * f.second,
+                acc.w * f.first * f.second};
   const T* res = p.residual ? static_cast<const T*>(p.residual) + m * p.residual_row + n : nullptr;
   T* out = static_cast<T*>(p.out) + m * p.out_row + n;
   if (p.bias) {
@@ -277,7 +295,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_free<kTmemCols>(tmem);
   }
 
-  const float f = p.alpha / mul_of(p.a) / mul_of(p.b);
+  const Factor f = factor_of(p);
   const int64_t m0 = (SWAP ? col_row : lane_row) + (int64_t)rank * rows_each, n0 = SWAP ? lane_row : col_row;
   for (int r = warp; r < rows_each; r += kTileThreads / 32) {
     if (m0 + r >= p.a.rows) break;
@@ -352,7 +370,7 @@ __device__ __forceinline__ uint4 ld_bias(const void* p) {
 // them into registers; false: they did not come. The residual's first piece is
 // on its way before.
 template <typename T, bool RES, bool SUMS, typename Load>
-__device__ __forceinline__ bool finish_full(const ProductArgs& p, int64_t m0, int64_t n0, float f,
+__device__ __forceinline__ bool finish_full(const ProductArgs& p, int64_t m0, int64_t n0, Factor f,
                                             unsigned char* piece, Load load) {
   constexpr int N = Vec<T>::N, kCols = 4 * N, kPieces = 128 / kCols;
   const int lane = threadIdx.x & 31, part = lane & 3, row = lane >> 2;
@@ -388,7 +406,8 @@ __device__ __forceinline__ bool finish_full(const ProductArgs& p, int64_t m0, in
       float2 o[N / 2];
 #pragma unroll
       for (int i = 0; i < N / 2; ++i)
-        o[i] = mul2(make_float2(__uint_as_float(v[at + 2 * i]), __uint_as_float(v[at + 2 * i + 1])), splat2(f));
+        o[i] = mul2(mul2(make_float2(__uint_as_float(v[at + 2 * i]), __uint_as_float(v[at + 2 * i + 1])),
+                         splat2(f.first)), splat2(f.second));
       if (bias) {
         float2 b[N / 2];
         unpack2<T>(ld_bias(bias + at), b);
@@ -452,7 +471,7 @@ __device__ __forceinline__ bool finish_full(const ProductArgs& p, int64_t m0, in
 // anywhere), 16 columns at a time as fp32 in shared memory: 16 lanes a row for
 // what is read and written.
 template <typename T, typename Load>
-__device__ __forceinline__ bool finish_ragged(const ProductArgs& p, int64_t m0, int64_t n0, float f,
+__device__ __forceinline__ bool finish_ragged(const ProductArgs& p, int64_t m0, int64_t n0, Factor f,
                                               unsigned char* piece, Load load) {
   const int lane = threadIdx.x & 31, c = lane & 15;
   const int rows = (int)max((int64_t)0, min((int64_t)32, p.a.rows - m0));
@@ -471,8 +490,10 @@ __device__ __forceinline__ bool finish_ragged(const ProductArgs& p, int64_t m0, 
     if (rows == 0 || col >= width) break;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      own[i] = make_float4(__uint_as_float(v[col + 4 * i]) * f, __uint_as_float(v[col + 4 * i + 1]) * f,
-                           __uint_as_float(v[col + 4 * i + 2]) * f, __uint_as_float(v[col + 4 * i + 3]) * f);
+      own[i] = make_float4(__uint_as_float(v[col + 4 * i]) * f.first * f.second,
+                           __uint_as_float(v[col + 4 * i + 1]) * f.first * f.second,
+                           __uint_as_float(v[col + 4 * i + 2]) * f.first * f.second,
+                           __uint_as_float(v[col + 4 * i + 3]) * f.first * f.second);
     __syncwarp();
     const int live = col + c < width ? (rows - (lane >> 4) + 1) / 2 : 0;    // rows of this lane's column
     const float b = p.bias && live > 0 ? to_f(static_cast<const T*>(p.bias)[n0 + col + c]) : 0.f;
@@ -658,7 +679,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int e = max(0, n - kBufs); e < n && ok; ++e) mbar_wait_cluster(&drained[e % kBufs], (e / kBufs) & 1);
   } else if (warp >= 4) {
     const int quarter = warp & 3, group = (warp - 4) >> 2;
-    const float f = p.alpha / mul_of(p.a) / mul_of(p.b);
+    const Factor f = factor_of(p);
     unsigned char* piece = smem_raw + (base - smem_addr(smem_raw)) + p.stages * kStage + (warp - 4) * kPieceBytes;
     int n = 0;
     for (int t = pair; t < tiles; t += pairs, ++n) {
