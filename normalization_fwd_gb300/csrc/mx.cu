@@ -34,17 +34,12 @@ int class_of(int fmt) { return fmt == MX_FP8_ROW ? 0 : mx_four(fmt) ? 2 : 1; }
 // 160 vectors, four vectors a lane where the row splits evenly, then a CTA
 // fitted to the row (8192 x 5120 bf16 LayerNorm to mxfp4 56 us with four
 // vectors a thread, 58 with three, 61 with six, 73 with eight). A block of 128
-// columns needs 16 lanes (32 for fp32). `few` rows leave threads idle anyway, so
-// a row is spread over as many as there are (1024 x 320 fp16 to mxfp8 3.9 us as
-// 32 x 2 against 5.7 as 8 x 5, 512 x 1000 fp32 3.6 as a CTA of two vectors a
-// thread against 4.5 of four; 8192 x 320, which is not few, 7.3 against 6.1).
+// columns needs 16 lanes (32 for fp32).
 struct NormPlan {
   int lanes = -1, n = 0, block = 256;
 };
-NormPlan norm_plan(int slots, int least_lanes, bool few) {
+NormPlan norm_plan(int slots, int least_lanes) {
   NormPlan p;
-  if (few && slots <= 64) return {32, (slots + 31) / 32, kBulkThreads};
-  if (few && slots <= 2 * kMaxFitThreads) return {0, 2, std::max(64, (slots + 63) / 64 * 32)};
   if (slots <= 160) {
     for (int n : {4, 3, 5, 2, 1}) {
       const int lanes = slots / n;
@@ -68,6 +63,19 @@ NormPlan norm_plan(int slots, int least_lanes, bool few) {
     p = {0, n, nt};
   }
   return p;
+}
+
+// Few rows leave threads idle anyway, so a row is spread over as many as there are,
+// two vectors each, and its sums are put in the order of the plan above (on the GPU
+// 64 x 1280 bf16 to mxfp8 2.6 us against 3.8, 1 x 4096 to mxfp4 2.5 against 3.1, 1024 x
+// 320 fp16 to mxfp8 3.4 against 4.1; 8192 x 320, which is not few, 7.3 against 6.1; a
+// CTA's longer row takes as long either way where a CTA an SM is not enough, 512 x
+// 1000 fp32 4.3). n = 0: rows are not few, or too wide.
+NormPlan few_plan(int slots, int64_t rows, int sms) {
+  const bool few = slots <= 160 ? rows * slots <= (int64_t)sms * 1024 : rows <= sms;
+  if (!few || slots > 2 * kMaxFitThreads) return {-1, 0, 0};
+  if (slots <= 64) return {32, (slots + 31) / 32, kBulkThreads};
+  return {0, 2, std::max(64, (slots + 63) / 64 * 32)};
 }
 
 int64_t padded_rows(const QuantOut& q) { return mx_tiled(q.fmt) ? (q.rows + 127) / 128 * 128 : q.rows; }
@@ -218,7 +226,13 @@ ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, con
     int sms = 0;
     const cudaError_t e = (cudaError_t)device_sm_count(&sms);
     if (e != cudaSuccess) return cuda_fail(e);
-    p = norm_plan((int)slots, q->format == MX_FP8_BLOCK ? 128 / per : 8, rows * slots <= (int64_t)sms * 1024);
+    p = norm_plan((int)slots, q->format == MX_FP8_BLOCK ? 128 / per : 8);
+    const NormPlan few = few_plan((int)slots, rows, sms);
+    if (few.n > 0 && few.n < p.n) {
+      a.order_lanes = p.lanes > 0 ? p.lanes : p.block;
+      a.order_n = p.n;
+      p = few;
+    }
   }
   if (!vec && hidden > 128 * kChunks) {
     p.lanes = -2;
@@ -230,7 +244,9 @@ ln_status mx_norm_fwd(const void* x, const void* bias, const void* residual, con
   int64_t grid = a.padded_rows;
   if (p.lanes > 0) grid = (a.padded_rows + 256 / p.lanes - 1) / (256 / p.lanes);
   if (p.lanes == -1) grid = (a.padded_rows + 7) / 8;
-  const size_t smem = p.lanes < 0 && cls != 0 ? (size_t)p.block / 32 * kChunks * 128 * sizeof(float) : 0;
+  size_t smem = 0;
+  if (p.lanes < 0 && cls != 0) smem = (size_t)p.block / 32 * kChunks * 128 * sizeof(float);
+  if (p.lanes == 0 && a.order_n > 0) smem = 2 * (size_t)p.n * p.block * sizeof(float2);
   void* args[] = {&a};
   const cudaError_t e = launch_overlapped(fn, dim3((unsigned)grid), dim3(p.block), args, smem, stream);
   return e == cudaSuccess ? LN_OK : cuda_fail(e);

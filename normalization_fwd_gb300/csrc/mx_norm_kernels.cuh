@@ -23,7 +23,70 @@ struct MxNormArgs {
   FwdArgs f;       // y may be null; amax and y_fp8 are not used
   QuantOut q;
   int64_t padded_rows;   // rows whose scales are written: a multiple of 128 in tiles
+  int order_lanes;       // few rows: lanes or threads of a row, and vectors of each,
+  int order_n;           // in the plan for many, whose order of sums they keep; else 0
 };
+
+// Few rows are spread over more threads than many. So that a row's result does not
+// depend on how many others there are, both add in the order of the plan for many:
+// each vector's values as a pair, the vectors of one of its order_lanes threads one
+// after the other, the pair, the lanes, the warps. That costs many rows nothing
+// (16384 x 8192 bf16 to nvfp4 152 us with and without) and few some 0.1 to 0.5 us; one
+// tree over the vectors, a shuffle more for each, cost many rows 2 to 4%.
+
+// In a warp that has N vectors a lane, where order_lanes is a power of two: the order_n
+// vectors of a lane in the plan for many come by shuffles, from one of N places each.
+template <int N> __device__ __forceinline__ float ordered_warp_sum(const MxNormArgs& a, const float2* part) {
+  const int L = a.order_lanes, lane = threadIdx.x & 31;
+  float2 t = splat2(0.f);
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    if (k >= a.order_n || k * L >= 32 * N) break;      // what is behind are zeros
+    const float2 from = N == 2 && k * L >= 32 ? part[N - 1] : part[0];
+    const int at = (k * L + (lane & (L - 1))) & 31;
+    const float2 v = {__shfl_sync(0xffffffffu, from.x, at), __shfl_sync(0xffffffffu, from.y, at)};
+    t = k == 0 ? v : add2(t, v);
+  }
+  float sum = t.x + t.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < L) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// The vectors of thread u in the plan for many, out of shared memory with `room` for
+// them.
+__device__ __forceinline__ float ordered_thread_sum(const MxNormArgs& a, const float2* parts, int u, int room) {
+  float2 t = parts[u];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    const int v = k * a.order_lanes + u;
+    if (k < a.order_n) t = add2(t, v < room ? parts[v] : splat2(0.f));
+  }
+  return t.x + t.y;
+}
+// In a CTA of `room` vectors; `parts` and `red`, each one of two in turn. Where a lane
+// group has a row in the plan for many, each warp adds all of it.
+__device__ __forceinline__ float ordered_cta_sum(const MxNormArgs& a, float2* parts, int room, float* red) {
+  const int L = a.order_lanes;
+  __syncthreads();
+  if (L <= 32) {
+    float v = ordered_thread_sum(a, parts, threadIdx.x & (L - 1), room);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < L) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  if ((int)threadIdx.x < L) {                           // whole warps
+    const float v = group_sum<32>(ordered_thread_sum(a, parts, threadIdx.x, room));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  }
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < (L >> 5); ++i) t += red[i];       // as cta_sum_db_fit
+  return t;
+}
 
 // Rows in registers. CLS: 0 a scale a row, 1 blocks of E4M3, 2 blocks of E2M1.
 // G0 > 0: a group of G0 lanes a row; 0: the CTA.
@@ -52,7 +115,7 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
   if (CLS != 0 && mx_tiled(a.q.fmt) && row < a.padded_rows) put_padding(a.q, row, t, G);
 
   float2 s[N][P];
-  float2 t1 = splat2(0.f);
+  float2 part[N], all;             // sums of the vectors and of the thread
   T* sum_row = f.out_sum ? static_cast<T*>(f.out_sum) + off : nullptr;
   const ParamRow<T> w_row = {nullptr, static_cast<const T*>(f.gamma), H, f.zero_centered != 0};
   const ParamRow<T> bias_row = {nullptr, static_cast<const T*>(f.bias), H, false};
@@ -62,6 +125,7 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
     const int v = k * G + t;
 #pragma unroll
     for (int i = 0; i < P; ++i) s[k][i] = splat2(0.f);
+    part[k] = splat2(0.f);
     if (row_ok && v < V) {
       unpack2<T>(xr[k], s[k]);
       if (bias_row.g) {
@@ -79,24 +143,27 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
       const uint4 packed = pack2<T>(s[k]);
       if (sum_row) st_vec(sum_row + v * VEC, packed);
       unpack2<T>(packed, s[k]);
+      part[k] = s[k][0];
 #pragma unroll
-      for (int i = 0; i < P; ++i) t1 = add2(t1, s[k][i]);
+      for (int i = 1; i < P; ++i) part[k] = add2(part[k], s[k][i]);
     }
+    all = k > 0 ? add2(all, part[k]) : part[k];
   }
-  const float mean = f.rms ? 0.f : reduce(t1.x + t1.y) / (float)H;
+  const float mean = f.rms ? 0.f : reduce(all.x + all.y, part) / (float)H;
   const float2 neg_mean = splat2(-mean);
-  float2 t2 = splat2(0.f);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
+    part[k] = splat2(0.f);
     if (row_ok && (k * G + t) < V) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         s[k][i] = add2(s[k][i], neg_mean);
-        t2 = fma2(s[k][i], s[k][i], t2);
+        part[k] = i == 0 ? mul2(s[k][i], s[k][i]) : fma2(s[k][i], s[k][i], part[k]);
       }
     }
+    all = k > 0 ? add2(all, part[k]) : part[k];
   }
-  const float rstd = 1.0f / sqrtf(reduce(t2.x + t2.y) / (float)H + f.eps);
+  const float rstd = 1.0f / sqrtf(reduce(all.x + all.y, part) / (float)H + f.eps);
   if (row_ok && t == 0) {
     if (f.mean) f.mean[row] = mean;
     if (f.rstd) f.rstd[row] = rstd;
@@ -168,14 +235,20 @@ __device__ __forceinline__ void mx_norm_row(const MxNormArgs& a, int64_t row, in
 
 // A tile of 8 * (32 / LANES) rows a CTA, a lane group a row.
 template <typename T, int LANES, int N, int CLS>
-__global__ void __launch_bounds__(kBulkThreads, N <= 3 ? 4 : 2) mx_norm_tile_kernel(const MxNormArgs a) {
+__global__ void __launch_bounds__(kBulkThreads, N <= 3 ? 4 : 3) mx_norm_tile_kernel(const MxNormArgs a) {
   constexpr int RPW = 32 / LANES;
   const int lane = threadIdx.x & 31;
   const int64_t row =
       ((int64_t)blockIdx.x * kConsumerWarps + (threadIdx.x >> 5)) * RPW + lane / LANES;
   start_after_stream();
   mx_norm_row<T, LANES, N, CLS>(
-      a, row, lane % LANES, [](float v) { return group_sum<LANES>(v); },
+      a, row, lane % LANES,
+      [&](float all, const float2* part) {
+        if constexpr (LANES == 32 && N <= 2) {         // may be the plan for few rows
+          if (a.order_n) return ordered_warp_sum<N>(a, part);
+        }
+        return group_sum<LANES>(all);
+      },
       [](unsigned v) { return lanes_max<LANES>(v); });
 }
 
@@ -184,6 +257,7 @@ template <typename T, int N, int CLS>
 __global__ void __launch_bounds__(kMaxFitThreads) __maxnreg__(N <= 4 ? 64 : 128) mx_norm_cta_kernel(const MxNormArgs a) {
   __shared__ float red[2][kMaxFitWarps];
   __shared__ unsigned red_max[kMaxFitWarps];
+  extern __shared__ float2 parts[];                    // few rows: 2 * N * blockDim.x
   start_after_stream();
   if (blockIdx.x >= a.f.rows) {    // the scales behind the last row
     if (CLS != 0) put_padding(a.q, blockIdx.x, threadIdx.x, blockDim.x);
@@ -191,7 +265,21 @@ __global__ void __launch_bounds__(kMaxFitThreads) __maxnreg__(N <= 4 ? 64 : 128)
   }
   int parity = 0;
   mx_norm_row<T, 0, N, CLS>(
-      a, blockIdx.x, threadIdx.x, [&](float v) { return cta_sum_db_fit(v, red, parity); },
+      a, blockIdx.x, threadIdx.x,
+      [&](float all, const float2* part) {
+        if constexpr (N == 2) {                        // may be the plan for few rows
+          if (a.order_n) {
+            const int room = N * blockDim.x;
+            float2* row = parts + parity * room;
+#pragma unroll
+            for (int k = 0; k < N; ++k) row[k * blockDim.x + threadIdx.x] = part[k];
+            const float t = ordered_cta_sum(a, row, room, red[parity]);
+            parity ^= 1;
+            return t;
+          }
+        }
+        return cta_sum_db_fit(all, red, parity);
+      },
       [&](unsigned v) {
         v = __reduce_max_sync(0xffffffffu, v);
         if ((threadIdx.x & 31) == 0) red_max[threadIdx.x >> 5] = v;
