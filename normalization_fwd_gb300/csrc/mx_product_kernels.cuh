@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_wait_cluster(&full[(i - c0) % p.stages], ((i - c0) / p.stages) & 1);
     }
   } else if (warp == 1) {
-    bool ok = true, here = mbar_test_cluster(smem_addr(&full[0]), 0);
+    bool ok = true, here = mbar_ready_cluster(smem_addr(&full[0]), 0);
     int st = 0, round = 0;
     for (int c = c0; c < c1; ++c) {
       const int i = c - c0;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int next = st + 1 == p.stages ? 0 : st + 1;
-      here = c + 1 < c1 && mbar_test_cluster(smem_addr(&full[next]), (next == 0 ? round + 1 : round) & 1);
+      here = c + 1 < c1 && mbar_ready_cluster(smem_addr(&full[next]), (next == 0 ? round + 1 : round) & 1);
       const uint32_t at = base + st * stage_size;
       const uint32_t sc = at + (kTileLanes + cols) * kChunkBytes;
       const uint32_t sa = tmem + kScaleCol + st * 8 * kTiles, sb = sa + 4 * kTiles;
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     bool ok = true;
     int i = 0, n = 0;                                    // chunks and tiles so far
     int st = 0, round = 0;
-    bool here = mbar_test_cluster(smem_addr(&full[0]), 0);
+    bool here = mbar_ready_cluster(smem_addr(&full[0]), 0);
     for (int t = pair; t < tiles && ok; t += pairs, ++n) {
       const int buf = n % kBufs;
       if (n >= kBufs) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&drained[buf], (n / kBufs - 1) & 1));
@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int next = st + 1 == p.stages ? 0 : st + 1;
-        here = mbar_test_cluster(smem_addr(&full[next]), (next == 0 ? round + 1 : round) & 1);
+        here = (c + 1 < p.chunks || t + pairs < tiles) &&
+               mbar_ready_cluster(smem_addr(&full[next]), (next == 0 ? round + 1 : round) & 1);
         const uint32_t at = base + st * kStage, sc = at + (128 + WN / 2) * kChunkBytes;
         const uint32_t sa = tmem + 256 + st * kScaleStep, sb = sa + 4 * kTiles;
         const uint64_t da = operand_desc(at), db = operand_desc(at + 128 * kChunkBytes), ds = scales_desc(sc);

@@ -70,3 +70,15 @@ def test_tensor_memory_is_taken_between_the_wait_and_the_signal(name):
     at = [body.index(s) for s in steps]
     assert at == sorted(at) and "start_after_stream" not in body
     assert all(body.count(s) == 1 for s in (steps[0], steps[1], steps[3]))
+
+
+def test_looking_ahead_does_not_hold_work_back():
+    """A product's issuing warp asks for the next stage before it issues the work of
+    this one: by a test that returns at once, and only for a stage that will come."""
+    text = SOURCES["mx_product_kernels.cuh"]
+    asked = [a for a in re.findall(r"\bhere\s*=\s*([^;]*);", text) if "mbar_wait_cluster" not in a]
+    assert len(asked) == 4 and all("mbar_ready_cluster" in a for a in asked)
+    assert all("smem_addr(&full[0])" in a or re.match(r"\(?c \+ 1 <", a) for a in asked)
+    assert "mbar_test_cluster" not in text
+    body = re.search(r"bool mbar_ready_cluster\(.*?\n}", SOURCES["tcgen05.cuh"], flags=re.S).group(0)
+    assert "mbarrier.test_wait" in body and "try_wait" not in body
