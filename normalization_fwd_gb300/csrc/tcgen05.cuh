@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 
+#include "../../include/normfuse.h"
 #include "bulk.cuh"
 
 namespace nf {
@@ -252,12 +253,13 @@ __device__ __forceinline__ bool mbar_ready_cluster(uint32_t bar, uint32_t parity
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  long long limit = kWaitLimitCycles) {
   const uint32_t at = smem_addr(bar);
   if (mbar_test_cluster(at, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_test_cluster(at, parity))
-    if (clock64() - t0 > kWaitLimitCycles) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
 }
 
