@@ -4,8 +4,8 @@ The functions here have the names of the C entry points declared in
 ``include/normfuse.h`` and only marshal arguments: torch tensors become
 device pointers, the torch stream becomes a ``cudaStream_t``, and the return
 status becomes an exception. The quantised calls that allocate their outputs
-do so in C++ (``csrc/marshal.cc``) where the call is on the current device and
-stream. Every step of the computation runs in the CUDA
+do so in C++ (``csrc/marshal.cc``) where that is built and the call is on the
+current device and stream. Every step of the computation runs in the CUDA
 kernels of the library; there is no fallback. If the library has not been
 built, loading it raises.
 
@@ -77,7 +77,7 @@ _FORMAT_CODES = {"fp8_row": MX_FP8_ROW, "fp8_block": MX_FP8_BLOCK, "mxfp8": MX_M
 _MX_MATRIX = struct.Struct("@PPPiqq")
 
 _lib = None
-_marshal = None     # the binding's C++ part (csrc/marshal.cc), loaded with the library
+_marshal = None     # the binding's C++ part (csrc/marshal.cc), where it is built for this torch
 _lock = threading.Lock()
 
 
@@ -93,7 +93,9 @@ class NormError(RuntimeError):
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
-    """Load ``libnormfuse.so`` (built in-tree by ``build_library()``)."""
+    """Load ``libnormfuse.so`` (built in-tree by ``build_library()``), or the one at
+    ``path``. The binding's C++ part calls the same one; where it is not built for
+    the torch that runs, its calls go through ctypes like all others."""
     global _lib, _marshal
     with _lock:
         if _lib is not None:
@@ -103,10 +105,6 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             raise RuntimeError(
                 f"CUDA library not built: {path} is missing. "
                 "Run `python -m normalization_fwd_gb300.build` (needs nvcc).")
-        if not os.path.isfile(marshal_path()):
-            raise RuntimeError(
-                f"the binding is not built for this torch: {marshal_path()} is missing. "
-                "Run `python -m normalization_fwd_gb300.build`.")
         lib = ctypes.CDLL(path)
         vp, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         ci = ctypes.c_int
@@ -169,10 +167,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.mx_dequantize.restype = ci
         lib.mx_product.argtypes = [vp, vp, f32, vp, vp, i64, vp, i64, vp, vp, vp, ci]
         lib.mx_product.restype = ci
-        loader = importlib.machinery.ExtensionFileLoader("_marshal", marshal_path())
-        spec = importlib.util.spec_from_loader("_marshal", loader)
-        _marshal = importlib.util.module_from_spec(spec)
-        loader.exec_module(_marshal)
+        if os.path.isfile(marshal_path()):
+            loader = importlib.machinery.ExtensionFileLoader("_marshal", marshal_path())
+            spec = importlib.util.spec_from_loader("_marshal", loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(f, vp).value for f in (
+                lib.mx_matrix_bytes, lib.mx_norm_fwd, lib.mx_quantize, lib.mx_dequantize,
+                lib.mx_product, lib.ln_fwd_from_partials)))
+            _marshal = module
         _lib = lib
         return lib
 
@@ -494,7 +497,7 @@ def fused_norm_fwd_from_partials(x, psum, psq, tile_cols, gamma, beta=None, *, k
                                  amax=False, stream=None):
     """Allocate the outputs with torch and run ``ln_fwd_from_partials``;
     returns a dict with ``y``, ``mean`` (LayerNorm), ``rstd``, ``amax``."""
-    if stream is None and not amax and (_lib or load_library()):
+    if stream is None and not amax and (_lib or load_library()) and _marshal:
         r = _marshal.norm_from_partials(x, psum, psq, tile_cols, _PARTIAL_CODES.get(kind, -1), gamma,
                                         beta, eps, _mode(mode), zero_centered_gamma)
         if r is not None:
@@ -1328,7 +1331,7 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
     """
     if store_sum is None:
         store_sum = bias is not None or residual is not None
-    if stream is None and (_lib or load_library()):
+    if stream is None and (_lib or load_library()) and _marshal:
         r = _marshal.norm_quant(x, gamma, beta, bias, residual, mul, _format(format), _mode(mode),
                                 zero_centered_gamma, eps, store_sum, store_y)
         if r is not None:
@@ -1358,7 +1361,7 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
 def quantize(x, format, *, mul=None, transpose=False, stream=None) -> Quantized:
     """The matrix ``x``, or its transpose, in 8 or 4 bits with scales. Rows of x
     may be any distance apart (a slice of a wider tensor)."""
-    if stream is None and (_lib or load_library()):
+    if stream is None and (_lib or load_library()) and _marshal:
         r = _marshal.quantize(x, _format(format), transpose, mul)
         if r is not None:
             codes, scales = _made(r, "mx_quantize")
@@ -1378,7 +1381,7 @@ def quantize(x, format, *, mul=None, transpose=False, stream=None) -> Quantized:
 
 def dequantize(q, dtype=torch.float32, *, out=None, stream=None):
     """The values of ``q`` as a [rows, cols] tensor of ``dtype``."""
-    if stream is None and out is None and (_lib or load_library()):
+    if stream is None and out is None and (_lib or load_library()) and _marshal:
         codes, scales, format, rows, cols, mul = q
         r = _marshal.dequantize(codes, scales, mul, _format(format), rows, cols,
                                 _DTYPE_CODES.get(dtype, -1))
@@ -1407,7 +1410,8 @@ def scaled_product(a, b, *, alpha=1.0, bias=None, residual=None, dtype=torch.bfl
     quantise the output's gradient and the weights (transpose=True) for the
     input's, both operands transposed for the weights'.
     """
-    if stream is None and a.format == b.format and a.cols == b.cols and (_lib or load_library()):
+    if (stream is None and a.format == b.format and a.cols == b.cols and (_lib or load_library())
+            and _marshal):
         r = _marshal.product(a.codes, a.scales, a.mul, b.codes, b.scales, b.mul, _format(a.format),
                              a.rows, b.rows, a.cols, alpha, bias, residual,
                              _DTYPE_CODES.get(dtype, -1), out, partials)

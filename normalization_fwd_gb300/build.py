@@ -54,7 +54,8 @@ def marshal_path() -> str:
 
 
 def _marshal_commands(nvcc):
-    """(compile, link): the link comes after the library's."""
+    """(compile, link). Nothing of the library is linked in: the binding gives the
+    addresses of the one that it has loaded."""
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
@@ -64,9 +65,8 @@ def _marshal_commands(nvcc):
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     return (["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
              *[f"-I{d}" for d in dirs], "-c", os.path.join(CSRC, "marshal.cc"), "-o", obj],
-            ["g++", "-shared", obj, "-o", marshal_path() + ".tmp", f"-L{PKG}", f"-l:{LIB_NAME}",
-             "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-             "-ltorch_python"])
+            ["g++", "-shared", obj, "-o", marshal_path() + ".tmp", f"-L{os.path.join(at, 'lib')}", "-lc10",
+             "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
 
 
 def _sources():

@@ -8,7 +8,8 @@
 // CUDA device, on the current stream, of the types and layouts that the entry
 // point takes. It returns None where anything is otherwise, and the caller in
 // __init__.py, which has the checks and their messages, goes its own way. A
-// status other than LN_OK comes back as a number.
+// status other than LN_OK comes back as a number. The entry points are those of the
+// library that the caller has loaded: bind() takes their addresses.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -17,11 +18,22 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <type_traits>
+
 #include "../../include/normfuse.h"
 
 namespace {
 
 using at::Tensor;
+
+struct Library {
+  decltype(&::mx_matrix_bytes) matrix_bytes;
+  decltype(&::mx_norm_fwd) norm_fwd;
+  decltype(&::mx_quantize) quantize;
+  decltype(&::mx_dequantize) dequantize;
+  decltype(&::mx_product) product;
+  decltype(&::ln_fwd_from_partials) fwd_from_partials;
+} lib;
 
 int dtype_code(at::ScalarType t) {
   return t == at::kFloat ? LN_F32 : t == at::kBFloat16 ? LN_BF16 : t == at::kHalf ? LN_F16 : -1;
@@ -89,7 +101,7 @@ at::ScalarType scale_type(long fmt) {
   return fmt <= MX_FP8_BLOCK ? at::kFloat : fmt == MX_NVFP4 ? at::kFloat8_e4m3fn : at::kFloat8_e8m0fnu;
 }
 bool sizes(long fmt, int64_t rows, int64_t cols, size_t* codes, size_t* scales) {
-  return mx_matrix_bytes((mx_format)fmt, rows, cols, codes, scales) == LN_OK;
+  return lib.matrix_bytes((mx_format)fmt, rows, cols, codes, scales) == LN_OK;
 }
 // Room for a matrix; false where there is no such one.
 bool room(long fmt, int64_t rows, int64_t cols, const at::TensorOptions& at_, Tensor* codes, Tensor* scales) {
@@ -166,7 +178,7 @@ PyObject* norm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (store_y) y = at::empty(x->sizes(), options);
       if (!rms) mean = at::empty({rows}, options.dtype(at::kFloat));
       rstd = at::empty({rows}, options.dtype(at::kFloat));
-      st = mx_norm_fwd(x->data_ptr(), ptr(bias), ptr(res), gamma->data_ptr(), ptr(beta), (float)eps, (ln_mode)mode, zero,
+      st = lib.norm_fwd(x->data_ptr(), ptr(bias), ptr(res), gamma->data_ptr(), ptr(beta), (float)eps, (ln_mode)mode, zero,
                        store_sum ? sum.data_ptr() : nullptr, store_y ? y.data_ptr() : nullptr,
                        rms ? nullptr : mean.data_ptr<float>(), rstd.data_ptr<float>(), &q,
                        c10::cuda::getCurrentCUDAStream(device).stream(), (ln_dtype)dt);
@@ -201,7 +213,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     made = room(fmt, rows, cols, x->options().requires_grad(false), &codes, &scales) &&
            matrix(&codes, &scales, mul, fmt, rows, cols, &q);
     if (made)
-      st = mx_quantize(x->data_ptr(), stride, transpose, &q, c10::cuda::getCurrentCUDAStream(device).stream(), (ln_dtype)dt);
+      st = lib.quantize(x->data_ptr(), stride, transpose, &q, c10::cuda::getCurrentCUDAStream(device).stream(), (ln_dtype)dt);
   }
   if (!made) return none();
   if (st != LN_OK) return PyLong_FromLong(st);
@@ -226,7 +238,7 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   {
     pybind11::gil_scoped_release away;
     y = at::empty({rows, cols}, codes->options().requires_grad(false).dtype(dtype_of(dt)));
-    st = mx_dequantize(&q, y.data_ptr(), cols, c10::cuda::getCurrentCUDAStream(device).stream(), (ln_dtype)dt);
+    st = lib.dequantize(&q, y.data_ptr(), cols, c10::cuda::getCurrentCUDAStream(device).stream(), (ln_dtype)dt);
   }
   if (st != LN_OK) return PyLong_FromLong(st);
   return wrap(y);
@@ -269,7 +281,7 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
       psum = at::empty({M, (N + 127) / 128}, options.dtype(at::kFloat));
       psq = at::empty({M, (N + 127) / 128}, options.dtype(at::kFloat));
     }
-    st = mx_product(&left, &right, (float)alpha, ptr(bias), ptr(res), res_row, out.data_ptr(), out_row,
+    st = lib.product(&left, &right, (float)alpha, ptr(bias), ptr(res), res_row, out.data_ptr(), out_row,
                     partials ? psum.data_ptr<float>() : nullptr, partials ? psq.data_ptr<float>() : nullptr,
                     c10::cuda::getCurrentCUDAStream(device).stream(), (ln_dtype)dt);
   }
@@ -308,7 +320,7 @@ PyObject* norm_from_partials(PyObject*, PyObject* const* a, Py_ssize_t n) {
     y = at::empty(x->sizes(), options);
     if (!rms) mean = at::empty({rows}, options.dtype(at::kFloat));
     rstd = at::empty({rows}, options.dtype(at::kFloat));
-    st = ln_fwd_from_partials(x->data_ptr(), static_cast<const float*>(ptr(psum)), static_cast<const float*>(ptr(psq)),
+    st = lib.fwd_from_partials(x->data_ptr(), static_cast<const float*>(ptr(psum)), static_cast<const float*>(ptr(psq)),
                               psum->size(-1), tile, (ln_partials)kind, gamma->data_ptr(), rms ? nullptr : ptr(beta),
                               (float)eps, (ln_mode)mode, zero, y.data_ptr(), rms ? nullptr : mean.data_ptr<float>(),
                               rstd.data_ptr<float>(), nullptr, c10::cuda::getCurrentCUDAStream(device).stream(), rows,
@@ -319,8 +331,28 @@ PyObject* norm_from_partials(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// bind(mx_matrix_bytes, mx_norm_fwd, mx_quantize, mx_dequantize, mx_product,
+// ln_fwd_from_partials): addresses of the library's entry points. Called once, before
+// anything else here.
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* at[6];
+  if (n != 6) return PyErr_Format(PyExc_TypeError, "bind: six addresses, not %zd", n);
+  for (int i = 0; i < 6; ++i) {
+    at[i] = PyLong_AsVoidPtr(a[i]);
+    if (at[i] == nullptr) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "bind: no address");
+  }
+  const auto set = [&](auto& fn, int i) { fn = reinterpret_cast<std::remove_reference_t<decltype(fn)>>(at[i]); };
+  set(lib.matrix_bytes, 0);
+  set(lib.norm_fwd, 1);
+  set(lib.quantize, 2);
+  set(lib.dequantize, 3);
+  set(lib.product, 4);
+  set(lib.fwd_from_partials, 5);
+  Py_RETURN_NONE;
+}
+
 #define FAST(NAME) {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(NAME)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(norm_quant), FAST(quantize), FAST(dequantize), FAST(product), FAST(norm_from_partials),
+PyMethodDef methods[] = {FAST(bind), FAST(norm_quant), FAST(quantize), FAST(dequantize), FAST(product), FAST(norm_from_partials),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods};
 
