@@ -4,8 +4,9 @@ binding's C++ part beside it.
 Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then the
 objects are linked into a shared library next to this file (the CUDA runtime
 is linked statically). ``csrc/marshal.cc`` is compiled at the same time by the
-host compiler, against the headers of the torch and Python that run this; its
-file has torch's version in its name. Nothing is installed anywhere else.
+host compiler, against the headers of the torch and Python that run this, where
+they are there; its file has torch's version in its name. Nothing is installed
+anywhere else.
 
     python -m normalization_fwd_gb300.build [--force] [--verbose] [--ptxas-info]
 """
@@ -53,14 +54,25 @@ def marshal_path() -> str:
     return os.path.join(PKG, f"_marshal-{tag}.so")
 
 
-def _marshal_commands(nvcc):
-    """(compile, link). Nothing of the library is linked in: the binding gives the
+def _marshal_commands():
+    """(compile, link), or None where the C++ part cannot be built: it wants g++, a
+    torch with CUDA and the headers of torch, Python and CUDA; the library does
+    without it. Nothing of the library is linked in: the binding gives the
     addresses of the one that it has loaded."""
     import torch
+    if torch.version.cuda is None or not shutil.which("g++"):
+        return None
     at = os.path.dirname(torch.__file__)
-    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+    try:
+        cuda = os.path.join(os.path.dirname(os.path.dirname(find_nvcc())), "include")
+    except RuntimeError:
+        return None
     dirs = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
             sysconfig.get_paths()["include"], cuda, os.path.join(ROOT, "include")]
+    if not all(any(os.path.isfile(os.path.join(d, name)) for d in dirs)
+               for name in ("c10/cuda/CUDAStream.h", "torch/csrc/autograd/python_variable.h", "Python.h",
+                            "cuda_runtime_api.h")):
+        return None
     obj = os.path.join(BUILD, "marshal.o")
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     return (["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
@@ -79,9 +91,10 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.isfile(LIB_PATH) or not os.path.isfile(marshal_path()):
+    made = [LIB_PATH] + ([marshal_path()] if _marshal_commands() else [])
+    if not all(os.path.isfile(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(marshal_path()))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -104,15 +117,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
 
     jobs = jobs or min(len(_sources()), os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs + 1) as ex:
-        compile_marshal, link_marshal = _marshal_commands(nvcc)
-        marshal = ex.submit(subprocess.run, compile_marshal, capture_output=True, text=True)
+        commands = _marshal_commands()
+        marshal = ex.submit(subprocess.run, commands[0], capture_output=True, text=True) if commands else None
         results = list(ex.map(compile_one, _sources()))
-        marshal = marshal.result()
+        marshal = marshal.result() if marshal else None
     failed = [(s, r) for s, _, r in results if r.returncode != 0]
     for s, _, r in results:
         if (verbose or ptxas_info) and (r.stdout or r.stderr):
             sys.stdout.write(r.stdout + r.stderr)
-    if marshal.returncode != 0:
+    if marshal is not None and marshal.returncode != 0:
         raise RuntimeError(f"g++ failed:\n--- marshal.cc\n{marshal.stdout}{marshal.stderr}")
     if failed:
         msg = "\n".join(f"--- {s}\n{r.stdout}{r.stderr}" for s, r in failed)
@@ -125,10 +138,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    r = subprocess.run(link_marshal, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
-    os.replace(marshal_path() + ".tmp", marshal_path())
+    if commands:
+        r = subprocess.run(commands[1], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
+        os.replace(marshal_path() + ".tmp", marshal_path())
+    elif verbose:
+        print("the binding's C++ part is left out: no g++, no torch with CUDA, or no headers", flush=True)
     return LIB_PATH
 
 

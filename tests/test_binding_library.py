@@ -80,3 +80,41 @@ def test_both_ways_give_the_same(cuda_lib, monkeypatch, fmt):
     monkeypatch.setattr(cuda_lib, "_marshal", None)
     for a, b in zip(run(), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lacking", ["g++", "a torch with CUDA", "torch's headers", "nothing"])
+def test_the_library_builds_without_what_only_the_cpp_part_wants(built, monkeypatch, tmp_path, lacking):
+    """The commands of a build, none of them run."""
+    import torch
+
+    from normalization_fwd_gb300 import build as b
+    ran, moved = [], []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        return Done
+
+    which = shutil.which
+    if lacking == "g++":
+        monkeypatch.setattr(b.shutil, "which", lambda name, *a, **k: None if name == "g++" else which(name, *a, **k))
+    elif lacking == "a torch with CUDA":
+        monkeypatch.setattr(torch.version, "cuda", None)
+    elif lacking == "torch's headers":
+        monkeypatch.setattr(torch, "__file__", str(tmp_path / "torch" / "__init__.py"))
+    # the library alone, newer than its sources
+    with monkeypatch.context() as m:
+        made = tmp_path / "lib.so"
+        made.touch()
+        m.setattr(b, "LIB_PATH", str(made))
+        m.setattr(b, "marshal_path", lambda: str(tmp_path / "none.so"))
+        assert b.up_to_date() == (lacking != "nothing")
+    monkeypatch.setattr(b.subprocess, "run", run)
+    monkeypatch.setattr(b.os, "replace", lambda src, dst: moved.append(dst))
+    assert b.build(force=True) == b.LIB_PATH
+    host = [c for c in ran if c[0] == "g++"]
+    assert len(host) == (2 if lacking == "nothing" else 0)
+    assert len(ran) == len(b._sources()) + 1 + len(host)
+    assert moved == [b.LIB_PATH] + ([b.marshal_path()] if host else [])
