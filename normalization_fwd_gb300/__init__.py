@@ -328,6 +328,13 @@ def ln_fwd_ex(x, bias, residual, gamma, beta, eps, mode, zero_centered_gamma, ou
         raise NormError(st, "ln_fwd_ex")
 
 
+def _partials(kind) -> int:
+    try:
+        return _PARTIAL_CODES[kind]
+    except KeyError:
+        raise ValueError(f"unknown partial kind {kind!r}") from None
+
+
 def ln_fwd_from_partials(x, psum, psq, tile_cols, kind, gamma, beta, eps, mode,
                          zero_centered_gamma, y, mean, rstd, amax, stream=None) -> None:
     """Enqueue the normalize step with row statistics combined from per
@@ -337,12 +344,8 @@ def ln_fwd_from_partials(x, psum, psq, tile_cols, kind, gamma, beta, eps, mode,
     lib = load_library()
     rows, hidden = _shape(x)
     n_tiles = psum.shape[-1] if psum is not None else -(-hidden // int(tile_cols))
-    try:
-        k = _PARTIAL_CODES[kind]
-    except KeyError:
-        raise ValueError(f"unknown partial kind {kind!r}") from None
     st = lib.ln_fwd_from_partials(_ptr(x), _ptr(psum), _ptr(psq), int(n_tiles), int(tile_cols),
-                                  k, _ptr(gamma), _ptr(beta), float(eps), _mode(mode),
+                                  _partials(kind), _ptr(gamma), _ptr(beta), float(eps), _mode(mode),
                                   int(bool(zero_centered_gamma)), _ptr(y), _ptr(mean),
                                   _ptr(rstd), _ptr(amax), _stream(stream), rows, hidden,
                                   _dtype(x))
@@ -498,8 +501,8 @@ def fused_norm_fwd_from_partials(x, psum, psq, tile_cols, gamma, beta=None, *, k
     """Allocate the outputs with torch and run ``ln_fwd_from_partials``;
     returns a dict with ``y``, ``mean`` (LayerNorm), ``rstd``, ``amax``."""
     if stream is None and not amax and (_lib or load_library()) and _marshal:
-        r = _marshal.norm_from_partials(x, psum, psq, tile_cols, _PARTIAL_CODES.get(kind, -1), gamma,
-                                        beta, eps, _mode(mode), zero_centered_gamma)
+        r = _marshal.norm_from_partials(x, psum, psq, tile_cols, _partials(kind), gamma, beta, eps,
+                                        _mode(mode), zero_centered_gamma)
         if r is not None:
             y, mean, rstd = _made(r, "ln_fwd_from_partials")
             return {"y": y, "mean": mean, "rstd": rstd, "amax": None}

@@ -118,3 +118,21 @@ def test_the_library_builds_without_what_only_the_cpp_part_wants(built, monkeypa
     assert len(host) == (2 if lacking == "nothing" else 0)
     assert len(ran) == len(b._sources()) + 1 + len(host)
     assert moved == [b.LIB_PATH] + ([b.marshal_path()] if host else [])
+
+
+def test_an_unknown_kind_of_partials(built):
+    """The binding's own error, whichever way the call would go."""
+    import torch
+    x = torch.zeros(2, 64)
+    p = torch.zeros(2, 1)
+    with pytest.raises(ValueError, match="unknown partial kind 'sum'"):
+        nf.fused_norm_fwd_from_partials(x, p, p, 64, x[0], kind="sum")
+
+
+@pytest.mark.gpu
+def test_an_unknown_kind_of_partials_on_the_gpu(cuda_lib):
+    import torch
+    x, p = torch.zeros(2, 64, device="cuda"), torch.zeros(2, 1, device="cuda")
+    for kw in ({}, {"stream": torch.cuda.current_stream()}, {"amax": True}):
+        with pytest.raises(ValueError, match="unknown partial kind 'sum'"):
+            cuda_lib.fused_norm_fwd_from_partials(x, p, p, 64, x[0], kind="sum", **kw)
