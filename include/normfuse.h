@@ -632,7 +632,9 @@ ln_status mx_dequantize(const mx_matrix* q, void* y, int64_t y_row, cudaStream_t
  *
  * bias      [N] dtype, NULL = none.
  * residual  [M, N] dtype, residual_row >= N elements a row, NULL = none; may be out
- *           itself (same row stride), overlaps it in no other way.
+ *           itself (same row stride), shares no element with it otherwise (columns
+ *           of one buffer side by side are accepted where that can be seen from the
+ *           strides).
  * out       [M, N] dtype, out_row >= N elements a row.
  * psum, psq [M, ceil(N / 128)] fp32 or NULL (both or none): sums of the stored
  *           rows over tiles of 128 columns and their squares about the tile's

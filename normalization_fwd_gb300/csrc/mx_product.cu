@@ -214,12 +214,18 @@ ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const 
   if (!aligned(psum, 4) || !aligned(psq, 4)) return LN_ERR_ALIGN;
   if (M == 0 || N == 0) return LN_OK;
   const size_t tiles = (size_t)M * (size_t)((N + 127) / 128) * 4;
-  const Range outs[] = {{out, (size_t)((M - 1) * out_row + N) * es}, {psum, psum ? tiles : 0}, {psq, psq ? tiles : 0}};
-  const bool in_place = residual == out && residual_row == out_row;
+  const auto rows_of = [&](const void* t, int64_t row) {
+    return Strided{t, {M, 1, 1}, {row * (int64_t)es, 0, 0}, N * (int64_t)es};
+  };
+  const Strided results = rows_of(out, out_row), added = rows_of(residual, residual_row);
+  const Range outs[] = {results.range(), {psum, psum ? tiles : 0}, {psq, psq ? tiles : 0}};
   const Range ins[] = {codes_range(*a), scales_range(*a), mul_range(*a), codes_range(*b), scales_range(*b),
-                       mul_range(*b), {bias, (size_t)N * es},
-                       {in_place ? nullptr : residual, (size_t)((M - 1) * residual_row + N) * es}};
-  if (any_overlap(outs, 3, ins, 8)) return LN_ERR_INVALID;
+                       mul_range(*b), {bias, (size_t)N * es}};
+  const Range residual_range[] = {added.range()};
+  if (any_overlap(outs, 3, ins, 7) || any_overlap(outs + 1, 2, residual_range, 1)) return LN_ERR_INVALID;
+  // in place, or apart: two slices of one buffer are
+  const bool in_place = residual == out && (residual_row == out_row || M == 1);
+  if (!in_place && may_overlap(results, added)) return LN_ERR_INVALID;
   int sms = 0;
   cudaError_t e = (cudaError_t)device_sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
