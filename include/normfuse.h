@@ -558,7 +558,12 @@ ln_status rope_frequencies(int64_t rot, double base, rope_scaling scaling, doubl
  *                code = E2M1(u / scale), at most 6; 0 where the scale is 0
  * so a value is code * scale (MX_NVFP4: / *mul). A row or block that holds an
  * infinity or a NaN has a NaN for its scale and codes of 0. The blocks begin at
- * column 0; the last one of a row may be narrower.
+ * column 0; the last one of a row may be narrower. Here E8M0 scales round up: the
+ * OCP document's own conversion takes the exponent of amax less that of M, and the
+ * values of a block that are past M 2^e then become M 2^e. Either reads the other's
+ * matrices. MX_NVFP4's *mul is the caller's to find, an amax of this step or of one
+ * before. The product below takes the microscaled formats; the two with fp32 scales
+ * are for products elsewhere that scale by rows or by blocks of 128.
  *
  * Layout. MX_FP8_ROW and MX_FP8_BLOCK: codes [rows, cols] bytes, scales [rows]
  * or [rows, ceil(cols / 128)] fp32. The microscaled formats: a row of codes is

@@ -1330,7 +1330,7 @@ def fused_norm_quant_fwd(x, gamma, beta=None, *, format, mul=None, bias=None, re
     ``fused_norm_bwd`` on ``sum`` (or x), ``mean`` and ``rstd`` is its backward,
     the gradient of the dequantised result passed straight through. ``mul`` is
     nvfp4's factor (one float32 on the device, commonly 2688 over the largest
-    magnitude seen).
+    magnitude seen, which is the caller's to find).
     """
     if store_sum is None:
         store_sum = bias is not None or residual is not None

@@ -32,8 +32,8 @@ int class_of(int fmt) { return fmt == MX_FP8_ROW ? 0 : mx_four(fmt) ? 2 : 1; }
 // Lanes a row (0: a CTA), vectors a lane and threads for rows of `slots` 16-byte
 // vectors, room for codes included. As in the 16-bit forward: lane groups up to
 // 160 vectors, four vectors a lane where the row splits evenly, then a CTA
-// fitted to the row (8192 x 5120 bf16 LayerNorm to mxfp4 56 us with four
-// vectors a thread, 58 with three, 61 with six, 73 with eight). A block of 128
+// fitted to the row (8192 x 5120 bf16 LayerNorm to mxfp4 49.7 us with four
+// vectors a thread, 53.4 with three, 55.2 with six, 65.6 with eight). A block of 128
 // columns needs 16 lanes (32 for fp32).
 struct NormPlan {
   int lanes = -1, n = 0, block = 256;
@@ -68,9 +68,10 @@ NormPlan norm_plan(int slots, int least_lanes) {
 // Few rows leave threads idle anyway, so a row is spread over as many as there are,
 // two vectors each, and its sums are put in the order of the plan above (on the GPU
 // 64 x 1280 bf16 to mxfp8 2.6 us against 3.8, 1 x 4096 to mxfp4 2.5 against 3.1, 1024 x
-// 320 fp16 to mxfp8 3.4 against 4.1; 8192 x 320, which is not few, 7.3 against 6.1; a
-// CTA's longer row takes as long either way where a CTA an SM is not enough, 512 x
-// 1000 fp32 4.3). n = 0: rows are not few, or too wide.
+// 320 fp16 to mxfp8 3.3 against 4.1; 8192 x 320, which is not few, 7.3 against 6.1; a
+// CTA's longer row gains or loses 0.2 us where a CTA an SM is not enough, 512 x 1000
+// fp32 4.2 against 4.4, 300 x 2560 bf16 4.65 against 4.45). n = 0: rows are not few, or
+// too wide.
 NormPlan few_plan(int slots, int64_t rows, int sms) {
   const bool few = slots <= 160 ? rows * slots <= (int64_t)sms * 1024 : rows <= sms;
   if (!few || slots > 2 * kMaxFitThreads) return {-1, 0, 0};

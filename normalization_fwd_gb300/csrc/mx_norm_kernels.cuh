@@ -9,8 +9,8 @@
 //
 // What bounds it: HBM (x and residual read, the sum and 0.5 to 1 bytes a value
 // written) and, with block scales, the instructions: 16384 x 8192 bf16 RMSNorm
-// with a residual takes 138 us to fp8_row (6.8 TB/s), 145 to mxfp8 (6.5), 157 to
-// nvfp4 (5.6 TB/s, 81% of the issue slots).
+// with a residual takes 137 us to fp8_row (6.9 TB/s), 142 to mxfp8 (6.7), 153 to
+// nvfp4 (5.8 TB/s, 82% of the issue slots).
 #pragma once
 
 #include "bulk.cuh"

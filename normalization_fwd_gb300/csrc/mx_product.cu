@@ -160,11 +160,12 @@ cudaError_t launch_format(ProductArgs p, int sms, cudaStream_t st) {
     return launch_tiles<T, FMT, true>(p, sms, st);
   }
   // Pairs of CTAs from where single tiles are more than the SMs (nvfp4 4096 x 4096
-  // x 8192 51 us against 98 as single tiles, 512 x 8192 x 8192 20 against 29; 256
-  // x 8192 x 8192, 128 tiles, 15.3 single against 18.7). Tiles of 256 columns
-  // unless they take more than 5 rounds for 8 of half the width (the first 51 us
-  // against 73, mxfp8 2100 x 2300 x 800 20.4 against 19.3): a tile of 128 takes
-  // some five eighths of one of 256, as its operands are copied for half the results.
+  // x 8192 49 us against 101 as single tiles, 512 x 8192 x 8192 18.5 against 29.5; 256
+  // x 8192 x 8192, 128 tiles, 15.6 single, 14.9 as narrow pairs, 17.5 as wide ones).
+  // Tiles of 256 columns unless they take more than 5 rounds for 8 of half the width
+  // (the first 49 us against 71, mxfp8 2100 x 2300 x 800 19.0 against 18.3): a tile of
+  // 128 takes some five eighths of one of 256, as its operands are copied for half the
+  // results.
   const int64_t tm = (p.a.rows + 255) / 256, tn = (p.b.rows + 127) / 128, pairs = sms / 2;
   if (p.a.rows > 128 && pairs > 0 && tm * tn * 2 > sms) {
     const int64_t narrow = (tm * tn + pairs - 1) / pairs, wide = (tm * ((tn + 1) / 2) + pairs - 1) / pairs;

@@ -13,14 +13,16 @@
 // on to tensor memory and issues four instructions of 32 bytes of K. Scales
 // have a buffer there for each stage: a stage that is full again says that the
 // instructions on what it held before are done, and so are those that read that
-// buffer. The issuing warp asks for the next stage before it issues.
+// buffer. The issuing warp asks for the next stage before it issues, by a test that
+// returns at once (with one that may hold it back 16384 x 8192 x 8192 took 335 us).
 //
 // What bounds it: few rows of A, the weights' bytes and the fixed 4 us of a launch,
-// a ring's first round and the join (16 x 8192 x 8192 nvfp4 11.0 us: 42 MB at 5.6
-// TB/s on 128 SMs). Many rows, the tensor cores: a chunk's four instructions take a
+// a ring's first round and the join (16 x 8192 x 8192 nvfp4 10.7 us: 38 MB, 5.6 us of
+// HBM's time, on 128 SMs). Many rows, the tensor cores: a chunk's four instructions take a
 // pair of CTAs 512 cycles, moving its scales 10 cycles for each of their 12 (nvfp4),
 // 6 (mxfp4) or 3 (mxfp8) tiles, and data is always there (16384 x 8192 x 8192
-// nvfp4 333 us, 6.6 PFLOP/s, tensor pipe 66% active on a smaller case).
+// nvfp4 314 us, 7.0 PFLOP/s, alone; 356 us in a loop, under the power limit; tensor
+// pipe 74% active on a smaller case).
 //
 // Few tiles: K is split over the CTAs of a cluster. Each gets the tile's rows
 // of results that it is to finish from all others through distributed shared
