@@ -5,8 +5,8 @@ Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then the
 objects are linked into a shared library next to this file (the CUDA runtime
 is linked statically). ``csrc/marshal.cc`` is compiled at the same time by the
 host compiler, against the headers of the torch and Python that run this, where
-they are there; its file has torch's version in its name. Nothing is installed
-anywhere else.
+they are there; its file has torch's version and a hash of its source in its name.
+Nothing is installed anywhere else.
 
     python -m normalization_fwd_gb300.build [--force] [--verbose] [--ptxas-info]
 """
@@ -14,6 +14,7 @@ anywhere else.
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -48,9 +49,15 @@ def find_nvcc() -> str:
 
 
 def marshal_path() -> str:
-    """Where the C++ part of the binding is, for this torch and this Python."""
+    """Where the C++ part of the binding is, for this torch, this Python, its own
+    source and the declarations that it calls: one of another state is not taken."""
     import torch
-    tag = f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}"
+    state = hashlib.sha256()
+    for path in (os.path.join(CSRC, "marshal.cc"), os.path.join(ROOT, "include", "normfuse.h")):
+        if os.path.isfile(path):
+            with open(path, "rb") as f:
+                state.update(f.read() + b"\0")
+    tag = f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}-{state.hexdigest()[:8]}"
     return os.path.join(PKG, f"_marshal-{tag}.so")
 
 

@@ -136,3 +136,23 @@ def test_an_unknown_kind_of_partials_on_the_gpu(cuda_lib):
     for kw in ({}, {"stream": torch.cuda.current_stream()}, {"amax": True}):
         with pytest.raises(ValueError, match="unknown partial kind 'sum'"):
             cuda_lib.fused_norm_fwd_from_partials(x, p, p, 64, x[0], kind="sum", **kw)
+
+
+def test_a_cpp_part_of_another_state_is_not_taken(built, monkeypatch, tmp_path):
+    """One that was built from other declarations than the library's, under another
+    torch say, has another name."""
+    from normalization_fwd_gb300 import build as b
+    now = b.marshal_path()
+    assert os.path.isfile(now)
+    for path in ("include/normfuse.h", "normalization_fwd_gb300/csrc/marshal.cc"):
+        target = tmp_path / path
+        target.parent.mkdir(parents=True, exist_ok=True)
+        shutil.copy(os.path.join(ROOT, path), target)
+    monkeypatch.setattr(b, "ROOT", str(tmp_path))
+    monkeypatch.setattr(b, "CSRC", str(tmp_path / "normalization_fwd_gb300" / "csrc"))
+    assert b.marshal_path() == now
+    for path in ("include/normfuse.h", "normalization_fwd_gb300/csrc/marshal.cc"):
+        with open(tmp_path / path, "a") as f:
+            f.write("// another state\n")
+        assert b.marshal_path() != now
+        now = b.marshal_path()
