@@ -218,7 +218,7 @@ ln_status mx_product(const mx_matrix* a, const mx_matrix* b, float alpha, const 
   const auto rows_of = [&](const void* t, int64_t row) {
     return Strided{t, {M, 1, 1}, {row * (int64_t)es, 0, 0}, N * (int64_t)es};
   };
-  const Strided results = rows_of(out, out_row), added = rows_of(residual, residual_row);
+  const Strided results = rows_of(out, out_row), added = residual != nullptr ? rows_of(residual, residual_row) : Strided();
   const Range outs[] = {results.range(), {psum, psum ? tiles : 0}, {psq, psq ? tiles : 0}};
   const Range ins[] = {codes_range(*a), scales_range(*a), mul_range(*a), codes_range(*b), scales_range(*b),
                        mul_range(*b), {bias, (size_t)N * es}};

@@ -28,6 +28,7 @@ def call(lib, out, out_row, res, res_row, M=40, N=50, ps=None, pq=None):
     dict(out=Y, out_row=50, res=Y, res_row=50),                  # in place
     dict(out=Y, out_row=200, res=Y, res_row=200),
     dict(out=Y, out_row=50, res=Y, res_row=64, M=1),             # one row: strides say nothing
+    dict(out=Y, out_row=50, res=None, res_row=(1 << 63) - 1),    # no residual: its row is not looked at
 ])
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the call would be launched on made-up addresses")
 def test_accepted(lib, kw):
